@@ -289,6 +289,98 @@ moe_status_t moe_layer_decode_host_rows(const uint16_t* x, int32_t B, const moe_
 moe_status_t moe_prefetch_experts(const moe_experts_t* experts, const int32_t* idx, int32_t n,
                                   size_t max_bytes, void* stream);
 
+/* ---------------- uncompressed 16-bit weights ----------------
+ *
+ * The same expert and layer without FloE's compression (the SwiGLU expert formula of FloE
+ * sec. 三, "MoE 专家前向计算"), in fp16 or bf16, and the matrix product with an epilogue that
+ * stands around them in a model.  Sums are fp32 and have a fixed order: equal calls give
+ * equal bits.  16-bit tensors are passed as uint16_t (or void*) bit patterns; one call has one type.
+ *
+ * Workspaces: the calls of this section may share one that is large enough for each, as long as they
+ * are ordered on one stream; it is zero-filled once before its first use (moe_workspace_init), and
+ * again after MOE_ERR_TIMEOUT.  It may not be shared with the calls of the other sections.
+ */
+enum { MOE_F16 = 0, MOE_BF16 = 1, MOE_F32 = 2 };
+enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3, MOE_ACT_SILU = 4 };
+enum { MOE_W_NK = 0, MOE_W_KN = 1 };
+
+/*
+ * moe_linear -- y = act(x w^T + bias) [* (x w_mul^T + bias_mul)] [+ residual], rounded once.
+ *   M 0..1048576 tokens (0 is a no-op), N 1..1048576 outputs, K 8..262144 inputs, a multiple of 8;
+ *   dtype      MOE_F16 or MOE_BF16: x, w, w_mul, bias, bias_mul, residual
+ *   out_dtype  of y: dtype, or MOE_F32
+ *   w_layout   MOE_W_NK: w [N][K] (row n = output n, as gate_t); MOE_W_KN: w [K][N] (as down and
+ *              w_router), N a multiple of 8
+ *   act        MOE_ACT_*: GELU by erf or by tanh, SiLU
+ *   x [M][K]; y [M][N]; w_mul [as w], bias [N], bias_mul [N] (only with w_mul), residual [M][N]: NULL
+ *   leaves that part out.  y may be the residual's buffer (with out_dtype = dtype), no other input's.
+ *   With w_mul = W^up, w = W^gate and MOE_ACT_SILU this is the first half of a SwiGLU block.
+ *   ws / ws_bytes: at least moe_linear_workspace_bytes(M, N, K, w_mul != NULL) bytes.
+ */
+typedef struct {
+  int32_t M, N, K;
+  int32_t dtype, out_dtype, w_layout, act;
+  const void* x;
+  const void* w;
+  const void* w_mul;
+  const void* bias;
+  const void* bias_mul;
+  const void* residual;
+  void* y;
+} moe_linear_t;
+
+size_t moe_linear_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t gated);
+moe_status_t moe_linear(const moe_linear_t* op, void* ws, size_t ws_bytes, void* stream);
+
+/* One stack of equally shaped uncompressed experts: d 8..16384, f 8..65536, multiples of 8; E 1..256. */
+typedef struct {
+  int32_t E;
+  int32_t d;
+  int32_t f;
+  int32_t dtype;             /* MOE_F16 or MOE_BF16 */
+  const uint16_t* gate_t;    /* [E][f][d]: row i = column i of W^gate */
+  const uint16_t* up_t;      /* [E][f][d]: row i = column i of W^up */
+  const uint16_t* down;      /* [E][f][d]: row i = row i of W^down; down = gate_t + d: interleaved
+                                rows [E][f][2][d], as in moe_experts_t */
+} moe_dense_experts_t;
+
+/*
+ * moe_expert_dense_swiglu -- one expert on n tokens (0..1048576):
+ *   y[b] = (SiLU(x_b W^gate) (.) x_b W^up) W^down [+ residual[b]]
+ *   x, y [n][d] of experts->dtype; residual [n][d] or NULL; y may be the residual's buffer.
+ *   Up to 64 tokens run in one kernel and keep h = SiLU(.) (.) . to 16 bits and more beyond the
+ *   type's own; more tokens run as two products, with h rounded to the type.  In fp16 |h| > 65504
+ *   is infinite.
+ *   ws / ws_bytes: at least moe_expert_dense_workspace_bytes(n, d, f) bytes.
+ */
+size_t moe_expert_dense_workspace_bytes(int32_t n, int32_t d, int32_t f);
+moe_status_t moe_expert_dense_swiglu(const uint16_t* x, int32_t n, const moe_dense_experts_t* experts,
+                                     int32_t expert, const uint16_t* residual, uint16_t* y, void* ws,
+                                     size_t ws_bytes, void* stream);
+
+/* One MoE layer of uncompressed experts. */
+typedef struct {
+  int32_t k;                   /* experts per token, 1..min(E, 8) */
+  int32_t renorm;              /* as in moe_layer_t */
+  const uint16_t* w_router;    /* [d][E], the experts' dtype */
+  moe_dense_experts_t routed;
+  moe_dense_experts_t shared;  /* always-on experts, weight 1 (E = 0: none; else 1..8); same d, f, dtype */
+} moe_dense_layer_t;
+
+/*
+ * moe_layer_dense_decode -- moe_layer_decode with uncompressed experts, on B = 0..64 tokens:
+ *   y[b] = sum_j topk_w[b][j] * E_{topk_idx[b][j]}(x[b]) + sum_s E^shared_s(x[b]) [+ residual[b]]
+ * and with rmsnorm_out = 1 that divided by sqrt(mean of its squares + 1e-6).  Routing as in
+ * moe_route_topk.  One kernel (a cooperative launch on every SM).
+ *   x, y [B][d]; residual [B][d] or NULL; y may be the residual's buffer, not x's;
+ *   dbg: optional, topk_idx and topk_w only (the other members are not used).
+ *   ws / ws_bytes: at least moe_layer_dense_workspace_bytes(layer, B) bytes.
+ */
+size_t moe_layer_dense_workspace_bytes(const moe_dense_layer_t* layer, int32_t B);
+moe_status_t moe_layer_dense_decode(const uint16_t* x, int32_t B, const moe_dense_layer_t* layer,
+                                    const uint16_t* residual, uint16_t* y, int32_t rmsnorm_out,
+                                    const moe_debug_t* dbg, void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------- expert activation tracking and expert cache (host) ----------------
  *
  * "MoE-Infinity" (sec. 4.3, 4.5, 4.7 Algorithm 1 "专家缓存检索", appendix B.1): request-level

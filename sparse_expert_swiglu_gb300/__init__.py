@@ -6,6 +6,8 @@ the seeded synthetic-input generator.
 """
 
 from ._lib import (  # noqa: F401
+    DenseExperts,
+    DenseLayer,
     EAMC,
     EXPORTED,
     ExpertCache,
@@ -14,15 +16,21 @@ from ._lib import (  # noqa: F401
     MoeError,
     Workspace,
     eam_add_counts,
+    expert_dense_swiglu,
+    expert_dense_workspace_bytes,
     expert_sparse_swiglu,
     expert_workspace_bytes,
     layer_decode,
     layer_decode_host_rows,
+    layer_dense_decode,
+    layer_dense_workspace_bytes,
     layer_host_rows_workspace_bytes,
     layer_path,
     layer_workspace_bytes,
     lib,
     lib_path,
+    linear,
+    linear_workspace_bytes,
     pack_int2_up,
     packed_bytes,
     prefetch_experts,

@@ -48,6 +48,21 @@ class _Debug(ctypes.Structure):
                 ("events", ctypes.POINTER(ctypes.c_void_p))]
 
 
+class _DenseExperts(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("d", ctypes.c_int32), ("f", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("gate_t", ctypes.c_void_p), ("up_t", ctypes.c_void_p), ("down", ctypes.c_void_p)]
+
+
+class _DenseLayer(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_int32), ("renorm", ctypes.c_int32), ("w_router", ctypes.c_void_p),
+                ("routed", _DenseExperts), ("shared", _DenseExperts)]
+
+
+class _Linear(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "dtype", "out_dtype", "w_layout", "act")] + \
+               [(n, ctypes.c_void_p) for n in ("x", "w", "w_mul", "bias", "bias_mul", "residual", "y")]
+
+
 _LIB = None
 _SIGS = {
     "expert_int2_up_packed_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
@@ -102,6 +117,17 @@ _SIGS = {
                                                ctypes.c_int32, ctypes.c_int32, ctypes.c_double, ctypes.c_void_p,
                                                ctypes.c_void_p]),
     "moe_expert_cache_contents": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_linear_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 4),
+    "moe_linear": (ctypes.c_int, [ctypes.POINTER(_Linear), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_expert_dense_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 3),
+    "moe_expert_dense_swiglu": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(_DenseExperts),
+                                               ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                               ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_layer_dense_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(_DenseLayer), ctypes.c_int32]),
+    "moe_layer_dense_decode": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(_DenseLayer),
+                                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                              ctypes.POINTER(_Debug), ctypes.c_void_p, ctypes.c_size_t,
+                                              ctypes.c_void_p]),
     "moe_workspace_init": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "moe_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32,
                                                  ctypes.c_void_p]),
@@ -486,6 +512,238 @@ def layer_decode_host_rows(x: torch.Tensor, layer: Layer, rmsnorm: bool = False,
                                             ctypes.byref(dbg) if dbg is not None else None,
                                             ws.ptr(), ws.nbytes, _stream()))
     return (y, dt) if debug else y
+
+
+# ---------------------------------------------------------------------------
+# uncompressed 16-bit weights: products with an epilogue, experts, layers
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+_ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+_LAYOUTS = {"nk": 0, "kn": 1}
+
+
+def _dense_in(t, dtype, device: int, shape, name: str) -> int:
+    """Address of an input of a call on uncompressed weights: type, device, shape and density checked."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _dense_x(x, name: str = "x") -> int:
+    """The device of a call's tokens, a CUDA fp16 or bf16 matrix on the current device."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not x.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if x.dtype != torch.float16 and x.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    device = x.get_device()
+    if device != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{device}, which is not the current device")
+    return device
+
+
+def _dense_ws(ws, nbytes: int, device: int) -> "Workspace":
+    """The caller's workspace, or a new one of nbytes."""
+    if ws is None:
+        if nbytes == 0:
+            raise ValueError("sizes outside the supported range")
+        return Workspace(nbytes, torch.device("cuda", device))
+    if ws.buf.get_device() != device:
+        raise ValueError(f"ws must be on cuda:{device}")
+    return ws
+
+
+def linear_workspace_bytes(M: int, N: int, K: int, gated: bool = False) -> int:
+    return int(lib().moe_linear_workspace_bytes(M, N, K, 1 if gated else 0))
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
+           w_mul: Optional[torch.Tensor] = None, bias_mul: Optional[torch.Tensor] = None,
+           residual: Optional[torch.Tensor] = None, w_layout: str = "nk", out_dtype=None,
+           ws: Optional[Workspace] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y = act(x w^T + bias) [* (x w_mul^T + bias_mul)] [+ residual], fp32 sums, rounded once.
+
+    x [M, K] fp16 or bf16; w (and w_mul) [N, K] ("nk": row n = output n, as gate_t) or [K, N] ("kn", as down
+    and w_router); act "none", "relu", "gelu", "gelu_tanh" or "silu"; out_dtype x's (default) or torch.float32.
+    out may be the residual's tensor, no other input's."""
+    device = _dense_x(x)
+    dt = x.dtype
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {tuple(_ACTS)}, got {act!r}")
+    if w_layout not in _LAYOUTS:
+        raise ValueError(f"w_layout must be 'nk' or 'kn', got {w_layout!r}")
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be a matrix")
+    if bias_mul is not None and w_mul is None:
+        raise ValueError("bias_mul goes with w_mul")
+    M, K = x.shape
+    N = w.shape[0] if w_layout == "nk" else w.shape[1]
+    wshape = (N, K) if w_layout == "nk" else (K, N)
+    if out_dtype is None:
+        out_dtype = dt
+    elif out_dtype != dt and out_dtype != torch.float32:
+        raise TypeError(f"out_dtype must be {dt} or torch.float32, got {out_dtype}")
+    if out is None:
+        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        yp = y.data_ptr()
+    else:
+        y = out
+        yp = _dense_in(out, out_dtype, device, (M, N), "out")
+    op = _Linear(M, N, K, _DTYPES[dt], _DTYPES[out_dtype], _LAYOUTS[w_layout], _ACTS[act],
+                 _dense_in(x, dt, device, (M, K), "x"), _dense_in(w, dt, device, wshape, "w"),
+                 None if w_mul is None else _dense_in(w_mul, dt, device, wshape, "w_mul"),
+                 None if bias is None else _dense_in(bias, dt, device, (N,), "bias"),
+                 None if bias_mul is None else _dense_in(bias_mul, dt, device, (N,), "bias_mul"),
+                 None if residual is None else _dense_in(residual, dt, device, (M, N), "residual"), yp)
+    if M == 0:
+        return y
+    ws = _dense_ws(ws, 0 if ws is not None else linear_workspace_bytes(M, N, K, w_mul is not None), device)
+    _check("moe_linear", lib().moe_linear(ctypes.byref(op), ws.buf.data_ptr(), ws.nbytes,
+                                          torch.cuda.current_stream().cuda_stream))
+    return y
+
+
+@dataclass
+class DenseExperts:
+    """A stack of E equally shaped uncompressed experts (device tensors, fp16 or bf16): gate_t, up_t and
+    down [E, f, d]; row i of gate_t / up_t is column i of W^gate / W^up, row i of down is row i of W^down.
+    gate_t and down may be the two halves of one interleaved buffer, as in Experts."""
+    gate_t: torch.Tensor
+    up_t: torch.Tensor
+    down: torch.Tensor
+
+    @property
+    def E(self):
+        return self.gate_t.shape[0]
+
+    @property
+    def f(self):
+        return self.gate_t.shape[1]
+
+    @property
+    def d(self):
+        return self.gate_t.shape[2]
+
+    def c_struct(self) -> _DenseExperts:
+        g, dn = self.gate_t, self.down
+        if not isinstance(g, torch.Tensor) or g.dim() != 3:
+            raise ValueError("gate_t must have shape [E, f, d]")
+        if g.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError(f"gate_t must be torch.float16 or torch.bfloat16, got {g.dtype}")
+        if not g.is_cuda:
+            raise TypeError("gate_t must be a CUDA tensor")
+        E, f, d = g.shape
+        device = g.get_device()
+        if (isinstance(dn, torch.Tensor) and dn.shape == g.shape and dn.stride() == g.stride() and dn.dtype == g.dtype
+                and dn.is_cuda and g.stride() == (2 * f * d, 2 * d, 1) and dn.data_ptr() == g.data_ptr() + 2 * d):
+            gp, dp = g.data_ptr(), dn.data_ptr()  # interleaved
+        else:
+            gp = _dense_in(g, g.dtype, device, g.shape, "gate_t")
+            dp = _dense_in(dn, g.dtype, device, g.shape, "down")
+        return _DenseExperts(E, d, f, _DTYPES[g.dtype], gp, _dense_in(self.up_t, g.dtype, device, g.shape, "up_t"), dp)
+
+
+@dataclass
+class DenseLayer:
+    """One MoE layer of uncompressed experts."""
+    w_router: torch.Tensor       # [d, E], the experts' type
+    routed: DenseExperts
+    k: int
+    renorm: bool = True
+    shared: Optional[DenseExperts] = None
+
+    def c_struct(self) -> _DenseLayer:
+        r = self.routed.c_struct()
+        g = self.routed.gate_t
+        wr = _dense_in(self.w_router, g.dtype, g.get_device(), (r.d, r.E), "w_router")
+        if self.shared is None:
+            s = _DenseExperts(0, r.d, r.f, r.dtype, None, None, None)
+        else:
+            s = self.shared.c_struct()
+            if self.shared.gate_t.get_device() != g.get_device():
+                raise ValueError("shared experts must be on the routed experts' device")
+        return _DenseLayer(self.k, 1 if self.renorm else 0, wr, r, s)
+
+
+def expert_dense_workspace_bytes(n: int, d: int, f: int) -> int:
+    return int(lib().moe_expert_dense_workspace_bytes(n, d, f))
+
+
+def expert_dense_swiglu(x: torch.Tensor, experts: DenseExperts, expert: int, residual: Optional[torch.Tensor] = None,
+                        ws: Optional[Workspace] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One uncompressed SwiGLU expert on every row of x [n, d]: (SiLU(x W^gate) * x W^up) W^down [+ residual].
+    out may be the residual's tensor."""
+    device = _dense_x(x)
+    dt = x.dtype
+    n = x.shape[0]
+    ex = experts.c_struct()
+    if experts.gate_t.dtype != dt or experts.gate_t.get_device() != device:
+        raise ValueError("x and the experts must have one type and device")
+    shape = (n, ex.d)
+    xp = _dense_in(x, dt, device, shape, "x")
+    rp = None if residual is None else _dense_in(residual, dt, device, shape, "residual")
+    if out is None:
+        y = torch.empty_like(x)
+    else:
+        y = out
+        _dense_in(out, dt, device, shape, "out")
+    if n == 0:
+        return y
+    ws = _dense_ws(ws, 0 if ws is not None else expert_dense_workspace_bytes(n, ex.d, ex.f), device)
+    _check("moe_expert_dense_swiglu",
+           lib().moe_expert_dense_swiglu(xp, n, ctypes.byref(ex), expert, rp, y.data_ptr(), ws.buf.data_ptr(), ws.nbytes,
+                                         torch.cuda.current_stream().cuda_stream))
+    return y
+
+
+def layer_dense_workspace_bytes(layer: DenseLayer, B: int) -> int:
+    return int(lib().moe_layer_dense_workspace_bytes(ctypes.byref(layer.c_struct()), B))
+
+
+def layer_dense_decode(x: torch.Tensor, layer: DenseLayer, residual: Optional[torch.Tensor] = None, rmsnorm: bool = False,
+                       ws: Optional[Workspace] = None, debug: bool = False, out: Optional[torch.Tensor] = None):
+    """One MoE layer of uncompressed experts on x [B, d], B <= 64 -> y [B, d] (and, with debug, a dict with
+    topk_idx and topk_w): the weighted sum of the experts [+ residual] [RMSNorm].  out may be the residual's
+    tensor, not x."""
+    device = _dense_x(x)
+    dt = x.dtype
+    B = x.shape[0]
+    c = layer.c_struct()
+    if layer.routed.gate_t.dtype != dt or layer.routed.gate_t.get_device() != device:
+        raise ValueError("x and the experts must have one type and device")
+    shape = (B, c.routed.d)
+    xp = _dense_in(x, dt, device, shape, "x")
+    rp = None if residual is None else _dense_in(residual, dt, device, shape, "residual")
+    if out is None:
+        y = torch.empty_like(x)
+    else:
+        y = out
+        _dense_in(out, dt, device, shape, "out")
+    dbg, dt_ = None, None
+    if debug:
+        dt_ = dict(topk_idx=torch.zeros((B, layer.k), dtype=torch.int32, device=x.device),
+                   topk_w=torch.zeros((B, layer.k), dtype=torch.float32, device=x.device))
+        dbg = ctypes.byref(_Debug(_ptr(dt_["topk_idx"]), _ptr(dt_["topk_w"]), None, None, None))
+    if B:
+        ws = _dense_ws(ws, 0 if ws is not None else int(lib().moe_layer_dense_workspace_bytes(ctypes.byref(c), B)), device)
+        _check("moe_layer_dense_decode",
+               lib().moe_layer_dense_decode(xp, B, ctypes.byref(c), rp, y.data_ptr(), 1 if rmsnorm else 0, dbg,
+                                            ws.buf.data_ptr(), ws.nbytes, torch.cuda.current_stream().cuda_stream))
+    return (y, dt_) if debug else y
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,300 @@
+// Shared parts of the kernels on uncompressed 16-bit weights (linear.cu, dense_layer.cu).
+//
+// Both kernels are streams of weight tiles through tcgen05: D[feature][token] +=
+// W[feature][k] x[token][k].  The weights are the 128-row operand A, so that one token
+// costs no more than 16 (the smallest N); the tokens are operand B.  One CTA per SM; a TMA
+// warp fills a ring of stages of 64 k each (A: two 128-feature tiles, 32 KB; B: up to 256
+// token rows of 128 bytes), one thread issues the products into TMEM, four warps read the
+// sums back.  Every operand is stored with the 128-byte swizzle.
+//
+// Tiles go to the CTAs in full waves, and the tiles that are left over are cut along k
+// into equal shares for all of them (Sched).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "params.cuh"
+
+namespace sesg {
+
+constexpr int kDnThreads = 256;      // warps: 0 TMA, 1 products, 2 TMEM, 4-7 epilogue
+constexpr int kDnChunk = 64;         // k per stage: 128 bytes, one swizzled row
+constexpr int kDnHalf = 128;         // features of one product (TMEM lanes)
+constexpr int kDnBytesA = 2 * kDnHalf * kDnChunk * 2;
+constexpr int kDnMaxStages = 8;
+constexpr int kDnMaxSplit = 16;      // shares of one tile along k, at most (plus a border)
+constexpr int kDnMaxCtas = 1024;
+
+// ---------------------------------------------------------------------------
+// workspace head, the same for every call on uncompressed weights: Ctrl, the grid
+// barriers' counts and the shares' counts, all zero between calls
+// ---------------------------------------------------------------------------
+struct DenseHead {
+  Ctrl ctrl;
+  unsigned bar[8];                 // grid barriers of the layer kernel
+  unsigned tok[64];                // router slices done, per token
+  unsigned pad[64 - 16];
+  unsigned cnt[kDnMaxCtas];        // shares done, per split tile
+};
+
+// ---------------------------------------------------------------------------
+// Work of CTA c of P: T tiles of KC chunks each.  Tiles below dp are whole: c, c + P, ...
+// The others lie in one line of (T - dp) * KC chunks, of which CTA c takes q from c * q.
+// ---------------------------------------------------------------------------
+struct Sched {
+  int T, KC, P, dp, q, total;
+  __host__ __device__ static Sched make(int T, int KC, int P) {
+    Sched s;
+    s.T = T;
+    s.KC = KC;
+    s.P = P;
+    const int rest = T % P;
+    // a rest of nearly a whole wave gains less from being cut than its joining costs
+    s.dp = rest * 10 >= P * 9 ? T : T - rest;
+    s.total = (T - s.dp) * KC;
+    const int by_ctas = (s.total + P - 1) / P, by_split = (KC + kDnMaxSplit - 1) / kDnMaxSplit;
+    s.q = by_ctas > by_split ? by_ctas : by_split;
+    if (s.q < 1) s.q = 1;
+    return s;
+  }
+  __host__ __device__ int ctas() const { return dp ? P : (total + q - 1) / q; }
+  // shares of a split tile (t >= dp) and the CTA of the first one
+  __host__ __device__ int first(int t) const { return (t - dp) * KC / q; }
+  __host__ __device__ int parts(int t) const { return t < dp ? 1 : ((t - dp + 1) * KC - 1) / q - first(t) + 1; }
+  __host__ __device__ int max_parts() const { return total ? (KC + q - 1) / q + 1 : 1; }
+  // partial sums in the workspace: numbered along the line of shares
+  __host__ __device__ int segments() const { return total ? (T - dp) + (total + q - 1) / q : 0; }
+};
+
+struct Seg {
+  int t, k0, k1;
+};
+
+struct SegIter {
+  Sched s;
+  int c, t, i0, i1;
+  __device__ SegIter(const Sched& sc, int cta) : s(sc), c(cta), t(cta) {
+    i0 = (int)((long long)cta * sc.q < sc.total ? cta * sc.q : sc.total);
+    i1 = i0 + sc.q < sc.total ? i0 + sc.q : sc.total;
+  }
+  __device__ bool next(Seg& g) {
+    if (t < s.dp) {
+      g.t = t;
+      g.k0 = 0;
+      g.k1 = s.KC;
+      t += s.P;
+      return true;
+    }
+    if (i0 >= i1) return false;
+    const int r = i0 / s.KC;
+    g.t = s.dp + r;
+    g.k0 = i0 - r * s.KC;
+    g.k1 = g.k0 + i1 - i0 < s.KC ? g.k0 + i1 - i0 : s.KC;
+    i0 += g.k1 - g.k0;
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// tcgen05, TMA
+// ---------------------------------------------------------------------------
+// Shared-memory operand descriptor, 128-byte swizzle.  Rows along k (128 bytes per row):
+// groups of 8 rows are 1024 bytes apart.  Rows along the other axis (the operand lies
+// [k][64 features]): groups of 8 k are 1024 bytes apart, groups of 64 features `lead`.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// fp32 sums, both operands fp16 (bf16 = 0) or bf16, A's rows along k (a_mn = 0) or not
+__device__ __forceinline__ uint32_t mma_desc(int n, int bf16, int a_mn) {
+  return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)a_mn << 15) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kDnHalf >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(desc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tmem_alloc(uint32_t* at, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(at)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// 16 columns of this warp's 32 lanes; the values are there after tmem_wait
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// waits for this thread's tmem loads; the loaded values pass through, so that none is used before
+__device__ __forceinline__ void tmem_wait(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint64_t* bar,
+                                       uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(m), "r"(x), "r"(y), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar,
+                                       uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+}
+// four rows of a matrix, one under the other; a row index behind the last one reads zeros
+__device__ __forceinline__ void tma_rows4(uint32_t dst, const CUtensorMap* m, int x, int r0, int r1, int r2, int r3,
+                                          uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+      "l"(m), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
+// 16-bit values of either type
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float ld16(const void* p, size_t i, int bf16) {
+  const unsigned short b = reinterpret_cast<const unsigned short*>(p)[i];
+  return bf16 ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
+}
+__device__ __forceinline__ unsigned short to16(float v, int bf16) {
+  return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+__device__ __forceinline__ float from16(unsigned short b, int bf16) {
+  return bf16 ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
+}
+
+// ---------------------------------------------------------------------------
+// the ring of stages and the barriers of a CTA
+// ---------------------------------------------------------------------------
+struct DenseBars {
+  uint64_t full[kDnMaxStages];   // TMA bytes of a stage have come
+  uint64_t empty[kDnMaxStages];  // its products are done
+  uint64_t tfull[2];             // a tile's sums are in TMEM
+  uint64_t tempty[2];            // ... and have been read
+  uint64_t drain;                // on an abort: the products in flight
+  uint32_t tmem;
+  int abort;
+  int last;
+};
+
+// Bounded wait for a phase of a barrier; false when the time is over or another warp gave up.
+__device__ __forceinline__ bool dn_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  for (uint32_t i = 0; i < kWaitTries; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+  }
+  return false;
+}
+
+__device__ __forceinline__ void dn_fail(DenseBars* b, int* status) {
+  *reinterpret_cast<volatile int*>(&b->abort) = 1;
+  set_status(status, MOE_ERR_TIMEOUT);
+}
+
+__device__ __forceinline__ void dn_init_bars(DenseBars* b) {
+  for (int i = 0; i < kDnMaxStages; ++i) {
+    mbar_init(&b->full[i], 1);
+    mbar_init(&b->empty[i], 1);
+  }
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&b->tfull[i], 1);
+    mbar_init(&b->tempty[i], 4);
+  }
+  mbar_init(&b->drain, 1);
+  b->abort = 0;
+  b->last = 0;
+  fence_barrier_init();
+}
+
+// True in all `n` threads of a named barrier if any of them passes true.
+__device__ __forceinline__ bool dn_any(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred pin, pout;\n\t"
+      "setp.ne.u32 pin, %3, 0;\n\t"
+      "barrier.red.or.pred pout, %1, %2, pin;\n\t"
+      "selp.u32 %0, 1, 0, pout;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((uint32_t)v)
+      : "memory");
+  __syncwarp();
+  return r != 0;
+}
+
+// Counts the shares done of a split tile: true in every epilogue thread of the CTA whose share came
+// last.  The barrier orders the CTA's stores of its partial sums before the count, whose release
+// publishes them; the count's acquire and the second barrier order the reads that follow.
+__device__ __forceinline__ bool dn_last_share(unsigned* cnt, int parts, DenseBars* b, int etid) {
+  __syncwarp();
+  __threadfence();
+  named_barrier(1, 128);
+  if (etid == 0) {
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(cnt) : "memory");
+    b->last = old == (unsigned)(parts - 1);
+    if (b->last) *cnt = 0u;  // zero again for the next call
+  }
+  named_barrier(1, 128);
+  return b->last != 0;
+}
+
+// One stage's products of both 128-feature tiles.  `lead` = 0: A's rows lie along k.
+__device__ __forceinline__ void dn_stage_products(uint32_t a, uint32_t b, uint32_t d0, uint32_t d1, uint32_t desc,
+                                                  bool a_mn, bool first) {
+#pragma unroll
+  for (int ks = 0; ks < kDnChunk / 16; ++ks) {
+    const uint32_t ao = a_mn ? ks * 2048 : ks * 32;
+    const uint32_t lead = a_mn ? 8192 : 16;
+    const uint64_t bd = smem_desc(b + ks * 32, 16);
+    const uint32_t add = !(first && ks == 0);
+    mma_f16(d0, smem_desc(a + ao, lead), bd, desc, add);
+    mma_f16(d1, smem_desc(a + kDnBytesA / 2 + ao, lead), bd, desc, add);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host: tensor maps
+// ---------------------------------------------------------------------------
+// A map of a [z][rows][cols] 16-bit array (row stride and z stride in elements) whose box is
+// 64 columns by box_rows rows; out-of-range elements read as zeros.  z = 0: a plain matrix.
+cudaError_t dense_map(CUtensorMap* m, const void* base, int bf16, uint64_t cols, uint64_t rows, uint64_t row_stride,
+                      uint64_t z, uint64_t z_stride, uint32_t box_rows);
+
+}  // namespace sesg

@@ -1,0 +1,818 @@
+// A whole mixture-of-experts layer with uncompressed 16-bit SwiGLU experts on up to 64 tokens,
+// in one kernel:
+//
+//   l = x Wr, top-k softmax                                     (route)
+//   h = SiLU(x G^T) * (x U^T) for every (token, expert) pair       (first phase)
+//   y = sum of weight * (h D) over a token's experts               (second phase, join)
+//
+// With so few tokens the layer is bound by HBM: every active expert's 3 f d weights are read
+// once and stream through tcgen05 as the 128-row operand (dense.cuh); an expert's own tokens
+// are gathered as the other one.  One CTA per SM stays for the whole layer; three barriers over
+// the grid order its phases (cooperative launch, bounded waits), and at the second one the TMA
+// warp already streams the next phase's weights.
+//
+// h goes to the second phase as two 16-bit values, hi + lo, in two columns of the same
+// product: h = hi + lo to 2^-16 (bf16) or 2^-22 (fp16), so that y loses nothing to the operand's
+// type, at no cost in bytes from HBM (fp16: |h| > 65504 is infinite, as in fp16 arithmetic).
+// Every sum has a fixed order.
+#include "dense.cuh"
+#include "dense_params.cuh"
+
+namespace sesg {
+
+namespace {
+
+constexpr int kMaxExperts = 256;
+constexpr int kMaxActive = kMaxExperts + 8;
+constexpr int kMaxPairSlots = 16;                // k + shared experts of a token, at most
+constexpr int kPartFloats = 2 * kDenseMaxTok * kDnHalf;
+constexpr int kFewTok = 8;                       // up to here every CTA chooses the experts itself
+
+// Groups of 8 slots that the active experts' tokens fill, at most.
+__host__ __device__ inline int max_groups(int B, int E, int k, int ns) {
+  const int pairs = B * k, by_e = (E < pairs ? E : pairs) + pairs / 8;
+  return (pairs < by_e ? pairs : by_e) + ns * ((B + 7) / 8);
+}
+
+struct LayerArgs {
+  int B, d, f, E, k, ns, renorm, rmsnorm, bf16;
+  const void *x, *w_router, *residual;
+  void* y;
+  int32_t* user_idx;
+  float* user_w;
+  DenseHead* head;
+  float* logits;       // [B][slices][E]
+  int* top_idx;        // [B][k]
+  float* top_w;
+  unsigned short* h;   // [groups][hi, lo][8][f]
+  float* part;         // [segment][gate, up][64][128]
+  float* ypart;        // [share][8 groups][d]
+  int slots;           // 8 * max_groups
+  int slices;          // router: CTAs per token
+  int stages, stage_bytes;
+};
+
+struct LayerMisc {
+  DenseBars bars;
+  unsigned long long mask[kMaxExperts];  // tokens of each routed expert
+  short where[kMaxExperts];              // its place among the active ones
+  short act[kMaxActive];                 // active experts: shared ones (E + s) first
+  short cnt[kMaxActive];                 // ... tokens
+  short grp[kMaxActive];                 // ... first group of 8 slots
+  int n_act;
+  int last;
+  int fail;
+  int idx[kDenseMaxTok * 8];
+  float w[kDenseMaxTok * 8];
+  short row[kDenseMaxTok * kMaxPairSlots];    // slot of each (token, choice)
+  short place[kDenseMaxTok * kMaxPairSlots];  // active expert of each (token, choice)
+  float sum[8];
+};
+
+// Arrive at / wait for barrier i over the grid.  All CTAs are resident (cooperative launch).
+__device__ __forceinline__ void grid_arrive(unsigned* bar) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(bar) : "memory");
+}
+__device__ __forceinline__ bool grid_wait(unsigned* bar, volatile int* abort) {
+  for (int i = 0; i < (1 << 22); ++i) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(bar) : "memory");
+    if (v >= gridDim.x) return true;
+    if (*abort) return false;
+  }
+  return false;
+}
+
+// Logits of token b over the rows [r0, r1) of the router weight, to out[E].  A thread owns EV
+// neighbouring experts and every nrs-th row; red: 256 * EV floats.
+template <int EV>
+__device__ void slice_logits(const LayerArgs& p, int b, int r0, int r1, float* out, float* red) {
+  constexpr int RU = 8;
+  const int tid = threadIdx.x, nchunk = p.E / EV, nrs = kDnThreads / nchunk;
+  const int ec = tid % nchunk, rs = tid / nchunk;
+  float acc[EV];
+#pragma unroll
+  for (int i = 0; i < EV; ++i) acc[i] = 0.f;
+  if (rs < nrs) {
+    for (int q = r0 + rs; q < r1; q += nrs * RU) {
+      float xv[RU];
+      uint4 wv[RU];
+#pragma unroll
+      for (int u = 0; u < RU; ++u) {
+        const int r = q + u * nrs;
+        xv[u] = 0.f;
+        wv[u] = make_uint4(0, 0, 0, 0);
+        if (r < r1) {
+          xv[u] = ld16(p.x, (size_t)b * p.d + r, p.bf16);
+          const unsigned short* wr = reinterpret_cast<const unsigned short*>(p.w_router) + (size_t)r * p.E + ec * EV;
+          if constexpr (EV == 8) wv[u] = *reinterpret_cast<const uint4*>(wr);
+          else wv[u].x = wr[0];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < RU; ++u) {
+        const uint32_t w4[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
+#pragma unroll
+        for (int i = 0; i < EV; ++i)
+          acc[i] = fmaf(xv[u], from16((unsigned short)(w4[i / 2] >> (16 * (i & 1))), p.bf16), acc[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < EV; ++i) red[rs * p.E + ec * EV + i] = acc[i];
+  }
+  __syncthreads();
+  const int lane = tid & 31;
+  for (int e = tid >> 5; e < p.E; e += kDnThreads / 32) {
+    float s = 0.f;
+    for (int r = lane; r < nrs; r += 32) s += red[r * p.E + e];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (lane == 0) __stcg(out + e, s);
+  }
+}
+
+// One warp: token b's logits (the slices added in order), its k experts by logit descending (ties:
+// the lower index; NaN ranks as -inf) and their weights.
+__device__ void choose(const LayerArgs& p, int b, int* idx, float* w) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kPer = kMaxExperts / 32;
+  float l[kPer];
+  uint32_t taken = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane + 32 * i;
+    l[i] = -INFINITY;
+    if (e < p.E) {
+      float s = 0.f;
+      for (int q = 0; q < p.slices; ++q) s += __ldcg(p.logits + ((size_t)b * p.slices + q) * p.E + e);
+      if (!isnan(s)) l[i] = s;
+    } else {
+      taken |= 1u << i;
+    }
+  }
+  float mine = 0.f, top = -INFINITY;  // lane j keeps the j-th choice
+  int mine_e = 0;
+  for (int j = 0; j < p.k; ++j) {
+    float best = -INFINITY;
+    int at = 0x7fffffff;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = lane + 32 * i;
+      if (!(taken >> i & 1) && (l[i] > best || (l[i] == best && e < at))) {
+        best = l[i];
+        at = e;
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      const float ob = __shfl_xor_sync(0xffffffffu, best, off);
+      const int oa = __shfl_xor_sync(0xffffffffu, at, off);
+      if (ob > best || (ob == best && oa < at)) {
+        best = ob;
+        at = oa;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (lane + 32 * i == at) taken |= 1u << i;
+    if (j == 0) top = best;
+    if (lane == j) {
+      mine = best;
+      mine_e = at;
+    }
+  }
+  float sum = 0.f;
+  if (p.renorm) {
+    for (int j = 0; j < p.k; ++j) sum += expf(__shfl_sync(0xffffffffu, mine, j) - top);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (lane + 32 * i < p.E) sum += expf(l[i] - top);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  }
+  if (lane < p.k) {
+    idx[b * p.k + lane] = mine_e;
+    w[b * p.k + lane] = expf(mine - top) / sum;
+  }
+}
+
+// Routing of every token into m.idx / m.w.  False: a wait ran out.
+__device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
+  const int tid = threadIdx.x, warp = tid >> 5, cta = blockIdx.x;
+  const bool few = p.B <= kFewTok;
+  if (cta < p.B * p.slices) {
+    const int b = cta / p.slices, s = cta - b * p.slices;
+    const int len = (p.d + p.slices - 1) / p.slices;
+    const int r0 = s * len, r1 = r0 + len < p.d ? r0 + len : p.d;
+    float* out = p.logits + ((size_t)b * p.slices + s) * p.E;
+    if (p.E % 8 == 0) slice_logits<8>(p, b, r0, r1, out, scratch);
+    else slice_logits<1>(p, b, r0, r1, out, scratch);
+    __threadfence();
+    __syncthreads();
+    if (!few) {
+      // the token's last slice to come chooses its experts
+      if (tid == 0) {
+        unsigned old;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(&p.head->tok[b]) : "memory");
+        m.last = old == (unsigned)(p.slices - 1);
+        if (m.last) p.head->tok[b] = 0u;
+      }
+      __syncthreads();
+      if (m.last && warp == 0) {
+        choose(p, b, p.top_idx, p.top_w);
+        __threadfence();
+      }
+      __syncthreads();
+    }
+  }
+  if (tid == 0) {
+    grid_arrive(&p.head->bar[0]);
+    m.fail = !grid_wait(&p.head->bar[0], &m.bars.abort);
+  }
+  __syncthreads();
+  if (m.fail) return false;
+  if (few) {
+    if (warp < p.B) choose(p, warp, m.idx, m.w);
+  } else {
+    for (int i = tid; i < p.B * p.k; i += kDnThreads) {
+      m.idx[i] = __ldcg(p.top_idx + i);
+      m.w[i] = __ldcg(p.top_w + i);
+    }
+  }
+  __syncthreads();
+  if (cta == 0) {
+    for (int i = tid; i < p.B * p.k; i += kDnThreads) {
+      if (p.user_idx) p.user_idx[i] = m.idx[i];
+      if (p.user_w) p.user_w[i] = m.w[i];
+    }
+  }
+  return true;
+}
+
+// The active experts, their tokens in ascending order, and the slot of every (token, choice).
+__device__ void make_lists(const LayerArgs& p, LayerMisc& m, uint8_t* tok) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int pairs = p.B * p.k, gs = (p.B + 7) / 8;
+  for (int e = tid; e < p.E; e += kDnThreads) m.mask[e] = 0ull;
+  for (int i = tid; i < p.slots; i += kDnThreads) tok[i] = (uint8_t)p.B;  // no token
+  __syncthreads();
+  for (int i = tid; i < pairs; i += kDnThreads) atomicOr(&m.mask[m.idx[i]], 1ull << (i / p.k));
+  __syncthreads();
+  if (tid < 32) {
+    if (lane < p.ns) {
+      m.act[lane] = (short)(p.E + lane);
+      m.cnt[lane] = (short)p.B;
+      m.grp[lane] = (short)(lane * gs);
+    }
+    int na = p.ns, ng = p.ns * gs;
+    for (int base = 0; base < p.E; base += 32) {
+      const int e = base + lane;
+      const int n = e < p.E ? __popcll(m.mask[e]) : 0, g = (n + 7) / 8;
+      const uint32_t on = __ballot_sync(0xffffffffu, n > 0);
+      int sg = g;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, sg, off);
+        if (lane >= off) sg += o;
+      }
+      if (n > 0) {
+        const int a = na + __popc(on & ((1u << lane) - 1));
+        m.act[a] = (short)e;
+        m.cnt[a] = (short)n;
+        m.grp[a] = (short)(ng + sg - g);
+        m.where[e] = (short)a;
+      }
+      na += __popc(on);
+      ng += __shfl_sync(0xffffffffu, sg, 31);
+    }
+    if (lane == 0) m.n_act = na;
+  }
+  __syncthreads();
+  for (int i = tid; i < pairs; i += kDnThreads) {
+    const int b = i / p.k, j = i - b * p.k, e = m.idx[i], a = m.where[e];
+    const int row = m.grp[a] * 8 + __popcll(m.mask[e] & ((1ull << b) - 1));
+    tok[row] = (uint8_t)b;
+    m.row[b * kMaxPairSlots + j] = (short)row;
+    m.place[b * kMaxPairSlots + j] = (short)a;
+  }
+  for (int i = tid; i < p.B * p.ns; i += kDnThreads) {
+    const int s = i / p.B, b = i - s * p.B, row = s * gs * 8 + b;
+    tok[row] = (uint8_t)b;
+    m.row[b * kMaxPairSlots + p.k + s] = (short)row;
+    m.place[b * kMaxPairSlots + p.k + s] = (short)s;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void store_h(const LayerArgs& p, int slot, int feat, float g, float u) {
+  const float h = silu_f(g) * u;
+  const unsigned short hi = to16(h, p.bf16);
+  const float hf = from16(hi, p.bf16);
+  const unsigned short lo = isfinite(hf) ? to16(h - hf, p.bf16) : (unsigned short)0;
+  const size_t at = ((size_t)(slot >> 3) * 16 + (slot & 7)) * p.f + feat;
+  p.h[at] = hi;
+  p.h[at + (size_t)8 * p.f] = lo;
+}
+
+struct LayerMaps {
+  CUtensorMap gate, up, down;        // routed experts
+  CUtensorMap sgate, sup, sdown;     // shared experts
+  CUtensorMap x, h;
+};
+
+__global__ void __launch_bounds__(kDnThreads, 1)
+dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  LayerMisc& m = *reinterpret_cast<LayerMisc*>(ring + (size_t)p.stages * p.stage_bytes);
+  uint8_t* tok = reinterpret_cast<uint8_t*>(&m + 1);
+  DenseBars* bars = &m.bars;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  const int S = p.stages;
+  int* status = &p.head->ctrl.status;
+  volatile int* abort = &bars->abort;
+
+  if (tid == 0) {
+    dn_init_bars(bars);
+    m.fail = 0;
+  }
+  if (warp == 2) tmem_alloc(&bars->tmem, 512);
+  tc_before_sync();
+  __syncthreads();
+  tc_after_sync();
+  const uint32_t tmem = bars->tmem;
+
+  bool ok = true;
+  if (p.E > 0) ok = route(p, m, reinterpret_cast<float*>(ring));
+  if (!ok && tid == 0) dn_fail(bars, status);
+  if (ok) make_lists(p, m, tok);
+  // the ring was scratch of the router: its generic accesses come before the copies into it
+  fence_proxy_async_smem();
+  __syncthreads();
+
+  const int FT = (p.f + kDnHalf - 1) / kDnHalf, DT = (p.d + 2 * kDnHalf - 1) / (2 * kDnHalf);
+  const Sched s1 = Sched::make(m.n_act * FT, (p.d + kDnChunk - 1) / kDnChunk, gridDim.x);
+  const Sched s2 = Sched::make(m.n_act * DT, (p.f + kDnChunk - 1) / kDnChunk, gridDim.x);
+
+  if (!ok) {
+  } else if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pw = policy_evict_first(), px = policy_evict_normal();
+      int st = 0, issued = 0;
+      uint32_t ph = 0;
+      auto advance = [&](int& s, uint32_t& h) {
+        if (++s == S) {
+          s = 0;
+          h ^= 1;
+        }
+      };
+      Seg g;
+      SegIter it(s1, cta);
+      bool go = true;
+      while (go && it.next(g)) {
+        const int a = g.t / FT, f0 = (g.t - a * FT) * kDnHalf;
+        const int e = m.act[a], n4 = (m.cnt[a] + 3) / 4, row = m.grp[a] * 8;
+        const bool sh = e >= p.E;
+        const int z = sh ? e - p.E : e;
+        const CUtensorMap *mg = sh ? &maps.sgate : &maps.gate, *mu = sh ? &maps.sup : &maps.up;
+        for (int kc = g.k0; kc < g.k1; ++kc) {
+          if (!dn_wait(&bars->empty[st], ph ^ 1, abort)) {
+            dn_fail(bars, status);
+            go = false;
+            break;
+          }
+          uint64_t* full = &bars->full[st];
+          mbar_arrive_expect_tx(full, kDnBytesA + n4 * 512);
+          ++issued;
+          const uint32_t at = smem_addr(ring + (size_t)st * p.stage_bytes);
+          const int k = kc * kDnChunk;
+          tma_3d(at, mg, k, f0, z, full, pw);
+          tma_3d(at + kDnBytesA / 2, mu, k, f0, z, full, pw);
+          for (int i = 0; i < n4; ++i) {
+            const uint8_t* t = tok + row + 4 * i;
+            tma_rows4(at + kDnBytesA + i * 512, &maps.x, k, t[0], t[1], t[2], t[3], full, px);
+          }
+          advance(st, ph);
+        }
+      }
+      // second phase: the weights of the first stages are asked for before the grid's h is there
+      auto load_down = [&](const Seg& q, int kc, int stage) {
+        const int a = q.t / DT, d0 = (q.t - a * DT) * 2 * kDnHalf, e = m.act[a], ng = (m.cnt[a] + 7) / 8;
+        const bool sh = e >= p.E;
+        const CUtensorMap* md = sh ? &maps.sdown : &maps.down;
+        uint64_t* full = &bars->full[stage];
+        mbar_arrive_expect_tx(full, kDnBytesA + ng * 2048);
+        const uint32_t at = smem_addr(ring + (size_t)stage * p.stage_bytes);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          tma_3d(at + i * 8192, md, d0 + 64 * i, kc * kDnChunk, sh ? e - p.E : e, full, pw);
+      };
+      auto load_h = [&](const Seg& q, int kc, int stage) {
+        const int a = q.t / DT, ng = (m.cnt[a] + 7) / 8, row = m.grp[a] * 16;
+        const uint32_t at = smem_addr(ring + (size_t)stage * p.stage_bytes) + kDnBytesA;
+        for (int i = 0; i < ng; ++i)
+          tma_2d(at + i * 2048, &maps.h, kc * kDnChunk, row + 16 * i, &bars->full[stage], px);
+      };
+      SegIter w2(s2, cta), h2(s2, cta);
+      Seg gw, gh;
+      bool more = go && w2.next(gw);
+      int kw = more ? gw.k0 : 0, hs = st, ahead = 0;
+      uint32_t hp = ph;
+      bool hmore = more && h2.next(gh), waited = false;
+      int kh = hmore ? gh.k0 : 0;
+      while (go && hmore) {
+        // weights as far ahead as there are stages, then the h of the oldest of them
+        while (more && ahead < (waited ? 1 : S)) {
+          if (!dn_wait(&bars->empty[st], ph ^ 1, abort)) {
+            dn_fail(bars, status);
+            go = false;
+            break;
+          }
+          load_down(gw, kw, st);
+          ++issued;
+          ++ahead;
+          advance(st, ph);
+          if (++kw == gw.k1) {
+            more = w2.next(gw);
+            if (more) kw = gw.k0;
+          }
+        }
+        if (!go) break;
+        if (!waited) {
+          waited = true;
+          if (!grid_wait(&p.head->bar[1], abort)) {
+            dn_fail(bars, status);
+            break;
+          }
+          fence_proxy_async_all();  // the other CTAs' stores of h before this thread's copies of it
+        }
+        load_h(gh, kh, hs);
+        --ahead;
+        advance(hs, hp);
+        if (++kh == gh.k1) {
+          hmore = h2.next(gh);
+          if (hmore) kh = gh.k0;
+        }
+      }
+      // no copy of this CTA is in flight when it ends.  Stages whose h was never asked for (an
+      // abort) cannot complete: their weights have come long before this bounded wait is over.
+      const int n = issued < S ? issued : S;
+      for (int i = 0; i < n; ++i) {
+        if (--st < 0) {
+          st = S - 1;
+          ph ^= 1;
+        }
+        for (uint32_t w = 0; w < (*abort ? 8u : kWaitTries) && !mbar_try_wait(&bars->full[st], ph); ++w) {}
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int st = 0, buf = 0;
+      uint32_t ph = 0, tph = 0;
+      bool go = true, open = false;
+      Seg g;
+#pragma unroll 1
+      for (int phase = 0; phase < 2 && go; ++phase) {
+        const Sched& sc = phase ? s2 : s1;
+        const int TT = phase ? DT : FT;
+        SegIter it(sc, cta);
+        while (go && it.next(g)) {
+          const int n = m.cnt[g.t / TT];
+          const uint32_t desc = mma_desc(phase ? (n + 7) / 8 * 16 : (n + 15) / 16 * 16, p.bf16, phase);
+          if (!dn_wait(&bars->tempty[buf], tph ^ 1, abort)) {
+            dn_fail(bars, status);
+            go = false;
+            break;
+          }
+          tc_after_sync();
+          const uint32_t d0 = tmem + buf * 256;
+          for (int kc = g.k0; kc < g.k1; ++kc) {
+            if (!dn_wait(&bars->full[st], ph, abort)) {
+              dn_fail(bars, status);
+              go = false;
+              break;
+            }
+            tc_after_sync();
+            const uint32_t a = smem_addr(ring + (size_t)st * p.stage_bytes);
+            dn_stage_products(a, a + kDnBytesA, d0, d0 + 128, desc, phase != 0, kc == g.k0);
+            mma_commit(&bars->empty[st]);
+            open = true;
+            if (++st == S) {
+              st = 0;
+              ph ^= 1;
+            }
+          }
+          if (!go) break;
+          mma_commit(&bars->tfull[buf]);
+          buf ^= 1;
+          tph ^= buf == 0;
+        }
+      }
+      if (open) {
+        mma_commit(&bars->drain);
+        for (uint32_t w = 0; w < kWaitTries && !mbar_try_wait(&bars->drain, 0); ++w) {}
+      }
+    }
+  } else if (warp >= 4) {
+    const int q = warp - 4, r = q * 32 + lane, etid = tid - 128;
+    int buf = 0;
+    uint32_t tph = 0;
+    bool go = true;
+    Seg g;
+    {
+      SegIter it(s1, cta);
+      while (it.next(g)) {
+        const bool good = dn_wait(&bars->tfull[buf], tph, abort);
+        if (!good) dn_fail(bars, status);
+        if (dn_any(1, 128, !good)) {
+          go = false;
+          break;
+        }
+        tc_after_sync();
+        const int a = g.t / FT, feat = (g.t - a * FT) * kDnHalf + r, n = m.cnt[a], slot = m.grp[a] * 8;
+        const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + buf * 256;
+        const int parts = s1.parts(g.t);
+        float* mine = p.part + ((size_t)(g.t - s1.dp) + cta) * kPartFloats + r;  // used where parts > 1
+        for (int n0 = 0; n0 < n; n0 += 16) {
+          float vg[16], vu[16];
+          tmem_ld16(t0 + n0, vg);
+          tmem_ld16(t0 + 128 + n0, vu);
+          tmem_wait(vg);
+          tmem_wait(vu);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (n0 + i < n) {
+              if (parts == 1) {
+                if (feat < p.f) store_h(p, slot + n0 + i, feat, vg[i], vu[i]);
+              } else {
+                __stcg(mine + (n0 + i) * kDnHalf, vg[i]);
+                __stcg(mine + (kDenseMaxTok + n0 + i) * kDnHalf, vu[i]);
+              }
+            }
+          }
+        }
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->tempty[buf]);
+        if (parts > 1 && dn_last_share(&p.head->cnt[g.t - s1.dp], parts, bars, etid) && feat < p.f) {
+          const float* from = p.part + ((size_t)(g.t - s1.dp) + s1.first(g.t)) * kPartFloats + r;
+          for (int n0 = 0; n0 < n; n0 += 8) {
+            float vg[8], vu[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) vg[i] = vu[i] = 0.f;
+            for (int s = 0; s < parts; ++s) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (n0 + i < n) {
+                  vg[i] += __ldcg(from + (size_t)s * kPartFloats + (n0 + i) * kDnHalf);
+                  vu[i] += __ldcg(from + (size_t)s * kPartFloats + (kDenseMaxTok + n0 + i) * kDnHalf);
+                }
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (n0 + i < n) store_h(p, slot + n0 + i, feat, vg[i], vu[i]);
+          }
+        }
+        buf ^= 1;
+        tph ^= buf == 0;
+      }
+    }
+    __syncwarp();
+    if (go) {
+      // this CTA's h: its stores before the other CTAs' copies (which the async proxy makes)
+      __threadfence();
+      fence_proxy_async_all();
+      named_barrier(1, 128);
+      if (etid == 0) grid_arrive(&p.head->bar[1]);
+      SegIter it(s2, cta);
+      while (it.next(g)) {
+        const bool good = dn_wait(&bars->tfull[buf], tph, abort);
+        if (!good) dn_fail(bars, status);
+        if (dn_any(1, 128, !good)) break;
+        tc_after_sync();
+        const int a = g.t / DT, feat = (g.t - a * DT) * 2 * kDnHalf + r, n = m.cnt[a], slot = m.grp[a] * 8;
+        const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + buf * 256;
+        const int share = s2.parts(g.t) == 1 ? 0 : cta - s2.first(g.t);
+        float* out = p.ypart + ((size_t)share * p.slots + slot) * p.d + feat;
+        for (int n0 = 0; n0 < n; n0 += 8) {  // columns: 8 tokens' hi, then their lo
+          float va[16], vb[16];
+          tmem_ld16(t0 + 2 * n0, va);
+          tmem_ld16(t0 + 128 + 2 * n0, vb);
+          tmem_wait(va);
+          tmem_wait(vb);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (n0 + i < n) {
+              if (feat < p.d) __stcg(out + (size_t)(n0 + i) * p.d, va[i] + va[i + 8]);
+              if (feat + kDnHalf < p.d) __stcg(out + (size_t)(n0 + i) * p.d + kDnHalf, vb[i] + vb[i + 8]);
+            }
+          }
+        }
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->tempty[buf]);
+        buf ^= 1;
+        tph ^= buf == 0;
+      }
+      __threadfence();
+    }
+  }
+  __syncwarp();
+  tc_before_sync();
+  __syncthreads();
+  tc_after_sync();
+  if (warp == 2) tmem_free(tmem, 512);
+
+  // join: every token's experts and their shares, in order
+  if (tid == 0) {
+    if (!*abort) {
+      grid_arrive(&p.head->bar[2]);
+      if (!grid_wait(&p.head->bar[2], abort)) dn_fail(bars, status);
+    }
+    m.fail = *abort;
+  }
+  __syncthreads();
+  if (m.fail) return;
+  const int units = p.rmsnorm ? p.B : p.B * DT;
+  float* row = reinterpret_cast<float*>(ring);
+  for (int u = cta; u < units; u += gridDim.x) {
+    const int b = p.rmsnorm ? u : u / DT;
+    const int dt0 = p.rmsnorm ? 0 : u - b * DT, dt1 = p.rmsnorm ? DT : dt0 + 1;
+    float sq = 0.f;
+    for (int dt = dt0; dt < dt1; ++dt) {
+      const int feat = dt * 2 * kDnHalf + tid;
+      if (feat < p.d) {
+        float acc = 0.f;
+        for (int j = 0; j < p.k + p.ns; ++j) {
+          const int a = m.place[b * kMaxPairSlots + j], slot = m.row[b * kMaxPairSlots + j];
+          const int parts = s2.parts(a * DT + dt);
+          float v = 0.f;
+          for (int s = 0; s < parts; ++s) v += __ldcg(p.ypart + ((size_t)s * p.slots + slot) * p.d + feat);
+          acc = fmaf(j < p.k ? m.w[b * p.k + j] : 1.f, v, acc);
+        }
+        if (p.residual) acc += ld16(p.residual, (size_t)b * p.d + feat, p.bf16);
+        if (p.rmsnorm) {
+          row[feat] = acc;
+          sq = fmaf(acc, acc, sq);
+        } else {
+          reinterpret_cast<unsigned short*>(p.y)[(size_t)b * p.d + feat] = to16(acc, p.bf16);
+        }
+      }
+    }
+    if (p.rmsnorm) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, off);
+      if (lane == 0) m.sum[warp] = sq;
+      __syncthreads();
+      float t = 0.f;
+#pragma unroll
+      for (int i = 0; i < kDnThreads / 32; ++i) t += m.sum[i];
+      const float scale = rsqrtf(t / (float)p.d + 1e-6f);
+      for (int feat = tid; feat < p.d; feat += kDnThreads)
+        reinterpret_cast<unsigned short*>(p.y)[(size_t)b * p.d + feat] = to16(row[feat] * scale, p.bf16);
+      __syncthreads();
+    }
+  }
+  // the last CTA to leave clears the barriers for the next call
+  if (tid == 0) {
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(&p.head->bar[3]) : "memory");
+    if (old == gridDim.x - 1) {
+      for (int i = 0; i < 4; ++i) p.head->bar[i] = 0u;
+    }
+  }
+}
+
+struct LayerPlan {
+  int B = -1, d, f, E, k, ns, sms;
+  int groups, slices, grid;
+  size_t logits, top_idx, top_w, h, part, ypart, total;
+};
+
+// The plan goes by the sizes alone; a thread keeps the last one, since a program calls with the same
+// sizes again and again.
+const LayerPlan& layer_plan(int B, int d, int f, int E, int k, int ns, int sms) {
+  static thread_local LayerPlan l;
+  if (l.B == B && l.d == d && l.f == f && l.E == E && l.k == k && l.ns == ns && l.sms == sms) return l;
+  l.B = B;
+  l.d = d;
+  l.f = f;
+  l.E = E;
+  l.k = k;
+  l.ns = ns;
+  l.sms = sms;
+  l.grid = sms;
+  l.groups = max_groups(B, E, k, ns);
+  l.slices = B > 0 ? sms / B : 1;
+  const int most = (d + 63) / 64;  // 64 rows of the router weight at least
+  if (l.slices > 32) l.slices = 32;
+  if (l.slices > most) l.slices = most;
+  if (l.slices < 1) l.slices = 1;
+  const int FT = (f + kDnHalf - 1) / kDnHalf, DT = (d + 2 * kDnHalf - 1) / (2 * kDnHalf);
+  const int KC1 = (d + kDnChunk - 1) / kDnChunk, KC2 = (f + kDnChunk - 1) / kDnChunk;
+  // the number of active experts is known on the device only: the largest need of any
+  int segs = 0, parts = 1;
+  const int most_act = (E < B * k ? E : B * k) + ns;
+  for (int a = 1; a <= most_act; ++a) {
+    const Sched s1 = Sched::make(a * FT, KC1, sms), s2 = Sched::make(a * DT, KC2, sms);
+    if (s1.segments() > segs) segs = s1.segments();
+    if (s2.max_parts() > parts) parts = s2.max_parts();
+  }
+  size_t o = (sizeof(DenseHead) + 255) / 256 * 256;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = (o + bytes + 255) / 256 * 256;
+    return at;
+  };
+  l.logits = take((size_t)B * l.slices * E * 4);
+  l.top_idx = take((size_t)B * k * 4);
+  l.top_w = take((size_t)B * k * 4);
+  l.h = take((size_t)l.groups * 16 * f * 2);
+  l.part = take((size_t)segs * kPartFloats * 4);
+  l.ypart = take((size_t)parts * l.groups * 8 * d * 4);
+  l.total = o;
+  return l;
+}
+
+}  // namespace
+
+size_t dense_layer_ws_bytes(int B, int d, int f, int E, int k, int ns, int sms) {
+  return layer_plan(B, d, f, E, k, ns, sms).total;
+}
+
+cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int smem_optin, cudaStream_t st) {
+  const LayerPlan& l = layer_plan(c.B, c.d, c.f, c.routed.E, c.k, c.shared.E, sms);
+  uint8_t* w8 = reinterpret_cast<uint8_t*>(ws);
+  LayerMaps maps;
+  cudaError_t e = cudaSuccess;
+  auto set_maps = [&](const DenseExpertSet& s, CUtensorMap* g, CUtensorMap* u, CUtensorMap* d) {
+    if (e == cudaSuccess)
+      e = dense_map(g, s.gate_t, c.bf16, c.d, c.f, s.gate_rs, s.E, s.gate_rs * c.f, kDnHalf);
+    if (e == cudaSuccess) e = dense_map(u, s.up_t, c.bf16, c.d, c.f, s.up_rs, s.E, s.up_rs * c.f, kDnHalf);
+    if (e == cudaSuccess) e = dense_map(d, s.down, c.bf16, c.d, c.f, s.down_rs, s.E, s.down_rs * c.f, kDnChunk);
+  };
+  if (c.routed.E > 0) set_maps(c.routed, &maps.gate, &maps.up, &maps.down);
+  if (c.shared.E > 0) set_maps(c.shared, &maps.sgate, &maps.sup, &maps.sdown);
+  if (c.routed.E == 0) {
+    maps.gate = maps.sgate;
+    maps.up = maps.sup;
+    maps.down = maps.sdown;
+  }
+  if (c.shared.E == 0) {
+    maps.sgate = maps.gate;
+    maps.sup = maps.up;
+    maps.sdown = maps.down;
+  }
+  if (e == cudaSuccess) e = dense_map(&maps.x, c.x, c.bf16, c.d, c.B, c.d, 0, 0, 1);
+  if (e == cudaSuccess) e = dense_map(&maps.h, w8 + l.h, c.bf16, c.f, (uint64_t)l.groups * 16, c.f, 0, 0, 16);
+  if (e != cudaSuccess) return e;
+  LayerArgs p;
+  p.B = c.B;
+  p.d = c.d;
+  p.f = c.f;
+  p.E = c.routed.E;
+  p.k = c.k;
+  p.ns = c.shared.E;
+  p.renorm = c.renorm;
+  p.rmsnorm = c.rmsnorm;
+  p.bf16 = c.bf16;
+  p.x = c.x;
+  p.w_router = c.w_router;
+  p.residual = c.residual;
+  p.y = c.y;
+  p.user_idx = c.user_idx;
+  p.user_w = c.user_w;
+  p.head = reinterpret_cast<DenseHead*>(ws);
+  p.logits = reinterpret_cast<float*>(w8 + l.logits);
+  p.top_idx = reinterpret_cast<int*>(w8 + l.top_idx);
+  p.top_w = reinterpret_cast<float*>(w8 + l.top_w);
+  p.h = reinterpret_cast<unsigned short*>(w8 + l.h);
+  p.part = reinterpret_cast<float*>(w8 + l.part);
+  p.ypart = reinterpret_cast<float*>(w8 + l.ypart);
+  p.slots = l.groups * 8;
+  p.slices = l.slices;
+  p.stage_bytes = kDnBytesA + (c.B + 7) / 8 * 16 * 128;
+  const int fixed = 1024 + (int)sizeof(LayerMisc) + p.slots;
+  int S = (smem_optin - fixed) / p.stage_bytes;
+  p.stages = S > kDnMaxStages ? kDnMaxStages : S;
+  // RMSNorm keeps a token's row of sums in the ring
+  if (p.stages < 2 || (size_t)c.d * 4 > (size_t)p.stages * p.stage_bytes) return cudaErrorInvalidValue;
+  const size_t smem = fixed + (size_t)p.stages * p.stage_bytes;
+  e = cudaFuncSetAttribute(dense_layer_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(l.grid);
+  cfg.blockDim = dim3(kDnThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, dense_layer_kernel, maps, p);
+}
+
+}  // namespace sesg

@@ -1,0 +1,42 @@
+// Parameter blocks and launchers of the kernels on uncompressed weights.
+#pragma once
+
+#include "params.cuh"
+
+namespace sesg {
+
+struct LinearCall {
+  int M, N, K;
+  int bf16;             // x, w, bias, residual (and y unless out_f32): bf16, else fp16
+  int kn;               // w is [K][N], else [N][K]
+  int act;              // MOE_ACT_*
+  int out_f32;
+  const void *x, *w, *w_mul, *bias, *bias_mul, *residual;
+  void* y;
+  size_t w_stride, w_mul_stride;  // elements between rows
+};
+
+size_t linear_ws_bytes(int M, int N, int K, bool gated, int sms);
+cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin, cudaStream_t st);
+
+struct DenseExpertSet {
+  int E;
+  const void *gate_t, *up_t, *down;  // [E][f][d]
+  size_t gate_rs, up_rs, down_rs;    // elements between rows
+};
+
+struct DenseLayerCall {
+  int B, d, f, k, renorm, rmsnorm, bf16;
+  DenseExpertSet routed, shared;     // routed.E = 0: no routing
+  const void *x, *w_router, *residual;
+  void* y;
+  int32_t* user_idx;                 // optional copies of the routing
+  float* user_w;
+};
+
+constexpr int kDenseMaxTok = 64;
+
+size_t dense_layer_ws_bytes(int B, int d, int f, int E, int k, int ns, int sms);
+cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int smem_optin, cudaStream_t st);
+
+}  // namespace sesg
