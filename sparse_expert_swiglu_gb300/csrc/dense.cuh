@@ -18,7 +18,8 @@
 
 namespace sesg {
 
-constexpr int kDnThreads = 256;      // warps: 0 TMA, 1 products, 2 TMEM, 4-7 epilogue
+constexpr int kDnThreads = 384;      // warps: 0 TMA, 1 products, 2 TMEM, 4-11 epilogue
+constexpr int kDnEpi = 256;          // ... threads: two warps for every 32 TMEM lanes
 constexpr int kDnChunk = 64;         // k per stage: 128 bytes, one swizzled row
 constexpr int kDnHalf = 128;         // features of one product (TMEM lanes)
 constexpr int kDnBytesA = 2 * kDnHalf * kDnChunk * 2;
@@ -235,7 +236,7 @@ __device__ __forceinline__ void dn_init_bars(DenseBars* b) {
   }
   for (int i = 0; i < 2; ++i) {
     mbar_init(&b->tfull[i], 1);
-    mbar_init(&b->tempty[i], 4);
+    mbar_init(&b->tempty[i], kDnEpi / 32);
   }
   mbar_init(&b->drain, 1);
   b->abort = 0;
@@ -264,15 +265,40 @@ __device__ __forceinline__ bool dn_any(int id, int n, bool v) {
 __device__ __forceinline__ bool dn_last_share(unsigned* cnt, int parts, DenseBars* b, int etid) {
   __syncwarp();
   __threadfence();
-  named_barrier(1, 128);
+  named_barrier(1, kDnEpi);
   if (etid == 0) {
     unsigned old;
     asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(cnt) : "memory");
     b->last = old == (unsigned)(parts - 1);
     if (b->last) *cnt = 0u;  // zero again for the next call
   }
-  named_barrier(1, 128);
+  named_barrier(1, kDnEpi);
   return b->last != 0;
+}
+
+// v[i] = the sum over a split tile's shares, in order, of from[share * stride + i * 128], for i < n.
+// The loads of 16 values are in flight together: few tokens, many shares at a time.
+template <int G>
+__device__ __forceinline__ void sum_shares_by(const float* from, size_t stride, int parts, int n, float (&v)[16]) {
+  constexpr int U = G >= 16 ? 2 : 16 / G;
+  for (int s = 0; s < parts; s += U) {
+    float t[U][G];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < G; ++i) t[u][i] = s + u < parts && i < n ? __ldcg(from + (s + u) * stride + i * 128) : 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < G; ++i) v[i] += t[u][i];
+  }
+}
+__device__ __forceinline__ void sum_shares(const float* from, size_t stride, int parts, int n, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = 0.f;
+  if (n <= 1) sum_shares_by<1>(from, stride, parts, n, v);
+  else if (n <= 4) sum_shares_by<4>(from, stride, parts, n, v);
+  else sum_shares_by<16>(from, stride, parts, n, v);
 }
 
 // One stage's products of both 128-feature tiles.  `lead` = 0: A's rows lie along k.

@@ -47,6 +47,8 @@ struct LayerArgs {
   unsigned short* h;   // [groups][hi, lo][8][f]
   float* part;         // [segment][gate, up][64][128]
   float* ypart;        // [share][8 groups][d]
+  float* yrow;         // [B][d] sums before RMSNorm
+  float* ysq;          // [B][256-feature tiles] their squares
   int slots;           // 8 * max_groups
   int slices;          // router: CTAs per token
   int stages, stage_bytes;
@@ -66,7 +68,11 @@ struct LayerMisc {
   float w[kDenseMaxTok * 8];
   short row[kDenseMaxTok * kMaxPairSlots];    // slot of each (token, choice)
   short place[kDenseMaxTok * kMaxPairSlots];  // active expert of each (token, choice)
-  float sum[8];
+  float sum[kDnThreads / 32];
+  // a token's partial sums: where they begin and their weights
+  size_t from[kMaxPairSlots * (kDnMaxSplit + 1)];
+  float weight[kMaxPairSlots * (kDnMaxSplit + 1)];
+  int n_from;
 };
 
 // Arrive at / wait for barrier i over the grid.  All CTAs are resident (cooperative launch).
@@ -84,7 +90,7 @@ __device__ __forceinline__ bool grid_wait(unsigned* bar, volatile int* abort) {
 }
 
 // Logits of token b over the rows [r0, r1) of the router weight, to out[E].  A thread owns EV
-// neighbouring experts and every nrs-th row; red: 256 * EV floats.
+// neighbouring experts and every nrs-th row; red: kDnThreads * EV floats.
 template <int EV>
 __device__ void slice_logits(const LayerArgs& p, int b, int r0, int r1, float* out, float* red) {
   constexpr int RU = 8;
@@ -131,9 +137,9 @@ __device__ void slice_logits(const LayerArgs& p, int b, int r0, int r1, float* o
   }
 }
 
-// One warp: token b's logits (the slices added in order), its k experts by logit descending (ties:
-// the lower index; NaN ranks as -inf) and their weights.
-__device__ void choose(const LayerArgs& p, int b, int* idx, float* w) {
+// One warp: token b's logits (its slices [slices][E] added in order), its k experts by logit descending
+// (ties: the lower index; NaN ranks as -inf) and their weights.
+__device__ void choose(const LayerArgs& p, int b, const float* slices, int* idx, float* w) {
   const int lane = threadIdx.x & 31;
   constexpr int kPer = kMaxExperts / 32;
   float l[kPer];
@@ -144,7 +150,7 @@ __device__ void choose(const LayerArgs& p, int b, int* idx, float* w) {
     l[i] = -INFINITY;
     if (e < p.E) {
       float s = 0.f;
-      for (int q = 0; q < p.slices; ++q) s += __ldcg(p.logits + ((size_t)b * p.slices + q) * p.E + e);
+      for (int q = 0; q < p.slices; ++q) s += slices[q * p.E + e];
       if (!isnan(s)) l[i] = s;
     } else {
       taken |= 1u << i;
@@ -219,9 +225,13 @@ __device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
         if (m.last) p.head->tok[b] = 0u;
       }
       __syncthreads();
-      if (m.last && warp == 0) {
-        choose(p, b, p.top_idx, p.top_w);
-        __threadfence();
+      if (m.last) {
+        for (int i = tid; i < p.slices * p.E; i += kDnThreads) scratch[i] = __ldcg(p.logits + (size_t)b * p.slices * p.E + i);
+        __syncthreads();
+        if (warp == 0) {
+          choose(p, b, scratch, p.top_idx, p.top_w);
+          __threadfence();
+        }
       }
       __syncthreads();
     }
@@ -233,7 +243,9 @@ __device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
   __syncthreads();
   if (m.fail) return false;
   if (few) {
-    if (warp < p.B) choose(p, warp, m.idx, m.w);
+    for (int i = tid; i < p.B * p.slices * p.E; i += kDnThreads) scratch[i] = __ldcg(p.logits + i);
+    __syncthreads();
+    if (warp < p.B) choose(p, warp, scratch + warp * p.slices * p.E, m.idx, m.w);
   } else {
     for (int i = tid; i < p.B * p.k; i += kDnThreads) {
       m.idx[i] = __ldcg(p.top_idx + i);
@@ -515,7 +527,9 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       }
     }
   } else if (warp >= 4) {
-    const int q = warp - 4, r = q * 32 + lane, etid = tid - 128;
+    // lanes 32 (warp % 4) ... are this warp's; of the two warps that have them, in the first phase each takes
+    // every other 16 tokens, in the second each takes 128 features
+    const int q = warp & 3, half = (warp - 4) >> 2, r = q * 32 + lane, etid = tid - 128;
     int buf = 0;
     uint32_t tph = 0;
     bool go = true;
@@ -525,7 +539,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       while (it.next(g)) {
         const bool good = dn_wait(&bars->tfull[buf], tph, abort);
         if (!good) dn_fail(bars, status);
-        if (dn_any(1, 128, !good)) {
+        if (dn_any(1, kDnEpi, !good)) {
           go = false;
           break;
         }
@@ -534,7 +548,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
         const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + buf * 256;
         const int parts = s1.parts(g.t);
         float* mine = p.part + ((size_t)(g.t - s1.dp) + cta) * kPartFloats + r;  // used where parts > 1
-        for (int n0 = 0; n0 < n; n0 += 16) {
+        for (int n0 = 16 * half; n0 < n; n0 += 32) {
           float vg[16], vu[16];
           tmem_ld16(t0 + n0, vg);
           tmem_ld16(t0 + 128 + n0, vu);
@@ -551,27 +565,19 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
               }
             }
           }
+          __syncwarp();
         }
         tc_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->tempty[buf]);
         if (parts > 1 && dn_last_share(&p.head->cnt[g.t - s1.dp], parts, bars, etid) && feat < p.f) {
           const float* from = p.part + ((size_t)(g.t - s1.dp) + s1.first(g.t)) * kPartFloats + r;
-          for (int n0 = 0; n0 < n; n0 += 8) {
-            float vg[8], vu[8];
+          for (int n0 = 16 * half; n0 < n; n0 += 32) {
+            float vg[16], vu[16];
+            sum_shares(from + n0 * kDnHalf, kPartFloats, parts, n - n0, vg);
+            sum_shares(from + (kDenseMaxTok + n0) * kDnHalf, kPartFloats, parts, n - n0, vu);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) vg[i] = vu[i] = 0.f;
-            for (int s = 0; s < parts; ++s) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                if (n0 + i < n) {
-                  vg[i] += __ldcg(from + (size_t)s * kPartFloats + (n0 + i) * kDnHalf);
-                  vu[i] += __ldcg(from + (size_t)s * kPartFloats + (kDenseMaxTok + n0 + i) * kDnHalf);
-                }
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 16; ++i)
               if (n0 + i < n) store_h(p, slot + n0 + i, feat, vg[i], vu[i]);
           }
         }
@@ -584,31 +590,27 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       // this CTA's h: its stores before the other CTAs' copies (which the async proxy makes)
       __threadfence();
       fence_proxy_async_all();
-      named_barrier(1, 128);
+      named_barrier(1, kDnEpi);
       if (etid == 0) grid_arrive(&p.head->bar[1]);
       SegIter it(s2, cta);
       while (it.next(g)) {
         const bool good = dn_wait(&bars->tfull[buf], tph, abort);
         if (!good) dn_fail(bars, status);
-        if (dn_any(1, 128, !good)) break;
+        if (dn_any(1, kDnEpi, !good)) break;
         tc_after_sync();
-        const int a = g.t / DT, feat = (g.t - a * DT) * 2 * kDnHalf + r, n = m.cnt[a], slot = m.grp[a] * 8;
-        const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + buf * 256;
+        const int a = g.t / DT, n = m.cnt[a], slot = m.grp[a] * 8;
+        const int feat = (g.t - a * DT) * 2 * kDnHalf + half * kDnHalf + r;
+        const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + buf * 256 + half * 128;
         const int share = s2.parts(g.t) == 1 ? 0 : cta - s2.first(g.t);
         float* out = p.ypart + ((size_t)share * p.slots + slot) * p.d + feat;
         for (int n0 = 0; n0 < n; n0 += 8) {  // columns: 8 tokens' hi, then their lo
-          float va[16], vb[16];
-          tmem_ld16(t0 + 2 * n0, va);
-          tmem_ld16(t0 + 128 + 2 * n0, vb);
-          tmem_wait(va);
-          tmem_wait(vb);
+          float v[16];
+          tmem_ld16(t0 + 2 * n0, v);
+          tmem_wait(v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (n0 + i < n) {
-              if (feat < p.d) __stcg(out + (size_t)(n0 + i) * p.d, va[i] + va[i + 8]);
-              if (feat + kDnHalf < p.d) __stcg(out + (size_t)(n0 + i) * p.d + kDnHalf, vb[i] + vb[i + 8]);
-            }
-          }
+          for (int i = 0; i < 8; ++i)
+            if (n0 + i < n && feat < p.d) __stcg(out + (size_t)(n0 + i) * p.d, v[i] + v[i + 8]);
+          __syncwarp();
         }
         tc_before_sync();
         __syncwarp();
@@ -635,52 +637,90 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   }
   __syncthreads();
   if (m.fail) return;
-  const int units = p.rmsnorm ? p.B : p.B * DT;
-  float* row = reinterpret_cast<float*>(ring);
-  for (int u = cta; u < units; u += gridDim.x) {
-    const int b = p.rmsnorm ? u : u / DT;
-    const int dt0 = p.rmsnorm ? 0 : u - b * DT, dt1 = p.rmsnorm ? DT : dt0 + 1;
-    float sq = 0.f;
-    for (int dt = dt0; dt < dt1; ++dt) {
-      const int feat = dt * 2 * kDnHalf + tid;
-      if (feat < p.d) {
-        float acc = 0.f;
-        for (int j = 0; j < p.k + p.ns; ++j) {
-          const int a = m.place[b * kMaxPairSlots + j], slot = m.row[b * kMaxPairSlots + j];
-          const int parts = s2.parts(a * DT + dt);
-          float v = 0.f;
-          for (int s = 0; s < parts; ++s) v += __ldcg(p.ypart + ((size_t)s * p.slots + slot) * p.d + feat);
-          acc = fmaf(j < p.k ? m.w[b * p.k + j] : 1.f, v, acc);
-        }
-        if (p.residual) acc += ld16(p.residual, (size_t)b * p.d + feat, p.bf16);
-        if (p.rmsnorm) {
-          row[feat] = acc;
-          sq = fmaf(acc, acc, sq);
-        } else {
-          reinterpret_cast<unsigned short*>(p.y)[(size_t)b * p.d + feat] = to16(acc, p.bf16);
-        }
+  for (int u = cta; u < p.B * DT; u += gridDim.x) {
+    const int b = u / DT, dt = u - b * DT, feat = dt * 2 * kDnHalf + tid;
+    __syncthreads();
+    if (warp == 0) {
+      int a = 0, slot = 0, parts = 0;
+      if (lane < p.k + p.ns) {
+        a = m.place[b * kMaxPairSlots + lane];
+        slot = m.row[b * kMaxPairSlots + lane];
+        parts = s2.parts(a * DT + dt);
       }
+      int end = parts;
+#pragma unroll
+      for (int off = 1; off < 16; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, end, off);
+        if (lane >= off) end += o;
+      }
+      for (int s = 0; s < parts; ++s) {
+        m.from[end - parts + s] = ((size_t)s * p.slots + slot) * p.d;
+        m.weight[end - parts + s] = lane < p.k ? m.w[b * p.k + lane] : 1.f;
+      }
+      if (lane == 15) m.n_from = end;
+    }
+    __syncthreads();
+    float acc = 0.f;
+    if (tid < 2 * kDnHalf && feat < p.d) {
+      const int n = m.n_from;
+      const float r = p.residual ? ld16(p.residual, (size_t)b * p.d + feat, p.bf16) : 0.f;
+      for (int i = 0; i < n; i += 8) {
+        float t[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = i + j < n ? __ldcg(p.ypart + m.from[i + j] + feat) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (i + j < n) acc = fmaf(m.weight[i + j], t[j], acc);
+      }
+      acc += r;
+      if (p.rmsnorm) p.yrow[(size_t)b * p.d + feat] = acc;
+      else reinterpret_cast<unsigned short*>(p.y)[(size_t)b * p.d + feat] = to16(acc, p.bf16);
     }
     if (p.rmsnorm) {
+      float sq = acc * acc;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, off);
       if (lane == 0) m.sum[warp] = sq;
       __syncthreads();
-      float t = 0.f;
-#pragma unroll
-      for (int i = 0; i < kDnThreads / 32; ++i) t += m.sum[i];
-      const float scale = rsqrtf(t / (float)p.d + 1e-6f);
-      for (int feat = tid; feat < p.d; feat += kDnThreads)
-        reinterpret_cast<unsigned short*>(p.y)[(size_t)b * p.d + feat] = to16(row[feat] * scale, p.bf16);
+      if (tid == 0) {
+        float t = 0.f;
+        for (int i = 0; i < 2 * kDnHalf / 32; ++i) t += m.sum[i];
+        __stcg(p.ysq + u, t);
+      }
+    }
+  }
+  if (p.rmsnorm) {
+    // every tile's squares, then the same thread's values again
+    if (tid == 0) {
+      grid_arrive(&p.head->bar[3]);
+      if (!grid_wait(&p.head->bar[3], abort)) dn_fail(bars, status);
+      m.fail = *abort;
+    }
+    __syncthreads();
+    if (m.fail) return;
+    for (int u = cta; u < p.B * DT; u += gridDim.x) {
+      const int b = u / DT, dt = u - b * DT, feat = dt * 2 * kDnHalf + tid;
       __syncthreads();
+      if (warp == 0) {
+        float t = 0.f;
+        for (int i = lane; i < DT; i += 32) t += __ldcg(p.ysq + b * DT + i);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+        if (lane == 0) m.sum[0] = rsqrtf(t / (float)p.d + 1e-6f);
+      }
+      __syncthreads();
+      if (tid < 2 * kDnHalf && feat < p.d) {
+        const size_t at = (size_t)b * p.d + feat;
+        reinterpret_cast<unsigned short*>(p.y)[at] = to16(p.yrow[at] * m.sum[0], p.bf16);
+      }
     }
   }
   // the last CTA to leave clears the barriers for the next call
   if (tid == 0) {
     unsigned old;
-    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(&p.head->bar[3]) : "memory");
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(&p.head->bar[4]) : "memory");
     if (old == gridDim.x - 1) {
-      for (int i = 0; i < 4; ++i) p.head->bar[i] = 0u;
+      for (int i = 0; i < 5; ++i) p.head->bar[i] = 0u;
     }
   }
 }
@@ -688,7 +728,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
 struct LayerPlan {
   int B = -1, d, f, E, k, ns, sms;
   int groups, slices, grid;
-  size_t logits, top_idx, top_w, h, part, ypart, total;
+  size_t logits, top_idx, top_w, h, part, yrow, ysq, ypart, total;
 };
 
 // The plan goes by the sizes alone; a thread keeps the last one, since a program calls with the same
@@ -708,6 +748,8 @@ const LayerPlan& layer_plan(int B, int d, int f, int E, int k, int ns, int sms) 
   l.slices = B > 0 ? sms / B : 1;
   const int most = (d + 63) / 64;  // 64 rows of the router weight at least
   if (l.slices > 32) l.slices = 32;
+  // the logits of a few tokens' slices are gathered in shared memory
+  if (B <= kFewTok && E > 0 && l.slices > 16384 / (B * E)) l.slices = 16384 / (B * E);
   if (l.slices > most) l.slices = most;
   if (l.slices < 1) l.slices = 1;
   const int FT = (f + kDnHalf - 1) / kDnHalf, DT = (d + 2 * kDnHalf - 1) / (2 * kDnHalf);
@@ -731,6 +773,8 @@ const LayerPlan& layer_plan(int B, int d, int f, int E, int k, int ns, int sms) 
   l.top_w = take((size_t)B * k * 4);
   l.h = take((size_t)l.groups * 16 * f * 2);
   l.part = take((size_t)segs * kPartFloats * 4);
+  l.yrow = take((size_t)B * d * 4);
+  l.ysq = take((size_t)B * DT * 4);
   l.ypart = take((size_t)parts * l.groups * 8 * d * 4);
   l.total = o;
   return l;
@@ -791,14 +835,15 @@ cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int s
   p.h = reinterpret_cast<unsigned short*>(w8 + l.h);
   p.part = reinterpret_cast<float*>(w8 + l.part);
   p.ypart = reinterpret_cast<float*>(w8 + l.ypart);
+  p.yrow = reinterpret_cast<float*>(w8 + l.yrow);
+  p.ysq = reinterpret_cast<float*>(w8 + l.ysq);
   p.slots = l.groups * 8;
   p.slices = l.slices;
   p.stage_bytes = kDnBytesA + (c.B + 7) / 8 * 16 * 128;
   const int fixed = 1024 + (int)sizeof(LayerMisc) + p.slots;
   int S = (smem_optin - fixed) / p.stage_bytes;
   p.stages = S > kDnMaxStages ? kDnMaxStages : S;
-  // RMSNorm keeps a token's row of sums in the ring
-  if (p.stages < 2 || (size_t)c.d * 4 > (size_t)p.stages * p.stage_bytes) return cudaErrorInvalidValue;
+  if (p.stages < 3) return cudaErrorInvalidValue;
   const size_t smem = fixed + (size_t)p.stages * p.stage_bytes;
   e = cudaFuncSetAttribute(dense_layer_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;

@@ -23,36 +23,75 @@ struct LinearArgs {
   int stages, acc_bufs, tmem_cols, stream;
 };
 
-__device__ __forceinline__ float activate(float a, int act) {
+// One decision for 16 values, not one for each.
+__device__ __forceinline__ void activate(float (&v)[16], int act) {
   switch (act) {
-    case MOE_ACT_RELU: return a < 0.f ? 0.f : a;  // NaN stays NaN
-    case MOE_ACT_GELU: return 0.5f * a * (1.f + erff(a * 0.70710678118654752f));
-    case MOE_ACT_GELU_TANH: return 0.5f * a * (1.f + tanhf(0.79788456080286536f * (a + 0.044715f * a * a * a)));
-    case MOE_ACT_SILU: return silu_f(a);
-    default: return a;
+    case MOE_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];  // NaN stays NaN
+      break;
+    case MOE_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0.5f * v[i] * (1.f + erff(v[i] * 0.70710678118654752f));
+      break;
+    case MOE_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        v[i] = 0.5f * v[i] * (1.f + tanhf(0.79788456080286536f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));
+      break;
+    case MOE_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = silu_f(v[i]);
+      break;
+    default: break;
   }
 }
 
-// Epilogue of 16 tokens of one feature: v (and m, the multiplier's sums) of tokens t0 ...
-__device__ __forceinline__ void linear_store(const LinearArgs& p, int feat, int t0, int t_end, float bias, float bias_mul,
-                                             const float (&v)[16], const float (&m)[16], bool gated) {
-  float r[16];
-  const int n = t_end - t0;
+// Residual and store of 16 tokens' values of one feature; token i at offset at + i * N.
+template <bool FULL>
+__device__ __forceinline__ void linear_write(const LinearArgs& p, size_t at, int n, float (&v)[16]) {
   if (p.residual) {
+    const unsigned short* r = reinterpret_cast<const unsigned short*>(p.residual) + at;
+    unsigned short t[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = i < n ? ld16(p.residual, (size_t)(t0 + i) * p.N + feat, p.bf16) : 0.f;
+    for (int i = 0; i < 16; ++i) t[i] = FULL || i < n ? r[(size_t)i * p.N] : (unsigned short)0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] += from16(t[i], p.bf16);
   }
+  if (p.out_f32) {
+    float* y = reinterpret_cast<float*>(p.y) + at;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if (i < n) {
-      float a = activate(v[i] + bias, p.act);
-      if (gated) a *= m[i] + bias_mul;
-      if (p.residual) a += r[i];
-      const size_t at = (size_t)(t0 + i) * p.N + feat;
-      if (p.out_f32) reinterpret_cast<float*>(p.y)[at] = a;
-      else reinterpret_cast<unsigned short*>(p.y)[at] = to16(a, p.bf16);
+    for (int i = 0; i < 16; ++i)
+      if (FULL || i < n) y[(size_t)i * p.N] = v[i];
+  } else {
+    unsigned short* y = reinterpret_cast<unsigned short*>(p.y) + at;
+    unsigned short t[16];
+    if (p.bf16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) t[i] = to16(v[i], 1);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) t[i] = to16(v[i], 0);
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (FULL || i < n) y[(size_t)i * p.N] = t[i];
   }
+}
+
+// Epilogue of 16 tokens of one feature: v, and with w_mul m, are the sums; n tokens from t0 exist.
+__device__ __forceinline__ void linear_store(const LinearArgs& p, int feat, int t0, int n, float bias, float bias_mul,
+                                             float (&v)[16], const float (&m)[16], bool gated) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] += bias;
+  activate(v, p.act);
+  if (gated) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= m[i] + bias_mul;
+  }
+  const size_t at = (size_t)t0 * p.N + feat;
+  if (n >= 16) linear_write<true>(p, at, n, v);
+  else linear_write<false>(p, at, n, v);
 }
 
 __global__ void __launch_bounds__(kDnThreads, 1)
@@ -178,7 +217,10 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
       }
     }
   } else if (warp >= 4) {
-    const int q = warp - 4, r = q * 32 + lane, etid = tid - 128;
+    // lanes 32 (warp % 4) ... are this warp's; of the two warps that have them, with w_mul each takes
+    // every other 16 tokens, without it one takes each 128 features
+    const int q = warp & 3, half = (warp - 4) >> 2, r = q * 32 + lane, etid = tid - 128;
+    const int step = p.gated ? 32 : 16, begin = p.gated ? 16 * half : 0;
     SegIter it(p.s, cta);
     Seg g;
     int buf = 0;
@@ -186,72 +228,49 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     while (it.next(g)) {
       const bool ok = dn_wait(&bars->tfull[buf], tph, abort);
       if (!ok) dn_fail(bars, status);
-      if (dn_any(1, 128, !ok)) break;  // one decision for the four warps: they meet at barriers below
+      if (dn_any(1, kDnEpi, !ok)) break;  // one decision for the warps: they meet at barriers below
       tc_after_sync();
-      const int ft = g.t / p.MT, mt = g.t - ft * p.MT, f0 = ft * width, m0 = mt * NT;
+      const int ft = g.t / p.MT, mt = g.t - ft * p.MT, m0 = mt * NT;
       const int nt = p.M - m0 < NT ? p.M - m0 : NT;  // tokens of this tile
-      const uint32_t d0 = tmem + ((uint32_t)(q * 32) << 16) + buf * 2 * NT;
+      const int feat = ft * width + (p.gated ? 0 : half * kDnHalf) + r;
+      const bool on = feat < p.N;
+      const uint32_t d0 = tmem + ((uint32_t)(q * 32) << 16) + buf * 2 * NT + (p.gated ? 0 : half * NT);
       const int parts = p.s.parts(g.t);
-      const int fa = f0 + r, fb = fa + kDnHalf;  // this thread's features (fb: without w_mul)
-      const bool on_a = fa < p.N, on_b = !p.gated && fb < p.N;
-      float ba = 0.f, bb = 0.f;
-      if (p.bias && on_a) ba = ld16(p.bias, fa, p.bf16);
-      if (p.gated) {
-        if (p.bias_mul && on_a) bb = ld16(p.bias_mul, fa, p.bf16);
-      } else if (p.bias && on_b) {
-        bb = ld16(p.bias, fb, p.bf16);
-      }
+      const float ba = p.bias && on ? ld16(p.bias, feat, p.bf16) : 0.f;
+      const float bb = p.bias_mul && on ? ld16(p.bias_mul, feat, p.bf16) : 0.f;
       const size_t seg_floats = (size_t)2 * NT * 128;
-      float* mine = nullptr;
-      if (parts > 1) mine = p.part + ((size_t)(g.t - p.s.dp) + cta) * seg_floats;
-      for (int n0 = 0; n0 < nt; n0 += 16) {
+      float* mine = p.part + ((size_t)(g.t - p.s.dp) + cta) * seg_floats + r;  // used where parts > 1
+      if (!p.gated) mine += half * NT * 128;
+      for (int n0 = begin; n0 < nt; n0 += step) {
         float v[16], m[16];
         tmem_ld16(d0 + n0, v);
-        tmem_ld16(d0 + NT + n0, m);
+        if (p.gated) tmem_ld16(d0 + NT + n0, m);
         tmem_wait(v);
-        tmem_wait(m);
+        if (p.gated) tmem_wait(m);
         if (parts == 1) {
-          if (p.gated) {
-            if (on_a) linear_store(p, fa, m0 + n0, m0 + nt, ba, bb, v, m, true);
-          } else {
-            if (on_a) linear_store(p, fa, m0 + n0, m0 + nt, ba, 0.f, v, v, false);
-            if (on_b) linear_store(p, fb, m0 + n0, m0 + nt, bb, 0.f, m, m, false);
-          }
+          if (on) linear_store(p, feat, m0 + n0, nt - n0, ba, bb, v, m, p.gated);
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             if (n0 + i < nt) {
-              __stcg(mine + (n0 + i) * 128 + r, v[i]);
-              __stcg(mine + (NT + n0 + i) * 128 + r, m[i]);
+              __stcg(mine + (n0 + i) * 128, v[i]);
+              if (p.gated) __stcg(mine + (NT + n0 + i) * 128, m[i]);
             }
           }
         }
+        __syncwarp();
       }
       tc_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->tempty[buf]);
-      if (parts > 1 && dn_last_share(&p.head->cnt[g.t - p.s.dp], parts, bars, etid)) {
-        const int c0 = p.s.first(g.t);
-        const float* from = p.part + ((size_t)(g.t - p.s.dp) + c0) * seg_floats + r;
-        for (int n0 = 0; n0 < nt; n0 += 16) {
+      if (parts > 1 && dn_last_share(&p.head->cnt[g.t - p.s.dp], parts, bars, etid) && on) {
+        const float* from = p.part + ((size_t)(g.t - p.s.dp) + p.s.first(g.t)) * seg_floats + r;
+        if (!p.gated) from += half * NT * 128;
+        for (int n0 = begin; n0 < nt; n0 += step) {
           float v[16], m[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = m[i] = 0.f;
-          for (int s = 0; s < parts; ++s) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (n0 + i < nt) {
-                v[i] += __ldcg(from + s * seg_floats + (n0 + i) * 128);
-                m[i] += __ldcg(from + s * seg_floats + (NT + n0 + i) * 128);
-              }
-            }
-          }
-          if (p.gated) {
-            if (on_a) linear_store(p, fa, m0 + n0, m0 + nt, ba, bb, v, m, true);
-          } else {
-            if (on_a) linear_store(p, fa, m0 + n0, m0 + nt, ba, 0.f, v, v, false);
-            if (on_b) linear_store(p, fb, m0 + n0, m0 + nt, bb, 0.f, m, m, false);
-          }
+          sum_shares(from + n0 * 128, seg_floats, parts, nt - n0, v);
+          if (p.gated) sum_shares(from + (NT + n0) * 128, seg_floats, parts, nt - n0, m);
+          linear_store(p, feat, m0 + n0, nt - n0, ba, bb, v, m, p.gated);
         }
       }
       if (++buf == p.acc_bufs) {
