@@ -518,13 +518,15 @@ def layer_decode_host_rows(x: torch.Tensor, layer: Layer, rmsnorm: bool = False,
 # uncompressed 16-bit weights: products with an epilogue, experts, layers
 # ---------------------------------------------------------------------------
 
-_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 _ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _LAYOUTS = {"nk": 0, "kn": 1}
 
 
 def _dense_in(t, dtype, device: int, shape, name: str) -> int:
     """Address of an input of a call on uncompressed weights: type, device, shape and density checked."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if not t.is_cuda:
@@ -535,36 +537,40 @@ def _dense_in(t, dtype, device: int, shape, name: str) -> int:
         raise ValueError(f"{name} must be on cuda:{device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _dense_x(x, name: str = "x") -> int:
     """The device of a call's tokens, a CUDA fp16 or bf16 matrix on the current device."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if not x.is_cuda:
+    device = x.get_device()
+    if device < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if x.dtype != torch.float16 and x.dtype != torch.bfloat16:
+    if x.dtype is not torch.float16 and x.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {x.dtype}")
     if x.dim() != 2:
         raise ValueError(f"{name} must be a matrix")
-    device = x.get_device()
     if device != torch.cuda.current_device():
         raise ValueError(f"{name} is on cuda:{device}, which is not the current device")
     return device
 
 
-def _dense_ws(ws, nbytes: int, device: int) -> "Workspace":
-    """The caller's workspace, or a new one of nbytes."""
+def _dense_ws(ws, device: int, nbytes, *sizes) -> "Workspace":
+    """The caller's workspace, or a new one of nbytes(*sizes)."""
     if ws is None:
-        if nbytes == 0:
+        n = nbytes(*sizes)
+        if n == 0:
             raise ValueError("sizes outside the supported range")
-        return Workspace(nbytes, torch.device("cuda", device))
+        return Workspace(n, torch.device("cuda", device))
     if ws.buf.get_device() != device:
         raise ValueError(f"ws must be on cuda:{device}")
     return ws
+
+
+def _stream_of(device: int) -> int:
+    """The current stream's handle (without a Stream object: a decode step makes many calls)."""
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def linear_workspace_bytes(M: int, N: int, K: int, gated: bool = False) -> int:
@@ -582,20 +588,28 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     out may be the residual's tensor, no other input's."""
     device = _dense_x(x)
     dt = x.dtype
-    if act not in _ACTS:
+    dtype_code = 0 if dt is torch.float16 else 1
+    act_code, layout_code = _ACTS.get(act, -1), _LAYOUTS.get(w_layout, -1)
+    if act_code < 0:
         raise ValueError(f"act must be one of {tuple(_ACTS)}, got {act!r}")
-    if w_layout not in _LAYOUTS:
+    if layout_code < 0:
         raise ValueError(f"w_layout must be 'nk' or 'kn', got {w_layout!r}")
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be a matrix")
     if bias_mul is not None and w_mul is None:
         raise ValueError("bias_mul goes with w_mul")
     M, K = x.shape
-    N = w.shape[0] if w_layout == "nk" else w.shape[1]
-    wshape = (N, K) if w_layout == "nk" else (K, N)
-    if out_dtype is None:
-        out_dtype = dt
-    elif out_dtype != dt and out_dtype != torch.float32:
+    if layout_code:
+        N = w.shape[1]
+        wshape = (K, N)
+    else:
+        N = w.shape[0]
+        wshape = (N, K)
+    if out_dtype is None or out_dtype is dt:
+        out_dtype, out_code = dt, dtype_code
+    elif out_dtype is torch.float32:
+        out_code = 2
+    else:
         raise TypeError(f"out_dtype must be {dt} or torch.float32, got {out_dtype}")
     if out is None:
         y = torch.empty((M, N), dtype=out_dtype, device=x.device)
@@ -603,7 +617,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     else:
         y = out
         yp = _dense_in(out, out_dtype, device, (M, N), "out")
-    op = _Linear(M, N, K, _DTYPES[dt], _DTYPES[out_dtype], _LAYOUTS[w_layout], _ACTS[act],
+    op = _Linear(M, N, K, dtype_code, out_code, layout_code, act_code,
                  _dense_in(x, dt, device, (M, K), "x"), _dense_in(w, dt, device, wshape, "w"),
                  None if w_mul is None else _dense_in(w_mul, dt, device, wshape, "w_mul"),
                  None if bias is None else _dense_in(bias, dt, device, (N,), "bias"),
@@ -611,9 +625,10 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
                  None if residual is None else _dense_in(residual, dt, device, (M, N), "residual"), yp)
     if M == 0:
         return y
-    ws = _dense_ws(ws, 0 if ws is not None else linear_workspace_bytes(M, N, K, w_mul is not None), device)
-    _check("moe_linear", lib().moe_linear(ctypes.byref(op), ws.buf.data_ptr(), ws.nbytes,
-                                          torch.cuda.current_stream().cuda_stream))
+    ws = _dense_ws(ws, device, linear_workspace_bytes, M, N, K, w_mul is not None)
+    status = (_LIB or lib()).moe_linear(ctypes.byref(op), ws.buf.data_ptr(), ws.nbytes, _stream_of(device))
+    if status:
+        raise MoeError("moe_linear", status)
     return y
 
 
@@ -642,19 +657,20 @@ class DenseExperts:
         g, dn = self.gate_t, self.down
         if not isinstance(g, torch.Tensor) or g.dim() != 3:
             raise ValueError("gate_t must have shape [E, f, d]")
-        if g.dtype not in (torch.float16, torch.bfloat16):
-            raise TypeError(f"gate_t must be torch.float16 or torch.bfloat16, got {g.dtype}")
-        if not g.is_cuda:
+        dt, shape, device = g.dtype, g.shape, g.get_device()
+        if dt is not torch.float16 and dt is not torch.bfloat16:
+            raise TypeError(f"gate_t must be torch.float16 or torch.bfloat16, got {dt}")
+        if device < 0:
             raise TypeError("gate_t must be a CUDA tensor")
-        E, f, d = g.shape
-        device = g.get_device()
-        if (isinstance(dn, torch.Tensor) and dn.shape == g.shape and dn.stride() == g.stride() and dn.dtype == g.dtype
-                and dn.is_cuda and g.stride() == (2 * f * d, 2 * d, 1) and dn.data_ptr() == g.data_ptr() + 2 * d):
+        E, f, d = shape
+        if (isinstance(dn, torch.Tensor) and not g.is_contiguous() and dn.shape == shape and dn.dtype is dt
+                and dn.stride() == g.stride() == (2 * f * d, 2 * d, 1) and dn.get_device() == device
+                and dn.data_ptr() == g.data_ptr() + 2 * d):
             gp, dp = g.data_ptr(), dn.data_ptr()  # interleaved
         else:
-            gp = _dense_in(g, g.dtype, device, g.shape, "gate_t")
-            dp = _dense_in(dn, g.dtype, device, g.shape, "down")
-        return _DenseExperts(E, d, f, _DTYPES[g.dtype], gp, _dense_in(self.up_t, g.dtype, device, g.shape, "up_t"), dp)
+            gp, dp = _dense_in(g, dt, device, shape, "gate_t"), _dense_in(dn, dt, device, shape, "down")
+        return _DenseExperts(E, d, f, 0 if dt is torch.float16 else 1, gp,
+                             _dense_in(self.up_t, dt, device, shape, "up_t"), dp)
 
 
 @dataclass
@@ -703,10 +719,11 @@ def expert_dense_swiglu(x: torch.Tensor, experts: DenseExperts, expert: int, res
         _dense_in(out, dt, device, shape, "out")
     if n == 0:
         return y
-    ws = _dense_ws(ws, 0 if ws is not None else expert_dense_workspace_bytes(n, ex.d, ex.f), device)
-    _check("moe_expert_dense_swiglu",
-           lib().moe_expert_dense_swiglu(xp, n, ctypes.byref(ex), expert, rp, y.data_ptr(), ws.buf.data_ptr(), ws.nbytes,
-                                         torch.cuda.current_stream().cuda_stream))
+    ws = _dense_ws(ws, device, expert_dense_workspace_bytes, n, ex.d, ex.f)
+    status = (_LIB or lib()).moe_expert_dense_swiglu(xp, n, ctypes.byref(ex), expert, rp, y.data_ptr(),
+                                                     ws.buf.data_ptr(), ws.nbytes, _stream_of(device))
+    if status:
+        raise MoeError("moe_expert_dense_swiglu", status)
     return y
 
 
@@ -739,10 +756,11 @@ def layer_dense_decode(x: torch.Tensor, layer: DenseLayer, residual: Optional[to
                    topk_w=torch.zeros((B, layer.k), dtype=torch.float32, device=x.device))
         dbg = ctypes.byref(_Debug(_ptr(dt_["topk_idx"]), _ptr(dt_["topk_w"]), None, None, None))
     if B:
-        ws = _dense_ws(ws, 0 if ws is not None else int(lib().moe_layer_dense_workspace_bytes(ctypes.byref(c), B)), device)
-        _check("moe_layer_dense_decode",
-               lib().moe_layer_dense_decode(xp, B, ctypes.byref(c), rp, y.data_ptr(), 1 if rmsnorm else 0, dbg,
-                                            ws.buf.data_ptr(), ws.nbytes, torch.cuda.current_stream().cuda_stream))
+        ws = _dense_ws(ws, device, layer_dense_workspace_bytes, layer, B)
+        status = (_LIB or lib()).moe_layer_dense_decode(xp, B, ctypes.byref(c), rp, y.data_ptr(), 1 if rmsnorm else 0,
+                                                        dbg, ws.buf.data_ptr(), ws.nbytes, _stream_of(device))
+        if status:
+            raise MoeError("moe_layer_dense_decode", status)
     return (y, dt_) if debug else y
 
 

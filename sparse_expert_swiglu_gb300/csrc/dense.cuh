@@ -134,8 +134,8 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
 }
 __device__ __forceinline__ void tc_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// 16 columns of this warp's 32 lanes; the values are there after tmem_wait
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+// W columns of this warp's 32 lanes; the values are there after tmem_wait
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[16]) {
   uint32_t r[16];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -145,11 +145,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[2]) {
+  uint32_t r[2];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+  v[0] = __uint_as_float(r[0]);
+  v[1] = __uint_as_float(r[1]);
+}
 // waits for this thread's tmem loads; the loaded values pass through, so that none is used before
-__device__ __forceinline__ void tmem_wait(float (&v)[16]) {
+template <int W>
+__device__ __forceinline__ void tmem_wait(float (&v)[W]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(v[i]));
+  for (int i = 0; i < W; ++i) asm volatile("" : "+f"(v[i]));
 }
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint64_t* bar,
@@ -264,7 +271,6 @@ __device__ __forceinline__ bool dn_any(int id, int n, bool v) {
 // publishes them; the count's acquire and the second barrier order the reads that follow.
 __device__ __forceinline__ bool dn_last_share(unsigned* cnt, int parts, DenseBars* b, int etid) {
   __syncwarp();
-  __threadfence();
   named_barrier(1, kDnEpi);
   if (etid == 0) {
     unsigned old;
@@ -277,28 +283,24 @@ __device__ __forceinline__ bool dn_last_share(unsigned* cnt, int parts, DenseBar
 }
 
 // v[i] = the sum over a split tile's shares, in order, of from[share * stride + i * 128], for i < n.
-// The loads of 16 values are in flight together: few tokens, many shares at a time.
-template <int G>
-__device__ __forceinline__ void sum_shares_by(const float* from, size_t stride, int parts, int n, float (&v)[16]) {
-  constexpr int U = G >= 16 ? 2 : 16 / G;
+// 16 loads are in flight together: few tokens, many shares at a time.
+template <int W>
+__device__ __forceinline__ void sum_shares(const float* from, size_t stride, int parts, int n, float (&v)[W]) {
+  constexpr int U = W >= 16 ? 2 : 16 / W;
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = 0.f;
+#pragma unroll 1
   for (int s = 0; s < parts; s += U) {
-    float t[U][G];
+    float t[U][W];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < G; ++i) t[u][i] = s + u < parts && i < n ? __ldcg(from + (s + u) * stride + i * 128) : 0.f;
+      for (int i = 0; i < W; ++i) t[u][i] = s + u < parts && i < n ? __ldcg(from + (s + u) * stride + i * 128) : 0.f;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < G; ++i) v[i] += t[u][i];
+      for (int i = 0; i < W; ++i) v[i] += t[u][i];
   }
-}
-__device__ __forceinline__ void sum_shares(const float* from, size_t stride, int parts, int n, float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = 0.f;
-  if (n <= 1) sum_shares_by<1>(from, stride, parts, n, v);
-  else if (n <= 4) sum_shares_by<4>(from, stride, parts, n, v);
-  else sum_shares_by<16>(from, stride, parts, n, v);
 }
 
 // One stage's products of both 128-feature tiles.  `lead` = 0: A's rows lie along k.

@@ -138,68 +138,83 @@ __device__ void slice_logits(const LayerArgs& p, int b, int r0, int r1, float* o
 }
 
 // One warp: token b's logits (its slices [slices][E] added in order), its k experts by logit descending
-// (ties: the lower index; NaN ranks as -inf) and their weights.
-__device__ void choose(const LayerArgs& p, int b, const float* slices, int* idx, float* w) {
+// (ties: the lower index; NaN ranks as -inf) and their weights.  A logit's key orders as the logit
+// does; an expert that is taken has key 0, below every logit's.
+template <int PER>
+__device__ __forceinline__ void choose(const LayerArgs& p, int b, const float* slices, int* idx, float* w) {
   const int lane = threadIdx.x & 31;
-  constexpr int kPer = kMaxExperts / 32;
-  float l[kPer];
-  uint32_t taken = 0;
+  float l[PER];
+  uint32_t key[PER];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int e = lane + 32 * i;
     l[i] = -INFINITY;
+    key[i] = 0u;
     if (e < p.E) {
       float s = 0.f;
+#pragma unroll 4
       for (int q = 0; q < p.slices; ++q) s += slices[q * p.E + e];
+      s += 0.f;  // -0 and +0 are one logit
       if (!isnan(s)) l[i] = s;
-    } else {
-      taken |= 1u << i;
+      const uint32_t u = __float_as_uint(l[i]);
+      key[i] = u >> 31 ? ~u : u | 0x80000000u;
     }
   }
   float mine = 0.f, top = -INFINITY;  // lane j keeps the j-th choice
   int mine_e = 0;
+#pragma unroll 1
   for (int j = 0; j < p.k; ++j) {
-    float best = -INFINITY;
-    int at = 0x7fffffff;
+    uint32_t best = key[0];
+    int at = lane;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane + 32 * i;
-      if (!(taken >> i & 1) && (l[i] > best || (l[i] == best && e < at))) {
-        best = l[i];
-        at = e;
+    for (int i = 1; i < PER; ++i) {
+      if (key[i] > best) {
+        best = key[i];
+        at = lane + 32 * i;
       }
     }
+    const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+    const int e = __reduce_min_sync(0xffffffffu, best == most ? at : 0x7fffffff);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const float ob = __shfl_xor_sync(0xffffffffu, best, off);
-      const int oa = __shfl_xor_sync(0xffffffffu, at, off);
-      if (ob > best || (ob == best && oa < at)) {
-        best = ob;
-        at = oa;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i == at) taken |= 1u << i;
-    if (j == 0) top = best;
+    for (int i = 0; i < PER; ++i)
+      if (lane + 32 * i == e) key[i] = 0u;
+    const float v = __uint_as_float(most >> 31 ? most & 0x7fffffffu : ~most);
+    if (j == 0) top = v;
     if (lane == j) {
-      mine = best;
-      mine_e = at;
+      mine = v;
+      mine_e = e;
     }
   }
   float sum = 0.f;
   if (p.renorm) {
-    for (int j = 0; j < p.k; ++j) sum += expf(__shfl_sync(0xffffffffu, mine, j) - top);
+    if (lane < p.k) sum = expf(mine - top);
   } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
+    for (int i = 0; i < PER; ++i)
       if (lane + 32 * i < p.E) sum += expf(l[i] - top);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   if (lane < p.k) {
     idx[b * p.k + lane] = mine_e;
     w[b * p.k + lane] = expf(mine - top) / sum;
+  }
+}
+
+__device__ void choose_any(const LayerArgs& p, int b, const float* slices, int* idx, float* w) {
+  if (p.E <= 64) choose<2>(p, b, slices, idx, w);
+  else choose<kMaxExperts / 32>(p, b, slices, idx, w);
+}
+
+// Whole CTA: n values of other CTAs to shared memory, eight of a thread's in flight.
+__device__ void gather_logits(const float* from, int n, float* to) {
+  for (int i = threadIdx.x; i < n; i += 8 * kDnThreads) {
+    float t[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = i + j * kDnThreads < n ? __ldcg(from + i + j * kDnThreads) : 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j * kDnThreads < n) to[i + j * kDnThreads] = t[j];
   }
 }
 
@@ -214,7 +229,6 @@ __device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
     float* out = p.logits + ((size_t)b * p.slices + s) * p.E;
     if (p.E % 8 == 0) slice_logits<8>(p, b, r0, r1, out, scratch);
     else slice_logits<1>(p, b, r0, r1, out, scratch);
-    __threadfence();
     __syncthreads();
     if (!few) {
       // the token's last slice to come chooses its experts
@@ -226,11 +240,10 @@ __device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
       }
       __syncthreads();
       if (m.last) {
-        for (int i = tid; i < p.slices * p.E; i += kDnThreads) scratch[i] = __ldcg(p.logits + (size_t)b * p.slices * p.E + i);
+        gather_logits(p.logits + (size_t)b * p.slices * p.E, p.slices * p.E, scratch);
         __syncthreads();
         if (warp == 0) {
-          choose(p, b, scratch, p.top_idx, p.top_w);
-          __threadfence();
+          choose_any(p, b, scratch, p.top_idx, p.top_w);
         }
       }
       __syncthreads();
@@ -243,9 +256,9 @@ __device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
   __syncthreads();
   if (m.fail) return false;
   if (few) {
-    for (int i = tid; i < p.B * p.slices * p.E; i += kDnThreads) scratch[i] = __ldcg(p.logits + i);
+    gather_logits(p.logits, p.B * p.slices * p.E, scratch);
     __syncthreads();
-    if (warp < p.B) choose(p, warp, scratch + warp * p.slices * p.E, m.idx, m.w);
+    if (warp < p.B) choose_any(p, warp, scratch + warp * p.slices * p.E, m.idx, m.w);
   } else {
     for (int i = tid; i < p.B * p.k; i += kDnThreads) {
       m.idx[i] = __ldcg(p.top_idx + i);
@@ -266,9 +279,6 @@ __device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
 __device__ void make_lists(const LayerArgs& p, LayerMisc& m, uint8_t* tok) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int pairs = p.B * p.k, gs = (p.B + 7) / 8;
-  for (int e = tid; e < p.E; e += kDnThreads) m.mask[e] = 0ull;
-  for (int i = tid; i < p.slots; i += kDnThreads) tok[i] = (uint8_t)p.B;  // no token
-  __syncthreads();
   for (int i = tid; i < pairs; i += kDnThreads) atomicOr(&m.mask[m.idx[i]], 1ull << (i / p.k));
   __syncthreads();
   if (tid < 32) {
@@ -317,14 +327,64 @@ __device__ void make_lists(const LayerArgs& p, LayerMisc& m, uint8_t* tok) {
   __syncthreads();
 }
 
-__device__ __forceinline__ void store_h(const LayerArgs& p, int slot, int feat, float g, float u) {
-  const float h = silu_f(g) * u;
-  const unsigned short hi = to16(h, p.bf16);
-  const float hf = from16(hi, p.bf16);
-  const unsigned short lo = isfinite(hf) ? to16(h - hf, p.bf16) : (unsigned short)0;
-  const size_t at = ((size_t)(slot >> 3) * 16 + (slot & 7)) * p.f + feat;
-  p.h[at] = hi;
-  p.h[at + (size_t)8 * p.f] = lo;
+// h of W tokens of one feature (n of them exist), from their sums of gate and up, to slots slot ...
+template <int W>
+__device__ __forceinline__ void store_h(const LayerArgs& p, int slot, int n, int feat, const float (&g)[W],
+                                        const float (&u)[W]) {
+  unsigned short hi[W], lo[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const float h = silu_f(g[i]) * u[i];
+    hi[i] = to16(h, p.bf16);
+    const float hf = from16(hi[i], p.bf16);
+    lo[i] = isfinite(hf) ? to16(h - hf, p.bf16) : (unsigned short)0;
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const int s = slot + i;
+    unsigned short* to = p.h + ((size_t)(s >> 3) * 16 + (s & 7)) * p.f + feat;
+    if (i < n) {
+      to[0] = hi[i];
+      to[(size_t)8 * p.f] = lo[i];
+    }
+  }
+}
+
+// First phase's epilogue of W tokens (n of them exist) of a tile that one CTA did whole, ...
+template <int W>
+__device__ __forceinline__ void whole_h(const LayerArgs& p, uint32_t t, int slot, int n, int feat) {
+  float g[W], u[W];
+  tmem_ld(t, g);
+  tmem_ld(t + 128, u);
+  tmem_wait(g);
+  tmem_wait(u);
+  if (feat < p.f) store_h(p, slot, n, feat, g, u);
+  __syncwarp();
+}
+// ... of a share of a split tile, to its place among the partial sums, ...
+template <int W>
+__device__ __forceinline__ void share_h(uint32_t t, int n, float* to) {
+  float g[W], u[W];
+  tmem_ld(t, g);
+  tmem_ld(t + 128, u);
+  tmem_wait(g);
+  tmem_wait(u);
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if (i < n) {
+      __stcg(to + i * kDnHalf, g[i]);
+      __stcg(to + (kDenseMaxTok + i) * kDnHalf, u[i]);
+    }
+  }
+  __syncwarp();
+}
+// ... and of the shares together.
+template <int W>
+__device__ __forceinline__ void joined_h(const LayerArgs& p, const float* from, int parts, int slot, int n, int feat) {
+  float g[W], u[W];
+  sum_shares(from, kPartFloats, parts, n, g);
+  sum_shares(from + kDenseMaxTok * kDnHalf, kPartFloats, parts, n, u);
+  store_h(p, slot, n, feat, g, u);
 }
 
 struct LayerMaps {
@@ -350,6 +410,10 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
     m.fail = 0;
   }
   if (warp == 2) tmem_alloc(&bars->tmem, 512);
+  if (warp == 3 && lane < 8) tma_prefetch_map(&maps.gate + lane);
+  // make_lists starts from no tokens
+  for (int e = tid; e < p.E; e += kDnThreads) m.mask[e] = 0ull;
+  for (int i = tid; i < p.slots; i += kDnThreads) tok[i] = (uint8_t)p.B;
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
@@ -457,7 +521,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
             dn_fail(bars, status);
             break;
           }
-          fence_proxy_async_all();  // the other CTAs' stores of h before this thread's copies of it
+          fence_proxy_async_all();  // h was stored by threads, and is read by the async proxy
         }
         load_h(gh, kh, hs);
         --ahead;
@@ -548,37 +612,28 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
         const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + buf * 256;
         const int parts = s1.parts(g.t);
         float* mine = p.part + ((size_t)(g.t - s1.dp) + cta) * kPartFloats + r;  // used where parts > 1
-        for (int n0 = 16 * half; n0 < n; n0 += 32) {
-          float vg[16], vu[16];
-          tmem_ld16(t0 + n0, vg);
-          tmem_ld16(t0 + 128 + n0, vu);
-          tmem_wait(vg);
-          tmem_wait(vu);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (n0 + i < n) {
-              if (parts == 1) {
-                if (feat < p.f) store_h(p, slot + n0 + i, feat, vg[i], vu[i]);
-              } else {
-                __stcg(mine + (n0 + i) * kDnHalf, vg[i]);
-                __stcg(mine + (kDenseMaxTok + n0 + i) * kDnHalf, vu[i]);
-              }
-            }
+        // up to two tokens in code of their own: a kernel this short pays for every line of code it fetches
+        if (n <= 2) {
+          if (half == 0) {
+            if (parts == 1) whole_h<2>(p, t0, slot, n, feat);
+            else share_h<2>(t0, n, mine);
           }
-          __syncwarp();
+        } else {
+          for (int n0 = 16 * half; n0 < n; n0 += 32) {
+            if (parts == 1) whole_h<16>(p, t0 + n0, slot + n0, n - n0, feat);
+            else share_h<16>(t0 + n0, n - n0, mine + n0 * kDnHalf);
+          }
         }
         tc_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->tempty[buf]);
         if (parts > 1 && dn_last_share(&p.head->cnt[g.t - s1.dp], parts, bars, etid) && feat < p.f) {
           const float* from = p.part + ((size_t)(g.t - s1.dp) + s1.first(g.t)) * kPartFloats + r;
-          for (int n0 = 16 * half; n0 < n; n0 += 32) {
-            float vg[16], vu[16];
-            sum_shares(from + n0 * kDnHalf, kPartFloats, parts, n - n0, vg);
-            sum_shares(from + (kDenseMaxTok + n0) * kDnHalf, kPartFloats, parts, n - n0, vu);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (n0 + i < n) store_h(p, slot + n0 + i, feat, vg[i], vu[i]);
+          if (n <= 2) {
+            if (half == 0) joined_h<2>(p, from, parts, slot, n, feat);
+          } else {
+            for (int n0 = 16 * half; n0 < n; n0 += 32)
+              joined_h<16>(p, from + n0 * kDnHalf, parts, slot + n0, n - n0, feat);
           }
         }
         buf ^= 1;
@@ -587,9 +642,8 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
     }
     __syncwarp();
     if (go) {
-      // this CTA's h: its stores before the other CTAs' copies (which the async proxy makes)
-      __threadfence();
-      fence_proxy_async_all();
+      // this CTA's h: the barrier and the count's release order its stores before what the other CTAs do
+      // once they have seen the count
       named_barrier(1, kDnEpi);
       if (etid == 0) grid_arrive(&p.head->bar[1]);
       SegIter it(s2, cta);
@@ -605,7 +659,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
         float* out = p.ypart + ((size_t)share * p.slots + slot) * p.d + feat;
         for (int n0 = 0; n0 < n; n0 += 8) {  // columns: 8 tokens' hi, then their lo
           float v[16];
-          tmem_ld16(t0 + 2 * n0, v);
+          tmem_ld(t0 + 2 * n0, v);
           tmem_wait(v);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -618,7 +672,6 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
         buf ^= 1;
         tph ^= buf == 0;
       }
-      __threadfence();
     }
   }
   __syncwarp();
@@ -627,7 +680,27 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   tc_after_sync();
   if (warp == 2) tmem_free(tmem, 512);
 
-  // join: every token's experts and their shares, in order
+  // join: every token's experts and their shares, in order.  One warp lists where a token's sums lie.
+  auto list_sums = [&](int b, int dt) {
+    int a = 0, slot = 0, parts = 0;
+    if (lane < p.k + p.ns) {
+      a = m.place[b * kMaxPairSlots + lane];
+      slot = m.row[b * kMaxPairSlots + lane];
+      parts = s2.parts(a * DT + dt);
+    }
+    int end = parts;
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, end, off);
+      if (lane >= off) end += o;
+    }
+    for (int s = 0; s < parts; ++s) {
+      m.from[end - parts + s] = ((size_t)s * p.slots + slot) * p.d;
+      m.weight[end - parts + s] = lane < p.k ? m.w[b * p.k + lane] : 1.f;
+    }
+    if (lane == 15) m.n_from = end;
+  };
+  if (ok && warp == 1 && cta < p.B * DT) list_sums(cta / DT, cta % DT);
   if (tid == 0) {
     if (!*abort) {
       grid_arrive(&p.head->bar[2]);
@@ -639,27 +712,11 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   if (m.fail) return;
   for (int u = cta; u < p.B * DT; u += gridDim.x) {
     const int b = u / DT, dt = u - b * DT, feat = dt * 2 * kDnHalf + tid;
-    __syncthreads();
-    if (warp == 0) {
-      int a = 0, slot = 0, parts = 0;
-      if (lane < p.k + p.ns) {
-        a = m.place[b * kMaxPairSlots + lane];
-        slot = m.row[b * kMaxPairSlots + lane];
-        parts = s2.parts(a * DT + dt);
-      }
-      int end = parts;
-#pragma unroll
-      for (int off = 1; off < 16; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, end, off);
-        if (lane >= off) end += o;
-      }
-      for (int s = 0; s < parts; ++s) {
-        m.from[end - parts + s] = ((size_t)s * p.slots + slot) * p.d;
-        m.weight[end - parts + s] = lane < p.k ? m.w[b * p.k + lane] : 1.f;
-      }
-      if (lane == 15) m.n_from = end;
+    if (u != cta) {
+      __syncthreads();
+      if (warp == 1) list_sums(b, dt);
+      __syncthreads();
     }
-    __syncthreads();
     float acc = 0.f;
     if (tid < 2 * kDnHalf && feat < p.d) {
       const int n = m.n_from;

@@ -103,7 +103,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   DenseBars* bars = reinterpret_cast<DenseBars*>(ring + (size_t)p.stages * stage_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
-  const int S = p.stages, NT = p.NT, KC = p.s.KC;
+  const int S = p.stages, NT = p.NT;
   const int width = p.gated ? kDnHalf : 2 * kDnHalf;  // features of a tile
   int* status = &p.head->ctrl.status;
   volatile int* abort = &bars->abort;
@@ -243,8 +243,8 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
       if (!p.gated) mine += half * NT * 128;
       for (int n0 = begin; n0 < nt; n0 += step) {
         float v[16], m[16];
-        tmem_ld16(d0 + n0, v);
-        if (p.gated) tmem_ld16(d0 + NT + n0, m);
+        tmem_ld(d0 + n0, v);
+        if (p.gated) tmem_ld(d0 + NT + n0, m);
         tmem_wait(v);
         if (p.gated) tmem_wait(m);
         if (parts == 1) {
