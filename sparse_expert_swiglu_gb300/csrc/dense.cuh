@@ -145,6 +145,14 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[4]) {
+  uint32_t r[4];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[2]) {
   uint32_t r[2];
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
@@ -157,6 +165,18 @@ __device__ __forceinline__ void tmem_wait(float (&v)[W]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < W; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+// One thread of the warp.  (The compiler then knows that what follows runs in one thread: products and
+// copies take their operands from uniform registers, and with `lane == 0` in its place each cost over 100 clocks.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint64_t* bar,
@@ -184,6 +204,43 @@ __device__ __forceinline__ void tma_rows4(uint32_t dst, const CUtensorMap* m, in
       "l"(m), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_addr(bar)), "l"(policy)
       : "memory");
 }
+// A CTA pair's products (cta_group::2): both CTAs' copies count on the first one's barrier, one thread of the
+// first CTA issues them, and their completion arrives at both.
+__device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(m), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(desc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_addr(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* at, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(at)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+// a box into L2 alone; what a later copy reads there is what memory holds then
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* m, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
@@ -193,6 +250,45 @@ __device__ __forceinline__ uint64_t policy_evict_normal() {
   return p;
 }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
+// clusters
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// the same shared-memory address in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void peer_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// 16 bytes into a CTA of the cluster, counted on that CTA's barrier
+__device__ __forceinline__ void peer_store(uint32_t to, const float* v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+               "r"(__float_as_uint(v[3])), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool cluster_try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 1000000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
 // ---------------------------------------------------------------------------
 // 16-bit values of either type
@@ -217,15 +313,39 @@ struct DenseBars {
   uint64_t tfull[2];             // a tile's sums are in TMEM
   uint64_t tempty[2];            // ... and have been read
   uint64_t drain;                // on an abort: the products in flight
+  uint64_t xready, xfull;        // linear: the cluster's stages are free; its partial sums have come
   uint32_t tmem;
   int abort;
   int last;
 };
 
+// Whether a phase of a barrier is over, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Bounded wait for a phase of a barrier; false when the time is over or another warp gave up.
 __device__ __forceinline__ bool dn_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_test(bar, parity)) return true;
   for (uint32_t i = 0; i < kWaitTries; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+  }
+  return false;
+}
+
+// The same for a barrier that the cluster's CTAs arrive at.
+__device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  for (uint32_t i = 0; i < kWaitTries; ++i) {
+    if (cluster_try_wait(bar, parity)) return true;
     if (*abort) return false;
   }
   return false;
@@ -236,14 +356,15 @@ __device__ __forceinline__ void dn_fail(DenseBars* b, int* status) {
   set_status(status, MOE_ERR_TIMEOUT);
 }
 
-__device__ __forceinline__ void dn_init_bars(DenseBars* b) {
+// epi_warps: epilogue warps that read a tile's sums
+__device__ __forceinline__ void dn_init_bars(DenseBars* b, int epi_warps = kDnEpi / 32) {
   for (int i = 0; i < kDnMaxStages; ++i) {
     mbar_init(&b->full[i], 1);
     mbar_init(&b->empty[i], 1);
   }
   for (int i = 0; i < 2; ++i) {
     mbar_init(&b->tfull[i], 1);
-    mbar_init(&b->tempty[i], kDnEpi / 32);
+    mbar_init(&b->tempty[i], epi_warps);
   }
   mbar_init(&b->drain, 1);
   b->abort = 0;
@@ -303,17 +424,17 @@ __device__ __forceinline__ void sum_shares(const float* from, size_t stride, int
   }
 }
 
-// One stage's products of both 128-feature tiles.  `lead` = 0: A's rows lie along k.
+// One stage's products of both 128-feature tiles (or, with `both` false, of the first alone).  The k steps of an
+// operand are 32 bytes apart along its rows, 2048 across them: 2 and 128 of the descriptor's units.
 __device__ __forceinline__ void dn_stage_products(uint32_t a, uint32_t b, uint32_t d0, uint32_t d1, uint32_t desc,
-                                                  bool a_mn, bool first) {
+                                                  bool a_mn, bool first, bool both = true) {
+  const uint64_t ad = smem_desc(a, a_mn ? 8192 : 16), bd = smem_desc(b, 16);
+  const uint32_t step = a_mn ? 128 : 2;
 #pragma unroll
   for (int ks = 0; ks < kDnChunk / 16; ++ks) {
-    const uint32_t ao = a_mn ? ks * 2048 : ks * 32;
-    const uint32_t lead = a_mn ? 8192 : 16;
-    const uint64_t bd = smem_desc(b + ks * 32, 16);
     const uint32_t add = !(first && ks == 0);
-    mma_f16(d0, smem_desc(a + ao, lead), bd, desc, add);
-    mma_f16(d1, smem_desc(a + kDnBytesA / 2 + ao, lead), bd, desc, add);
+    mma_f16(d0, ad + ks * step, bd + ks * 2, desc, add);
+    if (both) mma_f16(d1, ad + kDnBytesA / 32 + ks * step, bd + ks * 2, desc, add);
   }
 }
 

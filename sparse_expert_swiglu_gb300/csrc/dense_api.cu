@@ -82,10 +82,7 @@ moe_status_t check_dense_layer(const moe_dense_layer_t* layer, int B) {
 }
 
 // n > kDenseMaxTok tokens of one expert: h [n][f], then the two products' workspace
-size_t expert_products_ws(int n, int d, int f, int sms) {
-  const size_t a = linear_ws_bytes(n, f, d, true, sms), b = linear_ws_bytes(n, d, f, false, sms);
-  return align_up(a > b ? a : b, kWsAlign) + (size_t)n * f * 2;
-}
+size_t expert_products_ws(int n, int f) { return align_up(linear_ws_bytes(), kWsAlign) + (size_t)n * f * 2; }
 
 }  // namespace
 
@@ -93,9 +90,7 @@ extern "C" {
 
 size_t moe_linear_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t gated) {
   if (check_linear_sizes(M, N, K) != MOE_OK) return 0;
-  int sms = 0, smem = 0;
-  if (device_sizes(sms, smem) != cudaSuccess) return 0;
-  return linear_ws_bytes(M, N, K, gated != 0, sms);
+  return linear_ws_bytes();
 }
 
 moe_status_t moe_linear(const moe_linear_t* op, void* ws, size_t ws_bytes, void* stream) {
@@ -113,9 +108,9 @@ moe_status_t moe_linear(const moe_linear_t* op, void* ws, size_t ws_bytes, void*
   if (!aligned(op->x, 16) || !aligned(op->w, 16) || !aligned(op->w_mul, 16) || !aligned(op->bias, 16) ||
       !aligned(op->bias_mul, 16) || !aligned(op->residual, 16) || !aligned(op->y, 16) || !aligned(ws, kWsAlign))
     return MOE_ERR_ALIGNMENT;
+  if (ws_bytes < linear_ws_bytes()) return MOE_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0, smem = 0;
   if (device_sizes(sms, smem) != cudaSuccess) return MOE_ERR_CUDA;
-  if (ws_bytes < linear_ws_bytes(op->M, op->N, op->K, op->w_mul != nullptr, sms)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   LinearCall c = {};
   c.M = op->M;
   c.N = op->N;
@@ -137,10 +132,10 @@ moe_status_t moe_linear(const moe_linear_t* op, void* ws, size_t ws_bytes, void*
 
 size_t moe_expert_dense_workspace_bytes(int32_t n, int32_t d, int32_t f) {
   if (n < 0 || n > kMaxTokens || check_dense_sizes(d, f) != MOE_OK) return 0;
+  if (n > kDenseMaxTok) return expert_products_ws(n, f);
   int sms = 0, smem = 0;
   if (device_sizes(sms, smem) != cudaSuccess) return 0;
-  if (n <= kDenseMaxTok) return dense_layer_ws_bytes(n, d, f, 0, 0, 1, sms);
-  return expert_products_ws(n, d, f, sms);
+  return dense_layer_ws_bytes(n, d, f, 0, 0, 1, sms);
 }
 
 moe_status_t moe_expert_dense_swiglu(const uint16_t* x, int32_t n, const moe_dense_experts_t* experts,
@@ -177,7 +172,7 @@ moe_status_t moe_expert_dense_swiglu(const uint16_t* x, int32_t n, const moe_den
     c.y = y;
     return cuda_status(launch_dense_layer(c, ws, sms, smem, st));
   }
-  const size_t need = expert_products_ws(n, d, f, sms);
+  const size_t need = expert_products_ws(n, f);
   if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   // h in the operand's type, as the second product reads it
   void* h = reinterpret_cast<uint8_t*>(ws) + (need - (size_t)n * f * 2);

@@ -433,7 +433,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
 
   if (!ok) {
   } else if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint64_t pw = policy_evict_first(), px = policy_evict_normal();
       int st = 0, issued = 0;
       uint32_t ph = 0;
@@ -543,7 +543,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       int st = 0, buf = 0;
       uint32_t ph = 0, tph = 0;
       bool go = true, open = false;

@@ -16,7 +16,7 @@ struct LinearCall {
   size_t w_stride, w_mul_stride;  // elements between rows
 };
 
-size_t linear_ws_bytes(int M, int N, int K, bool gated, int sms);
+size_t linear_ws_bytes();
 cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin, cudaStream_t st);
 
 struct DenseExpertSet {

@@ -1,11 +1,12 @@
 // y = act(x w^T + bias) [* (x w_mul^T + bias_mul)] [+ residual] on 16-bit x and w, fp32 sums.
 //
-// The features lie on the 128 TMEM lanes, the tokens on the columns: a tile is 256 features
-// (two products of 128 that share the token operand; with w_mul 128 features of each matrix)
-// by up to 256 tokens.  With few tokens the call is a stream of w, bound by HBM: the work is
-// cut along k so that every SM streams an equal share, and the last share of a tile to come
-// adds the others' partial sums (in the order of k) and runs the epilogue.  With many tokens
-// it is bound by the tensor cores.
+// The features lie on the 128 TMEM lanes, the tokens on the columns: a tile is up to 256 features
+// (two products of 128 lanes that share the token operand; with w_mul one of each matrix) by up to
+// 256 tokens.  With few tokens the call is a stream of w, bound by HBM; with many it is bound by the
+// tensor cores.  Where there are fewer tiles than SMs, a cluster of 2, 4 or 8 CTAs shares a tile
+// along k: each CTA pushes its partial sums into the shared memory of the CTA that owns their features,
+// which adds them in the order of k and runs the epilogue for them (no workspace, no
+// count in global memory).  linear_plan chooses the tile and the cluster.
 #include "dense.cuh"
 #include "dense_params.cuh"
 
@@ -14,102 +15,134 @@ namespace sesg {
 namespace {
 
 struct LinearArgs {
-  int M, N, MT, NT, gated, bf16, kn, act, out_f32;
-  Sched s;
+  int M, N, gated, bf16, kn, act, out_f32;
+  int MT, NT, T;    // token tiles, tokens of a tile, tiles
+  int rows;         // features of one product, <= 128
+  int both;         // two products (always with w_mul)
+  int KC, S;        // chunks of k, CTAs of a tile
+  int groups;       // accumulators of a product: chunk c of a tile goes to c % groups
   const void *bias, *bias_mul, *residual;
   void* y;
-  float* part;      // [segment][2][NT][128]
   DenseHead* head;
-  int stages, acc_bufs, tmem_cols, stream;
+  int stages, acc_bufs, buf_cols, tmem_cols, stream;
+  int ahead;        // chunks of a CTA's first tile that are asked for before the previous kernel has ended
 };
 
-// One decision for 16 values, not one for each.
-__device__ __forceinline__ void activate(float (&v)[16], int act) {
+// One decision for W values, not one for each.
+template <int W>
+__device__ __forceinline__ void activate(float (&v)[W], int act) {
   switch (act) {
     case MOE_ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];  // NaN stays NaN
+      for (int i = 0; i < W; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];  // NaN stays NaN
       break;
     case MOE_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0.5f * v[i] * (1.f + erff(v[i] * 0.70710678118654752f));
+      for (int i = 0; i < W; ++i) v[i] = 0.5f * v[i] * (1.f + erff(v[i] * 0.70710678118654752f));
       break;
     case MOE_ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < W; ++i)
         v[i] = 0.5f * v[i] * (1.f + tanhf(0.79788456080286536f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));
       break;
     case MOE_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = silu_f(v[i]);
+      for (int i = 0; i < W; ++i) v[i] = silu_f(v[i]);
       break;
     default: break;
   }
 }
 
-// Residual and store of 16 tokens' values of one feature; token i at offset at + i * N.
-template <bool FULL>
-__device__ __forceinline__ void linear_write(const LinearArgs& p, size_t at, int n, float (&v)[16]) {
+// Residual and store of W tokens' values of one feature; token i at offset at + i * N.
+template <int W, bool FULL>
+__device__ __forceinline__ void linear_write(const LinearArgs& p, size_t at, int n, float (&v)[W]) {
   if (p.residual) {
     const unsigned short* r = reinterpret_cast<const unsigned short*>(p.residual) + at;
-    unsigned short t[16];
+    unsigned short t[W];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t[i] = FULL || i < n ? r[(size_t)i * p.N] : (unsigned short)0;
+    for (int i = 0; i < W; ++i) t[i] = FULL || i < n ? r[(size_t)i * p.N] : (unsigned short)0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] += from16(t[i], p.bf16);
+    for (int i = 0; i < W; ++i) v[i] += from16(t[i], p.bf16);
   }
   if (p.out_f32) {
     float* y = reinterpret_cast<float*>(p.y) + at;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < W; ++i)
       if (FULL || i < n) y[(size_t)i * p.N] = v[i];
   } else {
     unsigned short* y = reinterpret_cast<unsigned short*>(p.y) + at;
-    unsigned short t[16];
+    unsigned short t[W];
     if (p.bf16) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) t[i] = to16(v[i], 1);
+      for (int i = 0; i < W; ++i) t[i] = to16(v[i], 1);
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) t[i] = to16(v[i], 0);
+      for (int i = 0; i < W; ++i) t[i] = to16(v[i], 0);
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < W; ++i)
       if (FULL || i < n) y[(size_t)i * p.N] = t[i];
   }
 }
 
-// Epilogue of 16 tokens of one feature: v, and with w_mul m, are the sums; n tokens from t0 exist.
+// Epilogue of W tokens of one feature: v, and with w_mul m, are the sums; n tokens from t0 exist.
+template <int W>
 __device__ __forceinline__ void linear_store(const LinearArgs& p, int feat, int t0, int n, float bias, float bias_mul,
-                                             float (&v)[16], const float (&m)[16], bool gated) {
+                                             float (&v)[W], const float (&m)[W]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] += bias;
+  for (int i = 0; i < W; ++i) v[i] += bias;
   activate(v, p.act);
-  if (gated) {
+  if (p.gated) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] *= m[i] + bias_mul;
+    for (int i = 0; i < W; ++i) v[i] *= m[i] + bias_mul;
   }
   const size_t at = (size_t)t0 * p.N + feat;
-  if (n >= 16) linear_write<true>(p, at, n, v);
-  else linear_write<false>(p, at, n, v);
+  if (n >= W) linear_write<W, true>(p, at, n, v);
+  else linear_write<W, false>(p, at, n, v);
 }
 
-__global__ void __launch_bounds__(kDnThreads, 1)
+// W columns of a product, its accumulators added.
+template <int W>
+__device__ __forceinline__ void linear_sums(uint32_t addr, int groups, int stride, float (&v)[W]) {
+  tmem_ld(addr, v);
+  tmem_wait(v);
+  for (int g = 1; g < groups; ++g) {
+    float t[W];
+    tmem_ld(addr + g * stride, t);
+    tmem_wait(t);
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] += t[i];
+  }
+}
+
+// FEW: up to kFewTokens tokens.  Half the shared memory and registers, so that the next call's CTAs start
+// beside this one's and ask for their weights while these still stream: a chain of such calls keeps HBM
+// busy.  (Asked for into L2 alone, since the previous kernel may still write them.)
+template <bool FEW>
+__global__ void __launch_bounds__(kDnThreads, FEW ? 2 : 1)
 linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mw2,
               const __grid_constant__ CUtensorMap mx, const LinearArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  const uint32_t stage_bytes = kDnBytesA + p.NT * 128;
+  const int bytes_a = p.both ? kDnBytesA : kDnBytesA / 2;  // of a stage; rows behind p.rows stay unwritten
+  const uint32_t stage_bytes = bytes_a + p.NT * 128;
+  const uint32_t load_bytes = (p.both ? 2 : 1) * p.rows * 128 + p.NT * 128;
   DenseBars* bars = reinterpret_cast<DenseBars*>(ring + (size_t)p.stages * stage_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int cta = blockIdx.x;
-  const int S = p.stages, NT = p.NT;
-  const int width = p.gated ? kDnHalf : 2 * kDnHalf;  // features of a tile
+  const int S = p.S, ns = p.stages, NT = p.NT;
+  const int rank = S > 1 ? (int)cluster_rank() : 0;
+  const int first = blockIdx.x / S, step = gridDim.x / S;  // tiles of this CTA; S > 1: one
+  const int kc0 = p.KC * rank / S, kc1 = p.KC * (rank + 1) / S;
+  const int width = p.gated || !p.both ? p.rows : 2 * p.rows;  // features of a tile
   int* status = &p.head->ctrl.status;
   volatile int* abort = &bars->abort;
+  const uint32_t ring_at = smem_addr(ring);
 
   if (tid == 0) {
     dn_init_bars(bars);
+    mbar_init(&bars->xready, S);
+    mbar_init(&bars->xfull, 1);
+    fence_barrier_init();
     tma_prefetch_map(&mw);
     tma_prefetch_map(&mx);
     if (p.gated) tma_prefetch_map(&mw2);
@@ -117,89 +150,106 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   if (warp == 2) tmem_alloc(&bars->tmem, p.tmem_cols);
   tc_before_sync();
   __syncthreads();
+  if (S > 1) cluster_sync_all();  // the barriers are there before any CTA of the cluster uses them
   tc_after_sync();
   const uint32_t tmem = bars->tmem;
-  griddep_wait();
   griddep_launch_dependents();
+  if (FEW && warp == 0 && elect_one()) {
+    const int f0 = first / p.MT * width, n = kc1 - kc0 < p.ahead ? kc1 - kc0 : p.ahead;
+    const CUtensorMap* m2 = p.gated ? &mw2 : &mw;
+    const int f1 = p.gated ? f0 : f0 + p.rows;
+    for (int i = 0; i < n; ++i) {
+      const int k = (kc0 + i) * kDnChunk;
+      if (!p.kn) {
+        tma_prefetch_2d(&mw, k, f0);
+        if (p.both) tma_prefetch_2d(m2, k, f1);
+      } else {
+        for (int j = 0; j < p.rows; j += 64) {
+          tma_prefetch_2d(&mw, f0 + j, k);
+          if (p.both) tma_prefetch_2d(m2, f1 + j, k);
+        }
+      }
+    }
+  }
+  griddep_wait();
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       // w is read once when one tile of tokens covers them all
       const uint64_t pw = p.stream ? policy_evict_first() : policy_evict_normal();
       const uint64_t px = policy_evict_normal();
-      SegIter it(p.s, cta);
-      Seg g;
       int st = 0, issued = 0;
       uint32_t ph = 0;
       bool ok = true;
-      while (ok && it.next(g)) {
-        const int ft = g.t / p.MT, mt = g.t - ft * p.MT, f0 = ft * width, m0 = mt * NT;
-        for (int kc = g.k0; kc < g.k1; ++kc) {
+      for (int t = first; ok && t < p.T; t += step) {
+        const int ft = t / p.MT, mt = t - ft * p.MT, f0 = ft * width, m0 = mt * NT;
+        const CUtensorMap* m2 = p.gated ? &mw2 : &mw;
+        const int f1 = p.gated ? f0 : f0 + p.rows;
+        for (int kc = kc0; kc < kc1; ++kc) {
           if (!dn_wait(&bars->empty[st], ph ^ 1, abort)) {
             dn_fail(bars, status);
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&bars->full[st], stage_bytes);
+          uint64_t* full = &bars->full[st];
+          mbar_arrive_expect_tx(full, load_bytes);
           ++issued;
-          const uint32_t a = smem_addr(ring + (size_t)st * stage_bytes);
+          const uint32_t a = ring_at + st * stage_bytes;
           const int k = kc * kDnChunk;
           if (!p.kn) {
-            tma_2d(a, &mw, k, f0, &bars->full[st], pw);
-            if (p.gated) tma_2d(a + kDnBytesA / 2, &mw2, k, f0, &bars->full[st], pw);
-            else tma_2d(a + kDnBytesA / 2, &mw, k, f0 + kDnHalf, &bars->full[st], pw);
+            tma_2d(a, &mw, k, f0, full, pw);
+            if (p.both) tma_2d(a + kDnBytesA / 2, m2, k, f1, full, pw);
           } else {
-            tma_2d(a, &mw, f0, k, &bars->full[st], pw);
-            tma_2d(a + 8192, &mw, f0 + 64, k, &bars->full[st], pw);
-            const CUtensorMap* m2 = p.gated ? &mw2 : &mw;
-            const int f1 = p.gated ? f0 : f0 + kDnHalf;
-            tma_2d(a + 16384, m2, f1, k, &bars->full[st], pw);
-            tma_2d(a + 24576, m2, f1 + 64, k, &bars->full[st], pw);
+            for (int i = 0; i < p.rows; i += 64) {
+              tma_2d(a + i * 128, &mw, f0 + i, k, full, pw);
+              if (p.both) tma_2d(a + kDnBytesA / 2 + i * 128, m2, f1 + i, k, full, pw);
+            }
           }
-          tma_2d(a + kDnBytesA, &mx, k, m0, &bars->full[st], px);
-          if (++st == S) {
+          tma_2d(a + bytes_a, &mx, k, m0, full, px);
+          if (++st == ns) {
             st = 0;
             ph ^= 1;
           }
         }
       }
-      // no copy of this CTA is in flight when it ends: the last S stages have come
-      const int n = issued < S ? issued : S;
+      // no copy of this CTA is in flight when it ends: the last stages have come
+      const int n = issued < ns ? issued : ns;
       for (int i = 0; i < n; ++i) {
         if (--st < 0) {
-          st = S - 1;
+          st = ns - 1;
           ph ^= 1;
         }
         for (uint32_t w = 0; w < kWaitTries && !mbar_try_wait(&bars->full[st], ph); ++w) {}
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t desc = mma_desc(NT, p.bf16, p.kn);
-      SegIter it(p.s, cta);
-      Seg g;
+      const int grp_cols = (p.both ? 2 : 1) * NT;
       int st = 0, buf = 0;
       uint32_t ph = 0, tph = 0;
       bool ok = true, open = false;
-      while (ok && it.next(g)) {
+      for (int t = first; ok && t < p.T; t += step) {
         if (!dn_wait(&bars->tempty[buf], tph ^ 1, abort)) {
           dn_fail(bars, status);
           break;
         }
         tc_after_sync();
-        const uint32_t d0 = tmem + buf * 2 * NT, d1 = d0 + NT;
-        for (int kc = g.k0; kc < g.k1; ++kc) {
+        int grp = 0;
+        for (int kc = kc0; kc < kc1; ++kc) {
           if (!dn_wait(&bars->full[st], ph, abort)) {
             dn_fail(bars, status);
             ok = false;
             break;
           }
           tc_after_sync();
-          const uint32_t a = smem_addr(ring + (size_t)st * stage_bytes);
-          dn_stage_products(a, a + kDnBytesA, d0, d1, desc, p.kn, kc == g.k0);
+          const uint32_t a = ring_at + st * stage_bytes;
+          const uint32_t d0 = tmem + buf * p.buf_cols + grp * grp_cols;
+          dn_stage_products(a, a + bytes_a, d0, d0 + NT, desc, p.kn, kc - kc0 < p.groups, p.both);
           mma_commit(&bars->empty[st]);
           open = true;
-          if (++st == S) {
+          if (++grp == p.groups) grp = 0;
+          if (++st == ns) {
             st = 0;
             ph ^= 1;
           }
@@ -217,89 +267,463 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
       }
     }
   } else if (warp >= 4) {
-    // lanes 32 (warp % 4) ... are this warp's; of the two warps that have them, with w_mul each takes
-    // every other 16 tokens, without it one takes each 128 features
-    const int q = warp & 3, half = (warp - 4) >> 2, r = q * 32 + lane, etid = tid - 128;
-    const int step = p.gated ? 32 : 16, begin = p.gated ? 16 * half : 0;
-    SegIter it(p.s, cta);
-    Seg g;
+    // Lanes 32 (warp % 4) ... are this warp's.  Of the two warps that have them, each takes one of the
+    // two products, or, where both products belong to one feature (or there is one), every other 16 tokens.
+    constexpr int W = FEW ? 4 : 16;  // tokens at a time
+    const int q = warp & 3, half = (warp - 4) >> 2, etid = tid - 128;
+    const bool by_tok = p.gated || !p.both;
+    const int tok0 = by_tok ? 16 * half : 0, tok_step = by_tok ? 32 : 16;
+    const int r = q * 32 + lane;
+    const int groups = kc1 - kc0 < p.groups ? kc1 - kc0 : p.groups, grp_cols = (p.both ? 2 : 1) * NT;
     int buf = 0;
     uint32_t tph = 0;
-    while (it.next(g)) {
-      const bool ok = dn_wait(&bars->tfull[buf], tph, abort);
-      if (!ok) dn_fail(bars, status);
-      if (dn_any(1, kDnEpi, !ok)) break;  // one decision for the warps: they meet at barriers below
-      tc_after_sync();
-      const int ft = g.t / p.MT, mt = g.t - ft * p.MT, m0 = mt * NT;
+    for (int t = first; t < p.T; t += step) {
+      const int ft = t / p.MT, mt = t - ft * p.MT, m0 = mt * NT;
       const int nt = p.M - m0 < NT ? p.M - m0 : NT;  // tokens of this tile
-      const int feat = ft * width + (p.gated ? 0 : half * kDnHalf) + r;
-      const bool on = feat < p.N;
-      const uint32_t d0 = tmem + ((uint32_t)(q * 32) << 16) + buf * 2 * NT + (p.gated ? 0 : half * NT);
-      const int parts = p.s.parts(g.t);
-      const float ba = p.bias && on ? ld16(p.bias, feat, p.bf16) : 0.f;
-      const float bb = p.bias_mul && on ? ld16(p.bias_mul, feat, p.bf16) : 0.f;
-      const size_t seg_floats = (size_t)2 * NT * 128;
-      float* mine = p.part + ((size_t)(g.t - p.s.dp) + cta) * seg_floats + r;  // used where parts > 1
-      if (!p.gated) mine += half * NT * 128;
-      for (int n0 = begin; n0 < nt; n0 += step) {
-        float v[16], m[16];
-        tmem_ld(d0 + n0, v);
-        if (p.gated) tmem_ld(d0 + NT + n0, m);
-        tmem_wait(v);
-        if (p.gated) tmem_wait(m);
-        if (parts == 1) {
-          if (on) linear_store(p, feat, m0 + n0, nt - n0, ba, bb, v, m, p.gated);
-        } else {
+      if (S == 1) {
+        const int feat = ft * width + (by_tok ? 0 : half * p.rows) + r;
+        const bool on = r < p.rows && feat < p.N;
+        const float ba = p.bias && on ? ld16(p.bias, feat, p.bf16) : 0.f;
+        const float bb = p.bias_mul && on ? ld16(p.bias_mul, feat, p.bf16) : 0.f;
+        const bool ok = dn_wait(&bars->tfull[buf], tph, abort);
+        if (!ok) dn_fail(bars, status);
+        if (dn_any(1, kDnEpi, !ok)) break;  // one decision for the warps
+        tc_after_sync();
+        const uint32_t d0 = tmem + ((uint32_t)(q * 32) << 16) + buf * p.buf_cols + (by_tok ? 0 : half * NT);
+        for (int n0 = tok0; n0 < nt; n0 += tok_step) {
+#pragma unroll 1
+          for (int i = n0; i < nt && i < n0 + 16; i += W) {
+            float v[W], m[W];
+            linear_sums(d0 + i, groups, grp_cols, v);
+            if (p.gated) linear_sums(d0 + NT + i, groups, grp_cols, m);
+            if (on) linear_store(p, feat, m0 + i, nt - i, ba, bb, v, m);
+            __syncwarp();
+          }
+        }
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->tempty[buf]);
+        if (++buf == p.acc_bufs) {
+          buf = 0;
+          tph ^= 1;
+        }
+      } else {
+        // The warp pair's unit 2 q + half of sums belongs to CTA unit * S / 8: 4 tokens of a feature are 16
+        // bytes at [unit of the owner][rank][matrix][4 tokens][lane] in its first stages.
+        const int mats = p.gated ? 2 : 1, g4 = (NT + 3) / 4;  // room for all tokens' groups of 4 in a unit
+        const uint32_t unit_bytes = mats * g4 * 512;
+        const int per = 8 / S, unit = 2 * q + half;
+        auto groups4 = [&](int h) {  // groups of 4 tokens that exist in a unit of half h
+          if (!by_tok) return (nt + 3) / 4;
+          int n = 0;
+          for (int n0 = 16 * h; n0 < nt; n0 += 32) n += ((nt - n0 < 16 ? nt - n0 : 16) + 3) / 4;
+          return n;
+        };
+        bool ok = dn_wait(&bars->tfull[0], 0, abort);
+        if (etid == 0 && ok) {
+          uint32_t bytes = 0;
+          for (int i = 0; i < per; ++i) bytes += S * mats * groups4((rank * per + i) & 1) * 512;
+          mbar_arrive_expect_tx(&bars->xfull, bytes);
+          for (int i = 0; i < S; ++i) peer_arrive(peer_addr(smem_addr(&bars->xready), i));
+        }
+        ok = ok && cluster_wait(&bars->xready, 0, abort);
+        if (!ok) dn_fail(bars, status);
+        if (dn_any(1, kDnEpi, !ok)) break;
+        tc_after_sync();
+        {
+          const int owner = unit / per;
+          const uint32_t d0 = tmem + ((uint32_t)(q * 32) << 16) + (by_tok ? 0 : half * NT);
+          uint32_t to = peer_addr(smem_addr(ring), owner) + ((unit - owner * per) * S + rank) * unit_bytes + lane * 16;
+          const uint32_t bar = peer_addr(smem_addr(&bars->xfull), owner);
+          for (int n0 = tok0; n0 < nt; n0 += tok_step) {
+#pragma unroll 1
+            for (int i = n0; i < nt && i < n0 + 16; i += W) {
+#pragma unroll 1
+              for (int mat = 0; mat < mats; ++mat) {
+                float v[W];
+                linear_sums(d0 + mat * NT + i, groups, grp_cols, v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (n0 + i < nt) {
-              __stcg(mine + (n0 + i) * 128, v[i]);
-              if (p.gated) __stcg(mine + (NT + n0 + i) * 128, m[i]);
+                for (int j = 0; j < W; j += 4)
+                  if (i + j < nt) peer_store(to + (mat * g4 + j / 4) * 512, v + j, bar);
+              }
+              to += W / 4 * 512;
             }
           }
         }
-        __syncwarp();
-      }
-      tc_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->tempty[buf]);
-      if (parts > 1 && dn_last_share(&p.head->cnt[g.t - p.s.dp], parts, bars, etid) && on) {
-        const float* from = p.part + ((size_t)(g.t - p.s.dp) + p.s.first(g.t)) * seg_floats + r;
-        if (!p.gated) from += half * NT * 128;
-        for (int n0 = begin; n0 < nt; n0 += step) {
-          float v[16], m[16];
-          sum_shares(from + n0 * 128, seg_floats, parts, nt - n0, v);
-          if (p.gated) sum_shares(from + (NT + n0) * 128, seg_floats, parts, nt - n0, m);
-          linear_store(p, feat, m0 + n0, nt - n0, ba, bb, v, m, p.gated);
+        ok = cluster_wait(&bars->xfull, 0, abort);
+        if (!ok) dn_fail(bars, status);
+        if (dn_any(1, kDnEpi, !ok)) break;
+        {
+          // S warps for each of this CTA's units, taking its groups of 4 tokens in turn
+          const int w = warp - 4, ul = w / S, u = rank * per + ul, uq = u >> 1, uh = u & 1;
+          const int feat = ft * width + (by_tok ? 0 : uh * p.rows) + uq * 32 + lane;
+          const bool on = uq * 32 + lane < p.rows && feat < p.N;
+          const float ba = p.bias && on ? ld16(p.bias, feat, p.bf16) : 0.f;
+          const float bb = p.bias_mul && on ? ld16(p.bias_mul, feat, p.bf16) : 0.f;
+          const int n4 = groups4(uh);
+          const uint8_t* from = ring + (size_t)ul * S * unit_bytes + lane * 16;
+          for (int i = w % S; i < n4; i += S) {
+            float v[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+            for (int s = 0; s < S; ++s) {
+              const float4 a = *reinterpret_cast<const float4*>(from + s * unit_bytes + i * 512);
+              v[0] += a.x;
+              v[1] += a.y;
+              v[2] += a.z;
+              v[3] += a.w;
+              if (p.gated) {
+                const float4 b = *reinterpret_cast<const float4*>(from + s * unit_bytes + (g4 + i) * 512);
+                m[0] += b.x;
+                m[1] += b.y;
+                m[2] += b.z;
+                m[3] += b.w;
+              }
+            }
+            const int n0 = by_tok ? 16 * uh + 32 * (i >> 2) + 4 * (i & 3) : 4 * i;
+            if (on) linear_store(p, feat, m0 + n0, nt - n0, ba, bb, v, m);
+          }
         }
-      }
-      if (++buf == p.acc_bufs) {
-        buf = 0;
-        tph ^= 1;
       }
     }
   }
   __syncwarp();
   tc_before_sync();
   __syncthreads();
+  if (S > 1) cluster_sync_all();  // no CTA leaves while another may store into it
   tc_after_sync();
   if (warp == 2) tmem_free(tmem, p.tmem_cols);
 }
 
-struct LinearPlan {
-  int NT, MT, FT;
-  Sched s;
+// ---------------------------------------------------------------------------
+// Many tokens: CTA pairs (cta_group::2).  Here the tokens lie on the lanes, 128 of a tile's 256 in each
+// CTA, and 256 columns of weights are the other operand, 128 from each CTA's shared memory (with
+// w_mul: 128 rows of w from the first CTA, the same rows of w_mul from the second, so that one thread has both
+// sums of a feature).  A stage is 32 KB for 4 products of 128 clocks, half of what one CTA alone would have to
+// fetch and read, and the 256 columns of sums are doubled: the epilogue of a tile runs under the next one's
+// products, and stores 16 bytes of a token's row at a time.
+// ---------------------------------------------------------------------------
+constexpr int kPairStage = 2 * kDnHalf * kDnChunk * 2;
+constexpr int kPairStages = 7;
+
+struct PairArgs {
+  int M, N, gated, bf16, kn, act, out_f32;
+  int MT, T, KC;
+  const void *bias, *bias_mul, *residual;
+  void* y;
+  DenseHead* head;
 };
 
-LinearPlan linear_plan(int M, int N, int K, bool gated, int sms) {
+// 8 neighbouring features of a token from a 16-bit array, added or assigned; n of them exist.
+__device__ __forceinline__ void load8(const void* base, size_t at, int n, int bf16, float (&v)[8]) {
+  uint4 t = make_uint4(0, 0, 0, 0);
+  if (n > 0) t = *reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned short*>(base) + at);
+  const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = from16((unsigned short)(w[i / 2] >> (16 * (i & 1))), bf16);
+}
+
+// Epilogue of 16 neighbouring features of one token (N a multiple of 8: of each 8 all exist or none).
+__device__ __forceinline__ void pair_store(const PairArgs& p, size_t row, int feat, float (&v)[16], const float (&m)[16]) {
+  float t[8];
+  if (p.bias) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      load8(p.bias, feat + 8 * h, p.N - feat - 8 * h, p.bf16, t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[8 * h + i] += t[i];
+    }
+  }
+  activate(v, p.act);
+  if (p.gated) {
+    if (p.bias_mul) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        load8(p.bias_mul, feat + 8 * h, p.N - feat - 8 * h, p.bf16, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * h + i] *= m[8 * h + i] + t[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] *= m[i];
+    }
+  }
+  const size_t at = row * p.N + feat;
+  if (p.residual) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      load8(p.residual, at + 8 * h, p.N - feat - 8 * h, p.bf16, t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[8 * h + i] += t[i];
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (feat + 8 * h >= p.N) break;
+    if (p.out_f32) {
+      float4* y = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.y) + at + 8 * h);
+      y[0] = make_float4(v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]);
+      y[1] = make_float4(v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = (uint32_t)to16(v[8 * h + 2 * i], p.bf16) | (uint32_t)to16(v[8 * h + 2 * i + 1], p.bf16) << 16;
+      *reinterpret_cast<uint4*>(reinterpret_cast<unsigned short*>(p.y) + at + 8 * h) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDnThreads, 1)
+linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mw2,
+                   const __grid_constant__ CUtensorMap mx, const PairArgs p) {
+  extern __shared__ uint8_t raw[];
+  // the same offset in both CTAs: the products address both CTAs' stages by it
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  DenseBars* bars = reinterpret_cast<DenseBars*>(ring + (size_t)kPairStages * kPairStage);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_rank(), first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int width = p.gated ? kDnHalf : 2 * kDnHalf;  // features of a tile
+  int* status = &p.head->ctrl.status;
+  volatile int* abort = &bars->abort;
+  const uint32_t ring_at = smem_addr(ring);
+
+  if (tid == 0) {
+    dn_init_bars(bars, 2 * kDnEpi / 32);
+    tma_prefetch_map(&mw);
+    tma_prefetch_map(&mx);
+    if (p.gated) tma_prefetch_map(&mw2);
+  }
+  if (warp == 2) tmem_alloc_pair(&bars->tmem, 512);
+  tc_before_sync();
+  __syncthreads();
+  cluster_sync_all();
+  tc_after_sync();
+  const uint32_t tmem = bars->tmem;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == 0) {
+    if (elect_one()) {
+      const uint64_t pol = policy_evict_normal();
+      const CUtensorMap* mb = p.gated && rank ? &mw2 : &mw;
+      const uint32_t full_at = peer_addr(smem_addr(&bars->full[0]), 0);
+      int st = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = first; ok && t < p.T; t += step) {
+        const int ft = t / p.MT, mt = t - ft * p.MT;
+        const int m0 = mt * 2 * kDnHalf + rank * kDnHalf, f0 = ft * width + (p.gated ? 0 : rank * kDnHalf);
+        for (int kc = 0; kc < p.KC; ++kc) {
+          if (!dn_wait(&bars->empty[st], ph ^ 1, abort)) {
+            dn_fail(bars, status);
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&bars->full[st], 2 * kPairStage);
+          const uint32_t full = full_at + st * 8;
+          const uint32_t a = ring_at + st * kPairStage, b = a + kPairStage / 2;
+          const int k = kc * kDnChunk;
+          tma_2d_pair(a, &mx, k, m0, full, pol);
+          if (!p.kn) {
+            tma_2d_pair(b, mb, k, f0, full, pol);
+          } else {
+            tma_2d_pair(b, mb, f0, k, full, pol);
+            tma_2d_pair(b + 8192, mb, f0 + 64, k, full, pol);
+          }
+          if (++st == kPairStages) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      // After an abort copies may be in flight that no barrier of this CTA counts: they come long before
+      // this is over.  (Without one, every copy has been used.)
+      if (*abort)
+        for (int i = 0; i < 8; ++i) __nanosleep(1000000);
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && elect_one()) {
+      // 256 lanes (both CTAs) by 256 columns
+      const uint32_t desc = (1u << 4) | ((uint32_t)p.bf16 << 7) | ((uint32_t)p.bf16 << 10) | ((uint32_t)p.kn << 16) |
+                            ((256u >> 3) << 17) | ((256u >> 4) << 24);
+      int st = 0, buf = 0;
+      uint32_t ph = 0, tph = 0;
+      bool ok = true, open = false;
+      for (int t = first; ok && t < p.T; t += step) {
+        if (!cluster_wait(&bars->tempty[buf], tph ^ 1, abort)) {
+          dn_fail(bars, status);
+          break;
+        }
+        tc_after_sync();
+        const uint32_t d = tmem + buf * 256;
+        for (int kc = 0; kc < p.KC; ++kc) {
+          if (!dn_wait(&bars->full[st], ph, abort)) {
+            dn_fail(bars, status);
+            ok = false;
+            break;
+          }
+          tc_after_sync();
+          const uint32_t a = ring_at + st * kPairStage;
+          const uint64_t ad = smem_desc(a, 16), bd = smem_desc(a + kPairStage / 2, p.kn ? 8192 : 16);
+          const uint32_t step = p.kn ? 128 : 2;
+#pragma unroll
+          for (int ks = 0; ks < kDnChunk / 16; ++ks)
+            mma_f16_pair(d, ad + ks * 2, bd + ks * step, desc, kc > 0 || ks > 0);
+          mma_commit_pair(&bars->empty[st]);
+          open = true;
+          if (++st == kPairStages) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair(&bars->tfull[buf]);
+        buf ^= 1;
+        tph ^= buf == 0;
+      }
+      if (open) {  // every product is done before TMEM is given back
+        mma_commit_pair(&bars->drain);
+        for (uint32_t w = 0; w < kWaitTries && !cluster_try_wait(&bars->drain, 0); ++w) {}
+      }
+    }
+  } else if (warp >= 4) {
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const int cols = p.gated ? kDnHalf / 2 : kDnHalf;  // features of this warp
+    int buf = 0;
+    uint32_t tph = 0;
+    for (int t = first; t < p.T; t += step) {
+      const int ft = t / p.MT, mt = t - ft * p.MT;
+      const int tok = mt * 2 * kDnHalf + rank * kDnHalf + q * 32 + lane;
+      const int f0 = ft * width + half * cols;
+      const bool ok = dn_wait(&bars->tfull[buf], tph, abort);
+      if (!ok) dn_fail(bars, status);
+      if (dn_any(1, kDnEpi, !ok)) break;
+      tc_after_sync();
+      const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + buf * 256 + half * cols;
+      for (int c = 0; c < cols && f0 + c < p.N; c += 16) {
+        float v[16], m[16];
+        tmem_ld(d + c, v);
+        if (p.gated) tmem_ld(d + kDnHalf + c, m);
+        tmem_wait(v);
+        if (p.gated) tmem_wait(m);
+        if (tok < p.M) pair_store(p, tok, f0 + c, v, m);
+        __syncwarp();
+      }
+      tc_before_sync();
+      __syncwarp();
+      if (lane == 0) peer_arrive(peer_addr(smem_addr(&bars->tempty[buf]), 0));
+      buf ^= 1;
+      tph ^= buf == 0;
+    }
+  }
+  __syncwarp();
+  tc_before_sync();
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while the other's copies or arrivals may reach it
+  tc_after_sync();
+  if (warp == 2) tmem_free_pair(tmem, 512);
+}
+
+struct LinearPlan {
+  int M = -1, N, K, gated, kn, wide, sms;   // what it is for
+  int pair, NT, MT, rows, both, S, T;
+};
+
+constexpr int kFewTokens = 32;
+
+// Clusters of S CTAs that fit the GPU at once, of at most one CTA per SM (152 SMs: 76, 36 and 15; the SMs of a
+// cluster lie in one part of the chip).
+int clusters(int S, int sms) { return S == 1 ? sms : S == 2 ? sms / 2 : S == 4 ? sms / 4 - 2 : sms / 8 - 4; }
+
+int linear_stages(const LinearPlan& l, int smem) {
+  const int stage = (l.both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128;
+  // few tokens: two CTAs on an SM
+  const int room = (l.NT <= kFewTokens ? smem / 2 - 2048 : smem) - 1024 - (int)sizeof(DenseBars);
+  const int n = room / stage;
+  return n > kDnMaxStages ? kDnMaxStages : n;
+}
+
+// The tile and the cluster with the least time by a model in SM clocks.  Its terms, as measured (GB300,
+// 1.9 GHz): a call costs 9500 whatever it does; an SM takes 52 bytes a clock from L2 (g = 4096 x 14336
+// gated: 47 KB stages in 1240 clocks, 64 KB stages in 1270) and all SMs 3550 out of HBM; a product of 128 x NT
+// x 16 takes NT / 2, and 2 at least 40 together; joining a cluster's sums 3000 and 50 for each token;
+// a tile's epilogue 600 and 12 for each token, which runs under the next tile's products where TMEM holds
+// both (NT <= 128).  A pair's stage is 700 (300 tokens: 78 us against the model's 76).
+LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool wide, int sms, int smem) {
+  LinearPlan best;
+  double best_t = 1e30;
+  const int KC = (K + kDnChunk - 1) / kDnChunk, mats = gated ? 2 : 1;
+  const double w_bytes = 2.0 * mats * N * K, hbm = 3550;
+  auto keep = [&](const LinearPlan& l, double t) {
+    if (t < best_t) {
+      best_t = t;
+      best = l;
+    }
+  };
   LinearPlan l;
-  // equal tiles of at most 256 tokens, a multiple of 16
-  l.MT = (M + 255) / 256;
-  l.NT = ((M + l.MT - 1) / l.MT + 15) / 16 * 16;
-  l.MT = (M + l.NT - 1) / l.NT;
-  const int width = gated ? kDnHalf : 2 * kDnHalf;
-  l.FT = (N + width - 1) / width;
-  l.s = Sched::make(l.FT * l.MT, (K + kDnChunk - 1) / kDnChunk, sms);
+  if (N % 8 == 0 && M > 64) {
+    const int width = gated ? kDnHalf : 2 * kDnHalf, MT = (M + 255) / 256;
+    const long long T = (long long)MT * ((N + width - 1) / width);
+    if (T < (1 << 30)) {
+      l.pair = 1;
+      l.S = 1;
+      l.T = (int)T;
+      l.MT = MT;
+      const double waves = (double)((T + sms / 2 - 1) / (sms / 2)), t = waves * KC * 700;
+      keep(l, 9500 + 4000 + (t > w_bytes / hbm ? t : w_bytes / hbm));
+    }
+  }
+  auto consider = [&](int NT, int rows, int both, int S) {
+    l.pair = 0;
+    l.MT = (M + NT - 1) / NT;
+    l.NT = ((M + l.MT - 1) / l.MT + 15) / 16 * 16;
+    l.rows = rows;
+    l.both = both;
+    l.S = S;
+    const int width = gated || !both ? rows : 2 * rows, fit = clusters(S, sms);
+    const long long T = (long long)((N + width - 1) / width) * l.MT;
+    if (T > (1 << 30) || (S > 1 && (T > fit || S > KC))) return;
+    l.T = (int)T;
+    const int stage = (both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128, stages = linear_stages(l, smem);
+    // a cluster's partial sums lie in the stages
+    if (stages < 2 || (S > 1 && mats * ((l.NT + 3) / 4) * 512 * 8 > stages * stage)) return;
+    const double waves = (double)((T + fit - 1) / fit), active = (double)(T < fit ? T : fit) * S;
+    const double load = ((both ? 2 : 1) * rows + l.NT) * 128.0;
+    const double mma = (both ? 2 : 1) * 4 * (l.NT / 2 > 20 ? l.NT / 2 : 20);
+    const double l2 = load / 52, mem = (load - l.NT * 128.0) * active / hbm / (T < fit ? l.MT : l.MT < waves ? 1 : l.MT / waves);
+    double chunk = l2 > mem ? l2 + 0.15 * mem : mem + 0.15 * l2;
+    if (chunk < mma) chunk = mma;
+    const double epi = 600 + 12.0 * l.NT * mats;
+    double t = waves * ((KC + S - 1) / S) * chunk;
+    if (t < w_bytes / hbm) t = w_bytes / hbm;
+    t += S > 1 ? 3000 + 50.0 * l.NT : l.NT <= 128 ? epi : epi * waves;
+    keep(l, 9500 + t);
+  };
+  const int top = M < 256 ? (M + 15) / 16 * 16 : 256;
+  for (int both = gated ? 1 : 0; both < 2; ++both)
+    for (int rows = both && !gated ? kDnHalf : kn ? 64 : 32; rows <= kDnHalf; rows += kn ? 64 : 32)
+      for (int NT = 16; NT <= top; NT += 16)
+        for (int S = 1; S <= 8; S *= 2) consider(NT, rows, both, S);
+  best.M = M;
+  best.N = N;
+  best.K = K;
+  best.gated = gated;
+  best.kn = kn;
+  best.wide = wide;
+  best.sms = sms;
+  return best;
+}
+
+// The plan goes by the sizes alone.  A thread keeps the plans of the sizes that it used last: a
+// model's calls come again with every token.
+const LinearPlan& linear_plan(int M, int N, int K, bool gated, bool kn, bool wide, int sms, int smem) {
+  constexpr int kKept = 64;
+  static thread_local LinearPlan kept[kKept];
+  const uint32_t at = ((uint32_t)M * 2654435761u ^ (uint32_t)N * 2246822519u ^ (uint32_t)K * 3266489917u ^
+                       (uint32_t)(gated * 4 + kn * 2 + wide) * 668265263u) >> 26;
+  LinearPlan& l = kept[at % kKept];
+  if (l.M != M || l.N != N || l.K != K || l.gated != gated || l.kn != kn || l.wide != wide || l.sms != sms)
+    l = make_plan(M, N, K, gated, kn, wide, sms, smem);
   return l;
 }
 
@@ -307,18 +731,60 @@ constexpr size_t kHeadBytes = (sizeof(DenseHead) + 255) / 256 * 256;
 
 }  // namespace
 
-size_t linear_ws_bytes(int M, int N, int K, bool gated, int sms) {
-  if (M == 0) return kHeadBytes;
-  const LinearPlan l = linear_plan(M, N, K, gated, sms);
-  return kHeadBytes + (size_t)l.s.segments() * 2 * l.NT * 128 * sizeof(float);
+size_t linear_ws_bytes() { return kHeadBytes; }
+
+static cudaError_t launch_linear_pair(const LinearCall& c, const LinearPlan& l, void* ws, int sms, cudaStream_t st) {
+  const bool gated = c.w_mul != nullptr;
+  CUtensorMap mw, mw2, mx;
+  const uint64_t cols = c.kn ? c.N : c.K, rows = c.kn ? c.K : c.N;
+  const uint32_t box = c.kn ? kDnChunk : kDnHalf;
+  cudaError_t e = dense_map(&mw, c.w, c.bf16, cols, rows, c.w_stride, 0, 0, box);
+  if (e != cudaSuccess) return e;
+  mw2 = mw;
+  if (gated) e = dense_map(&mw2, c.w_mul, c.bf16, cols, rows, c.w_mul_stride, 0, 0, box);
+  if (e == cudaSuccess) e = dense_map(&mx, c.x, c.bf16, c.K, c.M, c.K, 0, 0, kDnHalf);
+  if (e != cudaSuccess) return e;
+  PairArgs p;
+  p.M = c.M;
+  p.N = c.N;
+  p.gated = gated;
+  p.bf16 = c.bf16;
+  p.kn = c.kn;
+  p.act = c.act;
+  p.out_f32 = c.out_f32;
+  p.MT = l.MT;
+  p.T = l.T;
+  p.KC = (c.K + kDnChunk - 1) / kDnChunk;
+  p.bias = c.bias;
+  p.bias_mul = c.bias_mul;
+  p.residual = c.residual;
+  p.y = c.y;
+  p.head = reinterpret_cast<DenseHead*>(ws);
+  const size_t smem = 1024 + (size_t)kPairStages * kPairStage + sizeof(DenseBars);
+  e = cudaFuncSetAttribute(linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (p.T < sms / 2 ? p.T : sms / 2));
+  cfg.blockDim = dim3(kDnThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, linear_pair_kernel, mw, mw2, mx, p);
 }
 
 cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin, cudaStream_t st) {
   const bool gated = c.w_mul != nullptr;
-  const LinearPlan l = linear_plan(c.M, c.N, c.K, gated, sms);
+  const LinearPlan& l = linear_plan(c.M, c.N, c.K, gated, c.kn, c.out_f32, sms, smem_optin);
+  if (!l.S) return cudaErrorInvalidValue;
+  if (l.pair) return launch_linear_pair(c, l, ws, sms, st);
+  const bool few = l.NT <= kFewTokens;
   CUtensorMap mw, mw2, mx;
   const uint64_t cols = c.kn ? c.N : c.K, rows = c.kn ? c.K : c.N;
-  const uint32_t box = c.kn ? kDnChunk : kDnHalf;
+  const uint32_t box = c.kn ? kDnChunk : l.rows;
   cudaError_t e = dense_map(&mw, c.w, c.bf16, cols, rows, c.w_stride, 0, 0, box);
   if (e != cudaSuccess) return e;
   mw2 = mw;
@@ -328,41 +794,57 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   LinearArgs p;
   p.M = c.M;
   p.N = c.N;
-  p.MT = l.MT;
-  p.NT = l.NT;
   p.gated = gated;
   p.bf16 = c.bf16;
   p.kn = c.kn;
   p.act = c.act;
   p.out_f32 = c.out_f32;
-  p.s = l.s;
+  p.MT = l.MT;
+  p.NT = l.NT;
+  p.T = l.T;
+  p.rows = l.rows;
+  p.both = l.both;
+  p.KC = (c.K + kDnChunk - 1) / kDnChunk;
+  p.S = l.S;
   p.bias = c.bias;
   p.bias_mul = c.bias_mul;
   p.residual = c.residual;
   p.y = c.y;
   p.head = reinterpret_cast<DenseHead*>(ws);
-  p.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + kHeadBytes);
-  const int stage = kDnBytesA + l.NT * 128;
-  int S = (smem_optin - 1024 - (int)sizeof(DenseBars)) / stage;
-  p.stages = S > kDnMaxStages ? kDnMaxStages : S;
-  p.acc_bufs = l.NT <= 128 ? 2 : 1;
+  const int stage = (l.both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128, cols_of = (l.both ? 2 : 1) * l.NT;
+  p.stages = linear_stages(l, smem_optin);
+  p.acc_bufs = cols_of <= 256 ? 2 : 1;
+  // fp32 results: several accumulators, so that each adds up fewer products (the tensor core's
+  // additions cut off; 256 of them in a row cost 3e-6 of the result, 32 cost 4e-7)
+  p.groups = 1;
+  const int most_cols = few ? 256 : 512;  // two CTAs on an SM share its 512 columns
+  while (c.out_f32 && p.groups < 8 && 2 * p.groups * cols_of * p.acc_bufs <= most_cols) p.groups *= 2;
+  p.buf_cols = p.groups * cols_of;
   p.tmem_cols = 32;
-  while (p.tmem_cols < 2 * l.NT * p.acc_bufs) p.tmem_cols *= 2;
+  while (p.tmem_cols < p.buf_cols * p.acc_bufs) p.tmem_cols *= 2;
   p.stream = l.MT == 1;
+  const int ctas = l.S > 1 ? l.T * l.S : l.T < sms ? l.T : sms;
+  p.ahead = (int)((32 << 20) / ((size_t)ctas * (l.both ? 2 : 1) * l.rows * 128));  // 32 MB of L2 in all
   const size_t smem = 1024 + (size_t)p.stages * stage + sizeof(DenseBars);
-  e = cudaFuncSetAttribute(linear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = cudaFuncSetAttribute(few ? linear_kernel<true> : linear_kernel<false>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(l.s.ctas());
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kDnThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = l.S;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_kernel, mw, mw2, mx, p);
+  cfg.numAttrs = l.S > 1 ? 2 : 1;
+  return few ? cudaLaunchKernelEx(&cfg, linear_kernel<true>, mw, mw2, mx, p)
+             : cudaLaunchKernelEx(&cfg, linear_kernel<false>, mw, mw2, mx, p);
 }
 
 }  // namespace sesg
