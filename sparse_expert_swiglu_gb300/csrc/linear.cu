@@ -625,8 +625,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
 }
 
 struct LinearPlan {
-  int M = -1, N, K, gated, kn, wide, sms;   // what it is for
-  int pair, NT, MT, rows, both, S, T;
+  int M = -1, N = 0, K = 0, gated = 0, kn = 0, wide = 0, sms = 0;  // what it is for
+  int pair = 0, NT = 0, MT = 0, rows = 0, both = 0, S = 0, T = 0;
 };
 
 constexpr int kFewTokens = 32;
@@ -644,11 +644,18 @@ int linear_stages(const LinearPlan& l, int smem) {
 }
 
 // The tile and the cluster with the least time by a model in SM clocks.  Its terms, as measured (GB300,
-// 1.9 GHz): a call costs 9500 whatever it does; an SM takes 52 bytes a clock from L2 (g = 4096 x 14336
-// gated: 47 KB stages in 1240 clocks, 64 KB stages in 1270) and all SMs 3550 out of HBM; a product of 128 x NT
-// x 16 takes NT / 2, and 2 at least 40 together; joining a cluster's sums 3000 and 50 for each token;
-// a tile's epilogue 600 and 12 for each token, which runs under the next tile's products where TMEM holds
-// both (NT <= 128).  A pair's stage is 700 (300 tokens: 78 us against the model's 76).
+// 1.9 GHz):
+//   a call costs 7000 whatever it does (256 x 512, one token: 3.8 us);
+//   an SM takes 62 bytes a clock from L2 (tiles of 128 x 128: 32 KB in 516 clocks), all SMs together
+//   3550 out of HBM, and where both are needed the lesser adds 0.15 of itself;
+//   a stage's bytes come 2400 after they are asked for (4096 x 4096, one token, 16 KB stages: six of them
+//   run at 383 clocks each, three 32 KB ones at 831), and a stage costs its issuing threads 330,
+//   60 more where its rows are shorter boxes;
+//   a product of 128 x NT x 16 takes NT / 2, and a quarter more with all SMs at it (the clock drops);
+//   joining a cluster's sums 3300 and 48 for each token and product; a tile's epilogue 600 and 12 for
+//   each token, which runs under the next tile's products where TMEM holds both tiles (NT <= 128);
+//   a CTA pair's stage 650, and 8000 for its first and last tile (2048 x 14336 gated, K = 4096: 275 us
+//   against the model's 270; one CTA a tile 321).
 LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool wide, int sms, int smem) {
   LinearPlan best;
   double best_t = 1e30;
@@ -669,8 +676,8 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool wide, int sm
       l.S = 1;
       l.T = (int)T;
       l.MT = MT;
-      const double waves = (double)((T + sms / 2 - 1) / (sms / 2)), t = waves * KC * 700;
-      keep(l, 9500 + 4000 + (t > w_bytes / hbm ? t : w_bytes / hbm));
+      const double waves = (double)((T + sms / 2 - 1) / (sms / 2)), t = waves * KC * 650;
+      keep(l, 7000 + 8000 + (t > w_bytes / hbm ? t : w_bytes / hbm));
     }
   }
   auto consider = [&](int NT, int rows, int both, int S) {
@@ -689,15 +696,18 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool wide, int sm
     if (stages < 2 || (S > 1 && mats * ((l.NT + 3) / 4) * 512 * 8 > stages * stage)) return;
     const double waves = (double)((T + fit - 1) / fit), active = (double)(T < fit ? T : fit) * S;
     const double load = ((both ? 2 : 1) * rows + l.NT) * 128.0;
-    const double mma = (both ? 2 : 1) * 4 * (l.NT / 2 > 20 ? l.NT / 2 : 20);
-    const double l2 = load / 52, mem = (load - l.NT * 128.0) * active / hbm / (T < fit ? l.MT : l.MT < waves ? 1 : l.MT / waves);
+    const double mma = (both ? 2 : 1) * 4 * 1.25 * l.NT / 2, l2 = load / 62;
+    // weights that several token tiles of a wave share come out of HBM once
+    const double mem = (load - l.NT * 128.0) * active / hbm / (T < fit ? l.MT : l.MT < waves ? 1 : l.MT / waves);
     double chunk = l2 > mem ? l2 + 0.15 * mem : mem + 0.15 * l2;
-    if (chunk < mma) chunk = mma;
+    for (const double least : {mma, 2400.0 / stages, 330.0})
+      if (chunk < least) chunk = least;
+    if (rows < kDnHalf) chunk += 60;
     const double epi = 600 + 12.0 * l.NT * mats;
     double t = waves * ((KC + S - 1) / S) * chunk;
     if (t < w_bytes / hbm) t = w_bytes / hbm;
-    t += S > 1 ? 3000 + 50.0 * l.NT : l.NT <= 128 ? epi : epi * waves;
-    keep(l, 9500 + t);
+    t += S > 1 ? 3300 + 48.0 * l.NT * (both ? 2 : 1) : l.NT <= 128 ? epi : epi * waves;
+    keep(l, 7000 + t);
   };
   const int top = M < 256 ? (M + 15) / 16 * 16 : 256;
   for (int both = gated ? 1 : 0; both < 2; ++both)
