@@ -145,6 +145,14 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[4]) {
   uint32_t r[4];
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
@@ -403,24 +411,32 @@ __device__ __forceinline__ bool dn_last_share(unsigned* cnt, int parts, DenseBar
   return b->last != 0;
 }
 
-// v[i] = the sum over a split tile's shares, in order, of from[share * stride + i * 128], for i < n.
-// 16 loads are in flight together: few tokens, many shares at a time.
+// g[i], u[i] = the sums over a split tile's shares, in order, of from[share * stride + i * 128] and of what lies
+// `second` behind it, for i < n.  32 loads are in flight together: few tokens, many shares at a time.
 template <int W>
-__device__ __forceinline__ void sum_shares(const float* from, size_t stride, int parts, int n, float (&v)[W]) {
-  constexpr int U = W >= 16 ? 2 : 16 / W;
+__device__ __forceinline__ void sum_shares(const float* from, size_t second, size_t stride, int parts, int n,
+                                           float (&g)[W], float (&u)[W]) {
+  constexpr int U = 16 / W;
 #pragma unroll
-  for (int i = 0; i < W; ++i) v[i] = 0.f;
+  for (int i = 0; i < W; ++i) g[i] = u[i] = 0.f;
 #pragma unroll 1
   for (int s = 0; s < parts; s += U) {
-    float t[U][W];
+    float tg[U][W], tu[U][W];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int j = 0; j < U; ++j)
 #pragma unroll
-      for (int i = 0; i < W; ++i) t[u][i] = s + u < parts && i < n ? __ldcg(from + (s + u) * stride + i * 128) : 0.f;
+      for (int i = 0; i < W; ++i) {
+        const bool on = s + j < parts && i < n;
+        tg[j][i] = on ? __ldcg(from + (s + j) * stride + i * 128) : 0.f;
+        tu[j][i] = on ? __ldcg(from + (s + j) * stride + second + i * 128) : 0.f;
+      }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int j = 0; j < U; ++j)
 #pragma unroll
-      for (int i = 0; i < W; ++i) v[i] += t[u][i];
+      for (int i = 0; i < W; ++i) {
+        g[i] += tg[j][i];
+        u[i] += tu[j][i];
+      }
   }
 }
 

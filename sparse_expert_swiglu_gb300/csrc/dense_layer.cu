@@ -26,6 +26,7 @@ constexpr int kMaxExperts = 256;
 constexpr int kMaxActive = kMaxExperts + 8;
 constexpr int kMaxPairSlots = 16;                // k + shared experts of a token, at most
 constexpr int kPartFloats = 2 * kDenseMaxTok * kDnHalf;
+constexpr int kJoinGroups = kDnThreads / kDnHalf;
 constexpr int kFewTok = 8;                       // up to here every CTA chooses the experts itself
 
 // Groups of 8 slots that the active experts' tokens fill, at most.
@@ -48,7 +49,7 @@ struct LayerArgs {
   float* part;         // [segment][gate, up][64][128]
   float* ypart;        // [share][8 groups][d]
   float* yrow;         // [B][d] sums before RMSNorm
-  float* ysq;          // [B][256-feature tiles] their squares
+  float* ysq;          // [B][128 features][4 warps] their squares
   int slots;           // 8 * max_groups
   int slices;          // router: CTAs per token
   int stages, stage_bytes;
@@ -57,6 +58,7 @@ struct LayerArgs {
 struct LayerMisc {
   DenseBars bars;
   unsigned long long mask[kMaxExperts];  // tokens of each routed expert
+  uint32_t on[kMaxExperts / 32];         // experts with tokens (few tokens)
   short where[kMaxExperts];              // its place among the active ones
   short act[kMaxActive];                 // active experts: shared ones (E + s) first
   short cnt[kMaxActive];                 // ... tokens
@@ -68,11 +70,10 @@ struct LayerMisc {
   float w[kDenseMaxTok * 8];
   short row[kDenseMaxTok * kMaxPairSlots];    // slot of each (token, choice)
   short place[kDenseMaxTok * kMaxPairSlots];  // active expert of each (token, choice)
-  float sum[kDnThreads / 32];
   // a token's partial sums: where they begin and their weights
-  size_t from[kMaxPairSlots * (kDnMaxSplit + 1)];
-  float weight[kMaxPairSlots * (kDnMaxSplit + 1)];
-  int n_from;
+  size_t from[kJoinGroups][kMaxPairSlots * (kDnMaxSplit + 1)];
+  float weight[kJoinGroups][kMaxPairSlots * (kDnMaxSplit + 1)];
+  int n_from[kJoinGroups];
 };
 
 // Arrive at / wait for barrier i over the grid.  All CTAs are resident (cooperative launch).
@@ -123,11 +124,31 @@ __device__ void slice_logits(const LayerArgs& p, int b, int r0, int r1, float* o
           acc[i] = fmaf(xv[u], from16((unsigned short)(w4[i / 2] >> (16 * (i & 1))), p.bf16), acc[i]);
       }
     }
+  }
+  const int lane = tid & 31;
+  if (32 % nchunk == 0) {
+    // a warp's rows by shuffles, then the warps' sums
+#pragma unroll
+    for (int i = 0; i < EV; ++i)
+      for (int off = nchunk; off < 32; off <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
+    if (lane < nchunk) {
+#pragma unroll
+      for (int i = 0; i < EV; ++i) red[(tid >> 5) * p.E + ec * EV + i] = acc[i];
+    }
+    __syncthreads();
+    if (tid < p.E) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDnThreads / 32; ++w) s += red[w * p.E + tid];
+      __stcg(out + tid, s);
+    }
+    return;
+  }
+  if (rs < nrs) {
 #pragma unroll
     for (int i = 0; i < EV; ++i) red[rs * p.E + ec * EV + i] = acc[i];
   }
   __syncthreads();
-  const int lane = tid & 31;
   for (int e = tid >> 5; e < p.E; e += kDnThreads / 32) {
     float s = 0.f;
     for (int r = lane; r < nrs; r += 32) s += red[r * p.E + e];
@@ -139,9 +160,10 @@ __device__ void slice_logits(const LayerArgs& p, int b, int r0, int r1, float* o
 
 // One warp: token b's logits (its slices [slices][E] added in order), its k experts by logit descending
 // (ties: the lower index; NaN ranks as -inf) and their weights.  A logit's key orders as the logit
-// does; an expert that is taken has key 0, below every logit's.
+// does; an expert that is taken has key 0, below every logit's.  m: where to mark the choice, or null.
 template <int PER>
-__device__ __forceinline__ void choose(const LayerArgs& p, int b, const float* slices, int* idx, float* w) {
+__device__ __forceinline__ void choose(const LayerArgs& p, int b, const float* slices, int* idx, float* w,
+                                       LayerMisc* m) {
   const int lane = threadIdx.x & 31;
   float l[PER];
   uint32_t key[PER];
@@ -198,12 +220,16 @@ __device__ __forceinline__ void choose(const LayerArgs& p, int b, const float* s
   if (lane < p.k) {
     idx[b * p.k + lane] = mine_e;
     w[b * p.k + lane] = expf(mine - top) / sum;
+    if (m) {
+      atomicOr(&m->mask[mine_e], 1ull << b);
+      atomicOr(&m->on[mine_e >> 5], 1u << (mine_e & 31));
+    }
   }
 }
 
-__device__ void choose_any(const LayerArgs& p, int b, const float* slices, int* idx, float* w) {
-  if (p.E <= 64) choose<2>(p, b, slices, idx, w);
-  else choose<kMaxExperts / 32>(p, b, slices, idx, w);
+__device__ void choose_any(const LayerArgs& p, int b, const float* slices, int* idx, float* w, LayerMisc* m) {
+  if (p.E <= 64) choose<2>(p, b, slices, idx, w, m);
+  else choose<kMaxExperts / 32>(p, b, slices, idx, w, m);
 }
 
 // Whole CTA: n values of other CTAs to shared memory, eight of a thread's in flight.
@@ -243,7 +269,7 @@ __device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
         gather_logits(p.logits + (size_t)b * p.slices * p.E, p.slices * p.E, scratch);
         __syncthreads();
         if (warp == 0) {
-          choose_any(p, b, scratch, p.top_idx, p.top_w);
+          choose_any(p, b, scratch, p.top_idx, p.top_w, nullptr);
         }
       }
       __syncthreads();
@@ -258,7 +284,7 @@ __device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
   if (few) {
     gather_logits(p.logits, p.B * p.slices * p.E, scratch);
     __syncthreads();
-    if (warp < p.B) choose_any(p, warp, scratch + warp * p.slices * p.E, m.idx, m.w);
+    if (warp < p.B) choose_any(p, warp, scratch + warp * p.slices * p.E, m.idx, m.w, &m);
   } else {
     for (int i = tid; i < p.B * p.k; i += kDnThreads) {
       m.idx[i] = __ldcg(p.top_idx + i);
@@ -279,6 +305,46 @@ __device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
 __device__ void make_lists(const LayerArgs& p, LayerMisc& m, uint8_t* tok) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int pairs = p.B * p.k, gs = (p.B + 7) / 8;
+  if (p.B <= kFewTok) {
+    // One group of 8 slots for each active expert, in the order of the experts; the routing has marked the
+    // masks.  One thread for each (token, choice).
+    if (tid < pairs + p.B * p.ns) {
+      int b, j, a, before;
+      if (tid < pairs) {
+        b = tid / p.k;
+        j = tid - b * p.k;
+        const int e = m.idx[tid];
+        a = p.ns + __popc(m.on[e >> 5] & ((1u << (e & 31)) - 1));
+        for (int i = 0; i < e >> 5; ++i) a += __popc(m.on[i]);
+        const unsigned long long mask = m.mask[e];
+        before = __popcll(mask & ((1ull << b) - 1));
+        if (before == 0) {
+          m.act[a] = (short)e;
+          m.cnt[a] = (short)__popcll(mask);
+          m.grp[a] = (short)a;
+        }
+      } else {
+        a = (tid - pairs) / p.B;
+        b = before = (tid - pairs) - a * p.B;
+        j = p.k + a;
+        if (b == 0) {
+          m.act[a] = (short)(p.E + a);
+          m.cnt[a] = (short)p.B;
+          m.grp[a] = (short)a;
+        }
+      }
+      tok[a * 8 + before] = (uint8_t)b;
+      m.row[b * kMaxPairSlots + j] = (short)(a * 8 + before);
+      m.place[b * kMaxPairSlots + j] = (short)a;
+    }
+    if (tid == kDnThreads - 1) {
+      int n = p.ns;
+      for (int i = 0; i < (p.E + 31) / 32; ++i) n += __popc(m.on[i]);
+      m.n_act = n;
+    }
+    __syncthreads();
+    return;
+  }
   for (int i = tid; i < pairs; i += kDnThreads) atomicOr(&m.mask[m.idx[i]], 1ull << (i / p.k));
   __syncthreads();
   if (tid < 32) {
@@ -382,8 +448,7 @@ __device__ __forceinline__ void share_h(uint32_t t, int n, float* to) {
 template <int W>
 __device__ __forceinline__ void joined_h(const LayerArgs& p, const float* from, int parts, int slot, int n, int feat) {
   float g[W], u[W];
-  sum_shares(from, kPartFloats, parts, n, g);
-  sum_shares(from + kDenseMaxTok * kDnHalf, kPartFloats, parts, n, u);
+  sum_shares(from, kDenseMaxTok * kDnHalf, kPartFloats, parts, n, g, u);
   store_h(p, slot, n, feat, g, u);
 }
 
@@ -402,6 +467,11 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   DenseBars* bars = &m.bars;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   const int S = p.stages;
+  const int FT = (p.f + kDnHalf - 1) / kDnHalf, DT = (p.d + 2 * kDnHalf - 1) / (2 * kDnHalf);
+  const int KC1 = (p.d + kDnChunk - 1) / kDnChunk;
+  const uint32_t ring_at = smem_addr(ring);
+  // The shared experts' tiles come first: they do not depend on the routing.
+  const Sched s0 = Sched::make(p.ns * FT, KC1, gridDim.x);
   int* status = &p.head->ctrl.status;
   volatile int* abort = &bars->abort;
 
@@ -413,29 +483,61 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   if (warp == 3 && lane < 8) tma_prefetch_map(&maps.gate + lane);
   // make_lists starts from no tokens
   for (int e = tid; e < p.E; e += kDnThreads) m.mask[e] = 0ull;
+  if (tid < kMaxExperts / 32) m.on[tid] = 0u;
   for (int i = tid; i < p.slots; i += kDnThreads) tok[i] = (uint8_t)p.B;
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
   const uint32_t tmem = bars->tmem;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  // Chunk kc of tile t of the shared or of the active routed experts, into a stage.
+  const uint64_t pw = policy_evict_first(), px = policy_evict_normal();
+  auto load_gate_up = [&](bool routed, int t, int kc, int stage) {
+    const int i = t / FT, a = p.ns + i, f0 = (t - i * FT) * kDnHalf, k = kc * kDnChunk;
+    const int z = routed ? m.act[a] : i, n4 = ((routed ? m.cnt[a] : p.B) + 3) / 4;
+    uint64_t* full = &bars->full[stage];
+    mbar_arrive_expect_tx(full, kDnBytesA + n4 * 512);
+    const uint32_t at = ring_at + stage * p.stage_bytes;
+    tma_3d(at, routed ? &maps.gate : &maps.sgate, k, f0, z, full, pw);
+    tma_3d(at + kDnBytesA / 2, routed ? &maps.up : &maps.sup, k, f0, z, full, pw);
+    if (routed) {
+      const uint8_t* q = tok + m.grp[a] * 8;
+      for (int r = 0; r < n4; ++r, q += 4) tma_rows4(at + kDnBytesA + r * 512, &maps.x, k, q[0], q[1], q[2], q[3], full, px);
+    } else {
+      for (int r = 0; r < n4; ++r)
+        tma_rows4(at + kDnBytesA + r * 512, &maps.x, k, 4 * r, 4 * r + 1, 4 * r + 2, 4 * r + 3, full, px);
+    }
+  };
+  // Their first stages are on their way while the tokens are routed, whose scratch is the last stage.
+  int sent = 0;
+  if (warp == 0 && elect_one()) {
+    SegIter it(s0, cta);
+    Seg g;
+    while (sent < S - 1 && it.next(g))
+      for (int kc = g.k0; kc < g.k1 && sent < S - 1; ++kc) load_gate_up(false, g.t, kc, sent++);
+  }
+  __syncwarp();
 
   bool ok = true;
-  if (p.E > 0) ok = route(p, m, reinterpret_cast<float*>(ring));
+  if (p.E > 0) ok = route(p, m, reinterpret_cast<float*>(ring + (size_t)(S - 1) * p.stage_bytes));
   if (!ok && tid == 0) dn_fail(bars, status);
   if (ok) make_lists(p, m, tok);
   // the ring was scratch of the router: its generic accesses come before the copies into it
   fence_proxy_async_smem();
   __syncthreads();
 
-  const int FT = (p.f + kDnHalf - 1) / kDnHalf, DT = (p.d + 2 * kDnHalf - 1) / (2 * kDnHalf);
-  const Sched s1 = Sched::make(m.n_act * FT, (p.d + kDnChunk - 1) / kDnChunk, gridDim.x);
+  const Sched s1 = Sched::make((m.n_act - p.ns) * FT, KC1, gridDim.x);
   const Sched s2 = Sched::make(m.n_act * DT, (p.f + kDnChunk - 1) / kDnChunk, gridDim.x);
 
   if (!ok) {
+    // no copy is in flight when the CTA ends
+    for (int i = 0; i < sent; ++i)
+      for (uint32_t w = 0; w < kWaitTries && !mbar_try_wait(&bars->full[i], 0); ++w) {}
   } else if (warp == 0) {
     if (elect_one()) {
-      const uint64_t pw = policy_evict_first(), px = policy_evict_normal();
-      int st = 0, issued = 0;
+      int st = 0, issued = sent;
       uint32_t ph = 0;
       auto advance = [&](int& s, uint32_t& h) {
         if (++s == S) {
@@ -444,32 +546,27 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
         }
       };
       Seg g;
-      SegIter it(s1, cta);
       bool go = true;
-      while (go && it.next(g)) {
-        const int a = g.t / FT, f0 = (g.t - a * FT) * kDnHalf;
-        const int e = m.act[a], n4 = (m.cnt[a] + 3) / 4, row = m.grp[a] * 8;
-        const bool sh = e >= p.E;
-        const int z = sh ? e - p.E : e;
-        const CUtensorMap *mg = sh ? &maps.sgate : &maps.gate, *mu = sh ? &maps.sup : &maps.up;
-        for (int kc = g.k0; kc < g.k1; ++kc) {
-          if (!dn_wait(&bars->empty[st], ph ^ 1, abort)) {
-            dn_fail(bars, status);
-            go = false;
-            break;
+      int skip = sent;  // chunks that are on their way
+#pragma unroll 1
+      for (int part = 0; part < 2 && go; ++part) {
+        SegIter it(part ? s1 : s0, cta);
+        while (go && it.next(g)) {
+          for (int kc = g.k0; kc < g.k1; ++kc) {
+            if (skip > 0) {
+              --skip;
+              advance(st, ph);
+              continue;
+            }
+            if (!dn_wait(&bars->empty[st], ph ^ 1, abort)) {
+              dn_fail(bars, status);
+              go = false;
+              break;
+            }
+            load_gate_up(part != 0, g.t, kc, st);
+            ++issued;
+            advance(st, ph);
           }
-          uint64_t* full = &bars->full[st];
-          mbar_arrive_expect_tx(full, kDnBytesA + n4 * 512);
-          ++issued;
-          const uint32_t at = smem_addr(ring + (size_t)st * p.stage_bytes);
-          const int k = kc * kDnChunk;
-          tma_3d(at, mg, k, f0, z, full, pw);
-          tma_3d(at + kDnBytesA / 2, mu, k, f0, z, full, pw);
-          for (int i = 0; i < n4; ++i) {
-            const uint8_t* t = tok + row + 4 * i;
-            tma_rows4(at + kDnBytesA + i * 512, &maps.x, k, t[0], t[1], t[2], t[3], full, px);
-          }
-          advance(st, ph);
         }
       }
       // second phase: the weights of the first stages are asked for before the grid's h is there
@@ -479,14 +576,14 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
         const CUtensorMap* md = sh ? &maps.sdown : &maps.down;
         uint64_t* full = &bars->full[stage];
         mbar_arrive_expect_tx(full, kDnBytesA + ng * 2048);
-        const uint32_t at = smem_addr(ring + (size_t)stage * p.stage_bytes);
+        const uint32_t at = ring_at + stage * p.stage_bytes;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           tma_3d(at + i * 8192, md, d0 + 64 * i, kc * kDnChunk, sh ? e - p.E : e, full, pw);
       };
       auto load_h = [&](const Seg& q, int kc, int stage) {
         const int a = q.t / DT, ng = (m.cnt[a] + 7) / 8, row = m.grp[a] * 16;
-        const uint32_t at = smem_addr(ring + (size_t)stage * p.stage_bytes) + kDnBytesA;
+        const uint32_t at = ring_at + stage * p.stage_bytes + kDnBytesA;
         for (int i = 0; i < ng; ++i)
           tma_2d(at + i * 2048, &maps.h, kc * kDnChunk, row + 16 * i, &bars->full[stage], px);
       };
@@ -549,12 +646,12 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       bool go = true, open = false;
       Seg g;
 #pragma unroll 1
-      for (int phase = 0; phase < 2 && go; ++phase) {
-        const Sched& sc = phase ? s2 : s1;
-        const int TT = phase ? DT : FT;
-        SegIter it(sc, cta);
+      for (int part = 0; part < 3 && go; ++part) {
+        const bool phase = part == 2;
+        const int TT = phase ? DT : FT, first = part == 1 ? p.ns : 0;
+        SegIter it(part == 0 ? s0 : part == 1 ? s1 : s2, cta);
         while (go && it.next(g)) {
-          const int n = m.cnt[g.t / TT];
+          const int n = m.cnt[first + g.t / TT];
           const uint32_t desc = mma_desc(phase ? (n + 7) / 8 * 16 : (n + 15) / 16 * 16, p.bf16, phase);
           if (!dn_wait(&bars->tempty[buf], tph ^ 1, abort)) {
             dn_fail(bars, status);
@@ -570,8 +667,8 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
               break;
             }
             tc_after_sync();
-            const uint32_t a = smem_addr(ring + (size_t)st * p.stage_bytes);
-            dn_stage_products(a, a + kDnBytesA, d0, d0 + 128, desc, phase != 0, kc == g.k0);
+            const uint32_t a = ring_at + st * p.stage_bytes;
+            dn_stage_products(a, a + kDnBytesA, d0, d0 + 128, desc, phase, kc == g.k0);
             mma_commit(&bars->empty[st]);
             open = true;
             if (++st == S) {
@@ -592,14 +689,20 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
     }
   } else if (warp >= 4) {
     // lanes 32 (warp % 4) ... are this warp's; of the two warps that have them, in the first phase each takes
-    // every other 16 tokens, in the second each takes 128 features
+    // every other 8 tokens, in the second each takes 128 features
     const int q = warp & 3, half = (warp - 4) >> 2, r = q * 32 + lane, etid = tid - 128;
     int buf = 0;
     uint32_t tph = 0;
     bool go = true;
     Seg g;
-    {
-      SegIter it(s1, cta);
+#pragma unroll 1
+    for (int part = 0; part < 2 && go; ++part) {
+      const Sched& sc = part ? s1 : s0;
+      const int first = part ? p.ns : 0;
+      // the two parts' shares have counts and places of their own
+      unsigned* counts = p.head->cnt + (part ? kDnMaxCtas / 2 : 0);
+      float* sums = p.part + (part ? (size_t)s0.segments() * kPartFloats : 0);
+      SegIter it(sc, cta);
       while (it.next(g)) {
         const bool good = dn_wait(&bars->tfull[buf], tph, abort);
         if (!good) dn_fail(bars, status);
@@ -608,10 +711,10 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
           break;
         }
         tc_after_sync();
-        const int a = g.t / FT, feat = (g.t - a * FT) * kDnHalf + r, n = m.cnt[a], slot = m.grp[a] * 8;
+        const int a = first + g.t / FT, feat = g.t % FT * kDnHalf + r, n = m.cnt[a], slot = m.grp[a] * 8;
         const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + buf * 256;
-        const int parts = s1.parts(g.t);
-        float* mine = p.part + ((size_t)(g.t - s1.dp) + cta) * kPartFloats + r;  // used where parts > 1
+        const int parts = sc.parts(g.t);
+        float* mine = sums + ((size_t)(g.t - sc.dp) + cta) * kPartFloats + r;  // used where parts > 1
         // up to two tokens in code of their own: a kernel this short pays for every line of code it fetches
         if (n <= 2) {
           if (half == 0) {
@@ -619,21 +722,21 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
             else share_h<2>(t0, n, mine);
           }
         } else {
-          for (int n0 = 16 * half; n0 < n; n0 += 32) {
-            if (parts == 1) whole_h<16>(p, t0 + n0, slot + n0, n - n0, feat);
-            else share_h<16>(t0 + n0, n - n0, mine + n0 * kDnHalf);
+          for (int n0 = 8 * half; n0 < n; n0 += 16) {
+            if (parts == 1) whole_h<8>(p, t0 + n0, slot + n0, n - n0, feat);
+            else share_h<8>(t0 + n0, n - n0, mine + n0 * kDnHalf);
           }
         }
         tc_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->tempty[buf]);
-        if (parts > 1 && dn_last_share(&p.head->cnt[g.t - s1.dp], parts, bars, etid) && feat < p.f) {
-          const float* from = p.part + ((size_t)(g.t - s1.dp) + s1.first(g.t)) * kPartFloats + r;
+        if (parts > 1 && dn_last_share(counts + (g.t - sc.dp), parts, bars, etid) && feat < p.f) {
+          const float* from = sums + ((size_t)(g.t - sc.dp) + sc.first(g.t)) * kPartFloats + r;
           if (n <= 2) {
             if (half == 0) joined_h<2>(p, from, parts, slot, n, feat);
           } else {
-            for (int n0 = 16 * half; n0 < n; n0 += 32)
-              joined_h<16>(p, from + n0 * kDnHalf, parts, slot + n0, n - n0, feat);
+            for (int n0 = 8 * half; n0 < n; n0 += 16)
+              joined_h<8>(p, from + n0 * kDnHalf, parts, slot + n0, n - n0, feat);
           }
         }
         buf ^= 1;
@@ -680,8 +783,12 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   tc_after_sync();
   if (warp == 2) tmem_free(tmem, 512);
 
-  // join: every token's experts and their shares, in order.  One warp lists where a token's sums lie.
-  auto list_sums = [&](int b, int dt) {
+  // join: every token's experts and their shares, in order.  A unit is 128 features of a token; each four
+  // warps take one at a time, the first of them lists where the token's sums lie.
+  const int grp = tid / kDnHalf, gtid = tid - grp * kDnHalf, HT = (p.d + kDnHalf - 1) / kDnHalf;
+  const int u0 = cta * kJoinGroups + grp, ustep = gridDim.x * kJoinGroups;
+  auto list_sums = [&](int u) {
+    const int b = u / HT, dt = (u - b * HT) / 2;
     int a = 0, slot = 0, parts = 0;
     if (lane < p.k + p.ns) {
       a = m.place[b * kMaxPairSlots + lane];
@@ -695,12 +802,13 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       if (lane >= off) end += o;
     }
     for (int s = 0; s < parts; ++s) {
-      m.from[end - parts + s] = ((size_t)s * p.slots + slot) * p.d;
-      m.weight[end - parts + s] = lane < p.k ? m.w[b * p.k + lane] : 1.f;
+      m.from[grp][end - parts + s] = ((size_t)s * p.slots + slot) * p.d;
+      m.weight[grp][end - parts + s] = lane < p.k ? m.w[b * p.k + lane] : 1.f;
     }
-    if (lane == 15) m.n_from = end;
+    if (lane == 15) m.n_from[grp] = end;
+    __syncwarp();
   };
-  if (ok && warp == 1 && cta < p.B * DT) list_sums(cta / DT, cta % DT);
+  if (ok && gtid < 32 && u0 < p.B * HT) list_sums(u0);
   if (tid == 0) {
     if (!*abort) {
       grid_arrive(&p.head->bar[2]);
@@ -710,24 +818,25 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   }
   __syncthreads();
   if (m.fail) return;
-  for (int u = cta; u < p.B * DT; u += gridDim.x) {
-    const int b = u / DT, dt = u - b * DT, feat = dt * 2 * kDnHalf + tid;
-    if (u != cta) {
-      __syncthreads();
-      if (warp == 1) list_sums(b, dt);
-      __syncthreads();
+  for (int u = u0; u < p.B * HT; u += ustep) {
+    const int b = u / HT, feat = (u - b * HT) * kDnHalf + gtid;
+    if (u != u0) {
+      named_barrier(2 + grp, kDnHalf);
+      if (gtid < 32) list_sums(u);
+      named_barrier(2 + grp, kDnHalf);
     }
     float acc = 0.f;
-    if (tid < 2 * kDnHalf && feat < p.d) {
-      const int n = m.n_from;
+    if (feat < p.d) {
+      const int n = m.n_from[grp];
       const float r = p.residual ? ld16(p.residual, (size_t)b * p.d + feat, p.bf16) : 0.f;
-      for (int i = 0; i < n; i += 8) {
-        float t[8];
+#pragma unroll 1
+      for (int i = 0; i < n; i += 16) {
+        float t[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t[j] = i + j < n ? __ldcg(p.ypart + m.from[i + j] + feat) : 0.f;
+        for (int j = 0; j < 16; ++j) t[j] = i + j < n ? __ldcg(p.ypart + m.from[grp][i + j] + feat) : 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (i + j < n) acc = fmaf(m.weight[i + j], t[j], acc);
+        for (int j = 0; j < 16; ++j)
+          if (i + j < n) acc = fmaf(m.weight[grp][i + j], t[j], acc);
       }
       acc += r;
       if (p.rmsnorm) p.yrow[(size_t)b * p.d + feat] = acc;
@@ -737,17 +846,12 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       float sq = acc * acc;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, off);
-      if (lane == 0) m.sum[warp] = sq;
-      __syncthreads();
-      if (tid == 0) {
-        float t = 0.f;
-        for (int i = 0; i < 2 * kDnHalf / 32; ++i) t += m.sum[i];
-        __stcg(p.ysq + u, t);
-      }
+      if (lane == 0) __stcg(p.ysq + (size_t)u * 4 + (gtid >> 5), sq);
     }
   }
   if (p.rmsnorm) {
-    // every tile's squares, then the same thread's values again
+    // every token's squares, in order, then the same thread's values again
+    __syncthreads();
     if (tid == 0) {
       grid_arrive(&p.head->bar[3]);
       if (!grid_wait(&p.head->bar[3], abort)) dn_fail(bars, status);
@@ -755,20 +859,16 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
     }
     __syncthreads();
     if (m.fail) return;
-    for (int u = cta; u < p.B * DT; u += gridDim.x) {
-      const int b = u / DT, dt = u - b * DT, feat = dt * 2 * kDnHalf + tid;
-      __syncthreads();
-      if (warp == 0) {
-        float t = 0.f;
-        for (int i = lane; i < DT; i += 32) t += __ldcg(p.ysq + b * DT + i);
+    for (int u = u0; u < p.B * HT; u += ustep) {
+      const int b = u / HT, feat = (u - b * HT) * kDnHalf + gtid;
+      float t = 0.f;  // every warp alike
+      for (int i = lane; i < 4 * HT; i += 32) t += __ldcg(p.ysq + (size_t)b * 4 * HT + i);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-        if (lane == 0) m.sum[0] = rsqrtf(t / (float)p.d + 1e-6f);
-      }
-      __syncthreads();
-      if (tid < 2 * kDnHalf && feat < p.d) {
+      for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+      const float scale = rsqrtf(t / (float)p.d + 1e-6f);
+      if (feat < p.d) {
         const size_t at = (size_t)b * p.d + feat;
-        reinterpret_cast<unsigned short*>(p.y)[at] = to16(p.yrow[at] * m.sum[0], p.bf16);
+        reinterpret_cast<unsigned short*>(p.y)[at] = to16(p.yrow[at] * scale, p.bf16);
       }
     }
   }
@@ -803,22 +903,23 @@ const LayerPlan& layer_plan(int B, int d, int f, int E, int k, int ns, int sms) 
   l.grid = sms;
   l.groups = max_groups(B, E, k, ns);
   l.slices = B > 0 ? sms / B : 1;
-  const int most = (d + 63) / 64;  // 64 rows of the router weight at least
-  if (l.slices > 32) l.slices = 32;
-  // the logits of a few tokens' slices are gathered in shared memory
-  if (B <= kFewTok && E > 0 && l.slices > 16384 / (B * E)) l.slices = 16384 / (B * E);
-  if (l.slices > most) l.slices = most;
+  const int rows = (d + 63) / 64;  // 64 rows of the router weight at least
+  if (l.slices > 16) l.slices = 16;
+  // the logits of a few tokens' slices are gathered in one stage
+  if (B <= kFewTok && E > 0 && l.slices > 8192 / (B * E)) l.slices = 8192 / (B * E);
+  if (l.slices > rows) l.slices = rows;
   if (l.slices < 1) l.slices = 1;
   const int FT = (f + kDnHalf - 1) / kDnHalf, DT = (d + 2 * kDnHalf - 1) / (2 * kDnHalf);
   const int KC1 = (d + kDnChunk - 1) / kDnChunk, KC2 = (f + kDnChunk - 1) / kDnChunk;
   // the number of active experts is known on the device only: the largest need of any
   int segs = 0, parts = 1;
-  const int most_act = (E < B * k ? E : B * k) + ns;
-  for (int a = 1; a <= most_act; ++a) {
-    const Sched s1 = Sched::make(a * FT, KC1, sms), s2 = Sched::make(a * DT, KC2, sms);
+  const int most = E < B * k ? E : B * k;
+  for (int a = 0; a <= most; ++a) {
+    const Sched s1 = Sched::make(a * FT, KC1, sms), s2 = Sched::make((a + ns) * DT, KC2, sms);
     if (s1.segments() > segs) segs = s1.segments();
     if (s2.max_parts() > parts) parts = s2.max_parts();
   }
+  segs += Sched::make(ns * FT, KC1, sms).segments();
   size_t o = (sizeof(DenseHead) + 255) / 256 * 256;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -831,7 +932,7 @@ const LayerPlan& layer_plan(int B, int d, int f, int E, int k, int ns, int sms) 
   l.h = take((size_t)l.groups * 16 * f * 2);
   l.part = take((size_t)segs * kPartFloats * 4);
   l.yrow = take((size_t)B * d * 4);
-  l.ysq = take((size_t)B * DT * 4);
+  l.ysq = take((size_t)B * 2 * DT * 16);
   l.ypart = take((size_t)parts * l.groups * 8 * d * 4);
   l.total = o;
   return l;
@@ -909,11 +1010,13 @@ cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int s
   cfg.blockDim = dim3(kDnThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, dense_layer_kernel, maps, p);
 }
 
