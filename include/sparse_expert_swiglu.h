@@ -348,9 +348,8 @@ typedef struct {
  * moe_expert_dense_swiglu -- one expert on n tokens (0..1048576):
  *   y[b] = (SiLU(x_b W^gate) (.) x_b W^up) W^down [+ residual[b]]
  *   x, y [n][d] of experts->dtype; residual [n][d] or NULL; y may be the residual's buffer.
- *   Up to 64 tokens run in one kernel and keep h = SiLU(.) (.) . to 16 bits and more beyond the
- *   type's own; more tokens run as two products, with h rounded to the type.  In fp16 |h| > 65504
- *   is infinite.
+ *   Two products (moe_linear's kernels).  Up to 64 tokens keep h = SiLU(.) (.) . as two 16-bit values,
+ *   the rounded one and the rest; with more, h is rounded to the type.  In fp16 |h| > 65504 is infinite.
  *   ws / ws_bytes: at least moe_expert_dense_workspace_bytes(n, d, f) bytes.
  */
 size_t moe_expert_dense_workspace_bytes(int32_t n, int32_t d, int32_t f);

@@ -81,8 +81,9 @@ moe_status_t check_dense_layer(const moe_dense_layer_t* layer, int B) {
   return MOE_OK;
 }
 
-// n > kDenseMaxTok tokens of one expert: h [n][f], then the two products' workspace
-size_t expert_products_ws(int n, int f) { return align_up(linear_ws_bytes(), kWsAlign) + (size_t)n * f * 2; }
+// Up to kDenseMaxTok tokens keep h as two 16-bit rows each, more round it.
+inline int h_rows(int n) { return n <= kDenseMaxTok ? 2 * n : n; }
+size_t expert_ws(int n, int f) { return align_up(linear_ws_bytes(), kWsAlign) + (size_t)h_rows(n) * f * 2; }
 
 }  // namespace
 
@@ -132,10 +133,7 @@ moe_status_t moe_linear(const moe_linear_t* op, void* ws, size_t ws_bytes, void*
 
 size_t moe_expert_dense_workspace_bytes(int32_t n, int32_t d, int32_t f) {
   if (n < 0 || n > kMaxTokens || check_dense_sizes(d, f) != MOE_OK) return 0;
-  if (n > kDenseMaxTok) return expert_products_ws(n, f);
-  int sms = 0, smem = 0;
-  if (device_sizes(sms, smem) != cudaSuccess) return 0;
-  return dense_layer_ws_bytes(n, d, f, 0, 0, 1, sms);
+  return expert_ws(n, f);
 }
 
 moe_status_t moe_expert_dense_swiglu(const uint16_t* x, int32_t n, const moe_dense_experts_t* experts,
@@ -158,30 +156,19 @@ moe_status_t moe_expert_dense_swiglu(const uint16_t* x, int32_t n, const moe_den
   const int bf16 = experts->dtype == MOE_BF16;
   const DenseExpertSet one = to_set(*experts, expert);
   cudaStream_t st = (cudaStream_t)stream;
-  if (n <= kDenseMaxTok) {
-    // the layer's kernel with this expert as its only, always-on one
-    if (ws_bytes < dense_layer_ws_bytes(n, d, f, 0, 0, 1, sms)) return MOE_ERR_WORKSPACE_TOO_SMALL;
-    DenseLayerCall c = {};
-    c.B = n;
-    c.d = d;
-    c.f = f;
-    c.bf16 = bf16;
-    c.shared = one;
-    c.x = x;
-    c.residual = residual;
-    c.y = y;
-    return cuda_status(launch_dense_layer(c, ws, sms, smem, st));
-  }
-  const size_t need = expert_products_ws(n, f);
-  if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  // h in the operand's type, as the second product reads it
-  void* h = reinterpret_cast<uint8_t*>(ws) + (need - (size_t)n * f * 2);
+  if (ws_bytes < expert_ws(n, f)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  // Two products.  Up to 64 tokens are bound by the weights' bytes, and a second row for each token costs
+  // nothing: h goes to the second product as hi + lo, to 2^-16 (bf16) or 2^-22 (fp16).  For more tokens
+  // it would cost the tensor cores twice the work, and h is rounded to the type.
+  const bool two = n <= kDenseMaxTok;
+  void* h = reinterpret_cast<uint8_t*>(ws) + align_up(linear_ws_bytes(), kWsAlign);
   LinearCall c = {};
   c.M = n;
   c.N = f;
   c.K = d;
   c.bf16 = bf16;
   c.act = MOE_ACT_SILU;
+  c.split = two;
   c.x = x;
   c.w = one.gate_t;
   c.w_mul = one.up_t;
@@ -191,7 +178,8 @@ moe_status_t moe_expert_dense_swiglu(const uint16_t* x, int32_t n, const moe_den
   cudaError_t e = launch_linear(c, ws, sms, smem, st);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   LinearCall c2 = {};
-  c2.M = n;
+  c2.M = h_rows(n);
+  c2.pairs = two;
   c2.N = d;
   c2.K = f;
   c2.bf16 = bf16;

@@ -517,11 +517,17 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
     Seg g;
     while (sent < S - 1 && it.next(g))
       for (int kc = g.k0; kc < g.k1 && sent < S - 1; ++kc) load_gate_up(false, g.t, kc, sent++);
+    // ... and the first of their down rows on the way to L2
+    const int KC2 = (p.f + kDnChunk - 1) / kDnChunk;
+    for (int i = cta, n = 0; i < p.ns * DT * KC2 && n < 4; i += gridDim.x, ++n) {
+      const int t = i / KC2, z = t / DT;
+      for (int j = 0; j < 4; ++j)
+        tma_prefetch_3d(&maps.sdown, (t - z * DT) * 2 * kDnHalf + 64 * j, (i - t * KC2) * kDnChunk, z);
+    }
   }
   __syncwarp();
 
-  bool ok = true;
-  if (p.E > 0) ok = route(p, m, reinterpret_cast<float*>(ring + (size_t)(S - 1) * p.stage_bytes));
+  const bool ok = route(p, m, reinterpret_cast<float*>(ring + (size_t)(S - 1) * p.stage_bytes));
   if (!ok && tid == 0) dn_fail(bars, status);
   if (ok) make_lists(p, m, tok);
   // the ring was scratch of the router: its generic accesses come before the copies into it
@@ -906,7 +912,7 @@ const LayerPlan& layer_plan(int B, int d, int f, int E, int k, int ns, int sms) 
   const int rows = (d + 63) / 64;  // 64 rows of the router weight at least
   if (l.slices > 16) l.slices = 16;
   // the logits of a few tokens' slices are gathered in one stage
-  if (B <= kFewTok && E > 0 && l.slices > 8192 / (B * E)) l.slices = 8192 / (B * E);
+  if (B > 0 && B <= kFewTok && l.slices > 8192 / (B * E)) l.slices = 8192 / (B * E);
   if (l.slices > rows) l.slices = rows;
   if (l.slices < 1) l.slices = 1;
   const int FT = (f + kDnHalf - 1) / kDnHalf, DT = (d + 2 * kDnHalf - 1) / (2 * kDnHalf);
@@ -955,13 +961,8 @@ cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int s
     if (e == cudaSuccess) e = dense_map(u, s.up_t, c.bf16, c.d, c.f, s.up_rs, s.E, s.up_rs * c.f, kDnHalf);
     if (e == cudaSuccess) e = dense_map(d, s.down, c.bf16, c.d, c.f, s.down_rs, s.E, s.down_rs * c.f, kDnChunk);
   };
-  if (c.routed.E > 0) set_maps(c.routed, &maps.gate, &maps.up, &maps.down);
+  set_maps(c.routed, &maps.gate, &maps.up, &maps.down);
   if (c.shared.E > 0) set_maps(c.shared, &maps.sgate, &maps.sup, &maps.sdown);
-  if (c.routed.E == 0) {
-    maps.gate = maps.sgate;
-    maps.up = maps.sup;
-    maps.down = maps.sdown;
-  }
   if (c.shared.E == 0) {
     maps.sgate = maps.gate;
     maps.sup = maps.up;

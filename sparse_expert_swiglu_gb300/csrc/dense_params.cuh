@@ -11,6 +11,8 @@ struct LinearCall {
   int kn;               // w is [K][N], else [N][K]
   int act;              // MOE_ACT_*
   int out_f32;
+  int split;            // y as two rows for each token, the rounded value and what the rounding left
+  int pairs;            // x has two such rows for each token of y: M = 2 tokens (no bias, act, w_mul)
   const void *x, *w, *w_mul, *bias, *bias_mul, *residual;
   void* y;
   size_t w_stride, w_mul_stride;  // elements between rows
@@ -27,7 +29,7 @@ struct DenseExpertSet {
 
 struct DenseLayerCall {
   int B, d, f, k, renorm, rmsnorm, bf16;
-  DenseExpertSet routed, shared;     // routed.E = 0: no routing
+  DenseExpertSet routed, shared;
   const void *x, *w_router, *residual;
   void* y;
   int32_t* user_idx;                 // optional copies of the routing

@@ -20,6 +20,8 @@ struct LinearArgs {
   int rows;         // features of one product, <= 128
   int both;         // two products (always with w_mul)
   int KC, S;        // chunks of k, CTAs of a tile
+  int split;        // y as two 16-bit rows for each token, 2 t and 2 t + 1: the rounded value and the rest
+  int pairs;        // x has two such rows for each token of y
   int groups;       // accumulators of a product: chunk c of a tile goes to c % groups
   const void *bias, *bias_mul, *residual;
   void* y;
@@ -96,9 +98,31 @@ __device__ __forceinline__ void linear_store(const LinearArgs& p, int feat, int 
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] *= m[i] + bias_mul;
   }
+  if (p.split) {
+    unsigned short* y = reinterpret_cast<unsigned short*>(p.y) + (size_t)t0 * 2 * p.N + feat;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const unsigned short hi = to16(v[i], p.bf16);
+      const float h = from16(hi, p.bf16);
+      if (i < n) {
+        y[(size_t)2 * i * p.N] = hi;
+        y[(size_t)(2 * i + 1) * p.N] = isfinite(h) ? to16(v[i] - h, p.bf16) : (unsigned short)0;
+      }
+    }
+    return;
+  }
   const size_t at = (size_t)t0 * p.N + feat;
   if (n >= W) linear_write<W, true>(p, at, n, v);
   else linear_write<W, false>(p, at, n, v);
+}
+
+// The same where x has two rows for each token: their sums are added first.  (Without bias, act and w_mul.)
+template <int W>
+__device__ __forceinline__ void linear_store_pairs(const LinearArgs& p, int feat, int t0, int n, const float (&v)[W]) {
+  float s[W / 2];
+#pragma unroll
+  for (int i = 0; i < W / 2; ++i) s[i] = v[2 * i] + v[2 * i + 1];
+  linear_write<W / 2, false>(p, (size_t)(t0 / 2) * p.N + feat, n / 2, s);
 }
 
 // W columns of a product, its accumulators added.
@@ -296,7 +320,8 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
             float v[W], m[W];
             linear_sums(d0 + i, groups, grp_cols, v);
             if (p.gated) linear_sums(d0 + NT + i, groups, grp_cols, m);
-            if (on) linear_store(p, feat, m0 + i, nt - i, ba, bb, v, m);
+            if (on && p.pairs) linear_store_pairs(p, feat, m0 + i, nt - i, v);
+            else if (on) linear_store(p, feat, m0 + i, nt - i, ba, bb, v, m);
             __syncwarp();
           }
         }
@@ -380,7 +405,8 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
               }
             }
             const int n0 = by_tok ? 16 * uh + 32 * (i >> 2) + 4 * (i & 3) : 4 * i;
-            if (on) linear_store(p, feat, m0 + n0, nt - n0, ba, bb, v, m);
+            if (on && p.pairs) linear_store_pairs(p, feat, m0 + n0, nt - n0, v);
+            else if (on) linear_store(p, feat, m0 + n0, nt - n0, ba, bb, v, m);
           }
         }
       }
@@ -625,7 +651,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
 }
 
 struct LinearPlan {
-  int M = -1, N = 0, K = 0, gated = 0, kn = 0, wide = 0, sms = 0;  // what it is for
+  int M = -1, N = 0, K = 0, gated = 0, kn = 0, plain = 0, sms = 0;  // what it is for
   int pair = 0, NT = 0, MT = 0, rows = 0, both = 0, S = 0, T = 0;
 };
 
@@ -656,7 +682,7 @@ int linear_stages(const LinearPlan& l, int smem) {
 //   each token, which runs under the next tile's products where TMEM holds both tiles (NT <= 128);
 //   a CTA pair's stage 650, and 8000 for its first and last tile (2048 x 14336 gated, K = 4096: 275 us
 //   against the model's 270; one CTA a tile 321).
-LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool wide, int sms, int smem) {
+LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int sms, int smem) {
   LinearPlan best;
   double best_t = 1e30;
   const int KC = (K + kDnChunk - 1) / kDnChunk, mats = gated ? 2 : 1;
@@ -668,7 +694,7 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool wide, int sm
     }
   };
   LinearPlan l;
-  if (N % 8 == 0 && M > 64) {
+  if (plain && N % 8 == 0 && M > 64) {
     const int width = gated ? kDnHalf : 2 * kDnHalf, MT = (M + 255) / 256;
     const long long T = (long long)MT * ((N + width - 1) / width);
     if (T < (1 << 30)) {
@@ -719,21 +745,21 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool wide, int sm
   best.K = K;
   best.gated = gated;
   best.kn = kn;
-  best.wide = wide;
+  best.plain = plain;
   best.sms = sms;
   return best;
 }
 
 // The plan goes by the sizes alone.  A thread keeps the plans of the sizes that it used last: a
 // model's calls come again with every token.
-const LinearPlan& linear_plan(int M, int N, int K, bool gated, bool kn, bool wide, int sms, int smem) {
+const LinearPlan& linear_plan(int M, int N, int K, bool gated, bool kn, bool plain, int sms, int smem) {
   constexpr int kKept = 64;
   static thread_local LinearPlan kept[kKept];
   const uint32_t at = ((uint32_t)M * 2654435761u ^ (uint32_t)N * 2246822519u ^ (uint32_t)K * 3266489917u ^
-                       (uint32_t)(gated * 4 + kn * 2 + wide) * 668265263u) >> 26;
+                       (uint32_t)(gated * 4 + kn * 2 + plain) * 668265263u) >> 26;
   LinearPlan& l = kept[at % kKept];
-  if (l.M != M || l.N != N || l.K != K || l.gated != gated || l.kn != kn || l.wide != wide || l.sms != sms)
-    l = make_plan(M, N, K, gated, kn, wide, sms, smem);
+  if (l.M != M || l.N != N || l.K != K || l.gated != gated || l.kn != kn || l.plain != plain || l.sms != sms)
+    l = make_plan(M, N, K, gated, kn, plain, sms, smem);
   return l;
 }
 
@@ -788,7 +814,7 @@ static cudaError_t launch_linear_pair(const LinearCall& c, const LinearPlan& l, 
 
 cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin, cudaStream_t st) {
   const bool gated = c.w_mul != nullptr;
-  const LinearPlan& l = linear_plan(c.M, c.N, c.K, gated, c.kn, c.out_f32, sms, smem_optin);
+  const LinearPlan& l = linear_plan(c.M, c.N, c.K, gated, c.kn, !c.split && !c.pairs, sms, smem_optin);
   if (!l.S) return cudaErrorInvalidValue;
   if (l.pair) return launch_linear_pair(c, l, ws, sms, st);
   const bool few = l.NT <= kFewTokens;
@@ -816,6 +842,8 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   p.both = l.both;
   p.KC = (c.K + kDnChunk - 1) / kDnChunk;
   p.S = l.S;
+  p.split = c.split;
+  p.pairs = c.pairs;
   p.bias = c.bias;
   p.bias_mul = c.bias_mul;
   p.residual = c.residual;
