@@ -617,8 +617,10 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     else:
         y = out
         yp = _dense_in(out, out_dtype, device, (M, N), "out")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     op = _Linear(M, N, K, dtype_code, out_code, layout_code, act_code,
-                 _dense_in(x, dt, device, (M, K), "x"), _dense_in(w, dt, device, wshape, "w"),
+                 x.data_ptr(), _dense_in(w, dt, device, wshape, "w"),
                  None if w_mul is None else _dense_in(w_mul, dt, device, wshape, "w_mul"),
                  None if bias is None else _dense_in(bias, dt, device, (N,), "bias"),
                  None if bias_mul is None else _dense_in(bias_mul, dt, device, (N,), "bias_mul"),
@@ -710,7 +712,8 @@ def expert_dense_swiglu(x: torch.Tensor, experts: DenseExperts, expert: int, res
     if experts.gate_t.dtype != dt or experts.gate_t.get_device() != device:
         raise ValueError("x and the experts must have one type and device")
     shape = (n, ex.d)
-    xp = _dense_in(x, dt, device, shape, "x")
+    if x.shape[1] != ex.d or not x.is_contiguous():
+        raise ValueError(f"x must be contiguous with shape {shape}, got {tuple(x.shape)}")
     rp = None if residual is None else _dense_in(residual, dt, device, shape, "residual")
     if out is None:
         y = torch.empty_like(x)
@@ -720,7 +723,7 @@ def expert_dense_swiglu(x: torch.Tensor, experts: DenseExperts, expert: int, res
     if n == 0:
         return y
     ws = _dense_ws(ws, device, expert_dense_workspace_bytes, n, ex.d, ex.f)
-    status = (_LIB or lib()).moe_expert_dense_swiglu(xp, n, ctypes.byref(ex), expert, rp, y.data_ptr(),
+    status = (_LIB or lib()).moe_expert_dense_swiglu(x.data_ptr(), n, ctypes.byref(ex), expert, rp, y.data_ptr(),
                                                      ws.buf.data_ptr(), ws.nbytes, _stream_of(device))
     if status:
         raise MoeError("moe_expert_dense_swiglu", status)
@@ -742,8 +745,10 @@ def layer_dense_decode(x: torch.Tensor, layer: DenseLayer, residual: Optional[to
     c = layer.c_struct()
     if layer.routed.gate_t.dtype != dt or layer.routed.gate_t.get_device() != device:
         raise ValueError("x and the experts must have one type and device")
-    shape = (B, c.routed.d)
-    xp = _dense_in(x, dt, device, shape, "x")
+    d = layer.routed.gate_t.shape[2]
+    shape = (B, d)
+    if x.shape[1] != d or not x.is_contiguous():
+        raise ValueError(f"x must be contiguous with shape {shape}, got {tuple(x.shape)}")
     rp = None if residual is None else _dense_in(residual, dt, device, shape, "residual")
     if out is None:
         y = torch.empty_like(x)
@@ -757,7 +762,7 @@ def layer_dense_decode(x: torch.Tensor, layer: DenseLayer, residual: Optional[to
         dbg = ctypes.byref(_Debug(_ptr(dt_["topk_idx"]), _ptr(dt_["topk_w"]), None, None, None))
     if B:
         ws = _dense_ws(ws, device, layer_dense_workspace_bytes, layer, B)
-        status = (_LIB or lib()).moe_layer_dense_decode(xp, B, ctypes.byref(c), rp, y.data_ptr(), 1 if rmsnorm else 0,
+        status = (_LIB or lib()).moe_layer_dense_decode(x.data_ptr(), B, ctypes.byref(c), rp, y.data_ptr(), 1 if rmsnorm else 0,
                                                         dbg, ws.buf.data_ptr(), ws.nbytes, _stream_of(device))
         if status:
             raise MoeError("moe_layer_dense_decode", status)

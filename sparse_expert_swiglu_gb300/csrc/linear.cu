@@ -27,6 +27,7 @@ struct LinearArgs {
   void* y;
   DenseHead* head;
   int stages, acc_bufs, buf_cols, tmem_cols, stream;
+  int own_x;        // the cluster's partial sums have memory of their own, behind the stages
   int ahead;        // chunks of a CTA's first tile that are asked for before the previous kernel has ended
 };
 
@@ -151,7 +152,11 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   const int bytes_a = p.both ? kDnBytesA : kDnBytesA / 2;  // of a stage; rows behind p.rows stay unwritten
   const uint32_t stage_bytes = bytes_a + p.NT * 128;
   const uint32_t load_bytes = (p.both ? 2 : 1) * p.rows * 128 + p.NT * 128;
-  DenseBars* bars = reinterpret_cast<DenseBars*>(ring + (size_t)p.stages * stage_bytes);
+  // partial sums that a cluster's CTAs push here: behind the stages, or in them once they are free
+  const int most = p.M < p.NT ? p.M : p.NT, g4 = (most + 3) / 4, mats = p.gated ? 2 : 1;
+  uint8_t* xsums = p.own_x ? ring + (size_t)p.stages * stage_bytes : ring;
+  DenseBars* bars = reinterpret_cast<DenseBars*>(ring + (size_t)p.stages * stage_bytes +
+                                                 (p.own_x ? (size_t)mats * g4 * 4096 : 0));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int S = p.S, ns = p.stages, NT = p.NT;
   const int rank = S > 1 ? (int)cluster_rank() : 0;
@@ -334,8 +339,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         }
       } else {
         // The warp pair's unit 2 q + half of sums belongs to CTA unit * S / 8: 4 tokens of a feature are 16
-        // bytes at [unit of the owner][rank][matrix][4 tokens][lane] in its first stages.
-        const int mats = p.gated ? 2 : 1, g4 = (NT + 3) / 4;  // room for all tokens' groups of 4 in a unit
+        // bytes at [unit of the owner][rank][matrix][4 tokens][lane], with room for all tokens in a unit.
         const uint32_t unit_bytes = mats * g4 * 512;
         const int per = 8 / S, unit = 2 * q + half;
         auto groups4 = [&](int h) {  // groups of 4 tokens that exist in a unit of half h
@@ -349,16 +353,17 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           uint32_t bytes = 0;
           for (int i = 0; i < per; ++i) bytes += S * mats * groups4((rank * per + i) & 1) * 512;
           mbar_arrive_expect_tx(&bars->xfull, bytes);
-          for (int i = 0; i < S; ++i) peer_arrive(peer_addr(smem_addr(&bars->xready), i));
+          if (!p.own_x)
+            for (int i = 0; i < S; ++i) peer_arrive(peer_addr(smem_addr(&bars->xready), i));
         }
-        ok = ok && cluster_wait(&bars->xready, 0, abort);
+        if (!p.own_x) ok = ok && cluster_wait(&bars->xready, 0, abort);
         if (!ok) dn_fail(bars, status);
         if (dn_any(1, kDnEpi, !ok)) break;
         tc_after_sync();
         {
           const int owner = unit / per;
           const uint32_t d0 = tmem + ((uint32_t)(q * 32) << 16) + (by_tok ? 0 : half * NT);
-          uint32_t to = peer_addr(smem_addr(ring), owner) + ((unit - owner * per) * S + rank) * unit_bytes + lane * 16;
+          uint32_t to = peer_addr(smem_addr(xsums), owner) + ((unit - owner * per) * S + rank) * unit_bytes + lane * 16;
           const uint32_t bar = peer_addr(smem_addr(&bars->xfull), owner);
           for (int n0 = tok0; n0 < nt; n0 += tok_step) {
 #pragma unroll 1
@@ -386,7 +391,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           const float ba = p.bias && on ? ld16(p.bias, feat, p.bf16) : 0.f;
           const float bb = p.bias_mul && on ? ld16(p.bias_mul, feat, p.bf16) : 0.f;
           const int n4 = groups4(uh);
-          const uint8_t* from = ring + (size_t)ul * S * unit_bytes + lane * 16;
+          const uint8_t* from = xsums + (size_t)ul * S * unit_bytes + lane * 16;
           for (int i = w % S; i < n4; i += S) {
             float v[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
@@ -661,10 +666,17 @@ constexpr int kFewTokens = 32;
 // cluster lie in one part of the chip).
 int clusters(int S, int sms) { return S == 1 ? sms : S == 2 ? sms / 2 : S == 4 ? sms / 4 - 2 : sms / 8 - 4; }
 
-int linear_stages(const LinearPlan& l, int smem) {
-  const int stage = (l.both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128;
-  // few tokens: two CTAs on an SM
-  const int room = (l.NT <= kFewTokens ? smem / 2 - 2048 : smem) - 1024 - (int)sizeof(DenseBars);
+// Bytes of a cluster's partial sums in one CTA.
+int linear_sum_bytes(const LinearPlan& l, int M, bool gated) {
+  return (gated ? 2 : 1) * (((M < l.NT ? M : l.NT) + 3) / 4) * 4096;
+}
+
+// Stages of a CTA, and whether the partial sums have memory behind them (up to 16 KB).
+int linear_stages(const LinearPlan& l, int M, bool gated, int smem, bool& own_x) {
+  const int stage = (l.both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128, sums = linear_sum_bytes(l, M, gated);
+  own_x = l.S > 1 && sums <= 16384;
+  // few tokens: two CTAs on an SM (each with 1 KB that the system takes)
+  const int room = (l.NT <= kFewTokens ? smem / 2 - 512 : smem) - 1024 - (int)sizeof(DenseBars) - (own_x ? sums : 0);
   const int n = room / stage;
   return n > kDnMaxStages ? kDnMaxStages : n;
 }
@@ -717,9 +729,9 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
     const long long T = (long long)((N + width - 1) / width) * l.MT;
     if (T > (1 << 30) || (S > 1 && (T > fit || S > KC))) return;
     l.T = (int)T;
-    const int stage = (both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128, stages = linear_stages(l, smem);
-    // a cluster's partial sums lie in the stages
-    if (stages < 2 || (S > 1 && mats * ((l.NT + 3) / 4) * 512 * 8 > stages * stage)) return;
+    bool own_x;
+    const int stage = (both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128, stages = linear_stages(l, M, gated, smem, own_x);
+    if (stages < 2 || (S > 1 && !own_x && linear_sum_bytes(l, M, gated) > stages * stage)) return;
     const double waves = (double)((T + fit - 1) / fit), active = (double)(T < fit ? T : fit) * S;
     const double load = ((both ? 2 : 1) * rows + l.NT) * 128.0;
     const double mma = (both ? 2 : 1) * 4 * 1.25 * l.NT / 2, l2 = load / 62;
@@ -850,7 +862,9 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   p.y = c.y;
   p.head = reinterpret_cast<DenseHead*>(ws);
   const int stage = (l.both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128, cols_of = (l.both ? 2 : 1) * l.NT;
-  p.stages = linear_stages(l, smem_optin);
+  bool own_x;
+  p.stages = linear_stages(l, c.M, gated, smem_optin, own_x);
+  p.own_x = own_x;
   p.acc_bufs = cols_of <= 256 ? 2 : 1;
   // fp32 results: several accumulators, so that each adds up fewer products (the tensor core's
   // additions cut off; 256 of them in a row cost 3e-6 of the result, 32 cost 4e-7)
@@ -863,7 +877,7 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   p.stream = l.MT == 1;
   const int ctas = l.S > 1 ? l.T * l.S : l.T < sms ? l.T : sms;
   p.ahead = (int)((32 << 20) / ((size_t)ctas * (l.both ? 2 : 1) * l.rows * 128));  // 32 MB of L2 in all
-  const size_t smem = 1024 + (size_t)p.stages * stage + sizeof(DenseBars);
+  const size_t smem = 1024 + (size_t)p.stages * stage + sizeof(DenseBars) + (own_x ? linear_sum_bytes(l, c.M, gated) : 0);
   e = cudaFuncSetAttribute(few ? linear_kernel<true> : linear_kernel<false>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
