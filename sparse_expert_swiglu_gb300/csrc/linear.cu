@@ -56,16 +56,21 @@ __device__ __forceinline__ void activate(float (&v)[W], int act) {
   }
 }
 
+// The residual of W tokens of one feature; token i at offset at + i * N.
+template <int W>
+__device__ __forceinline__ void linear_residual(const LinearArgs& p, size_t at, int n, unsigned short (&r)[W]) {
+  const unsigned short* from = reinterpret_cast<const unsigned short*>(p.residual) + at;
+#pragma unroll
+  for (int i = 0; i < W; ++i) r[i] = i < n ? from[(size_t)i * p.N] : (unsigned short)0;
+}
+
 // Residual and store of W tokens' values of one feature; token i at offset at + i * N.
 template <int W, bool FULL>
-__device__ __forceinline__ void linear_write(const LinearArgs& p, size_t at, int n, float (&v)[W]) {
+__device__ __forceinline__ void linear_write(const LinearArgs& p, size_t at, int n, float (&v)[W],
+                                             const unsigned short (&r)[W]) {
   if (p.residual) {
-    const unsigned short* r = reinterpret_cast<const unsigned short*>(p.residual) + at;
-    unsigned short t[W];
 #pragma unroll
-    for (int i = 0; i < W; ++i) t[i] = FULL || i < n ? r[(size_t)i * p.N] : (unsigned short)0;
-#pragma unroll
-    for (int i = 0; i < W; ++i) v[i] += from16(t[i], p.bf16);
+    for (int i = 0; i < W; ++i) v[i] += from16(r[i], p.bf16);
   }
   if (p.out_f32) {
     float* y = reinterpret_cast<float*>(p.y) + at;
@@ -88,10 +93,10 @@ __device__ __forceinline__ void linear_write(const LinearArgs& p, size_t at, int
   }
 }
 
-// Epilogue of W tokens of one feature: v, and with w_mul m, are the sums; n tokens from t0 exist.
+// Epilogue of W tokens of one feature: v, and with w_mul m, are the sums, r the residual; n tokens from t0 exist.
 template <int W>
 __device__ __forceinline__ void linear_store(const LinearArgs& p, int feat, int t0, int n, float bias, float bias_mul,
-                                             float (&v)[W], const float (&m)[W]) {
+                                             float (&v)[W], const float (&m)[W], const unsigned short (&r)[W]) {
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] += bias;
   activate(v, p.act);
@@ -113,8 +118,8 @@ __device__ __forceinline__ void linear_store(const LinearArgs& p, int feat, int 
     return;
   }
   const size_t at = (size_t)t0 * p.N + feat;
-  if (n >= W) linear_write<W, true>(p, at, n, v);
-  else linear_write<W, false>(p, at, n, v);
+  if (n >= W) linear_write<W, true>(p, at, n, v, r);
+  else linear_write<W, false>(p, at, n, v, r);
 }
 
 // The same where x has two rows for each token: their sums are added first.  (Without bias, act and w_mul.)
@@ -123,7 +128,10 @@ __device__ __forceinline__ void linear_store_pairs(const LinearArgs& p, int feat
   float s[W / 2];
 #pragma unroll
   for (int i = 0; i < W / 2; ++i) s[i] = v[2 * i] + v[2 * i + 1];
-  linear_write<W / 2, false>(p, (size_t)(t0 / 2) * p.N + feat, n / 2, s);
+  const size_t at = (size_t)(t0 / 2) * p.N + feat;
+  unsigned short r[W / 2];
+  if (p.residual) linear_residual(p, at, n / 2, r);
+  linear_write<W / 2, false>(p, at, n / 2, s, r);
 }
 
 // W columns of a product, its accumulators added.
@@ -302,7 +310,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     const int q = warp & 3, half = (warp - 4) >> 2, etid = tid - 128;
     const bool by_tok = p.gated || !p.both;
     const int tok0 = by_tok ? 16 * half : 0, tok_step = by_tok ? 32 : 16;
-    const int r = q * 32 + lane;
+    const int row = q * 32 + lane;
     const int groups = kc1 - kc0 < p.groups ? kc1 - kc0 : p.groups, grp_cols = (p.both ? 2 : 1) * NT;
     int buf = 0;
     uint32_t tph = 0;
@@ -310,10 +318,14 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
       const int ft = t / p.MT, mt = t - ft * p.MT, m0 = mt * NT;
       const int nt = p.M - m0 < NT ? p.M - m0 : NT;  // tokens of this tile
       if (S == 1) {
-        const int feat = ft * width + (by_tok ? 0 : half * p.rows) + r;
-        const bool on = r < p.rows && feat < p.N;
+        const int feat = ft * width + (by_tok ? 0 : half * p.rows) + row;
+        const bool on = row < p.rows && feat < p.N;
         const float ba = p.bias && on ? ld16(p.bias, feat, p.bf16) : 0.f;
         const float bb = p.bias_mul && on ? ld16(p.bias_mul, feat, p.bf16) : 0.f;
+        // the residual is asked for ahead, one step before it is added
+        const bool with_r = p.residual && on && !p.pairs;
+        unsigned short r[W], rn[W];
+        if (with_r && tok0 < nt) linear_residual(p, (size_t)(m0 + tok0) * p.N + feat, nt - tok0, rn);
         const bool ok = dn_wait(&bars->tfull[buf], tph, abort);
         if (!ok) dn_fail(bars, status);
         if (dn_any(1, kDnEpi, !ok)) break;  // one decision for the warps
@@ -323,10 +335,14 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
 #pragma unroll 1
           for (int i = n0; i < nt && i < n0 + 16; i += W) {
             float v[W], m[W];
+            const int next = i + W < n0 + 16 ? i + W : n0 + tok_step;
+#pragma unroll
+            for (int j = 0; j < W; ++j) r[j] = rn[j];
+            if (with_r && next < nt) linear_residual(p, (size_t)(m0 + next) * p.N + feat, nt - next, rn);
             linear_sums(d0 + i, groups, grp_cols, v);
             if (p.gated) linear_sums(d0 + NT + i, groups, grp_cols, m);
             if (on && p.pairs) linear_store_pairs(p, feat, m0 + i, nt - i, v);
-            else if (on) linear_store(p, feat, m0 + i, nt - i, ba, bb, v, m);
+            else if (on) linear_store(p, feat, m0 + i, nt - i, ba, bb, v, m, r);
             __syncwarp();
           }
         }
@@ -393,6 +409,9 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           const int n4 = groups4(uh);
           const uint8_t* from = xsums + (size_t)ul * S * unit_bytes + lane * 16;
           for (int i = w % S; i < n4; i += S) {
+            const int n0 = by_tok ? 16 * uh + 32 * (i >> 2) + 4 * (i & 3) : 4 * i;
+            unsigned short r[4];
+            if (p.residual && on && !p.pairs) linear_residual(p, (size_t)(m0 + n0) * p.N + feat, nt - n0, r);
             float v[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
             for (int s = 0; s < S; ++s) {
@@ -409,9 +428,8 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
                 m[3] += b.w;
               }
             }
-            const int n0 = by_tok ? 16 * uh + 32 * (i >> 2) + 4 * (i & 3) : 4 * i;
             if (on && p.pairs) linear_store_pairs(p, feat, m0 + n0, nt - n0, v);
-            else if (on) linear_store(p, feat, m0 + n0, nt - n0, ba, bb, v, m);
+            else if (on) linear_store(p, feat, m0 + n0, nt - n0, ba, bb, v, m, r);
           }
         }
       }
@@ -427,11 +445,12 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
 
 // ---------------------------------------------------------------------------
 // Many tokens: CTA pairs (cta_group::2).  Here the tokens lie on the lanes, 128 of a tile's 256 in each
-// CTA, and 256 columns of weights are the other operand, 128 from each CTA's shared memory (with
-// w_mul: 128 rows of w from the first CTA, the same rows of w_mul from the second, so that one thread has both
-// sums of a feature).  A stage is 32 KB for 4 products of 128 clocks, half of what one CTA alone would have to
-// fetch and read, and the 256 columns of sums are doubled: the epilogue of a tile runs under the next one's
-// products, and stores 16 bytes of a token's row at a time.
+// CTA, and up to 256 columns of weights are the other operand, half from each CTA's shared memory (with
+// w_mul: rows of w from the first CTA, the same rows of w_mul from the second, so that one thread has both
+// sums of a feature).  A stage is up to 32 KB for 4 products of up to 128 clocks, half of what one CTA alone would
+// have to fetch and read, and the columns of sums are doubled: the epilogue of a tile runs under the next one's
+// products, and stores 16 bytes of a token's row at a time.  The number of columns is chosen so that the
+// tiles fill whole waves.
 // ---------------------------------------------------------------------------
 constexpr int kPairStage = 2 * kDnHalf * kDnChunk * 2;
 constexpr int kPairStages = 7;
@@ -439,6 +458,7 @@ constexpr int kPairStages = 7;
 struct PairArgs {
   int M, N, gated, bf16, kn, act, out_f32;
   int MT, T, KC;
+  int rows;         // of weights from each CTA: a multiple of 16 (with w_mul 32), <= 128
   const void *bias, *bias_mul, *residual;
   void* y;
   DenseHead* head;
@@ -454,7 +474,8 @@ __device__ __forceinline__ void load8(const void* base, size_t at, int n, int bf
 }
 
 // Epilogue of 16 neighbouring features of one token (N a multiple of 8: of each 8 all exist or none).
-__device__ __forceinline__ void pair_store(const PairArgs& p, size_t row, int feat, float (&v)[16], const float (&m)[16]) {
+__device__ __forceinline__ void pair_store(const PairArgs& p, size_t row, int feat, float (&v)[16], const float (&m)[16],
+                                           const uint4 (&r)[2]) {
   float t[8];
   if (p.bias) {
 #pragma unroll
@@ -482,9 +503,9 @@ __device__ __forceinline__ void pair_store(const PairArgs& p, size_t row, int fe
   if (p.residual) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      load8(p.residual, at + 8 * h, p.N - feat - 8 * h, p.bf16, t);
+      const uint32_t w[4] = {r[h].x, r[h].y, r[h].z, r[h].w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[8 * h + i] += t[i];
+      for (int i = 0; i < 8; ++i) v[8 * h + i] += from16((unsigned short)(w[i / 2] >> (16 * (i & 1))), p.bf16);
     }
   }
 #pragma unroll
@@ -513,7 +534,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
   DenseBars* bars = reinterpret_cast<DenseBars*>(ring + (size_t)kPairStages * kPairStage);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_rank(), first = blockIdx.x / 2, step = gridDim.x / 2;
-  const int width = p.gated ? kDnHalf : 2 * kDnHalf;  // features of a tile
+  const int width = p.gated ? p.rows : 2 * p.rows;  // features of a tile
+  const int load_rows = p.kn ? (p.rows + 63) / 64 * 64 : p.rows;
   int* status = &p.head->ctrl.status;
   volatile int* abort = &bars->abort;
   const uint32_t ring_at = smem_addr(ring);
@@ -543,14 +565,14 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
       bool ok = true;
       for (int t = first; ok && t < p.T; t += step) {
         const int ft = t / p.MT, mt = t - ft * p.MT;
-        const int m0 = mt * 2 * kDnHalf + rank * kDnHalf, f0 = ft * width + (p.gated ? 0 : rank * kDnHalf);
+        const int m0 = mt * 2 * kDnHalf + rank * kDnHalf, f0 = ft * width + (p.gated ? 0 : rank * p.rows);
         for (int kc = 0; kc < p.KC; ++kc) {
           if (!dn_wait(&bars->empty[st], ph ^ 1, abort)) {
             dn_fail(bars, status);
             ok = false;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(&bars->full[st], 2 * kPairStage);
+          if (rank == 0) mbar_arrive_expect_tx(&bars->full[st], 2 * (kPairStage / 2 + load_rows * 128));
           const uint32_t full = full_at + st * 8;
           const uint32_t a = ring_at + st * kPairStage, b = a + kPairStage / 2;
           const int k = kc * kDnChunk;
@@ -558,8 +580,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
           if (!p.kn) {
             tma_2d_pair(b, mb, k, f0, full, pol);
           } else {
-            tma_2d_pair(b, mb, f0, k, full, pol);
-            tma_2d_pair(b + 8192, mb, f0 + 64, k, full, pol);
+            for (int i = 0; i < load_rows; i += 64) tma_2d_pair(b + i * 128, mb, f0 + i, k, full, pol);
           }
           if (++st == kPairStages) {
             st = 0;
@@ -574,9 +595,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
     }
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
-      // 256 lanes (both CTAs) by 256 columns
+      // 256 lanes (both CTAs) by 2 rows columns
       const uint32_t desc = (1u << 4) | ((uint32_t)p.bf16 << 7) | ((uint32_t)p.bf16 << 10) | ((uint32_t)p.kn << 16) |
-                            ((256u >> 3) << 17) | ((256u >> 4) << 24);
+                            ((uint32_t)(2 * p.rows >> 3) << 17) | ((256u >> 4) << 24);
       int st = 0, buf = 0;
       uint32_t ph = 0, tph = 0;
       bool ok = true, open = false;
@@ -619,13 +640,23 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
     }
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;
-    const int cols = p.gated ? kDnHalf / 2 : kDnHalf;  // features of this warp
+    const int cols = p.gated ? p.rows / 2 : p.rows;  // features of this warp
     int buf = 0;
     uint32_t tph = 0;
     for (int t = first; t < p.T; t += step) {
       const int ft = t / p.MT, mt = t - ft * p.MT;
       const int tok = mt * 2 * kDnHalf + rank * kDnHalf + q * 32 + lane;
       const int f0 = ft * width + half * cols;
+      // the residual is asked for ahead, one step before it is added
+      uint4 r[2], rn[2];
+      auto residual = [&](int c) {
+        if (!p.residual || tok >= p.M) return;
+        const unsigned short* from = reinterpret_cast<const unsigned short*>(p.residual) + (size_t)tok * p.N + f0 + c;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (f0 + c + 8 * h < p.N) rn[h] = *reinterpret_cast<const uint4*>(from + 8 * h);
+      };
+      residual(0);
       const bool ok = dn_wait(&bars->tfull[buf], tph, abort);
       if (!ok) dn_fail(bars, status);
       if (dn_any(1, kDnEpi, !ok)) break;
@@ -633,11 +664,14 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
       const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + buf * 256 + half * cols;
       for (int c = 0; c < cols && f0 + c < p.N; c += 16) {
         float v[16], m[16];
+        r[0] = rn[0];
+        r[1] = rn[1];
+        if (c + 16 < cols) residual(c + 16);
         tmem_ld(d + c, v);
-        if (p.gated) tmem_ld(d + kDnHalf + c, m);
+        if (p.gated) tmem_ld(d + p.rows + c, m);
         tmem_wait(v);
         if (p.gated) tmem_wait(m);
-        if (tok < p.M) pair_store(p, tok, f0 + c, v, m);
+        if (tok < p.M) pair_store(p, tok, f0 + c, v, m, r);
         __syncwarp();
       }
       tc_before_sync();
@@ -692,8 +726,8 @@ int linear_stages(const LinearPlan& l, int M, bool gated, int smem, bool& own_x)
 //   a product of 128 x NT x 16 takes NT / 2, and a quarter more with all SMs at it (the clock drops);
 //   joining a cluster's sums 3300 and 48 for each token and product; a tile's epilogue 600 and 12 for
 //   each token, which runs under the next tile's products where TMEM holds both tiles (NT <= 128);
-//   a CTA pair's stage 650, and 8000 for its first and last tile (2048 x 14336 gated, K = 4096: 275 us
-//   against the model's 270; one CTA a tile 321).
+//   a CTA pair's stage 650 with 256 columns, and 8000 for its first and last tile (2048 x 14336 gated,
+//   K = 4096: 275 us against the model's 270; one CTA a tile 321).
 LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int sms, int smem) {
   LinearPlan best;
   double best_t = 1e30;
@@ -707,14 +741,18 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
   };
   LinearPlan l;
   if (plain && N % 8 == 0 && M > 64) {
-    const int width = gated ? kDnHalf : 2 * kDnHalf, MT = (M + 255) / 256;
-    const long long T = (long long)MT * ((N + width - 1) / width);
-    if (T < (1 << 30)) {
+    // [K][N] weights come in boxes of 64 columns: narrower tiles would start inside a line
+    for (int rows = 64; rows <= kDnHalf; rows += gated || kn ? 64 : 16) {
+      const int width = gated ? rows : 2 * rows, MT = (M + 255) / 256;
+      const long long T = (long long)MT * ((N + width - 1) / width);
+      if (T > (1 << 30)) continue;
       l.pair = 1;
       l.S = 1;
       l.T = (int)T;
       l.MT = MT;
-      const double waves = (double)((T + sms / 2 - 1) / (sms / 2)), t = waves * KC * 650;
+      l.rows = rows;
+      const double waves = (double)((T + sms / 2 - 1) / (sms / 2)), chunk = 650.0 * rows / kDnHalf;
+      const double t = waves * KC * (chunk > 400 ? chunk : 400);
       keep(l, 7000 + 8000 + (t > w_bytes / hbm ? t : w_bytes / hbm));
     }
   }
@@ -785,7 +823,7 @@ static cudaError_t launch_linear_pair(const LinearCall& c, const LinearPlan& l, 
   const bool gated = c.w_mul != nullptr;
   CUtensorMap mw, mw2, mx;
   const uint64_t cols = c.kn ? c.N : c.K, rows = c.kn ? c.K : c.N;
-  const uint32_t box = c.kn ? kDnChunk : kDnHalf;
+  const uint32_t box = c.kn ? kDnChunk : l.rows;
   cudaError_t e = dense_map(&mw, c.w, c.bf16, cols, rows, c.w_stride, 0, 0, box);
   if (e != cudaSuccess) return e;
   mw2 = mw;
@@ -802,6 +840,7 @@ static cudaError_t launch_linear_pair(const LinearCall& c, const LinearPlan& l, 
   p.out_f32 = c.out_f32;
   p.MT = l.MT;
   p.T = l.T;
+  p.rows = l.rows;
   p.KC = (c.K + kDnChunk - 1) / kDnChunk;
   p.bias = c.bias;
   p.bias_mul = c.bias_mul;
@@ -865,9 +904,9 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   bool own_x;
   p.stages = linear_stages(l, c.M, gated, smem_optin, own_x);
   p.own_x = own_x;
-  p.acc_bufs = cols_of <= 256 ? 2 : 1;
+  p.acc_bufs = cols_of <= 256 && l.S == 1 && l.T > sms ? 2 : 1;  // two where a CTA has more than one tile
   // fp32 results: several accumulators, so that each adds up fewer products (the tensor core's
-  // additions cut off; 256 of them in a row cost 3e-6 of the result, 32 cost 4e-7)
+  // additions cut off; K = 4096 in one row costs 3e-6 of the result, in eight 6e-7)
   p.groups = 1;
   const int most_cols = few ? 256 : 512;  // two CTAs on an SM share its 512 columns
   while (c.out_f32 && p.groups < 8 && 2 * p.groups * cols_of * p.acc_bufs <= most_cols) p.groups *= 2;
