@@ -31,6 +31,16 @@ struct LinearArgs {
   int ahead;        // chunks of a CTA's first tile that are asked for before the previous kernel has ended
 };
 
+// Tile t's feature and token tile.  Tiles that run together share operands: eight token tiles at a time go
+// through all features, so that a wave of them is about as many features as tokens.
+__device__ __forceinline__ void tile_at(int t, int T, int MT, int& ft, int& mt) {
+  constexpr int kTogether = 8;
+  const int block = T / MT * kTogether, b = t / block, r = t - b * block;
+  const int here = MT - b * kTogether < kTogether ? MT - b * kTogether : kTogether;
+  ft = r / here;
+  mt = b * kTogether + r - ft * here;
+}
+
 // One decision for W values, not one for each.
 template <int W>
 __device__ __forceinline__ void activate(float (&v)[W], int act) {
@@ -192,7 +202,9 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   const uint32_t tmem = bars->tmem;
   griddep_launch_dependents();
   if (FEW && warp == 0 && elect_one()) {
-    const int f0 = first / p.MT * width, n = kc1 - kc0 < p.ahead ? kc1 - kc0 : p.ahead;
+    int ft, mt;
+    tile_at(first, p.T, p.MT, ft, mt);
+    const int f0 = ft * width, n = kc1 - kc0 < p.ahead ? kc1 - kc0 : p.ahead;
     const CUtensorMap* m2 = p.gated ? &mw2 : &mw;
     const int f1 = p.gated ? f0 : f0 + p.rows;
     for (int i = 0; i < n; ++i) {
@@ -219,7 +231,9 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
       uint32_t ph = 0;
       bool ok = true;
       for (int t = first; ok && t < p.T; t += step) {
-        const int ft = t / p.MT, mt = t - ft * p.MT, f0 = ft * width, m0 = mt * NT;
+        int ft, mt;
+        tile_at(t, p.T, p.MT, ft, mt);
+        const int f0 = ft * width, m0 = mt * NT;
         const CUtensorMap* m2 = p.gated ? &mw2 : &mw;
         const int f1 = p.gated ? f0 : f0 + p.rows;
         for (int kc = kc0; kc < kc1; ++kc) {
@@ -315,7 +329,9 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     int buf = 0;
     uint32_t tph = 0;
     for (int t = first; t < p.T; t += step) {
-      const int ft = t / p.MT, mt = t - ft * p.MT, m0 = mt * NT;
+      int ft, mt;
+      tile_at(t, p.T, p.MT, ft, mt);
+      const int m0 = mt * NT;
       const int nt = p.M - m0 < NT ? p.M - m0 : NT;  // tokens of this tile
       if (S == 1) {
         const int feat = ft * width + (by_tok ? 0 : half * p.rows) + row;
@@ -564,7 +580,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
       uint32_t ph = 0;
       bool ok = true;
       for (int t = first; ok && t < p.T; t += step) {
-        const int ft = t / p.MT, mt = t - ft * p.MT;
+        int ft, mt;
+        tile_at(t, p.T, p.MT, ft, mt);
         const int m0 = mt * 2 * kDnHalf + rank * kDnHalf, f0 = ft * width + (p.gated ? 0 : rank * p.rows);
         for (int kc = 0; kc < p.KC; ++kc) {
           if (!dn_wait(&bars->empty[st], ph ^ 1, abort)) {
@@ -644,7 +661,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
     int buf = 0;
     uint32_t tph = 0;
     for (int t = first; t < p.T; t += step) {
-      const int ft = t / p.MT, mt = t - ft * p.MT;
+      int ft, mt;
+      tile_at(t, p.T, p.MT, ft, mt);
       const int tok = mt * 2 * kDnHalf + rank * kDnHalf + q * 32 + lane;
       const int f0 = ft * width + half * cols;
       // the residual is asked for ahead, one step before it is added
