@@ -489,6 +489,13 @@ __device__ __forceinline__ void load8(const void* base, size_t at, int n, int bf
   for (int i = 0; i < 8; ++i) v[i] = from16((unsigned short)(w[i / 2] >> (16 * (i & 1))), bf16);
 }
 
+// 32 bytes at a time: whole sectors (32-byte aligned)
+__device__ __forceinline__ void store32(void* to, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // Epilogue of 16 neighbouring features of one token (N a multiple of 8: of each 8 all exist or none).
 __device__ __forceinline__ void pair_store(const PairArgs& p, size_t row, int feat, float (&v)[16], const float (&m)[16],
                                            const uint4 (&r)[2]) {
@@ -523,6 +530,24 @@ __device__ __forceinline__ void pair_store(const PairArgs& p, size_t row, int fe
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[8 * h + i] += from16((unsigned short)(w[i / 2] >> (16 * (i & 1))), p.bf16);
     }
+  }
+  if (p.N % 16 == 0) {
+    uint32_t w[8];
+    if (p.out_f32) {
+      float* y = reinterpret_cast<float*>(p.y) + at;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
+        store32(y + 8 * h, w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i] = (uint32_t)to16(v[2 * i], p.bf16) | (uint32_t)to16(v[2 * i + 1], p.bf16) << 16;
+      store32(reinterpret_cast<unsigned short*>(p.y) + at, w);
+    }
+    return;
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -742,8 +767,8 @@ int linear_stages(const LinearPlan& l, int M, bool gated, int smem, bool& own_x)
 //   run at 383 clocks each, three 32 KB ones at 831), and a stage costs its issuing threads 330,
 //   60 more where its rows are shorter boxes;
 //   a product of 128 x NT x 16 takes NT / 2, and a quarter more with all SMs at it (the clock drops);
-//   joining a cluster's sums 3300 and 48 for each token and product; a tile's epilogue 600 and 12 for
-//   each token, which runs under the next tile's products where TMEM holds both tiles (NT <= 128);
+//   joining a cluster's sums 3300 and 48 for each token and product; a tile's epilogue 600 and 26 for
+//   each token and product, which runs under the next tile's products where TMEM holds both tiles (NT <= 128);
 //   a CTA pair's stage 650 with 256 columns, and 8000 for its first and last tile (2048 x 14336 gated,
 //   K = 4096: 275 us against the model's 270; one CTA a tile 321).
 LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int sms, int smem) {
@@ -797,7 +822,7 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
     for (const double least : {mma, 2400.0 / stages, 330.0})
       if (chunk < least) chunk = least;
     if (rows < kDnHalf) chunk += 60;
-    const double epi = 600 + 12.0 * l.NT * mats;
+    const double epi = 600 + 26.0 * l.NT * (both ? 2 : 1);
     double t = waves * ((KC + S - 1) / S) * chunk;
     if (t < w_bytes / hbm) t = w_bytes / hbm;
     t += S > 1 ? 3300 + 48.0 * l.NT * (both ? 2 : 1) : l.NT <= 128 ? epi : epi * waves;
