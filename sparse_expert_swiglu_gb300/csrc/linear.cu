@@ -19,16 +19,16 @@ struct LinearArgs {
   int MT, NT, T;    // token tiles, tokens of a tile, tiles
   int rows;         // features of one product, <= 128
   int both;         // two products (always with w_mul)
-  int KC, S;        // chunks of k, CTAs of a tile
+  int wide;         // chunks of 64 k in a stage, one behind the other
+  int KC, S;        // stages of a tile, CTAs of a tile
   int split;        // y as two 16-bit rows for each token, 2 t and 2 t + 1: the rounded value and the rest
   int pairs;        // x has two such rows for each token of y
-  int groups;       // accumulators of a product: chunk c of a tile goes to c % groups
+  int groups;       // accumulators of a product: stage c of a tile goes to c % groups
   const void *bias, *bias_mul, *residual;
   void* y;
   DenseHead* head;
   int stages, acc_bufs, buf_cols, tmem_cols, stream;
   int own_x;        // the cluster's partial sums have memory of their own, behind the stages
-  int ahead;        // chunks of a CTA's first tile that are asked for before the previous kernel has ended
 };
 
 // Tile t's feature and token tile.  Tiles that run together share operands: eight token tiles at a time go
@@ -158,18 +158,17 @@ __device__ __forceinline__ void linear_sums(uint32_t addr, int groups, int strid
   }
 }
 
-// FEW: up to kFewTokens tokens.  Half the shared memory and registers, so that the next call's CTAs start
-// beside this one's and ask for their weights while these still stream: a chain of such calls keeps HBM
-// busy.  (Asked for into L2 alone, since the previous kernel may still write them.)
+// FEW: up to kFewTokens tokens, whose epilogue takes 4 at a time: a call this short pays for every line of
+// code it fetches.
 template <bool FEW>
-__global__ void __launch_bounds__(kDnThreads, FEW ? 2 : 1)
+__global__ void __launch_bounds__(kDnThreads, 1)
 linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mw2,
               const __grid_constant__ CUtensorMap mx, const LinearArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  const int bytes_a = p.both ? kDnBytesA : kDnBytesA / 2;  // of a stage; rows behind p.rows stay unwritten
-  const uint32_t stage_bytes = bytes_a + p.NT * 128;
-  const uint32_t load_bytes = (p.both ? 2 : 1) * p.rows * 128 + p.NT * 128;
+  const int bytes_a = p.both ? kDnBytesA : kDnBytesA / 2;  // of a chunk; rows behind p.rows stay unwritten
+  const uint32_t chunk_bytes = bytes_a + p.NT * 128, stage_bytes = p.wide * chunk_bytes;
+  const uint32_t load_bytes = p.wide * ((p.both ? 2 : 1) * p.rows * 128 + p.NT * 128);
   // partial sums that a cluster's CTAs push here: behind the stages, or in them once they are free
   const int most = p.M < p.NT ? p.M : p.NT, g4 = (most + 3) / 4, mats = p.gated ? 2 : 1;
   uint8_t* xsums = p.own_x ? ring + (size_t)p.stages * stage_bytes : ring;
@@ -201,25 +200,6 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   tc_after_sync();
   const uint32_t tmem = bars->tmem;
   griddep_launch_dependents();
-  if (FEW && warp == 0 && elect_one()) {
-    int ft, mt;
-    tile_at(first, p.T, p.MT, ft, mt);
-    const int f0 = ft * width, n = kc1 - kc0 < p.ahead ? kc1 - kc0 : p.ahead;
-    const CUtensorMap* m2 = p.gated ? &mw2 : &mw;
-    const int f1 = p.gated ? f0 : f0 + p.rows;
-    for (int i = 0; i < n; ++i) {
-      const int k = (kc0 + i) * kDnChunk;
-      if (!p.kn) {
-        tma_prefetch_2d(&mw, k, f0);
-        if (p.both) tma_prefetch_2d(m2, k, f1);
-      } else {
-        for (int j = 0; j < p.rows; j += 64) {
-          tma_prefetch_2d(&mw, f0 + j, k);
-          if (p.both) tma_prefetch_2d(m2, f1 + j, k);
-        }
-      }
-    }
-  }
   griddep_wait();
 
   if (warp == 0) {
@@ -245,18 +225,20 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           uint64_t* full = &bars->full[st];
           mbar_arrive_expect_tx(full, load_bytes);
           ++issued;
-          const uint32_t a = ring_at + st * stage_bytes;
-          const int k = kc * kDnChunk;
-          if (!p.kn) {
-            tma_2d(a, &mw, k, f0, full, pw);
-            if (p.both) tma_2d(a + kDnBytesA / 2, m2, k, f1, full, pw);
-          } else {
-            for (int i = 0; i < p.rows; i += 64) {
-              tma_2d(a + i * 128, &mw, f0 + i, k, full, pw);
-              if (p.both) tma_2d(a + kDnBytesA / 2 + i * 128, m2, f1 + i, k, full, pw);
+          uint32_t a = ring_at + st * stage_bytes;
+          for (int c = 0; c < p.wide; ++c, a += chunk_bytes) {
+            const int k = (kc * p.wide + c) * kDnChunk;
+            if (!p.kn) {
+              tma_2d(a, &mw, k, f0, full, pw);
+              if (p.both) tma_2d(a + kDnBytesA / 2, m2, k, f1, full, pw);
+            } else {
+              for (int i = 0; i < p.rows; i += 64) {
+                tma_2d(a + i * 128, &mw, f0 + i, k, full, pw);
+                if (p.both) tma_2d(a + kDnBytesA / 2 + i * 128, m2, f1 + i, k, full, pw);
+              }
             }
+            tma_2d(a + bytes_a, &mx, k, m0, full, px);
           }
-          tma_2d(a + bytes_a, &mx, k, m0, full, px);
           if (++st == ns) {
             st = 0;
             ph ^= 1;
@@ -297,6 +279,8 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           const uint32_t a = ring_at + st * stage_bytes;
           const uint32_t d0 = tmem + buf * p.buf_cols + grp * grp_cols;
           dn_stage_products(a, a + bytes_a, d0, d0 + NT, desc, p.kn, kc - kc0 < p.groups, p.both);
+          if (p.wide > 1)
+            dn_stage_products(a + chunk_bytes, a + chunk_bytes + bytes_a, d0, d0 + NT, desc, p.kn, false, p.both);
           mma_commit(&bars->empty[st]);
           open = true;
           if (++grp == p.groups) grp = 0;
@@ -734,7 +718,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
 
 struct LinearPlan {
   int M = -1, N = 0, K = 0, gated = 0, kn = 0, plain = 0, sms = 0;  // what it is for
-  int pair = 0, NT = 0, MT = 0, rows = 0, both = 0, S = 0, T = 0;
+  int pair = 0, NT = 0, MT = 0, rows = 0, both = 0, wide = 1, S = 0, T = 0;
 };
 
 constexpr int kFewTokens = 32;
@@ -750,10 +734,9 @@ int linear_sum_bytes(const LinearPlan& l, int M, bool gated) {
 
 // Stages of a CTA, and whether the partial sums have memory behind them (up to 16 KB).
 int linear_stages(const LinearPlan& l, int M, bool gated, int smem, bool& own_x) {
-  const int stage = (l.both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128, sums = linear_sum_bytes(l, M, gated);
+  const int stage = l.wide * ((l.both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128), sums = linear_sum_bytes(l, M, gated);
   own_x = l.S > 1 && sums <= 16384;
-  // few tokens: two CTAs on an SM (each with 1 KB that the system takes)
-  const int room = (l.NT <= kFewTokens ? smem / 2 - 512 : smem) - 1024 - (int)sizeof(DenseBars) - (own_x ? sums : 0);
+  const int room = smem - 1024 - (int)sizeof(DenseBars) - (own_x ? sums : 0);
   const int n = room / stage;
   return n > kDnMaxStages ? kDnMaxStages : n;
 }
@@ -764,8 +747,8 @@ int linear_stages(const LinearPlan& l, int M, bool gated, int smem, bool& own_x)
 //   an SM takes 62 bytes a clock from L2 (tiles of 128 x 128: 32 KB in 516 clocks), all SMs together
 //   3550 out of HBM, and where both are needed the lesser adds 0.15 of itself;
 //   a stage's bytes come 2400 after they are asked for (4096 x 4096, one token, 16 KB stages: six of them
-//   run at 383 clocks each, three 32 KB ones at 831), and a stage costs its issuing threads 330,
-//   60 more where its rows are shorter boxes;
+//   run at 383 clocks each, three 32 KB ones at 831), and a stage costs its issuing threads 330, or
+//   430 with twice the k, and 60 more for each 64 k where its rows are shorter boxes;
 //   a product of 128 x NT x 16 takes NT / 2, and a quarter more with all SMs at it (the clock drops);
 //   joining a cluster's sums 3300 and 48 for each token and product; a tile's epilogue 600 and 26 for
 //   each token and product, which runs under the next tile's products where TMEM holds both tiles (NT <= 128);
@@ -774,7 +757,7 @@ int linear_stages(const LinearPlan& l, int M, bool gated, int smem, bool& own_x)
 LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int sms, int smem) {
   LinearPlan best;
   double best_t = 1e30;
-  const int KC = (K + kDnChunk - 1) / kDnChunk, mats = gated ? 2 : 1;
+  const int chunks = (K + kDnChunk - 1) / kDnChunk, mats = gated ? 2 : 1;
   const double w_bytes = 2.0 * mats * N * K, hbm = 3550;
   auto keep = [&](const LinearPlan& l, double t) {
     if (t < best_t) {
@@ -795,12 +778,14 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
       l.MT = MT;
       l.rows = rows;
       const double waves = (double)((T + sms / 2 - 1) / (sms / 2)), chunk = 650.0 * rows / kDnHalf;
-      const double t = waves * KC * (chunk > 400 ? chunk : 400);
+      const double t = waves * chunks * (chunk > 400 ? chunk : 400);
       keep(l, 7000 + 8000 + (t > w_bytes / hbm ? t : w_bytes / hbm));
     }
   }
-  auto consider = [&](int NT, int rows, int both, int S) {
+  auto consider = [&](int NT, int rows, int both, int wide, int S) {
     l.pair = 0;
+    l.wide = wide;
+    const int KC = (chunks + wide - 1) / wide;
     l.MT = (M + NT - 1) / NT;
     l.NT = ((M + l.MT - 1) / l.MT + 15) / 16 * 16;
     l.rows = rows;
@@ -811,20 +796,22 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
     if (T > (1 << 30) || (S > 1 && (T > fit || S > KC))) return;
     l.T = (int)T;
     bool own_x;
-    const int stage = (both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128, stages = linear_stages(l, M, gated, smem, own_x);
+    const int stage = wide * ((both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128);
+    const int stages = linear_stages(l, M, gated, smem, own_x);
     if (stages < 2 || (S > 1 && !own_x && linear_sum_bytes(l, M, gated) > stages * stage)) return;
     const double waves = (double)((T + fit - 1) / fit), active = (double)(T < fit ? T : fit) * S;
-    const double load = ((both ? 2 : 1) * rows + l.NT) * 128.0;
-    const double mma = (both ? 2 : 1) * 4 * 1.25 * l.NT / 2, l2 = load / 62;
+    const double load = wide * ((both ? 2 : 1) * rows + l.NT) * 128.0;
+    const double mma = wide * (both ? 2 : 1) * 4 * 1.25 * l.NT / 2, l2 = load / 62;
     // weights that several token tiles of a wave share come out of HBM once
-    const double mem = (load - l.NT * 128.0) * active / hbm / (T < fit ? l.MT : l.MT < waves ? 1 : l.MT / waves);
+    const double mem = (load - wide * l.NT * 128.0) * active / hbm / (T < fit ? l.MT : l.MT < waves ? 1 : l.MT / waves);
     double chunk = l2 > mem ? l2 + 0.15 * mem : mem + 0.15 * l2;
-    for (const double least : {mma, 2400.0 / stages, 330.0})
+    for (const double least : {mma, 2400.0 / stages, 230.0 + 100 * wide})
       if (chunk < least) chunk = least;
-    if (rows < kDnHalf) chunk += 60;
+    if (rows < kDnHalf) chunk += 60 * wide;
     const double epi = 600 + 26.0 * l.NT * (both ? 2 : 1);
     double t = waves * ((KC + S - 1) / S) * chunk;
     if (t < w_bytes / hbm) t = w_bytes / hbm;
+    if (wide > 1) t *= 0.98;  // 216 KB in flight instead of 147
     t += S > 1 ? 3300 + 48.0 * l.NT * (both ? 2 : 1) : l.NT <= 128 ? epi : epi * waves;
     keep(l, 7000 + t);
   };
@@ -832,7 +819,8 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
   for (int both = gated ? 1 : 0; both < 2; ++both)
     for (int rows = both && !gated ? kDnHalf : kn ? 64 : 32; rows <= kDnHalf; rows += kn ? 64 : 32)
       for (int NT = 16; NT <= top; NT += 16)
-        for (int S = 1; S <= 8; S *= 2) consider(NT, rows, both, S);
+        for (int S = 1; S <= 8; S *= 2)
+          for (int wide = 1; wide <= (NT <= kFewTokens ? 2 : 1); ++wide) consider(NT, rows, both, wide, S);
   best.M = M;
   best.N = N;
   best.K = K;
@@ -934,7 +922,8 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   p.T = l.T;
   p.rows = l.rows;
   p.both = l.both;
-  p.KC = (c.K + kDnChunk - 1) / kDnChunk;
+  p.wide = l.wide;
+  p.KC = ((c.K + kDnChunk - 1) / kDnChunk + l.wide - 1) / l.wide;
   p.S = l.S;
   p.split = c.split;
   p.pairs = c.pairs;
@@ -943,7 +932,7 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   p.residual = c.residual;
   p.y = c.y;
   p.head = reinterpret_cast<DenseHead*>(ws);
-  const int stage = (l.both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128, cols_of = (l.both ? 2 : 1) * l.NT;
+  const int stage = l.wide * ((l.both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128), cols_of = (l.both ? 2 : 1) * l.NT;
   bool own_x;
   p.stages = linear_stages(l, c.M, gated, smem_optin, own_x);
   p.own_x = own_x;
@@ -951,14 +940,12 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   // fp32 results: several accumulators, so that each adds up fewer products (the tensor core's
   // additions cut off; K = 4096 in one row costs 3e-6 of the result, in eight 6e-7)
   p.groups = 1;
-  const int most_cols = few ? 256 : 512;  // two CTAs on an SM share its 512 columns
-  while (c.out_f32 && p.groups < 8 && 2 * p.groups * cols_of * p.acc_bufs <= most_cols) p.groups *= 2;
+  while (c.out_f32 && p.groups < 8 && 2 * p.groups * cols_of * p.acc_bufs <= 512) p.groups *= 2;
   p.buf_cols = p.groups * cols_of;
   p.tmem_cols = 32;
   while (p.tmem_cols < p.buf_cols * p.acc_bufs) p.tmem_cols *= 2;
   p.stream = l.MT == 1;
   const int ctas = l.S > 1 ? l.T * l.S : l.T < sms ? l.T : sms;
-  p.ahead = (int)((32 << 20) / ((size_t)ctas * (l.both ? 2 : 1) * l.rows * 128));  // 32 MB of L2 in all
   const size_t smem = 1024 + (size_t)p.stages * stage + sizeof(DenseBars) + (own_x ? linear_sum_bytes(l, c.M, gated) : 0);
   e = cudaFuncSetAttribute(few ? linear_kernel<true> : linear_kernel<false>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
