@@ -540,20 +540,31 @@ def _dense_in(t, dtype, device: int, shape, name: str) -> int:
     raise ValueError(f"{name} must be contiguous")
 
 
-def _dense_x(x, name: str = "x") -> int:
-    """The device of a call's tokens, a CUDA fp16 or bf16 matrix on the current device."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    device = x.get_device()
+def _dense_x(x) -> int:
+    """The device of a call's tokens x: a dense CUDA fp16 or bf16 matrix on the current device."""
+    if isinstance(x, torch.Tensor):
+        dt, device = x.dtype, x.get_device()
+        if ((dt is torch.float16 or dt is torch.bfloat16) and device >= 0 and x.dim() == 2 and x.is_contiguous()
+                and device == torch._C._cuda_getDevice()):
+            return device
+    else:
+        raise TypeError("x must be a tensor")
     if device < 0:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if x.dtype is not torch.float16 and x.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {x.dtype}")
+        raise TypeError("x must be a CUDA tensor")
+    if dt is not torch.float16 and dt is not torch.bfloat16:
+        raise TypeError(f"x must be torch.float16 or torch.bfloat16, got {dt}")
     if x.dim() != 2:
-        raise ValueError(f"{name} must be a matrix")
-    if device != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{device}, which is not the current device")
-    return device
+        raise ValueError("x must be a matrix")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    raise ValueError(f"x is on cuda:{device}, which is not the current device")
+
+
+try:  # torch.empty on the current CUDA device without the dispatcher: half its time in a decode step's many calls
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    def _empty_strided_cuda(shape, stride, dtype):
+        return torch.empty_strided(shape, stride, dtype=dtype, device="cuda")
 
 
 def _dense_ws(ws, device: int, nbytes, *sizes) -> "Workspace":
@@ -612,13 +623,11 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     else:
         raise TypeError(f"out_dtype must be {dt} or torch.float32, got {out_dtype}")
     if out is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        y = _empty_strided_cuda((M, N), (N, 1), out_dtype)
         yp = y.data_ptr()
     else:
         y = out
         yp = _dense_in(out, out_dtype, device, (M, N), "out")
-    if not x.is_contiguous():
-        raise ValueError("x must be contiguous")
     op = _Linear(M, N, K, dtype_code, out_code, layout_code, act_code,
                  x.data_ptr(), _dense_in(w, dt, device, wshape, "w"),
                  None if w_mul is None else _dense_in(w_mul, dt, device, wshape, "w_mul"),
@@ -712,11 +721,11 @@ def expert_dense_swiglu(x: torch.Tensor, experts: DenseExperts, expert: int, res
     if experts.gate_t.dtype != dt or experts.gate_t.get_device() != device:
         raise ValueError("x and the experts must have one type and device")
     shape = (n, ex.d)
-    if x.shape[1] != ex.d or not x.is_contiguous():
-        raise ValueError(f"x must be contiguous with shape {shape}, got {tuple(x.shape)}")
+    if x.shape[1] != ex.d:
+        raise ValueError(f"x must have shape {shape}, got {tuple(x.shape)}")
     rp = None if residual is None else _dense_in(residual, dt, device, shape, "residual")
     if out is None:
-        y = torch.empty_like(x)
+        y = _empty_strided_cuda(shape, (shape[1], 1), dt)
     else:
         y = out
         _dense_in(out, dt, device, shape, "out")
@@ -747,11 +756,11 @@ def layer_dense_decode(x: torch.Tensor, layer: DenseLayer, residual: Optional[to
         raise ValueError("x and the experts must have one type and device")
     d = layer.routed.gate_t.shape[2]
     shape = (B, d)
-    if x.shape[1] != d or not x.is_contiguous():
-        raise ValueError(f"x must be contiguous with shape {shape}, got {tuple(x.shape)}")
+    if x.shape[1] != d:
+        raise ValueError(f"x must have shape {shape}, got {tuple(x.shape)}")
     rp = None if residual is None else _dense_in(residual, dt, device, shape, "residual")
     if out is None:
-        y = torch.empty_like(x)
+        y = _empty_strided_cuda(shape, (shape[1], 1), dt)
     else:
         y = out
         _dense_in(out, dt, device, shape, "out")

@@ -489,8 +489,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   __syncthreads();
   tc_after_sync();
   const uint32_t tmem = bars->tmem;
-  griddep_launch_dependents();
-  griddep_wait();
+  griddep_launch_dependents();  // the next call's CTAs take the SMs that this kernel's leave
 
   // Chunk kc of tile t of the shared or of the active routed experts, into a stage.
   const uint64_t pw = policy_evict_first(), px = policy_evict_normal();
@@ -1011,13 +1010,11 @@ cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int s
   cfg.blockDim = dim3(kDnThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, dense_layer_kernel, maps, p);
 }
 
