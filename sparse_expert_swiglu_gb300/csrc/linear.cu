@@ -751,7 +751,7 @@ int linear_stages(const LinearPlan& l, int M, bool gated, int smem, bool& own_x)
 //   430 with twice the k, and 60 more for each 64 k where its rows are shorter boxes;
 //   a product of 128 x NT x 16 takes NT / 2, and a quarter more with all SMs at it (the clock drops);
 //   joining a cluster's sums 3300 and 48 for each token and product; a tile's epilogue 600 and 26 for
-//   each token and product, which runs under the next tile's products where TMEM holds both tiles (NT <= 128);
+//   each token and product, which runs under the next tile's products where TMEM holds both tiles;
 //   a CTA pair's stage 650 with 256 columns, and 8000 for its first and last tile (2048 x 14336 gated,
 //   K = 4096: 275 us against the model's 270; one CTA a tile 321).
 LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int sms, int smem) {
@@ -809,10 +809,12 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
       if (chunk < least) chunk = least;
     if (rows < kDnHalf) chunk += 60 * wide;
     const double epi = 600 + 26.0 * l.NT * (both ? 2 : 1);
-    double t = waves * ((KC + S - 1) / S) * chunk;
+    const double products = ((KC + S - 1) / S) * chunk;
+    double t = S > 1 ? products + 3300 + 48.0 * l.NT * (both ? 2 : 1)
+               : l.NT * (both ? 2 : 1) <= 256 ? waves * (products > epi ? products : epi) + epi
+                                              : waves * (products + epi);
     if (t < w_bytes / hbm) t = w_bytes / hbm;
     if (wide > 1) t *= 0.98;  // 216 KB in flight instead of 147
-    t += S > 1 ? 3300 + 48.0 * l.NT * (both ? 2 : 1) : l.NT <= 128 ? epi : epi * waves;
     keep(l, 7000 + t);
   };
   const int top = M < 256 ? (M + 15) / 16 * 16 : 256;

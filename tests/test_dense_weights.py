@@ -156,6 +156,43 @@ def test_linear_split_sum_and_full_waves():
 
 
 @gpu
+@pytest.mark.parametrize("M,N,K,gated,layout", [
+    (1, 4096, 4096, False, "nk"), (1, 1024, 8192, False, "kn"), (4, 512, 16384, True, "nk"), (5, 520, 8200, True, "kn"),
+    (16, 2048, 2048, False, "nk"), (33, 768, 8192, False, "nk"), (64, 1000, 4096, True, "kn"), (100, 300, 16384, False, "nk"),
+    (128, 2048, 2048, False, "kn"), (300, 264, 8192, False, "nk")])
+def test_linear_sums_shared_by_a_cluster(M, N, K, gated, layout):
+    """Few tiles and a long k: two to eight CTAs share a tile."""
+    for bias, residual, out in ((False, False, None), (True, True, F32)):
+        c = _linear_case(M, N, K, BF16, "gelu_tanh", bias, gated, residual, layout, out)
+        y = _linear_check(c)
+        assert torch.equal(y, _linear_run(c))
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(256, 256, 64), (512, 520, 1000), (700, 1032, 520), (1500, 1040, 136), (1025, 4096, 72),
+                                   (2048, 2048, 264)])
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+def test_linear_many_tokens(M, N, K, layout):
+    for dtype, gated, bias, residual, out in ((BF16, False, False, True, None), (F16, True, True, False, None),
+                                              (F16, False, True, True, F32), (BF16, True, False, True, F32)):
+        _linear_check(_linear_case(M, N, K, dtype, "silu", bias, gated, residual, layout, out))
+
+
+@gpu
+def test_linear_output_behind_2_to_the_31():
+    M, N, K = 65537, 40000, 64
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(M, K, device="cuda", dtype=F16, generator=g)
+    w = torch.randn(N, K, device="cuda", dtype=F16, generator=g)
+    y = ses.linear(x, w)
+    for rows in (slice(0, 3), slice(53685, 53690), slice(M - 3, M)):  # 53687 * 40000 crosses 2^31
+        a, b = x[rows].double().cpu(), w.double().cpu()
+        _within(y[rows], a @ b.t(), _tau(K) * (a.abs() @ b.abs().t()), F16)
+    odd = ses.linear(x, w[:39999])
+    assert torch.equal(odd[-3:], y[-3:, :39999]) and torch.equal(odd[53687], y[53687, :39999])
+
+
+@gpu
 def test_linear_large_values_and_nan():
     """A token with NaN or inf spoils its own row alone; sums beyond fp16 round to inf."""
     c = _linear_case(20, 130, 256, F16, "relu")
@@ -298,6 +335,65 @@ def _layer_check(c, ws=None, idx_as_oracle=True):
 def test_layer_sizes(B, d, f, E, k, ns, dtype):
     for renorm, residual, rmsnorm in ((True, False, False), (False, True, True), (True, True, False)):
         _layer_check(_layer_case(B, d, f, E, k, ns, dtype, renorm, residual, rmsnorm))
+
+
+@gpu
+def test_layer_of_the_largest_experts():
+    """d = 16384, f = 65536: an expert's rows lie behind 2^31 elements."""
+    d, f, E = 16384, 65536, 3
+    g = torch.Generator(device="cuda").manual_seed(4)
+    gate, up, down = (torch.empty(E, f, d, device="cuda", dtype=BF16).normal_(0, 0.01, generator=g) for _ in range(3))
+    wr = torch.randn(d, E, device="cuda", dtype=BF16, generator=g) * 0.05
+    x = torch.randn(3, d, device="cuda", dtype=BF16, generator=g)
+    y, dbg = ses.layer_dense_decode(x, ses.DenseLayer(wr, ses.DenseExperts(gate, up, down), 1), debug=True)
+    idx = dbg["topk_idx"][:, 0].cpu()
+    assert torch.equal(idx, (x.double() @ wr.double()).argmax(1).int().cpu())
+    for e in sorted(set(idx.tolist())):
+        one = ses.expert_dense_swiglu(x, ses.DenseExperts(gate, up, down), e)
+        b = [i for i in range(3) if idx[i] == e]
+        xd = x[b].double()
+        h = torch.nn.functional.silu(xd @ gate[e].double().t()) * (xd @ up[e].double().t())
+        ref = (h @ down[e].double()).cpu()
+        for got in (y[b], one[b]):
+            # h and its sums: at most a part in 2^14 of the terms' root sum of squares; then the rounding
+            lim = 2.0 ** -14 * float(h.norm(dim=1).max()) * 0.01 * 8 + _half_step(BF16) * ref.abs() * 1.01
+            assert ((got.double().cpu() - ref).abs() <= lim).all()
+
+
+@gpu
+def test_layers_on_two_streams_at_once():
+    """Each call's kernel takes every SM and waits for its own CTAs: two streams, two workspaces."""
+    a = _layer_case(17, 1024, 520, 8, 2, 1, BF16, True, False, False)
+    b = _layer_case(1, 512, 1024, 16, 4, 0, F16, False, False, True)
+    want = [ses.layer_dense_decode(c["x"].cuda(), c["layer"], rmsnorm=c["rmsnorm"]) for c in (a, b)]
+    ws = [ses.Workspace(ses.layer_dense_workspace_bytes(c["layer"], len(c["x"]))) for c in (a, b)]
+    xs = [c["x"].cuda() for c in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, c in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(ses.layer_dense_decode(xs[i], c["layer"], rmsnorm=c["rmsnorm"], ws=ws[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert ws[i].status() == 0
+        assert all(torch.equal(y, want[i]) for y in got[i])
+
+
+@gpu
+def test_outputs_in_the_residual():
+    c = _layer_case(5, 264, 200, 8, 2, 1, F16, True, True, False)
+    x, r = c["x"].cuda(), c["residual"].cuda()
+    for rmsnorm in (False, True):
+        y = ses.layer_dense_decode(x, c["layer"], residual=r, rmsnorm=rmsnorm)
+        z = r.clone()
+        assert ses.layer_dense_decode(x, c["layer"], residual=z, rmsnorm=rmsnorm, out=z) is z and torch.equal(z, y)
+    for n in (5, 70):
+        xn, rn = x.repeat(14, 1)[:n].contiguous(), r.repeat(14, 1)[:n].contiguous()
+        y = ses.expert_dense_swiglu(xn, c["layer"].routed, 2, residual=rn)
+        z = rn.clone()
+        assert ses.expert_dense_swiglu(xn, c["layer"].routed, 2, residual=z, out=z) is z and torch.equal(z, y)
 
 
 @gpu
@@ -576,3 +672,15 @@ def test_binding_refusals_on_the_device():
     with pytest.raises(MoeError) as err:
         ses.linear(x, w, ws=ses.Workspace(256))
     assert err.value.status == -4
+    c = _layer_case(2, 64, 72, 4, 2, 0, F16, True, False, False)
+    for call in (lambda ws: ses.layer_dense_decode(c["x"].cuda(), c["layer"], ws=ws),
+                 lambda ws: ses.expert_dense_swiglu(c["x"].cuda(), c["layer"].routed, 0, ws=ws)):
+        with pytest.raises(MoeError) as err:
+            call(ses.Workspace(256))
+        assert err.value.status == -4
+    with pytest.raises(ValueError):  # 65 tokens: more than the layer takes
+        ses.layer_dense_decode(torch.zeros(65, 64, dtype=F16, device="cuda"), c["layer"])
+    with pytest.raises(ValueError):
+        ses.layer_dense_decode(torch.zeros(2, 72, dtype=F16, device="cuda"), c["layer"])
+    with pytest.raises(ValueError):
+        ses.layer_dense_decode(c["x"].cuda().bfloat16(), c["layer"])
