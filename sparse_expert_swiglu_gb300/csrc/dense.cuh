@@ -45,21 +45,23 @@ struct DenseHead {
 // ---------------------------------------------------------------------------
 struct Sched {
   int T, KC, P, dp, q, total;
-  __host__ __device__ static Sched make(int T, int KC, int P) {
+  // at least the first `whole` tiles stay whole
+  __host__ __device__ static Sched make(int T, int KC, int P, int whole) {
     Sched s;
     s.T = T;
     s.KC = KC;
     s.P = P;
+    // Joining the shares of the last tiles takes about 4 us, and a chunk 0.7 us: a last wave that leaves less
+    // than that idle on average is not cut.
     const int rest = T % P;
-    // a rest of nearly a whole wave gains less from being cut than its joining costs
-    s.dp = rest * 10 >= P * 9 ? T : T - rest;
+    s.dp = (P - rest) * KC * 10 <= 57 * P ? T : T - rest;
+    if (s.dp < whole) s.dp = whole;
     s.total = (T - s.dp) * KC;
     const int by_ctas = (s.total + P - 1) / P, by_split = (KC + kDnMaxSplit - 1) / kDnMaxSplit;
     s.q = by_ctas > by_split ? by_ctas : by_split;
     if (s.q < 1) s.q = 1;
     return s;
   }
-  __host__ __device__ int ctas() const { return dp ? P : (total + q - 1) / q; }
   // shares of a split tile (t >= dp) and the CTA of the first one
   __host__ __device__ int first(int t) const { return (t - dp) * KC / q; }
   __host__ __device__ int parts(int t) const { return t < dp ? 1 : ((t - dp + 1) * KC - 1) / q - first(t) + 1; }
@@ -441,17 +443,19 @@ __device__ __forceinline__ void sum_shares(const float* from, size_t second, siz
   }
 }
 
-// One stage's products of both 128-feature tiles (or, with `both` false, of the first alone).  The k steps of an
+// One stage's products of both 128-feature tiles, the second one `second` bytes behind the first (or, with `both`
+// false, of the first alone).  The k steps of an
 // operand are 32 bytes apart along its rows, 2048 across them: 2 and 128 of the descriptor's units.
 __device__ __forceinline__ void dn_stage_products(uint32_t a, uint32_t b, uint32_t d0, uint32_t d1, uint32_t desc,
-                                                  bool a_mn, bool first, bool both = true) {
+                                                  bool a_mn, bool first, bool both = true,
+                                                  uint32_t second = kDnBytesA / 2) {
   const uint64_t ad = smem_desc(a, a_mn ? 8192 : 16), bd = smem_desc(b, 16);
   const uint32_t step = a_mn ? 128 : 2;
 #pragma unroll
   for (int ks = 0; ks < kDnChunk / 16; ++ks) {
     const uint32_t add = !(first && ks == 0);
     mma_f16(d0, ad + ks * step, bd + ks * 2, desc, add);
-    if (both) mma_f16(d1, ad + kDnBytesA / 32 + ks * step, bd + ks * 2, desc, add);
+    if (both) mma_f16(d1, ad + (second >> 4) + ks * step, bd + ks * 2, desc, add);
   }
 }
 

@@ -51,6 +51,7 @@ struct LayerArgs {
   float* yrow;         // [B][d] sums before RMSNorm
   float* ysq;          // [B][128 features][4 warps] their squares
   int slots;           // 8 * max_groups
+  int rows;            // features of a tile of the first phase
   int slices;          // router: CTAs per token
   int stages, stage_bytes;
 };
@@ -467,11 +468,10 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   DenseBars* bars = &m.bars;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   const int S = p.stages;
-  const int FT = (p.f + kDnHalf - 1) / kDnHalf, DT = (p.d + 2 * kDnHalf - 1) / (2 * kDnHalf);
-  const int KC1 = (p.d + kDnChunk - 1) / kDnChunk;
+  const int FT = (p.f + p.rows - 1) / p.rows, DT = (p.d + 2 * kDnHalf - 1) / (2 * kDnHalf);
+  const int KC1 = (p.d + kDnChunk - 1) / kDnChunk, KC2 = (p.f + kDnChunk - 1) / kDnChunk;
   const uint32_t ring_at = smem_addr(ring);
-  // The shared experts' tiles come first: they do not depend on the routing.
-  const Sched s0 = Sched::make(p.ns * FT, KC1, gridDim.x);
+  const uint32_t half_a = p.rows * 128;  // bytes of a chunk of gate rows, or of up rows
   int* status = &p.head->ctrl.status;
   volatile int* abort = &bars->abort;
 
@@ -491,33 +491,32 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   const uint32_t tmem = bars->tmem;
   griddep_launch_dependents();  // the next call's CTAs take the SMs that this kernel's leave
 
-  // Chunk kc of tile t of the shared or of the active routed experts, into a stage.
+  // Chunk kc of a tile of the first phase, into a stage.  The shared experts' tiles come first and stay whole:
+  // they do not depend on the routing.
   const uint64_t pw = policy_evict_first(), px = policy_evict_normal();
-  auto load_gate_up = [&](bool routed, int t, int kc, int stage) {
-    const int i = t / FT, a = p.ns + i, f0 = (t - i * FT) * kDnHalf, k = kc * kDnChunk;
-    const int z = routed ? m.act[a] : i, n4 = ((routed ? m.cnt[a] : p.B) + 3) / 4;
+  auto load_gate_up = [&](int t, int kc, int stage) {
+    const int a = t / FT, f0 = (t - a * FT) * p.rows, k = kc * kDnChunk;
+    const bool routed = a >= p.ns;
+    const int z = routed ? m.act[a] : a, n4 = ((routed ? m.cnt[a] : p.B) + 3) / 4;
     uint64_t* full = &bars->full[stage];
-    mbar_arrive_expect_tx(full, kDnBytesA + n4 * 512);
-    const uint32_t at = ring_at + stage * p.stage_bytes;
+    mbar_arrive_expect_tx(full, 2 * half_a + n4 * 512);
+    uint32_t at = ring_at + stage * p.stage_bytes;
     tma_3d(at, routed ? &maps.gate : &maps.sgate, k, f0, z, full, pw);
-    tma_3d(at + kDnBytesA / 2, routed ? &maps.up : &maps.sup, k, f0, z, full, pw);
+    tma_3d(at + half_a, routed ? &maps.up : &maps.sup, k, f0, z, full, pw);
+    at += kDnBytesA;
     if (routed) {
       const uint8_t* q = tok + m.grp[a] * 8;
-      for (int r = 0; r < n4; ++r, q += 4) tma_rows4(at + kDnBytesA + r * 512, &maps.x, k, q[0], q[1], q[2], q[3], full, px);
+      for (int r = 0; r < n4; ++r, q += 4) tma_rows4(at + r * 512, &maps.x, k, q[0], q[1], q[2], q[3], full, px);
     } else {
-      for (int r = 0; r < n4; ++r)
-        tma_rows4(at + kDnBytesA + r * 512, &maps.x, k, 4 * r, 4 * r + 1, 4 * r + 2, 4 * r + 3, full, px);
+      for (int r = 0; r < n4; ++r) tma_rows4(at + r * 512, &maps.x, k, 4 * r, 4 * r + 1, 4 * r + 2, 4 * r + 3, full, px);
     }
   };
   // Their first stages are on their way while the tokens are routed, whose scratch is the last stage.
   int sent = 0;
   if (warp == 0 && elect_one()) {
-    SegIter it(s0, cta);
-    Seg g;
-    while (sent < S - 1 && it.next(g))
-      for (int kc = g.k0; kc < g.k1 && sent < S - 1; ++kc) load_gate_up(false, g.t, kc, sent++);
+    for (int t = cta; t < p.ns * FT; t += gridDim.x)
+      for (int kc = 0; kc < KC1 && sent < S - 1; ++kc) load_gate_up(t, kc, sent++);
     // ... and the first of their down rows on the way to L2
-    const int KC2 = (p.f + kDnChunk - 1) / kDnChunk;
     for (int i = cta, n = 0; i < p.ns * DT * KC2 && n < 4; i += gridDim.x, ++n) {
       const int t = i / KC2, z = t / DT;
       for (int j = 0; j < 4; ++j)
@@ -533,9 +532,34 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   fence_proxy_async_smem();
   __syncthreads();
 
-  const Sched s1 = Sched::make((m.n_act - p.ns) * FT, KC1, gridDim.x);
-  const Sched s2 = Sched::make(m.n_act * DT, (p.f + kDnChunk - 1) / kDnChunk, gridDim.x);
+  const Sched s1 = Sched::make(m.n_act * FT, KC1, gridDim.x, p.ns * FT);
+  const Sched s2 = Sched::make(m.n_act * DT, KC2, gridDim.x, 0);
 
+  // join: every token's experts and their shares, in order.  A unit is 128 features of a token; each four
+  // warps take one at a time, the first of them lists where the token's sums lie.
+  const int grp = tid / kDnHalf, gtid = tid - grp * kDnHalf, HT = (p.d + kDnHalf - 1) / kDnHalf;
+  const int u0 = cta * kJoinGroups + grp, ustep = gridDim.x * kJoinGroups;
+  auto list_sums = [&](int u, int grp) {
+    const int b = u / HT, dt = (u - b * HT) / 2;
+    int a = 0, slot = 0, parts = 0;
+    if (lane < p.k + p.ns) {
+      a = m.place[b * kMaxPairSlots + lane];
+      slot = m.row[b * kMaxPairSlots + lane];
+      parts = s2.parts(a * DT + dt);
+    }
+    int end = parts;
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, end, off);
+      if (lane >= off) end += o;
+    }
+    for (int s = 0; s < parts; ++s) {
+      m.from[grp][end - parts + s] = ((size_t)s * p.slots + slot) * p.d;
+      m.weight[grp][end - parts + s] = lane < p.k ? m.w[b * p.k + lane] : 1.f;
+    }
+    if (lane == 15) m.n_from[grp] = end;
+    __syncwarp();
+  };
   if (!ok) {
     // no copy is in flight when the CTA ends
     for (int i = 0; i < sent; ++i)
@@ -553,25 +577,22 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       Seg g;
       bool go = true;
       int skip = sent;  // chunks that are on their way
-#pragma unroll 1
-      for (int part = 0; part < 2 && go; ++part) {
-        SegIter it(part ? s1 : s0, cta);
-        while (go && it.next(g)) {
-          for (int kc = g.k0; kc < g.k1; ++kc) {
-            if (skip > 0) {
-              --skip;
-              advance(st, ph);
-              continue;
-            }
-            if (!dn_wait(&bars->empty[st], ph ^ 1, abort)) {
-              dn_fail(bars, status);
-              go = false;
-              break;
-            }
-            load_gate_up(part != 0, g.t, kc, st);
-            ++issued;
+      SegIter it(s1, cta);
+      while (go && it.next(g)) {
+        for (int kc = g.k0; kc < g.k1; ++kc) {
+          if (skip > 0) {
+            --skip;
             advance(st, ph);
+            continue;
           }
+          if (!dn_wait(&bars->empty[st], ph ^ 1, abort)) {
+            dn_fail(bars, status);
+            go = false;
+            break;
+          }
+          load_gate_up(g.t, kc, st);
+          ++issued;
+          advance(st, ph);
         }
       }
       // second phase: the weights of the first stages are asked for before the grid's h is there
@@ -644,6 +665,10 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
         for (uint32_t w = 0; w < (*abort ? 8u : kWaitTries) && !mbar_try_wait(&bars->full[st], ph); ++w) {}
       }
     }
+  } else if (warp == 2 || warp == 3) {
+    // the join's first units are listed while the other warps work
+    for (int i = warp - 2; i < kJoinGroups; i += 2)
+      if (cta * kJoinGroups + i < p.B * HT) list_sums(cta * kJoinGroups + i, i);
   } else if (warp == 1) {
     if (elect_one()) {
       int st = 0, buf = 0;
@@ -651,12 +676,12 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       bool go = true, open = false;
       Seg g;
 #pragma unroll 1
-      for (int part = 0; part < 3 && go; ++part) {
-        const bool phase = part == 2;
-        const int TT = phase ? DT : FT, first = part == 1 ? p.ns : 0;
-        SegIter it(part == 0 ? s0 : part == 1 ? s1 : s2, cta);
+      for (int phase = 0; phase < 2 && go; ++phase) {
+        const int TT = phase ? DT : FT;
+        const uint32_t second = phase ? kDnBytesA / 2 : half_a;
+        SegIter it(phase ? s2 : s1, cta);
         while (go && it.next(g)) {
-          const int n = m.cnt[first + g.t / TT];
+          const int n = m.cnt[g.t / TT];
           const uint32_t desc = mma_desc(phase ? (n + 7) / 8 * 16 : (n + 15) / 16 * 16, p.bf16, phase);
           if (!dn_wait(&bars->tempty[buf], tph ^ 1, abort)) {
             dn_fail(bars, status);
@@ -673,7 +698,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
             }
             tc_after_sync();
             const uint32_t a = ring_at + st * p.stage_bytes;
-            dn_stage_products(a, a + kDnBytesA, d0, d0 + 128, desc, phase, kc == g.k0);
+            dn_stage_products(a, a + kDnBytesA, d0, d0 + 128, desc, phase != 0, kc == g.k0, true, second);
             mma_commit(&bars->empty[st]);
             open = true;
             if (++st == S) {
@@ -700,14 +725,8 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
     uint32_t tph = 0;
     bool go = true;
     Seg g;
-#pragma unroll 1
-    for (int part = 0; part < 2 && go; ++part) {
-      const Sched& sc = part ? s1 : s0;
-      const int first = part ? p.ns : 0;
-      // the two parts' shares have counts and places of their own
-      unsigned* counts = p.head->cnt + (part ? kDnMaxCtas / 2 : 0);
-      float* sums = p.part + (part ? (size_t)s0.segments() * kPartFloats : 0);
-      SegIter it(sc, cta);
+    {
+      SegIter it(s1, cta);
       while (it.next(g)) {
         const bool good = dn_wait(&bars->tfull[buf], tph, abort);
         if (!good) dn_fail(bars, status);
@@ -716,10 +735,11 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
           break;
         }
         tc_after_sync();
-        const int a = first + g.t / FT, feat = g.t % FT * kDnHalf + r, n = m.cnt[a], slot = m.grp[a] * 8;
+        const int a = g.t / FT, n = m.cnt[a], slot = m.grp[a] * 8;
+        const int feat = r < p.rows ? (g.t - a * FT) * p.rows + r : p.f;  // p.f: none
         const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + buf * 256;
-        const int parts = sc.parts(g.t);
-        float* mine = sums + ((size_t)(g.t - sc.dp) + cta) * kPartFloats + r;  // used where parts > 1
+        const int parts = s1.parts(g.t);
+        float* mine = p.part + ((size_t)(g.t - s1.dp) + cta) * kPartFloats + r;  // used where parts > 1
         // up to two tokens in code of their own: a kernel this short pays for every line of code it fetches
         if (n <= 2) {
           if (half == 0) {
@@ -735,8 +755,8 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
         tc_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->tempty[buf]);
-        if (parts > 1 && dn_last_share(counts + (g.t - sc.dp), parts, bars, etid) && feat < p.f) {
-          const float* from = sums + ((size_t)(g.t - sc.dp) + sc.first(g.t)) * kPartFloats + r;
+        if (parts > 1 && dn_last_share(&p.head->cnt[g.t - s1.dp], parts, bars, etid) && feat < p.f) {
+          const float* from = p.part + ((size_t)(g.t - s1.dp) + s1.first(g.t)) * kPartFloats + r;
           if (n <= 2) {
             if (half == 0) joined_h<2>(p, from, parts, slot, n, feat);
           } else {
@@ -788,32 +808,6 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   tc_after_sync();
   if (warp == 2) tmem_free(tmem, 512);
 
-  // join: every token's experts and their shares, in order.  A unit is 128 features of a token; each four
-  // warps take one at a time, the first of them lists where the token's sums lie.
-  const int grp = tid / kDnHalf, gtid = tid - grp * kDnHalf, HT = (p.d + kDnHalf - 1) / kDnHalf;
-  const int u0 = cta * kJoinGroups + grp, ustep = gridDim.x * kJoinGroups;
-  auto list_sums = [&](int u) {
-    const int b = u / HT, dt = (u - b * HT) / 2;
-    int a = 0, slot = 0, parts = 0;
-    if (lane < p.k + p.ns) {
-      a = m.place[b * kMaxPairSlots + lane];
-      slot = m.row[b * kMaxPairSlots + lane];
-      parts = s2.parts(a * DT + dt);
-    }
-    int end = parts;
-#pragma unroll
-    for (int off = 1; off < 16; off <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, end, off);
-      if (lane >= off) end += o;
-    }
-    for (int s = 0; s < parts; ++s) {
-      m.from[grp][end - parts + s] = ((size_t)s * p.slots + slot) * p.d;
-      m.weight[grp][end - parts + s] = lane < p.k ? m.w[b * p.k + lane] : 1.f;
-    }
-    if (lane == 15) m.n_from[grp] = end;
-    __syncwarp();
-  };
-  if (ok && gtid < 32 && u0 < p.B * HT) list_sums(u0);
   if (tid == 0) {
     if (!*abort) {
       grid_arrive(&p.head->bar[2]);
@@ -827,7 +821,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
     const int b = u / HT, feat = (u - b * HT) * kDnHalf + gtid;
     if (u != u0) {
       named_barrier(2 + grp, kDnHalf);
-      if (gtid < 32) list_sums(u);
+      if (gtid < 32) list_sums(u, grp);
       named_barrier(2 + grp, kDnHalf);
     }
     float acc = 0.f;
@@ -889,7 +883,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
 
 struct LayerPlan {
   int B = -1, d, f, E, k, ns, sms;
-  int groups, slices, grid;
+  int groups, slices, grid, rows;
   size_t logits, top_idx, top_w, h, part, yrow, ysq, ypart, total;
 };
 
@@ -914,17 +908,34 @@ const LayerPlan& layer_plan(int B, int d, int f, int E, int k, int ns, int sms) 
   if (B > 0 && B <= kFewTok && l.slices > 8192 / (B * E)) l.slices = 8192 / (B * E);
   if (l.slices > rows) l.slices = rows;
   if (l.slices < 1) l.slices = 1;
-  const int FT = (f + kDnHalf - 1) / kDnHalf, DT = (d + 2 * kDnHalf - 1) / (2 * kDnHalf);
+  const int DT = (d + 2 * kDnHalf - 1) / (2 * kDnHalf);
   const int KC1 = (d + kDnChunk - 1) / kDnChunk, KC2 = (f + kDnChunk - 1) / kDnChunk;
+  const int most = E < B * k ? E : B * k;
+  // Features of a tile: those with which the expected number of active experts (one token: the exact one)
+  // comes nearest to whole waves, so that no tile's sums have to be joined.
+  double miss = 1;
+  for (int b = 0; b < B; ++b) miss *= 1 - (double)k / E;
+  const int act = ns + (int)(E * (1 - miss) + 0.5);
+  double best = 1e30;
+  for (int rows = kDnHalf; rows >= 64; rows -= 8) {
+    const int FT = (f + rows - 1) / rows;
+    const Sched s = Sched::make(act * FT, KC1, sms, ns * FT);
+    // clocks of the slowest SM: a tile's chunks at its share of HBM, and 6 chunks' worth for joining
+    const double chunk = rows / 128.0, tail = s.total ? (double)s.total / sms * chunk + 6 : 0;
+    const double t = (s.dp + sms - 1) / sms * KC1 * chunk + tail;
+    if (t < best * 0.995) {
+      best = t;
+      l.rows = rows;
+    }
+  }
   // the number of active experts is known on the device only: the largest need of any
   int segs = 0, parts = 1;
-  const int most = E < B * k ? E : B * k;
+  const int FT = (f + l.rows - 1) / l.rows;
   for (int a = 0; a <= most; ++a) {
-    const Sched s1 = Sched::make(a * FT, KC1, sms), s2 = Sched::make((a + ns) * DT, KC2, sms);
+    const Sched s1 = Sched::make((a + ns) * FT, KC1, sms, ns * FT), s2 = Sched::make((a + ns) * DT, KC2, sms, 0);
     if (s1.segments() > segs) segs = s1.segments();
     if (s2.max_parts() > parts) parts = s2.max_parts();
   }
-  segs += Sched::make(ns * FT, KC1, sms).segments();
   size_t o = (sizeof(DenseHead) + 255) / 256 * 256;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -956,8 +967,8 @@ cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int s
   cudaError_t e = cudaSuccess;
   auto set_maps = [&](const DenseExpertSet& s, CUtensorMap* g, CUtensorMap* u, CUtensorMap* d) {
     if (e == cudaSuccess)
-      e = dense_map(g, s.gate_t, c.bf16, c.d, c.f, s.gate_rs, s.E, s.gate_rs * c.f, kDnHalf);
-    if (e == cudaSuccess) e = dense_map(u, s.up_t, c.bf16, c.d, c.f, s.up_rs, s.E, s.up_rs * c.f, kDnHalf);
+      e = dense_map(g, s.gate_t, c.bf16, c.d, c.f, s.gate_rs, s.E, s.gate_rs * c.f, l.rows);
+    if (e == cudaSuccess) e = dense_map(u, s.up_t, c.bf16, c.d, c.f, s.up_rs, s.E, s.up_rs * c.f, l.rows);
     if (e == cudaSuccess) e = dense_map(d, s.down, c.bf16, c.d, c.f, s.down_rs, s.E, s.down_rs * c.f, kDnChunk);
   };
   set_maps(c.routed, &maps.gate, &maps.up, &maps.down);
@@ -996,6 +1007,7 @@ cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int s
   p.yrow = reinterpret_cast<float*>(w8 + l.yrow);
   p.ysq = reinterpret_cast<float*>(w8 + l.ysq);
   p.slots = l.groups * 8;
+  p.rows = l.rows;
   p.slices = l.slices;
   p.stage_bytes = kDnBytesA + (c.B + 7) / 8 * 16 * 128;
   const int fixed = 1024 + (int)sizeof(LayerMisc) + p.slots;
