@@ -159,6 +159,11 @@ __device__ void slice_logits(const LayerArgs& p, int b, int r0, int r1, float* o
   }
 }
 
+// Token b's bit in expert e's mask, in the 32-bit half that has it.
+__device__ __forceinline__ void mark_token(LayerMisc& m, int e, int b) {
+  atomicOr(reinterpret_cast<uint32_t*>(&m.mask[e]) + (b >> 5), 1u << (b & 31));
+}
+
 // One warp: token b's logits (its slices [slices][E] added in order), its k experts by logit descending
 // (ties: the lower index; NaN ranks as -inf) and their weights.  A logit's key orders as the logit
 // does; an expert that is taken has key 0, below every logit's.  m: where to mark the choice, or null.
@@ -222,7 +227,7 @@ __device__ __forceinline__ void choose(const LayerArgs& p, int b, const float* s
     idx[b * p.k + lane] = mine_e;
     w[b * p.k + lane] = expf(mine - top) / sum;
     if (m) {
-      atomicOr(&m->mask[mine_e], 1ull << b);
+      mark_token(*m, mine_e, b);
       atomicOr(&m->on[mine_e >> 5], 1u << (mine_e & 31));
     }
   }
@@ -346,7 +351,7 @@ __device__ void make_lists(const LayerArgs& p, LayerMisc& m, uint8_t* tok) {
     __syncthreads();
     return;
   }
-  for (int i = tid; i < pairs; i += kDnThreads) atomicOr(&m.mask[m.idx[i]], 1ull << (i / p.k));
+  for (int i = tid; i < pairs; i += kDnThreads) mark_token(m, m.idx[i], i / p.k);
   __syncthreads();
   if (tid < 32) {
     if (lane < p.ns) {
