@@ -168,9 +168,11 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int bytes_a = p.both ? kDnBytesA : kDnBytesA / 2;  // of a chunk; rows behind p.rows stay unwritten
   const uint32_t chunk_bytes = bytes_a + p.NT * 128, stage_bytes = p.wide * chunk_bytes;
-  const uint32_t load_bytes = p.wide * ((p.both ? 2 : 1) * p.rows * 128 + p.NT * 128);
+  const int most = p.M < p.NT ? p.M : p.NT;  // tokens of a tile that exist
+  const int load_rows = p.kn || p.N > p.rows ? p.rows : p.N;  // boxes are no higher than the operands
+  const uint32_t load_bytes = p.wide * ((p.both ? 2 : 1) * load_rows + most) * 128;
   // partial sums that a cluster's CTAs push here: behind the stages, or in them once they are free
-  const int most = p.M < p.NT ? p.M : p.NT, g4 = (most + 3) / 4, mats = p.gated ? 2 : 1;
+  const int g4 = (most + 3) / 4, mats = p.gated ? 2 : 1;
   uint8_t* xsums = p.own_x ? ring + (size_t)p.stages * stage_bytes : ring;
   DenseBars* bars = reinterpret_cast<DenseBars*>(ring + (size_t)p.stages * stage_bytes +
                                                  (p.own_x ? (size_t)mats * g4 * 4096 : 0));
@@ -278,9 +280,9 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           tc_after_sync();
           const uint32_t a = ring_at + st * stage_bytes;
           const uint32_t d0 = tmem + buf * p.buf_cols + grp * grp_cols;
-          dn_stage_products(a, a + bytes_a, d0, d0 + NT, desc, p.kn, kc - kc0 < p.groups, p.both);
-          if (p.wide > 1)
-            dn_stage_products(a + chunk_bytes, a + chunk_bytes + bytes_a, d0, d0 + NT, desc, p.kn, false, p.both);
+          for (int c = 0; c < p.wide; ++c)
+            dn_stage_products(a + c * chunk_bytes, a + c * chunk_bytes + bytes_a, d0, d0 + NT, desc, p.kn,
+                              c == 0 && kc - kc0 < p.groups, p.both);
           mma_commit(&bars->empty[st]);
           open = true;
           if (++grp == p.groups) grp = 0;
@@ -745,15 +747,17 @@ int linear_stages(const LinearPlan& l, int M, bool gated, int smem, bool& own_x)
 // 1.9 GHz):
 //   a call costs 7000 whatever it does (256 x 512, one token: 3.8 us);
 //   an SM takes 62 bytes a clock from L2 (tiles of 128 x 128: 32 KB in 516 clocks), all SMs together
-//   3550 out of HBM, and where both are needed the lesser adds 0.15 of itself;
+//   3550 out of HBM, and where both are needed the lesser adds 0.15 of itself; rows that do not start on a
+//   line of 128 bytes take 1.7 times as long out of L2 (333 x 1024 by 128 x 32: K = 1000 8.9 us, K = 1024 7.0);
 //   a stage's bytes come 2400 after they are asked for (4096 x 4096, one token, 16 KB stages: six of them
-//   run at 383 clocks each, three 32 KB ones at 831), and a stage costs its issuing threads 330, or
-//   430 with twice the k, and 60 more for each 64 k where its rows are shorter boxes;
+//   run at 383 clocks each, three 32 KB ones at 831), and a stage costs its issuing threads 270 and for
+//   each 64 k 155 + 3 NT (2048 x 2048, 16 tokens: 64 / 128 / 256 k a stage 11.9 / 9.5 / 8.3 us), and 60 more
+//   where its rows are shorter boxes;
 //   a product of 128 x NT x 16 takes NT / 2, and a quarter more with all SMs at it (the clock drops);
 //   joining a cluster's sums 3300 and 48 for each token and product; a tile's epilogue 600 and 26 for
 //   each token and product, which runs under the next tile's products where TMEM holds both tiles;
-//   a CTA pair's stage 650 with 256 columns, and 8000 for its first and last tile (2048 x 14336 gated,
-//   K = 4096: 275 us against the model's 270; one CTA a tile 321).
+//   a CTA pair's stage 650 with 256 columns, 370 at least, and 27 a column for its last epilogue (2048 x
+//   14336 gated, K = 4096: 275 us against the model's 270; one CTA a tile 321).
 LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int sms, int smem) {
   LinearPlan best;
   double best_t = 1e30;
@@ -771,15 +775,15 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
     for (int rows = 64; rows <= kDnHalf; rows += gated || kn ? 64 : 16) {
       const int width = gated ? rows : 2 * rows, MT = (M + 255) / 256;
       const long long T = (long long)MT * ((N + width - 1) / width);
-      if (T > (1 << 30)) continue;
+      if (T > (1 << 30) || (!gated && N <= rows)) continue;
       l.pair = 1;
       l.S = 1;
       l.T = (int)T;
       l.MT = MT;
       l.rows = rows;
       const double waves = (double)((T + sms / 2 - 1) / (sms / 2)), chunk = 650.0 * rows / kDnHalf;
-      const double t = waves * chunks * (chunk > 400 ? chunk : 400);
-      keep(l, 7000 + 8000 + (t > w_bytes / hbm ? t : w_bytes / hbm));
+      const double t = waves * chunks * (chunk > 370 ? chunk : 370);
+      keep(l, 7000 + 27.0 * rows + (t > w_bytes / hbm ? t : w_bytes / hbm));
     }
   }
   auto consider = [&](int NT, int rows, int both, int wide, int S) {
@@ -793,7 +797,7 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
     l.S = S;
     const int width = gated || !both ? rows : 2 * rows, fit = clusters(S, sms);
     const long long T = (long long)((N + width - 1) / width) * l.MT;
-    if (T > (1 << 30) || (S > 1 && (T > fit || S > KC))) return;
+    if (T > (1 << 30) || (both && !gated && N <= rows) || (S > 1 && (T > fit || S > KC))) return;
     l.T = (int)T;
     bool own_x;
     const int stage = wide * ((both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128);
@@ -801,11 +805,13 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
     if (stages < 2 || (S > 1 && !own_x && linear_sum_bytes(l, M, gated) > stages * stage)) return;
     const double waves = (double)((T + fit - 1) / fit), active = (double)(T < fit ? T : fit) * S;
     const double load = wide * ((both ? 2 : 1) * rows + l.NT) * 128.0;
-    const double mma = wide * (both ? 2 : 1) * 4 * 1.25 * l.NT / 2, l2 = load / 62;
+    const double mma = wide * (both ? 2 : 1) * 4 * 1.25 * l.NT / 2;
+    const double l2 = (load + 0.7 * ((kn ? N : K) % 64 ? load - wide * l.NT * 128.0 : 0) +
+                       0.7 * (K % 64 ? wide * l.NT * 128.0 : 0)) / 62;
     // weights that several token tiles of a wave share come out of HBM once
     const double mem = (load - wide * l.NT * 128.0) * active / hbm / (T < fit ? l.MT : l.MT < waves ? 1 : l.MT / waves);
     double chunk = l2 > mem ? l2 + 0.15 * mem : mem + 0.15 * l2;
-    for (const double least : {mma, 2400.0 / stages, 230.0 + 100 * wide})
+    for (const double least : {mma, 2400.0 / stages, 270 + wide * (155 + 3.0 * l.NT)})
       if (chunk < least) chunk = least;
     if (rows < kDnHalf) chunk += 60 * wide;
     const double epi = 600 + 26.0 * l.NT * (both ? 2 : 1);
@@ -814,15 +820,15 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
                : l.NT * (both ? 2 : 1) <= 256 ? waves * (products > epi ? products : epi) + epi
                                               : waves * (products + epi);
     if (t < w_bytes / hbm) t = w_bytes / hbm;
-    if (wide > 1) t *= 0.98;  // 216 KB in flight instead of 147
+    t *= wide == 1 ? 1 : wide == 2 ? 0.98 : 0.96;  // 216 KB in flight instead of 147
     keep(l, 7000 + t);
   };
   const int top = M < 256 ? (M + 15) / 16 * 16 : 256;
   for (int both = gated ? 1 : 0; both < 2; ++both)
-    for (int rows = both && !gated ? kDnHalf : kn ? 64 : 32; rows <= kDnHalf; rows += kn ? 64 : 32)
+    for (int rows = both && !gated ? kDnHalf : kn ? 64 : 32; rows <= kDnHalf && (rows < N + 64 || rows <= 64); rows += kn ? 64 : 32)
       for (int NT = 16; NT <= top; NT += 16)
         for (int S = 1; S <= 8; S *= 2)
-          for (int wide = 1; wide <= (NT <= kFewTokens ? 2 : 1); ++wide) consider(NT, rows, both, wide, S);
+          for (int wide = 1; wide <= 4; wide *= 2) consider(NT, rows, both, wide, S);
   best.M = M;
   best.N = N;
   best.K = K;
@@ -904,12 +910,14 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   const bool few = l.NT <= kFewTokens;
   CUtensorMap mw, mw2, mx;
   const uint64_t cols = c.kn ? c.N : c.K, rows = c.kn ? c.K : c.N;
-  const uint32_t box = c.kn ? kDnChunk : l.rows;
+  // rows behind the last one would be slow to fetch where every tile has them (1542 x 18, K = 1400: 34 us
+  // with boxes of 128 rows, 10 with 18)
+  const uint32_t box = c.kn ? kDnChunk : c.N < l.rows ? c.N : l.rows;
   cudaError_t e = dense_map(&mw, c.w, c.bf16, cols, rows, c.w_stride, 0, 0, box);
   if (e != cudaSuccess) return e;
   mw2 = mw;
   if (gated) e = dense_map(&mw2, c.w_mul, c.bf16, cols, rows, c.w_mul_stride, 0, 0, box);
-  if (e == cudaSuccess) e = dense_map(&mx, c.x, c.bf16, c.K, c.M, c.K, 0, 0, l.NT);
+  if (e == cudaSuccess) e = dense_map(&mx, c.x, c.bf16, c.K, c.M, c.K, 0, 0, c.M < l.NT ? c.M : l.NT);
   if (e != cudaSuccess) return e;
   LinearArgs p;
   p.M = c.M;
