@@ -313,7 +313,8 @@ enum { MOE_W_NK = 0, MOE_W_KN = 1 };
  *              w_router), N a multiple of 8
  *   act        MOE_ACT_*: GELU by erf or by tanh, SiLU
  *   x [M][K]; y [M][N]; w_mul [as w], bias [N], bias_mul [N] (only with w_mul), residual [M][N]: NULL
- *   leaves that part out.  y may be the residual's buffer (with out_dtype = dtype), no other input's.
+ *   leaves that part out.  y may be the residual's buffer (with out_dtype = dtype); a y
+ *   that overlaps an input otherwise is refused (MOE_ERR_INVALID_ARG).
  *   With w_mul = W^up, w = W^gate and MOE_ACT_SILU this is the first half of a SwiGLU block.
  *   ws / ws_bytes: at least moe_linear_workspace_bytes(M, N, K, w_mul != NULL) bytes.
  */
@@ -347,7 +348,7 @@ typedef struct {
 /*
  * moe_expert_dense_swiglu -- one expert on n tokens (0..1048576):
  *   y[b] = (SiLU(x_b W^gate) (.) x_b W^up) W^down [+ residual[b]]
- *   x, y [n][d] of experts->dtype; residual [n][d] or NULL; y may be the residual's buffer.
+ *   x, y [n][d] of experts->dtype; residual [n][d] or NULL; y may be the residual's buffer or x's.
  *   Two products (moe_linear's kernels).  Up to 64 tokens keep h = SiLU(.) (.) . as two 16-bit values,
  *   the rounded one and the rest; with more, h is rounded to the type.  In fp16 |h| > 65504 is infinite.
  *   ws / ws_bytes: at least moe_expert_dense_workspace_bytes(n, d, f) bytes.
@@ -371,7 +372,8 @@ typedef struct {
  *   y[b] = sum_j topk_w[b][j] * E_{topk_idx[b][j]}(x[b]) + sum_s E^shared_s(x[b]) [+ residual[b]]
  * and with rmsnorm_out = 1 that divided by sqrt(mean of its squares + 1e-6).  Routing as in
  * moe_route_topk.  One kernel (a cooperative launch on every SM).
- *   x, y [B][d]; residual [B][d] or NULL; y may be the residual's buffer, not x's;
+ *   x, y [B][d]; residual [B][d] or NULL; y may be the residual's buffer; a y that overlaps x, or the
+ *   residual in part, is refused (MOE_ERR_INVALID_ARG);
  *   dbg: optional, topk_idx and topk_w only (the other members are not used).
  *   ws / ws_bytes: at least moe_layer_dense_workspace_bytes(layer, B) bytes.
  */

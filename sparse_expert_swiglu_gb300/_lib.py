@@ -596,7 +596,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
 
     x [M, K] fp16 or bf16; w (and w_mul) [N, K] ("nk": row n = output n, as gate_t) or [K, N] ("kn", as down
     and w_router); act "none", "relu", "gelu", "gelu_tanh" or "silu"; out_dtype x's (default) or torch.float32.
-    out may be the residual's tensor, no other input's."""
+    out may be the residual's tensor (with x's type), no other input's."""
     device = _dense_x(x)
     dt = x.dtype
     dtype_code = 0 if dt is torch.float16 else 1
@@ -713,7 +713,7 @@ def expert_dense_workspace_bytes(n: int, d: int, f: int) -> int:
 def expert_dense_swiglu(x: torch.Tensor, experts: DenseExperts, expert: int, residual: Optional[torch.Tensor] = None,
                         ws: Optional[Workspace] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """One uncompressed SwiGLU expert on every row of x [n, d]: (SiLU(x W^gate) * x W^up) W^down [+ residual].
-    out may be the residual's tensor."""
+    out may be the residual's tensor or x."""
     device = _dense_x(x)
     dt = x.dtype
     n = x.shape[0]

@@ -1,14 +1,15 @@
 // Shared parts of the kernels on uncompressed 16-bit weights (linear.cu, dense_layer.cu).
 //
-// Both kernels are streams of weight tiles through tcgen05: D[feature][token] +=
-// W[feature][k] x[token][k].  The weights are the 128-row operand A, so that one token
-// costs no more than 16 (the smallest N); the tokens are operand B.  One CTA per SM; a TMA
-// warp fills a ring of stages of 64 k each (A: two 128-feature tiles, 32 KB; B: up to 256
-// token rows of 128 bytes), one thread issues the products into TMEM, four warps read the
-// sums back.  Every operand is stored with the 128-byte swizzle.
+// The weights stream through tcgen05 as tiles: D[feature][token] += W[feature][k] x[token][k].  They
+// are the 128-row operand A, so that one token costs no more than 16 (the smallest N); the tokens are
+// operand B.  (Only the kernel for many tokens turns this round, linear.cu.)  One CTA per SM; a TMA warp
+// fills a ring of stages of 64 k or a multiple of it (A: one or two tiles of up to 128 features; B: token rows
+// of 128 bytes), one elected thread issues the products into TMEM, eight warps read the sums back.
+// Every operand is stored with the 128-byte swizzle.
 //
-// Tiles go to the CTAs in full waves, and the tiles that are left over are cut along k
-// into equal shares for all of them (Sched).
+// Work that does not fill the SMs is cut along k: in linear.cu a cluster's CTAs share a tile and join
+// their sums in shared memory; in the layer's one kernel the tiles behind the last full wave are cut into
+// equal shares for all CTAs, joined in global memory (Sched).
 #pragma once
 
 #include <cuda.h>

@@ -13,6 +13,12 @@ inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 inline moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
+// Whether a result of n bytes at y shares memory with an input of m bytes at p (NULL: none).
+inline bool overlaps(const void* y, size_t n, const void* p, size_t m) {
+  const uintptr_t a = (uintptr_t)y, b = (uintptr_t)p;
+  return p && a < b + m && b < a + n;
+}
+
 cudaError_t device_sizes(int& sms, int& smem) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -109,6 +115,14 @@ moe_status_t moe_linear(const moe_linear_t* op, void* ws, size_t ws_bytes, void*
   if (!aligned(op->x, 16) || !aligned(op->w, 16) || !aligned(op->w_mul, 16) || !aligned(op->bias, 16) ||
       !aligned(op->bias_mul, 16) || !aligned(op->residual, 16) || !aligned(op->y, 16) || !aligned(ws, kWsAlign))
     return MOE_ERR_ALIGNMENT;
+  const size_t out = (size_t)op->M * op->N * (op->out_dtype == MOE_F32 ? 4 : 2), wn = (size_t)op->N * op->K * 2;
+  if (overlaps(op->y, out, op->x, (size_t)op->M * op->K * 2) || overlaps(op->y, out, op->w, wn) ||
+      overlaps(op->y, out, op->w_mul, wn) || overlaps(op->y, out, op->bias, (size_t)op->N * 2) ||
+      overlaps(op->y, out, op->bias_mul, (size_t)op->N * 2))
+    return MOE_ERR_INVALID_ARG;
+  if ((op->y != op->residual || op->out_dtype != op->dtype) &&
+      overlaps(op->y, out, op->residual, (size_t)op->M * op->N * 2))
+    return MOE_ERR_INVALID_ARG;
   if (ws_bytes < linear_ws_bytes()) return MOE_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0, smem = 0;
   if (device_sizes(sms, smem) != cudaSuccess) return MOE_ERR_CUDA;
@@ -151,6 +165,8 @@ moe_status_t moe_expert_dense_swiglu(const uint16_t* x, int32_t n, const moe_den
   if (n == 0) return MOE_OK;
   if (!x || !y || !ws) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(ws, kWsAlign)) return MOE_ERR_ALIGNMENT;
+  // x is read before the first value of y is written
+  if (y != residual && overlaps(y, (size_t)n * d * 2, residual, (size_t)n * d * 2)) return MOE_ERR_INVALID_ARG;
   int sms = 0, smem = 0;
   if (device_sizes(sms, smem) != cudaSuccess) return MOE_ERR_CUDA;
   const int bf16 = experts->dtype == MOE_BF16;
@@ -207,6 +223,8 @@ moe_status_t moe_layer_dense_decode(const uint16_t* x, int32_t B, const moe_dens
   if (B == 0) return MOE_OK;
   if (!x || !y || !ws) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(ws, kWsAlign)) return MOE_ERR_ALIGNMENT;
+  const size_t bytes = (size_t)B * layer->routed.d * 2;
+  if (overlaps(y, bytes, x, bytes) || (y != residual && overlaps(y, bytes, residual, bytes))) return MOE_ERR_INVALID_ARG;
   int sms = 0, smem = 0;
   if (device_sizes(sms, smem) != cudaSuccess) return MOE_ERR_CUDA;
   const moe_dense_experts_t& r = layer->routed;

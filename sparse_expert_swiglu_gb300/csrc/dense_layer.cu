@@ -1018,9 +1018,9 @@ cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int s
   const int fixed = 1024 + (int)sizeof(LayerMisc) + p.slots;
   int S = (smem_optin - fixed) / p.stage_bytes;
   p.stages = S > kDnMaxStages ? kDnMaxStages : S;
-  if (p.stages < 3) return cudaErrorInvalidValue;
+  if (p.stages < 3 || l.grid < c.B) return cudaErrorInvalidValue;  // routing: a CTA for every token
   const size_t smem = fixed + (size_t)p.stages * p.stage_bytes;
-  e = cudaFuncSetAttribute(dense_layer_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = cudaFuncSetAttribute(dense_layer_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(l.grid);

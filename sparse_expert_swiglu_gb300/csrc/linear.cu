@@ -461,6 +461,7 @@ struct PairArgs {
   int M, N, gated, bf16, kn, act, out_f32;
   int MT, T, KC;
   int rows;         // of weights from each CTA: a multiple of 16 (with w_mul 32), <= 128
+  int sectors;      // every 16 features of a token's row start on a 32-byte boundary of y
   const void *bias, *bias_mul, *residual;
   void* y;
   DenseHead* head;
@@ -517,7 +518,7 @@ __device__ __forceinline__ void pair_store(const PairArgs& p, size_t row, int fe
       for (int i = 0; i < 8; ++i) v[8 * h + i] += from16((unsigned short)(w[i / 2] >> (16 * (i & 1))), p.bf16);
     }
   }
-  if (p.N % 16 == 0) {
+  if (p.sectors) {
     uint32_t w[8];
     if (p.out_f32) {
       float* y = reinterpret_cast<float*>(p.y) + at;
@@ -880,6 +881,7 @@ static cudaError_t launch_linear_pair(const LinearCall& c, const LinearPlan& l, 
   p.MT = l.MT;
   p.T = l.T;
   p.rows = l.rows;
+  p.sectors = c.N % 16 == 0 && (uintptr_t)c.y % 32 == 0;  // y itself may start on 16 bytes
   p.KC = (c.K + kDnChunk - 1) / kDnChunk;
   p.bias = c.bias;
   p.bias_mul = c.bias_mul;
@@ -957,8 +959,9 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   p.stream = l.MT == 1;
   const int ctas = l.S > 1 ? l.T * l.S : l.T < sms ? l.T : sms;
   const size_t smem = 1024 + (size_t)p.stages * stage + sizeof(DenseBars) + (own_x ? linear_sum_bytes(l, c.M, gated) : 0);
+  // the limit is the same in every call, so that calls of two threads do not lower each other's
   e = cudaFuncSetAttribute(few ? linear_kernel<true> : linear_kernel<false>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);

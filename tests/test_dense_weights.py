@@ -220,6 +220,21 @@ def test_linear_output_tensor_in_place_and_empty():
     assert ses.linear(c["x"].cuda()[:0], c["w"].cuda()).shape == (0, 72)
 
 
+@gpu
+@pytest.mark.parametrize("out", [F16, F32])
+@pytest.mark.parametrize("M,N,K,gated", [(2048, 4096, 256, False), (2048, 2048, 256, True), (300, 2048, 128, False),
+                                         (5, 512, 128, True)])
+def test_linear_output_on_any_16_bytes(M, N, K, gated, out):
+    c = _linear_case(M, N, K, F16, "silu", bias=True, gated=gated, residual=True, out=out)
+    y = _linear_run(c)
+    step = 128 // torch.finfo(out).bits
+    for at in range(1, 4):
+        buf = torch.full((M * N + 4 * step,), 7.0, dtype=out, device="cuda")
+        z = buf[at * step:at * step + M * N].view(M, N)
+        assert _linear_run(c, out=z) is z and torch.equal(z, y)
+        assert (buf[:at * step] == 7.0).all() and (buf[at * step + M * N:] == 7.0).all()
+
+
 # ---------------------------------------------------------------------------
 # experts and layers
 # ---------------------------------------------------------------------------
@@ -394,6 +409,8 @@ def test_outputs_in_the_residual():
         y = ses.expert_dense_swiglu(xn, c["layer"].routed, 2, residual=rn)
         z = rn.clone()
         assert ses.expert_dense_swiglu(xn, c["layer"].routed, 2, residual=z, out=z) is z and torch.equal(z, y)
+        y, z = ses.expert_dense_swiglu(xn, c["layer"].routed, 2, residual=xn), xn.clone()
+        assert ses.expert_dense_swiglu(z, c["layer"].routed, 2, residual=z, out=z) is z and torch.equal(z, y)
 
 
 @gpu
@@ -551,7 +568,10 @@ def _lin_op(**kw):
     (dict(N=(1 << 20) + 1), -2), (dict(w_layout=1, N=60), -2), (dict(w_layout=2), -1), (dict(act=5), -1), (dict(act=-1), -1),
     (dict(dtype=2), -1), (dict(out_dtype=1), -1), (dict(x=None), -1), (dict(w=None), -1), (dict(y=None), -1),
     (dict(bias_mul=0x40000), -1), (dict(x=0x10008), -3), (dict(w=0x20002), -3), (dict(y=0x30004), -3),
-    (dict(bias=0x40002), -3), (dict(residual=0x40008), -3), (dict(w_mul=0x40008), -3), (dict(M=0), 0)])
+    (dict(bias=0x40002), -3), (dict(residual=0x40008), -3), (dict(w_mul=0x40008), -3), (dict(M=0), 0),
+    (dict(y=0x10000), -1), (dict(y=0x0FE10), -1), (dict(y=0x101F0), -1), (dict(y=0x21FF0), -1),
+    (dict(w_mul=0x40000, y=0x40000), -1), (dict(bias=0x30010), -1), (dict(w_mul=0x40000, bias_mul=0x301F0), -1),
+    (dict(residual=0x30010), -1), (dict(residual=0x30000, out_dtype=2), -1)])
 def test_linear_refusals(change, status):
     lib = ses.lib()
     ws = ctypes.c_void_p(0x100000)
@@ -615,6 +635,7 @@ def test_expert_refusals():
     assert call(p, 1, ctypes.byref(ex), 0, None, p, None, 0, None) == -1
     assert call(odd, 1, ctypes.byref(ex), 0, None, p, ws, 0, None) == -3
     assert call(p, 1, ctypes.byref(ex), 0, odd, p, ws, 0, None) == -3
+    assert call(p, 4, ctypes.byref(ex), 0, ctypes.c_void_p(0x100010), p, ws, 0, None) == -1
     assert lib.moe_expert_dense_workspace_bytes(-1, 256, 512) == 0
     assert lib.moe_expert_dense_workspace_bytes(1, 250, 512) == 0
 
@@ -630,6 +651,15 @@ def test_layer_refusals(change, B, status):
     _, layer = _dense_structs(**change)
     p, ws = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x200000)
     assert ses.lib().moe_layer_dense_decode(p, B, ctypes.byref(layer), None, p, 0, None, ws, 0, None) == status
+
+
+def test_layer_refuses_outputs_in_its_inputs():
+    _, layer = _dense_structs()
+    ws = ctypes.c_void_p(0x200000)
+    for x, r, y in ((0x100000, None, 0x100000), (0x100000, None, 0x1001F0), (0x100000, 0x100000, 0x100000),
+                    (0x100000, 0x300010, 0x300000)):
+        assert ses.lib().moe_layer_dense_decode(ctypes.c_void_p(x), 1, ctypes.byref(layer), r, ctypes.c_void_p(y), 0, None,
+                                                ws, 0, None) == -1
 
 
 def test_binding_refuses_host_tensors_and_types():
