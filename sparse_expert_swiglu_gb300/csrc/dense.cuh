@@ -111,9 +111,9 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
          (1ull << 46) | (2ull << 61);
 }
 // fp32 sums, both operands fp16 (bf16 = 0) or bf16, A's rows along k (a_mn = 0) or not
-__device__ __forceinline__ uint32_t mma_desc(int n, int bf16, int a_mn) {
+__device__ __forceinline__ uint32_t mma_desc(int n, int bf16, int a_mn, int lanes = kDnHalf) {
   return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)a_mn << 15) |
-         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kDnHalf >> 4) << 24);
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(lanes >> 4) << 24);
 }
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t add) {
   asm volatile(
@@ -233,11 +233,12 @@ __device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t a, uint64_t b,
       "l"(a), "l"(b), "r"(desc), "r"(add)
       : "memory");
 }
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+// rank: of the pair's first CTA in its cluster
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, int rank = 0) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_addr(bar)),
-      "h"((uint16_t)3)
+      "h"((uint16_t)(3 << rank))
       : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* at, uint32_t cols) {
@@ -447,6 +448,8 @@ __device__ __forceinline__ void sum_shares(const float* from, size_t second, siz
 // One stage's products of both 128-feature tiles, the second one `second` bytes behind the first (or, with `both`
 // false, of the first alone).  The k steps of an
 // operand are 32 bytes apart along its rows, 2048 across them: 2 and 128 of the descriptor's units.
+// PAIR: of both CTAs of a pair.
+template <bool PAIR = false>
 __device__ __forceinline__ void dn_stage_products(uint32_t a, uint32_t b, uint32_t d0, uint32_t d1, uint32_t desc,
                                                   bool a_mn, bool first, bool both = true,
                                                   uint32_t second = kDnBytesA / 2) {
@@ -455,8 +458,13 @@ __device__ __forceinline__ void dn_stage_products(uint32_t a, uint32_t b, uint32
 #pragma unroll
   for (int ks = 0; ks < kDnChunk / 16; ++ks) {
     const uint32_t add = !(first && ks == 0);
-    mma_f16(d0, ad + ks * step, bd + ks * 2, desc, add);
-    if (both) mma_f16(d1, ad + (second >> 4) + ks * step, bd + ks * 2, desc, add);
+    if constexpr (PAIR) {
+      mma_f16_pair(d0, ad + ks * step, bd + ks * 2, desc, add);
+      if (both) mma_f16_pair(d1, ad + (second >> 4) + ks * step, bd + ks * 2, desc, add);
+    } else {
+      mma_f16(d0, ad + ks * step, bd + ks * 2, desc, add);
+      if (both) mma_f16(d1, ad + (second >> 4) + ks * step, bd + ks * 2, desc, add);
+    }
   }
 }
 

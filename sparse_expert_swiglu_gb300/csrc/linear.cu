@@ -20,7 +20,7 @@ struct LinearArgs {
   int rows;         // features of one product, <= 128
   int both;         // two products (always with w_mul)
   int wide;         // chunks of 64 k in a stage, one behind the other
-  int KC, S;        // stages of a tile, CTAs of a tile
+  int KC, S;        // stages of a tile, CTAs (or CTA pairs) that share it along k
   int split;        // y as two 16-bit rows for each token, 2 t and 2 t + 1: the rounded value and the rest
   int pairs;        // x has two such rows for each token of y
   int groups;       // accumulators of a product: stage c of a tile goes to c % groups
@@ -31,10 +31,11 @@ struct LinearArgs {
   int own_x;        // the cluster's partial sums have memory of their own, behind the stages
 };
 
+constexpr int kTogether = 8;
+
 // Tile t's feature and token tile.  Tiles that run together share operands: eight token tiles at a time go
 // through all features, so that a wave of them is about as many features as tokens.
 __device__ __forceinline__ void tile_at(int t, int T, int MT, int& ft, int& mt) {
-  constexpr int kTogether = 8;
   const int block = T / MT * kTogether, b = t / block, r = t - b * block;
   const int here = MT - b * kTogether < kTogether ? MT - b * kTogether : kTogether;
   ft = r / here;
@@ -158,19 +159,23 @@ __device__ __forceinline__ void linear_sums(uint32_t addr, int groups, int strid
   }
 }
 
-// FEW: up to kFewTokens tokens, whose epilogue takes 4 at a time: a call this short pays for every line of
-// code it fetches.
-template <bool FEW>
+// FEW: up to kFewTokens tokens and one tile for each CTA, whose epilogue takes 4 tokens at a time: a call this short
+// pays for every line of code it fetches.  PAIR: CTA pairs (cta_group::2).  A tile then has up to 256 lanes for each product, 128 in each
+// CTA, and either CTA fetches and keeps half of its tokens: with 100 to 500 tokens, where the bytes that
+// an SM can take from L2 bound the products (300 tokens of 14336 gated features of K = 4096: 72 us, 78 without).
+template <bool FEW, bool PAIR>
 __global__ void __launch_bounds__(kDnThreads, 1)
 linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mw2,
               const __grid_constant__ CUtensorMap mx, const LinearArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int bytes_a = p.both ? kDnBytesA : kDnBytesA / 2;  // of a chunk; rows behind p.rows stay unwritten
-  const uint32_t chunk_bytes = bytes_a + p.NT * 128, stage_bytes = p.wide * chunk_bytes;
+  constexpr int P = PAIR ? 2 : 1;  // CTAs that run one product
+  const uint32_t chunk_bytes = bytes_a + p.NT / P * 128, stage_bytes = p.wide * chunk_bytes;
   const int most = p.M < p.NT ? p.M : p.NT;  // tokens of a tile that exist
   const int load_rows = p.kn || p.N > p.rows ? p.rows : p.N;  // boxes are no higher than the operands
-  const uint32_t load_bytes = p.wide * ((p.both ? 2 : 1) * load_rows + most) * 128;
+  const int load_toks = p.M < p.NT / P ? p.M : p.NT / P;
+  const uint32_t load_bytes = P * p.wide * ((p.both ? 2 : 1) * load_rows + load_toks) * 128;
   // partial sums that a cluster's CTAs push here: behind the stages, or in them once they are free
   const int g4 = (most + 3) / 4, mats = p.gated ? 2 : 1;
   uint8_t* xsums = p.own_x ? ring + (size_t)p.stages * stage_bytes : ring;
@@ -178,16 +183,17 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
                                                  (p.own_x ? (size_t)mats * g4 * 4096 : 0));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int S = p.S, ns = p.stages, NT = p.NT;
-  const int rank = S > 1 ? (int)cluster_rank() : 0;
-  const int first = blockIdx.x / S, step = gridDim.x / S;  // tiles of this CTA; S > 1: one
+  const int crank = PAIR || S > 1 ? (int)cluster_rank() : 0, half_of = PAIR ? crank & 1 : 0, lead = crank - half_of;
+  const int rank = crank / P;                                              // share of k
+  const int first = blockIdx.x / (P * S), step = gridDim.x / (P * S);  // tiles of this CTA; S > 1: one
   const int kc0 = p.KC * rank / S, kc1 = p.KC * (rank + 1) / S;
-  const int width = p.gated || !p.both ? p.rows : 2 * p.rows;  // features of a tile
+  const int width = p.gated || !p.both ? p.rows : 2 * p.rows;  // features of a CTA in a tile
   int* status = &p.head->ctrl.status;
   volatile int* abort = &bars->abort;
   const uint32_t ring_at = smem_addr(ring);
 
   if (tid == 0) {
-    dn_init_bars(bars);
+    dn_init_bars(bars, P * kDnEpi / 32);
     mbar_init(&bars->xready, S);
     mbar_init(&bars->xfull, 1);
     fence_barrier_init();
@@ -195,10 +201,13 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     tma_prefetch_map(&mx);
     if (p.gated) tma_prefetch_map(&mw2);
   }
-  if (warp == 2) tmem_alloc(&bars->tmem, p.tmem_cols);
+  if (warp == 2) {
+    if (PAIR) tmem_alloc_pair(&bars->tmem, p.tmem_cols);
+    else tmem_alloc(&bars->tmem, p.tmem_cols);
+  }
   tc_before_sync();
   __syncthreads();
-  if (S > 1) cluster_sync_all();  // the barriers are there before any CTA of the cluster uses them
+  if (PAIR || S > 1) cluster_sync_all();  // the barriers are there before any CTA of the cluster uses them
   tc_after_sync();
   const uint32_t tmem = bars->tmem;
   griddep_launch_dependents();
@@ -209,13 +218,14 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
       // w is read once when one tile of tokens covers them all
       const uint64_t pw = p.stream ? policy_evict_first() : policy_evict_normal();
       const uint64_t px = policy_evict_normal();
+      const uint32_t full_at = PAIR ? peer_addr(smem_addr(&bars->full[0]), lead) : 0;
       int st = 0, issued = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int t = first; ok && t < p.T; t += step) {
         int ft, mt;
         tile_at(t, p.T, p.MT, ft, mt);
-        const int f0 = ft * width, m0 = mt * NT;
+        const int f0 = (ft * P + half_of) * width, m0 = mt * NT + half_of * (NT / P);
         const CUtensorMap* m2 = p.gated ? &mw2 : &mw;
         const int f1 = p.gated ? f0 : f0 + p.rows;
         for (int kc = kc0; kc < kc1; ++kc) {
@@ -225,21 +235,26 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
             break;
           }
           uint64_t* full = &bars->full[st];
-          mbar_arrive_expect_tx(full, load_bytes);
+          if (crank == lead) mbar_arrive_expect_tx(full, load_bytes);
           ++issued;
+          // a pair's copies count on the first CTA's barrier
+          auto copy = [&](uint32_t to, const CUtensorMap* m, int c0, int c1, uint64_t pol) {
+            if constexpr (PAIR) tma_2d_pair(to, m, c0, c1, full_at + st * 8, pol);
+            else tma_2d(to, m, c0, c1, full, pol);
+          };
           uint32_t a = ring_at + st * stage_bytes;
           for (int c = 0; c < p.wide; ++c, a += chunk_bytes) {
             const int k = (kc * p.wide + c) * kDnChunk;
             if (!p.kn) {
-              tma_2d(a, &mw, k, f0, full, pw);
-              if (p.both) tma_2d(a + kDnBytesA / 2, m2, k, f1, full, pw);
+              copy(a, &mw, k, f0, pw);
+              if (p.both) copy(a + kDnBytesA / 2, m2, k, f1, pw);
             } else {
               for (int i = 0; i < p.rows; i += 64) {
-                tma_2d(a + i * 128, &mw, f0 + i, k, full, pw);
-                if (p.both) tma_2d(a + kDnBytesA / 2 + i * 128, m2, f1 + i, k, full, pw);
+                copy(a + i * 128, &mw, f0 + i, k, pw);
+                if (p.both) copy(a + kDnBytesA / 2 + i * 128, m2, f1 + i, k, pw);
               }
             }
-            tma_2d(a + bytes_a, &mx, k, m0, full, px);
+            copy(a + bytes_a, &mx, k, m0, px);
           }
           if (++st == ns) {
             st = 0;
@@ -247,8 +262,11 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           }
         }
       }
-      // no copy of this CTA is in flight when it ends: the last stages have come
-      const int n = issued < ns ? issued : ns;
+      // No copy of this CTA is in flight when it ends: the last stages have come.  A pair has used every copy, unless
+      // it gave up: copies that no barrier of this CTA counts come long before this is over.
+      if (PAIR && *abort)
+        for (int i = 0; i < 8; ++i) __nanosleep(1000000);
+      const int n = PAIR ? 0 : issued < ns ? issued : ns;
       for (int i = 0; i < n; ++i) {
         if (--st < 0) {
           st = ns - 1;
@@ -258,14 +276,18 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
       }
     }
   } else if (warp == 1) {
-    if (elect_one()) {
-      const uint32_t desc = mma_desc(NT, p.bf16, p.kn);
+    if (crank == lead && elect_one()) {
+      const uint32_t desc = mma_desc(NT, p.bf16, p.kn, P * kDnHalf);
+      auto commit = [&](uint64_t* bar) {
+        if constexpr (PAIR) mma_commit_pair(bar, lead);
+        else mma_commit(bar);
+      };
       const int grp_cols = (p.both ? 2 : 1) * NT;
       int st = 0, buf = 0;
       uint32_t ph = 0, tph = 0;
       bool ok = true, open = false;
       for (int t = first; ok && t < p.T; t += step) {
-        if (!dn_wait(&bars->tempty[buf], tph ^ 1, abort)) {
+        if (!(PAIR ? cluster_wait(&bars->tempty[buf], tph ^ 1, abort) : dn_wait(&bars->tempty[buf], tph ^ 1, abort))) {
           dn_fail(bars, status);
           break;
         }
@@ -281,9 +303,9 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           const uint32_t a = ring_at + st * stage_bytes;
           const uint32_t d0 = tmem + buf * p.buf_cols + grp * grp_cols;
           for (int c = 0; c < p.wide; ++c)
-            dn_stage_products(a + c * chunk_bytes, a + c * chunk_bytes + bytes_a, d0, d0 + NT, desc, p.kn,
-                              c == 0 && kc - kc0 < p.groups, p.both);
-          mma_commit(&bars->empty[st]);
+            dn_stage_products<PAIR>(a + c * chunk_bytes, a + c * chunk_bytes + bytes_a, d0, d0 + NT, desc, p.kn,
+                                    c == 0 && kc - kc0 < p.groups, p.both);
+          commit(&bars->empty[st]);
           open = true;
           if (++grp == p.groups) grp = 0;
           if (++st == ns) {
@@ -292,15 +314,15 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           }
         }
         if (!ok) break;
-        mma_commit(&bars->tfull[buf]);
+        commit(&bars->tfull[buf]);
         if (++buf == p.acc_bufs) {
           buf = 0;
           tph ^= 1;
         }
       }
       if (open) {  // every product is done before TMEM is given back
-        mma_commit(&bars->drain);
-        for (uint32_t w = 0; w < kWaitTries && !mbar_try_wait(&bars->drain, 0); ++w) {}
+        commit(&bars->drain);
+        for (uint32_t w = 0; w < kWaitTries && !cluster_try_wait(&bars->drain, 0); ++w) {}
       }
     }
   } else if (warp >= 4) {
@@ -320,7 +342,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
       const int m0 = mt * NT;
       const int nt = p.M - m0 < NT ? p.M - m0 : NT;  // tokens of this tile
       if (S == 1) {
-        const int feat = ft * width + (by_tok ? 0 : half * p.rows) + row;
+        const int feat = (ft * P + half_of) * width + (by_tok ? 0 : half * p.rows) + row;
         const bool on = row < p.rows && feat < p.N;
         const float ba = p.bias && on ? ld16(p.bias, feat, p.bf16) : 0.f;
         const float bb = p.bias_mul && on ? ld16(p.bias_mul, feat, p.bf16) : 0.f;
@@ -350,14 +372,17 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         }
         tc_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->tempty[buf]);
+        if (lane == 0) {
+          if (PAIR) peer_arrive(peer_addr(smem_addr(&bars->tempty[buf]), lead));
+          else mbar_arrive(&bars->tempty[buf]);
+        }
         if (++buf == p.acc_bufs) {
           buf = 0;
           tph ^= 1;
         }
       } else {
-        // The warp pair's unit 2 q + half of sums belongs to CTA unit * S / 8: 4 tokens of a feature are 16
-        // bytes at [unit of the owner][rank][matrix][4 tokens][lane], with room for all tokens in a unit.
+        // The warp pair's unit 2 q + half of sums belongs to the share unit * S / 8's CTA with the same lanes: 4 tokens of a
+        // feature are 16 bytes at [unit of the owner][rank][matrix][4 tokens][lane], with room for all tokens in a unit.
         const uint32_t unit_bytes = mats * g4 * 512;
         const int per = 8 / S, unit = 2 * q + half;
         auto groups4 = [&](int h) {  // groups of 4 tokens that exist in a unit of half h
@@ -372,7 +397,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           for (int i = 0; i < per; ++i) bytes += S * mats * groups4((rank * per + i) & 1) * 512;
           mbar_arrive_expect_tx(&bars->xfull, bytes);
           if (!p.own_x)
-            for (int i = 0; i < S; ++i) peer_arrive(peer_addr(smem_addr(&bars->xready), i));
+            for (int i = 0; i < S; ++i) peer_arrive(peer_addr(smem_addr(&bars->xready), P * i + half_of));
         }
         if (!p.own_x) ok = ok && cluster_wait(&bars->xready, 0, abort);
         if (!ok) dn_fail(bars, status);
@@ -381,8 +406,9 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         {
           const int owner = unit / per;
           const uint32_t d0 = tmem + ((uint32_t)(q * 32) << 16) + (by_tok ? 0 : half * NT);
-          uint32_t to = peer_addr(smem_addr(xsums), owner) + ((unit - owner * per) * S + rank) * unit_bytes + lane * 16;
-          const uint32_t bar = peer_addr(smem_addr(&bars->xfull), owner);
+          const int peer = P * owner + half_of;
+          uint32_t to = peer_addr(smem_addr(xsums), peer) + ((unit - owner * per) * S + rank) * unit_bytes + lane * 16;
+          const uint32_t bar = peer_addr(smem_addr(&bars->xfull), peer);
           for (int n0 = tok0; n0 < nt; n0 += tok_step) {
 #pragma unroll 1
             for (int i = n0; i < nt && i < n0 + 16; i += W) {
@@ -404,7 +430,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         {
           // S warps for each of this CTA's units, taking its groups of 4 tokens in turn
           const int w = warp - 4, ul = w / S, u = rank * per + ul, uq = u >> 1, uh = u & 1;
-          const int feat = ft * width + (by_tok ? 0 : uh * p.rows) + uq * 32 + lane;
+          const int feat = (ft * P + half_of) * width + (by_tok ? 0 : uh * p.rows) + uq * 32 + lane;
           const bool on = uq * 32 + lane < p.rows && feat < p.N;
           const float ba = p.bias && on ? ld16(p.bias, feat, p.bf16) : 0.f;
           const float bb = p.bias_mul && on ? ld16(p.bias_mul, feat, p.bf16) : 0.f;
@@ -440,9 +466,12 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   __syncwarp();
   tc_before_sync();
   __syncthreads();
-  if (S > 1) cluster_sync_all();  // no CTA leaves while another may store into it
+  if (PAIR || S > 1) cluster_sync_all();  // no CTA leaves while another may store into it
   tc_after_sync();
-  if (warp == 2) tmem_free(tmem, p.tmem_cols);
+  if (warp == 2) {
+    if (PAIR) tmem_free_pair(tmem, p.tmem_cols);
+    else tmem_free(tmem, p.tmem_cols);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -721,7 +750,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
 
 struct LinearPlan {
   int M = -1, N = 0, K = 0, gated = 0, kn = 0, plain = 0, sms = 0;  // what it is for
-  int pair = 0, NT = 0, MT = 0, rows = 0, both = 0, wide = 1, S = 0, T = 0;
+  int by_token = 0;  // linear_pair_kernel
+  int P = 1, NT = 0, MT = 0, rows = 0, both = 0, wide = 1, S = 0, T = 0;
 };
 
 constexpr int kFewTokens = 32;
@@ -737,7 +767,7 @@ int linear_sum_bytes(const LinearPlan& l, int M, bool gated) {
 
 // Stages of a CTA, and whether the partial sums have memory behind them (up to 16 KB).
 int linear_stages(const LinearPlan& l, int M, bool gated, int smem, bool& own_x) {
-  const int stage = l.wide * ((l.both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128), sums = linear_sum_bytes(l, M, gated);
+  const int stage = l.wide * ((l.both ? kDnBytesA : kDnBytesA / 2) + l.NT / l.P * 128), sums = linear_sum_bytes(l, M, gated);
   own_x = l.S > 1 && sums <= 16384;
   const int room = smem - 1024 - (int)sizeof(DenseBars) - (own_x ? sums : 0);
   const int n = room / stage;
@@ -748,17 +778,21 @@ int linear_stages(const LinearPlan& l, int M, bool gated, int smem, bool& own_x)
 // 1.9 GHz):
 //   a call costs 7000 whatever it does (256 x 512, one token: 3.8 us);
 //   an SM takes 62 bytes a clock from L2 (tiles of 128 x 128: 32 KB in 516 clocks), all SMs together
-//   3550 out of HBM, and where both are needed the lesser adds 0.15 of itself; rows that do not start on a
-//   line of 128 bytes take 1.7 times as long out of L2 (333 x 1024 by 128 x 32: K = 1000 8.9 us, K = 1024 7.0);
-//   a stage's bytes come 2400 after they are asked for (4096 x 4096, one token, 16 KB stages: six of them
+//   3550 out of HBM, and where both are needed the lesser adds 0.15 of itself; rows that do not start
+//   on a line of 128 bytes take 1.35 times as long out of L2, and 1.8 times where they start inside a sector of
+//   32 (333 x 1024 by 128 x 32: K = 1000 8.9 us, K = 1024 7.0; 1017 x 7760 gated, K = 3280, pairs with 64 and 128 columns:
+//   537 and 704 clocks a stage instead of 370 and 650);
+//   a stage's bytes start to come 1950 after they are asked for (4096 x 4096, one token, 16 KB stages: six of them
 //   run at 383 clocks each, three 32 KB ones at 831), and a stage costs its issuing threads 270 and for
 //   each 64 k 155 + 3 NT (2048 x 2048, 16 tokens: 64 / 128 / 256 k a stage 11.9 / 9.5 / 8.3 us), and 60 more
 //   where its rows are shorter boxes;
 //   a product of 128 x NT x 16 takes NT / 2, and a quarter more with all SMs at it (the clock drops);
-//   joining a cluster's sums 3300 and 48 for each token and product; a tile's epilogue 600 and 26 for
+//   joining a cluster's sums 3300 and 48 for each token and product; a tile's epilogue 1500 and 18 for
 //   each token and product, which runs under the next tile's products where TMEM holds both tiles;
-//   a CTA pair's stage 650 with 256 columns, 370 at least, and 27 a column for its last epilogue (2048 x
-//   14336 gated, K = 4096: 275 us against the model's 270; one CTA a tile 321).
+//   a CTA pair's stage 650 with 256 columns, and 27 a column for its last epilogue, and HBM
+//   adds 0.25 of the weights' time (2048 x 14336 gated, K = 4096: 275 us against the model's 279; one CTA a
+//   tile 321; 300 tokens 80 and 80); 90 a column for the others,
+//   which run under the next tile's products (384 x 7808 gated, GELU, K = 120: 7200 for 64 columns).
 LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int sms, int smem) {
   LinearPlan best;
   double best_t = 1e30;
@@ -770,6 +804,8 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
       best = l;
     }
   };
+  auto slow = [](int row) { return row % 64 == 0 ? 1.0 : row % 16 == 0 ? 1.35 : 1.8; };
+  const double slow_x = slow(K), slow_w = slow(kn ? N : K);
   LinearPlan l;
   if (plain && N % 8 == 0 && M > 64) {
     // [K][N] weights come in boxes of 64 columns: narrower tiles would start inside a line
@@ -777,46 +813,49 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
       const int width = gated ? rows : 2 * rows, MT = (M + 255) / 256;
       const long long T = (long long)MT * ((N + width - 1) / width);
       if (T > (1 << 30) || (!gated && N <= rows)) continue;
-      l.pair = 1;
+      l.by_token = 1;
       l.S = 1;
       l.T = (int)T;
       l.MT = MT;
       l.rows = rows;
       const double waves = (double)((T + sms / 2 - 1) / (sms / 2)), chunk = 650.0 * rows / kDnHalf;
-      const double t = waves * chunks * (chunk > 370 ? chunk : 370);
-      keep(l, 7000 + 27.0 * rows + (t > w_bytes / hbm ? t : w_bytes / hbm));
+      const double l2 = (kDnHalf * slow_x + rows * slow_w) * 128 / 62;
+      const double products = chunks * (chunk > l2 ? chunk : l2), epi = 90.0 * rows;
+      const double t = waves * (products > epi ? products : epi);
+      const double mem = w_bytes / hbm;
+      keep(l, 7000 + 27.0 * rows + (t > mem ? t + 0.25 * mem : mem + 0.25 * t));
     }
   }
-  auto consider = [&](int NT, int rows, int both, int wide, int S) {
-    l.pair = 0;
+  auto consider = [&](int P, int NT, int rows, int both, int wide, int S) {
+    l.by_token = 0;
+    l.P = P;
     l.wide = wide;
     const int KC = (chunks + wide - 1) / wide;
     l.MT = (M + NT - 1) / NT;
-    l.NT = ((M + l.MT - 1) / l.MT + 15) / 16 * 16;
+    l.NT = ((M + l.MT - 1) / l.MT + 16 * P - 1) / (16 * P) * 16 * P;
     l.rows = rows;
     l.both = both;
     l.S = S;
-    const int width = gated || !both ? rows : 2 * rows, fit = clusters(S, sms);
+    const int width = P * (gated || !both ? rows : 2 * rows), fit = clusters(P * S, sms), toks = l.NT / P;
     const long long T = (long long)((N + width - 1) / width) * l.MT;
-    if (T > (1 << 30) || (both && !gated && N <= rows) || (S > 1 && (T > fit || S > KC))) return;
+    if (T > (1 << 30) || (both && !gated && N <= rows) || (P > 1 && N <= width / 2) || (S > 1 && (T > fit || S > KC))) return;
     l.T = (int)T;
     bool own_x;
-    const int stage = wide * ((both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128);
+    const int stage = wide * ((both ? kDnBytesA : kDnBytesA / 2) + toks * 128);
     const int stages = linear_stages(l, M, gated, smem, own_x);
     if (stages < 2 || (S > 1 && !own_x && linear_sum_bytes(l, M, gated) > stages * stage)) return;
-    const double waves = (double)((T + fit - 1) / fit), active = (double)(T < fit ? T : fit) * S;
-    const double load = wide * ((both ? 2 : 1) * rows + l.NT) * 128.0;
+    const double waves = (double)((T + fit - 1) / fit), active = (double)(T < fit ? T : fit) * S * P;
+    const double load = wide * ((both ? 2 : 1) * rows + toks) * 128.0, w_load = load - wide * toks * 128.0;
     const double mma = wide * (both ? 2 : 1) * 4 * 1.25 * l.NT / 2;
-    const double l2 = (load + 0.7 * ((kn ? N : K) % 64 ? load - wide * l.NT * 128.0 : 0) +
-                       0.7 * (K % 64 ? wide * l.NT * 128.0 : 0)) / 62;
-    // weights that several token tiles of a wave share come out of HBM once
-    const double mem = (load - wide * l.NT * 128.0) * active / hbm / (T < fit ? l.MT : l.MT < waves ? 1 : l.MT / waves);
+    const double l2 = (w_load * slow_w + (load - w_load) * slow_x) / 62;
+    // weights that several token tiles share come out of HBM once: those tiles run together
+    const double mem = w_load * active / hbm / (l.MT < kTogether ? l.MT : kTogether);
     double chunk = l2 > mem ? l2 + 0.15 * mem : mem + 0.15 * l2;
-    for (const double least : {mma, 2400.0 / stages, 270 + wide * (155 + 3.0 * l.NT)})
+    for (const double least : {mma, (1950 + l2 + mma) / stages, 270 + wide * (155 + 3.0 * toks)})
       if (chunk < least) chunk = least;
     if (rows < kDnHalf) chunk += 60 * wide;
-    const double epi = 600 + 26.0 * l.NT * (both ? 2 : 1);
-    const double products = ((KC + S - 1) / S) * chunk;
+    const double epi = 1500 + 18.0 * l.NT * (both ? 2 : 1);
+    const double products = (((KC + S - 1) / S) * chunk + (l2 + mma) / 2) * (P == 2 ? 1.1 : 1);
     double t = S > 1 ? products + 3300 + 48.0 * l.NT * (both ? 2 : 1)
                : l.NT * (both ? 2 : 1) <= 256 ? waves * (products > epi ? products : epi) + epi
                                               : waves * (products + epi);
@@ -829,7 +868,10 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
     for (int rows = both && !gated ? kDnHalf : kn ? 64 : 32; rows <= kDnHalf && (rows < N + 64 || rows <= 64); rows += kn ? 64 : 32)
       for (int NT = 16; NT <= top; NT += 16)
         for (int S = 1; S <= 8; S *= 2)
-          for (int wide = 1; wide <= 4; wide *= 2) consider(NT, rows, both, wide, S);
+          for (int wide = 1; wide <= 4; wide *= 2) {
+            consider(1, NT, rows, both, wide, S);
+            if (M > 64 && NT % 32 == 0 && S <= 4) consider(2, NT, rows, both, wide, S);
+          }
   best.M = M;
   best.N = N;
   best.K = K;
@@ -908,8 +950,7 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   const bool gated = c.w_mul != nullptr;
   const LinearPlan& l = linear_plan(c.M, c.N, c.K, gated, c.kn, !c.split && !c.pairs, sms, smem_optin);
   if (!l.S) return cudaErrorInvalidValue;
-  if (l.pair) return launch_linear_pair(c, l, ws, sms, st);
-  const bool few = l.NT <= kFewTokens;
+  if (l.by_token) return launch_linear_pair(c, l, ws, sms, st);
   CUtensorMap mw, mw2, mx;
   const uint64_t cols = c.kn ? c.N : c.K, rows = c.kn ? c.K : c.N;
   // rows behind the last one would be slow to fetch where every tile has them (1542 x 18, K = 1400: 34 us
@@ -919,7 +960,7 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   if (e != cudaSuccess) return e;
   mw2 = mw;
   if (gated) e = dense_map(&mw2, c.w_mul, c.bf16, cols, rows, c.w_mul_stride, 0, 0, box);
-  if (e == cudaSuccess) e = dense_map(&mx, c.x, c.bf16, c.K, c.M, c.K, 0, 0, c.M < l.NT ? c.M : l.NT);
+  if (e == cudaSuccess) e = dense_map(&mx, c.x, c.bf16, c.K, c.M, c.K, 0, 0, c.M < l.NT / l.P ? c.M : l.NT / l.P);
   if (e != cudaSuccess) return e;
   LinearArgs p;
   p.M = c.M;
@@ -944,11 +985,11 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   p.residual = c.residual;
   p.y = c.y;
   p.head = reinterpret_cast<DenseHead*>(ws);
-  const int stage = l.wide * ((l.both ? kDnBytesA : kDnBytesA / 2) + l.NT * 128), cols_of = (l.both ? 2 : 1) * l.NT;
+  const int stage = l.wide * ((l.both ? kDnBytesA : kDnBytesA / 2) + l.NT / l.P * 128), cols_of = (l.both ? 2 : 1) * l.NT;
   bool own_x;
   p.stages = linear_stages(l, c.M, gated, smem_optin, own_x);
   p.own_x = own_x;
-  p.acc_bufs = cols_of <= 256 && l.S == 1 && l.T > sms ? 2 : 1;  // two where a CTA has more than one tile
+  p.acc_bufs = cols_of <= 256 && l.S == 1 && l.T > sms / l.P ? 2 : 1;  // two where a CTA has more than one tile
   // fp32 results: several accumulators, so that each adds up fewer products (the tensor core's
   // additions cut off; K = 4096 in one row costs 3e-6 of the result, in eight 6e-7)
   p.groups = 1;
@@ -957,11 +998,12 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   p.tmem_cols = 32;
   while (p.tmem_cols < p.buf_cols * p.acc_bufs) p.tmem_cols *= 2;
   p.stream = l.MT == 1;
-  const int ctas = l.S > 1 ? l.T * l.S : l.T < sms ? l.T : sms;
+  const int ctas = l.P * (l.S > 1 ? l.T * l.S : l.T < sms / l.P ? l.T : sms / l.P);
   const size_t smem = 1024 + (size_t)p.stages * stage + sizeof(DenseBars) + (own_x ? linear_sum_bytes(l, c.M, gated) : 0);
   // the limit is the same in every call, so that calls of two threads do not lower each other's
-  e = cudaFuncSetAttribute(few ? linear_kernel<true> : linear_kernel<false>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin);
+  const auto kernel = l.P == 2 ? linear_kernel<false, true>
+                      : l.NT <= kFewTokens && l.S * l.T <= sms ? linear_kernel<true, false> : linear_kernel<false, false>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
@@ -972,13 +1014,12 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = l.S;
+  attr[1].val.clusterDim.x = l.P * l.S;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = l.S > 1 ? 2 : 1;
-  return few ? cudaLaunchKernelEx(&cfg, linear_kernel<true>, mw, mw2, mx, p)
-             : cudaLaunchKernelEx(&cfg, linear_kernel<false>, mw, mw2, mx, p);
+  cfg.numAttrs = l.P * l.S > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, mw, mw2, mx, p);
 }
 
 }  // namespace sesg

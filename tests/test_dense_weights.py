@@ -221,6 +221,16 @@ def test_linear_output_tensor_in_place_and_empty():
 
 
 @gpu
+@pytest.mark.parametrize("M,N,K,gated,layout,out", [
+    (128, 4096, 4096, False, "nk", None), (86, 4420, 2176, True, "nk", None), (592, 744, 6104, False, "kn", None),
+    (384, 7808, 120, True, "kn", None), (1421, 6484, 1000, False, "nk", None), (300, 14336, 512, True, "nk", None),
+    (128, 4096, 4096, False, "nk", F32), (592, 744, 6104, True, "kn", F32), (97, 2056, 1304, False, "kn", None)])
+def test_linear_of_cta_pairs_with_halved_tokens(M, N, K, gated, layout, out):
+    _linear_check(_linear_case(M, N, K, BF16, "silu" if gated else "none", bias=True, gated=gated, residual=True,
+                               layout=layout, out=out))
+
+
+@gpu
 @pytest.mark.parametrize("out", [F16, F32])
 @pytest.mark.parametrize("M,N,K,gated", [(2048, 4096, 256, False), (2048, 2048, 256, True), (300, 2048, 128, False),
                                          (5, 512, 128, True)])
