@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -61,6 +62,9 @@ class _DenseLayer(ctypes.Structure):
 class _Linear(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "dtype", "out_dtype", "w_layout", "act")] + \
                [(n, ctypes.c_void_p) for n in ("x", "w", "w_mul", "bias", "bias_mul", "residual", "y")]
+
+
+_LINEAR = struct.Struct("@7i7P").pack  # the same as bytes: filled in half the time
 
 
 _LIB = None
@@ -118,7 +122,7 @@ _SIGS = {
                                                ctypes.c_void_p]),
     "moe_expert_cache_contents": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "moe_linear_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 4),
-    "moe_linear": (ctypes.c_int, [ctypes.POINTER(_Linear), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_linear": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "moe_expert_dense_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 3),
     "moe_expert_dense_swiglu": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(_DenseExperts),
                                                ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
@@ -628,16 +632,16 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     else:
         y = out
         yp = _dense_in(out, out_dtype, device, (M, N), "out")
-    op = _Linear(M, N, K, dtype_code, out_code, layout_code, act_code,
+    op = _LINEAR(M, N, K, dtype_code, out_code, layout_code, act_code,
                  x.data_ptr(), _dense_in(w, dt, device, wshape, "w"),
-                 None if w_mul is None else _dense_in(w_mul, dt, device, wshape, "w_mul"),
-                 None if bias is None else _dense_in(bias, dt, device, (N,), "bias"),
-                 None if bias_mul is None else _dense_in(bias_mul, dt, device, (N,), "bias_mul"),
-                 None if residual is None else _dense_in(residual, dt, device, (M, N), "residual"), yp)
+                 0 if w_mul is None else _dense_in(w_mul, dt, device, wshape, "w_mul"),
+                 0 if bias is None else _dense_in(bias, dt, device, (N,), "bias"),
+                 0 if bias_mul is None else _dense_in(bias_mul, dt, device, (N,), "bias_mul"),
+                 0 if residual is None else _dense_in(residual, dt, device, (M, N), "residual"), yp)
     if M == 0:
         return y
     ws = _dense_ws(ws, device, linear_workspace_bytes, M, N, K, w_mul is not None)
-    status = (_LIB or lib()).moe_linear(ctypes.byref(op), ws.buf.data_ptr(), ws.nbytes, _stream_of(device))
+    status = (_LIB or lib()).moe_linear(op, ws.buf.data_ptr(), ws.nbytes, _stream_of(device))
     if status:
         raise MoeError("moe_linear", status)
     return y

@@ -1020,7 +1020,8 @@ cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int s
   p.stages = S > kDnMaxStages ? kDnMaxStages : S;
   if (p.stages < 3 || l.grid < c.B) return cudaErrorInvalidValue;  // routing: a CTA for every token
   const size_t smem = fixed + (size_t)p.stages * p.stage_bytes;
-  e = cudaFuncSetAttribute(dense_layer_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin);
+  static std::atomic<uint64_t> allowed{0};
+  e = allow_shared(dense_layer_kernel, allowed, smem_optin);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(l.grid);

@@ -1,6 +1,8 @@
 // Parameter blocks and launchers of the kernels on uncompressed weights.
 #pragma once
 
+#include <atomic>
+
 #include "params.cuh"
 
 namespace sesg {
@@ -19,6 +21,17 @@ struct LinearCall {
 };
 
 size_t linear_ws_bytes();
+// Lets a kernel have all of an SM's shared memory; `done` keeps the devices (the first 64) that know it.
+template <typename Kernel>
+cudaError_t allow_shared(Kernel* kernel, std::atomic<uint64_t>& done, int smem_optin) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done.load(std::memory_order_acquire) >> dev & 1)) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+  return e;
+}
+
 cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin, cudaStream_t st);
 
 struct DenseExpertSet {

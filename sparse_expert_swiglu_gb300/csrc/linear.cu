@@ -901,7 +901,8 @@ constexpr size_t kHeadBytes = (sizeof(DenseHead) + 255) / 256 * 256;
 
 size_t linear_ws_bytes() { return kHeadBytes; }
 
-static cudaError_t launch_linear_pair(const LinearCall& c, const LinearPlan& l, void* ws, int sms, cudaStream_t st) {
+static cudaError_t launch_linear_pair(const LinearCall& c, const LinearPlan& l, void* ws, int sms, int smem_optin,
+                                      cudaStream_t st) {
   const bool gated = c.w_mul != nullptr;
   CUtensorMap mw, mw2, mx;
   const uint64_t cols = c.kn ? c.N : c.K, rows = c.kn ? c.K : c.N;
@@ -931,7 +932,8 @@ static cudaError_t launch_linear_pair(const LinearCall& c, const LinearPlan& l, 
   p.y = c.y;
   p.head = reinterpret_cast<DenseHead*>(ws);
   const size_t smem = 1024 + (size_t)kPairStages * kPairStage + sizeof(DenseBars);
-  e = cudaFuncSetAttribute(linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> allowed{0};
+  e = allow_shared(linear_pair_kernel, allowed, smem_optin);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (p.T < sms / 2 ? p.T : sms / 2));
@@ -950,7 +952,7 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   const bool gated = c.w_mul != nullptr;
   const LinearPlan& l = linear_plan(c.M, c.N, c.K, gated, c.kn, !c.split && !c.pairs, sms, smem_optin);
   if (!l.S) return cudaErrorInvalidValue;
-  if (l.by_token) return launch_linear_pair(c, l, ws, sms, st);
+  if (l.by_token) return launch_linear_pair(c, l, ws, sms, smem_optin, st);
   CUtensorMap mw, mw2, mx;
   const uint64_t cols = c.kn ? c.N : c.K, rows = c.kn ? c.K : c.N;
   // rows behind the last one would be slow to fetch where every tile has them (1542 x 18, K = 1400: 34 us
@@ -1000,10 +1002,10 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   p.stream = l.MT == 1;
   const int ctas = l.P * (l.S > 1 ? l.T * l.S : l.T < sms / l.P ? l.T : sms / l.P);
   const size_t smem = 1024 + (size_t)p.stages * stage + sizeof(DenseBars) + (own_x ? linear_sum_bytes(l, c.M, gated) : 0);
-  // the limit is the same in every call, so that calls of two threads do not lower each other's
-  const auto kernel = l.P == 2 ? linear_kernel<false, true>
-                      : l.NT <= kFewTokens && l.S * l.T <= sms ? linear_kernel<true, false> : linear_kernel<false, false>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin);
+  static std::atomic<uint64_t> allowed[3];
+  const int which = l.P == 2 ? 2 : l.NT <= kFewTokens && l.S * l.T <= sms ? 1 : 0;
+  const auto kernel = which == 2 ? linear_kernel<false, true> : which ? linear_kernel<true, false> : linear_kernel<false, false>;
+  e = allow_shared(kernel, allowed[which], smem_optin);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
