@@ -77,15 +77,15 @@ struct LayerMisc {
   int n_from[kJoinGroups];
 };
 
-// Arrive at / wait for barrier i over the grid.  All CTAs are resident (cooperative launch).
+// Arrive at / wait for n CTAs at a barrier over the grid.  All CTAs are resident (cooperative launch).
 __device__ __forceinline__ void grid_arrive(unsigned* bar) {
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(bar) : "memory");
 }
-__device__ __forceinline__ bool grid_wait(unsigned* bar, volatile int* abort) {
+__device__ __forceinline__ bool grid_wait(unsigned* bar, unsigned n, volatile int* abort) {
   for (int i = 0; i < (1 << 22); ++i) {
     unsigned v;
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(bar) : "memory");
-    if (v >= gridDim.x) return true;
+    if (v >= n) return true;
     if (*abort) return false;
   }
   return false;
@@ -282,8 +282,8 @@ __device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
     }
   }
   if (tid == 0) {
-    grid_arrive(&p.head->bar[0]);
-    m.fail = !grid_wait(&p.head->bar[0], &m.bars.abort);
+    if (cta < p.B * p.slices) grid_arrive(&p.head->bar[0]);
+    m.fail = !grid_wait(&p.head->bar[0], p.B * p.slices, &m.bars.abort);
   }
   __syncthreads();
   if (m.fail) return false;
@@ -645,7 +645,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
         if (!go) break;
         if (!waited) {
           waited = true;
-          if (!grid_wait(&p.head->bar[1], abort)) {
+          if (!grid_wait(&p.head->bar[1], gridDim.x, abort)) {
             dn_fail(bars, status);
             break;
           }
@@ -816,7 +816,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   if (tid == 0) {
     if (!*abort) {
       grid_arrive(&p.head->bar[2]);
-      if (!grid_wait(&p.head->bar[2], abort)) dn_fail(bars, status);
+      if (!grid_wait(&p.head->bar[2], gridDim.x, abort)) dn_fail(bars, status);
     }
     m.fail = *abort;
   }
@@ -858,7 +858,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
     __syncthreads();
     if (tid == 0) {
       grid_arrive(&p.head->bar[3]);
-      if (!grid_wait(&p.head->bar[3], abort)) dn_fail(bars, status);
+      if (!grid_wait(&p.head->bar[3], gridDim.x, abort)) dn_fail(bars, status);
       m.fail = *abort;
     }
     __syncthreads();
