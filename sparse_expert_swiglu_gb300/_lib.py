@@ -64,7 +64,10 @@ class _Linear(ctypes.Structure):
                [(n, ctypes.c_void_p) for n in ("x", "w", "w_mul", "bias", "bias_mul", "residual", "y")]
 
 
-_LINEAR = struct.Struct("@7i7P").pack  # the same as bytes: filled in half the time
+# the same as bytes, which are filled in half the time
+_LINEAR = struct.Struct("@7i7P").pack
+_DENSE_EXPERTS = struct.Struct("@4i3P").pack
+_DENSE_LAYER = struct.Struct("@2iP4i3P4i3P").pack
 
 
 _LIB = None
@@ -124,11 +127,11 @@ _SIGS = {
     "moe_linear_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 4),
     "moe_linear": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "moe_expert_dense_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 3),
-    "moe_expert_dense_swiglu": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(_DenseExperts),
+    "moe_expert_dense_swiglu": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
                                                ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                                ctypes.c_size_t, ctypes.c_void_p]),
-    "moe_layer_dense_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(_DenseLayer), ctypes.c_int32]),
-    "moe_layer_dense_decode": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(_DenseLayer),
+    "moe_layer_dense_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_int32]),
+    "moe_layer_dense_decode": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
                                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                               ctypes.POINTER(_Debug), ctypes.c_void_p, ctypes.c_size_t,
                                               ctypes.c_void_p]),
@@ -669,7 +672,18 @@ class DenseExperts:
         return self.gate_t.shape[2]
 
     def c_struct(self) -> _DenseExperts:
-        g, dn = self.gate_t, self.down
+        return _DenseExperts(*self._args())
+
+    def _args(self):
+        """The members of the C structure, in its order: shapes, types, devices and strides checked."""
+        g, u, dn = self.gate_t, self.up_t, self.down
+        if isinstance(g, torch.Tensor) and isinstance(u, torch.Tensor) and isinstance(dn, torch.Tensor):
+            dt, shape, device = g.dtype, g.shape, g.get_device()
+            if (len(shape) == 3 and device >= 0 and (dt is torch.float16 or dt is torch.bfloat16) and u.dtype is dt
+                    and dn.dtype is dt and u.shape == shape and dn.shape == shape and u.get_device() == device
+                    and dn.get_device() == device and g.is_contiguous() and u.is_contiguous() and dn.is_contiguous()):
+                E, f, d = shape
+                return E, d, f, 0 if dt is torch.float16 else 1, g.data_ptr(), u.data_ptr(), dn.data_ptr()
         if not isinstance(g, torch.Tensor) or g.dim() != 3:
             raise ValueError("gate_t must have shape [E, f, d]")
         dt, shape, device = g.dtype, g.shape, g.get_device()
@@ -684,8 +698,7 @@ class DenseExperts:
             gp, dp = g.data_ptr(), dn.data_ptr()  # interleaved
         else:
             gp, dp = _dense_in(g, dt, device, shape, "gate_t"), _dense_in(dn, dt, device, shape, "down")
-        return _DenseExperts(E, d, f, 0 if dt is torch.float16 else 1, gp,
-                             _dense_in(self.up_t, dt, device, shape, "up_t"), dp)
+        return E, d, f, 0 if dt is torch.float16 else 1, gp, _dense_in(u, dt, device, shape, "up_t"), dp
 
 
 @dataclass
@@ -698,16 +711,20 @@ class DenseLayer:
     shared: Optional[DenseExperts] = None
 
     def c_struct(self) -> _DenseLayer:
-        r = self.routed.c_struct()
+        return _DenseLayer.from_buffer_copy(self._pack())
+
+    def _pack(self) -> bytes:
+        """The C structure, as bytes."""
+        r = self.routed._args()
         g = self.routed.gate_t
-        wr = _dense_in(self.w_router, g.dtype, g.get_device(), (r.d, r.E), "w_router")
+        wr = _dense_in(self.w_router, g.dtype, g.get_device(), (r[1], r[0]), "w_router")
         if self.shared is None:
-            s = _DenseExperts(0, r.d, r.f, r.dtype, None, None, None)
+            s = (0, r[1], r[2], r[3], 0, 0, 0)
         else:
-            s = self.shared.c_struct()
+            s = self.shared._args()
             if self.shared.gate_t.get_device() != g.get_device():
                 raise ValueError("shared experts must be on the routed experts' device")
-        return _DenseLayer(self.k, 1 if self.renorm else 0, wr, r, s)
+        return _DENSE_LAYER(self.k, 1 if self.renorm else 0, wr, *r, *s)
 
 
 def expert_dense_workspace_bytes(n: int, d: int, f: int) -> int:
@@ -721,11 +738,12 @@ def expert_dense_swiglu(x: torch.Tensor, experts: DenseExperts, expert: int, res
     device = _dense_x(x)
     dt = x.dtype
     n = x.shape[0]
-    ex = experts.c_struct()
+    ex = experts._args()
     if experts.gate_t.dtype != dt or experts.gate_t.get_device() != device:
         raise ValueError("x and the experts must have one type and device")
-    shape = (n, ex.d)
-    if x.shape[1] != ex.d:
+    d, f = ex[1], ex[2]
+    shape = (n, d)
+    if x.shape[1] != d:
         raise ValueError(f"x must have shape {shape}, got {tuple(x.shape)}")
     rp = None if residual is None else _dense_in(residual, dt, device, shape, "residual")
     if out is None:
@@ -735,8 +753,8 @@ def expert_dense_swiglu(x: torch.Tensor, experts: DenseExperts, expert: int, res
         _dense_in(out, dt, device, shape, "out")
     if n == 0:
         return y
-    ws = _dense_ws(ws, device, expert_dense_workspace_bytes, n, ex.d, ex.f)
-    status = (_LIB or lib()).moe_expert_dense_swiglu(x.data_ptr(), n, ctypes.byref(ex), expert, rp, y.data_ptr(),
+    ws = _dense_ws(ws, device, expert_dense_workspace_bytes, n, d, f)
+    status = (_LIB or lib()).moe_expert_dense_swiglu(x.data_ptr(), n, _DENSE_EXPERTS(*ex), expert, rp, y.data_ptr(),
                                                      ws.buf.data_ptr(), ws.nbytes, _stream_of(device))
     if status:
         raise MoeError("moe_expert_dense_swiglu", status)
@@ -744,7 +762,7 @@ def expert_dense_swiglu(x: torch.Tensor, experts: DenseExperts, expert: int, res
 
 
 def layer_dense_workspace_bytes(layer: DenseLayer, B: int) -> int:
-    return int(lib().moe_layer_dense_workspace_bytes(ctypes.byref(layer.c_struct()), B))
+    return int(lib().moe_layer_dense_workspace_bytes(layer._pack(), B))
 
 
 def layer_dense_decode(x: torch.Tensor, layer: DenseLayer, residual: Optional[torch.Tensor] = None, rmsnorm: bool = False,
@@ -755,7 +773,7 @@ def layer_dense_decode(x: torch.Tensor, layer: DenseLayer, residual: Optional[to
     device = _dense_x(x)
     dt = x.dtype
     B = x.shape[0]
-    c = layer.c_struct()
+    c = layer._pack()
     if layer.routed.gate_t.dtype != dt or layer.routed.gate_t.get_device() != device:
         raise ValueError("x and the experts must have one type and device")
     d = layer.routed.gate_t.shape[2]
@@ -775,7 +793,7 @@ def layer_dense_decode(x: torch.Tensor, layer: DenseLayer, residual: Optional[to
         dbg = ctypes.byref(_Debug(_ptr(dt_["topk_idx"]), _ptr(dt_["topk_w"]), None, None, None))
     if B:
         ws = _dense_ws(ws, device, layer_dense_workspace_bytes, layer, B)
-        status = (_LIB or lib()).moe_layer_dense_decode(x.data_ptr(), B, ctypes.byref(c), rp, y.data_ptr(), 1 if rmsnorm else 0,
+        status = (_LIB or lib()).moe_layer_dense_decode(x.data_ptr(), B, c, rp, y.data_ptr(), 1 if rmsnorm else 0,
                                                         dbg, ws.buf.data_ptr(), ws.nbytes, _stream_of(device))
         if status:
             raise MoeError("moe_layer_dense_decode", status)
