@@ -291,6 +291,12 @@ __device__ __forceinline__ void peer_store(uint32_t to, const float* v, uint32_t
                "r"(__float_as_uint(v[3])), "r"(bar)
                : "memory");
 }
+// ... and not counted
+__device__ __forceinline__ void peer_store(uint32_t to, const float* v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(__float_as_uint(v[0])),
+               "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3]))
+               : "memory");
+}
 __device__ __forceinline__ bool cluster_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
