@@ -384,7 +384,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         // The warp pair's unit 2 q + half of sums belongs to the share unit * S / 8's CTA with the same lanes: 4 tokens of a
         // feature are 16 bytes at [unit of the owner][rank][matrix][4 tokens][lane], with room for all tokens in a unit.
         // Few tokens' stores count their bytes on the owner's barrier themselves (one token of 4096 x 4096 9.35 us
-        // against 9.50); many go faster as plain stores with one arrival for each warp (300 tokens of 14336 down rows 39.7
+        // against 9.50); many go faster as plain stores with one arrival for each warp (300 tokens of 14336 down rows 39.8
         // against 41.3).
         const uint32_t unit_bytes = mats * g4 * 512;
         const int per = 8 / S, unit = 2 * q + half;
@@ -849,6 +849,7 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
     l.S = S;
     const int width = P * (gated || !both ? rows : 2 * rows), fit = clusters(P * S, sms), toks = l.NT / P;
     const long long T = (long long)((N + width - 1) / width) * l.MT;
+    if (wide / 2 >= chunks) return;  // half of the stage would do
     if (T > (1 << 30) || (both && !gated && N <= rows) || (P > 1 && N <= width / 2) || (S > 1 && (T > fit || S > KC))) return;
     l.T = (int)T;
     bool own_x;
@@ -859,14 +860,15 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
     const double load = wide * ((both ? 2 : 1) * rows + toks) * 128.0, w_load = load - wide * toks * 128.0;
     const double mma = wide * (both ? 2 : 1) * 4 * 1.25 * l.NT / 2;
     const double l2 = (w_load * slow_w + (load - w_load) * slow_x) / 62;
-    // weights that several token tiles share come out of HBM once: those tiles run together
-    const double mem = w_load * active / hbm / (l.MT < kTogether ? l.MT : kTogether);
+    // weights that several token tiles share come out of HBM little more than once: those tiles run together (32 x 4096 x
+    // 4096 as 16 + 16 tokens 13.2 us, as 32 11.3)
+    const double mem = w_load * active / hbm / (1 + 0.65 * ((l.MT < kTogether ? l.MT : kTogether) - 1));
     double chunk = l2 > mem ? l2 + 0.15 * mem : mem + 0.15 * l2;
     for (const double least : {mma, (1950 + l2 + mma) / stages, 270 + wide * (155 + 3.0 * toks)})
       if (chunk < least) chunk = least;
     if (rows < kDnHalf) chunk += 60 * wide;
     const double epi = 1500 + 18.0 * l.NT * (both ? 2 : 1);
-    const double products = (((KC + S - 1) / S) * chunk + (l2 + mma) / 2) * (P == 2 ? 1.1 : 1);
+    const double products = (((KC + S - 1) / S) * chunk + (l2 + mma) / 2) * (P == 2 ? 1.05 : 1);
     double t = S > 1 ? products + 3300 + 48.0 * l.NT * (both ? 2 : 1)
                : l.NT * (both ? 2 : 1) <= 256 ? waves * (products > epi ? products : epi) + epi
                                               : waves * (products + epi);

@@ -407,6 +407,34 @@ def test_layers_on_two_streams_at_once():
 
 
 @gpu
+def test_calls_of_two_threads():
+    import threading
+
+    cases = [[_linear_case(*s, F16, bias=True) for s in ((1, 264, 1000), (40, 520, 264), (200, 264, 136), (3, 72, 2048))],
+             [_linear_case(*s, BF16, "silu", gated=True) for s in ((300, 520, 264), (2, 264, 520), (70, 72, 1000))]]
+    serial = [[_linear_run(c) for c in cs] for cs in cases]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def calls(cs, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    for c, y in zip(cs, want):
+                        if not torch.equal(_linear_run(c), y):
+                            wrong.append(tuple(y.shape))
+        except Exception as e:  # an exception of a thread fails the test
+            wrong.append(e)
+
+    threads = [threading.Thread(target=calls, args=a) for a in zip(cases, serial)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+@gpu
 def test_outputs_in_the_residual():
     c = _layer_case(5, 264, 200, 8, 2, 1, F16, True, True, False)
     x, r = c["x"].cuda(), c["residual"].cuda()
