@@ -91,12 +91,13 @@ __device__ __forceinline__ bool grid_wait(unsigned* bar, unsigned n, volatile in
   return false;
 }
 
-// Logits of token b over the rows [r0, r1) of the router weight, to out[E].  A thread owns EV
-// neighbouring experts and every nrs-th row; red: kDnThreads * EV floats.
-template <int EV>
-__device__ void slice_logits(const LayerArgs& p, int b, int r0, int r1, float* out, float* red) {
-  constexpr int RU = 8;
-  const int tid = threadIdx.x, nchunk = p.E / EV, nrs = kDnThreads / nchunk;
+// Logits of token b over the rows [r0, r1) of the router weight, to out[E].  A thread owns 8
+// neighbouring experts and every nrs-th row; red: kDnThreads * 8 floats.  Short code on purpose, here and in choose:
+// the kernel fetches it anew in every call (one token of 8 x 1024: 8 rows in flight, code for odd E of its own and
+// choices in registers 22.4 us, this 20.9).
+__device__ __forceinline__ void slice_logits(const LayerArgs& p, int b, int r0, int r1, float* out, float* red) {
+  constexpr int RU = 4, EV = 8;
+  const int tid = threadIdx.x, nchunk = (p.E + EV - 1) / EV, E8 = nchunk * EV, nrs = kDnThreads / nchunk;
   const int ec = tid % nchunk, rs = tid / nchunk;
   float acc[EV];
 #pragma unroll
@@ -113,46 +114,60 @@ __device__ void slice_logits(const LayerArgs& p, int b, int r0, int r1, float* o
         if (r < r1) {
           xv[u] = ld16(p.x, (size_t)b * p.d + r, p.bf16);
           const unsigned short* wr = reinterpret_cast<const unsigned short*>(p.w_router) + (size_t)r * p.E + ec * EV;
-          if constexpr (EV == 8) wv[u] = *reinterpret_cast<const uint4*>(wr);
-          else wv[u].x = wr[0];
+          if (p.E % EV == 0) {
+            wv[u] = *reinterpret_cast<const uint4*>(wr);
+          } else {
+            unsigned long long w[2] = {0, 0};  // value by value, the last one first
+#pragma unroll 1
+            for (int i = p.E - ec * EV < EV ? p.E - ec * EV : EV; i-- > 0;) {
+              w[1] = w[1] << 16 | w[0] >> 48;
+              w[0] = w[0] << 16 | wr[i];
+            }
+            wv[u] = make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32));
+          }
         }
       }
+      auto rows = [&](auto value) {
 #pragma unroll
-      for (int u = 0; u < RU; ++u) {
-        const uint32_t w4[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
+        for (int u = 0; u < RU; ++u) {
+          const uint32_t w4[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
 #pragma unroll
-        for (int i = 0; i < EV; ++i)
-          acc[i] = fmaf(xv[u], from16((unsigned short)(w4[i / 2] >> (16 * (i & 1))), p.bf16), acc[i]);
-      }
+          for (int i = 0; i < EV; ++i) acc[i] = fmaf(xv[u], value(w4[i / 2], i & 1), acc[i]);
+        }
+      };
+      if (p.bf16) rows([](uint32_t w, int hi) { return __uint_as_float(hi ? w & 0xffff0000u : w << 16); });
+      else rows([](uint32_t w, int hi) { return from16((unsigned short)(hi ? w >> 16 : w), 0); });
     }
   }
   const int lane = tid & 31;
   if (32 % nchunk == 0) {
     // a warp's rows by shuffles, then the warps' sums
+#pragma unroll 1
+    for (int off = nchunk; off < 32; off <<= 1) {
 #pragma unroll
-    for (int i = 0; i < EV; ++i)
-      for (int off = nchunk; off < 32; off <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
+      for (int i = 0; i < EV; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
+    }
     if (lane < nchunk) {
 #pragma unroll
-      for (int i = 0; i < EV; ++i) red[(tid >> 5) * p.E + ec * EV + i] = acc[i];
+      for (int i = 0; i < EV; ++i) red[(tid >> 5) * E8 + ec * EV + i] = acc[i];
     }
     __syncthreads();
     if (tid < p.E) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kDnThreads / 32; ++w) s += red[w * p.E + tid];
+      for (int w = 0; w < kDnThreads / 32; ++w) s += red[w * E8 + tid];
       __stcg(out + tid, s);
     }
     return;
   }
   if (rs < nrs) {
 #pragma unroll
-    for (int i = 0; i < EV; ++i) red[rs * p.E + ec * EV + i] = acc[i];
+    for (int i = 0; i < EV; ++i) red[rs * E8 + ec * EV + i] = acc[i];
   }
   __syncthreads();
   for (int e = tid >> 5; e < p.E; e += kDnThreads / 32) {
     float s = 0.f;
-    for (int r = lane; r < nrs; r += 32) s += red[r * p.E + e];
+    for (int r = lane; r < nrs; r += 32) s += red[r * E8 + e];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     if (lane == 0) __stcg(out + e, s);
@@ -166,66 +181,62 @@ __device__ __forceinline__ void mark_token(LayerMisc& m, int e, int b) {
 
 // One warp: token b's logits (its slices [slices][E] added in order), its k experts by logit descending
 // (ties: the lower index; NaN ranks as -inf) and their weights.  A logit's key orders as the logit
-// does; an expert that is taken has key 0, below every logit's.  m: where to mark the choice, or null.
-template <int PER>
-__device__ __forceinline__ void choose(const LayerArgs& p, int b, const float* slices, int* idx, float* w,
-                                       LayerMisc* m) {
+// does; an expert that is taken has key 0, below every logit's.  The keys take the first slice's place.  m: where to
+// mark the choice, or null.
+__device__ __forceinline__ uint32_t logit_key(float l) {
+  const uint32_t u = __float_as_uint(l);
+  return u >> 31 ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float key_logit(uint32_t key) {
+  return __uint_as_float(key >> 31 ? key & 0x7fffffffu : ~key);
+}
+__device__ __forceinline__ void choose(const LayerArgs& p, int b, float* slices, int* idx, float* w, LayerMisc* m) {
   const int lane = threadIdx.x & 31;
-  float l[PER];
-  uint32_t key[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane + 32 * i;
-    l[i] = -INFINITY;
-    key[i] = 0u;
-    if (e < p.E) {
-      float s = 0.f;
+  uint32_t* keys = reinterpret_cast<uint32_t*>(slices);  // expert e's is lane e % 32's
+#pragma unroll 1
+  for (int e = lane; e < p.E; e += 32) {
+    float s = 0.f;
 #pragma unroll 4
-      for (int q = 0; q < p.slices; ++q) s += slices[q * p.E + e];
-      s += 0.f;  // -0 and +0 are one logit
-      if (!isnan(s)) l[i] = s;
-      const uint32_t u = __float_as_uint(l[i]);
-      key[i] = u >> 31 ? ~u : u | 0x80000000u;
-    }
+    for (int q = 0; q < p.slices; ++q) s += slices[q * p.E + e];
+    s += 0.f;  // -0 and +0 are one logit
+    keys[e] = logit_key(isnan(s) ? -INFINITY : s);
   }
   float mine = 0.f, top = -INFINITY;  // lane j keeps the j-th choice
   int mine_e = 0;
 #pragma unroll 1
   for (int j = 0; j < p.k; ++j) {
-    uint32_t best = key[0];
-    int at = lane;
-#pragma unroll
-    for (int i = 1; i < PER; ++i) {
-      if (key[i] > best) {
-        best = key[i];
-        at = lane + 32 * i;
+    uint32_t best = 0u;
+    int at = 0x7fffffff;
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += 32) {
+      const uint32_t key = keys[e];
+      if (key > best) {
+        best = key;
+        at = e;
       }
     }
     const uint32_t most = __reduce_max_sync(0xffffffffu, best);
     const int e = __reduce_min_sync(0xffffffffu, best == most ? at : 0x7fffffff);
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (lane + 32 * i == e) key[i] = 0u;
-    const float v = __uint_as_float(most >> 31 ? most & 0x7fffffffu : ~most);
+    if (lane == (e & 31)) keys[e] = 0u;
+    const float v = key_logit(most);
     if (j == 0) top = v;
     if (lane == j) {
       mine = v;
       mine_e = e;
     }
   }
-  float sum = 0.f;
-  if (p.renorm) {
-    if (lane < p.k) sum = expf(mine - top);
-  } else {
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (lane + 32 * i < p.E) sum += expf(l[i] - top);
+  const float num = expf(mine - top);
+  float sum = lane < p.k ? num : 0.f;
+  if (!p.renorm) {
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += 32)
+      if (keys[e]) sum += expf(key_logit(keys[e]) - top);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   if (lane < p.k) {
     idx[b * p.k + lane] = mine_e;
-    w[b * p.k + lane] = expf(mine - top) / sum;
+    w[b * p.k + lane] = num / sum;
     if (m) {
       mark_token(*m, mine_e, b);
       atomicOr(&m->on[mine_e >> 5], 1u << (mine_e & 31));
@@ -233,19 +244,14 @@ __device__ __forceinline__ void choose(const LayerArgs& p, int b, const float* s
   }
 }
 
-__device__ void choose_any(const LayerArgs& p, int b, const float* slices, int* idx, float* w, LayerMisc* m) {
-  if (p.E <= 64) choose<2>(p, b, slices, idx, w, m);
-  else choose<kMaxExperts / 32>(p, b, slices, idx, w, m);
-}
-
 // Whole CTA: n values of other CTAs to shared memory, eight of a thread's in flight.
 __device__ void gather_logits(const float* from, int n, float* to) {
-  for (int i = threadIdx.x; i < n; i += 8 * kDnThreads) {
-    float t[8];
+  for (int i = threadIdx.x; i < n; i += 4 * kDnThreads) {
+    float t[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) t[j] = i + j * kDnThreads < n ? __ldcg(from + i + j * kDnThreads) : 0.f;
+    for (int j = 0; j < 4; ++j) t[j] = i + j * kDnThreads < n ? __ldcg(from + i + j * kDnThreads) : 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 4; ++j)
       if (i + j * kDnThreads < n) to[i + j * kDnThreads] = t[j];
   }
 }
@@ -259,8 +265,7 @@ __device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
     const int len = (p.d + p.slices - 1) / p.slices;
     const int r0 = s * len, r1 = r0 + len < p.d ? r0 + len : p.d;
     float* out = p.logits + ((size_t)b * p.slices + s) * p.E;
-    if (p.E % 8 == 0) slice_logits<8>(p, b, r0, r1, out, scratch);
-    else slice_logits<1>(p, b, r0, r1, out, scratch);
+    slice_logits(p, b, r0, r1, out, scratch);
     __syncthreads();
     if (!few) {
       // the token's last slice to come chooses its experts
@@ -275,7 +280,7 @@ __device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
         gather_logits(p.logits + (size_t)b * p.slices * p.E, p.slices * p.E, scratch);
         __syncthreads();
         if (warp == 0) {
-          choose_any(p, b, scratch, p.top_idx, p.top_w, nullptr);
+          choose(p, b, scratch, p.top_idx, p.top_w, nullptr);
         }
       }
       __syncthreads();
@@ -290,7 +295,7 @@ __device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
   if (few) {
     gather_logits(p.logits, p.B * p.slices * p.E, scratch);
     __syncthreads();
-    if (warp < p.B) choose_any(p, warp, scratch + warp * p.slices * p.E, m.idx, m.w, &m);
+    if (warp < p.B) choose(p, warp, scratch + warp * p.slices * p.E, m.idx, m.w, &m);
   } else {
     for (int i = tid; i < p.B * p.k; i += kDnThreads) {
       m.idx[i] = __ldcg(p.top_idx + i);
