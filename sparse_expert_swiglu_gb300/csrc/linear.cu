@@ -163,7 +163,9 @@ __device__ __forceinline__ void linear_sums(uint32_t addr, int groups, int strid
 // pays for every line of code it fetches.  PAIR: CTA pairs (cta_group::2).  A tile then has up to 256 lanes for each product, 128 in each
 // CTA, and either CTA fetches and keeps half of its tokens: with 100 to 500 tokens, where the bytes that
 // an SM can take from L2 bound the products (300 tokens of 14336 gated features of K = 4096: 72 us, 78 without).
-template <bool FEW, bool PAIR>
+// SHARED: clusters share a tile along k; the one epilogue is not fetched with the other (an expert on 100 tokens, 2048 x
+// 1408: 20.8 us against 21.9).
+template <bool FEW, bool PAIR, bool SHARED>
 __global__ void __launch_bounds__(kDnThreads, 1)
 linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mw2,
               const __grid_constant__ CUtensorMap mx, const LinearArgs p) {
@@ -182,7 +184,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   DenseBars* bars = reinterpret_cast<DenseBars*>(ring + (size_t)p.stages * stage_bytes +
                                                  (p.own_x ? (size_t)mats * g4 * 4096 : 0));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int S = p.S, ns = p.stages, NT = p.NT;
+  const int S = SHARED ? p.S : 1, ns = p.stages, NT = p.NT;
   const int crank = PAIR || S > 1 ? (int)cluster_rank() : 0, half_of = PAIR ? crank & 1 : 0, lead = crank - half_of;
   const int rank = crank / P;                                              // share of k
   const int first = blockIdx.x / (P * S), step = gridDim.x / (P * S);  // tiles of this CTA; S > 1: one
@@ -341,7 +343,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
       tile_at(t, p.T, p.MT, ft, mt);
       const int m0 = mt * NT;
       const int nt = p.M - m0 < NT ? p.M - m0 : NT;  // tokens of this tile
-      if (S == 1) {
+      if constexpr (!SHARED) {
         const int feat = (ft * P + half_of) * width + (by_tok ? 0 : half * p.rows) + row;
         const bool on = row < p.rows && feat < p.N;
         const float ba = p.bias && on ? ld16(p.bias, feat, p.bf16) : 0.f;
@@ -1015,9 +1017,12 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   p.stream = l.MT == 1;
   const int ctas = l.P * (l.S > 1 ? l.T * l.S : l.T < sms / l.P ? l.T : sms / l.P);
   const size_t smem = 1024 + (size_t)p.stages * stage + sizeof(DenseBars) + (own_x ? linear_sum_bytes(l, c.M, gated) : 0);
-  static std::atomic<uint64_t> allowed[3];
-  const int which = l.P == 2 ? 2 : l.NT <= kFewTokens && l.S * l.T <= sms ? 1 : 0;
-  const auto kernel = which == 2 ? linear_kernel<false, true> : which ? linear_kernel<true, false> : linear_kernel<false, false>;
+  static std::atomic<uint64_t> allowed[6];
+  const int which = (l.P == 2 ? 4 : l.NT <= kFewTokens && l.S * l.T <= sms ? 2 : 0) + (l.S > 1);
+  constexpr decltype(&linear_kernel<false, false, false>) kernels[6] = {
+      linear_kernel<false, false, false>, linear_kernel<false, false, true>, linear_kernel<true, false, false>,
+      linear_kernel<true, false, true>,   linear_kernel<false, true, false>, linear_kernel<false, true, true>};
+  const auto kernel = kernels[which];
   e = allow_shared(kernel, allowed[which], smem_optin);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
