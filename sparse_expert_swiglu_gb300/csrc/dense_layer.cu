@@ -52,6 +52,7 @@ struct LayerArgs {
   float* ysq;          // [B][128 features][4 warps] their squares
   int slots;           // 8 * max_groups
   int rows;            // features of a tile of the first phase
+  int early;           // tiles of the first phase that stay whole and start before the routing
   int slices;          // router: CTAs per token
   int stages, stage_bytes;
 };
@@ -501,8 +502,8 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   const uint32_t tmem = bars->tmem;
   griddep_launch_dependents();  // the next call's CTAs take the SMs that this kernel's leave
 
-  // Chunk kc of a tile of the first phase, into a stage.  The shared experts' tiles come first and stay whole:
-  // they do not depend on the routing.
+  // Chunk kc of a tile of the first phase, into a stage.  The shared experts' tiles come first: they do not depend on the
+  // routing.
   const uint64_t pw = policy_evict_first(), px = policy_evict_normal();
   auto load_gate_up = [&](int t, int kc, int stage) {
     const int a = t / FT, f0 = (t - a * FT) * p.rows, k = kc * kDnChunk;
@@ -521,10 +522,10 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       for (int r = 0; r < n4; ++r) tma_rows4(at + r * 512, &maps.x, k, 4 * r, 4 * r + 1, 4 * r + 2, 4 * r + 3, full, px);
     }
   };
-  // Their first stages are on their way while the tokens are routed, whose scratch is the last stage.
+  // The first stages of whole ones are on their way while the tokens are routed, whose scratch is the last stage.
   int sent = 0;
   if (warp == 0 && elect_one()) {
-    for (int t = cta; t < p.ns * FT; t += gridDim.x)
+    for (int t = cta; t < p.early; t += gridDim.x)
       for (int kc = 0; kc < KC1 && sent < S - 1; ++kc) load_gate_up(t, kc, sent++);
     // ... and the first of their down rows on the way to L2
     for (int i = cta, n = 0; i < p.ns * DT * KC2 && n < 4; i += gridDim.x, ++n) {
@@ -542,7 +543,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   fence_proxy_async_smem();
   __syncthreads();
 
-  const Sched s1 = Sched::make(m.n_act * FT, KC1, gridDim.x, p.ns * FT);
+  const Sched s1 = Sched::make(m.n_act * FT, KC1, gridDim.x, p.early);
   const Sched s2 = Sched::make(m.n_act * DT, KC2, gridDim.x, 0);
 
   // join: every token's experts and their shares, in order.  A unit is 128 features of a token; each four
@@ -893,7 +894,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
 
 struct LayerPlan {
   int B = -1, d, f, E, k, ns, sms;
-  int groups, slices, grid, rows;
+  int groups, slices, grid, rows, early;
   size_t logits, top_idx, top_w, h, part, yrow, ysq, ypart, total;
 };
 
@@ -926,23 +927,29 @@ const LayerPlan& layer_plan(int B, int d, int f, int E, int k, int ns, int sms) 
   double miss = 1;
   for (int b = 0; b < B; ++b) miss *= 1 - (double)k / E;
   const int act = ns + (int)(E * (1 - miss) + 0.5);
+  // The shared experts' tiles may start before the routing, which is worth 2 chunks, but are whole then: with few
+  // tiles they last longer than all the others, cut into equal shares (61 tokens of 19 experts of 280 features, 8 + 2 for each:
+  // 76 us with whole ones, 55 without).
   double best = 1e30;
   for (int rows = kDnHalf; rows >= 64; rows -= 8) {
-    const int FT = (f + rows - 1) / rows;
-    const Sched s = Sched::make(act * FT, KC1, sms, ns * FT);
-    // clocks of the slowest SM: a tile's chunks at its share of HBM, and 6 chunks' worth for joining
-    const double chunk = rows / 128.0, tail = s.total ? (double)s.total / sms * chunk + 6 : 0;
-    const double t = (s.dp + sms - 1) / sms * KC1 * chunk + tail;
-    if (t < best * 0.995) {
-      best = t;
-      l.rows = rows;
+    for (int first = ns > 0; first >= 0; --first) {
+      const int FT = (f + rows - 1) / rows, early = first ? ns * FT : 0;
+      const Sched s = Sched::make(act * FT, KC1, sms, early);
+      // clocks of the slowest SM: a tile's chunks at its share of HBM, and 6 chunks' worth for joining
+      const double chunk = rows / 128.0, tail = s.total ? (double)s.total / sms * chunk + 6 : 0;
+      const double t = (s.dp + sms - 1) / sms * KC1 * chunk + tail + (ns > 0 && !first ? 2 : 0);
+      if (t < best * 0.995) {
+        best = t;
+        l.rows = rows;
+        l.early = early;
+      }
     }
   }
   // the number of active experts is known on the device only: the largest need of any
   int segs = 0, parts = 1;
   const int FT = (f + l.rows - 1) / l.rows;
   for (int a = 0; a <= most; ++a) {
-    const Sched s1 = Sched::make((a + ns) * FT, KC1, sms, ns * FT), s2 = Sched::make((a + ns) * DT, KC2, sms, 0);
+    const Sched s1 = Sched::make((a + ns) * FT, KC1, sms, l.early), s2 = Sched::make((a + ns) * DT, KC2, sms, 0);
     if (s1.segments() > segs) segs = s1.segments();
     if (s2.max_parts() > parts) parts = s2.max_parts();
   }
@@ -1018,6 +1025,7 @@ cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int s
   p.ysq = reinterpret_cast<float*>(w8 + l.ysq);
   p.slots = l.groups * 8;
   p.rows = l.rows;
+  p.early = l.early;
   p.slices = l.slices;
   p.stage_bytes = kDnBytesA + (c.B + 7) / 8 * 16 * 128;
   const int fixed = 1024 + (int)sizeof(LayerMisc) + p.slots;
