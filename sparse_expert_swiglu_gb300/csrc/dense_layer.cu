@@ -54,6 +54,8 @@ struct LayerArgs {
   int rows;            // features of a tile of the first phase
   int early;           // tiles of the first phase that stay whole and start before the routing
   int slices;          // router: CTAs per token
+  int block_rows, block_vecs, blocks;  // log2 of the rows of a block, its vectors, blocks that a CTA's threads take at a time
+  int sum_step;        // threads of the first step of the sums, a multiple of E
   int stages, stage_bytes;
 };
 
@@ -92,40 +94,43 @@ __device__ __forceinline__ bool grid_wait(unsigned* bar, unsigned n, volatile in
   return false;
 }
 
-// Logits of token b over the rows [r0, r1) of the router weight, to out[E].  A thread owns 8
-// neighbouring experts and every nrs-th row; red: kDnThreads * 8 floats.  Short code on purpose, here and in choose:
-// the kernel fetches it anew in every call (one token of 8 x 1024: 8 rows in flight, code for odd E of its own and
-// choices in registers 22.4 us, this 20.9).
+// Logits of token b over the rows [r0, r1) of the router weight (multiples of 8), to out[E].  A block is one row, or eight
+// where E is no multiple of 8: a whole number of vectors of 8 values.  A thread owns one vector of every nrs-th block,
+// whose values belong to the same experts each time and, from 8 experts on, to at most two rows.  (Fewer experts: one value
+// of every nrs-th row.)  red: 9 kDnThreads
+// floats.  Short code on purpose, here and in choose: the kernel fetches it anew in every call (one token of 8 x 1024: 8
+// rows in flight, code for odd E of its own and choices in registers 22.4 us, this 20.9; odd E value by value: 61 tokens of
+// 19 x 280 54.5 us, this 49.5).
 __device__ __forceinline__ void slice_logits(const LayerArgs& p, int b, int r0, int r1, float* out, float* red) {
-  constexpr int RU = 4, EV = 8;
-  const int tid = threadIdx.x, nchunk = (p.E + EV - 1) / EV, E8 = nchunk * EV, nrs = kDnThreads / nchunk;
-  const int ec = tid % nchunk, rs = tid / nchunk;
-  float acc[EV];
+  constexpr int RU = 4;  // vectors in flight
+  const int tid = threadIdx.x, E = p.E, V = p.block_vecs, nrs = p.blocks, rs = tid / V, v = tid - rs * V;
+  const unsigned short* x = reinterpret_cast<const unsigned short*>(p.x) + (size_t)b * p.d;
+  if (rs < nrs && E < 8) {
+    float acc = 0.f;
+#pragma unroll 4
+    for (int r = r0 + rs; r < r1; r += nrs)
+      acc = fmaf(ld16(x, r, p.bf16), ld16(p.w_router, (size_t)r * E + v, p.bf16), acc);
+    red[tid] = acc;
+  } else if (rs < nrs) {
+    float acc[8];
 #pragma unroll
-  for (int i = 0; i < EV; ++i) acc[i] = 0.f;
-  if (rs < nrs) {
-    for (int q = r0 + rs; q < r1; q += nrs * RU) {
-      float xv[RU];
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    const int ra = v * 8 / E, first = (ra + 1) * E - v * 8;  // values of the vector's first row
+    const uint4* w = reinterpret_cast<const uint4*>(p.w_router) + v;
+    const int end = r1 >> p.block_rows;
+    for (int q = (r0 >> p.block_rows) + rs; q < end; q += nrs * RU) {
+      float xa[RU], xc[RU];
       uint4 wv[RU];
 #pragma unroll
       for (int u = 0; u < RU; ++u) {
-        const int r = q + u * nrs;
-        xv[u] = 0.f;
+        const int at = q + u * nrs;
+        xa[u] = xc[u] = 0.f;
         wv[u] = make_uint4(0, 0, 0, 0);
-        if (r < r1) {
-          xv[u] = ld16(p.x, (size_t)b * p.d + r, p.bf16);
-          const unsigned short* wr = reinterpret_cast<const unsigned short*>(p.w_router) + (size_t)r * p.E + ec * EV;
-          if (p.E % EV == 0) {
-            wv[u] = *reinterpret_cast<const uint4*>(wr);
-          } else {
-            unsigned long long w[2] = {0, 0};  // value by value, the last one first
-#pragma unroll 1
-            for (int i = p.E - ec * EV < EV ? p.E - ec * EV : EV; i-- > 0;) {
-              w[1] = w[1] << 16 | w[0] >> 48;
-              w[0] = w[0] << 16 | wr[i];
-            }
-            wv[u] = make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32));
-          }
+        if (at < end) {
+          const int row = (at << p.block_rows) + ra;
+          wv[u] = w[(size_t)at * V];
+          xa[u] = ld16(x, row, p.bf16);
+          if (p.block_rows) xc[u] = ld16(x, row + (first < 8), p.bf16);
         }
       }
       auto rows = [&](auto value) {
@@ -133,45 +138,31 @@ __device__ __forceinline__ void slice_logits(const LayerArgs& p, int b, int r0, 
         for (int u = 0; u < RU; ++u) {
           const uint32_t w4[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
 #pragma unroll
-          for (int i = 0; i < EV; ++i) acc[i] = fmaf(xv[u], value(w4[i / 2], i & 1), acc[i]);
+          for (int i = 0; i < 8; ++i) acc[i] = fmaf(i < first ? xa[u] : xc[u], value(w4[i / 2], i & 1), acc[i]);
         }
       };
       if (p.bf16) rows([](uint32_t w, int hi) { return __uint_as_float(hi ? w & 0xffff0000u : w << 16); });
       else rows([](uint32_t w, int hi) { return from16((unsigned short)(hi ? w >> 16 : w), 0); });
     }
+    reinterpret_cast<float4*>(red)[tid * 2] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    reinterpret_cast<float4*>(red)[tid * 2 + 1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
   }
-  const int lane = tid & 31;
-  if (32 % nchunk == 0) {
-    // a warp's rows by shuffles, then the warps' sums
-#pragma unroll 1
-    for (int off = nchunk; off < 32; off <<= 1) {
-#pragma unroll
-      for (int i = 0; i < EV; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
-    }
-    if (lane < nchunk) {
-#pragma unroll
-      for (int i = 0; i < EV; ++i) red[(tid >> 5) * E8 + ec * EV + i] = acc[i];
-    }
-    __syncthreads();
-    if (tid < p.E) {
-      float s = 0.f;
-#pragma unroll
-      for (int w = 0; w < kDnThreads / 32; ++w) s += red[w * E8 + tid];
-      __stcg(out + tid, s);
-    }
-    return;
-  }
-  if (rs < nrs) {
-#pragma unroll
-    for (int i = 0; i < EV; ++i) red[rs * E8 + ec * EV + i] = acc[i];
+  // [rs][row of a block][expert], summed in two steps
+  __syncthreads();
+  float* sums = red + 8 * kDnThreads;
+  const int step = p.sum_step;
+  if (tid < step) {
+    float t = 0.f;
+#pragma unroll 4
+    for (int i = tid; i < (nrs * E) << p.block_rows; i += step) t += red[i];
+    sums[tid] = t;
   }
   __syncthreads();
-  for (int e = tid >> 5; e < p.E; e += kDnThreads / 32) {
-    float s = 0.f;
-    for (int r = lane; r < nrs; r += 32) s += red[r * E8 + e];
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    if (lane == 0) __stcg(out + e, s);
+  if (tid < E) {
+    float t = 0.f;
+#pragma unroll 4
+    for (int i = tid; i < step; i += E) t += sums[i];
+    __stcg(out + tid, t);
   }
 }
 
@@ -263,7 +254,7 @@ __device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
   const bool few = p.B <= kFewTok;
   if (cta < p.B * p.slices) {
     const int b = cta / p.slices, s = cta - b * p.slices;
-    const int len = (p.d + p.slices - 1) / p.slices;
+    const int len = (p.d / 8 + p.slices - 1) / p.slices * 8;
     const int r0 = s * len, r1 = r0 + len < p.d ? r0 + len : p.d;
     float* out = p.logits + ((size_t)b * p.slices + s) * p.E;
     slice_logits(p, b, r0, r1, out, scratch);
@@ -1027,6 +1018,10 @@ cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int s
   p.rows = l.rows;
   p.early = l.early;
   p.slices = l.slices;
+  p.block_rows = p.E % 8 && p.E >= 8 ? 3 : 0;
+  p.block_vecs = p.E < 8 ? p.E : (p.E << p.block_rows) / 8;
+  p.blocks = kDnThreads / p.block_vecs;
+  p.sum_step = (p.E < 16 ? 16 : kDnThreads / p.E) * p.E;
   p.stage_bytes = kDnBytesA + (c.B + 7) / 8 * 16 * 128;
   const int fixed = 1024 + (int)sizeof(LayerMisc) + p.slots;
   int S = (smem_optin - fixed) / p.stage_bytes;
