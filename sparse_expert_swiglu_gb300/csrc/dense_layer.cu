@@ -56,7 +56,7 @@ struct LayerArgs {
   int slices;          // router: CTAs per token
   int block_rows, block_vecs, blocks;  // log2 of the rows of a block, its vectors, blocks that a CTA's threads take at a time
   int sum_step;        // threads of the first step of the sums, a multiple of E
-  int stages, stage_bytes;
+  int stages, stage_bytes, a_bytes;  // a_bytes: of a stage, before the tokens
 };
 
 struct LayerMisc {
@@ -461,6 +461,8 @@ struct LayerMaps {
   CUtensorMap x, h;
 };
 
+// WIDE: chunks of 64 k in a stage of the first phase.
+template <int WIDE>
 __global__ void __launch_bounds__(kDnThreads, 1)
 dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   extern __shared__ uint8_t raw[];
@@ -471,9 +473,12 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   const int S = p.stages;
   const int FT = (p.f + p.rows - 1) / p.rows, DT = (p.d + 2 * kDnHalf - 1) / (2 * kDnHalf);
-  const int KC1 = (p.d + kDnChunk - 1) / kDnChunk, KC2 = (p.f + kDnChunk - 1) / kDnChunk;
+  const int chunks = (p.d + kDnChunk - 1) / kDnChunk;
+  const int KC1 = (chunks + WIDE - 1) / WIDE, KC2 = (p.f + kDnChunk - 1) / kDnChunk;  // stages of a tile
   const uint32_t ring_at = smem_addr(ring);
   const uint32_t half_a = p.rows * 128;  // bytes of a chunk of gate rows, or of up rows
+  const uint32_t x_bytes = (p.B + 7) / 8 * 1024;  // ... of the tokens'
+  const uint32_t a_bytes = WIDE == 1 ? kDnBytesA : p.a_bytes;
   int* status = &p.head->ctrl.status;
   volatile int* abort = &bars->abort;
 
@@ -497,20 +502,25 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   // routing.
   const uint64_t pw = policy_evict_first(), px = policy_evict_normal();
   auto load_gate_up = [&](int t, int kc, int stage) {
-    const int a = t / FT, f0 = (t - a * FT) * p.rows, k = kc * kDnChunk;
+    const int a = t / FT, f0 = (t - a * FT) * p.rows;
+    const int c0 = kc * WIDE, c1 = WIDE == 1 ? c0 + 1 : c0 + WIDE < chunks ? c0 + WIDE : chunks;
     const bool routed = a >= p.ns;
     const int z = routed ? m.act[a] : a, n4 = ((routed ? m.cnt[a] : p.B) + 3) / 4;
     uint64_t* full = &bars->full[stage];
-    mbar_arrive_expect_tx(full, 2 * half_a + n4 * 512);
-    uint32_t at = ring_at + stage * p.stage_bytes;
-    tma_3d(at, routed ? &maps.gate : &maps.sgate, k, f0, z, full, pw);
-    tma_3d(at + half_a, routed ? &maps.up : &maps.sup, k, f0, z, full, pw);
-    at += kDnBytesA;
-    if (routed) {
-      const uint8_t* q = tok + m.grp[a] * 8;
-      for (int r = 0; r < n4; ++r, q += 4) tma_rows4(at + r * 512, &maps.x, k, q[0], q[1], q[2], q[3], full, px);
-    } else {
-      for (int r = 0; r < n4; ++r) tma_rows4(at + r * 512, &maps.x, k, 4 * r, 4 * r + 1, 4 * r + 2, 4 * r + 3, full, px);
+    mbar_arrive_expect_tx(full, (c1 - c0) * (2 * half_a + n4 * 512));
+    uint32_t at = ring_at + stage * p.stage_bytes, xat = at + a_bytes;
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c, at += 2 * half_a, xat += x_bytes) {
+      const int k = c * kDnChunk;
+      tma_3d(at, routed ? &maps.gate : &maps.sgate, k, f0, z, full, pw);
+      tma_3d(at + half_a, routed ? &maps.up : &maps.sup, k, f0, z, full, pw);
+      if (routed) {
+        const uint8_t* q = tok + m.grp[a] * 8;
+        for (int r = 0; r < n4; ++r, q += 4) tma_rows4(xat + r * 512, &maps.x, k, q[0], q[1], q[2], q[3], full, px);
+      } else {
+        for (int r = 0; r < n4; ++r)
+          tma_rows4(xat + r * 512, &maps.x, k, 4 * r, 4 * r + 1, 4 * r + 2, 4 * r + 3, full, px);
+      }
     }
   };
   // The first stages of whole ones are on their way while the tokens are routed, whose scratch is the last stage.
@@ -611,7 +621,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       };
       auto load_h = [&](const Seg& q, int kc, int stage) {
         const int a = q.t / DT, ng = (m.cnt[a] + 7) / 8, row = m.grp[a] * 16;
-        const uint32_t at = ring_at + stage * p.stage_bytes + kDnBytesA;
+        const uint32_t at = ring_at + stage * p.stage_bytes + a_bytes;
         for (int i = 0; i < ng; ++i)
           tma_2d(at + i * 2048, &maps.h, kc * kDnChunk, row + 16 * i, &bars->full[stage], px);
       };
@@ -699,8 +709,11 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
               break;
             }
             tc_after_sync();
-            const uint32_t a = ring_at + st * p.stage_bytes;
-            dn_stage_products(a, a + kDnBytesA, d0, d0 + 128, desc, phase != 0, kc == g.k0, true, second);
+            uint32_t a = ring_at + st * p.stage_bytes, x = a + a_bytes;
+            const int left = chunks - kc * WIDE, nc = WIDE == 1 || phase ? 1 : left < WIDE ? left : WIDE;
+#pragma unroll 1
+            for (int c = 0; c < nc; ++c, a += 2 * half_a, x += x_bytes)
+              dn_stage_products(a, x, d0, d0 + 128, desc, phase != 0, c == 0 && kc == g.k0, true, second);
             mma_commit(&bars->empty[st]);
             open = true;
             if (++st == S) {
@@ -885,9 +898,18 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
 
 struct LayerPlan {
   int B = -1, d, f, E, k, ns, sms;
-  int groups, slices, grid, rows, early;
+  int groups, slices, grid, rows, wide, early;
   size_t logits, top_idx, top_w, h, part, yrow, ysq, ypart, total;
 };
+
+constexpr int kSmem = 232448;  // that the plan reckons with
+
+int layer_a_bytes(int rows, int wide) { return wide * 2 * rows * 128 > kDnBytesA ? wide * 2 * rows * 128 : kDnBytesA; }
+
+int layer_stages(int B, int rows, int wide, int slots, int smem) {
+  const int n = (smem - 1024 - (int)sizeof(LayerMisc) - slots) / (layer_a_bytes(rows, wide) + (B + 7) / 8 * 16 * 128);
+  return n > kDnMaxStages ? kDnMaxStages : n;
+}
 
 // The plan goes by the sizes alone; a thread keeps the last one, since a program calls with the same
 // sizes again and again.
@@ -911,7 +933,7 @@ const LayerPlan& layer_plan(int B, int d, int f, int E, int k, int ns, int sms) 
   if (l.slices > rows) l.slices = rows;
   if (l.slices < 1) l.slices = 1;
   const int DT = (d + 2 * kDnHalf - 1) / (2 * kDnHalf);
-  const int KC1 = (d + kDnChunk - 1) / kDnChunk, KC2 = (f + kDnChunk - 1) / kDnChunk;
+  const int chunks = (d + kDnChunk - 1) / kDnChunk, KC2 = (f + kDnChunk - 1) / kDnChunk;
   const int most = E < B * k ? E : B * k;
   // Features of a tile: those with which the expected number of active experts (one token: the exact one)
   // comes nearest to whole waves, so that no tile's sums have to be joined.
@@ -925,10 +947,10 @@ const LayerPlan& layer_plan(int B, int d, int f, int E, int k, int ns, int sms) 
   for (int rows = kDnHalf; rows >= 64; rows -= 8) {
     for (int first = ns > 0; first >= 0; --first) {
       const int FT = (f + rows - 1) / rows, early = first ? ns * FT : 0;
-      const Sched s = Sched::make(act * FT, KC1, sms, early);
+      const Sched s = Sched::make(act * FT, chunks, sms, early);
       // clocks of the slowest SM: a tile's chunks at its share of HBM, and 6 chunks' worth for joining
       const double chunk = rows / 128.0, tail = s.total ? (double)s.total / sms * chunk + 6 : 0;
-      const double t = (s.dp + sms - 1) / sms * KC1 * chunk + tail + (ns > 0 && !first ? 2 : 0);
+      const double t = (s.dp + sms - 1) / sms * chunks * chunk + tail + (ns > 0 && !first ? 2 : 0);
       if (t < best * 0.995) {
         best = t;
         l.rows = rows;
@@ -936,8 +958,12 @@ const LayerPlan& layer_plan(int B, int d, int f, int E, int k, int ns, int sms) 
       }
     }
   }
+  // Low tiles leave much of a stage empty.  Where the stages are too few for their bytes' 2.1 us under way (an SM's share of
+  // HBM brings 128 rows in 0.7), two chunks go into one (63 tokens of 6 x 1664, 72 rows: 76.8 us with one, 71.6 with two).
+  l.wide = l.rows <= 80 && 3.0 / layer_stages(B, l.rows, 1, l.groups * 8, kSmem) > l.rows / 128.0 ? 2 : 1;
   // the number of active experts is known on the device only: the largest need of any
   int segs = 0, parts = 1;
+  const int KC1 = (chunks + l.wide - 1) / l.wide;
   const int FT = (f + l.rows - 1) / l.rows;
   for (int a = 0; a <= most; ++a) {
     const Sched s1 = Sched::make((a + ns) * FT, KC1, sms, l.early), s2 = Sched::make((a + ns) * DT, KC2, sms, 0);
@@ -1022,14 +1048,16 @@ cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int s
   p.block_vecs = p.E < 8 ? p.E : (p.E << p.block_rows) / 8;
   p.blocks = kDnThreads / p.block_vecs;
   p.sum_step = (p.E < 16 ? 16 : kDnThreads / p.E) * p.E;
-  p.stage_bytes = kDnBytesA + (c.B + 7) / 8 * 16 * 128;
+  p.a_bytes = layer_a_bytes(l.rows, l.wide);
+  p.stage_bytes = p.a_bytes + (c.B + 7) / 8 * 16 * 128;
   const int fixed = 1024 + (int)sizeof(LayerMisc) + p.slots;
   int S = (smem_optin - fixed) / p.stage_bytes;
   p.stages = S > kDnMaxStages ? kDnMaxStages : S;
   if (p.stages < 3 || l.grid < c.B) return cudaErrorInvalidValue;  // routing: a CTA for every token
   const size_t smem = fixed + (size_t)p.stages * p.stage_bytes;
-  static std::atomic<uint64_t> allowed{0};
-  e = allow_shared(dense_layer_kernel, allowed, smem_optin);
+  static std::atomic<uint64_t> allowed[2];
+  const auto kernel = l.wide == 2 ? dense_layer_kernel<2> : dense_layer_kernel<1>;
+  e = allow_shared(kernel, allowed[l.wide - 1], smem_optin);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(l.grid);
@@ -1041,7 +1069,7 @@ cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int s
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dense_layer_kernel, maps, p);
+  return cudaLaunchKernelEx(&cfg, kernel, maps, p);
 }
 
 }  // namespace sesg

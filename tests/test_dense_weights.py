@@ -363,6 +363,15 @@ def test_layer_sizes(B, d, f, E, k, ns, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("B,d,f,E,k,ns", [(50, 1464, 840, 22, 4, 1), (13, 1344, 1680, 4, 3, 2), (61, 2272, 280, 19, 8, 2),
+                                          (2, 2720, 496, 9, 3, 2), (40, 1512, 600, 60, 4, 0), (20, 512, 256, 250, 8, 1),
+                                          (33, 1032, 264, 1, 1, 1), (9, 776, 328, 255, 8, 0), (64, 264, 1160, 5, 5, 8)])
+def test_layer_tiles_and_routers(B, d, f, E, k, ns, dtype):
+    _layer_check(_layer_case(B, d, f, E, k, ns, dtype, True, True, True))
+
+
+@gpu
 def test_layer_of_the_largest_experts():
     """d = 16384, f = 65536: an expert's rows lie behind 2^31 elements."""
     d, f, E = 16384, 65536, 3
