@@ -799,8 +799,8 @@ int linear_stages(const LinearPlan& l, int M, bool gated, int smem, bool& own_x)
 //   each 64 k 155 + 3 NT (2048 x 2048, 16 tokens: 64 / 128 / 256 k a stage 11.9 / 9.5 / 8.3 us), and 60 more
 //   where its rows are shorter boxes;
 //   a product of 128 x NT x 16 takes NT / 2, and a quarter more with all SMs at it (the clock drops);
-//   joining a cluster's sums 3300 and 48 for each token and product; a tile's epilogue 1500 and 18 for
-//   each token and product, which runs under the next tile's products where TMEM holds both tiles;
+//   joining a cluster's sums 3300 and 48 for each token and product; a tile's epilogue 18 for
+//   each token and product and, but for the last, 1500; it runs under the next tile's products where TMEM holds both;
 //   a CTA pair's stage 650 with 256 columns, and 27 a column for its last epilogue, and HBM
 //   adds 0.25 of the weights' time (2048 x 14336 gated, K = 4096: 275 us against the model's 279; one CTA a
 //   tile 321; 300 tokens 80 and 80); 90 a column for the others,
@@ -869,11 +869,11 @@ LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int s
     for (const double least : {mma, (1950 + l2 + mma) / stages, 270 + wide * (155 + 3.0 * toks)})
       if (chunk < least) chunk = least;
     if (rows < kDnHalf) chunk += 60 * wide;
-    const double epi = 1500 + 18.0 * l.NT * (both ? 2 : 1);
+    const double last = 18.0 * l.NT * (both ? 2 : 1), epi = 1500 + last;
     const double products = (((KC + S - 1) / S) * chunk + (l2 + mma) / 2) * (P == 2 ? 1.05 : 1);
     double t = S > 1 ? products + 3300 + 48.0 * l.NT * (both ? 2 : 1)
-               : l.NT * (both ? 2 : 1) <= 256 ? waves * (products > epi ? products : epi) + epi
-                                              : waves * (products + epi);
+               : l.NT * (both ? 2 : 1) <= 256 ? waves * (products > epi ? products : epi) + last
+                                              : waves * (products + epi) - 1500;
     if (t < w_bytes / hbm) t = w_bytes / hbm;
     t *= wide == 1 ? 1 : wide == 2 ? 0.98 : 0.96;  // 216 KB in flight instead of 147
     keep(l, 7000 + t);
