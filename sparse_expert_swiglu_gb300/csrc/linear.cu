@@ -212,6 +212,9 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   if (PAIR || S > 1) cluster_sync_all();  // the barriers are there before any CTA of the cluster uses them
   tc_after_sync();
   const uint32_t tmem = bars->tmem;
+  // Before the wait: the next call's CTAs start while the last one's may still run (0.8 to 1.4 us of a short call behind
+  // another).  This library's kernels touch no global memory before their own wait, but for the decode gather kernel's x,
+  // which is complete when the kernel in front of it passes its wait.
   griddep_launch_dependents();
   griddep_wait();
 
