@@ -299,6 +299,9 @@ moe_status_t moe_prefetch_experts(const moe_experts_t* experts, const int32_t* i
  * Workspaces: the calls of this section may share one that is large enough for each, as long as they
  * are ordered on one stream; it is zero-filled once before its first use (moe_workspace_init), and
  * again after MOE_ERR_TIMEOUT.  It may not be shared with the calls of the other sections.
+ *
+ * A y that overlaps the call's weights, and a workspace that overlaps any tensor of the call, is refused
+ * (MOE_ERR_INVALID_ARG).
  */
 enum { MOE_F16 = 0, MOE_BF16 = 1, MOE_F32 = 2 };
 enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3, MOE_ACT_SILU = 4 };

@@ -19,6 +19,13 @@ inline bool overlaps(const void* y, size_t n, const void* p, size_t m) {
   return p && a < b + m && b < a + n;
 }
 
+// ... or with an expert stack's rows, which lie d or, interleaved, 2 d elements apart.
+bool overlaps(const void* y, size_t n, const moe_dense_experts_t& ex) {
+  const size_t rows = (size_t)ex.E * ex.f, d = ex.d;
+  const size_t apart = ex.down == ex.gate_t + d ? 2 * d : d, bytes = ((rows - 1) * apart + d) * 2;
+  return overlaps(y, n, ex.gate_t, bytes) || overlaps(y, n, ex.down, bytes) || overlaps(y, n, ex.up_t, rows * d * 2);
+}
+
 cudaError_t device_sizes(int& sms, int& smem) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -123,7 +130,13 @@ moe_status_t moe_linear(const moe_linear_t* op, void* ws, size_t ws_bytes, void*
   if ((op->y != op->residual || op->out_dtype != op->dtype) &&
       overlaps(op->y, out, op->residual, (size_t)op->M * op->N * 2))
     return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < linear_ws_bytes()) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const size_t head = linear_ws_bytes();
+  if (ws_bytes < head) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (overlaps(ws, head, op->y, out) || overlaps(ws, head, op->x, (size_t)op->M * op->K * 2) ||
+      overlaps(ws, head, op->w, wn) || overlaps(ws, head, op->w_mul, wn) ||
+      overlaps(ws, head, op->bias, (size_t)op->N * 2) || overlaps(ws, head, op->bias_mul, (size_t)op->N * 2) ||
+      overlaps(ws, head, op->residual, (size_t)op->M * op->N * 2))
+    return MOE_ERR_INVALID_ARG;
   int sms = 0, smem = 0;
   if (device_sizes(sms, smem) != cudaSuccess) return MOE_ERR_CUDA;
   LinearCall c = {};
@@ -166,13 +179,17 @@ moe_status_t moe_expert_dense_swiglu(const uint16_t* x, int32_t n, const moe_den
   if (!x || !y || !ws) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(ws, kWsAlign)) return MOE_ERR_ALIGNMENT;
   // x is read before the first value of y is written
-  if (y != residual && overlaps(y, (size_t)n * d * 2, residual, (size_t)n * d * 2)) return MOE_ERR_INVALID_ARG;
+  const size_t bytes = (size_t)n * d * 2, need = expert_ws(n, f);
+  if ((y != residual && overlaps(y, bytes, residual, bytes)) || overlaps(y, bytes, *experts)) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (overlaps(ws, need, x, bytes) || overlaps(ws, need, y, bytes) || overlaps(ws, need, residual, bytes) ||
+      overlaps(ws, need, *experts))
+    return MOE_ERR_INVALID_ARG;
   int sms = 0, smem = 0;
   if (device_sizes(sms, smem) != cudaSuccess) return MOE_ERR_CUDA;
   const int bf16 = experts->dtype == MOE_BF16;
   const DenseExpertSet one = to_set(*experts, expert);
   cudaStream_t st = (cudaStream_t)stream;
-  if (ws_bytes < expert_ws(n, f)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   // Two products.  Up to 64 tokens are bound by the weights' bytes, and a second row for each token costs
   // nothing: h goes to the second product as hi + lo, to 2^-16 (bf16) or 2^-22 (fp16).  For more tokens
   // it would cost the tensor cores twice the work, and h is rounded to the type.
@@ -225,11 +242,20 @@ moe_status_t moe_layer_dense_decode(const uint16_t* x, int32_t B, const moe_dens
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(ws, kWsAlign)) return MOE_ERR_ALIGNMENT;
   const size_t bytes = (size_t)B * layer->routed.d * 2;
   if (overlaps(y, bytes, x, bytes) || (y != residual && overlaps(y, bytes, residual, bytes))) return MOE_ERR_INVALID_ARG;
+  const size_t router = (size_t)layer->routed.d * layer->routed.E * 2;
+  auto in_weights = [&](const void* p, size_t n) {
+    return overlaps(p, n, layer->w_router, router) || overlaps(p, n, layer->routed) ||
+           (layer->shared.E > 0 && overlaps(p, n, layer->shared));
+  };
+  if (in_weights(y, bytes)) return MOE_ERR_INVALID_ARG;
   int sms = 0, smem = 0;
   if (device_sizes(sms, smem) != cudaSuccess) return MOE_ERR_CUDA;
   const moe_dense_experts_t& r = layer->routed;
-  if (ws_bytes < dense_layer_ws_bytes(B, r.d, r.f, r.E, layer->k, layer->shared.E, sms))
-    return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = dense_layer_ws_bytes(B, r.d, r.f, r.E, layer->k, layer->shared.E, sms);
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (overlaps(ws, need, x, bytes) || overlaps(ws, need, y, bytes) || overlaps(ws, need, residual, bytes) ||
+      in_weights(ws, need))
+    return MOE_ERR_INVALID_ARG;
   DenseLayerCall c = {};
   c.B = B;
   c.d = r.d;
