@@ -3,6 +3,7 @@
 
 #include <atomic>
 
+#include "layer_plan.h"
 #include "params.cuh"
 
 namespace sesg {
@@ -48,8 +49,6 @@ struct DenseLayerCall {
   int32_t* user_idx;                 // optional copies of the routing
   float* user_w;
 };
-
-constexpr int kDenseMaxTok = 64;
 
 size_t dense_layer_ws_bytes(int B, int d, int f, int E, int k, int ns, int sms);
 cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int smem_optin, cudaStream_t st);

@@ -9,6 +9,7 @@
 // count in global memory).  linear_plan chooses the tile and the cluster.
 #include "dense.cuh"
 #include "dense_params.cuh"
+#include "linear_plan.h"
 
 namespace sesg {
 
@@ -30,8 +31,6 @@ struct LinearArgs {
   int stages, acc_bufs, buf_cols, tmem_cols, stream;
   int own_x;        // the cluster's partial sums have memory of their own, behind the stages
 };
-
-constexpr int kTogether = 8;
 
 // Tile t's feature and token tile.  Tiles that run together share operands: eight token tiles at a time go
 // through all features, so that a wave of them is about as many features as tokens.
@@ -763,156 +762,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
   if (warp == 2) tmem_free_pair(tmem, 512);
 }
 
-struct LinearPlan {
-  int M = -1, N = 0, K = 0, gated = 0, kn = 0, plain = 0, sms = 0;  // what it is for
-  int by_token = 0;  // linear_pair_kernel
-  int P = 1, NT = 0, MT = 0, rows = 0, both = 0, wide = 1, S = 0, T = 0;
-};
-
-constexpr int kFewTokens = 32;
-
-// Clusters of S CTAs that fit the GPU at once, of at most one CTA per SM (152 SMs: 76, 36 and 15; the SMs of a
-// cluster lie in one part of the chip).
-int clusters(int S, int sms) { return S == 1 ? sms : S == 2 ? sms / 2 : S == 4 ? sms / 4 - 2 : sms / 8 - 4; }
-
-// Bytes of a cluster's partial sums in one CTA.
-int linear_sum_bytes(const LinearPlan& l, int M, bool gated) {
-  return (gated ? 2 : 1) * (((M < l.NT ? M : l.NT) + 3) / 4) * 4096;
-}
-
-// Stages of a CTA, and whether the partial sums have memory behind them (up to 16 KB).
-int linear_stages(const LinearPlan& l, int M, bool gated, int smem, bool& own_x) {
-  const int stage = l.wide * ((l.both ? kDnBytesA : kDnBytesA / 2) + l.NT / l.P * 128), sums = linear_sum_bytes(l, M, gated);
-  own_x = l.S > 1 && sums <= 16384;
-  const int room = smem - 1024 - (int)sizeof(DenseBars) - (own_x ? sums : 0);
-  const int n = room / stage;
-  return n > kDnMaxStages ? kDnMaxStages : n;
-}
-
-// The tile and the cluster with the least time by a model in SM clocks.  Its terms, as measured (GB300,
-// 1.9 GHz):
-//   a call costs 7000 whatever it does (256 x 512, one token: 3.8 us);
-//   an SM takes 62 bytes a clock from L2 (tiles of 128 x 128: 32 KB in 516 clocks), all SMs together
-//   3550 out of HBM, and where both are needed the lesser adds 0.15 of itself; rows that do not start
-//   on a line of 128 bytes take 1.35 times as long out of L2, and 1.8 times where they start inside a sector of
-//   32 (333 x 1024 by 128 x 32: K = 1000 8.9 us, K = 1024 7.0; 1017 x 7760 gated, K = 3280, pairs with 64 and 128 columns:
-//   537 and 704 clocks a stage instead of 370 and 650);
-//   a stage's bytes start to come 1950 after they are asked for (4096 x 4096, one token, 16 KB stages: six of them
-//   run at 383 clocks each, three 32 KB ones at 831), and a stage costs its issuing threads 270 and for
-//   each 64 k 155 + 3 NT (2048 x 2048, 16 tokens: 64 / 128 / 256 k a stage 11.9 / 9.5 / 8.3 us), and 60 more
-//   where its rows are shorter boxes;
-//   a product of 128 x NT x 16 takes NT / 2, and a quarter more with all SMs at it (the clock drops);
-//   joining a cluster's sums 3300 and 48 for each token and product; a tile's epilogue 18 for
-//   each token and product and, but for the last, 1500; it runs under the next tile's products where TMEM holds both;
-//   a CTA pair's stage 650 with 256 columns, and 27 a column for its last epilogue, and HBM
-//   adds 0.25 of the weights' time (2048 x 14336 gated, K = 4096: 275 us against the model's 279; one CTA a
-//   tile 321; 300 tokens 80 and 80); 90 a column for the others,
-//   which run under the next tile's products (384 x 7808 gated, GELU, K = 120: 7200 for 64 columns).
-LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int sms, int smem) {
-  LinearPlan best;
-  double best_t = 1e30;
-  const int chunks = (K + kDnChunk - 1) / kDnChunk, mats = gated ? 2 : 1;
-  const double w_bytes = 2.0 * mats * N * K, hbm = 3550;
-  auto keep = [&](const LinearPlan& l, double t) {
-    if (t < best_t) {
-      best_t = t;
-      best = l;
-    }
-  };
-  auto slow = [](int row) { return row % 64 == 0 ? 1.0 : row % 16 == 0 ? 1.35 : 1.8; };
-  const double slow_x = slow(K), slow_w = slow(kn ? N : K);
-  LinearPlan l;
-  if (plain && N % 8 == 0 && M > 64) {
-    // [K][N] weights come in boxes of 64 columns: narrower tiles would start inside a line (2048 x 4096, K = 14336: 148 us
-    // with 128 columns, 186 with 112, which would fill two whole waves; [N][K] 176 and 158)
-    for (int rows = 64; rows <= kDnHalf; rows += gated || kn ? 64 : 16) {
-      const int width = gated ? rows : 2 * rows, MT = (M + 255) / 256;
-      const long long T = (long long)MT * ((N + width - 1) / width);
-      if (T > (1 << 30) || (!gated && N <= rows)) continue;
-      l.by_token = 1;
-      l.S = 1;
-      l.T = (int)T;
-      l.MT = MT;
-      l.rows = rows;
-      const double waves = (double)((T + sms / 2 - 1) / (sms / 2)), chunk = 650.0 * rows / kDnHalf;
-      const double l2 = (kDnHalf * slow_x + rows * slow_w) * 128 / 62;
-      const double products = chunks * (chunk > l2 ? chunk : l2), epi = 90.0 * rows;
-      const double t = waves * (products > epi ? products : epi);
-      const double mem = w_bytes / hbm;
-      keep(l, 7000 + 27.0 * rows + (t > mem ? t + 0.25 * mem : mem + 0.25 * t));
-    }
-  }
-  auto consider = [&](int P, int NT, int rows, int both, int wide, int S) {
-    l.by_token = 0;
-    l.P = P;
-    l.wide = wide;
-    const int KC = (chunks + wide - 1) / wide;
-    l.MT = (M + NT - 1) / NT;
-    l.NT = ((M + l.MT - 1) / l.MT + 16 * P - 1) / (16 * P) * 16 * P;
-    l.rows = rows;
-    l.both = both;
-    l.S = S;
-    const int width = P * (gated || !both ? rows : 2 * rows), fit = clusters(P * S, sms), toks = l.NT / P;
-    const long long T = (long long)((N + width - 1) / width) * l.MT;
-    if (wide / 2 >= chunks) return;  // half of the stage would do
-    if (T > (1 << 30) || (both && !gated && N <= rows) || (P > 1 && N <= width / 2) || (S > 1 && (T > fit || S > KC))) return;
-    l.T = (int)T;
-    bool own_x;
-    const int stage = wide * ((both ? kDnBytesA : kDnBytesA / 2) + toks * 128);
-    const int stages = linear_stages(l, M, gated, smem, own_x);
-    if (stages < 2 || (S > 1 && !own_x && linear_sum_bytes(l, M, gated) > stages * stage)) return;
-    const double waves = (double)((T + fit - 1) / fit), active = (double)(T < fit ? T : fit) * S * P;
-    const double load = wide * ((both ? 2 : 1) * rows + toks) * 128.0, w_load = load - wide * toks * 128.0;
-    const double mma = wide * (both ? 2 : 1) * 4 * 1.25 * l.NT / 2;
-    const double l2 = (w_load * slow_w + (load - w_load) * slow_x) / 62;
-    // weights that several token tiles share come out of HBM little more than once: those tiles run together (32 x 4096 x
-    // 4096 as 16 + 16 tokens 13.2 us, as 32 11.3)
-    const double mem = w_load * active / hbm / (1 + 0.65 * ((l.MT < kTogether ? l.MT : kTogether) - 1));
-    double chunk = l2 > mem ? l2 + 0.15 * mem : mem + 0.15 * l2;
-    for (const double least : {mma, (1950 + l2 + mma) / stages, 270 + wide * (155 + 3.0 * toks)})
-      if (chunk < least) chunk = least;
-    if (rows < kDnHalf) chunk += 60 * wide;
-    const double last = 18.0 * l.NT * (both ? 2 : 1), epi = 1500 + last;
-    const double products = (((KC + S - 1) / S) * chunk + (l2 + mma) / 2) * (P == 2 ? 1.05 : 1);
-    double t = S > 1 ? products + 3300 + 48.0 * l.NT * (both ? 2 : 1)
-               : l.NT * (both ? 2 : 1) <= 256 ? waves * (products > epi ? products : epi) + last
-                                              : waves * (products + epi) - 1500;
-    if (t < w_bytes / hbm) t = w_bytes / hbm;
-    t *= wide == 1 ? 1 : wide == 2 ? 0.98 : 0.96;  // 216 KB in flight instead of 147
-    keep(l, 7000 + t);
-  };
-  const int top = M < 256 ? (M + 15) / 16 * 16 : 256;
-  for (int both = gated ? 1 : 0; both < 2; ++both)
-    for (int rows = both && !gated ? kDnHalf : kn ? 64 : 32; rows <= kDnHalf && (rows < N + 64 || rows <= 64); rows += kn ? 64 : 32)
-      for (int NT = 16; NT <= top; NT += 16)
-        for (int S = 1; S <= 8; S *= 2)
-          for (int wide = 1; wide <= 4; wide *= 2) {
-            consider(1, NT, rows, both, wide, S);
-            if (M > 64 && NT % 32 == 0 && S <= 4) consider(2, NT, rows, both, wide, S);
-          }
-  best.M = M;
-  best.N = N;
-  best.K = K;
-  best.gated = gated;
-  best.kn = kn;
-  best.plain = plain;
-  best.sms = sms;
-  return best;
-}
-
-// The plan goes by the sizes alone.  A thread keeps the plans of the sizes that it used last: a
-// model's calls come again with every token.
-const LinearPlan& linear_plan(int M, int N, int K, bool gated, bool kn, bool plain, int sms, int smem) {
-  constexpr int kKept = 64;
-  static thread_local LinearPlan kept[kKept];
-  const uint32_t at = ((uint32_t)M * 2654435761u ^ (uint32_t)N * 2246822519u ^ (uint32_t)K * 3266489917u ^
-                       (uint32_t)(gated * 4 + kn * 2 + plain) * 668265263u) >> 26;
-  LinearPlan& l = kept[at % kKept];
-  if (l.M != M || l.N != N || l.K != K || l.gated != gated || l.kn != kn || l.plain != plain || l.sms != sms)
-    l = make_plan(M, N, K, gated, kn, plain, sms, smem);
-  return l;
-}
-
 constexpr size_t kHeadBytes = (sizeof(DenseHead) + 255) / 256 * 256;
 
 }  // namespace
@@ -968,7 +817,8 @@ static cudaError_t launch_linear_pair(const LinearCall& c, const LinearPlan& l, 
 
 cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin, cudaStream_t st) {
   const bool gated = c.w_mul != nullptr;
-  const LinearPlan& l = linear_plan(c.M, c.N, c.K, gated, c.kn, !c.split && !c.pairs, sms, smem_optin);
+  const int room = smem_optin - 1024 - (int)sizeof(DenseBars);
+  const LinearPlan& l = linear_plan(c.M, c.N, c.K, gated, c.kn, !c.split && !c.pairs, sms, room);
   if (!l.S) return cudaErrorInvalidValue;
   if (l.by_token) return launch_linear_pair(c, l, ws, sms, smem_optin, st);
   CUtensorMap mw, mw2, mx;
@@ -1007,7 +857,7 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   p.head = reinterpret_cast<DenseHead*>(ws);
   const int stage = l.wide * ((l.both ? kDnBytesA : kDnBytesA / 2) + l.NT / l.P * 128), cols_of = (l.both ? 2 : 1) * l.NT;
   bool own_x;
-  p.stages = linear_stages(l, c.M, gated, smem_optin, own_x);
+  p.stages = linear_stages(l, c.M, gated, room, own_x);
   p.own_x = own_x;
   p.acc_bufs = cols_of <= 256 && l.S == 1 && l.T > sms / l.P ? 2 : 1;  // two where a CTA has more than one tile
   // fp32 results: several accumulators, so that each adds up fewer products (the tensor core's
