@@ -8,7 +8,7 @@
 namespace sesg {
 
 struct LinearPlan {
-  int M = -1, N = 0, K = 0, gated = 0, kn = 0, plain = 0, sms = 0;  // what it is for
+  int M = -1, N = 0, K = 0, gated = 0, kn = 0, plain = 0, sms = 0, room = 0;  // what it is for
   int by_token = 0;  // linear_pair_kernel
   int P = 1, NT = 0, MT = 0, rows = 0, both = 0, wide = 1, S = 0, T = 0;
 };
@@ -141,20 +141,41 @@ inline LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain
   best.kn = kn;
   best.plain = plain;
   best.sms = sms;
+  best.room = room;
   return best;
 }
 
-// The plan goes by the sizes alone.  A thread keeps the plans of the sizes that it used last: a
-// model's calls come again with every token.
+// The plan goes by the sizes alone.  A thread keeps the plans of the sizes that it used last, since a model's calls come
+// again with every token: 16 sets of 8, of which a new plan takes the place of the one that was asked for longest
+// ago.  The sizes are mixed one into the other: two calls with the same M (the products of an expert) must not fall into
+// one set for every M.
 inline const LinearPlan& linear_plan(int M, int N, int K, bool gated, bool kn, bool plain, int sms, int room) {
-  constexpr int kKept = 64;
-  static thread_local LinearPlan kept[kKept];
-  const uint32_t at = ((uint32_t)M * 2654435761u ^ (uint32_t)N * 2246822519u ^ (uint32_t)K * 3266489917u ^
-                       (uint32_t)(gated * 4 + kn * 2 + plain) * 668265263u) >> 26;
-  LinearPlan& l = kept[at % kKept];
-  if (l.M != M || l.N != N || l.K != K || l.gated != gated || l.kn != kn || l.plain != plain || l.sms != sms)
-    l = make_plan(M, N, K, gated, kn, plain, sms, room);
-  return l;
+  constexpr int kSets = 16, kWays = 8;
+  struct Kept {
+    LinearPlan plan[kWays];
+    uint64_t used[kWays] = {};
+  };
+  static thread_local Kept sets[kSets];
+  static thread_local uint64_t now = 0;
+  uint64_t h = 0;
+  for (const int v : {M, N, K, (int)gated * 4 + (int)kn * 2 + (int)plain}) {
+    h = (h ^ (uint32_t)v) * 0x9E3779B97F4A7C15ull;
+    h ^= h >> 29;
+  }
+  Kept& s = sets[h % kSets];
+  int oldest = 0;
+  for (int i = 0; i < kWays; ++i) {
+    const LinearPlan& l = s.plan[i];
+    if (l.M == M && l.N == N && l.K == K && l.gated == gated && l.kn == kn && l.plain == plain && l.sms == sms &&
+        l.room == room) {
+      s.used[i] = ++now;
+      return l;
+    }
+    if (s.used[i] < s.used[oldest]) oldest = i;
+  }
+  s.plan[oldest] = make_plan(M, N, K, gated, kn, plain, sms, room);
+  s.used[oldest] = ++now;
+  return s.plan[oldest];
 }
 
 }  // namespace sesg

@@ -1,0 +1,93 @@
+"""The plans of the calls on uncompressed weights, compiled by the host compiler alone: what a thread keeps, and what a
+layer's workspace holds.  152 SMs and 227 KB of shared memory, as the GPU has."""
+
+from __future__ import annotations
+
+import ctypes
+import itertools
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from tests.conftest import ROOT
+
+SHIM = r"""
+#include "linear_plan.h"
+#include "layer_plan.h"
+using namespace sesg;
+constexpr int kSms = 152, kRoom = 232448 - 1024 - 256;
+static const LinearPlan& plan(const int* c, int room) {
+  return linear_plan(c[0], c[1], c[2], c[3], c[4], c[5], kSms, room);
+}
+extern "C" {
+// asks for n plans (M, N, K, gated, kn, plain) one after the other; how many of them are still kept then
+int plans_kept(const int* c, int n) {
+  const LinearPlan* at[1024];
+  for (int i = 0; i < n; ++i) at[i] = &plan(c + 6 * i, kRoom);
+  int kept = 0;
+  for (int i = 0; i < n; ++i) {
+    const int* q = c + 6 * i;
+    kept += at[i]->M == q[0] && at[i]->N == q[1] && at[i]->K == q[2] && at[i]->gated == q[3] && at[i]->kn == q[4] &&
+            at[i]->plain == q[5];
+  }
+  return kept;
+}
+// stages of the chosen tile for `room` bytes, after a call with `before` bytes
+int stages_for(const int* c, int before, int room) {
+  plan(c, before);
+  bool own_x;
+  const LinearPlan& l = plan(c, room);
+  return linear_stages(l, c[0], c[3], room, own_x);
+}
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def plans(tmp_path_factory):
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        pytest.skip("no host compiler")
+    d = tmp_path_factory.mktemp("plans")
+    src, so = d / "shim.cpp", d / "shim.so"
+    src.write_text(SHIM)
+    csrc = os.path.join(ROOT, "sparse_expert_swiglu_gb300", "csrc")
+    subprocess.run([cxx, "-std=c++17", "-O2", "-Wall", "-fPIC", "-shared", "-I", csrc, str(src), "-o", str(so)], check=True)
+    return ctypes.CDLL(str(so))
+
+
+def _ints(cases):
+    flat = list(itertools.chain.from_iterable(cases))
+    return (ctypes.c_int * len(flat))(*flat)
+
+
+def _expert(n, d, f):
+    """The two products of an expert on n tokens: gate and up with a split result or not, then down on pairs or not."""
+    two = n <= 64
+    return [(n, f, d, 1, 0, int(not two)), (2 * n if two else n, d, f, 0, 1, int(not two))]
+
+
+@pytest.mark.parametrize("d,f", [(5120, 8192), (4096, 14336), (2048, 1408), (6144, 16384), (4096, 4096), (8192, 8192)])
+def test_both_products_of_an_expert_are_kept(plans, d, f):
+    for n in list(range(1, 600, 7)) + [1024, 2048]:
+        assert plans.plans_kept(_ints(_expert(n, d, f)), 2) == 2, n
+
+
+def test_a_models_products_are_kept(plans):
+    """One token count at a time: projections, dense block, output head and experts of a model."""
+    for n in (1, 2, 3, 7, 16, 64, 65, 100, 256, 300, 512, 2048):
+        for d, f, vocab in ((4096, 14336, 32000), (2048, 1408, 102400), (6144, 16384, 32768)):
+            cases = [(n, d, d, 0, 0, 1), (n, d + d // 4, d, 0, 0, 1), (n, vocab, d, 0, 0, 1), (n, f, d, 1, 0, 1),
+                     (n, d, f, 0, 1, 1), (n, d, f, 0, 0, 1), (n, 8, d, 0, 1, 1), (n, 64, d, 0, 1, 1)] + _expert(n, d, f)
+            cases = list(dict.fromkeys(cases))
+            assert plans.plans_kept(_ints(cases), len(cases)) == len(cases), (n, d)
+
+
+def test_a_plan_goes_by_the_shared_memory_too(plans):
+    """The same sizes with half the shared memory: the tile's stages fit."""
+    case = _ints([(1024, 4095, 4096, 0, 0, 1)])
+    room = 232448 - 1024 - 256
+    assert plans.stages_for(case, room, room) >= 2
+    assert plans.stages_for(case, room, room // 4) >= 2
