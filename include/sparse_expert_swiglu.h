@@ -297,8 +297,8 @@ moe_status_t moe_prefetch_experts(const moe_experts_t* experts, const int32_t* i
  * equal bits.  16-bit tensors are passed as uint16_t (or void*) bit patterns; one call has one type.
  *
  * Workspaces: the calls of this section may share one that is large enough for each, as long as they
- * are ordered on one stream; it is zero-filled once before its first use (moe_workspace_init), and
- * again after MOE_ERR_TIMEOUT.  It may not be shared with the calls of the other sections.
+ * are ordered on one stream; it is zero-filled once before its first use (moe_workspace_init; its first
+ * moe_linear_workspace_bytes(1, 1, 8, 0) bytes are enough), and again after MOE_ERR_TIMEOUT.  It may not be shared with the calls of the other sections.
  *
  * A y that overlaps the call's weights, and a workspace that overlaps any tensor of the call, is refused
  * (MOE_ERR_INVALID_ARG).

@@ -194,12 +194,14 @@ def _need(t: torch.Tensor, dtype, name: str, host_ok: bool = False) -> torch.Ten
 # ---------------------------------------------------------------------------
 
 class Workspace:
-    """A zero-initialised device workspace (256-byte aligned torch allocation)."""
+    """A zero-initialised device workspace (256-byte aligned torch allocation).  clear: that only so many bytes at its
+    start are filled with zeros."""
 
-    def __init__(self, nbytes: int, device=None):
+    def __init__(self, nbytes: int, device=None, clear: Optional[int] = None):
         self.nbytes = int(nbytes)
         self.buf = torch.empty(max(self.nbytes, 256), dtype=torch.uint8, device=device or "cuda")
-        _check("moe_workspace_init", lib().moe_workspace_init(_ptr(self.buf), self.buf.numel(), _stream()))
+        size = self.buf.numel() if clear is None else min(clear, self.buf.numel())
+        _check("moe_workspace_init", lib().moe_workspace_init(_ptr(self.buf), size, _stream()))
 
     def ptr(self):
         return _ptr(self.buf)
@@ -575,12 +577,12 @@ except ImportError:
 
 
 def _dense_ws(ws, device: int, nbytes, *sizes) -> "Workspace":
-    """The caller's workspace, or a new one of nbytes(*sizes)."""
+    """The caller's workspace, or a new one of nbytes(*sizes), of which the counts at its start have to be zero."""
     if ws is None:
         n = nbytes(*sizes)
         if n == 0:
             raise ValueError("sizes outside the supported range")
-        return Workspace(n, torch.device("cuda", device))
+        return Workspace(n, torch.device("cuda", device), clear=linear_workspace_bytes(1, 1, 8))
     if ws.buf.get_device() != device:
         raise ValueError(f"ws must be on cuda:{device}")
     return ws

@@ -39,8 +39,9 @@ struct LayerArgs {
   int* top_idx;        // [B][k]
   float* top_w;
   unsigned short* h;   // [groups][hi, lo][8][f]
-  float* part;         // [segment][gate, up][64][128]
-  float* ypart;        // [share][8 groups][d]
+  float* part;         // first phase: [segment][gate, up][64][128]; second: [segment][B][256]
+  float* ysum;         // [sum row][d]
+  size_t cut;          // floats from ysum to part
   float* yrow;         // [B][d] sums before RMSNorm
   float* ysq;          // [B][128 features][4 warps] their squares
   int slots;           // 8 * max_groups
@@ -60,12 +61,13 @@ struct LayerMisc {
   short act[kMaxActive];                 // active experts: shared ones (E + s) first
   short cnt[kMaxActive];                 // ... tokens
   short grp[kMaxActive];                 // ... first group of 8 slots
+  short sum[kMaxActive];                 // ... first row of sums
   int n_act;
   int last;
   int fail;
   int idx[kDenseMaxTok * 8];
   float w[kDenseMaxTok * 8];
-  short row[kDenseMaxTok * kMaxPairSlots];    // slot of each (token, choice)
+  short row[kDenseMaxTok * kMaxPairSlots];    // sum row of each (token, choice)
   short place[kDenseMaxTok * kMaxPairSlots];  // active expert of each (token, choice)
   // a token's partial sums: where they begin and their weights
   size_t from[kJoinGroups][kMaxPairSlots * (kDnMaxSplit + 1)];
@@ -318,6 +320,7 @@ __device__ void make_lists(const LayerArgs& p, LayerMisc& m, uint8_t* tok) {
           m.act[a] = (short)e;
           m.cnt[a] = (short)__popcll(mask);
           m.grp[a] = (short)a;
+          m.sum[a] = (short)(8 * a);
         }
       } else {
         a = (tid - pairs) / p.B;
@@ -327,6 +330,7 @@ __device__ void make_lists(const LayerArgs& p, LayerMisc& m, uint8_t* tok) {
           m.act[a] = (short)(p.E + a);
           m.cnt[a] = (short)p.B;
           m.grp[a] = (short)a;
+          m.sum[a] = (short)(8 * a);
         }
       }
       tok[a * 8 + before] = (uint8_t)b;
@@ -348,13 +352,14 @@ __device__ void make_lists(const LayerArgs& p, LayerMisc& m, uint8_t* tok) {
       m.act[lane] = (short)(p.E + lane);
       m.cnt[lane] = (short)p.B;
       m.grp[lane] = (short)(lane * gs);
+      m.sum[lane] = (short)(lane * p.B);
     }
-    int na = p.ns, ng = p.ns * gs;
+    int na = p.ns, ng = p.ns * gs, nt = p.ns * p.B;
     for (int base = 0; base < p.E; base += 32) {
       const int e = base + lane;
       const int n = e < p.E ? __popcll(m.mask[e]) : 0, g = (n + 7) / 8;
       const uint32_t on = __ballot_sync(0xffffffffu, n > 0);
-      int sg = g;
+      int sg = g << 16 | n;  // at most 64 groups and 32 * 64 tokens in a step
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, sg, off);
@@ -364,26 +369,29 @@ __device__ void make_lists(const LayerArgs& p, LayerMisc& m, uint8_t* tok) {
         const int a = na + __popc(on & ((1u << lane) - 1));
         m.act[a] = (short)e;
         m.cnt[a] = (short)n;
-        m.grp[a] = (short)(ng + sg - g);
+        m.grp[a] = (short)(ng + (sg >> 16) - g);
+        m.sum[a] = (short)(nt + (sg & 0xffff) - n);
         m.where[e] = (short)a;
       }
       na += __popc(on);
-      ng += __shfl_sync(0xffffffffu, sg, 31);
+      sg = __shfl_sync(0xffffffffu, sg, 31);
+      ng += sg >> 16;
+      nt += sg & 0xffff;
     }
     if (lane == 0) m.n_act = na;
   }
   __syncthreads();
   for (int i = tid; i < pairs; i += kDnThreads) {
     const int b = i / p.k, j = i - b * p.k, e = m.idx[i], a = m.where[e];
-    const int row = m.grp[a] * 8 + __popcll(m.mask[e] & ((1ull << b) - 1));
-    tok[row] = (uint8_t)b;
-    m.row[b * kMaxPairSlots + j] = (short)row;
+    const int before = __popcll(m.mask[e] & ((1ull << b) - 1));
+    tok[m.grp[a] * 8 + before] = (uint8_t)b;
+    m.row[b * kMaxPairSlots + j] = (short)(m.sum[a] + before);
     m.place[b * kMaxPairSlots + j] = (short)a;
   }
   for (int i = tid; i < p.B * p.ns; i += kDnThreads) {
-    const int s = i / p.B, b = i - s * p.B, row = s * gs * 8 + b;
-    tok[row] = (uint8_t)b;
-    m.row[b * kMaxPairSlots + p.k + s] = (short)row;
+    const int s = i / p.B, b = i - s * p.B;
+    tok[s * gs * 8 + b] = (uint8_t)b;
+    m.row[b * kMaxPairSlots + p.k + s] = (short)(s * p.B + b);
     m.place[b * kMaxPairSlots + p.k + s] = (short)s;
   }
   __syncthreads();
@@ -546,11 +554,16 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   const int u0 = cta * kJoinGroups + grp, ustep = gridDim.x * kJoinGroups;
   auto list_sums = [&](int u, int grp) {
     const int b = u / HT, dt = (u - b * HT) / 2;
-    int a = 0, slot = 0, parts = 0;
+    int parts = 0;
+    size_t from = 0, step = 0;
     if (lane < p.k + p.ns) {
-      a = m.place[b * kMaxPairSlots + lane];
-      slot = m.row[b * kMaxPairSlots + lane];
-      parts = s2.parts(a * DT + dt);
+      const int a = m.place[b * kMaxPairSlots + lane], row = m.row[b * kMaxPairSlots + lane], t = a * DT + dt;
+      parts = s2.parts(t);
+      from = (size_t)row * p.d;
+      if (parts > 1) {
+        step = (size_t)p.B * 2 * kDnHalf;
+        from = p.cut + (t - s2.dp + s2.first(t)) * step + (row - m.sum[a]) * 2 * kDnHalf - dt * 2 * kDnHalf;
+      }
     }
     int end = parts;
 #pragma unroll
@@ -559,7 +572,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       if (lane >= off) end += o;
     }
     for (int s = 0; s < parts; ++s) {
-      m.from[grp][end - parts + s] = ((size_t)s * p.slots + slot) * p.d;
+      m.from[grp][end - parts + s] = from + s * step;
       m.weight[grp][end - parts + s] = lane < p.k ? m.w[b * p.k + lane] : 1.f;
     }
     if (lane == 15) m.n_from[grp] = end;
@@ -788,18 +801,21 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
         if (!good) dn_fail(bars, status);
         if (dn_any(1, kDnEpi, !good)) break;
         tc_after_sync();
-        const int a = g.t / DT, n = m.cnt[a], slot = m.grp[a] * 8;
+        const int a = g.t / DT, n = m.cnt[a];
         const int feat = (g.t - a * DT) * 2 * kDnHalf + half * kDnHalf + r;
         const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + buf * 256 + half * 128;
-        const int share = s2.parts(g.t) == 1 ? 0 : cta - s2.first(g.t);
-        float* out = p.ypart + ((size_t)share * p.slots + slot) * p.d + feat;
+        // a whole tile's sums to the tokens' rows, a share's to its place among the shares
+        const bool cut = s2.parts(g.t) > 1;
+        const size_t step = cut ? 2 * kDnHalf : p.d;
+        float* out = cut ? p.part + (size_t)(g.t - s2.dp + cta) * p.B * 2 * kDnHalf + half * kDnHalf + r
+                         : p.ysum + (size_t)m.sum[a] * p.d + feat;
         for (int n0 = 0; n0 < n; n0 += 8) {  // columns: 8 tokens' hi, then their lo
           float v[16];
           tmem_ld(t0 + 2 * n0, v);
           tmem_wait(v);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (n0 + i < n && feat < p.d) __stcg(out + (size_t)(n0 + i) * p.d, v[i] + v[i + 8]);
+            if (n0 + i < n && feat < p.d) __stcg(out + (n0 + i) * step, v[i] + v[i + 8]);
           __syncwarp();
         }
         tc_before_sync();
@@ -840,7 +856,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       for (int i = 0; i < n; i += 16) {
         float t[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) t[j] = i + j < n ? __ldcg(p.ypart + m.from[grp][i + j] + feat) : 0.f;
+        for (int j = 0; j < 16; ++j) t[j] = i + j < n ? __ldcg(p.ysum + m.from[grp][i + j] + feat) : 0.f;
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           if (i + j < n) acc = fmaf(m.weight[grp][i + j], t[j], acc);
@@ -938,7 +954,8 @@ cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int s
   p.top_w = reinterpret_cast<float*>(w8 + l.top_w);
   p.h = reinterpret_cast<unsigned short*>(w8 + l.h);
   p.part = reinterpret_cast<float*>(w8 + l.part);
-  p.ypart = reinterpret_cast<float*>(w8 + l.ypart);
+  p.ysum = reinterpret_cast<float*>(w8 + l.ysum);
+  p.cut = (l.part - l.ysum) / 4;
   p.yrow = reinterpret_cast<float*>(w8 + l.yrow);
   p.ysq = reinterpret_cast<float*>(w8 + l.ysq);
   p.slots = l.groups * 8;

@@ -11,14 +11,19 @@ constexpr int kFewTok = 8;                       // up to here every CTA chooses
 
 // Groups of 8 slots that the active experts' tokens fill, at most.
 inline int max_groups(int B, int E, int k, int ns) {
-  const int pairs = B * k, by_e = (E < pairs ? E : pairs) + pairs / 8;
-  return (pairs < by_e ? pairs : by_e) + ns * ((B + 7) / 8);
+  const int pairs = B * k, active = E < pairs ? E : pairs;  // one for each active expert, another for every 8 more pairs
+  return active + (pairs - active) / 8 + ns * ((B + 7) / 8);
+}
+
+// Rows of the second phase's sums: one for each (token, expert) pair; of a few tokens one for each slot.
+inline int sum_rows(int B, int E, int k, int ns) {
+  return B <= kFewTok ? 8 * max_groups(B, E, k, ns) : B * (k + ns);
 }
 
 struct LayerPlan {
   int B = -1, d, f, E, k, ns, sms;
   int groups, slices, grid, rows, wide, early;
-  size_t logits, top_idx, top_w, h, part, yrow, ysq, ypart, total;
+  size_t logits, top_idx, top_w, h, part, yrow, ysq, ysum, total;
 };
 
 constexpr int kSmem = 232448;  // that the plan reckons with
@@ -81,13 +86,13 @@ inline const LayerPlan& layer_plan(int B, int d, int f, int E, int k, int ns, in
   // HBM brings 128 rows in 0.7), two chunks go into one (63 tokens of 6 x 1664, 72 rows: 76.8 us with one, 71.6 with two).
   l.wide = l.rows <= 80 && 3.0 / layer_stages(B, l.rows, 1, l.groups * 8, misc, kSmem) > l.rows / 128.0 ? 2 : 1;
   // the number of active experts is known on the device only: the largest need of any
-  int segs = 0, parts = 1;
+  int segs1 = 0, segs2 = 0;
   const int KC1 = (chunks + l.wide - 1) / l.wide;
   const int FT = (f + l.rows - 1) / l.rows;
   for (int a = 0; a <= most; ++a) {
     const Sched s1 = Sched::make((a + ns) * FT, KC1, sms, l.early), s2 = Sched::make((a + ns) * DT, KC2, sms, 0);
-    if (s1.segments() > segs) segs = s1.segments();
-    if (s2.max_parts() > parts) parts = s2.max_parts();
+    if (s1.segments() > segs1) segs1 = s1.segments();
+    if (s2.segments() > segs2) segs2 = s2.segments();
   }
   size_t o = (head + 255) / 256 * 256;
   auto take = [&](size_t bytes) {
@@ -99,10 +104,13 @@ inline const LayerPlan& layer_plan(int B, int d, int f, int E, int k, int ns, in
   l.top_idx = take((size_t)B * k * 4);
   l.top_w = take((size_t)B * k * 4);
   l.h = take((size_t)l.groups * 16 * f * 2);
-  l.part = take((size_t)segs * kPartFloats * 4);
   l.yrow = take((size_t)B * d * 4);
   l.ysq = take((size_t)B * 2 * DT * 16);
-  l.ypart = take((size_t)parts * l.groups * 8 * d * 4);
+  // the second phase's sums: of whole tiles by token and expert, then the shares of cut tiles, which take the place
+  // of the first phase's shares (all of those are read before any CTA has h for its second phase)
+  l.ysum = take((size_t)sum_rows(B, E, k, ns) * d * 4);
+  const size_t part1 = (size_t)segs1 * kPartFloats * 4, part2 = (size_t)segs2 * B * 2 * kDnHalf * 4;
+  l.part = take(part1 > part2 ? part1 : part2);
   l.total = o;
   return l;
 }

@@ -41,6 +41,9 @@ int stages_for(const int* c, int before, int room) {
   const LinearPlan& l = plan(c, room);
   return linear_stages(l, c[0], c[3], room, own_x);
 }
+size_t layer_bytes(int B, int d, int f, int E, int k, int ns) {
+  return layer_plan(B, d, f, E, k, ns, kSms, 23 << 10, 4736).total;
+}
 }
 """
 
@@ -91,3 +94,35 @@ def test_a_plan_goes_by_the_shared_memory_too(plans):
     room = 232448 - 1024 - 256
     assert plans.stages_for(case, room, room) >= 2
     assert plans.stages_for(case, room, room // 4) >= 2
+
+
+# ---------------------------------------------------------------------------
+# a layer's workspace
+# ---------------------------------------------------------------------------
+
+def _layer_bytes(plans, B, d, f, E, k, ns):
+    plans.layer_bytes.restype = ctypes.c_size_t
+    return plans.layer_bytes(B, d, f, E, k, ns)
+
+
+@pytest.mark.parametrize("B,d,f,E,k,ns,mb", [(64, 2048, 1408, 64, 6, 2, 40), (64, 7168, 2048, 256, 8, 1, 100),
+                                             (1, 4096, 14336, 8, 2, 0, 25), (17, 4096, 14336, 8, 2, 0, 25),
+                                             (64, 16384, 65536, 256, 8, 8, 1000)])
+def test_layer_workspace_bytes(plans, B, d, f, E, k, ns, mb):
+    assert _layer_bytes(plans, B, d, f, E, k, ns) < mb * 1e6
+
+
+def test_layer_workspace_holds_one_sum_a_pair_and_the_cut_tiles(plans):
+    """Twice what cannot be done without (h of every token's experts as two rows in groups of 8, their fp32 sums, the
+    logits), and 64 KB for each of at most 2 x 152 shares of cut tiles."""
+    import random
+    rng = random.Random(4)
+    for _ in range(300):
+        B, E = rng.randint(1, 64), rng.randint(1, 256)
+        k, ns = rng.randint(1, min(8, E)), rng.randint(0, 8)
+        d, f = 8 * rng.randint(1, 1024), 8 * rng.randint(1, 2048)
+        pairs, active = B * k, min(E, B * k)
+        groups = active + (pairs - active) // 8 + ns * ((B + 7) // 8)
+        rows = 8 * groups if B <= 8 else pairs + B * ns
+        need = groups * 16 * f * 2 + rows * d * 4 + B * 16 * E * 4 + B * d * 4
+        assert _layer_bytes(plans, B, d, f, E, k, ns) <= 1.05 * need + 2 * 152 * 65536 + 65536, (B, d, f, E, k, ns)
