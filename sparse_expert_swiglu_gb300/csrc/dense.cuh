@@ -139,6 +139,20 @@ __device__ __forceinline__ void tmem_wait(float (&v)[W]) {
   for (int i = 0; i < W; ++i) asm volatile("" : "+f"(v[i]));
 }
 
+// 16 columns of this warp's 32 lanes; tmem_stored waits for this thread's stores
+__device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[16]) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // One thread of the warp.  (The compiler then knows that what follows runs in one thread: products and
 // copies take their operands from uniform registers, and with `lane == 0` in its place each cost over 100 clocks.)
 __device__ __forceinline__ bool elect_one() {

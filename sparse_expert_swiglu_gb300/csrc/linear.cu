@@ -24,7 +24,8 @@ struct LinearArgs {
   int KC, S;        // stages of a tile, CTAs (or CTA pairs) that share it along k
   int split;        // y as two 16-bit rows for each token, 2 t and 2 t + 1: the rounded value and the rest
   int pairs;        // x has two such rows for each token of y
-  int groups;       // accumulators of a product: stage c of a tile goes to c % groups
+  int groups;       // accumulators of a product: stage c of a round goes to c % groups
+  int per;          // stages of a round (with KEEP)
   const void *bias, *bias_mul, *residual;
   void* y;
   DenseHead* head;
@@ -158,13 +159,37 @@ __device__ __forceinline__ void linear_sums(uint32_t addr, int groups, int strid
   }
 }
 
+constexpr uint32_t kNoBlock = 0xffffffffu;
+
+// A round's sums of this warp's blocks of 16 columns (at(b): the address of block b, kNoBlock: there is none), added to
+// those of the rounds before; the last round's go back to where they were.  N columns at a time: as many as leave the
+// kernel without a stack frame, with which a call takes 3.5 us longer.
+template <int N, typename At>
+__device__ __forceinline__ void linear_round(float (&acc)[8][16], bool last, At at) {
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    const uint32_t a = at(b);
+    if (a == kNoBlock) continue;  // the same for the whole warp
+#pragma unroll
+    for (int h = 0; h < 16; h += N) {
+      float v[N];
+      tmem_ld(a + h, v);
+      tmem_wait(v);
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[b][h + i] += v[i];
+    }
+    if (last) tmem_st(a, acc[b]);
+  }
+}
+
 // FEW: up to kFewTokens tokens and one tile for each CTA, whose epilogue takes 4 tokens at a time: a call this short
 // pays for every line of code it fetches.  PAIR: CTA pairs (cta_group::2).  A tile then has up to 256 lanes for each product, 128 in each
 // CTA, and either CTA fetches and keeps half of its tokens: with 100 to 500 tokens, where the bytes that
 // an SM can take from L2 bound the products (300 tokens of 14336 gated features of K = 4096: 72 us, 78 without).
 // SHARED: clusters share a tile along k; the one epilogue is not fetched with the other (an expert on 100 tokens, 2048 x
 // 1408: 20.8 us against 21.9).
-template <bool FEW, bool PAIR, bool SHARED>
+// KEEP: a tile's stages in rounds (LinearSums), whose sums this warp's threads add up; never with FEW.
+template <bool FEW, bool PAIR, bool SHARED, bool KEEP>
 __global__ void __launch_bounds__(kDnThreads, 1)
 linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mw2,
               const __grid_constant__ CUtensorMap mx, const LinearArgs p) {
@@ -185,7 +210,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int S = SHARED ? p.S : 1, ns = p.stages, NT = p.NT;
   const int crank = PAIR || S > 1 ? (int)cluster_rank() : 0, half_of = PAIR ? crank & 1 : 0, lead = crank - half_of;
-  const int rank = crank / P;                                              // share of k
+  const int rank = SHARED ? crank / P : 0;                                 // share of k
   const int first = blockIdx.x / (P * S), step = gridDim.x / (P * S);  // tiles of this CTA; S > 1: one
   const int kc0 = p.KC * rank / S, kc1 = p.KC * (rank + 1) / S;
   const int width = p.gated || !p.both ? p.rows : 2 * p.rows;  // features of a CTA in a tile
@@ -291,37 +316,41 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
       uint32_t ph = 0, tph = 0;
       bool ok = true, open = false;
       for (int t = first; ok && t < p.T; t += step) {
-        if (!(PAIR ? cluster_wait(&bars->tempty[buf], tph ^ 1, abort) : dn_wait(&bars->tempty[buf], tph ^ 1, abort))) {
-          dn_fail(bars, status);
-          break;
-        }
-        tc_after_sync();
-        int grp = 0;
-        for (int kc = kc0; kc < kc1; ++kc) {
-          if (!dn_wait(&bars->full[st], ph, abort)) {
+        for (int kr = kc0, end; ok && kr < kc1; kr = end) {
+          end = KEEP && kr + p.per < kc1 ? kr + p.per : kc1;
+          if (!(PAIR ? cluster_wait(&bars->tempty[buf], tph ^ 1, abort) : dn_wait(&bars->tempty[buf], tph ^ 1, abort))) {
             dn_fail(bars, status);
             ok = false;
             break;
           }
           tc_after_sync();
-          const uint32_t a = ring_at + st * stage_bytes;
-          const uint32_t d0 = tmem + buf * p.buf_cols + grp * grp_cols;
-          for (int c = 0; c < p.wide; ++c)
-            dn_stage_products<PAIR>(a + c * chunk_bytes, a + c * chunk_bytes + bytes_a, d0, d0 + NT, desc, p.kn,
-                                    c == 0 && kc - kc0 < p.groups, p.both);
-          commit(&bars->empty[st]);
-          open = true;
-          if (++grp == p.groups) grp = 0;
-          if (++st == ns) {
-            st = 0;
-            ph ^= 1;
+          int grp = 0;
+          for (int kc = kr; kc < end; ++kc) {
+            if (!dn_wait(&bars->full[st], ph, abort)) {
+              dn_fail(bars, status);
+              ok = false;
+              break;
+            }
+            tc_after_sync();
+            const uint32_t a = ring_at + st * stage_bytes;
+            const uint32_t d0 = tmem + buf * p.buf_cols + grp * grp_cols;
+            for (int c = 0; c < p.wide; ++c)
+              dn_stage_products<PAIR>(a + c * chunk_bytes, a + c * chunk_bytes + bytes_a, d0, d0 + NT, desc, p.kn,
+                                      c == 0 && kc - kr < (KEEP ? 1 : p.groups), p.both);
+            commit(&bars->empty[st]);
+            open = true;
+            if (!KEEP && ++grp == p.groups) grp = 0;
+            if (++st == ns) {
+              st = 0;
+              ph ^= 1;
+            }
           }
-        }
-        if (!ok) break;
-        commit(&bars->tfull[buf]);
-        if (++buf == p.acc_bufs) {
-          buf = 0;
-          tph ^= 1;
+          if (!ok) break;
+          commit(&bars->tfull[buf]);
+          if (++buf == p.acc_bufs) {
+            buf = 0;
+            tph ^= 1;
+          }
         }
       }
       if (open) {  // every product is done before TMEM is given back
@@ -332,15 +361,53 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   } else if (warp >= 4) {
     // Lanes 32 (warp % 4) ... are this warp's.  Of the two warps that have them, each takes one of the
     // two products, or, where both products belong to one feature (or there is one), every other 16 tokens.
-    constexpr int W = FEW ? 4 : 16;  // tokens at a time
+    constexpr int W = FEW || (KEEP && !SHARED) ? 4 : 16;  // tokens at a time
     const int q = warp & 3, half = (warp - 4) >> 2, etid = tid - 128;
     const bool by_tok = p.gated || !p.both;
     const int tok0 = by_tok ? 16 * half : 0, tok_step = by_tok ? 32 : 16;
     const int row = q * 32 + lane;
-    const int groups = kc1 - kc0 < p.groups ? kc1 - kc0 : p.groups, grp_cols = (p.both ? 2 : 1) * NT;
+    const int grp_cols = (p.both ? 2 : 1) * NT;
+    const int groups = KEEP ? 1 : kc1 - kc0 < p.groups ? kc1 - kc0 : p.groups;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (by_tok ? 0 : half * NT);
     int buf = 0;
     uint32_t tph = 0;
     for (int t = first; t < p.T; t += step) {
+      // this warp's columns of the sets of accumulators that have been read
+      auto release = [&] {
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR) peer_arrive(peer_addr(smem_addr(&bars->tempty[buf]), lead));
+          else mbar_arrive(&bars->tempty[buf]);
+        }
+        if (++buf == p.acc_bufs) {
+          buf = 0;
+          tph ^= 1;
+        }
+      };
+      if constexpr (KEEP) {
+        float acc[8][16];
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[b][i] = 0.f;
+        bool ok = true;
+        for (int kr = kc0; kr < kc1; kr += p.per) {
+          ok = dn_wait(&bars->tfull[buf], tph, abort);
+          if (!ok) dn_fail(bars, status);
+          ok = !dn_any(1, kDnEpi, !ok);  // one decision for the warps
+          if (!ok) break;
+          tc_after_sync();
+          const bool last = kr + p.per >= kc1;
+          linear_round<16>(acc, last, [&](int b) {
+            const int n0 = tok0 + tok_step * (p.gated ? b & 3 : b);
+            return n0 < NT ? lanes + buf * p.buf_cols + (p.gated ? b >> 2 : 0) * NT + n0 : kNoBlock;
+          });
+          if (last) tmem_stored();
+          else release();
+        }
+        if (!ok) break;
+      }
       int ft, mt;
       tile_at(t, p.T, p.MT, ft, mt);
       const int m0 = mt * NT;
@@ -354,11 +421,13 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         const bool with_r = p.residual && on && !p.pairs;
         unsigned short r[W], rn[W];
         if (with_r && tok0 < nt) linear_residual(p, (size_t)(m0 + tok0) * p.N + feat, nt - tok0, rn);
-        const bool ok = dn_wait(&bars->tfull[buf], tph, abort);
-        if (!ok) dn_fail(bars, status);
-        if (dn_any(1, kDnEpi, !ok)) break;  // one decision for the warps
-        tc_after_sync();
-        const uint32_t d0 = tmem + ((uint32_t)(q * 32) << 16) + buf * p.buf_cols + (by_tok ? 0 : half * NT);
+        if constexpr (!KEEP) {
+          const bool ok = dn_wait(&bars->tfull[buf], tph, abort);
+          if (!ok) dn_fail(bars, status);
+          if (dn_any(1, kDnEpi, !ok)) break;  // one decision for the warps
+          tc_after_sync();
+        }
+        const uint32_t d0 = lanes + buf * p.buf_cols;
         for (int n0 = tok0; n0 < nt; n0 += tok_step) {
 #pragma unroll 1
           for (int i = n0; i < nt && i < n0 + 16; i += W) {
@@ -374,16 +443,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
             __syncwarp();
           }
         }
-        tc_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR) peer_arrive(peer_addr(smem_addr(&bars->tempty[buf]), lead));
-          else mbar_arrive(&bars->tempty[buf]);
-        }
-        if (++buf == p.acc_bufs) {
-          buf = 0;
-          tph ^= 1;
-        }
+        release();
       } else {
         // The warp pair's unit 2 q + half of sums belongs to the share unit * S / 8's CTA with the same lanes: 4 tokens of a
         // feature are 16 bytes at [unit of the owner][rank][matrix][4 tokens][lane], with room for all tokens in a unit.
@@ -398,7 +458,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           for (int n0 = 16 * h; n0 < nt; n0 += 32) n += ((nt - n0 < 16 ? nt - n0 : 16) + 3) / 4;
           return n;
         };
-        bool ok = dn_wait(&bars->tfull[0], 0, abort);
+        bool ok = KEEP || dn_wait(&bars->tfull[0], 0, abort);
         if (etid == 0 && ok) {
           if (FEW) {
             uint32_t bytes = 0;
@@ -414,7 +474,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         tc_after_sync();
         {
           const int owner = unit / per;
-          const uint32_t d0 = tmem + ((uint32_t)(q * 32) << 16) + (by_tok ? 0 : half * NT);
+          const uint32_t d0 = lanes + (KEEP ? buf * p.buf_cols : 0);
           const int peer = P * owner + half_of;
           uint32_t to = peer_addr(smem_addr(xsums), peer) + ((unit - owner * per) * S + rank) * unit_bytes + lane * 16;
           const uint32_t bar = peer_addr(smem_addr(&bars->xfull), peer);
@@ -504,6 +564,7 @@ struct PairArgs {
   int M, N, gated, bf16, kn, act, out_f32;
   int MT, T, KC;
   int rows;         // of weights from each CTA: a multiple of 16 (with w_mul 32), <= 128
+  int per;          // chunks of a round (with KEEP)
   int sectors;      // every 16 features of a token's row start on a 32-byte boundary of y
   const void *bias, *bias_mul, *residual;
   void* y;
@@ -596,6 +657,8 @@ __device__ __forceinline__ void pair_store(const PairArgs& p, size_t row, int fe
   }
 }
 
+// KEEP: a tile's chunks in rounds (LinearSums), whose sums this warp's threads add up.
+template <bool KEEP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDnThreads, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mw2,
                    const __grid_constant__ CUtensorMap mx, const PairArgs p) {
@@ -674,36 +737,40 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
       uint32_t ph = 0, tph = 0;
       bool ok = true, open = false;
       for (int t = first; ok && t < p.T; t += step) {
-        if (!cluster_wait(&bars->tempty[buf], tph ^ 1, abort)) {
-          dn_fail(bars, status);
-          break;
-        }
-        tc_after_sync();
-        const uint32_t d = tmem + buf * 256;
-        for (int kc = 0; kc < p.KC; ++kc) {
-          if (!dn_wait(&bars->full[st], ph, abort)) {
+        for (int kr = 0, end; ok && kr < p.KC; kr = end) {
+          end = KEEP && kr + p.per < p.KC ? kr + p.per : p.KC;
+          if (!cluster_wait(&bars->tempty[buf], tph ^ 1, abort)) {
             dn_fail(bars, status);
             ok = false;
             break;
           }
           tc_after_sync();
-          const uint32_t a = ring_at + st * kPairStage;
-          const uint64_t ad = smem_desc(a, 16), bd = smem_desc(a + kPairStage / 2, p.kn ? 8192 : 16);
-          const uint32_t step = p.kn ? 128 : 2;
+          const uint32_t d = tmem + buf * 256;
+          for (int kc = kr; kc < end; ++kc) {
+            if (!dn_wait(&bars->full[st], ph, abort)) {
+              dn_fail(bars, status);
+              ok = false;
+              break;
+            }
+            tc_after_sync();
+            const uint32_t a = ring_at + st * kPairStage;
+            const uint64_t ad = smem_desc(a, 16), bd = smem_desc(a + kPairStage / 2, p.kn ? 8192 : 16);
+            const uint32_t step = p.kn ? 128 : 2;
 #pragma unroll
-          for (int ks = 0; ks < kDnChunk / 16; ++ks)
-            mma_f16_pair(d, ad + ks * 2, bd + ks * step, desc, kc > 0 || ks > 0);
-          mma_commit_pair(&bars->empty[st]);
-          open = true;
-          if (++st == kPairStages) {
-            st = 0;
-            ph ^= 1;
+            for (int ks = 0; ks < kDnChunk / 16; ++ks)
+              mma_f16_pair(d, ad + ks * 2, bd + ks * step, desc, kc > kr || ks > 0);
+            mma_commit_pair(&bars->empty[st]);
+            open = true;
+            if (++st == kPairStages) {
+              st = 0;
+              ph ^= 1;
+            }
           }
+          if (!ok) break;
+          mma_commit_pair(&bars->tfull[buf]);
+          buf ^= 1;
+          tph ^= buf == 0;
         }
-        if (!ok) break;
-        mma_commit_pair(&bars->tfull[buf]);
-        buf ^= 1;
-        tph ^= buf == 0;
       }
       if (open) {  // every product is done before TMEM is given back
         mma_commit_pair(&bars->drain);
@@ -716,6 +783,37 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
     int buf = 0;
     uint32_t tph = 0;
     for (int t = first; t < p.T; t += step) {
+      const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * cols;
+      auto release = [&] {
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) peer_arrive(peer_addr(smem_addr(&bars->tempty[buf]), 0));
+        buf ^= 1;
+        tph ^= buf == 0;
+      };
+      if constexpr (KEEP) {
+        float acc[8][16];
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[b][i] = 0.f;
+        bool ok = true;
+        for (int kr = 0; kr < p.KC; kr += p.per) {
+          ok = dn_wait(&bars->tfull[buf], tph, abort);
+          if (!ok) dn_fail(bars, status);
+          ok = !dn_any(1, kDnEpi, !ok);  // one decision for the warps
+          if (!ok) break;
+          tc_after_sync();
+          const bool last = kr + p.per >= p.KC;
+          linear_round<4>(acc, last, [&](int b) {
+            const int c = 16 * (p.gated ? b & 3 : b);
+            return c < cols ? lanes + buf * 256 + (p.gated ? b >> 2 : 0) * p.rows + c : kNoBlock;
+          });
+          if (last) tmem_stored();
+          else release();
+        }
+        if (!ok) break;
+      }
       int ft, mt;
       tile_at(t, p.T, p.MT, ft, mt);
       const int tok = mt * 2 * kDnHalf + rank * kDnHalf + q * 32 + lane;
@@ -730,11 +828,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
           if (f0 + c + 8 * h < p.N) rn[h] = *reinterpret_cast<const uint4*>(from + 8 * h);
       };
       residual(0);
-      const bool ok = dn_wait(&bars->tfull[buf], tph, abort);
-      if (!ok) dn_fail(bars, status);
-      if (dn_any(1, kDnEpi, !ok)) break;
-      tc_after_sync();
-      const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + buf * 256 + half * cols;
+      if constexpr (!KEEP) {
+        const bool ok = dn_wait(&bars->tfull[buf], tph, abort);
+        if (!ok) dn_fail(bars, status);
+        if (dn_any(1, kDnEpi, !ok)) break;
+        tc_after_sync();
+      }
+      const uint32_t d = lanes + buf * 256;
       for (int c = 0; c < cols && f0 + c < p.N; c += 16) {
         float v[16], m[16];
         r[0] = rn[0];
@@ -747,11 +847,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
         if (tok < p.M) pair_store(p, tok, f0 + c, v, m, r);
         __syncwarp();
       }
-      tc_before_sync();
-      __syncwarp();
-      if (lane == 0) peer_arrive(peer_addr(smem_addr(&bars->tempty[buf]), 0));
-      buf ^= 1;
-      tph ^= buf == 0;
+      release();
     }
   }
   __syncwarp();
@@ -799,8 +895,11 @@ static cudaError_t launch_linear_pair(const LinearCall& c, const LinearPlan& l, 
   p.y = c.y;
   p.head = reinterpret_cast<DenseHead*>(ws);
   const size_t smem = 1024 + (size_t)kPairStages * kPairStage + sizeof(DenseBars);
-  static std::atomic<uint64_t> allowed{0};
-  e = allow_shared(linear_pair_kernel, allowed, smem_optin);
+  p.per = sum_chunks(c.out_f32);
+  const bool keep = p.KC > p.per;
+  static std::atomic<uint64_t> allowed[2];
+  const auto kernel = keep ? linear_pair_kernel<true> : linear_pair_kernel<false>;
+  e = allow_shared(kernel, allowed[keep], smem_optin);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (p.T < sms / 2 ? p.T : sms / 2));
@@ -812,13 +911,13 @@ static cudaError_t launch_linear_pair(const LinearCall& c, const LinearPlan& l, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_pair_kernel, mw, mw2, mx, p);
+  return cudaLaunchKernelEx(&cfg, kernel, mw, mw2, mx, p);
 }
 
 cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin, cudaStream_t st) {
   const bool gated = c.w_mul != nullptr;
   const int room = smem_optin - 1024 - (int)sizeof(DenseBars);
-  const LinearPlan& l = linear_plan(c.M, c.N, c.K, gated, c.kn, !c.split && !c.pairs, sms, room);
+  const LinearPlan& l = linear_plan(c.M, c.N, c.K, gated, c.kn, !c.split && !c.pairs, c.out_f32, sms, room);
   if (!l.S) return cudaErrorInvalidValue;
   if (l.by_token) return launch_linear_pair(c, l, ws, sms, smem_optin, st);
   CUtensorMap mw, mw2, mx;
@@ -855,26 +954,30 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   p.residual = c.residual;
   p.y = c.y;
   p.head = reinterpret_cast<DenseHead*>(ws);
-  const int stage = l.wide * ((l.both ? kDnBytesA : kDnBytesA / 2) + l.NT / l.P * 128), cols_of = (l.both ? 2 : 1) * l.NT;
+  const int stage = l.wide * ((l.both ? kDnBytesA : kDnBytesA / 2) + l.NT / l.P * 128);
   bool own_x;
   p.stages = linear_stages(l, c.M, gated, room, own_x);
   p.own_x = own_x;
-  p.acc_bufs = cols_of <= 256 && l.S == 1 && l.T > sms / l.P ? 2 : 1;  // two where a CTA has more than one tile
-  // fp32 results: several accumulators, so that each adds up fewer products (the tensor core's
-  // additions cut off; K = 4096 in one row costs 3e-6 of the result, in eight 6e-7)
-  p.groups = 1;
-  while (c.out_f32 && p.groups < 8 && 2 * p.groups * cols_of * p.acc_bufs <= 512) p.groups *= 2;
-  p.buf_cols = p.groups * cols_of;
+  LinearSums sums;
+  if (!linear_sums(l, c.K, c.out_f32, sums)) return cudaErrorInvalidValue;
+  p.acc_bufs = sums.bufs;
+  p.groups = sums.groups;
+  p.per = sums.per;
+  p.buf_cols = p.groups * (l.both ? 2 : 1) * l.NT;
   p.tmem_cols = 32;
-  while (p.tmem_cols < p.buf_cols * p.acc_bufs) p.tmem_cols *= 2;
+  while (p.tmem_cols < sums.cols) p.tmem_cols *= 2;
   p.stream = l.MT == 1;
   const int ctas = l.P * (l.S > 1 ? l.T * l.S : l.T < sms / l.P ? l.T : sms / l.P);
   const size_t smem = 1024 + (size_t)p.stages * stage + sizeof(DenseBars) + (own_x ? linear_sum_bytes(l, c.M, gated) : 0);
-  static std::atomic<uint64_t> allowed[6];
-  const int which = (l.P == 2 ? 4 : l.NT <= kFewTokens && l.S * l.T <= sms ? 2 : 0) + (l.S > 1);
-  constexpr decltype(&linear_kernel<false, false, false>) kernels[6] = {
-      linear_kernel<false, false, false>, linear_kernel<false, false, true>, linear_kernel<true, false, false>,
-      linear_kernel<true, false, true>,   linear_kernel<false, true, false>, linear_kernel<false, true, true>};
+  static std::atomic<uint64_t> allowed[10];
+  const bool few = l.P == 1 && !sums.keep && l.NT <= kFewTokens && l.S * l.T <= sms;
+  const int which = (few ? 8 : (l.P == 2 ? 4 : 0) + (sums.keep ? 2 : 0)) + (l.S > 1);
+  constexpr decltype(&linear_kernel<false, false, false, false>) kernels[10] = {
+      linear_kernel<false, false, false, false>, linear_kernel<false, false, true, false>,
+      linear_kernel<false, false, false, true>,  linear_kernel<false, false, true, true>,
+      linear_kernel<false, true, false, false>,  linear_kernel<false, true, true, false>,
+      linear_kernel<false, true, false, true>,   linear_kernel<false, true, true, true>,
+      linear_kernel<true, false, false, false>,  linear_kernel<true, false, true, false>};
   const auto kernel = kernels[which];
   e = allow_shared(kernel, allowed[which], smem_optin);
   if (e != cudaSuccess) return e;

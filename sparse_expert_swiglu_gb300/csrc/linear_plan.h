@@ -8,7 +8,7 @@
 namespace sesg {
 
 struct LinearPlan {
-  int M = -1, N = 0, K = 0, gated = 0, kn = 0, plain = 0, sms = 0, room = 0;  // what it is for
+  int M = -1, N = 0, K = 0, gated = 0, kn = 0, plain = 0, f32 = 0, sms = 0, room = 0;  // what it is for
   int by_token = 0;  // linear_pair_kernel
   int P = 1, NT = 0, MT = 0, rows = 0, both = 0, wide = 1, S = 0, T = 0;
 };
@@ -33,6 +33,37 @@ inline int linear_stages(const LinearPlan& l, int M, bool gated, int room, bool&
   return n > kDnMaxStages ? kDnMaxStages : n;
 }
 
+// Accumulators of a product.  The tensor core cuts off what its fp32 additions cannot hold: an accumulator that adds up
+// n steps of 16 k loses up to (2/3) n 2^-24 of its sum, always towards zero (measured at 4096 k: 4.4e-6 of the result).
+// So stages of an fp32 result go round up to eight accumulators where TMEM has the columns, none takes more than 1024 k
+// (16-bit results: 16384), and where that does not cover a tile's k, they start anew, in two sets by turns, and the
+// epilogue's warps add the rounds up in registers.
+struct LinearSums {
+  int groups, bufs;  // accumulators of a product; sets of them, so that one can be read while the next is filled
+  int per, keep;     // stages of a round; whether there are several
+  int cols;          // TMEM columns of all
+};
+constexpr int sum_chunks(bool f32) { return f32 ? 16 : 256; }  // of 64 k, that one accumulator takes
+
+// False: a warp's registers do not hold its share of the sums (128 columns).
+inline bool linear_sums(const LinearPlan& l, int K, bool f32, LinearSums& s) {
+  const int KC = ((K + kDnChunk - 1) / kDnChunk + l.wide - 1) / l.wide, share = (KC + l.S - 1) / l.S;
+  const int cols = (l.both ? 2 : 1) * l.NT, most = sum_chunks(f32) / l.wide;
+  s.keep = 0;
+  s.bufs = cols <= 256 && l.S == 1 && l.T > l.sms / l.P ? 2 : 1;  // two where a CTA has more than one tile
+  s.groups = 1;
+  while (f32 && s.groups < 8 && 2 * s.groups * cols * s.bufs <= 512) s.groups *= 2;
+  s.per = share;
+  if (share > s.groups * most) {
+    s.keep = 1;
+    s.groups = 1;
+    s.bufs = 2;
+    s.per = most;
+  }
+  s.cols = s.groups * cols * s.bufs;
+  return !s.keep || cols <= 256;
+}
+
 // The tile and the cluster with the least time by a model in SM clocks.  Its terms, as measured (GB300,
 // 1.9 GHz):
 //   a call costs 7000 whatever it does (256 x 512, one token: 3.8 us);
@@ -52,7 +83,7 @@ inline int linear_stages(const LinearPlan& l, int M, bool gated, int room, bool&
 //   adds 0.25 of the weights' time (2048 x 14336 gated, K = 4096: 275 us against the model's 279; one CTA a
 //   tile 321; 300 tokens 80 and 80); 90 a column for the others,
 //   which run under the next tile's products (384 x 7808 gated, GELU, K = 120: 7200 for 64 columns).
-inline LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, int sms, int room) {
+inline LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, bool f32, int sms, int room) {
   LinearPlan best;
   double best_t = 1e30;
   const int chunks = (K + kDnChunk - 1) / kDnChunk, mats = gated ? 2 : 1;
@@ -66,6 +97,7 @@ inline LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain
   auto slow = [](int row) { return row % 64 == 0 ? 1.0 : row % 16 == 0 ? 1.35 : 1.8; };
   const double slow_x = slow(K), slow_w = slow(kn ? N : K);
   LinearPlan l;
+  l.sms = sms;
   if (plain && N % 8 == 0 && M > 64) {
     // [K][N] weights come in boxes of 64 columns: narrower tiles would start inside a line (2048 x 4096, K = 14336: 148 us
     // with 128 columns, 186 with 112, which would fill two whole waves; [N][K] 176 and 158)
@@ -81,7 +113,9 @@ inline LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain
       const double waves = (double)((T + sms / 2 - 1) / (sms / 2)), chunk = 650.0 * rows / kDnHalf;
       const double l2 = (kDnHalf * slow_x + rows * slow_w) * 128 / 62;
       const double products = chunks * (chunk > l2 ? chunk : l2), epi = 90.0 * rows;
-      const double t = waves * (products > epi ? products : epi);
+      // rounds are added up under the next one's products
+      const double rounds = chunks > sum_chunks(f32) ? chunks / sum_chunks(f32) * 6.0 * rows : 0;
+      const double t = waves * (products > epi + rounds ? products : epi + rounds);
       const double mem = w_bytes / hbm;
       keep(l, 7000 + 27.0 * rows + (t > mem ? t + 0.25 * mem : mem + 0.25 * t));
     }
@@ -102,6 +136,8 @@ inline LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain
     if (T > (1 << 30) || (both && !gated && N <= rows) || (P > 1 && N <= width / 2) || (S > 1 && (T > fit || S > KC))) return;
     l.T = (int)T;
     bool own_x;
+    LinearSums sums;
+    if (!linear_sums(l, K, f32, sums)) return;
     const int stage = wide * ((both ? kDnBytesA : kDnBytesA / 2) + toks * 128);
     const int stages = linear_stages(l, M, gated, room, own_x);
     if (stages < 2 || (S > 1 && !own_x && linear_sum_bytes(l, M, gated) > stages * stage)) return;
@@ -140,6 +176,7 @@ inline LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain
   best.gated = gated;
   best.kn = kn;
   best.plain = plain;
+  best.f32 = f32;
   best.sms = sms;
   best.room = room;
   return best;
@@ -149,7 +186,7 @@ inline LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain
 // again with every token: 16 sets of 8, of which a new plan takes the place of the one that was asked for longest
 // ago.  The sizes are mixed one into the other: two calls with the same M (the products of an expert) must not fall into
 // one set for every M.
-inline const LinearPlan& linear_plan(int M, int N, int K, bool gated, bool kn, bool plain, int sms, int room) {
+inline const LinearPlan& linear_plan(int M, int N, int K, bool gated, bool kn, bool plain, bool f32, int sms, int room) {
   constexpr int kSets = 16, kWays = 8;
   struct Kept {
     LinearPlan plan[kWays];
@@ -158,7 +195,7 @@ inline const LinearPlan& linear_plan(int M, int N, int K, bool gated, bool kn, b
   static thread_local Kept sets[kSets];
   static thread_local uint64_t now = 0;
   uint64_t h = 0;
-  for (const int v : {M, N, K, (int)gated * 4 + (int)kn * 2 + (int)plain}) {
+  for (const int v : {M, N, K, (int)f32 * 8 + (int)gated * 4 + (int)kn * 2 + (int)plain}) {
     h = (h ^ (uint32_t)v) * 0x9E3779B97F4A7C15ull;
     h ^= h >> 29;
   }
@@ -166,14 +203,14 @@ inline const LinearPlan& linear_plan(int M, int N, int K, bool gated, bool kn, b
   int oldest = 0;
   for (int i = 0; i < kWays; ++i) {
     const LinearPlan& l = s.plan[i];
-    if (l.M == M && l.N == N && l.K == K && l.gated == gated && l.kn == kn && l.plain == plain && l.sms == sms &&
-        l.room == room) {
+    if (l.M == M && l.N == N && l.K == K && l.gated == gated && l.kn == kn && l.plain == plain && l.f32 == f32 &&
+        l.sms == sms && l.room == room) {
       s.used[i] = ++now;
       return l;
     }
     if (s.used[i] < s.used[oldest]) oldest = i;
   }
-  s.plan[oldest] = make_plan(M, N, K, gated, kn, plain, sms, room);
+  s.plan[oldest] = make_plan(M, N, K, gated, kn, plain, f32, sms, room);
   s.used[oldest] = ++now;
   return s.plan[oldest];
 }

@@ -19,18 +19,18 @@ SHIM = r"""
 using namespace sesg;
 constexpr int kSms = 152, kRoom = 232448 - 1024 - 256;
 static const LinearPlan& plan(const int* c, int room) {
-  return linear_plan(c[0], c[1], c[2], c[3], c[4], c[5], kSms, room);
+  return linear_plan(c[0], c[1], c[2], c[3], c[4], c[5], c[6], kSms, room);
 }
 extern "C" {
-// asks for n plans (M, N, K, gated, kn, plain) one after the other; how many of them are still kept then
+// asks for n plans (M, N, K, gated, kn, plain, fp32 result) one after the other; how many of them are still kept then
 int plans_kept(const int* c, int n) {
   const LinearPlan* at[1024];
-  for (int i = 0; i < n; ++i) at[i] = &plan(c + 6 * i, kRoom);
+  for (int i = 0; i < n; ++i) at[i] = &plan(c + 7 * i, kRoom);
   int kept = 0;
   for (int i = 0; i < n; ++i) {
-    const int* q = c + 6 * i;
+    const int* q = c + 7 * i;
     kept += at[i]->M == q[0] && at[i]->N == q[1] && at[i]->K == q[2] && at[i]->gated == q[3] && at[i]->kn == q[4] &&
-            at[i]->plain == q[5];
+            at[i]->plain == q[5] && at[i]->f32 == q[6];
   }
   return kept;
 }
@@ -40,6 +40,16 @@ int stages_for(const int* c, int before, int room) {
   bool own_x;
   const LinearPlan& l = plan(c, room);
   return linear_stages(l, c[0], c[3], room, own_x);
+}
+// an fp32 (16-bit) result's accumulators: the most chunks of 64 k that one takes, -1: without room in TMEM
+int most_chunks(const int* c) {
+  const LinearPlan& l = plan(c, kRoom);
+  if (!l.S) return -1;
+  const int KC = (c[2] + 63) / 64;
+  if (l.by_token) return KC < sum_chunks(c[6]) ? KC : sum_chunks(c[6]);
+  LinearSums s;
+  if (!linear_sums(l, c[2], c[6], s) || s.cols > 512 || (s.keep && (l.both ? 2 : 1) * l.NT > 256)) return -1;
+  return (s.per + s.groups - 1) / s.groups * l.wide;
 }
 size_t layer_bytes(int B, int d, int f, int E, int k, int ns) {
   return layer_plan(B, d, f, E, k, ns, kSms, 23 << 10, 4736).total;
@@ -69,7 +79,7 @@ def _ints(cases):
 def _expert(n, d, f):
     """The two products of an expert on n tokens: gate and up with a split result or not, then down on pairs or not."""
     two = n <= 64
-    return [(n, f, d, 1, 0, int(not two)), (2 * n if two else n, d, f, 0, 1, int(not two))]
+    return [(n, f, d, 1, 0, int(not two), 0), (2 * n if two else n, d, f, 0, 1, int(not two), 0)]
 
 
 @pytest.mark.parametrize("d,f", [(5120, 8192), (4096, 14336), (2048, 1408), (6144, 16384), (4096, 4096), (8192, 8192)])
@@ -82,18 +92,30 @@ def test_a_models_products_are_kept(plans):
     """One token count at a time: projections, dense block, output head and experts of a model."""
     for n in (1, 2, 3, 7, 16, 64, 65, 100, 256, 300, 512, 2048):
         for d, f, vocab in ((4096, 14336, 32000), (2048, 1408, 102400), (6144, 16384, 32768)):
-            cases = [(n, d, d, 0, 0, 1), (n, d + d // 4, d, 0, 0, 1), (n, vocab, d, 0, 0, 1), (n, f, d, 1, 0, 1),
-                     (n, d, f, 0, 1, 1), (n, d, f, 0, 0, 1), (n, 8, d, 0, 1, 1), (n, 64, d, 0, 1, 1)] + _expert(n, d, f)
+            cases = [(n, d, d, 0, 0, 1, 0), (n, d + d // 4, d, 0, 0, 1, 0), (n, vocab, d, 0, 0, 1, 1), (n, f, d, 1, 0, 1, 0),
+                     (n, d, f, 0, 1, 1, 0), (n, d, f, 0, 0, 1, 0), (n, 8, d, 0, 1, 1, 1), (n, 64, d, 0, 1, 1, 0)]
+            cases += _expert(n, d, f)
             cases = list(dict.fromkeys(cases))
             assert plans.plans_kept(_ints(cases), len(cases)) == len(cases), (n, d)
 
 
 def test_a_plan_goes_by_the_shared_memory_too(plans):
     """The same sizes with half the shared memory: the tile's stages fit."""
-    case = _ints([(1024, 4095, 4096, 0, 0, 1)])
+    case = _ints([(1024, 4095, 4096, 0, 0, 1, 0)])
     room = 232448 - 1024 - 256
     assert plans.stages_for(case, room, room) >= 2
     assert plans.stages_for(case, room, room // 4) >= 2
+
+
+def test_no_accumulator_adds_up_more_than_its_share(plans):
+    import random
+    rng = random.Random(7)
+    for _ in range(3000):
+        size = lambda lo, hi: int(lo * (hi / lo) ** rng.random())
+        gated, kn, f32 = (rng.randint(0, 1) for _ in range(3))
+        case = (size(1, 8192), 8 * size(1, 4096) if kn else size(1, 32768), 8 * size(1, 32768), gated, kn, 1, f32)
+        most = plans.most_chunks(_ints([case]))
+        assert 0 < most <= (16 if f32 else 256), (case, most)
 
 
 # ---------------------------------------------------------------------------
