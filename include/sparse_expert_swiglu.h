@@ -298,7 +298,8 @@ moe_status_t moe_prefetch_experts(const moe_experts_t* experts, const int32_t* i
  *
  * Workspaces: the calls of this section may share one that is large enough for each, as long as they
  * are ordered on one stream; it is zero-filled once before its first use (moe_workspace_init; its first
- * moe_linear_workspace_bytes(1, 1, 8, 0) bytes are enough), and again after MOE_ERR_TIMEOUT.  It may not be shared with the calls of the other sections.
+ * moe_linear_workspace_bytes(1, 1, 8, 0) bytes are enough), and again after MOE_ERR_TIMEOUT of a layer.  It may not be shared
+ * with the calls of the other sections.
  *
  * A y that overlaps the call's weights, and a workspace that overlaps any tensor of the call, is refused
  * (MOE_ERR_INVALID_ARG).
@@ -480,6 +481,19 @@ const char* moe_status_string(moe_status_t status);
  * is first), 256-byte aligned.  Nothing faults or hangs.
  */
 moe_status_t moe_selftest_wait_timeout(void* ws, size_t ws_bytes, uint32_t tries, void* stream);
+
+/*
+ * moe_selftest_linear_timeout, moe_selftest_layer_dense_timeout -- the same of the kernels on uncompressed weights:
+ * moe_linear or moe_layer_dense_decode with waits of at most `tries` (1..4000) rounds, of which one runs out.  In a product
+ * the first CTA's copies are taken for incomplete; in a layer an arrival at one of its barriers over the grid does
+ * not come (0: routing, 1: between the phases, 2: before the sums are added, 3: before RMSNorm, with rmsnorm_out).  Every
+ * CTA ends and MOE_ERR_TIMEOUT is recorded; y is undefined.
+ */
+moe_status_t moe_selftest_linear_timeout(const moe_linear_t* op, void* ws, size_t ws_bytes, uint32_t tries,
+                                         void* stream);
+moe_status_t moe_selftest_layer_dense_timeout(const uint16_t* x, int32_t B, const moe_dense_layer_t* layer, uint16_t* y,
+                                              int32_t rmsnorm_out, int32_t barrier, void* ws, size_t ws_bytes,
+                                              uint32_t tries, void* stream);
 
 #ifdef __cplusplus
 }

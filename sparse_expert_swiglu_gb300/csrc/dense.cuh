@@ -310,6 +310,7 @@ struct DenseBars {
   uint64_t xready, xfull;        // linear: the cluster's stages are free; its partial sums have come
   uint32_t tmem;
   int abort;
+  uint32_t tries;                // rounds of a wait, kWaitTries but for diagnostics
   int last;
 };
 
@@ -326,23 +327,34 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+__device__ __forceinline__ bool dn_aborted(const DenseBars* b) { return *reinterpret_cast<const volatile int*>(&b->abort); }
+
 // Bounded wait for a phase of a barrier; false when the time is over or another warp gave up.
-__device__ __forceinline__ bool dn_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool dn_wait(uint64_t* bar, uint32_t parity, const DenseBars* b) {
   if (mbar_test(bar, parity)) return true;
-  for (uint32_t i = 0; i < kWaitTries; ++i) {
+  for (uint32_t i = 0; i < b->tries; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
+    if (dn_aborted(b)) return false;
   }
   return false;
 }
 
 // The same for a barrier that the cluster's CTAs arrive at.
-__device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  for (uint32_t i = 0; i < kWaitTries; ++i) {
+__device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, const DenseBars* b) {
+  for (uint32_t i = 0; i < b->tries; ++i) {
     if (cluster_try_wait(bar, parity)) return true;
-    if (*abort) return false;
+    if (dn_aborted(b)) return false;
   }
   return false;
+}
+
+// Waits for what is in flight before a CTA ends, whoever gave up.
+__device__ __forceinline__ void dn_drain(uint64_t* bar, uint32_t parity, uint32_t tries) {
+  for (uint32_t i = 0; i < tries && !mbar_try_wait(bar, parity); ++i) {}
+}
+// ... and what no barrier of this CTA counts: after an abort it has long come when this is over.
+__device__ __forceinline__ void dn_settle() {
+  for (int i = 0; i < 8; ++i) __nanosleep(1000000);
 }
 
 __device__ __forceinline__ void dn_fail(DenseBars* b, int* status) {
@@ -350,10 +362,10 @@ __device__ __forceinline__ void dn_fail(DenseBars* b, int* status) {
   set_status(status, MOE_ERR_TIMEOUT);
 }
 
-// epi_warps: epilogue warps that read a tile's sums
-__device__ __forceinline__ void dn_init_bars(DenseBars* b, int epi_warps = kDnEpi / 32) {
+// tries: rounds of a wait; epi_warps: epilogue warps that read a tile's sums; copies: arrivals at a stage's barrier
+__device__ __forceinline__ void dn_init_bars(DenseBars* b, uint32_t tries, int epi_warps = kDnEpi / 32, int copies = 1) {
   for (int i = 0; i < kDnMaxStages; ++i) {
-    mbar_init(&b->full[i], 1);
+    mbar_init(&b->full[i], copies);
     mbar_init(&b->empty[i], 1);
   }
   for (int i = 0; i < 2; ++i) {
@@ -362,6 +374,7 @@ __device__ __forceinline__ void dn_init_bars(DenseBars* b, int epi_warps = kDnEp
   }
   mbar_init(&b->drain, 1);
   b->abort = 0;
+  b->tries = tries;
   b->last = 0;
   fence_barrier_init();
 }

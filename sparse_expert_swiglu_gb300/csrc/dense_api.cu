@@ -107,7 +107,12 @@ size_t moe_linear_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t gated
   return linear_ws_bytes();
 }
 
-moe_status_t moe_linear(const moe_linear_t* op, void* ws, size_t ws_bytes, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// tries: diagnostics (else 0), as in LinearCall
+moe_status_t linear_call(const moe_linear_t* op, void* ws, size_t ws_bytes, uint32_t tries, void* stream) {
   if (!op) return MOE_ERR_INVALID_ARG;
   if (op->dtype != MOE_F16 && op->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
   if (op->out_dtype != op->dtype && op->out_dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
@@ -155,7 +160,21 @@ moe_status_t moe_linear(const moe_linear_t* op, void* ws, size_t ws_bytes, void*
   c.residual = op->residual;
   c.y = op->y;
   c.w_stride = c.w_mul_stride = c.kn ? op->N : op->K;
+  c.tries = tries;
   return cuda_status(launch_linear(c, ws, sms, smem, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_linear(const moe_linear_t* op, void* ws, size_t ws_bytes, void* stream) {
+  return linear_call(op, ws, ws_bytes, 0, stream);
+}
+
+moe_status_t moe_selftest_linear_timeout(const moe_linear_t* op, void* ws, size_t ws_bytes, uint32_t tries, void* stream) {
+  if (tries < 1 || tries > 4000) return MOE_ERR_INVALID_ARG;
+  return linear_call(op, ws, ws_bytes, tries, stream);
 }
 
 size_t moe_expert_dense_workspace_bytes(int32_t n, int32_t d, int32_t f) {
@@ -232,9 +251,14 @@ size_t moe_layer_dense_workspace_bytes(const moe_dense_layer_t* layer, int32_t B
   return dense_layer_ws_bytes(B, layer->routed.d, layer->routed.f, layer->routed.E, layer->k, layer->shared.E, sms);
 }
 
-moe_status_t moe_layer_dense_decode(const uint16_t* x, int32_t B, const moe_dense_layer_t* layer,
-                                    const uint16_t* residual, uint16_t* y, int32_t rmsnorm_out,
-                                    const moe_debug_t* dbg, void* ws, size_t ws_bytes, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// tries, missing: diagnostics (else 0), as in DenseLayerCall
+moe_status_t layer_call(const uint16_t* x, int32_t B, const moe_dense_layer_t* layer, const uint16_t* residual,
+                        uint16_t* y, int32_t rmsnorm_out, const moe_debug_t* dbg, void* ws, size_t ws_bytes,
+                        uint32_t tries, int missing, void* stream) {
   moe_status_t s = check_dense_layer(layer, B);
   if (s != MOE_OK) return s;
   if (B == 0) return MOE_OK;
@@ -272,7 +296,26 @@ moe_status_t moe_layer_dense_decode(const uint16_t* x, int32_t B, const moe_dens
   c.y = y;
   c.user_idx = dbg ? dbg->topk_idx : nullptr;
   c.user_w = dbg ? dbg->topk_w : nullptr;
+  c.tries = tries;
+  c.missing = missing;
   return cuda_status(launch_dense_layer(c, ws, sms, smem, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_layer_dense_decode(const uint16_t* x, int32_t B, const moe_dense_layer_t* layer,
+                                    const uint16_t* residual, uint16_t* y, int32_t rmsnorm_out,
+                                    const moe_debug_t* dbg, void* ws, size_t ws_bytes, void* stream) {
+  return layer_call(x, B, layer, residual, y, rmsnorm_out, dbg, ws, ws_bytes, 0, 0, stream);
+}
+
+moe_status_t moe_selftest_layer_dense_timeout(const uint16_t* x, int32_t B, const moe_dense_layer_t* layer, uint16_t* y,
+                                              int32_t rmsnorm_out, int32_t barrier, void* ws, size_t ws_bytes,
+                                              uint32_t tries, void* stream) {
+  if (tries < 1 || tries > 4000 || barrier < 0 || barrier > (rmsnorm_out ? 3 : 2)) return MOE_ERR_INVALID_ARG;
+  return layer_call(x, B, layer, nullptr, y, rmsnorm_out, nullptr, ws, ws_bytes, tries, barrier, stream);
 }
 
 }  // extern "C"

@@ -51,6 +51,8 @@ struct LayerArgs {
   int block_rows, block_vecs, blocks;  // log2 of the rows of a block, its vectors, blocks that a CTA's threads take at a time
   int sum_step;        // threads of the first step of the sums, a multiple of E
   int stages, stage_bytes, a_bytes;  // a_bytes: of a stage, before the tokens
+  uint32_t tries;      // rounds of a wait
+  int missing;         // diagnostics: the barrier over the grid that misses an arrival, or -1
 };
 
 struct LayerMisc {
@@ -79,12 +81,12 @@ struct LayerMisc {
 __device__ __forceinline__ void grid_arrive(unsigned* bar) {
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(bar) : "memory");
 }
-__device__ __forceinline__ bool grid_wait(unsigned* bar, unsigned n, volatile int* abort) {
-  for (int i = 0; i < (1 << 22); ++i) {
+__device__ __forceinline__ bool grid_wait(unsigned* bar, unsigned n, const DenseBars* b) {
+  for (uint32_t i = 0; i < b->tries * 1024; ++i) {
     unsigned v;
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(bar) : "memory");
     if (v >= n) return true;
-    if (*abort) return false;
+    if (dn_aborted(b)) return false;
   }
   return false;
 }
@@ -275,7 +277,7 @@ __device__ bool route(const LayerArgs& p, LayerMisc& m, float* scratch) {
   }
   if (tid == 0) {
     if (cta < p.B * p.slices) grid_arrive(&p.head->bar[0]);
-    m.fail = !grid_wait(&p.head->bar[0], p.B * p.slices, &m.bars.abort);
+    m.fail = !grid_wait(&p.head->bar[0], p.B * p.slices + (p.missing == 0), &m.bars);
   }
   __syncthreads();
   if (m.fail) return false;
@@ -481,10 +483,9 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   const uint32_t x_bytes = (p.B + 7) / 8 * 1024;  // ... of the tokens'
   const uint32_t a_bytes = WIDE == 1 ? kDnBytesA : p.a_bytes;
   int* status = &p.head->ctrl.status;
-  volatile int* abort = &bars->abort;
 
   if (tid == 0) {
-    dn_init_bars(bars);
+    dn_init_bars(bars, p.tries);
     m.fail = 0;
   }
   if (warp == 2) tmem_alloc(&bars->tmem, 512);
@@ -581,7 +582,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   if (!ok) {
     // no copy is in flight when the CTA ends
     for (int i = 0; i < sent; ++i)
-      for (uint32_t w = 0; w < kWaitTries && !mbar_try_wait(&bars->full[i], 0); ++w) {}
+      dn_drain(&bars->full[i], 0, kWaitTries);
   } else if (warp == 0) {
     if (elect_one()) {
       int st = 0, issued = sent;
@@ -603,7 +604,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
             advance(st, ph);
             continue;
           }
-          if (!dn_wait(&bars->empty[st], ph ^ 1, abort)) {
+          if (!dn_wait(&bars->empty[st], ph ^ 1, bars)) {
             dn_fail(bars, status);
             go = false;
             break;
@@ -641,7 +642,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       while (go && hmore) {
         // weights as far ahead as there are stages, then the h of the oldest of them
         while (more && ahead < (waited ? 1 : S)) {
-          if (!dn_wait(&bars->empty[st], ph ^ 1, abort)) {
+          if (!dn_wait(&bars->empty[st], ph ^ 1, bars)) {
             dn_fail(bars, status);
             go = false;
             break;
@@ -658,7 +659,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
         if (!go) break;
         if (!waited) {
           waited = true;
-          if (!grid_wait(&p.head->bar[1], gridDim.x, abort)) {
+          if (!grid_wait(&p.head->bar[1], gridDim.x + (p.missing == 1), bars)) {
             dn_fail(bars, status);
             break;
           }
@@ -680,7 +681,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
           st = S - 1;
           ph ^= 1;
         }
-        for (uint32_t w = 0; w < (*abort ? 8u : kWaitTries) && !mbar_try_wait(&bars->full[st], ph); ++w) {}
+        dn_drain(&bars->full[st], ph, dn_aborted(bars) ? 8 : kWaitTries);
       }
     }
   } else if (warp == 2 || warp == 3) {
@@ -701,7 +702,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
         while (go && it.next(g)) {
           const int n = m.cnt[g.t / TT];
           const uint32_t desc = mma_desc(phase ? (n + 7) / 8 * 16 : (n + 15) / 16 * 16, p.bf16, phase);
-          if (!dn_wait(&bars->tempty[buf], tph ^ 1, abort)) {
+          if (!dn_wait(&bars->tempty[buf], tph ^ 1, bars)) {
             dn_fail(bars, status);
             go = false;
             break;
@@ -709,7 +710,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
           tc_after_sync();
           const uint32_t d0 = tmem + buf * 256;
           for (int kc = g.k0; kc < g.k1; ++kc) {
-            if (!dn_wait(&bars->full[st], ph, abort)) {
+            if (!dn_wait(&bars->full[st], ph, bars)) {
               dn_fail(bars, status);
               go = false;
               break;
@@ -735,7 +736,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       }
       if (open) {
         mma_commit(&bars->drain);
-        for (uint32_t w = 0; w < kWaitTries && !mbar_try_wait(&bars->drain, 0); ++w) {}
+        dn_drain(&bars->drain, 0, kWaitTries);
       }
     }
   } else if (warp >= 4) {
@@ -749,7 +750,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
     {
       SegIter it(s1, cta);
       while (it.next(g)) {
-        const bool good = dn_wait(&bars->tfull[buf], tph, abort);
+        const bool good = dn_wait(&bars->tfull[buf], tph, bars);
         if (!good) dn_fail(bars, status);
         if (dn_any(1, kDnEpi, !good)) {
           go = false;
@@ -797,7 +798,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       if (etid == 0) grid_arrive(&p.head->bar[1]);
       SegIter it(s2, cta);
       while (it.next(g)) {
-        const bool good = dn_wait(&bars->tfull[buf], tph, abort);
+        const bool good = dn_wait(&bars->tfull[buf], tph, bars);
         if (!good) dn_fail(bars, status);
         if (dn_any(1, kDnEpi, !good)) break;
         tc_after_sync();
@@ -833,11 +834,11 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
   if (warp == 2) tmem_free(tmem, 512);
 
   if (tid == 0) {
-    if (!*abort) {
+    if (!dn_aborted(bars)) {
       grid_arrive(&p.head->bar[2]);
-      if (!grid_wait(&p.head->bar[2], gridDim.x, abort)) dn_fail(bars, status);
+      if (!grid_wait(&p.head->bar[2], gridDim.x + (p.missing == 2), bars)) dn_fail(bars, status);
     }
-    m.fail = *abort;
+    m.fail = dn_aborted(bars);
   }
   __syncthreads();
   if (m.fail) return;
@@ -877,8 +878,8 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
     __syncthreads();
     if (tid == 0) {
       grid_arrive(&p.head->bar[3]);
-      if (!grid_wait(&p.head->bar[3], gridDim.x, abort)) dn_fail(bars, status);
-      m.fail = *abort;
+      if (!grid_wait(&p.head->bar[3], gridDim.x + (p.missing == 3), bars)) dn_fail(bars, status);
+      m.fail = dn_aborted(bars);
     }
     __syncthreads();
     if (m.fail) return;
@@ -949,6 +950,8 @@ cudaError_t launch_dense_layer(const DenseLayerCall& c, void* ws, int sms, int s
   p.user_idx = c.user_idx;
   p.user_w = c.user_w;
   p.head = reinterpret_cast<DenseHead*>(ws);
+  p.tries = c.tries ? c.tries : kWaitTries;
+  p.missing = c.tries ? c.missing : -1;
   p.logits = reinterpret_cast<float*>(w8 + l.logits);
   p.top_idx = reinterpret_cast<int*>(w8 + l.top_idx);
   p.top_w = reinterpret_cast<float*>(w8 + l.top_w);

@@ -19,6 +19,7 @@ struct LinearCall {
   const void *x, *w, *w_mul, *bias, *bias_mul, *residual;
   void* y;
   size_t w_stride, w_mul_stride;  // elements between rows
+  uint32_t tries;       // diagnostics (else 0): waits of so many rounds, of which the first CTA's run out
 };
 
 size_t linear_ws_bytes();
@@ -48,6 +49,8 @@ struct DenseLayerCall {
   void* y;
   int32_t* user_idx;                 // optional copies of the routing
   float* user_w;
+  uint32_t tries;                    // diagnostics (else 0): waits of so many rounds, ...
+  int missing;                       // ... and the barrier over the grid that misses an arrival
 };
 
 size_t dense_layer_ws_bytes(int B, int d, int f, int E, int k, int ns, int sms);

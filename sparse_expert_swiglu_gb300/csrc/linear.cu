@@ -31,6 +31,8 @@ struct LinearArgs {
   DenseHead* head;
   int stages, acc_bufs, buf_cols, tmem_cols, stream;
   int own_x;        // the cluster's partial sums have memory of their own, behind the stages
+  uint32_t tries;   // rounds of a wait
+  int missing;      // diagnostics: the first CTA's stages wait for an arrival that does not come
 };
 
 // Tile t's feature and token tile.  Tiles that run together share operands: eight token tiles at a time go
@@ -215,11 +217,10 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   const int kc0 = p.KC * rank / S, kc1 = p.KC * (rank + 1) / S;
   const int width = p.gated || !p.both ? p.rows : 2 * p.rows;  // features of a CTA in a tile
   int* status = &p.head->ctrl.status;
-  volatile int* abort = &bars->abort;
   const uint32_t ring_at = smem_addr(ring);
 
   if (tid == 0) {
-    dn_init_bars(bars, P * kDnEpi / 32);
+    dn_init_bars(bars, p.tries, P * kDnEpi / 32, 1 + (p.missing && blockIdx.x == 0));
     mbar_init(&bars->xready, S);
     mbar_init(&bars->xfull, FEW ? 1 : 8);
     fence_barrier_init();
@@ -258,7 +259,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         const CUtensorMap* m2 = p.gated ? &mw2 : &mw;
         const int f1 = p.gated ? f0 : f0 + p.rows;
         for (int kc = kc0; kc < kc1; ++kc) {
-          if (!dn_wait(&bars->empty[st], ph ^ 1, abort)) {
+          if (!dn_wait(&bars->empty[st], ph ^ 1, bars)) {
             dn_fail(bars, status);
             ok = false;
             break;
@@ -292,16 +293,15 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         }
       }
       // No copy of this CTA is in flight when it ends: the last stages have come.  A pair has used every copy, unless
-      // it gave up: copies that no barrier of this CTA counts come long before this is over.
-      if (PAIR && *abort)
-        for (int i = 0; i < 8; ++i) __nanosleep(1000000);
+      // it gave up: no barrier of this CTA counts them.
+      if (PAIR && dn_aborted(bars)) dn_settle();
       const int n = PAIR ? 0 : issued < ns ? issued : ns;
       for (int i = 0; i < n; ++i) {
         if (--st < 0) {
           st = ns - 1;
           ph ^= 1;
         }
-        for (uint32_t w = 0; w < kWaitTries && !mbar_try_wait(&bars->full[st], ph); ++w) {}
+        dn_drain(&bars->full[st], ph, p.tries);
       }
     }
   } else if (warp == 1) {
@@ -318,7 +318,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
       for (int t = first; ok && t < p.T; t += step) {
         for (int kr = kc0, end; ok && kr < kc1; kr = end) {
           end = KEEP && kr + p.per < kc1 ? kr + p.per : kc1;
-          if (!(PAIR ? cluster_wait(&bars->tempty[buf], tph ^ 1, abort) : dn_wait(&bars->tempty[buf], tph ^ 1, abort))) {
+          if (!(PAIR ? cluster_wait(&bars->tempty[buf], tph ^ 1, bars) : dn_wait(&bars->tempty[buf], tph ^ 1, bars))) {
             dn_fail(bars, status);
             ok = false;
             break;
@@ -326,7 +326,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           tc_after_sync();
           int grp = 0;
           for (int kc = kr; kc < end; ++kc) {
-            if (!dn_wait(&bars->full[st], ph, abort)) {
+            if (!dn_wait(&bars->full[st], ph, bars)) {
               dn_fail(bars, status);
               ok = false;
               break;
@@ -355,7 +355,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
       }
       if (open) {  // every product is done before TMEM is given back
         commit(&bars->drain);
-        for (uint32_t w = 0; w < kWaitTries && !cluster_try_wait(&bars->drain, 0); ++w) {}
+        dn_drain(&bars->drain, 0, kWaitTries);
       }
     }
   } else if (warp >= 4) {
@@ -393,13 +393,13 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           for (int i = 0; i < 16; ++i) acc[b][i] = 0.f;
         bool ok = true;
         for (int kr = kc0; kr < kc1; kr += p.per) {
-          ok = dn_wait(&bars->tfull[buf], tph, abort);
+          ok = dn_wait(&bars->tfull[buf], tph, bars);
           if (!ok) dn_fail(bars, status);
           ok = !dn_any(1, kDnEpi, !ok);  // one decision for the warps
           if (!ok) break;
           tc_after_sync();
           const bool last = kr + p.per >= kc1;
-          linear_round<16>(acc, last, [&](int b) {
+          linear_round<SHARED ? 16 : 8>(acc, last, [&](int b) {
             const int n0 = tok0 + tok_step * (p.gated ? b & 3 : b);
             return n0 < NT ? lanes + buf * p.buf_cols + (p.gated ? b >> 2 : 0) * NT + n0 : kNoBlock;
           });
@@ -422,7 +422,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         unsigned short r[W], rn[W];
         if (with_r && tok0 < nt) linear_residual(p, (size_t)(m0 + tok0) * p.N + feat, nt - tok0, rn);
         if constexpr (!KEEP) {
-          const bool ok = dn_wait(&bars->tfull[buf], tph, abort);
+          const bool ok = dn_wait(&bars->tfull[buf], tph, bars);
           if (!ok) dn_fail(bars, status);
           if (dn_any(1, kDnEpi, !ok)) break;  // one decision for the warps
           tc_after_sync();
@@ -458,7 +458,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           for (int n0 = 16 * h; n0 < nt; n0 += 32) n += ((nt - n0 < 16 ? nt - n0 : 16) + 3) / 4;
           return n;
         };
-        bool ok = KEEP || dn_wait(&bars->tfull[0], 0, abort);
+        bool ok = KEEP || dn_wait(&bars->tfull[0], 0, bars);
         if (etid == 0 && ok) {
           if (FEW) {
             uint32_t bytes = 0;
@@ -468,7 +468,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           if (!p.own_x)
             for (int i = 0; i < S; ++i) peer_arrive(peer_addr(smem_addr(&bars->xready), P * i + half_of));
         }
-        if (!p.own_x) ok = ok && cluster_wait(&bars->xready, 0, abort);
+        if (!p.own_x) ok = ok && cluster_wait(&bars->xready, 0, bars);
         if (!ok) dn_fail(bars, status);
         if (dn_any(1, kDnEpi, !ok)) break;
         tc_after_sync();
@@ -498,7 +498,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           __syncwarp();
           if (!FEW && lane == 0) peer_arrive(bar);  // releases the warp's stores
         }
-        ok = cluster_wait(&bars->xfull, 0, abort);
+        ok = cluster_wait(&bars->xfull, 0, bars);
         if (!ok) dn_fail(bars, status);
         if (dn_any(1, kDnEpi, !ok)) break;
         {
@@ -540,7 +540,10 @@ linear_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   __syncwarp();
   tc_before_sync();
   __syncthreads();
-  if (PAIR || S > 1) cluster_sync_all();  // no CTA leaves while another may store into it
+  if (PAIR || S > 1) {
+    cluster_sync_all();  // no CTA leaves while another may store into it
+    if (dn_aborted(bars)) dn_settle();  // stores that this CTA did not wait for
+  }
   tc_after_sync();
   if (warp == 2) {
     if (PAIR) tmem_free_pair(tmem, p.tmem_cols);
@@ -569,6 +572,8 @@ struct PairArgs {
   const void *bias, *bias_mul, *residual;
   void* y;
   DenseHead* head;
+  uint32_t tries;   // as in LinearArgs
+  int missing;
 };
 
 // 8 neighbouring features of a token from a 16-bit array, added or assigned; n of them exist.
@@ -671,11 +676,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
   const int width = p.gated ? p.rows : 2 * p.rows;  // features of a tile
   const int load_rows = p.kn ? (p.rows + 63) / 64 * 64 : p.rows;
   int* status = &p.head->ctrl.status;
-  volatile int* abort = &bars->abort;
   const uint32_t ring_at = smem_addr(ring);
 
   if (tid == 0) {
-    dn_init_bars(bars, 2 * kDnEpi / 32);
+    dn_init_bars(bars, p.tries, 2 * kDnEpi / 32, 1 + (p.missing && blockIdx.x == 0));
     tma_prefetch_map(&mw);
     tma_prefetch_map(&mx);
     if (p.gated) tma_prefetch_map(&mw2);
@@ -702,7 +706,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
         tile_at(t, p.T, p.MT, ft, mt);
         const int m0 = mt * 2 * kDnHalf + rank * kDnHalf, f0 = ft * width + (p.gated ? 0 : rank * p.rows);
         for (int kc = 0; kc < p.KC; ++kc) {
-          if (!dn_wait(&bars->empty[st], ph ^ 1, abort)) {
+          if (!dn_wait(&bars->empty[st], ph ^ 1, bars)) {
             dn_fail(bars, status);
             ok = false;
             break;
@@ -723,10 +727,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
           }
         }
       }
-      // After an abort copies may be in flight that no barrier of this CTA counts: they come long before
-      // this is over.  (Without one, every copy has been used.)
-      if (*abort)
-        for (int i = 0; i < 8; ++i) __nanosleep(1000000);
+      // After an abort copies may be in flight that no barrier of this CTA counts.  (Without one, every copy has been used.)
+      if (dn_aborted(bars)) dn_settle();
     }
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
@@ -739,7 +741,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
       for (int t = first; ok && t < p.T; t += step) {
         for (int kr = 0, end; ok && kr < p.KC; kr = end) {
           end = KEEP && kr + p.per < p.KC ? kr + p.per : p.KC;
-          if (!cluster_wait(&bars->tempty[buf], tph ^ 1, abort)) {
+          if (!cluster_wait(&bars->tempty[buf], tph ^ 1, bars)) {
             dn_fail(bars, status);
             ok = false;
             break;
@@ -747,7 +749,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
           tc_after_sync();
           const uint32_t d = tmem + buf * 256;
           for (int kc = kr; kc < end; ++kc) {
-            if (!dn_wait(&bars->full[st], ph, abort)) {
+            if (!dn_wait(&bars->full[st], ph, bars)) {
               dn_fail(bars, status);
               ok = false;
               break;
@@ -774,7 +776,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
       }
       if (open) {  // every product is done before TMEM is given back
         mma_commit_pair(&bars->drain);
-        for (uint32_t w = 0; w < kWaitTries && !cluster_try_wait(&bars->drain, 0); ++w) {}
+        dn_drain(&bars->drain, 0, kWaitTries);
       }
     }
   } else if (warp >= 4) {
@@ -799,7 +801,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
           for (int i = 0; i < 16; ++i) acc[b][i] = 0.f;
         bool ok = true;
         for (int kr = 0; kr < p.KC; kr += p.per) {
-          ok = dn_wait(&bars->tfull[buf], tph, abort);
+          ok = dn_wait(&bars->tfull[buf], tph, bars);
           if (!ok) dn_fail(bars, status);
           ok = !dn_any(1, kDnEpi, !ok);  // one decision for the warps
           if (!ok) break;
@@ -829,7 +831,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
       };
       residual(0);
       if constexpr (!KEEP) {
-        const bool ok = dn_wait(&bars->tfull[buf], tph, abort);
+        const bool ok = dn_wait(&bars->tfull[buf], tph, bars);
         if (!ok) dn_fail(bars, status);
         if (dn_any(1, kDnEpi, !ok)) break;
         tc_after_sync();
@@ -854,6 +856,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
   tc_before_sync();
   __syncthreads();
   cluster_sync_all();  // no CTA leaves while the other's copies or arrivals may reach it
+  if (dn_aborted(bars)) dn_settle();
   tc_after_sync();
   if (warp == 2) tmem_free_pair(tmem, 512);
 }
@@ -894,6 +897,8 @@ static cudaError_t launch_linear_pair(const LinearCall& c, const LinearPlan& l, 
   p.residual = c.residual;
   p.y = c.y;
   p.head = reinterpret_cast<DenseHead*>(ws);
+  p.tries = c.tries ? c.tries : kWaitTries;
+  p.missing = c.tries > 0;
   const size_t smem = 1024 + (size_t)kPairStages * kPairStage + sizeof(DenseBars);
   p.per = sum_chunks(c.out_f32);
   const bool keep = p.KC > p.per;
@@ -954,6 +959,8 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, int sms, int smem_optin
   p.residual = c.residual;
   p.y = c.y;
   p.head = reinterpret_cast<DenseHead*>(ws);
+  p.tries = c.tries ? c.tries : kWaitTries;
+  p.missing = c.tries > 0;
   const int stage = l.wide * ((l.both ? kDnBytesA : kDnBytesA / 2) + l.NT / l.P * 128);
   bool own_x;
   p.stages = linear_stages(l, c.M, gated, room, own_x);
