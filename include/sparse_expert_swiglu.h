@@ -298,8 +298,9 @@ moe_status_t moe_prefetch_experts(const moe_experts_t* experts, const int32_t* i
  *
  * Workspaces: the calls of this section may share one that is large enough for each, as long as they
  * are ordered on one stream; it is zero-filled once before its first use (moe_workspace_init; its first
- * moe_linear_workspace_bytes(1, 1, 8, 0) bytes are enough), and again after MOE_ERR_TIMEOUT of a layer.  It may not be shared
- * with the calls of the other sections.
+ * moe_linear_workspace_bytes(1, 1, 8, 0) bytes are enough).  A call that gives up (MOE_ERR_TIMEOUT) leaves
+ * it ready for the next one; what it wrote to y is undefined.  It may not be shared with the calls of the other
+ * sections.
  *
  * A y that overlaps the call's weights, and a workspace that overlaps any tensor of the call, is refused
  * (MOE_ERR_INVALID_ARG).
@@ -487,7 +488,7 @@ moe_status_t moe_selftest_wait_timeout(void* ws, size_t ws_bytes, uint32_t tries
  * moe_linear or moe_layer_dense_decode with waits of at most `tries` (1..4000) rounds, of which one runs out.  In a product
  * the first CTA's copies are taken for incomplete; in a layer an arrival at one of its barriers over the grid does
  * not come (0: routing, 1: between the phases, 2: before the sums are added, 3: before RMSNorm, with rmsnorm_out).  Every
- * CTA ends and MOE_ERR_TIMEOUT is recorded; y is undefined.
+ * CTA ends, MOE_ERR_TIMEOUT is recorded, and the workspace is ready for the next call; y is undefined.
  */
 moe_status_t moe_selftest_linear_timeout(const moe_linear_t* op, void* ws, size_t ws_bytes, uint32_t tries,
                                          void* stream);

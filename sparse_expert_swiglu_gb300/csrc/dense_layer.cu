@@ -841,8 +841,9 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
     m.fail = dn_aborted(bars);
   }
   __syncthreads();
-  if (m.fail) return;
-  for (int u = u0; u < p.B * HT; u += ustep) {
+  const bool failed = m.fail;
+  const int units = failed ? 0 : p.B * HT;
+  for (int u = u0; u < units; u += ustep) {
     const int b = u / HT, feat = (u - b * HT) * kDnHalf + gtid;
     if (u != u0) {
       named_barrier(2 + grp, kDnHalf);
@@ -873,7 +874,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       if (lane == 0) __stcg(p.ysq + (size_t)u * 4 + (gtid >> 5), sq);
     }
   }
-  if (p.rmsnorm) {
+  if (p.rmsnorm && !failed) {
     // every token's squares, in order, then the same thread's values again
     __syncthreads();
     if (tid == 0) {
@@ -882,8 +883,7 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       m.fail = dn_aborted(bars);
     }
     __syncthreads();
-    if (m.fail) return;
-    for (int u = u0; u < p.B * HT; u += ustep) {
+    for (int u = m.fail ? units : u0; u < units; u += ustep) {
       const int b = u / HT, feat = (u - b * HT) * kDnHalf + gtid;
       float t = 0.f;  // every warp alike
       for (int i = lane; i < 4 * HT; i += 32) t += __ldcg(p.ysq + (size_t)b * 4 * HT + i);
@@ -896,12 +896,21 @@ dense_layer_kernel(const __grid_constant__ LayerMaps maps, const LayerArgs p) {
       }
     }
   }
-  // the last CTA to leave clears the barriers for the next call
+  // The last CTA to leave clears the barriers for the next call; where a CTA gave up (counted in the upper half),
+  // the counts that may have been left halfway, too.
   if (tid == 0) {
+    const unsigned gave_up = dn_aborted(bars) ? 1u << 16 : 0u;
     unsigned old;
-    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(&p.head->bar[4]) : "memory");
-    if (old == gridDim.x - 1) {
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;"
+                 : "=r"(old)
+                 : "l"(&p.head->bar[4]), "r"(1u + gave_up)
+                 : "memory");
+    if ((old & 0xffffu) == gridDim.x - 1) {
       for (int i = 0; i < 5; ++i) p.head->bar[i] = 0u;
+      if ((old >> 16) + gave_up) {
+        for (int i = 0; i < 64; ++i) p.head->tok[i] = 0u;
+        for (int i = 0; i < kDnMaxCtas; ++i) p.head->cnt[i] = 0u;
+      }
     }
   }
 }

@@ -12,7 +12,7 @@ import torch
 ses = pytest.importorskip("sparse_expert_swiglu_gb300")
 
 from sparse_expert_swiglu_gb300 import _lib  # noqa: E402
-from tests.test_dense_weights import BF16, _linear_case, _linear_check  # noqa: E402
+from tests.test_dense_weights import BF16, F16, _layer_case, _layer_check, _linear_case, _linear_check  # noqa: E402
 
 gpu = pytest.mark.gpu
 
@@ -66,4 +66,27 @@ def test_products_that_give_up(M, N, K, gated, layout, out):
         assert ses.lib().moe_selftest_linear_timeout(ctypes.byref(op), ws.buf.data_ptr(), ws.nbytes, TRIES, stream) == 0
         assert ws.status() == TIMEOUT
         _linear_check(c, ws=ws)
+        assert ws.status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("barrier", [0, 1, 2, 3])
+@pytest.mark.parametrize("B,d,f,E,k,ns,dtype", [(1, 512, 1024, 16, 4, 0, BF16), (5, 1032, 520, 8, 2, 1, F16),
+                                                (17, 1024, 520, 8, 2, 1, F16), (64, 256, 264, 64, 6, 2, BF16)])
+def test_layers_that_give_up(B, d, f, E, k, ns, dtype, barrier):
+    """The counts that a layer leaves are zero again, so that the next call's barriers hold."""
+    c = _layer_case(B, d, f, E, k, ns, dtype, True, False, True)
+    x = c["x"].cuda()
+    head = ses.linear_workspace_bytes(1, 1, 8)
+    ws = ses.Workspace(ses.layer_dense_workspace_bytes(c["layer"], B))
+    y = torch.empty_like(x)
+    layer = c["layer"].c_struct()
+    want = _layer_check(c)
+    stream = torch.cuda.current_stream().cuda_stream
+    for _ in range(2):
+        assert ses.lib().moe_selftest_layer_dense_timeout(x.data_ptr(), B, ctypes.byref(layer), y.data_ptr(), 1, barrier,
+                                                          ws.buf.data_ptr(), ws.nbytes, TRIES, stream) == 0
+        assert ws.status() == TIMEOUT
+        assert (ws.buf[:head] == 0).all()
+        assert torch.equal(_layer_check(c, ws), want)
         assert ws.status() == 0
