@@ -574,7 +574,8 @@ def _dense_x(x) -> int:
     raise ValueError(f"x is on cuda:{device}, which is not the current device")
 
 
-try:  # torch.empty on the current CUDA device without the dispatcher: half its time in a decode step's many calls
+try:  # torch.empty on the current CUDA device without the dispatcher: half its time in a decode step's many calls.  (Dispatch
+      # modes do not see these outputs; every element is written by the call.)
     from torch._C._dynamo.guards import _empty_strided_cuda
 except ImportError:
     def _empty_strided_cuda(shape, stride, dtype):
@@ -610,7 +611,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
 
     x [M, K] fp16 or bf16; w (and w_mul) [N, K] ("nk": row n = output n, as gate_t) or [K, N] ("kn", as down
     and w_router); act "none", "relu", "gelu", "gelu_tanh" or "silu"; out_dtype x's (default) or torch.float32.
-    out may be the residual's tensor (with x's type), no other input's."""
+    out may be the residual's tensor (with x's type), no other input's.  Inference alone: gradients do not pass."""
     device = _dense_x(x)
     dt = x.dtype
     dtype_code = 0 if dt is torch.float16 else 1
@@ -741,7 +742,7 @@ def expert_dense_workspace_bytes(n: int, d: int, f: int) -> int:
 def expert_dense_swiglu(x: torch.Tensor, experts: DenseExperts, expert: int, residual: Optional[torch.Tensor] = None,
                         ws: Optional[Workspace] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """One uncompressed SwiGLU expert on every row of x [n, d]: (SiLU(x W^gate) * x W^up) W^down [+ residual].
-    out may be the residual's tensor or x."""
+    out may be the residual's tensor or x.  Inference alone: gradients do not pass."""
     device = _dense_x(x)
     dt = x.dtype
     n = x.shape[0]
@@ -776,7 +777,7 @@ def layer_dense_decode(x: torch.Tensor, layer: DenseLayer, residual: Optional[to
                        ws: Optional[Workspace] = None, debug: bool = False, out: Optional[torch.Tensor] = None):
     """One MoE layer of uncompressed experts on x [B, d], B <= 64 -> y [B, d] (and, with debug, a dict with
     topk_idx and topk_w): the weighted sum of the experts [+ residual] [RMSNorm].  out may be the residual's
-    tensor, not x."""
+    tensor, not x.  Inference alone: gradients do not pass."""
     device = _dense_x(x)
     dt = x.dtype
     B = x.shape[0]

@@ -233,7 +233,7 @@ __device__ __forceinline__ void choose(const LayerArgs& p, int b, float* slices,
   }
 }
 
-// Whole CTA: n values of other CTAs to shared memory, eight of a thread's in flight.
+// Whole CTA: n values of other CTAs to shared memory, four of a thread's in flight.
 __device__ void gather_logits(const float* from, int n, float* to) {
   for (int i = threadIdx.x; i < n; i += 4 * kDnThreads) {
     float t[4];

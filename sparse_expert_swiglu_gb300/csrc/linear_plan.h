@@ -17,7 +17,7 @@ constexpr int kFewTokens = 32;
 constexpr int kTogether = 8;  // token tiles that go through all features together
 
 // Clusters of S CTAs that fit the GPU at once, of at most one CTA per SM (152 SMs: 76, 36 and 15; the SMs of a
-// cluster lie in one part of the chip).
+// cluster lie in one part of the chip).  For the model alone: where fewer fit, a call takes longer and gives the same.
 inline int clusters(int S, int sms) { return S == 1 ? sms : S == 2 ? sms / 2 : S == 4 ? sms / 4 - 2 : sms / 8 - 4; }
 
 // Bytes of a cluster's partial sums in one CTA.
@@ -82,7 +82,8 @@ inline bool linear_sums(const LinearPlan& l, int K, bool f32, LinearSums& s) {
 //   a CTA pair's stage 650 with 256 columns, and 27 a column for its last epilogue, and HBM
 //   adds 0.25 of the weights' time (2048 x 14336 gated, K = 4096: 275 us against the model's 279; one CTA a
 //   tile 321; 300 tokens 80 and 80); 90 a column for the others,
-//   which run under the next tile's products (384 x 7808 gated, GELU, K = 120: 7200 for 64 columns).
+//   which run under the next tile's products (384 x 7808 gated, GELU, K = 120: 7200 for 64 columns); 6 a column for a
+//   round of sums that is added up, under the next round's products.
 inline LinearPlan make_plan(int M, int N, int K, bool gated, bool kn, bool plain, bool f32, int sms, int room) {
   LinearPlan best;
   double best_t = 1e30;
