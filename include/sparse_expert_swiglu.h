@@ -390,6 +390,121 @@ moe_status_t moe_layer_dense_decode(const uint16_t* x, int32_t B, const moe_dens
                                     const uint16_t* residual, uint16_t* y, int32_t rmsnorm_out,
                                     const moe_debug_t* dbg, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------- 8-bit integer weights and tokens ----------------
+ *
+ * Products whose weights and tokens are 8-bit integers with one fp32 scale for each weight row (output) and each token,
+ * the expert made of them, and the residual and norm between two blocks, which can hand on 8-bit tokens.  Sums over k are
+ * exact integers: a result does not depend on how many tokens the call has, and equal calls give equal bits.
+ * q = -128 is allowed in given integers and never made by a quantiser.
+ *
+ * Quantised rows (moe_quantize_int8 and the tokens that other calls quantise): with m the largest |x| of the row,
+ * scale = m / 127 in fp32 and q = 127 x / m rounded to the nearest integer, exact halves to the even one.  A row of
+ * zeros has scale 0; a row with an infinity or a NaN has scale NaN and q = 0.
+ *
+ * Workspaces: as in the section above, and the two sections' calls may share one.  A y that overlaps an input, and a
+ * workspace that overlaps any tensor of the call, is refused (MOE_ERR_INVALID_ARG) but where stated.
+ */
+enum { MOE_I8 = 3 };
+
+/*
+ * moe_quantize_int8 -- rows of 8-bit integers and their scales.
+ *   x [rows][K] of dtype MOE_F16, MOE_BF16 or MOE_F32; q int8 [rows][K]; scale fp32 [rows];
+ *   rows 0..2^31 - 1 (0 is a no-op), K 16..65536, a multiple of 16.
+ * Weights are quantised by output with the same call: w [N][K] -> q [N][K], scale [N].
+ */
+moe_status_t moe_quantize_int8(const void* x, int32_t dtype, int32_t rows, int32_t K, int8_t* q, float* scale,
+                               void* stream);
+
+/*
+ * moe_linear_int8 -- y = act(a(w) + bias) [* (a(w_mul) + bias_mul)] [+ residual], rounded once, with
+ *   a(w)[m][n] = x_scale[m] * w_scale[n] * sum_k x[m][k] w[n][k].
+ *   M 0..1048576 tokens (0 is a no-op), N 1..1048576 outputs, K 16..65536 inputs, a multiple of 16;
+ *   x_dtype    MOE_I8: x int8 [M][K] with x_scale [M]; or dtype: x [M][K] in 16 bits, quantised by token on
+ *              the way (x_scale NULL)
+ *   dtype      MOE_F16 or MOE_BF16: bias, bias_mul, residual
+ *   out_dtype  of y: dtype, or MOE_F32
+ *   act        MOE_ACT_*
+ *   w, w_mul int8 [N][K] with w_scale, w_mul_scale fp32 [N]; y [M][N]; bias [N], bias_mul [N] (only with w_mul),
+ *   residual [M][N]: NULL leaves that part out.  y may be the residual's buffer (with out_dtype = dtype).
+ *   ws / ws_bytes: at least moe_linear_int8_workspace_bytes(M, N, K, w_mul != NULL) bytes.
+ */
+typedef struct {
+  int32_t M, N, K;
+  int32_t x_dtype, dtype, out_dtype, act;
+  const void* x;
+  const float* x_scale;
+  const int8_t* w;
+  const float* w_scale;
+  const int8_t* w_mul;
+  const float* w_mul_scale;
+  const void* bias;
+  const void* bias_mul;
+  const void* residual;
+  void* y;
+} moe_linear_int8_t;
+
+size_t moe_linear_int8_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t gated);
+moe_status_t moe_linear_int8(const moe_linear_int8_t* op, void* ws, size_t ws_bytes, void* stream);
+
+/* One stack of equally shaped 8-bit experts: d 16..16384, f 16..65536, multiples of 16; E 1..256. */
+typedef struct {
+  int32_t E;
+  int32_t d;
+  int32_t f;
+  const int8_t* gate_t;      /* [E][f][d]: row i = column i of W^gate; gate_scale fp32 [E][f] */
+  const float* gate_scale;
+  const int8_t* up_t;        /* [E][f][d]: row i = column i of W^up; up_scale fp32 [E][f] */
+  const float* up_scale;
+  const int8_t* down_t;      /* [E][d][f]: row i = column i of W^down; down_scale fp32 [E][d] */
+  const float* down_scale;
+} moe_int8_experts_t;
+
+/*
+ * moe_expert_int8_swiglu -- one expert on n tokens (0..1048576):
+ *   h[b] = SiLU(x_b W^gate) (.) x_b W^up in fp32, quantised by token;  y[b] = h[b] W^down [+ residual[b]]
+ *   x, x_scale, x_dtype, dtype as in moe_linear_int8; y [n][d] and residual [n][d] (or NULL) of dtype; y may be the
+ *   residual's buffer or, in 16 bits, x's.
+ *   ws / ws_bytes: at least moe_expert_int8_workspace_bytes(n, d, f) bytes.
+ */
+size_t moe_expert_int8_workspace_bytes(int32_t n, int32_t d, int32_t f);
+moe_status_t moe_expert_int8_swiglu(const void* x, const float* x_scale, int32_t x_dtype, int32_t dtype, int32_t n,
+                                    const moe_int8_experts_t* experts, int32_t expert, const void* residual, void* y,
+                                    void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_residual_norm -- the norms behind and before a block, with its gate, its scale and the residual's:
+ *   s[b] = residual_scale * residual[b] + block_scale * gate[b / (M / gate_rows)] (.) post(x[b]),
+ *   y[b] = norm(s[b]), of s before its rounding; fp32 throughout, each result rounded once.
+ *   norms: MOE_NORM_NONE; MOE_NORM_RMS: v / sqrt(mean(v^2) + eps) * weight + bias;
+ *          MOE_NORM_LAYER: (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * weight + bias
+ *   M 0..1048576 tokens (0 is a no-op), d 8..16384, a multiple of 8 (y_dtype MOE_I8: of 16); eps >= 0
+ *   x [M][d], gate [gate_rows][d] (M a multiple of gate_rows; 0: no gate), post_weight, post_bias, weight, bias [d] or
+ *   NULL, of dtype MOE_F16 or MOE_BF16; residual [M][d] or NULL (0 in its place) and s [M][d] or NULL (not written) of
+ *   s_dtype: dtype or MOE_F32;
+ *   y [M][d] of y_dtype: dtype, or MOE_I8 with y_scale fp32 [M], y quantised by token; NULL with MOE_NORM_NONE.
+ *   s may be the residual's buffer, and s or y x's (of the same type); an output that overlaps another
+ *   tensor otherwise is refused (MOE_ERR_INVALID_ARG).  At least one of s and y.
+ */
+enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 };
+typedef struct {
+  int32_t M, d;
+  int32_t dtype, s_dtype, y_dtype;
+  int32_t post, norm, gate_rows;
+  float residual_scale, block_scale, eps;
+  const void* x;
+  const void* residual;
+  const void* gate;
+  const void* post_weight;
+  const void* post_bias;
+  const void* weight;
+  const void* bias;
+  void* s;
+  void* y;
+  float* y_scale;
+} moe_residual_norm_t;
+
+moe_status_t moe_residual_norm(const moe_residual_norm_t* op, void* stream);
+
 /* ---------------- expert activation tracking and expert cache (host) ----------------
  *
  * "MoE-Infinity" (sec. 4.3, 4.5, 4.7 Algorithm 1 "专家缓存检索", appendix B.1): request-level

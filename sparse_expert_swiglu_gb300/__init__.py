@@ -12,12 +12,15 @@ from ._lib import (  # noqa: F401
     EXPORTED,
     ExpertCache,
     Experts,
+    Int8Experts,
     Layer,
     MoeError,
     Workspace,
     eam_add_counts,
     expert_dense_swiglu,
     expert_dense_workspace_bytes,
+    expert_int8_swiglu,
+    expert_int8_workspace_bytes,
     expert_sparse_swiglu,
     expert_workspace_bytes,
     layer_decode,
@@ -30,10 +33,14 @@ from ._lib import (  # noqa: F401
     lib,
     lib_path,
     linear,
+    linear_int8,
+    linear_int8_workspace_bytes,
     linear_workspace_bytes,
     pack_int2_up,
     packed_bytes,
     prefetch_experts,
+    quantize_int8,
+    residual_norm,
     route_topk,
     route_topk_noalloc,
     route_workspace_bytes,

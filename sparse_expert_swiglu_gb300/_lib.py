@@ -64,10 +64,31 @@ class _Linear(ctypes.Structure):
                [(n, ctypes.c_void_p) for n in ("x", "w", "w_mul", "bias", "bias_mul", "residual", "y")]
 
 
+class _LinearInt8(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "x_dtype", "dtype", "out_dtype", "act")] + \
+               [(n, ctypes.c_void_p) for n in ("x", "x_scale", "w", "w_scale", "w_mul", "w_mul_scale", "bias", "bias_mul",
+                                               "residual", "y")]
+
+
+class _Int8Experts(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("d", ctypes.c_int32), ("f", ctypes.c_int32)] + \
+               [(n, ctypes.c_void_p) for n in ("gate_t", "gate_scale", "up_t", "up_scale", "down_t", "down_scale")]
+
+
+class _ResidualNorm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "d", "dtype", "s_dtype", "y_dtype", "post", "norm", "gate_rows")] + \
+               [(n, ctypes.c_float) for n in ("residual_scale", "block_scale", "eps")] + \
+               [(n, ctypes.c_void_p) for n in ("x", "residual", "gate", "post_weight", "post_bias", "weight", "bias", "s",
+                                               "y", "y_scale")]
+
+
 # the same as bytes, which are filled in half the time
 _LINEAR = struct.Struct("@7i7P").pack
 _DENSE_EXPERTS = struct.Struct("@4i3P").pack
 _DENSE_LAYER = struct.Struct("@2iP4i3P4i3P").pack
+_LINEAR_INT8 = struct.Struct("@7i10P").pack
+_INT8_EXPERTS = struct.Struct("@3i6P").pack
+_RESIDUAL_NORM = struct.Struct("@8i3f10P").pack
 
 
 _LIB = None
@@ -135,6 +156,15 @@ _SIGS = {
                                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                               ctypes.POINTER(_Debug), ctypes.c_void_p, ctypes.c_size_t,
                                               ctypes.c_void_p]),
+    "moe_quantize_int8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_linear_int8_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 4),
+    "moe_linear_int8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_expert_int8_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 3),
+    "moe_expert_int8_swiglu": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                              ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_residual_norm": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "moe_workspace_init": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "moe_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32,
                                                  ctypes.c_void_p]),
@@ -806,6 +836,285 @@ def layer_dense_decode(x: torch.Tensor, layer: DenseLayer, residual: Optional[to
         if status:
             raise MoeError("moe_layer_dense_decode", status)
     return (y, dt_) if debug else y
+
+
+# ---------------------------------------------------------------------------
+# 8-bit integer weights and tokens; the norms around a block
+# ---------------------------------------------------------------------------
+
+_CODES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2, torch.int8: 3}
+_NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+
+def _current(x, name: str) -> int:
+    """The device of x: a dense CUDA tensor on the current device."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    device = x.get_device()
+    if device < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on cuda:{device}, which is not the current device")
+    return device
+
+
+def _dense_out(out, shape, stride, dtype, device: int, name: str):
+    """(tensor, address) of an output: the caller's, checked, or a new one."""
+    if out is None:
+        y = _empty_strided_cuda(shape, stride, dtype)
+        return y, y.data_ptr()
+    return out, _dense_in(out, dtype, device, shape, name)
+
+
+def _int8_x(x, x_scale, dtype):
+    """(device, type of the call, code of x, address of x_scale) of a call's tokens: 8-bit with scales, or 16-bit."""
+    device = _current(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    if x.dtype is torch.int8:
+        if dtype is not torch.float16 and dtype is not torch.bfloat16:
+            raise TypeError(f"dtype must be torch.float16 or torch.bfloat16 with 8-bit x, got {dtype}")
+        if x_scale is None:
+            raise ValueError("8-bit x needs x_scale")
+        return device, dtype, 3, _dense_in(x_scale, torch.float32, device, (x.shape[0],), "x_scale")
+    if x.dtype is not torch.float16 and x.dtype is not torch.bfloat16:
+        raise TypeError(f"x must be torch.int8, torch.float16 or torch.bfloat16, got {x.dtype}")
+    if x_scale is not None:
+        raise ValueError("x_scale goes with 8-bit x")
+    if dtype is not None and dtype is not x.dtype:
+        raise TypeError(f"dtype must be x's, {x.dtype}, got {dtype}")
+    return device, x.dtype, _CODES[x.dtype], 0
+
+
+def quantize_int8(x: torch.Tensor, out: Optional[torch.Tensor] = None, out_scale: Optional[torch.Tensor] = None):
+    """Rows of 8-bit integers and their scales: x [..., K] fp16, bf16 or fp32 -> (q int8 [..., K], scale fp32 [...]).
+
+    scale = max|x| / 127 and q = 127 x / max|x| rounded to the nearest, halves to even, for each row: tokens, or weights
+    with one output a row.  A row of zeros has scale 0; one with an infinity or NaN has scale NaN and q = 0."""
+    device = _current(x, "x")
+    code = _CODES.get(x.dtype, 3)
+    if code == 3:
+        raise TypeError(f"x must be torch.float16, torch.bfloat16 or torch.float32, got {x.dtype}")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    rows, K = x.shape[:-1].numel(), x.shape[-1]
+    if out is None:
+        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    else:
+        q = out
+        _dense_in(out, torch.int8, device, x.shape, "out")
+    if out_scale is None:
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    else:
+        scale = out_scale
+        _dense_in(out_scale, torch.float32, device, x.shape[:-1], "out_scale")
+    status = (_LIB or lib()).moe_quantize_int8(x.data_ptr(), code, rows, K, q.data_ptr(), scale.data_ptr(),
+                                               _stream_of(device))
+    if status:
+        raise MoeError("moe_quantize_int8", status)
+    return q, scale
+
+
+def linear_int8_workspace_bytes(M: int, N: int, K: int, gated: bool = False) -> int:
+    return int(lib().moe_linear_int8_workspace_bytes(M, N, K, 1 if gated else 0))
+
+
+def linear_int8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, x_scale: Optional[torch.Tensor] = None,
+                bias: Optional[torch.Tensor] = None, act: str = "none", w_mul: Optional[torch.Tensor] = None,
+                w_mul_scale: Optional[torch.Tensor] = None, bias_mul: Optional[torch.Tensor] = None,
+                residual: Optional[torch.Tensor] = None, dtype=None, out_dtype=None, ws: Optional[Workspace] = None,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y = act(a(w) + bias) [* (a(w_mul) + bias_mul)] [+ residual] with a(w) = x_scale * w_scale * (x w^T), whose sums
+    are exact integers; rounded once.
+
+    x [M, K] int8 with x_scale fp32 [M], or fp16 or bf16, quantised by token on the way (as quantize_int8); w (and w_mul)
+    int8 [N, K] with w_scale fp32 [N]; dtype: the type of bias, residual and y, x's if x has 16 bits; out_dtype dtype
+    (default) or torch.float32; act as in linear.  out may be the residual's tensor (with out_dtype = dtype), no other
+    input's.  Inference alone: gradients do not pass."""
+    device, dt, x_code, xs = _int8_x(x, x_scale, dtype)
+    act_code = _ACTS.get(act, -1)
+    if act_code < 0:
+        raise ValueError(f"act must be one of {tuple(_ACTS)}, got {act!r}")
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be a matrix")
+    if (w_mul is None) != (w_mul_scale is None):
+        raise ValueError("w_mul and w_mul_scale go together")
+    if bias_mul is not None and w_mul is None:
+        raise ValueError("bias_mul goes with w_mul")
+    M, K = x.shape
+    N = w.shape[0]
+    if out_dtype is None:
+        out_dtype = dt
+    elif out_dtype is not dt and out_dtype is not torch.float32:
+        raise TypeError(f"out_dtype must be {dt} or torch.float32, got {out_dtype}")
+    y, yp = _dense_out(out, (M, N), (N, 1), out_dtype, device, "out")
+    wshape, vec = (N, K), (N,)
+    op = _LINEAR_INT8(M, N, K, x_code, _CODES[dt], _CODES[out_dtype], act_code, x.data_ptr(), xs,
+                      _dense_in(w, torch.int8, device, wshape, "w"),
+                      _dense_in(w_scale, torch.float32, device, vec, "w_scale"),
+                      0 if w_mul is None else _dense_in(w_mul, torch.int8, device, wshape, "w_mul"),
+                      0 if w_mul is None else _dense_in(w_mul_scale, torch.float32, device, vec, "w_mul_scale"),
+                      0 if bias is None else _dense_in(bias, dt, device, vec, "bias"),
+                      0 if bias_mul is None else _dense_in(bias_mul, dt, device, vec, "bias_mul"),
+                      0 if residual is None else _dense_in(residual, dt, device, (M, N), "residual"), yp)
+    if M == 0:
+        return y
+    ws = _dense_ws(ws, device, linear_int8_workspace_bytes, M, N, K, w_mul is not None)
+    status = (_LIB or lib()).moe_linear_int8(op, ws.buf.data_ptr(), ws.nbytes, _stream_of(device))
+    if status:
+        raise MoeError("moe_linear_int8", status)
+    return y
+
+
+@dataclass
+class Int8Experts:
+    """A stack of E equally shaped experts of 8-bit integers (device tensors): gate_t and up_t int8 [E, f, d] with scales
+    fp32 [E, f], down_t int8 [E, d, f] with scales [E, d]; one row and one scale for each output (a column of W)."""
+    gate_t: torch.Tensor
+    gate_scale: torch.Tensor
+    up_t: torch.Tensor
+    up_scale: torch.Tensor
+    down_t: torch.Tensor
+    down_scale: torch.Tensor
+
+    @classmethod
+    def from_dense(cls, experts: DenseExperts) -> "Int8Experts":
+        """Uncompressed experts, quantised by output."""
+        down_t = experts.down.transpose(1, 2).contiguous()
+        return cls(*quantize_int8(experts.gate_t.contiguous()), *quantize_int8(experts.up_t), *quantize_int8(down_t))
+
+    @property
+    def E(self):
+        return self.gate_t.shape[0]
+
+    @property
+    def f(self):
+        return self.gate_t.shape[1]
+
+    @property
+    def d(self):
+        return self.gate_t.shape[2]
+
+    def c_struct(self) -> _Int8Experts:
+        return _Int8Experts.from_buffer_copy(self._pack())
+
+    def _pack(self) -> bytes:
+        """The C structure, as bytes: shapes, types and devices checked."""
+        g = self.gate_t
+        if not isinstance(g, torch.Tensor) or g.dim() != 3:
+            raise ValueError("gate_t must have shape [E, f, d]")
+        device = g.get_device()
+        if device < 0:
+            raise TypeError("gate_t must be a CUDA tensor")
+        E, f, d = g.shape
+        i8, f32 = torch.int8, torch.float32
+        return _INT8_EXPERTS(E, d, f, _dense_in(g, i8, device, (E, f, d), "gate_t"),
+                             _dense_in(self.gate_scale, f32, device, (E, f), "gate_scale"),
+                             _dense_in(self.up_t, i8, device, (E, f, d), "up_t"),
+                             _dense_in(self.up_scale, f32, device, (E, f), "up_scale"),
+                             _dense_in(self.down_t, i8, device, (E, d, f), "down_t"),
+                             _dense_in(self.down_scale, f32, device, (E, d), "down_scale"))
+
+
+def expert_int8_workspace_bytes(n: int, d: int, f: int) -> int:
+    return int(lib().moe_expert_int8_workspace_bytes(n, d, f))
+
+
+def expert_int8_swiglu(x: torch.Tensor, experts: Int8Experts, expert: int, x_scale: Optional[torch.Tensor] = None,
+                       residual: Optional[torch.Tensor] = None, dtype=None, ws: Optional[Workspace] = None,
+                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One SwiGLU expert of 8-bit integers on every row of x [n, d]: h = SiLU(x W^gate) * x W^up in fp32, quantised by
+    token, then h W^down [+ residual].  x, x_scale and dtype as in linear_int8; out may be the residual's tensor or, if
+    x has 16 bits, x.  Inference alone: gradients do not pass."""
+    device, dt, x_code, xs = _int8_x(x, x_scale, dtype)
+    c = experts._pack()
+    if experts.gate_t.get_device() != device:
+        raise ValueError("x and the experts must be on one device")
+    _, f, d = experts.gate_t.shape
+    n = x.shape[0]
+    shape = (n, d)
+    if x.shape[1] != d:
+        raise ValueError(f"x must have shape {shape}, got {tuple(x.shape)}")
+    rp = None if residual is None else _dense_in(residual, dt, device, shape, "residual")
+    y, yp = _dense_out(out, shape, (d, 1), dt, device, "out")
+    if n == 0:
+        return y
+    ws = _dense_ws(ws, device, expert_int8_workspace_bytes, n, d, f)
+    status = (_LIB or lib()).moe_expert_int8_swiglu(x.data_ptr(), xs or None, x_code, _CODES[dt], n, c, expert, rp, yp,
+                                                    ws.buf.data_ptr(), ws.nbytes, _stream_of(device))
+    if status:
+        raise MoeError("moe_expert_int8_swiglu", status)
+    return y
+
+
+def residual_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, post: str = "none",
+                  post_weight: Optional[torch.Tensor] = None, post_bias: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0, block_scale: float = 1.0,
+                  norm: str = "rms", weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                  eps: float = 1e-6, int8: bool = False, residual_out: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, out_scale: Optional[torch.Tensor] = None):
+    """s = residual_scale * residual + block_scale * gate * post(x), y = norm(s): the norm behind a block, its gate, the
+    residual, and the next block's norm.  fp32 throughout; y is of s before its rounding.
+
+    x [M, d] fp16 or bf16; residual [M, d] of x's type or fp32; post and norm "none", "rms" or "layer" with weights and
+    biases [d]; gate [d] or [G, d], M a multiple of G: one for every M / G tokens.  int8: y is quantised by token
+    (quantize_int8 of the fp32 y).  Returns (s, y), with int8 (s, q, scale); with norm "none" s alone; without a residual
+    y, or (q, scale), alone.  s has the residual's type.  residual_out, out, out_scale take s, y (q), scale; residual_out
+    may be the residual's tensor, and either one x's.  Inference alone: gradients do not pass."""
+    device = _dense_x(x)
+    dt = x.dtype
+    M, d = x.shape
+    kinds = _NORMS.get(post, -1), _NORMS.get(norm, -1)
+    if min(kinds) < 0:
+        raise ValueError(f"post and norm must be one of {tuple(_NORMS)}, got {post!r} and {norm!r}")
+    if int8 and norm == "none":
+        raise ValueError("int8 goes with a norm")
+    if post == "none" and (post_weight is not None or post_bias is not None):
+        raise ValueError("post_weight and post_bias go with post")
+    if norm == "none" and (weight is not None or bias is not None or out is not None):
+        raise ValueError("weight, bias and out go with norm")
+    if out_scale is not None and not int8:
+        raise ValueError("out_scale goes with int8")
+    shape, vec = (M, d), (d,)
+    s_dt, rp = dt, 0
+    if residual is not None:
+        s_dt = torch.float32 if isinstance(residual, torch.Tensor) and residual.dtype is torch.float32 else dt
+        rp = _dense_in(residual, s_dt, device, shape, "residual")
+    gp, gate_rows = 0, 0
+    if gate is not None:
+        gate_rows = gate.shape[0] if isinstance(gate, torch.Tensor) and gate.dim() == 2 else 1
+        gp = _dense_in(gate, dt, device, (gate_rows, d) if isinstance(gate, torch.Tensor) and gate.dim() == 2 else vec, "gate")
+        if gate_rows < 1 or M % gate_rows:
+            raise ValueError(f"gate has {gate_rows} rows, which do not divide {M} tokens")
+
+    def vector(t, name):
+        return 0 if t is None else _dense_in(t, dt, device, vec, name)
+    vectors = (vector(post_weight, "post_weight"), vector(post_bias, "post_bias"), vector(weight, "weight"),
+               vector(bias, "bias"))
+    s = y = scale = None
+    sp = yp = scp = 0
+    if residual is not None or norm == "none":
+        s, sp = _dense_out(residual_out, shape, (d, 1), s_dt, device, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out goes with residual or norm 'none'")
+    y_dt = torch.int8 if int8 else dt
+    if norm != "none":
+        y, yp = _dense_out(out, shape, (d, 1), y_dt, device, "out")
+    if int8:
+        scale, scp = _dense_out(out_scale, (M,), (1,), torch.float32, device, "out_scale")
+    if M:
+        op = _RESIDUAL_NORM(M, d, _CODES[dt], _CODES[s_dt], _CODES[y_dt], kinds[0], kinds[1], gate_rows, residual_scale,
+                            block_scale, eps, x.data_ptr(), rp, gp, *vectors, sp, yp, scp)
+        status = (_LIB or lib()).moe_residual_norm(op, _stream_of(device))
+        if status:
+            raise MoeError("moe_residual_norm", status)
+    if norm == "none":
+        return s
+    if s is None:
+        return (y, scale) if int8 else y
+    return (s, y, scale) if int8 else (s, y)
 
 
 # ---------------------------------------------------------------------------

@@ -7,6 +7,7 @@
 // along k: each CTA pushes its partial sums into the shared memory of the CTA that owns their features,
 // which adds them in the order of k and runs the epilogue for them (no workspace, no
 // count in global memory).  linear_plan chooses the tile and the cluster.
+#include "activate.cuh"
 #include "dense.cuh"
 #include "dense_params.cuh"
 #include "linear_plan.h"
@@ -42,32 +43,6 @@ __device__ __forceinline__ void tile_at(int t, int T, int MT, int& ft, int& mt) 
   const int here = MT - b * kTogether < kTogether ? MT - b * kTogether : kTogether;
   ft = r / here;
   mt = b * kTogether + r - ft * here;
-}
-
-// One decision for W values, not one for each.  (silu_f's fast exponential is off by up to 2 + 1.2 |v| units in the last
-// place: below the sums' own error where the result is not small beside |v|.)
-template <int W>
-__device__ __forceinline__ void activate(float (&v)[W], int act) {
-  switch (act) {
-    case MOE_ACT_RELU:
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];  // NaN stays NaN
-      break;
-    case MOE_ACT_GELU:
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = 0.5f * v[i] * (1.f + erff(v[i] * 0.70710678118654752f));
-      break;
-    case MOE_ACT_GELU_TANH:
-#pragma unroll
-      for (int i = 0; i < W; ++i)
-        v[i] = 0.5f * v[i] * (1.f + tanhf(0.79788456080286536f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));
-      break;
-    case MOE_ACT_SILU:
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = silu_f(v[i]);
-      break;
-    default: break;
-  }
 }
 
 // The residual of W tokens of one feature; token i at offset at + i * N.

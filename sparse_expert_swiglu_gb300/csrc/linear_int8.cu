@@ -1,0 +1,239 @@
+// y = act(s_x s_w (x w^T) + bias) [* (s_x s_mul (x w_mul^T) + bias_mul)] [+ residual] on 8-bit integers.
+//
+// Few tokens: a stream of w, bound by HBM.  A warp takes RW neighbouring rows of w (with w_mul the same rows of both) at a
+// time, 16 bytes a lane and load, the next loads in flight while it multiplies; the tokens lie in shared memory, where every
+// CTA quantises them itself.  Four products and their sum are one instruction (dp4a: 254 products a clock and SM, of which
+// HBM's rate needs 23 for each token); sums are integers, so that their order is free.
+#include "activate.cuh"
+#include "dense.cuh"
+#include "dense_params.cuh"
+#include "int8.cuh"
+#include "int8_params.cuh"
+
+namespace sesg {
+
+namespace {
+
+constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32;
+constexpr int kFewShared = 96 << 10;  // bytes of tokens
+
+struct Int8Args {
+  int M, N, K, x16, bf16, act, out_f32;
+  int parts;            // warps that share a row along k
+  const void* x;
+  const float* x_scale;
+  const int8_t *w, *w_mul;
+  const float *w_scale, *w_mul_scale;
+  const void *bias, *bias_mul, *residual;
+  void* y;
+};
+
+__device__ __forceinline__ void store_one(const Int8Args& p, int tok, int row, int sum, int sum_mul, float xs) {
+  float v[1] = {(float)sum * (xs * p.w_scale[row])};
+  if (p.bias) v[0] += ld16(p.bias, row, p.bf16);
+  activate(v, p.act);
+  if (p.w_mul) {
+    float m = (float)sum_mul * (xs * p.w_mul_scale[row]);
+    if (p.bias_mul) m += ld16(p.bias_mul, row, p.bf16);
+    v[0] *= m;
+  }
+  const size_t at = (size_t)tok * p.N + row;
+  if (p.residual) v[0] += ld16(p.residual, at, p.bf16);
+  if (p.out_f32) reinterpret_cast<float*>(p.y)[at] = v[0];
+  else reinterpret_cast<unsigned short*>(p.y)[at] = to16(v[0], p.bf16);
+}
+
+// The tokens t0 .. t0 + nt - 1 as integers in shared memory, and their scales.
+__device__ __forceinline__ void few_tokens(const Int8Args& p, int t0, int nt, int8_t* xq, float* scales, uint32_t* most) {
+  const int tid = threadIdx.x;
+  if (!p.x16) {
+    const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const int8_t*>(p.x) + (size_t)t0 * p.K);
+    for (int i = tid; i < nt * (p.K / 16); i += kFewThreads) reinterpret_cast<uint4*>(xq)[i] = from[i];
+    if (tid < nt) scales[tid] = p.x_scale[t0 + tid];
+    __syncthreads();
+    return;
+  }
+  const int n = p.K / 8;
+  const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned short*>(p.x) + (size_t)t0 * p.K);
+  if (tid < nt) most[tid] = 0;
+  __syncthreads();
+  for (int t = 0; t < nt; ++t) {
+    uint32_t m = 0;
+    for (int i = tid; i < n; i += kFewThreads) m = most16(m, from[(size_t)t * n + i]);
+    m = warp_most(most_f32(m, p.bf16));
+    if ((tid & 31) == 0) atomicMax(&most[t], m);
+  }
+  __syncthreads();
+  for (int t = 0; t < nt; ++t) {
+    const RowScale s = row_scale(most[t]);
+    if (tid == 0) scales[t] = s.scale;
+    for (int i = tid; i < n; i += kFewThreads) {
+      float v[8];
+      unpack8(from[(size_t)t * n + i], p.bf16, v);
+      reinterpret_cast<uint2*>(xq)[t * n + i] = quantize8(v, s);
+    }
+  }
+  __syncthreads();
+}
+
+// TOK tokens, of which blockIdx.y takes the next; RW rows of w for a warp at a time.
+template <int TOK, int RW>
+__global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const Int8Args p) {
+  constexpr int U = 8 / RW;  // loads of a row in flight
+  extern __shared__ __align__(16) int8_t xq[];
+  __shared__ float scales[TOK];
+  __shared__ uint32_t most[TOK];
+  __shared__ int shared_sums[2][2][kFewWarps][32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int V = p.K / 16, segs = (V + 31) / 32, groups = (p.N + RW - 1) / RW;
+  const int part = warp % p.parts, per = kFewWarps / p.parts;
+  const int s0 = segs * part / p.parts, s1 = segs * (part + 1) / p.parts;
+  const int mats = p.w_mul ? 2 : 1;
+  const int first = (warp / p.parts) * gridDim.x + blockIdx.x, step = per * gridDim.x;
+
+  // a batch: U segments of 32 loads of the group's rows in one matrix
+  struct At {
+    int g, mat, s;
+  };
+  auto fetch = [&](const At& a, uint4 (&v)[RW][U]) {
+    const uint4* base = reinterpret_cast<const uint4*>(a.mat ? p.w_mul : p.w);
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      const int row = a.g * RW + r;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = (a.s + u) * 32 + lane;
+        v[r][u] = row < p.N && a.s + u < s1 && i < V ? ld_stream_v4(base + (size_t)row * V + i) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  uint4 cur[RW][U], next[RW][U];
+  int acc[RW][TOK], kept = 0, round = 0;  // kept: this lane's sum of w, (row, token) = lane
+  auto clear = [&] {
+#pragma unroll
+    for (int r = 0; r < RW; ++r)
+#pragma unroll
+      for (int t = 0; t < TOK; ++t) acc[r][t] = 0;
+  };
+  clear();
+  for (long long first_tok = (long long)blockIdx.y * TOK; first_tok < p.M; first_tok += (long long)gridDim.y * TOK) {
+  const int t0 = (int)first_tok, nt = p.M - t0 < TOK ? p.M - t0 : TOK;
+  At a = {first, 0, s0};
+  if (a.g < groups) fetch(a, cur);
+  __syncthreads();
+  few_tokens(p, t0, nt, xq, scales, most);
+  while (a.g < groups) {
+    At b = {a.g, a.mat, a.s + U};
+    if (b.s >= s1) {
+      b.s = s0;
+      if (++b.mat == mats) {
+        b.mat = 0;
+        b.g += step;
+      }
+    }
+    if (b.g < groups) fetch(b, next);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = (a.s + u) * 32 + lane, at = i < V ? i : 0;  // (behind the row: zeros times anything)
+#pragma unroll
+      for (int t = 0; t < TOK; ++t) {
+        if (t < nt) {
+          const uint4 x = reinterpret_cast<const uint4*>(xq)[(size_t)t * V + at];
+#pragma unroll
+          for (int r = 0; r < RW; ++r) {
+            acc[r][t] = __dp4a((int)cur[r][u].x, (int)x.x, acc[r][t]);
+            acc[r][t] = __dp4a((int)cur[r][u].y, (int)x.y, acc[r][t]);
+            acc[r][t] = __dp4a((int)cur[r][u].z, (int)x.z, acc[r][t]);
+            acc[r][t] = __dp4a((int)cur[r][u].w, (int)x.w, acc[r][t]);
+          }
+        }
+      }
+    }
+    if (b.g != a.g || b.mat != a.mat) {  // the rows' end in this matrix
+      int mine = 0;
+#pragma unroll
+      for (int r = 0; r < RW; ++r)
+#pragma unroll
+        for (int t = 0; t < TOK; ++t) {
+          const int s = __reduce_add_sync(0xffffffffu, acc[r][t]);
+          if (lane == r * TOK + t) mine = s;
+        }
+      clear();
+      if (p.parts > 1) shared_sums[round & 1][a.mat][warp][lane] = mine;
+      if (b.g == a.g) {
+        kept = mine;
+      } else {
+        int sum = mats == 2 ? kept : mine, sum_mul = mine;
+        if (p.parts > 1) {
+          named_barrier(1 + warp / p.parts, p.parts * 32);
+          sum = sum_mul = 0;
+          if (part == 0)
+            for (int i = 0; i < p.parts; ++i) {
+              sum += shared_sums[round & 1][0][warp + i][lane];
+              sum_mul += shared_sums[round & 1][mats - 1][warp + i][lane];
+            }
+        }
+        ++round;
+        const int row = a.g * RW + lane / TOK, tok = lane % TOK;
+        if (part == 0 && lane < RW * TOK && row < p.N && tok < nt) store_one(p, t0 + tok, row, sum, sum_mul, scales[tok]);
+      }
+    }
+    a = b;
+#pragma unroll
+    for (int r = 0; r < RW; ++r)
+#pragma unroll
+      for (int u = 0; u < U; ++u) cur[r][u] = next[r][u];
+  }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_linear_int8(const LinearInt8Call& c, void* ws, int sms, int smem_optin, cudaStream_t st) {
+  Int8Args p;
+  p.M = c.M;
+  p.N = c.N;
+  p.K = c.K;
+  p.x16 = c.x16;
+  p.bf16 = c.bf16;
+  p.act = c.act;
+  p.out_f32 = c.out_f32;
+  p.x = c.x;
+  p.x_scale = c.x_scale;
+  p.w = c.w;
+  p.w_mul = c.w_mul;
+  p.w_scale = c.w_scale;
+  p.w_mul_scale = c.w_mul_scale;
+  p.bias = c.bias;
+  p.bias_mul = c.bias_mul;
+  p.residual = c.residual;
+  p.y = c.y;
+  int tok = 1;
+  while (tok < 8 && tok < c.M && 2 * tok * c.K <= kFewShared) tok *= 2;
+  const int rw = tok == 1 ? 1 : tok == 8 ? 4 : 2, groups = (c.N + rw - 1) / rw;
+  const int segs = (c.K / 16 + 31) / 32;
+  p.parts = 1;
+  while (p.parts < kFewWarps && p.parts * 2 <= segs && (long long)groups * p.parts * 2 <= (long long)sms * kFewWarps)
+    p.parts *= 2;
+  using Kernel = void (*)(Int8Args);
+  const Kernel kernel = tok == 1 ? int8_few_kernel<1, 1> : tok == 2 ? int8_few_kernel<2, 2>
+                        : tok == 4 ? int8_few_kernel<4, 2> : int8_few_kernel<8, 4>;
+  static std::atomic<uint64_t> allowed[4];
+  cudaError_t e = allow_shared(kernel, allowed[tok == 1 ? 0 : tok == 2 ? 1 : tok == 4 ? 2 : 3], smem_optin - (16 << 10));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(groups < sms ? groups : sms, (c.M + tok - 1) / tok < 65535 ? (c.M + tok - 1) / tok : 65535);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = (size_t)tok * c.K;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace sesg
