@@ -607,6 +607,9 @@ moe_status_t moe_selftest_wait_timeout(void* ws, size_t ws_bytes, uint32_t tries
  */
 moe_status_t moe_selftest_linear_timeout(const moe_linear_t* op, void* ws, size_t ws_bytes, uint32_t tries,
                                          void* stream);
+/* ... and of moe_linear_int8's tensor-core kernels, which then run for any number of tokens, like moe_selftest_linear_timeout. */
+moe_status_t moe_selftest_linear_int8_timeout(const moe_linear_int8_t* op, void* ws, size_t ws_bytes, uint32_t tries,
+                                              void* stream);
 moe_status_t moe_selftest_layer_dense_timeout(const uint16_t* x, int32_t B, const moe_dense_layer_t* layer, uint16_t* y,
                                               int32_t rmsnorm_out, int32_t barrier, void* ws, size_t ws_bytes,
                                               uint32_t tries, void* stream);

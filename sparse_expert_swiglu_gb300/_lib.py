@@ -170,6 +170,8 @@ _SIGS = {
                                                  ctypes.c_void_p]),
     "moe_selftest_linear_timeout": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32,
                                                    ctypes.c_void_p]),
+    "moe_selftest_linear_int8_timeout": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32,
+                                                        ctypes.c_void_p]),
     "moe_selftest_layer_dense_timeout": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
                                                         ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                                         ctypes.c_size_t, ctypes.c_uint32, ctypes.c_void_p]),

@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(BUILD, LIB_NAME)
 SOURCES = ["pack.cu", "route.cu", "up.cu", "gather.cu", "combine.cu", "decode.cu", "fetch.cu", "api.cu",
            "noalloc.cu", "selftest.cu", "prefetch.cu", "batched.cu",
            "dense_map.cu", "linear.cu", "dense_layer.cu", "dense_api.cu",
-           "quantize.cu", "linear_int8.cu", "residual_norm.cu", "int8_api.cu", "eam.cpp"]
+           "quantize.cu", "linear_int8.cu", "linear_int8_tiles.cu", "residual_norm.cu", "int8_api.cu", "eam.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]

@@ -469,5 +469,7 @@ __device__ __forceinline__ void dn_stage_products(uint32_t a, uint32_t b, uint32
 // 64 columns by box_rows rows; out-of-range elements read as zeros.  z = 0: a plain matrix.
 cudaError_t dense_map(CUtensorMap* m, const void* base, int bf16, uint64_t cols, uint64_t rows, uint64_t row_stride,
                       uint64_t z, uint64_t z_stride, uint32_t box_rows);
+// A map of a dense [rows][cols] array of bytes (cols a multiple of 16) whose box is 128 columns by box_rows rows.
+cudaError_t int8_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows);
 
 }  // namespace sesg

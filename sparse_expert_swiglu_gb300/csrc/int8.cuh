@@ -82,10 +82,19 @@ __device__ __forceinline__ void unpack8(const uint4& v, int bf16, float (&x)[8])
   }
 }
 
+__device__ __forceinline__ void unpack8(const uint4& a, const uint4& b, float (&x)[8]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+}
+
 // The larger of two pairs of 16-bit |x| patterns, without signs.
 __device__ __forceinline__ uint32_t most16(uint32_t m, uint32_t v) { return __vmaxu2(m, v & 0x7fff7fffu); }
 __device__ __forceinline__ uint32_t most16(uint32_t m, const uint4& v) {
   return most16(most16(most16(most16(m, v.x), v.y), v.z), v.w);
+}
+__device__ __forceinline__ uint32_t most32(uint32_t m, const uint4& v) {
+  return max(max(max(m, v.x & 0x7fffffffu), max(v.y & 0x7fffffffu, v.z & 0x7fffffffu)), v.w & 0x7fffffffu);
 }
 // ... its larger half as the pattern of the same value in fp32
 __device__ __forceinline__ uint32_t most_f32(uint32_t m, int bf16) {
@@ -93,5 +102,20 @@ __device__ __forceinline__ uint32_t most_f32(uint32_t m, int bf16) {
   return bf16 ? h << 16 : __float_as_uint(__half2float(__ushort_as_half((unsigned short)h)));
 }
 __device__ __forceinline__ uint32_t warp_most(uint32_t m) { return __reduce_max_sync(0xffffffffu, m); }
+
+// Four 8-bit integers as fp16: q + 128 in the mantissa of 1024, less 1152.
+__device__ __forceinline__ void to_f16(uint32_t w, uint32_t& a, uint32_t& b) {
+  const uint32_t u = w ^ 0x80808080u;
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+  uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 l = __hsub2(*reinterpret_cast<__half2*>(&lo), bias), h = __hsub2(*reinterpret_cast<__half2*>(&hi), bias);
+  a = *reinterpret_cast<const uint32_t*>(&l);
+  b = *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A product's value from its integer sum and scales.  (Rounded one by one, so that every kernel gives the same bits.)
+__device__ __forceinline__ float int8_value(int sum, float x_scale, float w_scale, float bias) {
+  return __fadd_rn(__fmul_rn((float)sum, __fmul_rn(x_scale, w_scale)), bias);
+}
 
 }  // namespace sesg

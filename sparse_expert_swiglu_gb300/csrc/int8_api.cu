@@ -59,16 +59,12 @@ moe_status_t check_expert_sizes(int n, int d, int f) {
   return MOE_OK;
 }
 
-size_t product_ws(int, int) { return linear_ws_bytes(); }
-
-// Workspace of an expert: a product's, then h in fp32, its integers and their scales.
+// Workspace of an expert: a product's, then h in fp32.
 struct ExpertWs {
-  size_t h, q, scale, bytes;
+  size_t h, bytes;
   ExpertWs(int n, int d, int f) {
-    h = align_up(product_ws(n, d > f ? d : f), kWsAlign);
-    q = h + align_up((size_t)n * f * 4, kWsAlign);
-    scale = q + align_up((size_t)n * f, kWsAlign);
-    bytes = scale + align_up((size_t)n * 4, kWsAlign);
+    h = align_up(Int8Ws(n, d > f ? d : f).bytes, kWsAlign);
+    bytes = h + align_up((size_t)n * f * 4, kWsAlign);
   }
 };
 
@@ -90,10 +86,15 @@ moe_status_t moe_quantize_int8(const void* x, int32_t dtype, int32_t rows, int32
 
 size_t moe_linear_int8_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t gated) {
   if (check_sizes(M, N, K) != MOE_OK) return 0;
-  return product_ws(M, K);
+  return Int8Ws(M, K).bytes;
 }
 
-moe_status_t moe_linear_int8(const moe_linear_int8_t* op, void* ws, size_t ws_bytes, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// tries: diagnostics (else 0), as in LinearInt8Call
+moe_status_t linear_int8_call(const moe_linear_int8_t* op, void* ws, size_t ws_bytes, uint32_t tries, void* stream) {
   if (!op) return MOE_ERR_INVALID_ARG;
   if (!is16(op->dtype) || (op->x_dtype != op->dtype && op->x_dtype != MOE_I8)) return MOE_ERR_INVALID_ARG;
   if (op->out_dtype != op->dtype && op->out_dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
@@ -111,7 +112,7 @@ moe_status_t moe_linear_int8(const moe_linear_int8_t* op, void* ws, size_t ws_by
     return MOE_ERR_ALIGNMENT;
   if (y.overlaps_any(in)) return MOE_ERR_INVALID_ARG;
   if ((op->y != op->residual || op->out_dtype != op->dtype) && y.overlaps(residual)) return MOE_ERR_INVALID_ARG;
-  const size_t need = product_ws(op->M, op->K);
+  const size_t need = Int8Ws(op->M, op->K).bytes;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const Span work = {ws, need};
   if (work.overlaps_any(in) || work.overlaps(y) || work.overlaps(residual)) return MOE_ERR_INVALID_ARG;
@@ -121,7 +122,7 @@ moe_status_t moe_linear_int8(const moe_linear_int8_t* op, void* ws, size_t ws_by
   c.M = op->M;
   c.N = op->N;
   c.K = op->K;
-  c.x16 = x16;
+  c.x_dtype = op->x_dtype;
   c.bf16 = op->dtype == MOE_BF16;
   c.act = op->act;
   c.out_f32 = op->out_dtype == MOE_F32;
@@ -135,7 +136,22 @@ moe_status_t moe_linear_int8(const moe_linear_int8_t* op, void* ws, size_t ws_by
   c.bias_mul = op->bias_mul;
   c.residual = op->residual;
   c.y = op->y;
+  c.tries = tries;
   return cuda_status(launch_linear_int8(c, ws, sms, smem, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_linear_int8(const moe_linear_int8_t* op, void* ws, size_t ws_bytes, void* stream) {
+  return linear_int8_call(op, ws, ws_bytes, 0, stream);
+}
+
+moe_status_t moe_selftest_linear_int8_timeout(const moe_linear_int8_t* op, void* ws, size_t ws_bytes, uint32_t tries,
+                                              void* stream) {
+  if (tries < 1 || tries > 4000) return MOE_ERR_INVALID_ARG;
+  return linear_int8_call(op, ws, ws_bytes, tries, stream);
 }
 
 size_t moe_expert_int8_workspace_bytes(int32_t n, int32_t d, int32_t f) {
@@ -174,16 +190,13 @@ moe_status_t moe_expert_int8_swiglu(const void* x, const float* x_scale, int32_t
   int sms = 0, smem = 0;
   if (device_sizes(sms, smem) != cudaSuccess) return MOE_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
-  uint8_t* base = reinterpret_cast<uint8_t*>(ws);
-  float* h = reinterpret_cast<float*>(base + at.h);
-  int8_t* q = reinterpret_cast<int8_t*>(base + at.q);
-  float* scale = reinterpret_cast<float*>(base + at.scale);
+  float* h = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + at.h);
   const size_t stack = (size_t)expert * f * d;
   LinearInt8Call c = {};
   c.M = n;
   c.N = ex.f;
   c.K = ex.d;
-  c.x16 = x16;
+  c.x_dtype = x_dtype;
   c.bf16 = dtype == MOE_BF16;
   c.act = MOE_ACT_SILU;
   c.out_f32 = 1;
@@ -194,16 +207,15 @@ moe_status_t moe_expert_int8_swiglu(const void* x, const float* x_scale, int32_t
   c.w_scale = ex.gate_scale + expert * f;
   c.w_mul_scale = ex.up_scale + expert * f;
   c.y = h;
-  cudaError_t e = launch_linear_int8(c, ws, sms, smem, st);
-  if (e == cudaSuccess) e = launch_quantize(h, MOE_F32, n, ex.f, q, scale, st);
+  const cudaError_t e = launch_linear_int8(c, ws, sms, smem, st);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   LinearInt8Call c2 = {};
   c2.M = n;
   c2.N = ex.d;
   c2.K = ex.f;
   c2.bf16 = dtype == MOE_BF16;
-  c2.x = q;
-  c2.x_scale = scale;
+  c2.x_dtype = MOE_F32;
+  c2.x = h;
   c2.w = ex.down_t + stack;
   c2.w_scale = ex.down_scale + expert * d;
   c2.residual = residual;

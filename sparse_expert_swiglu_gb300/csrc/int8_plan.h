@@ -1,0 +1,73 @@
+// The tile, stages and cluster of a product of 8-bit integers (linear_int8_tiles.cu), by its sizes alone.
+#pragma once
+
+#include "linear_plan.h"
+
+namespace sesg {
+
+constexpr int kI8Threads = 640;      // warps: 0 TMA, 1 products, 2 TMEM, 4-11 integers to fp16, 12-19 epilogue
+constexpr int kI8Chunk = 128;        // k of a stage: 128 bytes of a row of w, 256 of a token
+constexpr int kI8Round = 8;          // stages that one accumulator takes: 1024 products of at most 2^14 are exact in fp32
+constexpr int kI8Cols = 192;         // TMEM columns of one set of accumulators, at most; there are two
+constexpr int kI8MaxSlots = 8;       // of 32 TMEM columns: 64 k of 128 rows of w as fp16
+
+struct Int8Plan {
+  int P = 1;       // CTAs that run one product (cta_group::2 with 2)
+  int S = 0;       // shares of k: a cluster has P S CTAs
+  int NT = 0, MT = 0, T = 0;  // tokens of a tile, token tiles, tiles
+  int blocks = 0;  // blocks of 16 columns that an epilogue warp adds up: 1, 2, 4 or 6
+  int stages = 0, slots = 0;
+};
+
+inline int int8_stage_bytes(const Int8Plan& l, bool gated) { return (gated ? 2 : 1) * 128 * kI8Chunk + l.NT / l.P * kI8Chunk * 2; }
+// Bytes of a cluster's partial sums in one CTA: 8 warps' tokens, 128 bytes each.
+inline int int8_sum_bytes(const Int8Plan& l, bool gated) { return (gated ? 2 : 1) * ((l.NT + 31) / 32 * 16) * 8 * 128; }
+
+inline Int8Plan int8_plan(int M, int N, int K, bool gated, int sms, int room) {
+  const int mats = gated ? 2 : 1, KC = (K + kI8Chunk - 1) / kI8Chunk;
+  Int8Plan best;
+  double best_t = 1e300;
+  for (int P = 1; P <= 2; ++P) {
+    if (P == 2 && (M <= 96 || N <= 128)) continue;
+    const int most = kI8Cols / mats;
+    for (int NT = 32; NT <= most; NT += 32) {
+      Int8Plan l;
+      l.P = P;
+      l.MT = (M + NT - 1) / NT;
+      if (M <= 16 && P == 1) l.NT = 16;
+      else l.NT = ((M + l.MT - 1) / l.MT + 31) / 32 * 32;
+      const int FT = (N + 128 * P - 1) / (128 * P);
+      if ((long long)FT * l.MT > (1 << 30)) continue;
+      l.T = FT * l.MT;
+      const int tb = mats * ((l.NT + 31) / 32);
+      l.blocks = tb <= 1 ? 1 : tb <= 2 ? 2 : tb <= 4 ? 4 : 6;
+      const int free_slots = (512 - 2 * mats * l.NT) / 32;
+      l.slots = free_slots < kI8MaxSlots ? free_slots : kI8MaxSlots;
+      const int stage = int8_stage_bytes(l, gated);
+      l.stages = room / stage < kDnMaxStages ? room / stage : kDnMaxStages;
+      if (l.stages < 2) continue;
+      for (int S = 1; S * P <= 8; S *= 2) {
+        l.S = S;
+        const int fit = clusters(P * S, sms);
+        if (S > 1 && (l.T > fit || S > KC || int8_sum_bytes(l, gated) > l.stages * stage)) continue;
+        const double waves = (double)((l.T + fit - 1) / fit);
+        const double active = (double)(l.T < fit ? l.T : fit) * S * P;
+        const double load = mats * 16384.0 + l.NT / P * 256.0;
+        const double mem = mats * 16384.0 * active / 3550;  // weights out of HBM, all SMs
+        double stage_t = load / 62;
+        for (const double least : {mem / (l.MT < kTogether ? l.MT : kTogether), mats * 8 * 1.25 * l.NT / 2.0, mats * 260.0, 300.0 + l.NT})
+          if (stage_t < least) stage_t = least;
+        const double tile = ((KC + S - 1) / S) * stage_t;
+        double t = waves * (tile > 1500 + 9.0 * mats * l.NT ? tile : 1500 + 9.0 * mats * l.NT) + 2500 + 18.0 * mats * l.NT +
+                   (S > 1 ? 2500 + 24.0 * mats * l.NT : 0);
+        if (t < best_t) {
+          best_t = t;
+          best = l;
+        }
+      }
+    }
+  }
+  return best;
+}
+
+}  // namespace sesg

@@ -18,7 +18,8 @@ constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32;
 constexpr int kFewShared = 96 << 10;  // bytes of tokens
 
 struct Int8Args {
-  int M, N, K, x16, bf16, act, out_f32;
+  int M, N, K, bf16, act, out_f32;
+  int x_dtype;          // MOE_I8, MOE_F32, else 16 bits
   int parts;            // warps that share a row along k
   const void* x;
   const float* x_scale;
@@ -29,38 +30,40 @@ struct Int8Args {
 };
 
 __device__ __forceinline__ void store_one(const Int8Args& p, int tok, int row, int sum, int sum_mul, float xs) {
-  float v[1] = {(float)sum * (xs * p.w_scale[row])};
-  if (p.bias) v[0] += ld16(p.bias, row, p.bf16);
+  float v[1] = {int8_value(sum, xs, p.w_scale[row], p.bias ? ld16(p.bias, row, p.bf16) : 0.f)};
   activate(v, p.act);
-  if (p.w_mul) {
-    float m = (float)sum_mul * (xs * p.w_mul_scale[row]);
-    if (p.bias_mul) m += ld16(p.bias_mul, row, p.bf16);
-    v[0] *= m;
-  }
+  if (p.w_mul)
+    v[0] = __fmul_rn(v[0], int8_value(sum_mul, xs, p.w_mul_scale[row], p.bias_mul ? ld16(p.bias_mul, row, p.bf16) : 0.f));
   const size_t at = (size_t)tok * p.N + row;
-  if (p.residual) v[0] += ld16(p.residual, at, p.bf16);
+  if (p.residual) v[0] = __fadd_rn(v[0], ld16(p.residual, at, p.bf16));
   if (p.out_f32) reinterpret_cast<float*>(p.y)[at] = v[0];
   else reinterpret_cast<unsigned short*>(p.y)[at] = to16(v[0], p.bf16);
 }
 
-// The tokens t0 .. t0 + nt - 1 as integers in shared memory, and their scales.
-__device__ __forceinline__ void few_tokens(const Int8Args& p, int t0, int nt, int8_t* xq, float* scales, uint32_t* most) {
+// The nt tokens as integers in shared memory, and their scales.
+__device__ __forceinline__ void few_tokens(const Int8Args& p, int nt, int8_t* xq, float* scales, uint32_t* most) {
   const int tid = threadIdx.x;
-  if (!p.x16) {
-    const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const int8_t*>(p.x) + (size_t)t0 * p.K);
+  if (p.x_dtype == MOE_I8) {
+    const uint4* from = reinterpret_cast<const uint4*>(p.x);
     for (int i = tid; i < nt * (p.K / 16); i += kFewThreads) reinterpret_cast<uint4*>(xq)[i] = from[i];
-    if (tid < nt) scales[tid] = p.x_scale[t0 + tid];
+    if (tid < nt) scales[tid] = p.x_scale[tid];
     __syncthreads();
     return;
   }
   const int n = p.K / 8;
-  const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned short*>(p.x) + (size_t)t0 * p.K);
+  const bool f32 = p.x_dtype == MOE_F32;
+  const uint4* from = reinterpret_cast<const uint4*>(p.x);
   if (tid < nt) most[tid] = 0;
   __syncthreads();
   for (int t = 0; t < nt; ++t) {
     uint32_t m = 0;
-    for (int i = tid; i < n; i += kFewThreads) m = most16(m, from[(size_t)t * n + i]);
-    m = warp_most(most_f32(m, p.bf16));
+    if (f32) {
+      for (int i = tid; i < 2 * n; i += kFewThreads) m = most32(m, from[(size_t)t * 2 * n + i]);
+    } else {
+      for (int i = tid; i < n; i += kFewThreads) m = most16(m, from[(size_t)t * n + i]);
+      m = most_f32(m, p.bf16);
+    }
+    m = warp_most(m);
     if ((tid & 31) == 0) atomicMax(&most[t], m);
   }
   __syncthreads();
@@ -69,14 +72,15 @@ __device__ __forceinline__ void few_tokens(const Int8Args& p, int t0, int nt, in
     if (tid == 0) scales[t] = s.scale;
     for (int i = tid; i < n; i += kFewThreads) {
       float v[8];
-      unpack8(from[(size_t)t * n + i], p.bf16, v);
+      if (f32) unpack8(from[((size_t)t * n + i) * 2], from[((size_t)t * n + i) * 2 + 1], v);
+      else unpack8(from[(size_t)t * n + i], p.bf16, v);
       reinterpret_cast<uint2*>(xq)[t * n + i] = quantize8(v, s);
     }
   }
   __syncthreads();
 }
 
-// TOK tokens, of which blockIdx.y takes the next; RW rows of w for a warp at a time.
+// Up to TOK tokens; RW rows of w for a warp at a time.
 template <int TOK, int RW>
 __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const Int8Args p) {
   constexpr int U = 8 / RW;  // loads of a row in flight
@@ -118,12 +122,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const Int8Args
       for (int t = 0; t < TOK; ++t) acc[r][t] = 0;
   };
   clear();
-  for (long long first_tok = (long long)blockIdx.y * TOK; first_tok < p.M; first_tok += (long long)gridDim.y * TOK) {
-  const int t0 = (int)first_tok, nt = p.M - t0 < TOK ? p.M - t0 : TOK;
+  const int nt = p.M;
   At a = {first, 0, s0};
   if (a.g < groups) fetch(a, cur);
-  __syncthreads();
-  few_tokens(p, t0, nt, xq, scales, most);
+  few_tokens(p, nt, xq, scales, most);
   while (a.g < groups) {
     At b = {a.g, a.mat, a.s + U};
     if (b.s >= s1) {
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const Int8Args
         }
         ++round;
         const int row = a.g * RW + lane / TOK, tok = lane % TOK;
-        if (part == 0 && lane < RW * TOK && row < p.N && tok < nt) store_one(p, t0 + tok, row, sum, sum_mul, scales[tok]);
+        if (part == 0 && lane < RW * TOK && row < p.N && tok < nt) store_one(p, tok, row, sum, sum_mul, scales[tok]);
       }
     }
     a = b;
@@ -186,17 +188,32 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const Int8Args
 #pragma unroll
       for (int u = 0; u < U; ++u) cur[r][u] = next[r][u];
   }
-  }
 }
 
 }  // namespace
 
+Int8Ws::Int8Ws(int M, int K) {
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  tokens = up(linear_ws_bytes());
+  scales = tokens + up((size_t)M * K * 2);
+  bytes = scales + up((size_t)M * 4 + 60);
+}
+
 cudaError_t launch_linear_int8(const LinearInt8Call& c, void* ws, int sms, int smem_optin, cudaStream_t st) {
+  const int tok = c.M <= 1 ? 1 : c.M <= 2 ? 2 : c.M <= 4 ? 4 : 8;
+  if (c.M > tok || (c.M > 1 && tok * c.K > kFewShared) || c.tries) {
+    const Int8Ws at(c.M, c.K);
+    uint8_t* base = reinterpret_cast<uint8_t*>(ws);
+    float* scales = reinterpret_cast<float*>(base + at.scales);
+    cudaError_t e = launch_tokens(c.x, c.x_dtype, c.x_scale, c.M, c.K, base + at.tokens, scales, st);
+    if (e == cudaSuccess) e = launch_int8_tiles(c, base + at.tokens, scales, ws, sms, smem_optin, st);
+    return e;
+  }
   Int8Args p;
   p.M = c.M;
   p.N = c.N;
   p.K = c.K;
-  p.x16 = c.x16;
+  p.x_dtype = c.x_dtype;
   p.bf16 = c.bf16;
   p.act = c.act;
   p.out_f32 = c.out_f32;
@@ -210,8 +227,6 @@ cudaError_t launch_linear_int8(const LinearInt8Call& c, void* ws, int sms, int s
   p.bias_mul = c.bias_mul;
   p.residual = c.residual;
   p.y = c.y;
-  int tok = 1;
-  while (tok < 8 && tok < c.M && 2 * tok * c.K <= kFewShared) tok *= 2;
   const int rw = tok == 1 ? 1 : tok == 8 ? 4 : 2, groups = (c.N + rw - 1) / rw;
   const int segs = (c.K / 16 + 31) / 32;
   p.parts = 1;
@@ -221,10 +236,10 @@ cudaError_t launch_linear_int8(const LinearInt8Call& c, void* ws, int sms, int s
   const Kernel kernel = tok == 1 ? int8_few_kernel<1, 1> : tok == 2 ? int8_few_kernel<2, 2>
                         : tok == 4 ? int8_few_kernel<4, 2> : int8_few_kernel<8, 4>;
   static std::atomic<uint64_t> allowed[4];
-  cudaError_t e = allow_shared(kernel, allowed[tok == 1 ? 0 : tok == 2 ? 1 : tok == 4 ? 2 : 3], smem_optin - (16 << 10));
+  cudaError_t e = allow_shared(kernel, allowed[tok == 1 ? 0 : tok == 2 ? 1 : tok == 4 ? 2 : 3], kFewShared);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(groups < sms ? groups : sms, (c.M + tok - 1) / tok < 65535 ? (c.M + tok - 1) / tok : 65535);
+  cfg.gridDim = dim3(groups < sms ? groups : sms);
   cfg.blockDim = dim3(kFewThreads);
   cfg.dynamicSmemBytes = (size_t)tok * c.K;
   cfg.stream = st;

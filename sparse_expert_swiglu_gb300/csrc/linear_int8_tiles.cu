@@ -1,0 +1,633 @@
+// The products of linear_int8.cu for more than a few tokens, on the tensor cores.
+//
+// Sums are exact integers: the operands are integers of at most 8 bits, which fp16 holds, their products have at most 14
+// bits and 1024 of them less than 24, which an fp32 accumulator holds.  (This chip's tensor cores have next to no
+// rate for 8-bit integers: mma.sync takes as long as dp4a.)  So a tile's k goes in rounds of 1024; two sets of accumulators take
+// turns, and the epilogue's warps add the rounds up as 32-bit integers in registers under the next round's products.
+//
+// The features lie on the 128 TMEM lanes, the tokens on the columns.  w comes from HBM in 8 bits; eight warps turn 64 k of
+// 128 rows at a time into fp16 on the way from shared memory to TMEM, where the products read them as operand A: the
+// conversion costs shared memory one read of a byte a weight, and no second copy of w exists anywhere.  (In shared memory the
+// fp16 tile would be written and read again, 6 bytes a weight.)  The tokens, few beside w or used by many tiles, have been made
+// fp16 integers by the kernel before (quantize.cu).  w's copies start before that kernel is done.
+//
+// Where there are fewer tiles than SMs, a cluster's CTAs share a tile along k and join their sums in shared memory; with many
+// tokens CTA pairs run one product, so that each fetches half of the tokens.  int8_plan chooses.
+#include "activate.cuh"
+#include "dense.cuh"
+#include "dense_params.cuh"
+#include "int8.cuh"
+#include "int8_params.cuh"
+#include "int8_plan.h"
+
+namespace sesg {
+
+namespace {
+
+struct TileArgs {
+  int M, N, gated, bf16, act, out_f32;
+  int MT, NT, T, KC, S;
+  int stages, slots;
+  int stream;              // w is read once
+  const float* x_scale;    // with room for whole blocks of 16 tokens
+  const float *w_scale, *w_mul_scale;
+  const void *bias, *bias_mul, *residual;
+  void* y;
+  DenseHead* head;
+  uint32_t tries;          // rounds of a wait
+  int missing;             // diagnostics: the first CTA's stages wait for an arrival that does not come
+};
+
+struct TileBars {
+  DenseBars d;
+  uint64_t afull[kI8MaxSlots];   // a slot has its fp16 weights
+  uint64_t aempty[kI8MaxSlots];  // its products are done
+};
+
+// D += A B with A in TMEM, fp16 operands
+template <bool PAIR>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, uint32_t add) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(desc), "r"(add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(desc), "r"(add)
+        : "memory");
+}
+
+// 32 columns of this warp's 32 lanes
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ void peer_store(uint32_t to, const int* v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+
+__device__ __forceinline__ void tile_of(int t, int T, int MT, int& ft, int& mt) {
+  const int block = T / MT * kTogether, b = t / block, r = t - b * block;
+  const int here = MT - b * kTogether < kTogether ? MT - b * kTogether : kTogether;
+  ft = r / here;
+  mt = b * kTogether + r - ft * here;
+}
+
+// One feature's scales and biases.
+struct Feature {
+  float scale, scale_mul, bias, bias_mul;
+  __device__ Feature(const TileArgs& p, int feat, bool on) {
+    scale = on ? p.w_scale[feat] : 0.f;
+    scale_mul = on && p.gated ? p.w_mul_scale[feat] : 0.f;
+    bias = on && p.bias ? ld16(p.bias, feat, p.bf16) : 0.f;
+    bias_mul = on && p.bias_mul ? ld16(p.bias_mul, feat, p.bf16) : 0.f;
+  }
+};
+
+// Epilogue of W tokens (a multiple of 4) of one feature: s, and with w_mul m, are the sums; n tokens from tok exist.
+template <int W>
+__device__ __forceinline__ void tile_store(const TileArgs& p, int feat, int tok, int n, const Feature& f, const int* s,
+                                           const int* m) {
+  float v[W], xs[W];
+#pragma unroll
+  for (int i = 0; i < W; i += 4) {
+    const float4 t = *reinterpret_cast<const float4*>(p.x_scale + tok + i);
+    xs[i] = t.x;
+    xs[i + 1] = t.y;
+    xs[i + 2] = t.z;
+    xs[i + 3] = t.w;
+  }
+  const size_t at = (size_t)tok * p.N + feat;
+  unsigned short r[W];
+  if (p.residual) {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      r[i] = i < n ? reinterpret_cast<const unsigned short*>(p.residual)[at + (size_t)i * p.N] : (unsigned short)0;
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = int8_value(s[i], xs[i], f.scale, f.bias);
+  activate(v, p.act);
+  if (p.gated) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = __fmul_rn(v[i], int8_value(m[i], xs[i], f.scale_mul, f.bias_mul));
+  }
+  if (p.residual) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = __fadd_rn(v[i], from16(r[i], p.bf16));
+  }
+  if (p.out_f32) {
+    float* y = reinterpret_cast<float*>(p.y) + at;
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (i < n) y[(size_t)i * p.N] = v[i];
+  } else {
+    unsigned short* y = reinterpret_cast<unsigned short*>(p.y) + at;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const unsigned short t = to16(v[i], p.bf16);
+      if (i < n) y[(size_t)i * p.N] = t;
+    }
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// PAIR: CTA pairs, whose tile has 256 features, 128 in each CTA, which keeps half of the tokens.  SHARED: clusters share a
+// tile along k, one tile for each.  TB: blocks of 16 columns of an epilogue warp; with w_mul the second half is w_mul's.
+template <bool PAIR, bool SHARED, int TB>
+__global__ void __launch_bounds__(kI8Threads, 1)
+int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mw2,
+                 const __grid_constant__ CUtensorMap mx, const TileArgs p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  constexpr int P = PAIR ? 2 : 1;
+  constexpr uint32_t kW = 128 * kI8Chunk;  // bytes of a stage's rows of one matrix
+  const int mats = p.gated ? 2 : 1, NT = p.NT, toks = NT / P, ns = p.stages;
+  const uint32_t tok_bytes = toks * 128, stage_bytes = mats * kW + 2 * tok_bytes;
+  const int load_rows = p.N < 128 ? p.N : 128, load_toks = p.M < toks ? p.M : toks;  // boxes no higher than the operands
+  const uint32_t load_bytes = mats * load_rows * kI8Chunk + 2 * load_toks * 128;
+  TileBars* tb = reinterpret_cast<TileBars*>(ring + (size_t)ns * stage_bytes);
+  DenseBars* bars = &tb->d;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int S = SHARED ? p.S : 1;
+  const int crank = PAIR || SHARED ? (int)cluster_rank() : 0, half_of = PAIR ? crank & 1 : 0, lead = crank - half_of;
+  const int rank = SHARED ? crank / P : 0;
+  const int first = blockIdx.x / (P * S), step = gridDim.x / (P * S);
+  const int kc0 = p.KC * rank / S, kc1 = p.KC * (rank + 1) / S;
+  int* status = &p.head->ctrl.status;
+  const uint32_t ring_at = smem_addr(ring);
+  const int set_cols = mats * NT;  // columns of one set of accumulators
+
+  if (tid == 0) {
+    dn_init_bars(bars, p.tries, P * 8, 1 + (p.missing && blockIdx.x == 0));
+    for (int i = 0; i < kI8MaxSlots; ++i) {
+      mbar_init(&tb->afull[i], 4 * P);
+      mbar_init(&tb->aempty[i], 1);
+    }
+    mbar_init(&bars->xready, S);
+    mbar_init(&bars->xfull, 8);
+    fence_barrier_init();
+    tma_prefetch_map(&mw);
+    tma_prefetch_map(&mx);
+    if (p.gated) tma_prefetch_map(&mw2);
+  }
+  if (warp == 2) {
+    if (PAIR) tmem_alloc_pair(&bars->tmem, 512);
+    else tmem_alloc(&bars->tmem, 512);
+  }
+  tc_before_sync();
+  __syncthreads();
+  if (PAIR || SHARED) cluster_sync_all();  // the barriers are there before any CTA of the cluster uses them
+  tc_after_sync();
+  const uint32_t tmem = bars->tmem;
+  const uint32_t slots_at = tmem + 2 * set_cols;
+  // The kernel before is the tokens' (quantize.cu): it started its dependents behind its own wait, so that everything
+  // before it is done, and only what it writes, tokens and scales, has to be waited for.
+  griddep_launch_dependents();
+
+  if (warp < 4) {
+    if constexpr (TB >= 4) fewer_registers<40>();
+    if (warp == 0 && elect_one()) {
+      const uint64_t pw = p.stream ? policy_evict_first() : policy_evict_normal();
+      const uint64_t px = policy_evict_normal();
+      int st = 0, issued = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      auto weights = [&](int s, int kc, int ft) {
+        const int f0 = (ft * P + half_of) * 128;
+        mbar_arrive_expect_tx(&bars->full[s], load_bytes);
+        ++issued;
+        const uint32_t a = ring_at + s * stage_bytes;
+        tma_2d(a, &mw, kc * kI8Chunk, f0, &bars->full[s], pw);
+        if (p.gated) tma_2d(a + kW, &mw2, kc * kI8Chunk, f0, &bars->full[s], pw);
+      };
+      auto tokens = [&](int s, int kc, int mt) {
+        const int m0 = mt * NT + half_of * toks;
+        const uint32_t b = ring_at + s * stage_bytes + mats * kW;
+        tma_2d(b, &mx, kc * kI8Chunk, m0, &bars->full[s], px);
+        tma_2d(b + tok_bytes, &mx, kc * kI8Chunk + 64, m0, &bars->full[s], px);
+      };
+      int ahead = 0;  // stages of the first tile whose weights are under way before the tokens can be
+      if (first < p.T) {
+        int ft, mt;
+        tile_of(first, p.T, p.MT, ft, mt);
+        for (; ahead < ns && kc0 + ahead < kc1; ++ahead) weights(ahead, kc0 + ahead, ft);
+      }
+      griddep_wait();
+      for (int t = first; ok && t < p.T; t += step) {
+        int ft, mt;
+        tile_of(t, p.T, p.MT, ft, mt);
+        for (int kc = kc0; kc < kc1; ++kc) {
+          if (ahead > 0) {
+            --ahead;
+          } else {
+            if (!dn_wait(&bars->empty[st], ph ^ 1, bars)) {
+              dn_fail(bars, status);
+              ok = false;
+              break;
+            }
+            weights(st, kc, ft);
+          }
+          tokens(st, kc, mt);
+          if (++st == ns) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      // No copy of this CTA is in flight when it ends: the last stages have come.
+      const int n = issued < ns ? issued : ns;
+      for (int i = 0; i < n; ++i) {
+        if (--st < 0) {
+          st = ns - 1;
+          ph ^= 1;
+        }
+        dn_drain(&bars->full[st], ph, p.tries);
+      }
+    } else if (warp == 1 && crank == lead && elect_one()) {
+      const uint32_t desc = mma_desc(NT, 0, 0, P * 128);
+      auto commit = [&](uint64_t* bar) {
+        if constexpr (PAIR) mma_commit_pair(bar, lead);
+        else mma_commit(bar);
+      };
+      int st = 0, buf = 0, slot = 0;
+      uint32_t tph = 0, sph = 0;
+      bool ok = true, open = false;
+      for (int t = first; ok && t < p.T; t += step) {
+        for (int kr = kc0, end; ok && kr < kc1; kr = end) {
+          end = kr + kI8Round < kc1 ? kr + kI8Round : kc1;
+          if (!(PAIR ? cluster_wait(&bars->tempty[buf], tph ^ 1, bars) : dn_wait(&bars->tempty[buf], tph ^ 1, bars))) {
+            dn_fail(bars, status);
+            ok = false;
+            break;
+          }
+          tc_after_sync();
+          for (int kc = kr; ok && kc < end; ++kc) {
+            const uint32_t b = ring_at + st * stage_bytes + mats * kW;
+            for (int hk = 0; ok && hk < 2; ++hk) {
+              const uint64_t bd = smem_desc(b + hk * tok_bytes, 16);
+              for (int m = 0; m < mats; ++m) {
+                if (!(PAIR ? cluster_wait(&tb->afull[slot], sph, bars) : dn_wait(&tb->afull[slot], sph, bars))) {
+                  dn_fail(bars, status);
+                  ok = false;
+                  break;
+                }
+                tc_after_sync();
+                const uint32_t d = tmem + buf * set_cols + m * NT, a = slots_at + slot * 32;
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_ts<PAIR>(d, a + ks * 8, bd + ks * 2, desc, kc > kr || hk > 0 || ks > 0);
+                commit(&tb->aempty[slot]);
+                open = true;
+                if (++slot == p.slots) {
+                  slot = 0;
+                  sph ^= 1;
+                }
+              }
+            }
+            if (!ok) break;
+            commit(&bars->empty[st]);
+            if (++st == ns) st = 0;
+          }
+          if (!ok) break;
+          commit(&bars->tfull[buf]);
+          if (++buf == 2) {
+            buf = 0;
+            tph ^= 1;
+          }
+        }
+      }
+      if (open) {  // every product is done before TMEM is given back
+        commit(&bars->drain);
+        dn_drain(&bars->drain, 0, kWaitTries);
+      }
+    }
+  } else if (warp < 12) {
+    // 64 k of each stage, of the 32 rows whose TMEM lanes this warp may write
+    if constexpr (TB >= 4) fewer_registers<80>();
+    const int q = warp & 3, hk = (warp - 4) >> 2, row = q * 32 + lane;
+    const uint32_t lanes = slots_at + ((uint32_t)(q * 32) << 16);
+    int st = 0, slot = hk * mats;
+    uint32_t ph = 0, sph = 0;
+    bool ok = true;
+    for (int t = first; ok && t < p.T; t += step) {
+      for (int kc = kc0; ok && kc < kc1; ++kc) {
+        ok = dn_wait(&bars->full[st], ph, bars);
+        for (int m = 0; m < mats; ++m) {
+          int s = slot + m;
+          uint32_t sp = sph;
+          if (s >= p.slots) {
+            s -= p.slots;
+            sp ^= 1;
+          }
+          uint32_t v[32];
+          if (ok) {
+            const uint32_t from = ring_at + st * stage_bytes + m * kW + row * 128;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint4 w = ld_shared_v4(from + (((hk * 4 + c) ^ (row & 7)) << 4));
+              to_f16(w.x, v[8 * c], v[8 * c + 1]);
+              to_f16(w.y, v[8 * c + 2], v[8 * c + 3]);
+              to_f16(w.z, v[8 * c + 4], v[8 * c + 5]);
+              to_f16(w.w, v[8 * c + 6], v[8 * c + 7]);
+            }
+            ok = PAIR ? cluster_wait(&tb->aempty[s], sp ^ 1, bars) : dn_wait(&tb->aempty[s], sp ^ 1, bars);
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) {
+            if (lane == 0) dn_fail(bars, status);
+            break;
+          }
+          tc_after_sync();
+          tmem_st32(lanes + s * 32, v);
+          tmem_stored();
+          tc_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if (PAIR) peer_arrive(peer_addr(smem_addr(&tb->afull[s]), lead));
+            else mbar_arrive(&tb->afull[s]);
+          }
+        }
+        slot += 2 * mats;
+        if (slot >= p.slots) {
+          slot -= p.slots;
+          sph ^= 1;
+        }
+        if (++st == ns) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    }
+  } else {
+    // Lanes 32 (warp % 4) ... are this warp's.  Of the two warps that have them, each takes every other 16 tokens.
+    if constexpr (TB >= 4) more_registers<136>();
+    const int q = warp & 3, half = (warp - 12) >> 2, etid = tid - 384;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    int buf = 0;
+    uint32_t tph = 0;
+    griddep_wait();  // the tokens' scales
+    for (int t = first; t < p.T; t += step) {
+      const bool one = kc1 - kc0 <= kI8Round;  // one round: its sums stay where they are, in fp32
+      bool ok = true;
+      auto release = [&] {  // this set of accumulators has been read
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR) peer_arrive(peer_addr(smem_addr(&bars->tempty[buf]), lead));
+          else mbar_arrive(&bars->tempty[buf]);
+        }
+        if (++buf == 2) {
+          buf = 0;
+          tph ^= 1;
+        }
+      };
+      auto sums_there = [&] {
+        ok = dn_wait(&bars->tfull[buf], tph, bars);
+        if (!ok) dn_fail(bars, status);
+        ok = !dn_any(1, 256, !ok);  // one decision for the warps
+        tc_after_sync();
+        return ok;
+      };
+      if (one) {
+        if (!sums_there()) break;
+      } else {
+        // rounds are added up in registers; the last one's go back to TMEM as integers, to be read a few at a time
+        int acc[TB][16];
+#pragma unroll
+        for (int b = 0; b < TB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[b][i] = 0;
+        for (int kr = kc0; kr < kc1; kr += kI8Round) {
+          if (!sums_there()) break;
+          const bool last = kr + kI8Round >= kc1;
+#pragma unroll
+          for (int b = 0; b < TB; ++b) {
+            // block b: with w_mul the second half of the blocks is w_mul's
+            const int m = p.gated && TB > 1 && b >= TB / 2 ? 1 : 0, n0 = 32 * (b - m * (TB / 2)) + 16 * half;
+            if (n0 >= NT) continue;  // the same for the whole warp
+            const uint32_t at = lanes + buf * set_cols + m * NT + n0;
+            float v[16];
+            tmem_ld(at, v);
+            tmem_wait(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[b][i] += __float2int_rn(v[i]);
+            if (last) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = __int_as_float(acc[b][i]);
+              tmem_st(at, v);
+            }
+          }
+          if (last) tmem_stored();
+          else release();
+        }
+        if (!ok) break;
+      }
+      const uint32_t from_tmem = lanes + buf * set_cols;
+      auto sums = [&](int m, int n0, auto& s) {
+        constexpr int W = sizeof(s) / 4;
+        float v[W];
+        tmem_ld(from_tmem + m * NT + n0, v);
+        tmem_wait(v);
+#pragma unroll
+        for (int i = 0; i < W; ++i) s[i] = one ? __float2int_rn(v[i]) : __float_as_int(v[i]);
+      };
+      int ft, mt;
+      tile_of(t, p.T, p.MT, ft, mt);
+      const int m0 = mt * NT, nt = p.M - m0 < NT ? p.M - m0 : NT, f0 = (ft * P + half_of) * 128;
+      if constexpr (!SHARED) {
+        constexpr int W = TB == 1 || TB == 6 ? 4 : 8;  // tokens at a time
+        const int feat = f0 + q * 32 + lane;
+        const bool on = feat < p.N;
+        const Feature f(p, feat, on);
+        for (int n0 = 16 * half; n0 < nt; n0 += 32)
+#pragma unroll 1
+          for (int i = n0; i < nt && i < n0 + 16; i += W) {
+            int v[W], m[W];
+            sums(0, i, v);
+            if (p.gated) sums(1, i, m);
+            if (on) tile_store<W>(p, feat, m0 + i, nt - i, f, v, m);
+            __syncwarp();
+          }
+        release();
+      } else {
+        // Unit 2 q + half of the sums belongs to the share unit * S / 8's CTA with the same lanes, at [unit of the
+        // owner][rank][matrix][4 tokens][lane] in the stages, which are free once every CTA's products are done.
+        const int g4 = (NT + 31) / 32 * 4;  // groups of 4 tokens of a unit
+        const uint32_t unit_bytes = mats * g4 * 512;
+        const int per = 8 / S, unit = 2 * q + half;
+        if (etid == 0)
+          for (int i = 0; i < S; ++i) peer_arrive(peer_addr(smem_addr(&bars->xready), P * i + half_of));
+        ok = cluster_wait(&bars->xready, 0, bars);
+        if (!ok) dn_fail(bars, status);
+        if (dn_any(1, 256, !ok)) break;
+        const int owner = unit / per, peer = P * owner + half_of;
+        const uint32_t to = peer_addr(ring_at, peer) + ((unit - owner * per) * S + rank) * unit_bytes + lane * 16;
+        for (int n0 = 16 * half; n0 < nt; n0 += 32)
+#pragma unroll 1
+          for (int i = n0; i < nt && i < n0 + 16; i += 8)
+            for (int m = 0; m < mats; ++m) {
+              int v[8];
+              sums(m, i, v);
+              const uint32_t g = to + (m * g4 + (n0 >> 5) * 4 + ((i & 15) >> 2)) * 512;
+              peer_store(g, v);
+              if (i + 4 < nt) peer_store(g + 512, v + 4);
+            }
+        __syncwarp();
+        if (lane == 0) peer_arrive(peer_addr(smem_addr(&bars->xfull), peer));  // releases the warp's stores
+        ok = cluster_wait(&bars->xfull, 0, bars);
+        if (!ok) dn_fail(bars, status);
+        if (dn_any(1, 256, !ok)) break;
+        // S warps for each of this CTA's units, taking its groups of 4 tokens in turn
+        const int w = warp - 12, ul = w / S, u = rank * per + ul;
+        const int feat = f0 + (u >> 1) * 32 + lane;
+        const bool on = feat < p.N;
+        const Feature f(p, feat, on);
+        const uint8_t* from = ring + (size_t)ul * S * unit_bytes + lane * 16;
+        for (int g = w % S; g < g4; g += S) {
+          const int tok = 32 * (g >> 2) + 16 * (u & 1) + 4 * (g & 3);
+          if (tok >= nt) continue;
+          int a[4] = {0, 0, 0, 0}, m[4] = {0, 0, 0, 0};
+          for (int s = 0; s < S; ++s) {
+            const int4 x = *reinterpret_cast<const int4*>(from + s * unit_bytes + g * 512);
+            a[0] += x.x;
+            a[1] += x.y;
+            a[2] += x.z;
+            a[3] += x.w;
+            if (p.gated) {
+              const int4 z = *reinterpret_cast<const int4*>(from + s * unit_bytes + (g4 + g) * 512);
+              m[0] += z.x;
+              m[1] += z.y;
+              m[2] += z.z;
+              m[3] += z.w;
+            }
+          }
+          if (on) tile_store<4>(p, feat, m0 + tok, nt - tok, f, a, m);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_before_sync();
+  __syncthreads();
+  if (PAIR || SHARED) {
+    cluster_sync_all();  // no CTA leaves while another may store into it or read its stages
+    if (dn_aborted(bars)) dn_settle();  // stores that this CTA did not wait for
+  }
+  tc_after_sync();
+  if (warp == 2) {
+    if (PAIR) tmem_free_pair(tmem, 512);
+    else tmem_free(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_int8_tiles(const LinearInt8Call& c, const void* tokens, const float* scales, void* ws, int sms,
+                              int smem_optin, cudaStream_t st) {
+  const bool gated = c.w_mul != nullptr;
+  const int room = smem_optin - 1024 - (int)sizeof(TileBars);
+  const Int8Plan l = int8_plan(c.M, c.N, c.K, gated, sms, room);
+  if (!l.S) return cudaErrorInvalidValue;
+  CUtensorMap mw, mw2, mx;
+  const uint32_t rows = c.N < 128 ? c.N : 128, toks = c.M < l.NT / l.P ? c.M : l.NT / l.P;
+  cudaError_t e = int8_map(&mw, c.w, c.K, c.N, rows);
+  if (e != cudaSuccess) return e;
+  mw2 = mw;
+  if (gated) e = int8_map(&mw2, c.w_mul, c.K, c.N, rows);
+  if (e == cudaSuccess) e = dense_map(&mx, tokens, 0, c.K, c.M, c.K, 0, 0, toks);
+  if (e != cudaSuccess) return e;
+  TileArgs p;
+  p.M = c.M;
+  p.N = c.N;
+  p.gated = gated;
+  p.bf16 = c.bf16;
+  p.act = c.act;
+  p.out_f32 = c.out_f32;
+  p.MT = l.MT;
+  p.NT = l.NT;
+  p.T = l.T;
+  p.KC = (c.K + kI8Chunk - 1) / kI8Chunk;
+  p.S = l.S;
+  p.stages = l.stages;
+  p.slots = l.slots;
+  p.stream = l.MT == 1;
+  p.x_scale = scales;
+  p.w_scale = c.w_scale;
+  p.w_mul_scale = c.w_mul_scale;
+  p.bias = c.bias;
+  p.bias_mul = c.bias_mul;
+  p.residual = c.residual;
+  p.y = c.y;
+  p.head = reinterpret_cast<DenseHead*>(ws);
+  p.tries = c.tries ? c.tries : kWaitTries;
+  p.missing = c.tries > 0;
+  using Kernel = decltype(&int8_tile_kernel<false, false, 1>);
+  static constexpr Kernel kernels[16] = {
+      int8_tile_kernel<false, false, 1>, int8_tile_kernel<false, false, 2>, int8_tile_kernel<false, false, 4>,
+      int8_tile_kernel<false, false, 6>, int8_tile_kernel<false, true, 1>,  int8_tile_kernel<false, true, 2>,
+      int8_tile_kernel<false, true, 4>,  int8_tile_kernel<false, true, 6>,  int8_tile_kernel<true, false, 1>,
+      int8_tile_kernel<true, false, 2>,  int8_tile_kernel<true, false, 4>,  int8_tile_kernel<true, false, 6>,
+      int8_tile_kernel<true, true, 1>,   int8_tile_kernel<true, true, 2>,   int8_tile_kernel<true, true, 4>,
+      int8_tile_kernel<true, true, 6>};
+  static std::atomic<uint64_t> allowed[16];
+  const int which = (l.P - 1) * 8 + (l.S > 1) * 4 + (l.blocks == 1 ? 0 : l.blocks == 2 ? 1 : l.blocks == 4 ? 2 : 3);
+  e = allow_shared(kernels[which], allowed[which], smem_optin);
+  if (e != cudaSuccess) return e;
+  if (l.blocks >= 4) {
+    // the warps' shares of the registers that a block is launched with: more than those would wait forever
+    static std::atomic<int> regs[16];
+    int n = regs[which].load(std::memory_order_relaxed);
+    if (!n) {
+      cudaFuncAttributes attr;
+      e = cudaFuncGetAttributes(&attr, kernels[which]);
+      if (e != cudaSuccess) return e;
+      regs[which].store(n = attr.numRegs, std::memory_order_relaxed);
+    }
+    if (n * kI8Threads < 128 * 40 + 256 * 80 + 256 * 136) return cudaErrorInvalidConfiguration;
+  }
+  const int fit = sms / l.P;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(l.P * (l.S > 1 ? l.T * l.S : l.T < fit ? l.T : fit));
+  cfg.blockDim = dim3(kI8Threads);
+  cfg.dynamicSmemBytes = 1024 + (size_t)l.stages * int8_stage_bytes(l, gated) + sizeof(TileBars);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = l.P * l.S;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = l.P * l.S > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernels[which], mw, mw2, mx, p);
+}
+
+}  // namespace sesg

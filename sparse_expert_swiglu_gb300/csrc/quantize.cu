@@ -11,18 +11,26 @@ namespace {
 
 template <bool F32>
 __device__ __forceinline__ uint32_t most_of(uint32_t m, const uint4& v) {
-  if constexpr (F32)
-    return max(max(max(m, v.x & 0x7fffffffu), max(v.y & 0x7fffffffu, v.z & 0x7fffffffu)), v.w & 0x7fffffffu);
+  if constexpr (F32) return most32(m, v);
   else return most16(m, v);
 }
 
-// KEEP loads of 16 bytes are kept by a thread; F32: pairs of them (a thread's eight elements).
-template <bool F32, int KEEP>
-__global__ void __launch_bounds__(1024) quantize_kernel(const void* x, int bf16, int rows, int K, int8_t* q, float* scale) {
+// Eight 8-bit integers as fp16.
+__device__ __forceinline__ uint4 widen8(const uint2& q) {
+  uint4 r;
+  to_f16(q.x, r.x, r.y);
+  to_f16(q.y, r.z, r.w);
+  return r;
+}
+
+// KEEP loads of 16 bytes are kept by a thread; F32: pairs of them (a thread's eight elements).  WIDE: q as fp16 integers.
+template <bool F32, int KEEP, bool WIDE>
+__global__ void __launch_bounds__(1024) quantize_kernel(const void* x, int bf16, int rows, int K, void* q, float* scale) {
   constexpr int L = F32 ? 2 : 1;  // loads of eight elements
   __shared__ uint32_t part[32];
-  griddep_launch_dependents();
+  // In this order: the product behind the tokens' kernel takes everything before this kernel for done.
   griddep_wait();
+  griddep_launch_dependents();
   const int T = blockDim.x, tid = threadIdx.x, n = K / 8;
   const size_t row = (size_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= (size_t)rows) return;  // whole warps, and the only row of a CTA that has barriers
@@ -50,17 +58,13 @@ __global__ void __launch_bounds__(1024) quantize_kernel(const void* x, int bf16,
   }
   const RowScale s = row_scale(m);
   if (tid == 0) scale[row] = s.scale;
-  uint2* to = reinterpret_cast<uint2*>(q + row * K);
   auto eight = [&](const uint4* w, int i) {
     float t[8];
-    if constexpr (F32) {
-      const uint32_t b[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = __uint_as_float(b[e]);
-    } else {
-      unpack8(w[0], bf16, t);
-    }
-    to[i] = quantize8(t, s);
+    if constexpr (F32) unpack8(w[0], w[1], t);
+    else unpack8(w[0], bf16, t);
+    const uint2 b = quantize8(t, s);
+    if constexpr (WIDE) reinterpret_cast<uint4*>(q)[row * n + i] = widen8(b);
+    else reinterpret_cast<uint2*>(q)[row * n + i] = b;
   };
 #pragma unroll
   for (int j = 0; j < KEEP; ++j)
@@ -72,25 +76,53 @@ __global__ void __launch_bounds__(1024) quantize_kernel(const void* x, int bf16,
   }
 }
 
-}  // namespace
+// 8-bit tokens as fp16 integers, eight for each thread, and a copy of their scales.
+__global__ void widen_kernel(const uint2* x, const float* x_scale, int M, size_t n, uint4* tokens, float* scales) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < n) tokens[i] = widen8(x[i]);
+  if (i < (size_t)M) scales[i] = x_scale[i];
+}
 
-cudaError_t launch_quantize(const void* x, int dtype, int rows, int K, int8_t* q, float* scale, cudaStream_t st) {
-  const int n = K / 8;
-  int T = 32;
-  while (T < 1024 && T * 2 < n) T *= 2;
-  const int R = T == 32 ? 8 : 1;
+template <typename... Par, typename... Arg>
+cudaError_t launch(void (*kernel)(Par...), dim3 grid, dim3 block, cudaStream_t st, Arg... arg) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((size_t)rows + R - 1) / R));
-  cfg.blockDim = dim3(T, R);
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const auto kernel = dtype == MOE_F32 ? (n <= 2 * T ? quantize_kernel<true, 2> : quantize_kernel<true, 4>)
-                                       : (n <= 2 * T ? quantize_kernel<false, 2> : quantize_kernel<false, 8>);
-  return cudaLaunchKernelEx(&cfg, kernel, x, (int)(dtype == MOE_BF16), rows, K, q, scale);
+  return cudaLaunchKernelEx(&cfg, kernel, arg...);
+}
+
+template <bool WIDE>
+cudaError_t launch_rows(const void* x, int dtype, int rows, int K, void* q, float* scale, cudaStream_t st) {
+  const int n = K / 8;
+  int T = 32;
+  while (T < 1024 && T * 2 < n) T *= 2;
+  const int R = T == 32 ? 8 : 1;
+  const auto kernel = dtype == MOE_F32 ? (n <= 2 * T ? quantize_kernel<true, 2, WIDE> : quantize_kernel<true, 4, WIDE>)
+                                       : (n <= 2 * T ? quantize_kernel<false, 2, WIDE> : quantize_kernel<false, 8, WIDE>);
+  return launch(kernel, dim3((unsigned)(((size_t)rows + R - 1) / R)), dim3(T, R), st, x, (int)(dtype == MOE_BF16), rows, K, q,
+                scale);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize(const void* x, int dtype, int rows, int K, int8_t* q, float* scale, cudaStream_t st) {
+  return launch_rows<false>(x, dtype, rows, K, q, scale, st);
+}
+
+cudaError_t launch_tokens(const void* x, int dtype, const float* x_scale, int M, int K, void* tokens, float* scales,
+                          cudaStream_t st) {
+  if (dtype != MOE_I8) return launch_rows<true>(x, dtype, M, K, tokens, scales, st);
+  const size_t n = (size_t)M * K / 8;  // at least 2 M
+  return launch(widen_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), st, reinterpret_cast<const uint2*>(x), x_scale, M,
+                n, reinterpret_cast<uint4*>(tokens), scales);
 }
 
 }  // namespace sesg
