@@ -9,7 +9,7 @@ constexpr int kI8Threads = 640;      // warps: 0 TMA, 1 products, 2 TMEM, 4-11 i
 constexpr int kI8Chunk = 128;        // k of a stage: 128 bytes of a row of w, 256 of a token
 constexpr int kI8Round = 8;          // stages that one accumulator takes: 1024 products of at most 2^14 are exact in fp32
 constexpr int kI8Cols = 192;         // TMEM columns of one set of accumulators, at most; there are two
-constexpr int kI8MaxSlots = 8;       // of 32 TMEM columns: 64 k of 128 rows of w as fp16
+constexpr int kI8MaxSlots = 8;       // of 32 TMEM columns (with w_mul 64): 64 k of 128 rows of w as fp16
 
 struct Int8Plan {
   int P = 1;       // CTAs that run one product (cta_group::2 with 2)
@@ -40,8 +40,8 @@ inline Int8Plan int8_plan(int M, int N, int K, bool gated, int sms, int room) {
       if ((long long)FT * l.MT > (1 << 30)) continue;
       l.T = FT * l.MT;
       const int tb = mats * ((l.NT + 31) / 32);
-      l.blocks = tb <= 1 ? 1 : tb <= 2 ? 2 : tb <= 4 ? 4 : 6;
-      const int free_slots = (512 - 2 * mats * l.NT) / 32;
+      l.blocks = P == 1 && tb <= 2 ? tb : tb <= 4 ? 4 : 6;
+      const int free_slots = (512 - 2 * mats * l.NT) / (32 * mats);
       l.slots = free_slots < kI8MaxSlots ? free_slots : kI8MaxSlots;
       const int stage = int8_stage_bytes(l, gated);
       l.stages = room / stage < kDnMaxStages ? room / stage : kDnMaxStages;

@@ -105,7 +105,7 @@ struct Feature {
 };
 
 // Epilogue of W tokens (a multiple of 4) of one feature: s, and with w_mul m, are the sums; n tokens from tok exist.
-template <int W>
+template <int W, bool GATED>
 __device__ __forceinline__ void tile_store(const TileArgs& p, int feat, int tok, int n, const Feature& f, const int* s,
                                            const int* m) {
   float v[W], xs[W];
@@ -127,7 +127,7 @@ __device__ __forceinline__ void tile_store(const TileArgs& p, int feat, int tok,
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] = int8_value(s[i], xs[i], f.scale, f.bias);
   activate(v, p.act);
-  if (p.gated) {
+  if (GATED) {
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = __fmul_rn(v[i], int8_value(m[i], xs[i], f.scale_mul, f.bias_mul));
   }
@@ -150,6 +150,12 @@ __device__ __forceinline__ void tile_store(const TileArgs& p, int feat, int tok,
   }
 }
 
+// Arrives at a barrier of the pair.  What it orders lies in TMEM, behind tcgen05's own fences; the release over the cluster of
+// peer_arrive would wait 1200 clocks for the thread's other stores.
+__device__ __forceinline__ void pair_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -160,8 +166,9 @@ __device__ __forceinline__ void fewer_registers() {
 }
 
 // PAIR: CTA pairs, whose tile has 256 features, 128 in each CTA, which keeps half of the tokens.  SHARED: clusters share a
-// tile along k, one tile for each.  TB: blocks of 16 columns of an epilogue warp; with w_mul the second half is w_mul's.
-template <bool PAIR, bool SHARED, int TB>
+// tile along k, one tile for each.  GATED: with w_mul.  TB: blocks of 16 columns of an epilogue warp;
+// with w_mul the second half is w_mul's.
+template <bool PAIR, bool SHARED, bool GATED, int TB>
 __global__ void __launch_bounds__(kI8Threads, 1)
 int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mw2,
                  const __grid_constant__ CUtensorMap mx, const TileArgs p) {
@@ -169,7 +176,8 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   constexpr int P = PAIR ? 2 : 1;
   constexpr uint32_t kW = 128 * kI8Chunk;  // bytes of a stage's rows of one matrix
-  const int mats = p.gated ? 2 : 1, NT = p.NT, toks = NT / P, ns = p.stages;
+  constexpr int mats = GATED ? 2 : 1;
+  const int NT = p.NT, toks = NT / P, ns = p.stages;
   const uint32_t tok_bytes = toks * 128, stage_bytes = mats * kW + 2 * tok_bytes;
   const int load_rows = p.N < 128 ? p.N : 128, load_toks = p.M < toks ? p.M : toks;  // boxes no higher than the operands
   const uint32_t load_bytes = mats * load_rows * kI8Chunk + 2 * load_toks * 128;
@@ -196,7 +204,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
     fence_barrier_init();
     tma_prefetch_map(&mw);
     tma_prefetch_map(&mx);
-    if (p.gated) tma_prefetch_map(&mw2);
+    if (GATED) tma_prefetch_map(&mw2);
   }
   if (warp == 2) {
     if (PAIR) tmem_alloc_pair(&bars->tmem, 512);
@@ -212,9 +220,9 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
   // before it is done, and only what it writes, tokens and scales, has to be waited for.
   griddep_launch_dependents();
 
-  if (warp < 4) {
+  if (warp == 0) {
     if constexpr (TB >= 4) fewer_registers<40>();
-    if (warp == 0 && elect_one()) {
+    if (elect_one()) {
       const uint64_t pw = p.stream ? policy_evict_first() : policy_evict_normal();
       const uint64_t px = policy_evict_normal();
       int st = 0, issued = 0;
@@ -226,7 +234,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
         ++issued;
         const uint32_t a = ring_at + s * stage_bytes;
         tma_2d(a, &mw, kc * kI8Chunk, f0, &bars->full[s], pw);
-        if (p.gated) tma_2d(a + kW, &mw2, kc * kI8Chunk, f0, &bars->full[s], pw);
+        if (GATED) tma_2d(a + kW, &mw2, kc * kI8Chunk, f0, &bars->full[s], pw);
       };
       auto tokens = [&](int s, int kc, int mt) {
         const int m0 = mt * NT + half_of * toks;
@@ -271,7 +279,10 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
         }
         dn_drain(&bars->full[st], ph, p.tries);
       }
-    } else if (warp == 1 && crank == lead && elect_one()) {
+    }
+  } else if (warp == 1) {
+    if constexpr (TB >= 4) fewer_registers<40>();
+    if (crank == lead && elect_one()) {
       const uint32_t desc = mma_desc(NT, 0, 0, P * 128);
       auto commit = [&](uint64_t* bar) {
         if constexpr (PAIR) mma_commit_pair(bar, lead);
@@ -289,32 +300,36 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
             break;
           }
           tc_after_sync();
-          for (int kc = kr; ok && kc < end; ++kc) {
-            const uint32_t b = ring_at + st * stage_bytes + mats * kW;
-            for (int hk = 0; ok && hk < 2; ++hk) {
-              const uint64_t bd = smem_desc(b + hk * tok_bytes, 16);
-              for (int m = 0; m < mats; ++m) {
-                if (!(PAIR ? cluster_wait(&tb->afull[slot], sph, bars) : dn_wait(&tb->afull[slot], sph, bars))) {
-                  dn_fail(bars, status);
-                  ok = false;
-                  break;
-                }
-                tc_after_sync();
-                const uint32_t d = tmem + buf * set_cols + m * NT, a = slots_at + slot * 32;
+          const uint32_t d = tmem + buf * set_cols;
+          // (One way back for each stage: a jump costs the issuing thread some 200 to 400 clocks beside 19 other warps.)
+#pragma unroll 1
+          for (int kc = kr; kc < end; ++kc) {
+            const uint64_t bd = smem_desc(ring_at + st * stage_bytes + mats * kW, 16);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_ts<PAIR>(d, a + ks * 8, bd + ks * 2, desc, kc > kr || hk > 0 || ks > 0);
-                commit(&tb->aempty[slot]);
-                open = true;
-                if (++slot == p.slots) {
-                  slot = 0;
-                  sph ^= 1;
-                }
+            for (int hk = 0; hk < 2; ++hk) {
+              if (!(PAIR ? cluster_wait(&tb->afull[slot], sph, bars) : dn_wait(&tb->afull[slot], sph, bars))) {
+                ok = false;
+                break;
               }
+              tc_after_sync();
+              const uint32_t a = slots_at + slot * 32 * mats;
+#pragma unroll
+              for (int m = 0; m < mats; ++m)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                  mma_ts<PAIR>(d + m * NT, a + m * 32 + ks * 8, bd + (hk ? tok_bytes >> 4 : 0) + ks * 2, desc,
+                               hk > 0 || ks > 0 || kc > kr);
+              commit(&tb->aempty[slot]);
+              open = true;
+              const bool wrap = ++slot == p.slots;
+              slot = wrap ? 0 : slot;
+              sph ^= wrap;
             }
             if (!ok) break;
             commit(&bars->empty[st]);
-            if (++st == ns) st = 0;
+            st = st + 1 == ns ? 0 : st + 1;
           }
+          if (!ok) dn_fail(bars, status);
           if (!ok) break;
           commit(&bars->tfull[buf]);
           if (++buf == 2) {
@@ -328,61 +343,61 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
         dn_drain(&bars->drain, 0, kWaitTries);
       }
     }
+  } else if (warp < 4) {
+    if constexpr (TB >= 4) fewer_registers<40>();
   } else if (warp < 12) {
     // 64 k of each stage, of the 32 rows whose TMEM lanes this warp may write
     if constexpr (TB >= 4) fewer_registers<80>();
     const int q = warp & 3, hk = (warp - 4) >> 2, row = q * 32 + lane;
     const uint32_t lanes = slots_at + ((uint32_t)(q * 32) << 16);
-    int st = 0, slot = hk * mats;
+    int st = 0, slot = hk;
     uint32_t ph = 0, sph = 0;
     bool ok = true;
     for (int t = first; ok && t < p.T; t += step) {
-      for (int kc = kc0; ok && kc < kc1; ++kc) {
+#pragma unroll 1
+      for (int kc = kc0; kc < kc1; ++kc) {
         ok = dn_wait(&bars->full[st], ph, bars);
-        for (int m = 0; m < mats; ++m) {
-          int s = slot + m;
-          uint32_t sp = sph;
-          if (s >= p.slots) {
-            s -= p.slots;
-            sp ^= 1;
-          }
-          uint32_t v[32];
-          if (ok) {
-            const uint32_t from = ring_at + st * stage_bytes + m * kW + row * 128;
+        uint32_t v[32];
+        auto convert = [&](int m) {
+          const uint32_t from = ring_at + st * stage_bytes + m * kW + row * 128;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint4 w = ld_shared_v4(from + (((hk * 4 + c) ^ (row & 7)) << 4));
-              to_f16(w.x, v[8 * c], v[8 * c + 1]);
-              to_f16(w.y, v[8 * c + 2], v[8 * c + 3]);
-              to_f16(w.z, v[8 * c + 4], v[8 * c + 5]);
-              to_f16(w.w, v[8 * c + 6], v[8 * c + 7]);
-            }
-            ok = PAIR ? cluster_wait(&tb->aempty[s], sp ^ 1, bars) : dn_wait(&tb->aempty[s], sp ^ 1, bars);
+          for (int c = 0; c < 4; ++c) {
+            const uint4 w = ld_shared_v4(from + (((hk * 4 + c) ^ (row & 7)) << 4));
+            to_f16(w.x, v[8 * c], v[8 * c + 1]);
+            to_f16(w.y, v[8 * c + 2], v[8 * c + 3]);
+            to_f16(w.z, v[8 * c + 4], v[8 * c + 5]);
+            to_f16(w.w, v[8 * c + 6], v[8 * c + 7]);
           }
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) {
-            if (lane == 0) dn_fail(bars, status);
-            break;
-          }
-          tc_after_sync();
-          tmem_st32(lanes + s * 32, v);
-          tmem_stored();
-          tc_before_sync();
-          __syncwarp();
-          if (lane == 0) {
-            if (PAIR) peer_arrive(peer_addr(smem_addr(&tb->afull[s]), lead));
-            else mbar_arrive(&tb->afull[s]);
-          }
+        };
+        if (ok) {
+          convert(0);
+          ok = PAIR ? cluster_wait(&tb->aempty[slot], sph ^ 1, bars) : dn_wait(&tb->aempty[slot], sph ^ 1, bars);
         }
-        slot += 2 * mats;
-        if (slot >= p.slots) {
-          slot -= p.slots;
-          sph ^= 1;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (lane == 0) dn_fail(bars, status);
+          break;
         }
-        if (++st == ns) {
-          st = 0;
-          ph ^= 1;
+        tc_after_sync();
+        tmem_st32(lanes + slot * mats * 32, v);
+        if (GATED) {
+          convert(1);
+          tmem_st32(lanes + (slot * mats + 1) * 32, v);
         }
+        tmem_stored();
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR) pair_arrive(peer_addr(smem_addr(&tb->afull[slot]), lead));
+          else mbar_arrive(&tb->afull[slot]);
+        }
+        slot += 2;
+        const bool wrap = slot >= p.slots;
+        slot -= wrap ? p.slots : 0;
+        sph ^= wrap;
+        const bool turn = ++st == ns;
+        st = turn ? 0 : st;
+        ph ^= turn;
       }
     }
   } else {
@@ -400,7 +415,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
         tc_before_sync();
         __syncwarp();
         if (lane == 0) {
-          if (PAIR) peer_arrive(peer_addr(smem_addr(&bars->tempty[buf]), lead));
+          if (PAIR) pair_arrive(peer_addr(smem_addr(&bars->tempty[buf]), lead));
           else mbar_arrive(&bars->tempty[buf]);
         }
         if (++buf == 2) {
@@ -430,7 +445,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
 #pragma unroll
           for (int b = 0; b < TB; ++b) {
             // block b: with w_mul the second half of the blocks is w_mul's
-            const int m = p.gated && TB > 1 && b >= TB / 2 ? 1 : 0, n0 = 32 * (b - m * (TB / 2)) + 16 * half;
+            const int m = GATED && b >= TB / 2 ? 1 : 0, n0 = 32 * (b - m * (TB / 2)) + 16 * half;
             if (n0 >= NT) continue;  // the same for the whole warp
             const uint32_t at = lanes + buf * set_cols + m * NT + n0;
             float v[16];
@@ -471,8 +486,8 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
           for (int i = n0; i < nt && i < n0 + 16; i += W) {
             int v[W], m[W];
             sums(0, i, v);
-            if (p.gated) sums(1, i, m);
-            if (on) tile_store<W>(p, feat, m0 + i, nt - i, f, v, m);
+            if (GATED) sums(1, i, m);
+            if (on) tile_store<W, GATED>(p, feat, m0 + i, nt - i, f, v, m);
             __syncwarp();
           }
         release();
@@ -520,7 +535,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
             a[1] += x.y;
             a[2] += x.z;
             a[3] += x.w;
-            if (p.gated) {
+            if (GATED) {
               const int4 z = *reinterpret_cast<const int4*>(from + s * unit_bytes + (g4 + g) * 512);
               m[0] += z.x;
               m[1] += z.y;
@@ -528,7 +543,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
               m[3] += z.w;
             }
           }
-          if (on) tile_store<4>(p, feat, m0 + tok, nt - tok, f, a, m);
+          if (on) tile_store<4, GATED>(p, feat, m0 + tok, nt - tok, f, a, m);
         }
       }
     }
@@ -588,21 +603,23 @@ cudaError_t launch_int8_tiles(const LinearInt8Call& c, const void* tokens, const
   p.head = reinterpret_cast<DenseHead*>(ws);
   p.tries = c.tries ? c.tries : kWaitTries;
   p.missing = c.tries > 0;
-  using Kernel = decltype(&int8_tile_kernel<false, false, 1>);
-  static constexpr Kernel kernels[16] = {
-      int8_tile_kernel<false, false, 1>, int8_tile_kernel<false, false, 2>, int8_tile_kernel<false, false, 4>,
-      int8_tile_kernel<false, false, 6>, int8_tile_kernel<false, true, 1>,  int8_tile_kernel<false, true, 2>,
-      int8_tile_kernel<false, true, 4>,  int8_tile_kernel<false, true, 6>,  int8_tile_kernel<true, false, 1>,
-      int8_tile_kernel<true, false, 2>,  int8_tile_kernel<true, false, 4>,  int8_tile_kernel<true, false, 6>,
-      int8_tile_kernel<true, true, 1>,   int8_tile_kernel<true, true, 2>,   int8_tile_kernel<true, true, 4>,
-      int8_tile_kernel<true, true, 6>};
-  static std::atomic<uint64_t> allowed[16];
-  const int which = (l.P - 1) * 8 + (l.S > 1) * 4 + (l.blocks == 1 ? 0 : l.blocks == 2 ? 1 : l.blocks == 4 ? 2 : 3);
+  using Kernel = decltype(&int8_tile_kernel<false, false, false, 1>);
+  static constexpr Kernel kernels[32] = {
+      int8_tile_kernel<false, false, false, 1>, int8_tile_kernel<false, false, false, 2>, int8_tile_kernel<false, false, false, 4>, int8_tile_kernel<false, false, false, 6>,
+      nullptr, int8_tile_kernel<false, false, true, 2>, int8_tile_kernel<false, false, true, 4>, int8_tile_kernel<false, false, true, 6>,
+      int8_tile_kernel<false, true, false, 1>, int8_tile_kernel<false, true, false, 2>, int8_tile_kernel<false, true, false, 4>, int8_tile_kernel<false, true, false, 6>,
+      nullptr, int8_tile_kernel<false, true, true, 2>, int8_tile_kernel<false, true, true, 4>, int8_tile_kernel<false, true, true, 6>,
+      nullptr, nullptr, int8_tile_kernel<true, false, false, 4>, int8_tile_kernel<true, false, false, 6>,
+      nullptr, nullptr, int8_tile_kernel<true, false, true, 4>, int8_tile_kernel<true, false, true, 6>,
+      nullptr, nullptr, int8_tile_kernel<true, true, false, 4>, int8_tile_kernel<true, true, false, 6>,
+      nullptr, nullptr, int8_tile_kernel<true, true, true, 4>, int8_tile_kernel<true, true, true, 6>};
+  static std::atomic<uint64_t> allowed[32];
+  const int which = (l.P - 1) * 16 + (l.S > 1) * 8 + gated * 4 + (l.blocks == 1 ? 0 : l.blocks == 2 ? 1 : l.blocks == 4 ? 2 : 3);
   e = allow_shared(kernels[which], allowed[which], smem_optin);
   if (e != cudaSuccess) return e;
   if (l.blocks >= 4) {
     // the warps' shares of the registers that a block is launched with: more than those would wait forever
-    static std::atomic<int> regs[16];
+    static std::atomic<int> regs[32];
     int n = regs[which].load(std::memory_order_relaxed);
     if (!n) {
       cudaFuncAttributes attr;
