@@ -9,7 +9,8 @@ constexpr int kI8Threads = 640;      // warps: 0 TMA, 1 products, 2 TMEM, 4-11 i
 constexpr int kI8Chunk = 128;        // k of a stage: 128 bytes of a row of w, 256 of a token
 constexpr int kI8Round = 8;          // stages that one accumulator takes: 1024 products of at most 2^14 are exact in fp32
 constexpr int kI8Cols = 192;         // TMEM columns of one set of accumulators, at most; there are two
-constexpr int kI8MaxSlots = 8;       // of 32 TMEM columns (with w_mul 64): 64 k of 128 rows of w as fp16
+constexpr int kI8MaxSlots = 8;       // of 64 k (32 columns) with more than 128 tokens in a tile, else 128 k: rows of w as fp16
+constexpr int kI8Halves = 16384;     // bytes: what epilogue warps exchange with w_mul
 
 struct Int8Plan {
   int P = 1;       // CTAs that run one product (cta_group::2 with 2)
@@ -19,47 +20,45 @@ struct Int8Plan {
   int stages = 0, slots = 0;
 };
 
-inline int int8_stage_bytes(const Int8Plan& l, bool gated) { return (gated ? 2 : 1) * 128 * kI8Chunk + l.NT / l.P * kI8Chunk * 2; }
+inline int int8_stage_bytes(const Int8Plan& l) { return 128 * kI8Chunk + l.NT / l.P * kI8Chunk * 2; }
 // Bytes of a cluster's partial sums in one CTA: 8 warps' tokens, 128 bytes each.
-inline int int8_sum_bytes(const Int8Plan& l, bool gated) { return (gated ? 2 : 1) * ((l.NT + 31) / 32 * 16) * 8 * 128; }
+inline int int8_sum_bytes(const Int8Plan& l) { return (l.NT + 31) / 32 * 16 * 8 * 128; }
 
 inline Int8Plan int8_plan(int M, int N, int K, bool gated, int sms, int room) {
-  const int mats = gated ? 2 : 1, KC = (K + kI8Chunk - 1) / kI8Chunk;
+  const int feats = gated ? 64 : 128, KC = (K + kI8Chunk - 1) / kI8Chunk;
   Int8Plan best;
   double best_t = 1e300;
   for (int P = 1; P <= 2; ++P) {
-    if (P == 2 && (M <= 96 || N <= 128)) continue;
-    const int most = kI8Cols / mats;
-    for (int NT = 32; NT <= most; NT += 32) {
+    if (P == 2 && (M <= 96 || N <= feats)) continue;
+    for (int NT = 32; NT <= kI8Cols; NT += 32) {
       Int8Plan l;
       l.P = P;
       l.MT = (M + NT - 1) / NT;
       if (M <= 16 && P == 1) l.NT = 16;
       else l.NT = ((M + l.MT - 1) / l.MT + 31) / 32 * 32;
-      const int FT = (N + 128 * P - 1) / (128 * P);
+      const int FT = (N + feats * P - 1) / (feats * P);
       if ((long long)FT * l.MT > (1 << 30)) continue;
       l.T = FT * l.MT;
-      const int tb = mats * ((l.NT + 31) / 32);
+      const int tb = (l.NT + 31) / 32;
       l.blocks = P == 1 && tb <= 2 ? tb : tb <= 4 ? 4 : 6;
-      const int free_slots = (512 - 2 * mats * l.NT) / (32 * mats);
+      const int free_slots = (512 - 2 * l.NT) / (l.blocks == 6 ? 32 : 64);
       l.slots = free_slots < kI8MaxSlots ? free_slots : kI8MaxSlots;
-      const int stage = int8_stage_bytes(l, gated);
+      const int stage = int8_stage_bytes(l);
       l.stages = room / stage < kDnMaxStages ? room / stage : kDnMaxStages;
       if (l.stages < 2) continue;
       for (int S = 1; S * P <= 8; S *= 2) {
         l.S = S;
         const int fit = clusters(P * S, sms);
-        if (S > 1 && (l.T > fit || S > KC || int8_sum_bytes(l, gated) > l.stages * stage)) continue;
+        if (S > 1 && (l.T > fit || S > KC || int8_sum_bytes(l) > l.stages * stage)) continue;
         const double waves = (double)((l.T + fit - 1) / fit);
         const double active = (double)(l.T < fit ? l.T : fit) * S * P;
-        const double load = mats * 16384.0 + l.NT / P * 256.0;
-        const double mem = mats * 16384.0 * active / 3550;  // weights out of HBM, all SMs
+        const double load = 16384.0 + l.NT / P * 256.0;
+        const double mem = 16384.0 * active / 3550;  // weights out of HBM, all SMs
         double stage_t = load / 62;
-        for (const double least : {mem / (l.MT < kTogether ? l.MT : kTogether), mats * 8 * 1.25 * l.NT / 2.0, mats * 260.0, 300.0 + l.NT})
+        for (const double least : {mem / (l.MT < kTogether ? l.MT : kTogether), 8 * 1.25 * l.NT / 2.0, 600.0})
           if (stage_t < least) stage_t = least;
-        const double tile = ((KC + S - 1) / S) * stage_t;
-        double t = waves * (tile > 1500 + 9.0 * mats * l.NT ? tile : 1500 + 9.0 * mats * l.NT) + 2500 + 18.0 * mats * l.NT +
-                   (S > 1 ? 2500 + 24.0 * mats * l.NT : 0);
+        const double tile = ((KC + S - 1) / S) * stage_t, epi = 1500 + 60.0 * l.NT + 14.0 * l.NT * (((KC + S - 1) / S + 7) / 8);
+        double t = waves * (tile > epi ? tile : epi) + 2500 + 60.0 * l.NT + (S > 1 ? 2500 + 24.0 * l.NT : 0);
         if (t < best_t) {
           best_t = t;
           best = l;

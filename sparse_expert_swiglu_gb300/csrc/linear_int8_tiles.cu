@@ -5,7 +5,7 @@
 // rate for 8-bit integers: mma.sync takes as long as dp4a.)  So a tile's k goes in rounds of 1024; two sets of accumulators take
 // turns, and the epilogue's warps add the rounds up as 32-bit integers in registers under the next round's products.
 //
-// The features lie on the 128 TMEM lanes, the tokens on the columns.  w comes from HBM in 8 bits; eight warps turn 64 k of
+// The features lie on the 128 TMEM lanes (with w_mul 64 of each matrix), the tokens on the columns.  w comes from HBM in 8 bits; eight warps turn 64 k of
 // 128 rows at a time into fp16 on the way from shared memory to TMEM, where the products read them as operand A: the
 // conversion costs shared memory one read of a byte a weight, and no second copy of w exists anywhere.  (In shared memory the
 // fp16 tile would be written and read again, 6 bytes a weight.)  The tokens, few beside w or used by many tiles, have been made
@@ -93,22 +93,19 @@ __device__ __forceinline__ void tile_of(int t, int T, int MT, int& ft, int& mt) 
   mt = b * kTogether + r - ft * here;
 }
 
-// One feature's scales and biases.
+// One feature's scale and bias in one matrix.
 struct Feature {
-  float scale, scale_mul, bias, bias_mul;
-  __device__ Feature(const TileArgs& p, int feat, bool on) {
-    scale = on ? p.w_scale[feat] : 0.f;
-    scale_mul = on && p.gated ? p.w_mul_scale[feat] : 0.f;
-    bias = on && p.bias ? ld16(p.bias, feat, p.bf16) : 0.f;
-    bias_mul = on && p.bias_mul ? ld16(p.bias_mul, feat, p.bf16) : 0.f;
+  float scale, bias;
+  __device__ Feature(const TileArgs& p, bool mul, int feat, bool on) {
+    scale = on ? (mul ? p.w_mul_scale : p.w_scale)[feat] : 0.f;
+    const void* b = mul ? p.bias_mul : p.bias;
+    bias = on && b ? ld16(b, feat, p.bf16) : 0.f;
   }
 };
 
-// Epilogue of W tokens (a multiple of 4) of one feature: s, and with w_mul m, are the sums; n tokens from tok exist.
-template <int W, bool GATED>
-__device__ __forceinline__ void tile_store(const TileArgs& p, int feat, int tok, int n, const Feature& f, const int* s,
-                                           const int* m) {
-  float v[W], xs[W];
+// The scales of W tokens (a multiple of 4) from tok.
+template <int W>
+__device__ __forceinline__ void token_scales(const TileArgs& p, int tok, float (&xs)[W]) {
 #pragma unroll
   for (int i = 0; i < W; i += 4) {
     const float4 t = *reinterpret_cast<const float4*>(p.x_scale + tok + i);
@@ -117,24 +114,31 @@ __device__ __forceinline__ void tile_store(const TileArgs& p, int feat, int tok,
     xs[i + 2] = t.z;
     xs[i + 3] = t.w;
   }
-  const size_t at = (size_t)tok * p.N + feat;
-  unsigned short r[W];
-  if (p.residual) {
+}
+
+// The residual of W tokens from tok of one feature; n of them exist.
+template <int W>
+__device__ __forceinline__ void tile_residual(const TileArgs& p, int feat, int tok, int n, unsigned short (&r)[W]) {
+  if (!p.residual) return;
+  const unsigned short* from = reinterpret_cast<const unsigned short*>(p.residual) + (size_t)tok * p.N + feat;
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-      r[i] = i < n ? reinterpret_cast<const unsigned short*>(p.residual)[at + (size_t)i * p.N] : (unsigned short)0;
-  }
-#pragma unroll
-  for (int i = 0; i < W; ++i) v[i] = int8_value(s[i], xs[i], f.scale, f.bias);
+  for (int i = 0; i < W; ++i) r[i] = i < n ? from[(size_t)i * p.N] : (unsigned short)0;
+}
+
+// Activation, product with m (with w_mul), residual and store of W tokens from tok of one feature; n of them exist.
+template <int W, bool GATED>
+__device__ __forceinline__ void tile_store(const TileArgs& p, int feat, int tok, int n, float (&v)[W], const float* m,
+                                           const unsigned short (&r)[W]) {
   activate(v, p.act);
   if (GATED) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = __fmul_rn(v[i], int8_value(m[i], xs[i], f.scale_mul, f.bias_mul));
+    for (int i = 0; i < W; ++i) v[i] = __fmul_rn(v[i], m[i]);
   }
   if (p.residual) {
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = __fadd_rn(v[i], from16(r[i], p.bf16));
   }
+  const size_t at = (size_t)tok * p.N + feat;
   if (p.out_f32) {
     float* y = reinterpret_cast<float*>(p.y) + at;
 #pragma unroll
@@ -166,22 +170,22 @@ __device__ __forceinline__ void fewer_registers() {
 }
 
 // PAIR: CTA pairs, whose tile has 256 features, 128 in each CTA, which keeps half of the tokens.  SHARED: clusters share a
-// tile along k, one tile for each.  GATED: with w_mul.  TB: blocks of 16 columns of an epilogue warp;
-// with w_mul the second half is w_mul's.
-template <bool PAIR, bool SHARED, bool GATED, int TB>
+// tile along k, one tile for each.  GATED: with w_mul; 64 features of w, then the same ones of w_mul.  TB: blocks of 16 columns
+// that an epilogue warp adds up.  KS: 64 k in a slot.
+template <bool PAIR, bool SHARED, bool GATED, int TB, int KS>
 __global__ void __launch_bounds__(kI8Threads, 1)
 int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mw2,
                  const __grid_constant__ CUtensorMap mx, const TileArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  constexpr int P = PAIR ? 2 : 1;
-  constexpr uint32_t kW = 128 * kI8Chunk;  // bytes of a stage's rows of one matrix
-  constexpr int mats = GATED ? 2 : 1;
+  constexpr int P = PAIR ? 2 : 1, kFeats = GATED ? 64 : 128;
+  constexpr uint32_t kW = 128 * kI8Chunk;  // bytes of a stage's rows of w
   const int NT = p.NT, toks = NT / P, ns = p.stages;
-  const uint32_t tok_bytes = toks * 128, stage_bytes = mats * kW + 2 * tok_bytes;
-  const int load_rows = p.N < 128 ? p.N : 128, load_toks = p.M < toks ? p.M : toks;  // boxes no higher than the operands
-  const uint32_t load_bytes = mats * load_rows * kI8Chunk + 2 * load_toks * 128;
+  const uint32_t tok_bytes = toks * 128, stage_bytes = kW + 2 * tok_bytes;
+  const int load_rows = p.N < kFeats ? p.N : kFeats, load_toks = p.M < toks ? p.M : toks;  // boxes no higher than the operands
+  const uint32_t load_bytes = (GATED ? 2 : 1) * load_rows * kI8Chunk + 2 * load_toks * 128;
   TileBars* tb = reinterpret_cast<TileBars*>(ring + (size_t)ns * stage_bytes);
+  float* halves = reinterpret_cast<float*>(tb + 1);  // GATED: kI8Halves bytes that pairs of epilogue warps exchange
   DenseBars* bars = &tb->d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int S = SHARED ? p.S : 1;
@@ -189,9 +193,9 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
   const int rank = SHARED ? crank / P : 0;
   const int first = blockIdx.x / (P * S), step = gridDim.x / (P * S);
   const int kc0 = p.KC * rank / S, kc1 = p.KC * (rank + 1) / S;
+  const int tiles = first < p.T ? (p.T - first + step - 1) / step : 0;
   int* status = &p.head->ctrl.status;
   const uint32_t ring_at = smem_addr(ring);
-  const int set_cols = mats * NT;  // columns of one set of accumulators
 
   if (tid == 0) {
     dn_init_bars(bars, p.tries, P * 8, 1 + (p.missing && blockIdx.x == 0));
@@ -200,7 +204,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
       mbar_init(&tb->aempty[i], 1);
     }
     mbar_init(&bars->xready, S);
-    mbar_init(&bars->xfull, 8);
+    mbar_init(&bars->xfull, GATED && S == 8 ? 16 : 8);
     fence_barrier_init();
     tma_prefetch_map(&mw);
     tma_prefetch_map(&mx);
@@ -215,7 +219,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
   if (PAIR || SHARED) cluster_sync_all();  // the barriers are there before any CTA of the cluster uses them
   tc_after_sync();
   const uint32_t tmem = bars->tmem;
-  const uint32_t slots_at = tmem + 2 * set_cols;
+  const uint32_t slots_at = tmem + 2 * NT;
   // The kernel before is the tokens' (quantize.cu): it started its dependents behind its own wait, so that everything
   // before it is done, and only what it writes, tokens and scales, has to be waited for.
   griddep_launch_dependents();
@@ -229,16 +233,16 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
       uint32_t ph = 0;
       bool ok = true;
       auto weights = [&](int s, int kc, int ft) {
-        const int f0 = (ft * P + half_of) * 128;
+        const int f0 = (ft * P + half_of) * kFeats;
         mbar_arrive_expect_tx(&bars->full[s], load_bytes);
         ++issued;
         const uint32_t a = ring_at + s * stage_bytes;
         tma_2d(a, &mw, kc * kI8Chunk, f0, &bars->full[s], pw);
-        if (GATED) tma_2d(a + kW, &mw2, kc * kI8Chunk, f0, &bars->full[s], pw);
+        if (GATED) tma_2d(a + kW / 2, &mw2, kc * kI8Chunk, f0, &bars->full[s], pw);
       };
       auto tokens = [&](int s, int kc, int mt) {
         const int m0 = mt * NT + half_of * toks;
-        const uint32_t b = ring_at + s * stage_bytes + mats * kW;
+        const uint32_t b = ring_at + s * stage_bytes + kW;
         tma_2d(b, &mx, kc * kI8Chunk, m0, &bars->full[s], px);
         tma_2d(b + tok_bytes, &mx, kc * kI8Chunk + 64, m0, &bars->full[s], px);
       };
@@ -291,7 +295,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
       int st = 0, buf = 0, slot = 0;
       uint32_t tph = 0, sph = 0;
       bool ok = true, open = false;
-      for (int t = first; ok && t < p.T; t += step) {
+      for (int t = 0; ok && t < tiles; ++t) {
         for (int kr = kc0, end; ok && kr < kc1; kr = end) {
           end = kr + kI8Round < kc1 ? kr + kI8Round : kc1;
           if (!(PAIR ? cluster_wait(&bars->tempty[buf], tph ^ 1, bars) : dn_wait(&bars->tempty[buf], tph ^ 1, bars))) {
@@ -300,25 +304,23 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
             break;
           }
           tc_after_sync();
-          const uint32_t d = tmem + buf * set_cols;
+          const uint32_t d = tmem + buf * NT;
           // (One way back for each stage: a jump costs the issuing thread some 200 to 400 clocks beside 19 other warps.)
 #pragma unroll 1
           for (int kc = kr; kc < end; ++kc) {
-            const uint64_t bd = smem_desc(ring_at + st * stage_bytes + mats * kW, 16);
+            const uint64_t bd = smem_desc(ring_at + st * stage_bytes + kW, 16);
 #pragma unroll
-            for (int hk = 0; hk < 2; ++hk) {
+            for (int hk = 0; hk < 2; hk += KS) {
               if (!(PAIR ? cluster_wait(&tb->afull[slot], sph, bars) : dn_wait(&tb->afull[slot], sph, bars))) {
                 ok = false;
                 break;
               }
               tc_after_sync();
-              const uint32_t a = slots_at + slot * 32 * mats;
+              const uint32_t a = slots_at + slot * 32 * KS;
 #pragma unroll
-              for (int m = 0; m < mats; ++m)
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  mma_ts<PAIR>(d + m * NT, a + m * 32 + ks * 8, bd + (hk ? tok_bytes >> 4 : 0) + ks * 2, desc,
-                               hk > 0 || ks > 0 || kc > kr);
+              for (int ks = 0; ks < 4 * KS; ++ks)
+                mma_ts<PAIR>(d, a + ks * 8, bd + (hk || ks >= 4 ? tok_bytes >> 4 : 0) + (ks & 3) * 2, desc,
+                             hk > 0 || ks > 0 || kc > kr);
               commit(&tb->aempty[slot]);
               open = true;
               const bool wrap = ++slot == p.slots;
@@ -329,8 +331,10 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
             commit(&bars->empty[st]);
             st = st + 1 == ns ? 0 : st + 1;
           }
-          if (!ok) dn_fail(bars, status);
-          if (!ok) break;
+          if (!ok) {
+            dn_fail(bars, status);
+            break;
+          }
           commit(&bars->tfull[buf]);
           if (++buf == 2) {
             buf = 0;
@@ -346,20 +350,22 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
   } else if (warp < 4) {
     if constexpr (TB >= 4) fewer_registers<40>();
   } else if (warp < 12) {
-    // 64 k of each stage, of the 32 rows whose TMEM lanes this warp may write
+    // Every other stage, of the 32 rows whose TMEM lanes this warp may write.
     if constexpr (TB >= 4) fewer_registers<80>();
-    const int q = warp & 3, hk = (warp - 4) >> 2, row = q * 32 + lane;
+    const int q = warp & 3, set = (warp - 4) >> 2, row = q * 32 + lane;
     const uint32_t lanes = slots_at + ((uint32_t)(q * 32) << 16);
-    int st = 0, slot = hk;
+    const int total = tiles * (kc1 - kc0);
+    int st = set, slot = set * (2 / KS);
     uint32_t ph = 0, sph = 0;
     bool ok = true;
-    for (int t = first; ok && t < p.T; t += step) {
 #pragma unroll 1
-      for (int kc = kc0; kc < kc1; ++kc) {
-        ok = dn_wait(&bars->full[st], ph, bars);
+    for (int it = set; ok && it < total; it += 2) {
+      ok = dn_wait(&bars->full[st], ph, bars);
+      const uint32_t from = ring_at + st * stage_bytes + row * 128;
+#pragma unroll
+      for (int hk = 0; hk < 2; ++hk) {
         uint32_t v[32];
-        auto convert = [&](int m) {
-          const uint32_t from = ring_at + st * stage_bytes + m * kW + row * 128;
+        if (ok) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint4 w = ld_shared_v4(from + (((hk * 4 + c) ^ (row & 7)) << 4));
@@ -368,37 +374,37 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
             to_f16(w.z, v[8 * c + 4], v[8 * c + 5]);
             to_f16(w.w, v[8 * c + 6], v[8 * c + 7]);
           }
-        };
-        if (ok) {
-          convert(0);
-          ok = PAIR ? cluster_wait(&tb->aempty[slot], sph ^ 1, bars) : dn_wait(&tb->aempty[slot], sph ^ 1, bars);
+          if (hk == 0 || KS == 1)
+            ok = PAIR ? cluster_wait(&tb->aempty[slot], sph ^ 1, bars) : dn_wait(&tb->aempty[slot], sph ^ 1, bars);
         }
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          if (lane == 0) dn_fail(bars, status);
-          break;
-        }
+        if (!ok) break;
         tc_after_sync();
-        tmem_st32(lanes + slot * mats * 32, v);
-        if (GATED) {
-          convert(1);
-          tmem_st32(lanes + (slot * mats + 1) * 32, v);
+        tmem_st32(lanes + (slot * KS + (KS == 2 ? hk : 0)) * 32, v);
+        if (hk == 1 || KS == 1) {
+          tmem_stored();
+          tc_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if (PAIR) pair_arrive(peer_addr(smem_addr(&tb->afull[slot]), lead));
+            else mbar_arrive(&tb->afull[slot]);
+          }
         }
-        tmem_stored();
-        tc_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR) pair_arrive(peer_addr(smem_addr(&tb->afull[slot]), lead));
-          else mbar_arrive(&tb->afull[slot]);
+        if (KS == 1 && hk == 0) {
+          const bool wrap = ++slot == p.slots;
+          slot = wrap ? 0 : slot;
+          sph ^= wrap;
         }
-        slot += 2;
-        const bool wrap = slot >= p.slots;
-        slot -= wrap ? p.slots : 0;
-        sph ^= wrap;
-        const bool turn = ++st == ns;
-        st = turn ? 0 : st;
-        ph ^= turn;
       }
+      if (!ok && lane == 0) dn_fail(bars, status);
+      slot += KS == 1 ? 3 : 2;
+      const bool wrap = slot >= p.slots;
+      slot -= wrap ? p.slots : 0;
+      sph ^= wrap;
+      st += 2;
+      const bool turn = st >= ns;
+      st -= turn ? ns : 0;
+      ph ^= turn;
     }
   } else {
     // Lanes 32 (warp % 4) ... are this warp's.  Of the two warps that have them, each takes every other 16 tokens.
@@ -444,10 +450,9 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
           const bool last = kr + kI8Round >= kc1;
 #pragma unroll
           for (int b = 0; b < TB; ++b) {
-            // block b: with w_mul the second half of the blocks is w_mul's
-            const int m = GATED && b >= TB / 2 ? 1 : 0, n0 = 32 * (b - m * (TB / 2)) + 16 * half;
+            const int n0 = 32 * b + 16 * half;
             if (n0 >= NT) continue;  // the same for the whole warp
-            const uint32_t at = lanes + buf * set_cols + m * NT + n0;
+            const uint32_t at = lanes + buf * NT + n0;
             float v[16];
             tmem_ld(at, v);
             tmem_wait(v);
@@ -464,86 +469,138 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
         }
         if (!ok) break;
       }
-      const uint32_t from_tmem = lanes + buf * set_cols;
-      auto sums = [&](int m, int n0, auto& s) {
+      const uint32_t from_tmem = lanes + buf * NT;
+      auto sums = [&](int n0, auto& s) {
         constexpr int W = sizeof(s) / 4;
         float v[W];
-        tmem_ld(from_tmem + m * NT + n0, v);
+        tmem_ld(from_tmem + n0, v);
         tmem_wait(v);
 #pragma unroll
         for (int i = 0; i < W; ++i) s[i] = one ? __float2int_rn(v[i]) : __float_as_int(v[i]);
       };
       int ft, mt;
       tile_of(t, p.T, p.MT, ft, mt);
-      const int m0 = mt * NT, nt = p.M - m0 < NT ? p.M - m0 : NT, f0 = (ft * P + half_of) * 128;
-      if constexpr (!SHARED) {
-        constexpr int W = TB == 1 || TB == 6 ? 4 : 8;  // tokens at a time
+      const int m0 = mt * NT, nt = p.M - m0 < NT ? p.M - m0 : NT, f0 = (ft * P + half_of) * kFeats;
+      if constexpr (!SHARED && !GATED) {
+        constexpr int W = TB == 1 ? 4 : TB == 2 ? 8 : 16;  // tokens at a time
         const int feat = f0 + q * 32 + lane;
         const bool on = feat < p.N;
-        const Feature f(p, feat, on);
+        const Feature f(p, false, feat, on);
         for (int n0 = 16 * half; n0 < nt; n0 += 32)
 #pragma unroll 1
           for (int i = n0; i < nt && i < n0 + 16; i += W) {
-            int v[W], m[W];
-            sums(0, i, v);
-            if (GATED) sums(1, i, m);
-            if (on) tile_store<W, GATED>(p, feat, m0 + i, nt - i, f, v, m);
+            unsigned short r[W];
+            float xs[W], v[W];
+            int s[W];
+            if (on) tile_residual(p, feat, m0 + i, nt - i, r);
+            token_scales(p, m0 + i, xs);
+            sums(i, s);
+#pragma unroll
+            for (int j = 0; j < W; ++j) v[j] = int8_value(s[j], xs[j], f.scale, f.bias);
+            if (on) tile_store<W, false>(p, feat, m0 + i, nt - i, v, nullptr, r);
             __syncwarp();
           }
         release();
+      } else if constexpr (!SHARED) {
+        // Warps q and q + 2 have the two matrices' sums of the same features: of 16 tokens the first finishes eight and
+        // the second eight, and each gives the other what it lacks.
+        const int pair = (q & 1) * 2 + half, mul = q >> 1;
+        const int feat = f0 + (q & 1) * 32 + lane;
+        const bool on = feat < p.N;
+        const Feature f(p, mul, feat, on);
+        int turn = 0;
+#pragma unroll 1
+        for (int n0 = 16 * half; n0 < nt; n0 += 32) {
+          float xs[16];
+          unsigned short r[8];
+          int s[16];
+          const int tok = n0 + 8 * mul;  // the eight of this warp
+          if (on) tile_residual(p, feat, m0 + tok, nt - tok, r);
+          token_scales(p, m0 + n0, xs);
+          sums(n0, s);
+          float* give = halves + ((turn * 4 + pair) * 2 + mul) * 256 + lane;
+          const float* take = halves + ((turn * 4 + pair) * 2 + (mul ^ 1)) * 256 + lane;
+          float v[8], m[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float a = int8_value(s[j], xs[j], f.scale, f.bias), b = int8_value(s[8 + j], xs[8 + j], f.scale, f.bias);
+            v[j] = mul ? b : a;
+            give[32 * j] = mul ? a : b;
+          }
+          named_barrier(2 + pair, 64);  // (the next turn's writes go to the other buffer)
+          turn ^= 1;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m[j] = take[32 * j];
+          if (mul) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float a = m[j];
+              m[j] = v[j];
+              v[j] = a;
+            }
+          }
+          if (on) tile_store<8, true>(p, feat, m0 + tok, nt - tok, v, m, r);
+          __syncwarp();
+        }
+        release();
       } else {
-        // Unit 2 q + half of the sums belongs to the share unit * S / 8's CTA with the same lanes, at [unit of the
-        // owner][rank][matrix][4 tokens][lane] in the stages, which are free once every CTA's products are done.
-        const int g4 = (NT + 31) / 32 * 4;  // groups of 4 tokens of a unit
-        const uint32_t unit_bytes = mats * g4 * 512;
-        const int per = 8 / S, unit = 2 * q + half;
+        // The sums go to the CTAs that finish them, in the stages, which are free once every CTA's products are done: 4 tokens
+        // of a feature are 16 bytes at [rank][matrix][unit and group of 4 tokens, of the owner's][lane].  A unit is 16 of every
+        // 32 tokens of 32 features: 8 of them, or 4 with w_mul, for S CTAs; 8 CTAs take every other group of a unit of 4.
+        constexpr int kUnits = GATED ? 4 : 8;
+        const int g4 = (NT + 31) / 32 * 4;
+        const bool odd = S > kUnits;  // owners by groups
+        const int per = odd ? 1 : kUnits / S, cells = odd ? g4 / 2 : per * g4;
+        const int unit = GATED ? (q & 1) * 2 + half : 2 * q + half, mul = GATED ? q >> 1 : 0;
         if (etid == 0)
           for (int i = 0; i < S; ++i) peer_arrive(peer_addr(smem_addr(&bars->xready), P * i + half_of));
         ok = cluster_wait(&bars->xready, 0, bars);
         if (!ok) dn_fail(bars, status);
         if (dn_any(1, 256, !ok)) break;
-        const int owner = unit / per, peer = P * owner + half_of;
-        const uint32_t to = peer_addr(ring_at, peer) + ((unit - owner * per) * S + rank) * unit_bytes + lane * 16;
+        auto cta = [&](int g) { return P * (odd ? 2 * unit + (g & 1) : unit / per) + half_of; };
+        const uint32_t to = ring_at + (uint32_t)((rank * (GATED ? 2 : 1) + mul) * cells * 512) + lane * 16;
         for (int n0 = 16 * half; n0 < nt; n0 += 32)
 #pragma unroll 1
-          for (int i = n0; i < nt && i < n0 + 16; i += 8)
-            for (int m = 0; m < mats; ++m) {
-              int v[8];
-              sums(m, i, v);
-              const uint32_t g = to + (m * g4 + (n0 >> 5) * 4 + ((i & 15) >> 2)) * 512;
-              peer_store(g, v);
-              if (i + 4 < nt) peer_store(g + 512, v + 4);
+          for (int i = n0; i < nt && i < n0 + 16; i += 8) {
+            int v[8];
+            sums(i, v);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int g = (n0 >> 5) * 4 + ((i & 15) >> 2) + h, cell = odd ? g >> 1 : (unit % per) * g4 + g;
+              if (i + 4 * h < nt) peer_store(peer_addr(to + cell * 512, cta(g)), v + 4 * h);
             }
+          }
         __syncwarp();
-        if (lane == 0) peer_arrive(peer_addr(smem_addr(&bars->xfull), peer));  // releases the warp's stores
+        if (lane == 0)  // releases the warp's stores
+          for (int g = 0; g < (odd ? 2 : 1); ++g) peer_arrive(peer_addr(smem_addr(&bars->xfull), cta(g)));
         ok = cluster_wait(&bars->xfull, 0, bars);
         if (!ok) dn_fail(bars, status);
         if (dn_any(1, 256, !ok)) break;
-        // S warps for each of this CTA's units, taking its groups of 4 tokens in turn
-        const int w = warp - 12, ul = w / S, u = rank * per + ul;
-        const int feat = f0 + (u >> 1) * 32 + lane;
-        const bool on = feat < p.N;
-        const Feature f(p, feat, on);
-        const uint8_t* from = ring + (size_t)ul * S * unit_bytes + lane * 16;
-        for (int g = w % S; g < g4; g += S) {
-          const int tok = 32 * (g >> 2) + 16 * (u & 1) + 4 * (g & 3);
-          if (tok >= nt) continue;
-          int a[4] = {0, 0, 0, 0}, m[4] = {0, 0, 0, 0};
-          for (int s = 0; s < S; ++s) {
-            const int4 x = *reinterpret_cast<const int4*>(from + s * unit_bytes + g * 512);
-            a[0] += x.x;
-            a[1] += x.y;
-            a[2] += x.z;
-            a[3] += x.w;
-            if (GATED) {
-              const int4 z = *reinterpret_cast<const int4*>(from + s * unit_bytes + (g4 + g) * 512);
-              m[0] += z.x;
-              m[1] += z.y;
-              m[2] += z.z;
-              m[3] += z.w;
+        for (int cell = warp - 12; cell < cells; cell += 8) {
+          const int u = odd ? rank >> 1 : rank * per + cell / g4, g = odd ? 2 * cell + (rank & 1) : cell % g4;
+          const int feat = f0 + (u >> 1) * 32 + lane, tok = 32 * (g >> 2) + 16 * (u & 1) + 4 * (g & 3);
+          if (tok >= nt || feat >= p.N) continue;
+          float xs[4];
+          unsigned short r[4];
+          tile_residual(p, feat, m0 + tok, nt - tok, r);
+          token_scales(p, m0 + tok, xs);
+          float v[2][4];
+          const uint8_t* from = ring + (size_t)cell * 512 + lane * 16;
+#pragma unroll
+          for (int m = 0; m < (GATED ? 2 : 1); ++m) {
+            const Feature f(p, m, feat, true);
+            int a[4] = {0, 0, 0, 0};
+            for (int s = 0; s < S; ++s) {
+              const int4 x = *reinterpret_cast<const int4*>(from + (size_t)((s * (GATED ? 2 : 1) + m) * cells) * 512);
+              a[0] += x.x;
+              a[1] += x.y;
+              a[2] += x.z;
+              a[3] += x.w;
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[m][j] = int8_value(a[j], xs[j], f.scale, f.bias);
           }
-          if (on) tile_store<4, GATED>(p, feat, m0 + tok, nt - tok, f, a, m);
+          tile_store<4, GATED>(p, feat, m0 + tok, nt - tok, v[0], v[1], r);
         }
       }
     }
@@ -567,11 +624,11 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
 cudaError_t launch_int8_tiles(const LinearInt8Call& c, const void* tokens, const float* scales, void* ws, int sms,
                               int smem_optin, cudaStream_t st) {
   const bool gated = c.w_mul != nullptr;
-  const int room = smem_optin - 1024 - (int)sizeof(TileBars);
+  const int room = smem_optin - 1024 - (int)sizeof(TileBars) - (gated ? kI8Halves : 0);
   const Int8Plan l = int8_plan(c.M, c.N, c.K, gated, sms, room);
   if (!l.S) return cudaErrorInvalidValue;
   CUtensorMap mw, mw2, mx;
-  const uint32_t rows = c.N < 128 ? c.N : 128, toks = c.M < l.NT / l.P ? c.M : l.NT / l.P;
+  const uint32_t feats = gated ? 64 : 128, rows = c.N < (int)feats ? c.N : feats, toks = c.M < l.NT / l.P ? c.M : l.NT / l.P;
   cudaError_t e = int8_map(&mw, c.w, c.K, c.N, rows);
   if (e != cudaSuccess) return e;
   mw2 = mw;
@@ -603,16 +660,16 @@ cudaError_t launch_int8_tiles(const LinearInt8Call& c, const void* tokens, const
   p.head = reinterpret_cast<DenseHead*>(ws);
   p.tries = c.tries ? c.tries : kWaitTries;
   p.missing = c.tries > 0;
-  using Kernel = decltype(&int8_tile_kernel<false, false, false, 1>);
+  using Kernel = decltype(&int8_tile_kernel<false, false, false, 1, 2>);
   static constexpr Kernel kernels[32] = {
-      int8_tile_kernel<false, false, false, 1>, int8_tile_kernel<false, false, false, 2>, int8_tile_kernel<false, false, false, 4>, int8_tile_kernel<false, false, false, 6>,
-      nullptr, int8_tile_kernel<false, false, true, 2>, int8_tile_kernel<false, false, true, 4>, int8_tile_kernel<false, false, true, 6>,
-      int8_tile_kernel<false, true, false, 1>, int8_tile_kernel<false, true, false, 2>, int8_tile_kernel<false, true, false, 4>, int8_tile_kernel<false, true, false, 6>,
-      nullptr, int8_tile_kernel<false, true, true, 2>, int8_tile_kernel<false, true, true, 4>, int8_tile_kernel<false, true, true, 6>,
-      nullptr, nullptr, int8_tile_kernel<true, false, false, 4>, int8_tile_kernel<true, false, false, 6>,
-      nullptr, nullptr, int8_tile_kernel<true, false, true, 4>, int8_tile_kernel<true, false, true, 6>,
-      nullptr, nullptr, int8_tile_kernel<true, true, false, 4>, int8_tile_kernel<true, true, false, 6>,
-      nullptr, nullptr, int8_tile_kernel<true, true, true, 4>, int8_tile_kernel<true, true, true, 6>};
+      int8_tile_kernel<false, false, false, 1, 2>, int8_tile_kernel<false, false, false, 2, 2>, int8_tile_kernel<false, false, false, 4, 2>, int8_tile_kernel<false, false, false, 6, 1>,
+      int8_tile_kernel<false, false, true, 1, 2>, int8_tile_kernel<false, false, true, 2, 2>, int8_tile_kernel<false, false, true, 4, 2>, int8_tile_kernel<false, false, true, 6, 1>,
+      int8_tile_kernel<false, true, false, 1, 2>, int8_tile_kernel<false, true, false, 2, 2>, int8_tile_kernel<false, true, false, 4, 2>, int8_tile_kernel<false, true, false, 6, 1>,
+      int8_tile_kernel<false, true, true, 1, 2>, int8_tile_kernel<false, true, true, 2, 2>, int8_tile_kernel<false, true, true, 4, 2>, int8_tile_kernel<false, true, true, 6, 1>,
+      nullptr, nullptr, int8_tile_kernel<true, false, false, 4, 2>, int8_tile_kernel<true, false, false, 6, 1>,
+      nullptr, nullptr, int8_tile_kernel<true, false, true, 4, 2>, int8_tile_kernel<true, false, true, 6, 1>,
+      nullptr, nullptr, int8_tile_kernel<true, true, false, 4, 2>, int8_tile_kernel<true, true, false, 6, 1>,
+      nullptr, nullptr, int8_tile_kernel<true, true, true, 4, 2>, int8_tile_kernel<true, true, true, 6, 1>};
   static std::atomic<uint64_t> allowed[32];
   const int which = (l.P - 1) * 16 + (l.S > 1) * 8 + gated * 4 + (l.blocks == 1 ? 0 : l.blocks == 2 ? 1 : l.blocks == 4 ? 2 : 3);
   e = allow_shared(kernels[which], allowed[which], smem_optin);
@@ -633,7 +690,7 @@ cudaError_t launch_int8_tiles(const LinearInt8Call& c, const void* tokens, const
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(l.P * (l.S > 1 ? l.T * l.S : l.T < fit ? l.T : fit));
   cfg.blockDim = dim3(kI8Threads);
-  cfg.dynamicSmemBytes = 1024 + (size_t)l.stages * int8_stage_bytes(l, gated) + sizeof(TileBars);
+  cfg.dynamicSmemBytes = 1024 + (size_t)l.stages * int8_stage_bytes(l) + sizeof(TileBars) + (gated ? kI8Halves : 0);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
