@@ -15,15 +15,19 @@ constexpr int kI8Halves = 16384;     // bytes: what epilogue warps exchange with
 struct Int8Plan {
   int P = 1;       // CTAs that run one product (cta_group::2 with 2)
   int S = 0;       // shares of k: a cluster has P S CTAs
+  int rows = 0;    // features of a CTA's tile: up to 128, with w_mul 64
   int NT = 0, MT = 0, T = 0;  // tokens of a tile, token tiles, tiles
   int blocks = 0;  // blocks of 16 columns that an epilogue warp adds up: 1, 2, 4 or 6
   int stages = 0, slots = 0;
 };
 
+// Shared memory behind the stages and barriers: the tokens' scales, one array for each epilogue warp, and those halves.
+inline int int8_extra_bytes(bool gated) { return kI8Cols / 2 * 8 * 4 + (gated ? kI8Halves : 0); }
 inline int int8_stage_bytes(const Int8Plan& l) { return 128 * kI8Chunk + l.NT / l.P * kI8Chunk * 2; }
 // Bytes of a cluster's partial sums in one CTA: 8 warps' tokens, 128 bytes each.
 inline int int8_sum_bytes(const Int8Plan& l) { return (l.NT + 31) / 32 * 16 * 8 * 128; }
 
+// The tile and the cluster with the least time by a model in SM clocks.
 inline Int8Plan int8_plan(int M, int N, int K, bool gated, int sms, int room) {
   const int feats = gated ? 64 : 128, KC = (K + kI8Chunk - 1) / kI8Chunk;
   Int8Plan best;
@@ -36,9 +40,6 @@ inline Int8Plan int8_plan(int M, int N, int K, bool gated, int sms, int room) {
       l.MT = (M + NT - 1) / NT;
       if (M <= 16 && P == 1) l.NT = 16;
       else l.NT = ((M + l.MT - 1) / l.MT + 31) / 32 * 32;
-      const int FT = (N + feats * P - 1) / (feats * P);
-      if ((long long)FT * l.MT > (1 << 30)) continue;
-      l.T = FT * l.MT;
       const int tb = (l.NT + 31) / 32;
       l.blocks = P == 1 && tb <= 2 ? tb : tb <= 4 ? 4 : 6;
       const int free_slots = (512 - 2 * l.NT) / (l.blocks == 6 ? 32 : 64);
@@ -49,11 +50,18 @@ inline Int8Plan int8_plan(int M, int N, int K, bool gated, int sms, int room) {
       for (int S = 1; S * P <= 8; S *= 2) {
         l.S = S;
         const int fit = clusters(P * S, sms);
+        // Where w's bytes are the bound: as few features as fill the last wave (whole 32-byte sectors of a token's row).
+        const long long most = (long long)((N + feats * P - 1) / (feats * P)) * l.MT;
+        if (most > (1 << 30)) continue;
+        const long long waves = (most + fit - 1) / fit, ft = waves * fit / l.MT;
+        l.rows = l.MT > 1 ? feats : (int)((N + ft * P - 1) / (ft * P) + 15) / 16 * 16;
+        if (l.rows > feats) l.rows = feats;
+        l.T = (N + l.rows * P - 1) / (l.rows * P) * l.MT;
         if (S > 1 && (l.T > fit || S > KC || int8_sum_bytes(l) > l.stages * stage)) continue;
-        const double waves = (double)((l.T + fit - 1) / fit);
         const double active = (double)(l.T < fit ? l.T : fit) * S * P;
-        const double load = 16384.0 + l.NT / P * 256.0;
-        const double mem = 16384.0 * active / 3550;  // weights out of HBM, all SMs
+        const double bytes = (gated ? 2 : 1) * l.rows * 128.0;
+        const double load = bytes + l.NT / P * 256.0;
+        const double mem = bytes * active / 3550;  // weights out of HBM, all SMs
         double stage_t = load / 62;
         for (const double least : {mem / (l.MT < kTogether ? l.MT : kTogether), 8 * 1.25 * l.NT / 2.0, 600.0})
           if (stage_t < least) stage_t = least;

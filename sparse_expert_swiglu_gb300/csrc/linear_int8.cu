@@ -31,7 +31,7 @@ struct Int8Args {
 
 __device__ __forceinline__ void store_one(const Int8Args& p, int tok, int row, int sum, int sum_mul, float xs) {
   float v[1] = {int8_value(sum, xs, p.w_scale[row], p.bias ? ld16(p.bias, row, p.bf16) : 0.f)};
-  activate(v, p.act);
+  activate<1, true>(v, p.act);
   if (p.w_mul)
     v[0] = __fmul_rn(v[0], int8_value(sum_mul, xs, p.w_mul_scale[row], p.bias_mul ? ld16(p.bias_mul, row, p.bf16) : 0.f));
   const size_t at = (size_t)tok * p.N + row;

@@ -27,6 +27,7 @@ namespace {
 struct TileArgs {
   int M, N, gated, bf16, act, out_f32;
   int MT, NT, T, KC, S;
+  int rows;                // features of a CTA's tile: up to 128, with w_mul 64
   int stages, slots;
   int stream;              // w is read once
   const float* x_scale;    // with room for whole blocks of 16 tokens
@@ -38,11 +39,12 @@ struct TileArgs {
   int missing;             // diagnostics: the first CTA's stages wait for an arrival that does not come
 };
 
-struct TileBars {
+struct alignas(16) TileBars {
   DenseBars d;
   uint64_t afull[kI8MaxSlots];   // a slot has its fp16 weights
   uint64_t aempty[kI8MaxSlots];  // its products are done
 };
+static_assert(sizeof(TileBars) % 16 == 0, "what follows is read 16 bytes at a time");
 
 // D += A B with A in TMEM, fp16 operands
 template <bool PAIR>
@@ -96,6 +98,7 @@ __device__ __forceinline__ void tile_of(int t, int T, int MT, int& ft, int& mt) 
 // One feature's scale and bias in one matrix.
 struct Feature {
   float scale, bias;
+  __device__ Feature(float s, float b) : scale(s), bias(b) {}
   __device__ Feature(const TileArgs& p, bool mul, int feat, bool on) {
     scale = on ? (mul ? p.w_mul_scale : p.w_scale)[feat] : 0.f;
     const void* b = mul ? p.bias_mul : p.bias;
@@ -103,12 +106,12 @@ struct Feature {
   }
 };
 
-// The scales of W tokens (a multiple of 4) from tok.
+// The scales of W tokens (a multiple of 4).
 template <int W>
-__device__ __forceinline__ void token_scales(const TileArgs& p, int tok, float (&xs)[W]) {
+__device__ __forceinline__ void token_scales(const float* from, float (&xs)[W]) {
 #pragma unroll
   for (int i = 0; i < W; i += 4) {
-    const float4 t = *reinterpret_cast<const float4*>(p.x_scale + tok + i);
+    const float4 t = *reinterpret_cast<const float4*>(from + i);
     xs[i] = t.x;
     xs[i + 1] = t.y;
     xs[i + 2] = t.z;
@@ -129,7 +132,7 @@ __device__ __forceinline__ void tile_residual(const TileArgs& p, int feat, int t
 template <int W, bool GATED>
 __device__ __forceinline__ void tile_store(const TileArgs& p, int feat, int tok, int n, float (&v)[W], const float* m,
                                            const unsigned short (&r)[W]) {
-  activate(v, p.act);
+  activate<W, true>(v, p.act);
   if (GATED) {
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = __fmul_rn(v[i], m[i]);
@@ -178,14 +181,15 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
                  const __grid_constant__ CUtensorMap mx, const TileArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  constexpr int P = PAIR ? 2 : 1, kFeats = GATED ? 64 : 128;
+  constexpr int P = PAIR ? 2 : 1;
+  const int feats = p.rows;
   constexpr uint32_t kW = 128 * kI8Chunk;  // bytes of a stage's rows of w
   const int NT = p.NT, toks = NT / P, ns = p.stages;
   const uint32_t tok_bytes = toks * 128, stage_bytes = kW + 2 * tok_bytes;
-  const int load_rows = p.N < kFeats ? p.N : kFeats, load_toks = p.M < toks ? p.M : toks;  // boxes no higher than the operands
+  const int load_rows = p.N < feats ? p.N : feats, load_toks = p.M < toks ? p.M : toks;  // boxes no higher than the operands
   const uint32_t load_bytes = (GATED ? 2 : 1) * load_rows * kI8Chunk + 2 * load_toks * 128;
   TileBars* tb = reinterpret_cast<TileBars*>(ring + (size_t)ns * stage_bytes);
-  float* halves = reinterpret_cast<float*>(tb + 1);  // GATED: kI8Halves bytes that pairs of epilogue warps exchange
+  float* halves = reinterpret_cast<float*>(tb + 1) + kI8Cols / 2 * 8;  // GATED: what pairs of epilogue warps exchange
   DenseBars* bars = &tb->d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int S = SHARED ? p.S : 1;
@@ -233,7 +237,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
       uint32_t ph = 0;
       bool ok = true;
       auto weights = [&](int s, int kc, int ft) {
-        const int f0 = (ft * P + half_of) * kFeats;
+        const int f0 = (ft * P + half_of) * feats;
         mbar_arrive_expect_tx(&bars->full[s], load_bytes);
         ++issued;
         const uint32_t a = ring_at + s * stage_bytes;
@@ -306,7 +310,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
           tc_after_sync();
           const uint32_t d = tmem + buf * NT;
           // (One way back for each stage: a jump costs the issuing thread some 200 to 400 clocks beside 19 other warps.)
-#pragma unroll 1
+#pragma unroll 2
           for (int kc = kr; kc < end; ++kc) {
             const uint64_t bd = smem_desc(ring_at + st * stage_bytes + kW, 16);
 #pragma unroll
@@ -351,7 +355,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
     if constexpr (TB >= 4) fewer_registers<40>();
   } else if (warp < 12) {
     // Every other stage, of the 32 rows whose TMEM lanes this warp may write.
-    if constexpr (TB >= 4) fewer_registers<80>();
+    if constexpr (TB >= 4) fewer_registers<72>();
     const int q = warp & 3, set = (warp - 4) >> 2, row = q * 32 + lane;
     const uint32_t lanes = slots_at + ((uint32_t)(q * 32) << 16);
     const int total = tiles * (kc1 - kc0);
@@ -408,14 +412,29 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
     }
   } else {
     // Lanes 32 (warp % 4) ... are this warp's.  Of the two warps that have them, each takes every other 16 tokens.
-    if constexpr (TB >= 4) more_registers<136>();
+    if constexpr (TB >= 4) more_registers<144>();
     const int q = warp & 3, half = (warp - 12) >> 2, etid = tid - 384;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     int buf = 0;
     uint32_t tph = 0;
     griddep_wait();  // the tokens' scales
     for (int t = first; t < p.T; t += step) {
-      const bool one = kc1 - kc0 <= kI8Round;  // one round: its sums stay where they are, in fp32
+      int ft, mt;
+      tile_of(t, p.T, p.MT, ft, mt);
+      const int m0 = mt * NT, nt = p.M - m0 < NT ? p.M - m0 : NT, f0 = (ft * P + half_of) * feats;
+      // this lane's feature (of the one or the other matrix), and in shared memory this half's tokens' scales: both are under
+      // way while the sums are
+      const int mul = GATED ? q >> 1 : 0, local = (GATED ? q & 1 : q) * 32 + lane, feat = f0 + local;
+      const bool on = local < feats && feat < p.N;
+      float* scales = reinterpret_cast<float*>(tb + 1) + (warp - 12) * (kI8Cols / 2);
+      Feature f = {0.f, 0.f};
+      if (!SHARED) {
+        f = Feature(p, mul, feat, on);
+        __syncwarp();
+        for (int i = lane; 32 * (i >> 4) + 16 * half < nt; i += 32)
+          scales[i] = p.x_scale[m0 + 32 * (i >> 4) + 16 * half + (i & 15)];
+        __syncwarp();
+      }
       bool ok = true;
       auto release = [&] {  // this set of accumulators has been read
         tc_before_sync();
@@ -436,94 +455,65 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
         tc_after_sync();
         return ok;
       };
-      if (one) {
-        if (!sums_there()) break;
-      } else {
-        // rounds are added up in registers; the last one's go back to TMEM as integers, to be read a few at a time
-        int acc[TB][16];
+      // Rounds are added up in registers, which frees TMEM for the next tile's products before this one's epilogue.
+      int acc[TB][16];
 #pragma unroll
-        for (int b = 0; b < TB; ++b)
+      for (int b = 0; b < TB; ++b)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[b][i] = 0;
-        for (int kr = kc0; kr < kc1; kr += kI8Round) {
-          if (!sums_there()) break;
-          const bool last = kr + kI8Round >= kc1;
-#pragma unroll
-          for (int b = 0; b < TB; ++b) {
-            const int n0 = 32 * b + 16 * half;
-            if (n0 >= NT) continue;  // the same for the whole warp
-            const uint32_t at = lanes + buf * NT + n0;
-            float v[16];
-            tmem_ld(at, v);
-            tmem_wait(v);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[b][i] += __float2int_rn(v[i]);
-            if (last) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = __int_as_float(acc[b][i]);
-              tmem_st(at, v);
-            }
-          }
-          if (last) tmem_stored();
-          else release();
-        }
-        if (!ok) break;
-      }
-      const uint32_t from_tmem = lanes + buf * NT;
-      auto sums = [&](int n0, auto& s) {
-        constexpr int W = sizeof(s) / 4;
-        float v[W];
-        tmem_ld(from_tmem + n0, v);
-        tmem_wait(v);
-#pragma unroll
-        for (int i = 0; i < W; ++i) s[i] = one ? __float2int_rn(v[i]) : __float_as_int(v[i]);
-      };
-      int ft, mt;
-      tile_of(t, p.T, p.MT, ft, mt);
-      const int m0 = mt * NT, nt = p.M - m0 < NT ? p.M - m0 : NT, f0 = (ft * P + half_of) * kFeats;
-      if constexpr (!SHARED && !GATED) {
-        constexpr int W = TB == 1 ? 4 : TB == 2 ? 8 : 16;  // tokens at a time
-        const int feat = f0 + q * 32 + lane;
-        const bool on = feat < p.N;
-        const Feature f(p, false, feat, on);
-        for (int n0 = 16 * half; n0 < nt; n0 += 32)
+        for (int i = 0; i < 16; ++i) acc[b][i] = 0;
 #pragma unroll 1
-          for (int i = n0; i < nt && i < n0 + 16; i += W) {
-            unsigned short r[W];
-            float xs[W], v[W];
-            int s[W];
-            if (on) tile_residual(p, feat, m0 + i, nt - i, r);
-            token_scales(p, m0 + i, xs);
-            sums(i, s);
+      for (int kr = kc0; kr < kc1; kr += kI8Round) {
+        if (!sums_there()) break;
 #pragma unroll
-            for (int j = 0; j < W; ++j) v[j] = int8_value(s[j], xs[j], f.scale, f.bias);
-            if (on) tile_store<W, false>(p, feat, m0 + i, nt - i, v, nullptr, r);
-            __syncwarp();
-          }
+        for (int b = 0; b < TB; ++b) {
+          const int n0 = 32 * b + 16 * half;
+          if (n0 >= NT) continue;  // the same for the whole warp
+          float v[16];
+          tmem_ld(lanes + buf * NT + n0, v);
+          tmem_wait(v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[b][i] += __float2int_rn(v[i]);
+        }
         release();
+      }
+      if (!ok) break;
+      // the next block's sums to acc[0]: the epilogue's code is there once
+      auto turn_blocks = [&] {
+#pragma unroll
+        for (int b = 0; b + 1 < TB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[b][i] = acc[b + 1][i];
+      };
+      if constexpr (!SHARED && !GATED) {
+#pragma unroll 1
+        for (int n0 = 16 * half; n0 < nt; n0 += 32) {
+          unsigned short r[16];
+          float xs[16], v[16];
+          if (on) tile_residual(p, feat, m0 + n0, nt - n0, r);
+          token_scales(scales + (n0 >> 5) * 16, xs);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = int8_value(acc[0][j], xs[j], f.scale, f.bias);
+          if (on) tile_store<16, false>(p, feat, m0 + n0, nt - n0, v, nullptr, r);
+          turn_blocks();
+        }
       } else if constexpr (!SHARED) {
         // Warps q and q + 2 have the two matrices' sums of the same features: of 16 tokens the first finishes eight and
         // the second eight, and each gives the other what it lacks.
-        const int pair = (q & 1) * 2 + half, mul = q >> 1;
-        const int feat = f0 + (q & 1) * 32 + lane;
-        const bool on = feat < p.N;
-        const Feature f(p, mul, feat, on);
+        const int pair = (q & 1) * 2 + half;
         int turn = 0;
 #pragma unroll 1
         for (int n0 = 16 * half; n0 < nt; n0 += 32) {
           float xs[16];
           unsigned short r[8];
-          int s[16];
           const int tok = n0 + 8 * mul;  // the eight of this warp
           if (on) tile_residual(p, feat, m0 + tok, nt - tok, r);
-          token_scales(p, m0 + n0, xs);
-          sums(n0, s);
+          token_scales(scales + (n0 >> 5) * 16, xs);
           float* give = halves + ((turn * 4 + pair) * 2 + mul) * 256 + lane;
           const float* take = halves + ((turn * 4 + pair) * 2 + (mul ^ 1)) * 256 + lane;
           float v[8], m[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float a = int8_value(s[j], xs[j], f.scale, f.bias), b = int8_value(s[8 + j], xs[8 + j], f.scale, f.bias);
+            const float a = int8_value(acc[0][j], xs[j], f.scale, f.bias), b = int8_value(acc[0][8 + j], xs[8 + j], f.scale, f.bias);
             v[j] = mul ? b : a;
             give[32 * j] = mul ? a : b;
           }
@@ -540,9 +530,8 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
             }
           }
           if (on) tile_store<8, true>(p, feat, m0 + tok, nt - tok, v, m, r);
-          __syncwarp();
+          turn_blocks();
         }
-        release();
       } else {
         // The sums go to the CTAs that finish them, in the stages, which are free once every CTA's products are done: 4 tokens
         // of a feature are 16 bytes at [rank][matrix][unit and group of 4 tokens, of the owner's][lane].  A unit is 16 of every
@@ -551,7 +540,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
         const int g4 = (NT + 31) / 32 * 4;
         const bool odd = S > kUnits;  // owners by groups
         const int per = odd ? 1 : kUnits / S, cells = odd ? g4 / 2 : per * g4;
-        const int unit = GATED ? (q & 1) * 2 + half : 2 * q + half, mul = GATED ? q >> 1 : 0;
+        const int unit = GATED ? (q & 1) * 2 + half : 2 * q + half;
         if (etid == 0)
           for (int i = 0; i < S; ++i) peer_arrive(peer_addr(smem_addr(&bars->xready), P * i + half_of));
         ok = cluster_wait(&bars->xready, 0, bars);
@@ -559,17 +548,15 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
         if (dn_any(1, 256, !ok)) break;
         auto cta = [&](int g) { return P * (odd ? 2 * unit + (g & 1) : unit / per) + half_of; };
         const uint32_t to = ring_at + (uint32_t)((rank * (GATED ? 2 : 1) + mul) * cells * 512) + lane * 16;
-        for (int n0 = 16 * half; n0 < nt; n0 += 32)
 #pragma unroll 1
-          for (int i = n0; i < nt && i < n0 + 16; i += 8) {
-            int v[8];
-            sums(i, v);
+        for (int n0 = 16 * half; n0 < nt; n0 += 32) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int g = (n0 >> 5) * 4 + ((i & 15) >> 2) + h, cell = odd ? g >> 1 : (unit % per) * g4 + g;
-              if (i + 4 * h < nt) peer_store(peer_addr(to + cell * 512, cta(g)), v + 4 * h);
-            }
+          for (int h = 0; h < 4; ++h) {
+            const int g = (n0 >> 5) * 4 + h, cell = odd ? g >> 1 : (unit % per) * g4 + g;
+            if (n0 + 4 * h < nt) peer_store(peer_addr(to + cell * 512, cta(g)), &acc[0][4 * h]);
           }
+          turn_blocks();
+        }
         __syncwarp();
         if (lane == 0)  // releases the warp's stores
           for (int g = 0; g < (odd ? 2 : 1); ++g) peer_arrive(peer_addr(smem_addr(&bars->xfull), cta(g)));
@@ -578,17 +565,17 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
         if (dn_any(1, 256, !ok)) break;
         for (int cell = warp - 12; cell < cells; cell += 8) {
           const int u = odd ? rank >> 1 : rank * per + cell / g4, g = odd ? 2 * cell + (rank & 1) : cell % g4;
-          const int feat = f0 + (u >> 1) * 32 + lane, tok = 32 * (g >> 2) + 16 * (u & 1) + 4 * (g & 3);
-          if (tok >= nt || feat >= p.N) continue;
+          const int at = (u >> 1) * 32 + lane, feat = f0 + at, tok = 32 * (g >> 2) + 16 * (u & 1) + 4 * (g & 3);
+          if (tok >= nt || at >= feats || feat >= p.N) continue;
           float xs[4];
           unsigned short r[4];
           tile_residual(p, feat, m0 + tok, nt - tok, r);
-          token_scales(p, m0 + tok, xs);
+          token_scales(p.x_scale + m0 + tok, xs);
           float v[2][4];
           const uint8_t* from = ring + (size_t)cell * 512 + lane * 16;
 #pragma unroll
           for (int m = 0; m < (GATED ? 2 : 1); ++m) {
-            const Feature f(p, m, feat, true);
+            const Feature fm(p, m, feat, true);
             int a[4] = {0, 0, 0, 0};
             for (int s = 0; s < S; ++s) {
               const int4 x = *reinterpret_cast<const int4*>(from + (size_t)((s * (GATED ? 2 : 1) + m) * cells) * 512);
@@ -598,7 +585,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
               a[3] += x.w;
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[m][j] = int8_value(a[j], xs[j], f.scale, f.bias);
+            for (int j = 0; j < 4; ++j) v[m][j] = int8_value(a[j], xs[j], fm.scale, fm.bias);
           }
           tile_store<4, GATED>(p, feat, m0 + tok, nt - tok, v[0], v[1], r);
         }
@@ -624,11 +611,11 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
 cudaError_t launch_int8_tiles(const LinearInt8Call& c, const void* tokens, const float* scales, void* ws, int sms,
                               int smem_optin, cudaStream_t st) {
   const bool gated = c.w_mul != nullptr;
-  const int room = smem_optin - 1024 - (int)sizeof(TileBars) - (gated ? kI8Halves : 0);
+  const int room = smem_optin - 1024 - (int)sizeof(TileBars) - int8_extra_bytes(gated);
   const Int8Plan l = int8_plan(c.M, c.N, c.K, gated, sms, room);
   if (!l.S) return cudaErrorInvalidValue;
   CUtensorMap mw, mw2, mx;
-  const uint32_t feats = gated ? 64 : 128, rows = c.N < (int)feats ? c.N : feats, toks = c.M < l.NT / l.P ? c.M : l.NT / l.P;
+  const uint32_t rows = c.N < l.rows ? c.N : l.rows, toks = c.M < l.NT / l.P ? c.M : l.NT / l.P;
   cudaError_t e = int8_map(&mw, c.w, c.K, c.N, rows);
   if (e != cudaSuccess) return e;
   mw2 = mw;
@@ -647,6 +634,7 @@ cudaError_t launch_int8_tiles(const LinearInt8Call& c, const void* tokens, const
   p.T = l.T;
   p.KC = (c.K + kI8Chunk - 1) / kI8Chunk;
   p.S = l.S;
+  p.rows = l.rows;
   p.stages = l.stages;
   p.slots = l.slots;
   p.stream = l.MT == 1;
@@ -684,13 +672,13 @@ cudaError_t launch_int8_tiles(const LinearInt8Call& c, const void* tokens, const
       if (e != cudaSuccess) return e;
       regs[which].store(n = attr.numRegs, std::memory_order_relaxed);
     }
-    if (n * kI8Threads < 128 * 40 + 256 * 80 + 256 * 136) return cudaErrorInvalidConfiguration;
+    if (n * kI8Threads < 128 * 40 + 256 * 72 + 256 * 144) return cudaErrorInvalidConfiguration;
   }
   const int fit = sms / l.P;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(l.P * (l.S > 1 ? l.T * l.S : l.T < fit ? l.T : fit));
   cfg.blockDim = dim3(kI8Threads);
-  cfg.dynamicSmemBytes = 1024 + (size_t)l.stages * int8_stage_bytes(l) + sizeof(TileBars) + (gated ? kI8Halves : 0);
+  cfg.dynamicSmemBytes = 1024 + (size_t)l.stages * int8_stage_bytes(l) + sizeof(TileBars) + int8_extra_bytes(gated);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
