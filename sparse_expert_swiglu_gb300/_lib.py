@@ -896,24 +896,20 @@ def quantize_int8(x: torch.Tensor, out: Optional[torch.Tensor] = None, out_scale
     scale = max|x| / 127 and q = 127 x / max|x| rounded to the nearest, halves to even, for each row: tokens, or weights
     with one output a row.  A row of zeros has scale 0; one with an infinity or NaN has scale NaN and q = 0."""
     device = _current(x, "x")
-    code = _CODES.get(x.dtype, 3)
-    if code == 3:
-        raise TypeError(f"x must be torch.float16, torch.bfloat16 or torch.float32, got {x.dtype}")
-    if x.dim() < 1:
+    dt, shape = x.dtype, tuple(x.shape)
+    code = 1 if dt is torch.bfloat16 else 0 if dt is torch.float16 else 2
+    if code == 2 and dt is not torch.float32:
+        raise TypeError(f"x must be torch.float16, torch.bfloat16 or torch.float32, got {dt}")
+    if len(shape) == 2:
+        (rows, K), lead, strides, lead_strides = shape, shape[:1], (shape[1], 1), (1,)
+    elif not shape:
         raise ValueError("x must have at least one dimension")
-    rows, K = x.shape[:-1].numel(), x.shape[-1]
-    if out is None:
-        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
     else:
-        q = out
-        _dense_in(out, torch.int8, device, x.shape, "out")
-    if out_scale is None:
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    else:
-        scale = out_scale
-        _dense_in(out_scale, torch.float32, device, x.shape[:-1], "out_scale")
-    status = (_LIB or lib()).moe_quantize_int8(x.data_ptr(), code, rows, K, q.data_ptr(), scale.data_ptr(),
-                                               _stream_of(device))
+        lead, K, strides = shape[:-1], shape[-1], x.stride()
+        rows, lead_strides = x.shape[:-1].numel(), tuple(v // max(K, 1) for v in strides[:-1])
+    q, qp = _dense_out(out, shape, strides, torch.int8, device, "out")
+    scale, sp = _dense_out(out_scale, lead, lead_strides, torch.float32, device, "out_scale")
+    status = (_LIB or lib()).moe_quantize_int8(x.data_ptr(), code, rows, K, qp, sp, _stream_of(device))
     if status:
         raise MoeError("moe_quantize_int8", status)
     return q, scale
@@ -1066,56 +1062,61 @@ def residual_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, post
     y, or (q, scale), alone.  s has the residual's type.  residual_out, out, out_scale take s, y (q), scale; residual_out
     may be the residual's tensor, and either one x's.  Inference alone: gradients do not pass."""
     device = _dense_x(x)
-    dt = x.dtype
-    M, d = x.shape
-    kinds = _NORMS.get(post, -1), _NORMS.get(norm, -1)
-    if min(kinds) < 0:
+    dt, shape = x.dtype, tuple(x.shape)
+    M, d = shape
+    post_code, norm_code = _NORMS.get(post, -1), _NORMS.get(norm, -1)
+    if post_code < 0 or norm_code < 0:
         raise ValueError(f"post and norm must be one of {tuple(_NORMS)}, got {post!r} and {norm!r}")
-    if int8 and norm == "none":
-        raise ValueError("int8 goes with a norm")
-    if post == "none" and (post_weight is not None or post_bias is not None):
-        raise ValueError("post_weight and post_bias go with post")
-    if norm == "none" and (weight is not None or bias is not None or out is not None):
-        raise ValueError("weight, bias and out go with norm")
-    if out_scale is not None and not int8:
-        raise ValueError("out_scale goes with int8")
-    shape, vec = (M, d), (d,)
-    s_dt, rp = dt, 0
-    if residual is not None:
-        s_dt = torch.float32 if isinstance(residual, torch.Tensor) and residual.dtype is torch.float32 else dt
-        rp = _dense_in(residual, s_dt, device, shape, "residual")
-    gp, gate_rows = 0, 0
-    if gate is not None:
-        gate_rows = gate.shape[0] if isinstance(gate, torch.Tensor) and gate.dim() == 2 else 1
-        gp = _dense_in(gate, dt, device, (gate_rows, d) if isinstance(gate, torch.Tensor) and gate.dim() == 2 else vec, "gate")
-        if gate_rows < 1 or M % gate_rows:
-            raise ValueError(f"gate has {gate_rows} rows, which do not divide {M} tokens")
-
-    def vector(t, name):
-        return 0 if t is None else _dense_in(t, dt, device, vec, name)
-    vectors = (vector(post_weight, "post_weight"), vector(post_bias, "post_bias"), vector(weight, "weight"),
-               vector(bias, "bias"))
+    code = s_code = 1 if dt is torch.bfloat16 else 0
+    s_dt = dt
+    vec, strides = (d,), (d, 1)
+    rp = gp = pw = pb = wp = bp = sp = yp = scp = gate_rows = 0
     s = y = scale = None
-    sp = yp = scp = 0
-    if residual is not None or norm == "none":
-        s, sp = _dense_out(residual_out, shape, (d, 1), s_dt, device, "residual_out")
-    elif residual_out is not None:
+    if post_code:
+        if post_weight is not None:
+            pw = _dense_in(post_weight, dt, device, vec, "post_weight")
+        if post_bias is not None:
+            pb = _dense_in(post_bias, dt, device, vec, "post_bias")
+    elif post_weight is not None or post_bias is not None:
+        raise ValueError("post_weight and post_bias go with post")
+    if gate is not None:
+        if isinstance(gate, torch.Tensor) and gate.dim() == 2:
+            gate_rows = gate.shape[0]
+            gp = _dense_in(gate, dt, device, (gate_rows, d), "gate")
+            if gate_rows < 1 or M % gate_rows:
+                raise ValueError(f"gate has {gate_rows} rows, which do not divide {M} tokens")
+        else:
+            gate_rows, gp = 1, _dense_in(gate, dt, device, vec, "gate")
+    if residual is not None:
+        if isinstance(residual, torch.Tensor) and residual.dtype is torch.float32:
+            s_dt, s_code = torch.float32, 2
+        rp = _dense_in(residual, s_dt, device, shape, "residual")
+    elif residual_out is not None and norm_code:
         raise ValueError("residual_out goes with residual or norm 'none'")
-    y_dt = torch.int8 if int8 else dt
-    if norm != "none":
-        y, yp = _dense_out(out, shape, (d, 1), y_dt, device, "out")
+    if residual is not None or not norm_code:
+        s, sp = _dense_out(residual_out, shape, strides, s_dt, device, "residual_out")
+    if norm_code:
+        if weight is not None:
+            wp = _dense_in(weight, dt, device, vec, "weight")
+        if bias is not None:
+            bp = _dense_in(bias, dt, device, vec, "bias")
+        y, yp = _dense_out(out, shape, strides, torch.int8 if int8 else dt, device, "out")
+    elif int8 or weight is not None or bias is not None or out is not None:
+        raise ValueError("weight, bias, out and int8 go with norm")
     if int8:
         scale, scp = _dense_out(out_scale, (M,), (1,), torch.float32, device, "out_scale")
+    elif out_scale is not None:
+        raise ValueError("out_scale goes with int8")
     if M:
-        op = _RESIDUAL_NORM(M, d, _CODES[dt], _CODES[s_dt], _CODES[y_dt], kinds[0], kinds[1], gate_rows, residual_scale,
-                            block_scale, eps, x.data_ptr(), rp, gp, *vectors, sp, yp, scp)
+        op = _RESIDUAL_NORM(M, d, code, s_code, 3 if int8 else code, post_code, norm_code, gate_rows, residual_scale,
+                            block_scale, eps, x.data_ptr(), rp, gp, pw, pb, wp, bp, sp, yp, scp)
         status = (_LIB or lib()).moe_residual_norm(op, _stream_of(device))
         if status:
             raise MoeError("moe_residual_norm", status)
-    if norm == "none":
-        return s
     if s is None:
         return (y, scale) if int8 else y
+    if y is None:
+        return s
     return (s, y, scale) if int8 else (s, y)
 
 

@@ -15,7 +15,7 @@ namespace sesg {
 namespace {
 
 constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32;
-constexpr int kFewShared = 96 << 10;  // bytes of tokens
+constexpr int kFewShared = 200 << 10;  // bytes of tokens
 
 struct Int8Args {
   int M, N, K, bf16, act, out_f32;
@@ -83,7 +83,7 @@ __device__ __forceinline__ void few_tokens(const Int8Args& p, int nt, int8_t* xq
 // Up to TOK tokens; RW rows of w for a warp at a time.
 template <int TOK, int RW>
 __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const Int8Args p) {
-  constexpr int U = 8 / RW;  // loads of a row in flight
+  constexpr int U = (TOK == 16 ? 4 : 8) / RW;  // loads of a row in flight
   extern __shared__ __align__(16) int8_t xq[];
   __shared__ float scales[TOK];
   __shared__ uint32_t most[TOK];
@@ -199,9 +199,18 @@ Int8Ws::Int8Ws(int M, int K) {
   bytes = scales + up((size_t)M * 4 + 60);
 }
 
+// Whether the stream of w takes the call, and not the tensor cores.  The stream is a single short kernel (512 x 512: 3.4 us
+// for 5 tokens and 4.5 for 16 against 6.3) whose time grows with the tokens: at 8 tokens they meet at 56 MB of weights (4096 x
+// 14336: 18.4 us both; 32000 x 4096: 36.4 us against 27.2), at 9 to 16 sooner (16 of 2048 x 1408: 6.0 us against 9.3, 16 of 4096 x
+// 4096: 13.0 against 12.2, 9 of them: 10.6 against 12.0).
+static bool int8_few(int M, int N, int K, bool gated, int tok) {
+  const double work = (gated ? 2.0 : 1.0) * N * K * M;
+  return M == 1 || (M <= tok && tok * K <= kFewShared && (M <= 4 || work <= (M <= 8 ? 450e6 : 160e6)));
+}
+
 cudaError_t launch_linear_int8(const LinearInt8Call& c, void* ws, int sms, int smem_optin, cudaStream_t st) {
-  const int tok = c.M <= 1 ? 1 : c.M <= 2 ? 2 : c.M <= 4 ? 4 : 8;
-  if (c.M > tok || (c.M > 1 && tok * c.K > kFewShared) || c.tries) {
+  const int tok = c.M <= 1 ? 1 : c.M <= 2 ? 2 : c.M <= 4 ? 4 : c.M <= 8 ? 8 : 16;
+  if (!int8_few(c.M, c.N, c.K, c.w_mul != nullptr, tok) || c.tries) {
     const Int8Ws at(c.M, c.K);
     uint8_t* base = reinterpret_cast<uint8_t*>(ws);
     float* scales = reinterpret_cast<float*>(base + at.scales);
@@ -234,9 +243,9 @@ cudaError_t launch_linear_int8(const LinearInt8Call& c, void* ws, int sms, int s
     p.parts *= 2;
   using Kernel = void (*)(Int8Args);
   const Kernel kernel = tok == 1 ? int8_few_kernel<1, 1> : tok == 2 ? int8_few_kernel<2, 2>
-                        : tok == 4 ? int8_few_kernel<4, 2> : int8_few_kernel<8, 4>;
-  static std::atomic<uint64_t> allowed[4];
-  cudaError_t e = allow_shared(kernel, allowed[tok == 1 ? 0 : tok == 2 ? 1 : tok == 4 ? 2 : 3], kFewShared);
+                        : tok == 4 ? int8_few_kernel<4, 2> : tok == 8 ? int8_few_kernel<8, 4> : int8_few_kernel<16, 2>;
+  static std::atomic<uint64_t> allowed[5];
+  cudaError_t e = allow_shared(kernel, allowed[tok == 1 ? 0 : tok == 2 ? 1 : tok == 4 ? 2 : tok == 8 ? 3 : 4], kFewShared);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(groups < sms ? groups : sms);

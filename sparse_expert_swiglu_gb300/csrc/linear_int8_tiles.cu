@@ -20,6 +20,8 @@
 #include "int8_params.cuh"
 #include "int8_plan.h"
 
+#include <type_traits>
+
 namespace sesg {
 
 namespace {
@@ -477,25 +479,27 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
         release();
       }
       if (!ok) break;
-      // the next block's sums to acc[0]: the epilogue's code is there once
-      auto turn_blocks = [&] {
+      // the next sums to acc[0]: the epilogue's code is there once
+      auto turn_blocks = [&](auto by) {
+        constexpr int W = decltype(by)::value;
 #pragma unroll
-        for (int b = 0; b + 1 < TB; ++b)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[b][i] = acc[b + 1][i];
+        for (int i = 0; i + W < TB * 16; ++i) acc[i / 16][i % 16] = acc[(i + W) / 16][(i + W) % 16];
       };
       if constexpr (!SHARED && !GATED) {
+        // W tokens at a time: a short call pays for every line of code that it fetches
+        constexpr int W = TB <= 2 ? 4 : 16;
+        for (int n0 = 16 * half; n0 < nt; n0 += 32)
 #pragma unroll 1
-        for (int n0 = 16 * half; n0 < nt; n0 += 32) {
-          unsigned short r[16];
-          float xs[16], v[16];
-          if (on) tile_residual(p, feat, m0 + n0, nt - n0, r);
-          token_scales(scales + (n0 >> 5) * 16, xs);
+          for (int i = n0; i < n0 + 16; i += W) {
+            unsigned short r[W];
+            float xs[W], v[W];
+            if (on) tile_residual(p, feat, m0 + i, nt - i, r);
+            token_scales(scales + (n0 >> 5) * 16 + (i & 15), xs);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = int8_value(acc[0][j], xs[j], f.scale, f.bias);
-          if (on) tile_store<16, false>(p, feat, m0 + n0, nt - n0, v, nullptr, r);
-          turn_blocks();
-        }
+            for (int j = 0; j < W; ++j) v[j] = int8_value(acc[0][j], xs[j], f.scale, f.bias);
+            if (on) tile_store<W, false>(p, feat, m0 + i, nt - i, v, nullptr, r);
+            turn_blocks(std::integral_constant<int, W>());
+          }
       } else if constexpr (!SHARED) {
         // Warps q and q + 2 have the two matrices' sums of the same features: of 16 tokens the first finishes eight and
         // the second eight, and each gives the other what it lacks.
@@ -530,7 +534,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
             }
           }
           if (on) tile_store<8, true>(p, feat, m0 + tok, nt - tok, v, m, r);
-          turn_blocks();
+          turn_blocks(std::integral_constant<int, 16>());
         }
       } else {
         // The sums go to the CTAs that finish them, in the stages, which are free once every CTA's products are done: 4 tokens
@@ -555,7 +559,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
             const int g = (n0 >> 5) * 4 + h, cell = odd ? g >> 1 : (unit % per) * g4 + g;
             if (n0 + 4 * h < nt) peer_store(peer_addr(to + cell * 512, cta(g)), &acc[0][4 * h]);
           }
-          turn_blocks();
+          turn_blocks(std::integral_constant<int, 16>());
         }
         __syncwarp();
         if (lane == 0)  // releases the warp's stores
