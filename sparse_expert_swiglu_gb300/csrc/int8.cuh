@@ -7,56 +7,78 @@
 namespace sesg {
 
 // What the elements of a row share.  m is found as the largest bit pattern of |x|: infinities and NaN come out on top.
+//
+// A row of 16-bit values takes no more than a product for each element.  With x and m integers X, Y below 2^11 times powers of
+// two, a quotient that is no half is at least 1 / (2 Y) >= 2^-12 away from one, and 127 x / m is a half only where 127 divides
+// 2 k + 1, at 63.5, which goes to the even 64, or Y.  So step, 127 / m or up to 2^-23 of it above, rounds every quotient
+// right (127 * 2^-23 < 2^-12, and 63.5 is never passed from below), but for Y = 127 j: those rows are decided exactly.
 struct RowScale {
-  float step;    // 127 / m: x * step is within 2e-5 of the quotient
-  float limit;   // quotients nearer than 0.5 - limit to a half are decided exactly; -1: all of them
-  float pre, a;  // 2^-e, and m 2^-e, which is below 2 (1 <= ... unless m is subnormal)
-  float scale;   // m / 127
+  float step;    // 127 / m; of an fp32 row to 2^-21
+  float limit;   // of an fp32 row quotients nearer than 0.5 - limit to a half are decided exactly; -1: every element of the row
+  float pre, a;  // 2^-e, and m 2^-e: from 1 up to 2, less where m is subnormal
+  float inv;     // 127 / a to 2^-21
+  float most;    // m
   int ok;        // finite
+  // m / 127, correctly rounded; only the thread that writes it pays for the division
+  __device__ __forceinline__ float scale() const { return ok ? most / 127.f : __uint_as_float(0x7fc00000u); }
 };
 
+// B16: of 16-bit values, with m as fp32
+template <bool B16>
 __device__ __forceinline__ RowScale row_scale(uint32_t most) {
   RowScale s;
   s.ok = most < 0x7f800000u;
-  const float m = __uint_as_float(most);
+  s.most = __uint_as_float(most);
   const uint32_t e = most >> 23 ? most >> 23 : 1;
   s.pre = __uint_as_float(e >= 254 ? 0x00400000u : (254 - e) << 23);
-  s.a = m * s.pre;
-  // 127 / m would be infinite below 2^-121: those rows are scaled first
-  const bool tiny = m < 1e-35f;
-  s.step = !s.ok || most == 0 || tiny ? 0.f : 127.f / m;
-  s.limit = tiny ? -1.f : 0.4999f;
-  s.scale = s.ok ? m / 127.f : __uint_as_float(0x7fc00000u);
+  s.a = s.most * s.pre;
+  s.inv = s.ok && most ? __fdividef(127.f, s.a) : 0.f;
+  // where 127 / m or its steps leave fp32's range, every quotient is decided exactly
+  bool plain = s.most >= 1e-30f && s.most <= 1e30f;
+  s.step = 0.f;
+  if (B16) {
+    plain = plain && ((most >> 13 & 0x3ff) | 0x400) % 127 != 0;
+    if (plain) {
+      // at or just above 127 / a: the approximation is within 8 units
+      float up = __uint_as_float(__float_as_uint(s.inv) + 8);
+      const float r = fmaf(-up, s.a, 127.f);  // <= 0, exact to its sign
+      up = fmaf(r, s.inv * (1.f / 127.f), up);
+      if (fmaf(-up, s.a, 127.f) > 0.f) up = __uint_as_float(__float_as_uint(up) + 1);
+      s.step = up * s.pre;
+    }
+  } else if (plain) {
+    s.step = s.inv * s.pre;
+  }
+  s.limit = plain || most == 0 ? 0.4999f : -1.f;
   return s;
 }
 
 // q of one element, exactly: whether 127 x is above or below a half-integer times m, by products whose rounding errors are
-// kept (two fused multiply-adds; the differences of the rounded products are exact, since those are within a factor of two).
-static __device__ __noinline__ int quantize_exact(float x, float pre, float a) {
-  if (a == 0.f) return 0;
-  const float v = x * pre;
-  const float lo = floorf(v * (127.f / a)), half = lo + 0.5f;
-  const float p = v * 127.f, pe = fmaf(v, 127.f, -p), h = half * a, he = fmaf(half, a, -h);
+// kept (two fused multiply-adds; near a half the rounded products are within a factor of two, so that their difference is exact).
+__device__ __forceinline__ float quantize_exact(float x, const RowScale& s) {
+  const float v = x * s.pre;
+  const float lo = floorf(v * s.inv), half = lo + 0.5f;
+  const float p = v * 127.f, pe = fmaf(v, 127.f, -p), h = half * s.a, he = fmaf(half, s.a, -h);
   const float over = (p - h) + (pe - he);
-  const int l = (int)lo;
-  return over > 0.f ? l + 1 : over < 0.f ? l : l + (l & 1);
+  const bool up = over > 0.f || (over == 0.f && ((int)lo & 1));
+  return up ? lo + 1.f : lo;
 }
 
 constexpr float kRoundMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, halves to even
 
-// Eight neighbouring elements -> eight bytes.  x * step lies within 2e-5 of the quotient, so that only quotients within
-// 1e-4 of a half need the exact decision (in 16 bits many are one exactly, x = m / 2 among them).
+// Eight neighbouring elements -> eight bytes.
+template <bool B16>
 __device__ __forceinline__ uint2 quantize8(const float (&x)[8], const RowScale& s) {
   if (!s.ok) return make_uint2(0, 0);
   float t[8], off = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     t[i] = fmaf(x[i], s.step, kRoundMagic);
-    off = fmaxf(off, fabsf(fmaf(x[i], s.step, kRoundMagic - t[i])));
+    if (!B16) off = fmaxf(off, fabsf(fmaf(x[i], s.step, kRoundMagic - t[i])));
   }
   if (off > s.limit) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = __int_as_float(quantize_exact(x[i], s.pre, s.a));
+    for (int i = 0; i < 8; ++i) t[i] = quantize_exact(x[i], s) + kRoundMagic;
   }
   uint2 r;
   r.x = __byte_perm(__byte_perm(__float_as_uint(t[0]), __float_as_uint(t[1]), 0x0040),

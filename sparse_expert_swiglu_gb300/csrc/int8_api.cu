@@ -252,7 +252,9 @@ moe_status_t moe_residual_norm(const moe_residual_norm_t* op, void* stream) {
   if ((!s_in_x && s.overlaps(x)) || (s.p != residual.p && s.overlaps(residual))) return MOE_ERR_INVALID_ARG;
   if ((!y_in_x && y.overlaps(x)) || y.overlaps(residual) || y.overlaps(s)) return MOE_ERR_INVALID_ARG;
   if (sc.overlaps(x) || sc.overlaps(residual) || sc.overlaps(s) || sc.overlaps(y)) return MOE_ERR_INVALID_ARG;
-  return cuda_status(launch_residual_norm(*op, (cudaStream_t)stream));
+  int sms = 0, smem = 0;
+  if (device_sizes(sms, smem) != cudaSuccess) return MOE_ERR_CUDA;
+  return cuda_status(launch_residual_norm(*op, sms, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -35,6 +35,6 @@ cudaError_t launch_linear_int8(const LinearInt8Call& c, void* ws, int sms, int s
 cudaError_t launch_int8_tiles(const LinearInt8Call& c, const void* tokens, const float* scales, void* ws, int sms,
                               int smem_optin, cudaStream_t st);
 
-cudaError_t launch_residual_norm(const moe_residual_norm_t& op, cudaStream_t st);
+cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStream_t st);
 
 }  // namespace sesg

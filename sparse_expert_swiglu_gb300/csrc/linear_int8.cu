@@ -68,13 +68,13 @@ __device__ __forceinline__ void few_tokens(const Int8Args& p, int nt, int8_t* xq
   }
   __syncthreads();
   for (int t = 0; t < nt; ++t) {
-    const RowScale s = row_scale(most[t]);
-    if (tid == 0) scales[t] = s.scale;
+    const RowScale s = f32 ? row_scale<false>(most[t]) : row_scale<true>(most[t]);
+    if (tid == 0) scales[t] = s.scale();
     for (int i = tid; i < n; i += kFewThreads) {
       float v[8];
       if (f32) unpack8(from[((size_t)t * n + i) * 2], from[((size_t)t * n + i) * 2 + 1], v);
       else unpack8(from[(size_t)t * n + i], p.bf16, v);
-      reinterpret_cast<uint2*>(xq)[t * n + i] = quantize8(v, s);
+      reinterpret_cast<uint2*>(xq)[t * n + i] = f32 ? quantize8<false>(v, s) : quantize8<true>(v, s);
     }
   }
   __syncthreads();

@@ -24,8 +24,8 @@ __device__ __forceinline__ uint4 widen8(const uint2& q) {
 }
 
 // KEEP loads of 16 bytes are kept by a thread; F32: pairs of them (a thread's eight elements).  WIDE: q as fp16 integers.
-template <bool F32, int KEEP, bool WIDE>
-__global__ void __launch_bounds__(1024) quantize_kernel(const void* x, int bf16, int rows, int K, void* q, float* scale) {
+template <bool F32, int KEEP, bool WIDE, int MOST>
+__global__ void __launch_bounds__(MOST) quantize_kernel(const void* x, int bf16, int rows, int K, void* q, float* scale) {
   constexpr int L = F32 ? 2 : 1;  // loads of eight elements
   __shared__ uint32_t part[32];
   // In this order: the product behind the tokens' kernel takes everything before this kernel for done.
@@ -56,13 +56,13 @@ __global__ void __launch_bounds__(1024) quantize_kernel(const void* x, int bf16,
     __syncthreads();
     m = warp_most((tid & 31) < T / 32 ? part[tid & 31] : 0);
   }
-  const RowScale s = row_scale(m);
-  if (tid == 0) scale[row] = s.scale;
+  const RowScale s = row_scale<!F32>(m);
+  if (tid == 0) scale[row] = s.scale();
   auto eight = [&](const uint4* w, int i) {
     float t[8];
     if constexpr (F32) unpack8(w[0], w[1], t);
     else unpack8(w[0], bf16, t);
-    const uint2 b = quantize8(t, s);
+    const uint2 b = quantize8<!F32>(t, s);
     if constexpr (WIDE) reinterpret_cast<uint4*>(q)[row * n + i] = widen8(b);
     else reinterpret_cast<uint2*>(q)[row * n + i] = b;
   };
@@ -102,11 +102,18 @@ cudaError_t launch(void (*kernel)(Par...), dim3 grid, dim3 block, cudaStream_t s
 template <bool WIDE>
 cudaError_t launch_rows(const void* x, int dtype, int rows, int K, void* q, float* scale, cudaStream_t st) {
   const int n = K / 8;
+  // Many rows: 8 loads for each thread, so that enough bytes are in flight beside the rows that wait or round.  Few: 2, so
+  // that a row is over soon.
+  const int keep = rows <= 2 * 152 ? 2 : (dtype == MOE_F32 ? 4 : 8);
   int T = 32;
-  while (T < 1024 && T * 2 < n) T *= 2;
+  while (T < 1024 && T * keep < n) T *= 2;
   const int R = T == 32 ? 8 : 1;
-  const auto kernel = dtype == MOE_F32 ? (n <= 2 * T ? quantize_kernel<true, 2, WIDE> : quantize_kernel<true, 4, WIDE>)
-                                       : (n <= 2 * T ? quantize_kernel<false, 2, WIDE> : quantize_kernel<false, 8, WIDE>);
+  using Kernel = void (*)(const void*, int, int, int, void*, float*);
+  const Kernel kernel =
+      dtype == MOE_F32 ? (n <= 2 * T ? quantize_kernel<true, 2, WIDE, 1024>
+                                     : T <= 256 ? quantize_kernel<true, 4, WIDE, 256> : quantize_kernel<true, 4, WIDE, 1024>)
+                       : (n <= 2 * T ? quantize_kernel<false, 2, WIDE, 1024>
+                                     : T <= 256 ? quantize_kernel<false, 8, WIDE, 256> : quantize_kernel<false, 8, WIDE, 1024>);
   return launch(kernel, dim3((unsigned)(((size_t)rows + R - 1) / R)), dim3(T, R), st, x, (int)(dtype == MOE_BF16), rows, K, q,
                 scale);
 }

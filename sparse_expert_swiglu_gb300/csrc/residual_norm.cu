@@ -1,9 +1,11 @@
 // The norms behind and before a block with its gate, its scale and the residual's:
 //   s = residual_scale * residual + block_scale * gate (.) post(x),  y = norm(s), in 16 bits or 8-bit integers.
 //
-// Bound by HBM (with few tokens by the latency of its barriers): x and the residual are read once, a CTA for each token
-// keeps the row in registers in fp32 through both norms and writes s and y.  Variances are sums of squared
-// differences from the mean, of values in registers.
+// Bound by HBM (with few tokens by the latency of its barriers): x and the residual are read once, a CTA keeps a token's
+// row in registers in fp32 through both norms and writes s and y.  Variances are sums of squared differences from the mean, of
+// values in registers.  With more tokens than CTAs fit at once a CTA goes from token to token, and while it works on one, every
+// thread's own parts of the next come into shared memory by asynchronous copies.
+#include "dense_params.cuh"
 #include "int8.cuh"
 #include "int8_params.cuh"
 
@@ -13,9 +15,12 @@ namespace sesg {
 
 namespace {
 
+constexpr size_t kNormShared = 200 << 10;  // of an SM, for what comes ahead
+
 struct NormArgs {
-  int d, bf16, s_f32, y_int8, post, norm, gate_every;
-  float residual_scale, block_scale, eps;
+  int M, d, bf16, s_f32, y_int8, post, norm, gate_every;
+  int sectors;  // s starts on 32 bytes: whole sectors of fp32 at a time
+  float residual_scale, block_scale, eps, per;  // per: 1 / d
   const void *x, *residual, *gate, *post_weight, *post_bias, *weight, *bias;
   void *s, *y;
   float* y_scale;
@@ -50,14 +55,44 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
   return v;
 }
 
-// One token for each CTA, NV vectors of 8 elements for each thread.
-template <int NV>
-__global__ void __launch_bounds__(NV == 1 ? 1024 : 512) residual_norm_kernel(const NormArgs p) {
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+}
+
+// One token for each CTA at a time, NV vectors of 8 elements for each thread.  AHEAD: the next token's come ahead.
+template <int NV, bool AHEAD>
+__global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs p) {
   __shared__ float part[2][32];
+  extern __shared__ uint4 next[];  // AHEAD: [NV][x, residual, the residual's second half][thread]
   griddep_launch_dependents();
   griddep_wait();
   const int T = blockDim.x, tid = threadIdx.x, n = p.d / 8;
-  const size_t row = blockIdx.x, at = row * n;
+  const int each = p.residual ? p.s_f32 ? 3 : 2 : 1;  // vectors of 16 bytes
+  auto ask = [&](int token) {
+    const size_t at = (size_t)token * n;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = tid + j * T;
+      if (token >= p.M || c >= n) break;
+      uint4* to = next + j * each * T + tid;
+      copy16(to, reinterpret_cast<const uint4*>(p.x) + at + c);
+      const uint4* from = reinterpret_cast<const uint4*>(p.residual);
+      if (p.residual && !p.s_f32) copy16(to + T, from + at + c);
+    }
+    if (p.s_f32 && p.residual) {
+      // 32 bytes of a thread: a warp copies its 1024 in their order, whole sectors at a time
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = (tid & ~31) * 2 + h * 32 + (tid & 31), k = 2 * j * T + c;
+          if (token < p.M && k < 2 * n) copy16(next + (3 * j + 1) * T + c, reinterpret_cast<const uint4*>(p.residual) + 2 * at + k);
+        }
+    }
+  };
+  if (AHEAD) ask(blockIdx.x);
+  for (int token = blockIdx.x; token < p.M; token += gridDim.x) {
+  const size_t row = token, at = row * n;
   int turn = 0;
   float v[NV][8];
   auto sum = [&](float t) {
@@ -73,7 +108,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) residual_norm_kernel(con
 #pragma unroll
           for (int i = 0; i < 8; ++i) t += v[j][i];
         }
-      const float mean = sum(t) / p.d;
+      const float mean = sum(t) * p.per;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -86,7 +121,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) residual_norm_kernel(con
 #pragma unroll
         for (int i = 0; i < 8; ++i) t = fmaf(v[j][i], v[j][i], t);
       }
-    const float inv = 1.f / sqrtf(sum(t) / p.d + p.eps);
+    const float inv = rsqrtf(fmaf(sum(t), p.per, p.eps));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = tid + j * T;
@@ -107,11 +142,38 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) residual_norm_kernel(con
     }
   };
 
+  // x and the residual are asked for together
+  uint4 r[NV][2];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = tid + j * T;
-    const uint4 t = c < n ? reinterpret_cast<const uint4*>(p.x)[at + c] : make_uint4(0, 0, 0, 0);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if (AHEAD) continue;
+    const uint4 t = c < n ? reinterpret_cast<const uint4*>(p.x)[at + c] : zero;
+    if (p.residual) {
+      const uint4* from = reinterpret_cast<const uint4*>(p.residual);
+      r[j][0] = c < n ? from[p.s_f32 ? 2 * (at + c) : at + c] : zero;
+      r[j][1] = c < n && p.s_f32 ? from[2 * (at + c) + 1] : zero;
+    }
     unpack8(t, p.bf16, v[j]);
+  }
+  if (AHEAD) {
+    // what a thread reads its own warp has copied: no barrier of the CTA
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      const bool on = tid + j * T < n;
+      const uint4* from = next + j * each * T + tid;
+      unpack8(on ? from[0] : zero, p.bf16, v[j]);
+      if (p.residual) {
+        r[j][0] = on ? p.s_f32 ? next[(3 * j + 1) * T + 2 * tid] : from[T] : zero;
+        r[j][1] = on && p.s_f32 ? next[(3 * j + 1) * T + 2 * tid + 1] : zero;
+      }
+    }
+    __syncwarp();
+    ask(token + gridDim.x);
   }
   if (p.post) normed(p.post, p.post_weight, p.post_bias);
 #pragma unroll
@@ -124,38 +186,39 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) residual_norm_kernel(con
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] *= w[i];
     }
+    if (p.block_scale != 1.f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[j][i] *= p.block_scale;
+      for (int i = 0; i < 8; ++i) v[j][i] *= p.block_scale;
+    }
     if (p.residual) {
-      if (p.s_f32) {
-        const float4* r = reinterpret_cast<const float4*>(p.residual) + 2 * (at + c);
-        const float4 a = r[0], b = r[1];
-        const float t[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = t[i];
-      } else {
-        unpack8(reinterpret_cast<const uint4*>(p.residual)[at + c], p.bf16, w);
-      }
+      if (p.s_f32) unpack8(r[j][0], r[j][1], w);
+      else unpack8(r[j][0], p.bf16, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] = fmaf(p.residual_scale, w[i], v[j][i]);
     }
     if (p.s) {
       if (p.s_f32) {
-        float4* s = reinterpret_cast<float4*>(p.s) + 2 * (at + c);
-        s[0] = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
-        s[1] = make_float4(v[j][4], v[j][5], v[j][6], v[j][7]);
+        float* s = reinterpret_cast<float*>(p.s) + 8 * (at + c);
+        if (p.sectors) {
+          asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(s), "f"(v[j][0]), "f"(v[j][1]),
+                       "f"(v[j][2]), "f"(v[j][3]), "f"(v[j][4]), "f"(v[j][5]), "f"(v[j][6]), "f"(v[j][7])
+                       : "memory");
+        } else {
+          reinterpret_cast<float4*>(s)[0] = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
+          reinterpret_cast<float4*>(s)[1] = make_float4(v[j][4], v[j][5], v[j][6], v[j][7]);
+        }
       } else {
         reinterpret_cast<uint4*>(p.s)[at + c] = pack8(v[j], p.bf16);
       }
     }
   }
-  if (!p.norm) return;
+  if (!p.norm) continue;
   normed(p.norm, p.weight, p.bias);
   if (!p.y_int8) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (tid + j * T < n) reinterpret_cast<uint4*>(p.y)[at + tid + j * T] = pack8(v[j], p.bf16);
-    return;
+    continue;
   }
   uint32_t m = 0;
 #pragma unroll
@@ -171,20 +234,24 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) residual_norm_kernel(con
     __syncthreads();
     m = warp_most((tid & 31) < T / 32 ? most[tid & 31] : 0);
   }
-  const RowScale s = row_scale(m);
-  if (tid == 0) p.y_scale[row] = s.scale;
+  const RowScale s = row_scale<false>(m);
+  if (tid == 0) p.y_scale[row] = s.scale();
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    if (tid + j * T < n) reinterpret_cast<uint2*>(p.y)[at + tid + j * T] = quantize8(v[j], s);
+    if (tid + j * T < n) reinterpret_cast<uint2*>(p.y)[at + tid + j * T] = quantize8<false>(v[j], s);
+  if (T > 32) __syncthreads();  // the maxima have been read
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_residual_norm(const moe_residual_norm_t& op, cudaStream_t st) {
+cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStream_t st) {
   NormArgs p;
+  p.M = op.M;
   p.d = op.d;
   p.bf16 = op.dtype == MOE_BF16;
   p.s_f32 = op.s_dtype == MOE_F32;
+  p.sectors = (uintptr_t)op.s % 32 == 0;
   p.y_int8 = op.y_dtype == MOE_I8;
   p.post = op.post;
   p.norm = op.norm;
@@ -192,6 +259,7 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, cudaStream_t st)
   p.residual_scale = op.residual_scale;
   p.block_scale = op.block_scale;
   p.eps = op.eps;
+  p.per = 1.f / op.d;
   p.x = op.x;
   p.residual = op.residual;
   p.gate = op.gate;
@@ -202,18 +270,38 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, cudaStream_t st)
   p.s = op.s;
   p.y = op.y;
   p.y_scale = op.y_scale;
-  const int n = op.d / 8, nv = n <= 512 ? 1 : n <= 1024 ? 2 : 4;
+  // Copies ahead pay from a few tokens for each CTA on.  With them 2 vectors for each thread (8192 x 4096, LayerNorms and an fp32
+  // residual: 73 us, with 1 81, with 4 79), without them 1, which leaves one token's barriers with the least work between.
+  const int n = op.d / 8;
+  const bool ahead = op.M > 2 * sms;
+  const int nv = n > 1024 ? 4 : n > 512 || ahead ? 2 : 1;
+  const int T = ((n + nv - 1) / nv + 31) / 32 * 32;
+  const int each = op.residual ? p.s_f32 ? 3 : 2 : 1;
+  const size_t bytes = ahead ? (size_t)nv * each * T * 16 : 0;
+  // CTAs that fit an SM at once, by threads and shared memory
+  int fit = 1024 / T < 24 ? 1024 / T : 24;
+  if (bytes && fit > (int)(kNormShared / (bytes + 1280))) fit = (int)(kNormShared / (bytes + 1280));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(op.M);
-  cfg.blockDim = dim3(((n + nv - 1) / nv + 31) / 32 * 32);
+  cfg.gridDim = dim3(ahead && op.M > fit * sms ? fit * sms : op.M);
+  cfg.blockDim = dim3(T);
+  cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const auto kernel = nv == 1 ? residual_norm_kernel<1> : nv == 2 ? residual_norm_kernel<2> : residual_norm_kernel<4>;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  using Kernel = void (*)(NormArgs);
+  static constexpr Kernel kernels[2][3] = {
+      {residual_norm_kernel<1, false>, residual_norm_kernel<2, false>, residual_norm_kernel<4, false>},
+      {residual_norm_kernel<1, true>, residual_norm_kernel<2, true>, residual_norm_kernel<4, true>}};
+  const int which = nv == 1 ? 0 : nv == 2 ? 1 : 2;
+  static std::atomic<uint64_t> allowed[3];
+  if (ahead) {
+    const cudaError_t e = allow_shared(kernels[1][which], allowed[which], kNormShared);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaLaunchKernelEx(&cfg, kernels[ahead][which], p);
 }
 
 }  // namespace sesg
