@@ -27,14 +27,22 @@ inline int int8_stage_bytes(const Int8Plan& l) { return 128 * kI8Chunk + l.NT / 
 // Bytes of a cluster's partial sums in one CTA: 8 warps' tokens, 128 bytes each.
 inline int int8_sum_bytes(const Int8Plan& l) { return (l.NT + 31) / 32 * 16 * 8 * 128; }
 
-// The tile and the cluster with the least time by a model in SM clocks.
-inline Int8Plan int8_plan(int M, int N, int K, bool gated, int sms, int room) {
+// The tile and the cluster with the least time by a model in SM clocks (at 1.9 GHz).  Its terms are fitted to 190 measured
+// times of 17 sizes under every tile and cluster that they allow (1 to 2048 tokens; the fit's error is 6 % in the root mean
+// square, and what it chooses is at most 5 % slower than the fastest measured):
+//   a call costs 9700 whatever it does, its tokens' kernel included, and 40 for each token of a tile;
+//   an SM takes 57 bytes a clock from L2, all SMs together 3200 out of HBM, to which token tiles that run together add little;
+//   a stage takes 6.8 for each token in one CTA, 5.6 in a pair, and never less than 470 (600), which its barriers take;
+//   filling the ring 1600 a tile; the epilogue 48 for each token and round (with w_mul 13 more a token), under the next
+//   tile's products; joining a cluster's sums 4200 and 68 for each token.
+inline Int8Plan make_int8_plan(int M, int N, int K, bool gated, int sms, int room) {
   const int feats = gated ? 64 : 128, KC = (K + kI8Chunk - 1) / kI8Chunk;
   Int8Plan best;
   double best_t = 1e300;
   for (int P = 1; P <= 2; ++P) {
     if (P == 2 && (M <= 96 || N <= feats)) continue;
     for (int NT = 32; NT <= kI8Cols; NT += 32) {
+      if (NT > 32 && NT - 32 >= M) break;  // the tile before holds them all
       Int8Plan l;
       l.P = P;
       l.MT = (M + NT - 1) / NT;
@@ -52,21 +60,21 @@ inline Int8Plan int8_plan(int M, int N, int K, bool gated, int sms, int room) {
         const int fit = clusters(P * S, sms);
         // Where w's bytes are the bound: as few features as fill the last wave (whole 32-byte sectors of a token's row).
         const long long most = (long long)((N + feats * P - 1) / (feats * P)) * l.MT;
-        if (most > (1 << 30)) continue;
+        if (most > (1 << 30) || fit < 1) continue;
         const long long waves = (most + fit - 1) / fit, ft = waves * fit / l.MT;
         l.rows = l.MT > 1 ? feats : (int)((N + ft * P - 1) / (ft * P) + 15) / 16 * 16;
         if (l.rows > feats) l.rows = feats;
         l.T = (N + l.rows * P - 1) / (l.rows * P) * l.MT;
         if (S > 1 && (l.T > fit || S > KC || int8_sum_bytes(l) > l.stages * stage)) continue;
         const double active = (double)(l.T < fit ? l.T : fit) * S * P;
-        const double bytes = (gated ? 2 : 1) * l.rows * 128.0;
-        const double load = bytes + l.NT / P * 256.0;
-        const double mem = bytes * active / 3550;  // weights out of HBM, all SMs
-        double stage_t = load / 62;
-        for (const double least : {mem / (l.MT < kTogether ? l.MT : kTogether), 8 * 1.25 * l.NT / 2.0, 600.0})
+        const double bytes = (gated ? 2 : 1) * l.rows * 128.0, load = bytes + l.NT / P * 256.0;
+        const double mem = bytes * active / 3200 / (1 + 0.5 * ((l.MT < kTogether ? l.MT : kTogether) - 1));
+        double stage_t = load / 57;
+        for (const double least : {mem, (P == 1 ? 6.8 : 5.6) * l.NT, P == 1 ? 470.0 : 600.0})
           if (stage_t < least) stage_t = least;
-        const double tile = ((KC + S - 1) / S) * stage_t, epi = 1500 + 60.0 * l.NT + 14.0 * l.NT * (((KC + S - 1) / S + 7) / 8);
-        double t = waves * (tile > epi ? tile : epi) + 2500 + 60.0 * l.NT + (S > 1 ? 2500 + 24.0 * l.NT : 0);
+        const int share = (KC + S - 1) / S;
+        const double tile = share * stage_t + 1600, epi = l.NT * (48.0 * ((share + kI8Round - 1) / kI8Round) + (gated ? 13 : 0));
+        const double t = waves * (tile > epi ? tile : epi) + 40.0 * l.NT + (S > 1 ? 4200 + 68.0 * l.NT : 0);
         if (t < best_t) {
           best_t = t;
           best = l;
@@ -75,6 +83,30 @@ inline Int8Plan int8_plan(int M, int N, int K, bool gated, int sms, int room) {
     }
   }
   return best;
+}
+
+// A thread keeps the plans of the sizes that it used last, which a model's calls come back to: 64 of them, by their mixed
+// sizes.
+inline const Int8Plan& int8_plan(int M, int N, int K, bool gated, int sms, int room) {
+  struct Kept {
+    int key[6] = {-1, 0, 0, 0, 0, 0};
+    Int8Plan plan;
+  };
+  static thread_local Kept kept[64];
+  const int key[6] = {M, N, K, (int)gated, sms, room};
+  uint64_t h = 0;
+  for (const int v : key) {
+    h = (h ^ (uint32_t)v) * 0x9E3779B97F4A7C15ull;
+    h ^= h >> 29;
+  }
+  Kept& k = kept[h % 64];
+  bool same = true;
+  for (int i = 0; i < 6; ++i) same = same && k.key[i] == key[i];
+  if (!same) {
+    k.plan = make_int8_plan(M, N, K, gated, sms, room);
+    for (int i = 0; i < 6; ++i) k.key[i] = key[i];
+  }
+  return k.plan;
 }
 
 }  // namespace sesg

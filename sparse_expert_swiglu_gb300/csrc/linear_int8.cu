@@ -201,11 +201,11 @@ Int8Ws::Int8Ws(int M, int K) {
 
 // Whether the stream of w takes the call, and not the tensor cores.  The stream is a single short kernel (512 x 512: 3.4 us
 // for 5 tokens and 4.5 for 16 against 6.3) whose time grows with the tokens: at 8 tokens they meet at 56 MB of weights (4096 x
-// 14336: 18.4 us both; 32000 x 4096: 36.4 us against 27.2), at 9 to 16 sooner (16 of 2048 x 1408: 6.0 us against 9.3, 16 of 4096 x
-// 4096: 13.0 against 12.2, 9 of them: 10.6 against 12.0).
+// 14336: 18.4 us both; 32000 x 4096: 36.4 us against 27.2, of 4 tokens 29.6), at 9 to 16 sooner (16 of 2048 x 1408: 6.0 us
+// against 9.3, 16 of 4096 x 4096: 13.0 against 12.2, 9 of them: 10.6 against 12.0).
 static bool int8_few(int M, int N, int K, bool gated, int tok) {
   const double work = (gated ? 2.0 : 1.0) * N * K * M;
-  return M == 1 || (M <= tok && tok * K <= kFewShared && (M <= 4 || work <= (M <= 8 ? 450e6 : 160e6)));
+  return M == 1 || (M <= tok && tok * K <= kFewShared && (M <= 2 || work <= (M <= 8 ? 450e6 : 160e6)));
 }
 
 cudaError_t launch_linear_int8(const LinearInt8Call& c, void* ws, int sms, int smem_optin, cudaStream_t st) {

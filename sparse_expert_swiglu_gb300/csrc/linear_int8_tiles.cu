@@ -616,7 +616,7 @@ cudaError_t launch_int8_tiles(const LinearInt8Call& c, const void* tokens, const
                               int smem_optin, cudaStream_t st) {
   const bool gated = c.w_mul != nullptr;
   const int room = smem_optin - 1024 - (int)sizeof(TileBars) - int8_extra_bytes(gated);
-  const Int8Plan l = int8_plan(c.M, c.N, c.K, gated, sms, room);
+  const Int8Plan& l = int8_plan(c.M, c.N, c.K, gated, sms, room);
   if (!l.S) return cudaErrorInvalidValue;
   CUtensorMap mw, mw2, mx;
   const uint32_t rows = c.N < l.rows ? c.N : l.rows, toks = c.M < l.NT / l.P ? c.M : l.NT / l.P;
