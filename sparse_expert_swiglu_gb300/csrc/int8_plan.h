@@ -54,6 +54,7 @@ inline Int8Plan make_int8_plan(int M, int N, int K, bool gated, int sms, int roo
       l.slots = free_slots < kI8MaxSlots ? free_slots : kI8MaxSlots;
       const int stage = int8_stage_bytes(l);
       l.stages = room / stage < kDnMaxStages ? room / stage : kDnMaxStages;
+      if (l.blocks <= 2 && l.stages > l.slots) l.stages = l.slots;  // a slot is free when its stage is
       if (l.stages < 2) continue;
       for (int S = 1; S * P <= 8; S *= 2) {
         l.S = S;

@@ -184,6 +184,8 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   constexpr int P = PAIR ? 2 : 1;
+  // With up to 64 tokens there are no fewer slots than stages: a slot is free when its stage is.
+  constexpr bool kSlotWaits = TB > 2;
   const int feats = p.rows;
   constexpr uint32_t kW = 128 * kI8Chunk;  // bytes of a stage's rows of w
   const int NT = p.NT, toks = NT / P, ns = p.stages;
@@ -230,131 +232,131 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
   // before it is done, and only what it writes, tokens and scales, has to be waited for.
   griddep_launch_dependents();
 
-  if (warp == 0) {
+  // (setmaxnreg is one instruction for all warps of a warpgroup: four from a multiple of four on.)
+  if (warp < 4) {
     if constexpr (TB >= 4) fewer_registers<40>();
-    if (elect_one()) {
-      const uint64_t pw = p.stream ? policy_evict_first() : policy_evict_normal();
-      const uint64_t px = policy_evict_normal();
-      int st = 0, issued = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      auto weights = [&](int s, int kc, int ft) {
-        const int f0 = (ft * P + half_of) * feats;
-        mbar_arrive_expect_tx(&bars->full[s], load_bytes);
-        ++issued;
-        const uint32_t a = ring_at + s * stage_bytes;
-        tma_2d(a, &mw, kc * kI8Chunk, f0, &bars->full[s], pw);
-        if (GATED) tma_2d(a + kW / 2, &mw2, kc * kI8Chunk, f0, &bars->full[s], pw);
-      };
-      auto tokens = [&](int s, int kc, int mt) {
-        const int m0 = mt * NT + half_of * toks;
-        const uint32_t b = ring_at + s * stage_bytes + kW;
-        tma_2d(b, &mx, kc * kI8Chunk, m0, &bars->full[s], px);
-        tma_2d(b + tok_bytes, &mx, kc * kI8Chunk + 64, m0, &bars->full[s], px);
-      };
-      int ahead = 0;  // stages of the first tile whose weights are under way before the tokens can be
-      if (first < p.T) {
-        int ft, mt;
-        tile_of(first, p.T, p.MT, ft, mt);
-        for (; ahead < ns && kc0 + ahead < kc1; ++ahead) weights(ahead, kc0 + ahead, ft);
+    if (warp == 0) {
+      if (elect_one()) {
+        const uint64_t pw = p.stream ? policy_evict_first() : policy_evict_normal();
+        const uint64_t px = policy_evict_normal();
+        int st = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        auto weights = [&](int s, int kc, int ft) {
+          const int f0 = (ft * P + half_of) * feats;
+          mbar_arrive_expect_tx(&bars->full[s], load_bytes);
+          ++issued;
+          const uint32_t a = ring_at + s * stage_bytes;
+          tma_2d(a, &mw, kc * kI8Chunk, f0, &bars->full[s], pw);
+          if (GATED) tma_2d(a + kW / 2, &mw2, kc * kI8Chunk, f0, &bars->full[s], pw);
+        };
+        auto tokens = [&](int s, int kc, int mt) {
+          const int m0 = mt * NT + half_of * toks;
+          const uint32_t b = ring_at + s * stage_bytes + kW;
+          tma_2d(b, &mx, kc * kI8Chunk, m0, &bars->full[s], px);
+          tma_2d(b + tok_bytes, &mx, kc * kI8Chunk + 64, m0, &bars->full[s], px);
+        };
+        int ahead = 0;  // stages of the first tile whose weights are under way before the tokens can be
+        if (first < p.T) {
+          int ft, mt;
+          tile_of(first, p.T, p.MT, ft, mt);
+          for (; ahead < ns && kc0 + ahead < kc1; ++ahead) weights(ahead, kc0 + ahead, ft);
+        }
+        griddep_wait();
+        for (int t = first; ok && t < p.T; t += step) {
+          int ft, mt;
+          tile_of(t, p.T, p.MT, ft, mt);
+          for (int kc = kc0; kc < kc1; ++kc) {
+            if (ahead > 0) {
+              --ahead;
+            } else {
+              if (!dn_wait(&bars->empty[st], ph ^ 1, bars)) {
+                dn_fail(bars, status);
+                ok = false;
+                break;
+              }
+              weights(st, kc, ft);
+            }
+            tokens(st, kc, mt);
+            if (++st == ns) {
+              st = 0;
+              ph ^= 1;
+            }
+          }
+        }
+        // No copy of this CTA is in flight when it ends: the last stages have come.
+        const int n = issued < ns ? issued : ns;
+        for (int i = 0; i < n; ++i) {
+          if (--st < 0) {
+            st = ns - 1;
+            ph ^= 1;
+          }
+          dn_drain(&bars->full[st], ph, p.tries);
+        }
       }
-      griddep_wait();
-      for (int t = first; ok && t < p.T; t += step) {
-        int ft, mt;
-        tile_of(t, p.T, p.MT, ft, mt);
-        for (int kc = kc0; kc < kc1; ++kc) {
-          if (ahead > 0) {
-            --ahead;
-          } else {
-            if (!dn_wait(&bars->empty[st], ph ^ 1, bars)) {
+    } else if (warp == 1) {
+      if (crank == lead && elect_one()) {
+        const uint32_t desc = mma_desc(NT, 0, 0, P * 128);
+        auto commit = [&](uint64_t* bar) {
+          if constexpr (PAIR) mma_commit_pair(bar, lead);
+          else mma_commit(bar);
+        };
+        int st = 0, buf = 0, slot = 0;
+        uint32_t tph = 0, sph = 0;
+        bool ok = true, open = false;
+        for (int t = 0; ok && t < tiles; ++t) {
+          for (int kr = kc0, end; ok && kr < kc1; kr = end) {
+            end = kr + kI8Round < kc1 ? kr + kI8Round : kc1;
+            if (!(PAIR ? cluster_wait(&bars->tempty[buf], tph ^ 1, bars) : dn_wait(&bars->tempty[buf], tph ^ 1, bars))) {
               dn_fail(bars, status);
               ok = false;
               break;
             }
-            weights(st, kc, ft);
-          }
-          tokens(st, kc, mt);
-          if (++st == ns) {
-            st = 0;
-            ph ^= 1;
-          }
-        }
-      }
-      // No copy of this CTA is in flight when it ends: the last stages have come.
-      const int n = issued < ns ? issued : ns;
-      for (int i = 0; i < n; ++i) {
-        if (--st < 0) {
-          st = ns - 1;
-          ph ^= 1;
-        }
-        dn_drain(&bars->full[st], ph, p.tries);
-      }
-    }
-  } else if (warp == 1) {
-    if constexpr (TB >= 4) fewer_registers<40>();
-    if (crank == lead && elect_one()) {
-      const uint32_t desc = mma_desc(NT, 0, 0, P * 128);
-      auto commit = [&](uint64_t* bar) {
-        if constexpr (PAIR) mma_commit_pair(bar, lead);
-        else mma_commit(bar);
-      };
-      int st = 0, buf = 0, slot = 0;
-      uint32_t tph = 0, sph = 0;
-      bool ok = true, open = false;
-      for (int t = 0; ok && t < tiles; ++t) {
-        for (int kr = kc0, end; ok && kr < kc1; kr = end) {
-          end = kr + kI8Round < kc1 ? kr + kI8Round : kc1;
-          if (!(PAIR ? cluster_wait(&bars->tempty[buf], tph ^ 1, bars) : dn_wait(&bars->tempty[buf], tph ^ 1, bars))) {
-            dn_fail(bars, status);
-            ok = false;
-            break;
-          }
-          tc_after_sync();
-          const uint32_t d = tmem + buf * NT;
-          // (One way back for each stage: a jump costs the issuing thread some 200 to 400 clocks beside 19 other warps.)
+            tc_after_sync();
+            const uint32_t d = tmem + buf * NT;
+            // (One way back for each stage: a jump costs the issuing thread some 200 to 400 clocks beside 19 other warps.)
 #pragma unroll 2
-          for (int kc = kr; kc < end; ++kc) {
-            const uint64_t bd = smem_desc(ring_at + st * stage_bytes + kW, 16);
+            for (int kc = kr; kc < end; ++kc) {
+              const uint64_t bd = smem_desc(ring_at + st * stage_bytes + kW, 16);
 #pragma unroll
-            for (int hk = 0; hk < 2; hk += KS) {
-              if (!(PAIR ? cluster_wait(&tb->afull[slot], sph, bars) : dn_wait(&tb->afull[slot], sph, bars))) {
-                ok = false;
-                break;
+              for (int hk = 0; hk < 2; hk += KS) {
+                if (!(PAIR ? cluster_wait(&tb->afull[slot], sph, bars) : dn_wait(&tb->afull[slot], sph, bars))) {
+                  ok = false;
+                  break;
+                }
+                tc_after_sync();
+                const uint32_t a = slots_at + slot * 32 * KS;
+#pragma unroll
+                for (int ks = 0; ks < 4 * KS; ++ks)
+                  mma_ts<PAIR>(d, a + ks * 8, bd + (hk || ks >= 4 ? tok_bytes >> 4 : 0) + (ks & 3) * 2, desc,
+                               hk > 0 || ks > 0 || kc > kr);
+                if (kSlotWaits) commit(&tb->aempty[slot]);
+                open = true;
+                const bool wrap = ++slot == p.slots;
+                slot = wrap ? 0 : slot;
+                sph ^= wrap;
               }
-              tc_after_sync();
-              const uint32_t a = slots_at + slot * 32 * KS;
-#pragma unroll
-              for (int ks = 0; ks < 4 * KS; ++ks)
-                mma_ts<PAIR>(d, a + ks * 8, bd + (hk || ks >= 4 ? tok_bytes >> 4 : 0) + (ks & 3) * 2, desc,
-                             hk > 0 || ks > 0 || kc > kr);
-              commit(&tb->aempty[slot]);
-              open = true;
-              const bool wrap = ++slot == p.slots;
-              slot = wrap ? 0 : slot;
-              sph ^= wrap;
+              if (!ok) break;
+              commit(&bars->empty[st]);
+              st = st + 1 == ns ? 0 : st + 1;
             }
-            if (!ok) break;
-            commit(&bars->empty[st]);
-            st = st + 1 == ns ? 0 : st + 1;
-          }
-          if (!ok) {
-            dn_fail(bars, status);
-            break;
-          }
-          commit(&bars->tfull[buf]);
-          if (++buf == 2) {
-            buf = 0;
-            tph ^= 1;
+            if (!ok) {
+              dn_fail(bars, status);
+              break;
+            }
+            commit(&bars->tfull[buf]);
+            if (++buf == 2) {
+              buf = 0;
+              tph ^= 1;
+            }
           }
         }
-      }
-      if (open) {  // every product is done before TMEM is given back
-        commit(&bars->drain);
-        dn_drain(&bars->drain, 0, kWaitTries);
+        if (open) {  // every product is done before TMEM is given back
+          commit(&bars->drain);
+          dn_drain(&bars->drain, 0, kWaitTries);
+        }
       }
     }
-  } else if (warp < 4) {
-    if constexpr (TB >= 4) fewer_registers<40>();
   } else if (warp < 12) {
     // Every other stage, of the 32 rows whose TMEM lanes this warp may write.
     if constexpr (TB >= 4) fewer_registers<72>();
@@ -367,25 +369,32 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
 #pragma unroll 1
     for (int it = set; ok && it < total; it += 2) {
       ok = dn_wait(&bars->full[st], ph, bars);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        if (lane == 0) dn_fail(bars, status);
+        break;
+      }
       const uint32_t from = ring_at + st * stage_bytes + row * 128;
+      uint4 w[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) w[c] = ld_shared_v4(from + ((c ^ (row & 7)) << 4));
+      if (!kSlotWaits) tc_after_sync();
 #pragma unroll
       for (int hk = 0; hk < 2; ++hk) {
         uint32_t v[32];
-        if (ok) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint4 w = ld_shared_v4(from + (((hk * 4 + c) ^ (row & 7)) << 4));
-            to_f16(w.x, v[8 * c], v[8 * c + 1]);
-            to_f16(w.y, v[8 * c + 2], v[8 * c + 3]);
-            to_f16(w.z, v[8 * c + 4], v[8 * c + 5]);
-            to_f16(w.w, v[8 * c + 6], v[8 * c + 7]);
-          }
-          if (hk == 0 || KS == 1)
-            ok = PAIR ? cluster_wait(&tb->aempty[slot], sph ^ 1, bars) : dn_wait(&tb->aempty[slot], sph ^ 1, bars);
+        for (int c = 0; c < 4; ++c) {
+          to_f16(w[4 * hk + c].x, v[8 * c], v[8 * c + 1]);
+          to_f16(w[4 * hk + c].y, v[8 * c + 2], v[8 * c + 3]);
+          to_f16(w[4 * hk + c].z, v[8 * c + 4], v[8 * c + 5]);
+          to_f16(w[4 * hk + c].w, v[8 * c + 6], v[8 * c + 7]);
         }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_after_sync();
+        if (kSlotWaits && (KS == 1 || hk == 0)) {
+          ok = PAIR ? cluster_wait(&tb->aempty[slot], sph ^ 1, bars) : dn_wait(&tb->aempty[slot], sph ^ 1, bars);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_after_sync();
+        }
         tmem_st32(lanes + (slot * KS + (KS == 2 ? hk : 0)) * 32, v);
         if (hk == 1 || KS == 1) {
           tmem_stored();
