@@ -130,6 +130,34 @@ __device__ __forceinline__ void tile_residual(const TileArgs& p, int feat, int t
   for (int i = 0; i < W; ++i) r[i] = i < n ? from[(size_t)i * p.N] : (unsigned short)0;
 }
 
+// Residual and store of W tokens' values of one feature; token i at offset at + i * N.
+template <int W, bool FULL>
+__device__ __forceinline__ void tile_write(const TileArgs& p, size_t at, int n, float (&v)[W], const unsigned short (&r)[W]) {
+  if (p.residual) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = __fadd_rn(v[i], from16(r[i], p.bf16));
+  }
+  if (p.out_f32) {
+    float* y = reinterpret_cast<float*>(p.y) + at;
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (FULL || i < n) y[(size_t)i * p.N] = v[i];
+    return;
+  }
+  unsigned short* y = reinterpret_cast<unsigned short*>(p.y) + at;
+  unsigned short t[W];
+  if (p.bf16) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) t[i] = to16(v[i], 1);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) t[i] = to16(v[i], 0);
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    if (FULL || i < n) y[(size_t)i * p.N] = t[i];
+}
+
 // Activation, product with m (with w_mul), residual and store of W tokens from tok of one feature; n of them exist.
 template <int W, bool GATED>
 __device__ __forceinline__ void tile_store(const TileArgs& p, int feat, int tok, int n, float (&v)[W], const float* m,
@@ -139,24 +167,9 @@ __device__ __forceinline__ void tile_store(const TileArgs& p, int feat, int tok,
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = __fmul_rn(v[i], m[i]);
   }
-  if (p.residual) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = __fadd_rn(v[i], from16(r[i], p.bf16));
-  }
   const size_t at = (size_t)tok * p.N + feat;
-  if (p.out_f32) {
-    float* y = reinterpret_cast<float*>(p.y) + at;
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-      if (i < n) y[(size_t)i * p.N] = v[i];
-  } else {
-    unsigned short* y = reinterpret_cast<unsigned short*>(p.y) + at;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const unsigned short t = to16(v[i], p.bf16);
-      if (i < n) y[(size_t)i * p.N] = t;
-    }
-  }
+  if (W >= 8 && n >= W) tile_write<W, true>(p, at, n, v, r);
+  else tile_write<W, false>(p, at, n, v, r);
 }
 
 // Arrives at a barrier of the pair.  What it orders lies in TMEM, behind tcgen05's own fences; the release over the cluster of
@@ -234,7 +247,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
 
   // (setmaxnreg is one instruction for all warps of a warpgroup: four from a multiple of four on.)
   if (warp < 4) {
-    if constexpr (TB >= 4) fewer_registers<40>();
+    if constexpr (TB >= 4) fewer_registers<48>();
     if (warp == 0) {
       if (elect_one()) {
         const uint64_t pw = p.stream ? policy_evict_first() : policy_evict_normal();
@@ -375,19 +388,27 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
         break;
       }
       const uint32_t from = ring_at + st * stage_bytes + row * 128;
-      uint4 w[8];
+      // (Both halves are read first where there are registers for them.)
+      constexpr int H = TB > 2 ? 1 : 2;
+      uint4 w[4 * H];
+      auto read = [&](int hk, int h) {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) w[c] = ld_shared_v4(from + ((c ^ (row & 7)) << 4));
+        for (int c = 0; c < 4; ++c) w[4 * h + c] = ld_shared_v4(from + (((4 * hk + c) ^ (row & 7)) << 4));
+      };
+      read(0, 0);
+      if (H == 2) read(1, 1);
       if (!kSlotWaits) tc_after_sync();
 #pragma unroll
       for (int hk = 0; hk < 2; ++hk) {
+        if (H == 1 && hk == 1) read(1, 0);
         uint32_t v[32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          to_f16(w[4 * hk + c].x, v[8 * c], v[8 * c + 1]);
-          to_f16(w[4 * hk + c].y, v[8 * c + 2], v[8 * c + 3]);
-          to_f16(w[4 * hk + c].z, v[8 * c + 4], v[8 * c + 5]);
-          to_f16(w[4 * hk + c].w, v[8 * c + 6], v[8 * c + 7]);
+          const uint4& t = w[H == 2 ? 4 * hk + c : c];
+          to_f16(t.x, v[8 * c], v[8 * c + 1]);
+          to_f16(t.y, v[8 * c + 2], v[8 * c + 3]);
+          to_f16(t.z, v[8 * c + 4], v[8 * c + 5]);
+          to_f16(t.w, v[8 * c + 6], v[8 * c + 7]);
         }
         if (kSlotWaits && (KS == 1 || hk == 0)) {
           ok = PAIR ? cluster_wait(&tb->aempty[slot], sph ^ 1, bars) : dn_wait(&tb->aempty[slot], sph ^ 1, bars);
@@ -685,7 +706,7 @@ cudaError_t launch_int8_tiles(const LinearInt8Call& c, const void* tokens, const
       if (e != cudaSuccess) return e;
       regs[which].store(n = attr.numRegs, std::memory_order_relaxed);
     }
-    if (n * kI8Threads < 128 * 40 + 256 * 72 + 256 * 144) return cudaErrorInvalidConfiguration;
+    if (n * kI8Threads < 128 * 48 + 256 * 72 + 256 * 144) return cudaErrorInvalidConfiguration;
   }
   const int fit = sms / l.P;
   cudaLaunchConfig_t cfg = {};
