@@ -55,6 +55,7 @@ inline Int8Plan make_int8_plan(int M, int N, int K, bool gated, int sms, int roo
       const int stage = int8_stage_bytes(l);
       l.stages = room / stage < kDnMaxStages ? room / stage : kDnMaxStages;
       if (l.blocks <= 2 && l.stages > l.slots) l.stages = l.slots;  // a slot is free when its stage is
+      l.stages &= ~1;  // two sets of warps take turns, and a stage must always be the same set's
       if (l.stages < 2) continue;
       for (int S = 1; S * P <= 8; S *= 2) {
         l.S = S;

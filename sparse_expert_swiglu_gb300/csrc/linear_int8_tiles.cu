@@ -371,7 +371,11 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
       }
     }
   } else if (warp < 12) {
-    // Every other stage, of the 32 rows whose TMEM lanes this warp may write.
+    // Every other stage, of the 32 rows whose TMEM lanes this warp may write.  The number of stages is even, so that a stage is
+    // always the same warps': a wait by parity tells a phase only from the one before it, which its warps must have seen end.
+    // (With seven, warps that ran ahead took a stage that the others had not seen loaded for their own next one: 3 of 80000
+    // calls of 4 tokens by 32000 x 4096 came to a stop.)  A slot's last use but one lies four stages back or more, and these
+    // warps have waited for the products of one four stages back when they took their stage before this.
     if constexpr (TB >= 4) fewer_registers<72>();
     const int q = warp & 3, set = (warp - 4) >> 2, row = q * 32 + lane;
     const uint32_t lanes = slots_at + ((uint32_t)(q * 32) << 16);

@@ -315,6 +315,21 @@ def test_linear_in_place_streams_and_graphs(M):
 
 
 @gpu
+@pytest.mark.parametrize("M,N,K,gated,calls", [(4, 32000, 4096, False, 20000), (40, 2048, 2048, True, 20000),
+                                               (300, 1024, 14336, False, 10000), (100, 4096, 4096, False, 10000)])
+def test_linear_many_calls_in_a_row(M, N, K, gated, calls):
+    """Thousands of calls without a break: every one ends by itself, and the last one's result is the first one's."""
+    c = _linear_case(M, N, K, F16, "int8", "silu" if gated else "none", gated=gated, out=F32)
+    a = {k: _cuda(v) for k, v in c.items()}
+    ws = ses.Workspace(ses.linear_int8_workspace_bytes(M, N, K, gated))
+    first, out = _linear_check(c, ws=ws), torch.empty(M, N, device="cuda")
+    kw = {k: v for k, v in a.items() if k not in ("x", "w", "w_scale")}
+    for i in range(calls):
+        ses.linear_int8(a["x"], a["w"], a["w_scale"], out=out, ws=ws, **kw)
+    assert ws.status() == 0 and torch.equal(out, first)
+
+
+@gpu
 def test_linear_output_behind_2_to_the_31():
     M, N, K = 65537, 40000, 64
     g = torch.Generator(device="cuda").manual_seed(2)
