@@ -236,14 +236,14 @@ cudaError_t launch_linear_int8(const LinearInt8Call& c, void* ws, int sms, int s
   p.bias_mul = c.bias_mul;
   p.residual = c.residual;
   p.y = c.y;
-  const int rw = tok == 1 ? 1 : tok == 8 ? 4 : 2, groups = (c.N + rw - 1) / rw;
+  const int rw = tok == 1 ? 1 : tok == 4 || tok == 8 ? 4 : 2, groups = (c.N + rw - 1) / rw;
   const int segs = (c.K / 16 + 31) / 32;
   p.parts = 1;
   while (p.parts < kFewWarps && p.parts * 2 <= segs && (long long)groups * p.parts * 2 <= (long long)sms * kFewWarps)
     p.parts *= 2;
   using Kernel = void (*)(Int8Args);
   const Kernel kernel = tok == 1 ? int8_few_kernel<1, 1> : tok == 2 ? int8_few_kernel<2, 2>
-                        : tok == 4 ? int8_few_kernel<4, 2> : tok == 8 ? int8_few_kernel<8, 4> : int8_few_kernel<16, 2>;
+                        : tok == 4 ? int8_few_kernel<4, 4> : tok == 8 ? int8_few_kernel<8, 4> : int8_few_kernel<16, 2>;
   static std::atomic<uint64_t> allowed[5];
   cudaError_t e = allow_shared(kernel, allowed[tok == 1 ? 0 : tok == 2 ? 1 : tok == 4 ? 2 : tok == 8 ? 3 : 4], kFewShared);
   if (e != cudaSuccess) return e;

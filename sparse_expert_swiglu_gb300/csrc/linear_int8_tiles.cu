@@ -85,8 +85,10 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ void peer_store(uint32_t to, const int* v) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+// 16 bytes into a CTA of the cluster, counted on that CTA's barrier
+__device__ __forceinline__ void peer_store(uint32_t to, const int* v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(bar)
                : "memory");
 }
 
@@ -225,7 +227,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
       mbar_init(&tb->aempty[i], 1);
     }
     mbar_init(&bars->xready, S);
-    mbar_init(&bars->xfull, GATED && S == 8 ? 16 : 8);
+    mbar_init(&bars->xfull, 1);
     fence_barrier_init();
     tma_prefetch_map(&mw);
     tma_prefetch_map(&mx);
@@ -521,7 +523,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
       };
       if constexpr (!SHARED && !GATED) {
         // W tokens at a time: a short call pays for every line of code that it fetches
-        constexpr int W = TB <= 2 ? 4 : 16;
+        constexpr int W = TB <= 2 ? 8 : 16;
         for (int n0 = 16 * half; n0 < nt; n0 += 32)
 #pragma unroll 1
           for (int i = n0; i < n0 + 16; i += W) {
@@ -579,8 +581,22 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
         const bool odd = S > kUnits;  // owners by groups
         const int per = odd ? 1 : kUnits / S, cells = odd ? g4 / 2 : per * g4;
         const int unit = GATED ? (q & 1) * 2 + half : 2 * q + half;
-        if (etid == 0)
-          for (int i = 0; i < S; ++i) peer_arrive(peer_addr(smem_addr(&bars->xready), P * i + half_of));
+        auto cell_at = [&](int cell, int& u, int& g) {  // of this CTA's
+          u = odd ? rank >> 1 : rank * per + cell / g4;
+          g = odd ? 2 * cell + (rank & 1) : cell % g4;
+          return 32 * (g >> 2) + 16 * (u & 1) + 4 * (g & 3);  // the first token
+        };
+        if (warp == 12) {
+          // what will come from every CTA of the cluster, then leave for them to store it
+          int there = 0, u, g;
+          for (int cell = lane; cell < cells; cell += 32) there += cell_at(cell, u, g) < nt;
+          there = __reduce_add_sync(0xffffffffu, there);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bars->xfull, there * 512 * S * (GATED ? 2 : 1));
+            for (int i = 0; i < S; ++i) peer_arrive(peer_addr(smem_addr(&bars->xready), P * i + half_of));
+          }
+          __syncwarp();
+        }
         ok = cluster_wait(&bars->xready, 0, bars);
         if (!ok) dn_fail(bars, status);
         if (dn_any(1, 256, !ok)) break;
@@ -591,19 +607,16 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             const int g = (n0 >> 5) * 4 + h, cell = odd ? g >> 1 : (unit % per) * g4 + g;
-            if (n0 + 4 * h < nt) peer_store(peer_addr(to + cell * 512, cta(g)), &acc[0][4 * h]);
+            if (n0 + 4 * h < nt) peer_store(peer_addr(to + cell * 512, cta(g)), &acc[0][4 * h], peer_addr(smem_addr(&bars->xfull), cta(g)));
           }
           turn_blocks(std::integral_constant<int, 16>());
         }
-        __syncwarp();
-        if (lane == 0)  // releases the warp's stores
-          for (int g = 0; g < (odd ? 2 : 1); ++g) peer_arrive(peer_addr(smem_addr(&bars->xfull), cta(g)));
         ok = cluster_wait(&bars->xfull, 0, bars);
         if (!ok) dn_fail(bars, status);
         if (dn_any(1, 256, !ok)) break;
         for (int cell = warp - 12; cell < cells; cell += 8) {
-          const int u = odd ? rank >> 1 : rank * per + cell / g4, g = odd ? 2 * cell + (rank & 1) : cell % g4;
-          const int at = (u >> 1) * 32 + lane, feat = f0 + at, tok = 32 * (g >> 2) + 16 * (u & 1) + 4 * (g & 3);
+          int u, g;
+          const int tok = cell_at(cell, u, g), at = (u >> 1) * 32 + lane, feat = f0 + at;
           if (tok >= nt || at >= feats || feat >= p.N) continue;
           float xs[4];
           unsigned short r[4];
