@@ -41,15 +41,45 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8], int bf16) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A sum over the CTA's threads, the same bits in all of them; part: one of two arrays, used by turns.
-__device__ __forceinline__ float block_sum(float v, float* part) {
+// Sums of 32 neighbouring vectors, one of each lane, for NV of them at once; lane 32 / NV * j has the j-th.  What a lane adds
+// are the same two numbers at every step, whatever NV is.
+template <int NV>
+__device__ __forceinline__ float warp_sums(const float (&t)[NV], int lane) {
+  float v = t[0];
+  if constexpr (NV == 1) {
+    v += __shfl_xor_sync(0xffffffffu, v, 16);
+  } else {
+    // lanes keep one of two sums and give the other half's lanes what they add to theirs
+    float h[NV / 2];
+    const bool high = lane & 16;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int j = 0; j < NV / 2; ++j) {
+      const float keep = high ? t[j + NV / 2] : t[j], give = high ? t[j] : t[j + NV / 2];
+      h[j] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+    }
+    v = h[0];
+    if constexpr (NV == 4) {
+      const bool odd = lane & 8;
+      const float keep = odd ? h[1] : h[0], give = odd ? h[0] : h[1];
+      v = keep + __shfl_xor_sync(0xffffffffu, give, 8);
+    }
+  }
+#pragma unroll
+  for (int o = NV == 4 ? 4 : 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The sum over the CTA of the vectors' sums, the same bits in all threads and for every NV; part: one of two arrays, by turns.
+template <int NV>
+__device__ __forceinline__ float block_sum(const float (&t)[NV], float* part) {
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-  if (warps == 1) return v;
-  if (lane == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = lane < warps ? part[lane] : 0.f;
+  float v = warp_sums<NV>(t, lane);
+  if (lane % (32 / NV) == 0) part[(threadIdx.x >> 5) * NV + lane / (32 / NV)] = v;
+  if (warps == 1) __syncwarp();
+  else __syncthreads();
+  const int groups = warps * NV;  // up to 64
+  v = lane < groups ? part[lane] : 0.f;
+  if (lane + 32 < groups) v += part[lane + 32];
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
@@ -59,20 +89,22 @@ __device__ __forceinline__ void copy16(void* to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
 }
 
-// One token for each CTA at a time, NV vectors of 8 elements for each thread.  AHEAD: the next token's come ahead.
+// One token for each CTA at a time, NV vectors of 8 elements for each thread: a warp has 32 NV neighbouring ones, its lanes
+// every 32nd.  AHEAD: the next token's come ahead.
 template <int NV, bool AHEAD>
 __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs p) {
-  __shared__ float part[2][32];
+  __shared__ float part[2][64];
   extern __shared__ uint4 next[];  // AHEAD: [NV][x, residual, the residual's second half][thread]
   griddep_launch_dependents();
   griddep_wait();
-  const int T = blockDim.x, tid = threadIdx.x, n = p.d / 8;
+  const int T = blockDim.x, tid = threadIdx.x, n = p.d / 8, lane = tid & 31;
+  const int c0 = (tid >> 5) * 32 * NV + lane;  // this thread's first vector
   const int each = p.residual ? p.s_f32 ? 3 : 2 : 1;  // vectors of 16 bytes
   auto ask = [&](int token) {
     const size_t at = (size_t)token * n;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = tid + j * T;
+      const int c = c0 + 32 * j;
       if (token >= p.M || c >= n) break;
       uint4* to = next + j * each * T + tid;
       copy16(to, reinterpret_cast<const uint4*>(p.x) + at + c);
@@ -85,28 +117,28 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs p) {
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int c = (tid & ~31) * 2 + h * 32 + (tid & 31), k = 2 * j * T + c;
+          const int c = (tid & ~31) * 2 + h * 32 + lane, k = 2 * (c0 - lane + 32 * j) + h * 32 + lane;
           if (token < p.M && k < 2 * n) copy16(next + (3 * j + 1) * T + c, reinterpret_cast<const uint4*>(p.residual) + 2 * at + k);
         }
     }
   };
   if (AHEAD) ask(blockIdx.x);
+  int turn = 0;  // of the arrays, over all tokens: between two uses of one all warps meet at a barrier of the other
   for (int token = blockIdx.x; token < p.M; token += gridDim.x) {
   const size_t row = token, at = row * n;
-  int turn = 0;
   float v[NV][8];
-  auto sum = [&](float t) {
+  auto sum = [&](const float (&t)[NV]) {
     turn ^= 1;
-    return block_sum(t, part[turn]);
+    return block_sum<NV>(t, part[turn]);
   };
   auto normed = [&](int kind, const void* weight, const void* bias) {
     if (kind == MOE_NORM_LAYER) {
-      float t = 0.f;
+      float t[NV] = {};
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (tid + j * T < n) {
+        if (c0 + 32 * j < n) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) t += v[j][i];
+          for (int i = 0; i < 8; ++i) t[j] += v[j][i];
         }
       const float mean = sum(t) * p.per;
 #pragma unroll
@@ -114,17 +146,17 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[j][i] -= mean;
     }
-    float t = 0.f;
+    float t[NV] = {};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (tid + j * T < n) {
+      if (c0 + 32 * j < n) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t = fmaf(v[j][i], v[j][i], t);
+        for (int i = 0; i < 8; ++i) t[j] = fmaf(v[j][i], v[j][i], t[j]);
       }
     const float inv = rsqrtf(fmaf(sum(t), p.per, p.eps));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = tid + j * T;
+      const int c = c0 + 32 * j;
       if (c >= n) break;
       float w[8];
 #pragma unroll
@@ -146,7 +178,7 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs p) {
   uint4 r[NV][2];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = tid + j * T;
+    const int c = c0 + 32 * j;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     if (AHEAD) continue;
     const uint4 t = c < n ? reinterpret_cast<const uint4*>(p.x)[at + c] : zero;
@@ -164,7 +196,7 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs p) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const uint4 zero = make_uint4(0, 0, 0, 0);
-      const bool on = tid + j * T < n;
+      const bool on = c0 + 32 * j < n;
       const uint4* from = next + j * each * T + tid;
       unpack8(on ? from[0] : zero, p.bf16, v[j]);
       if (p.residual) {
@@ -178,7 +210,7 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs p) {
   if (p.post) normed(p.post, p.post_weight, p.post_bias);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = tid + j * T;
+    const int c = c0 + 32 * j;
     if (c >= n) break;
     float w[8];
     if (p.gate) {
@@ -217,29 +249,29 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs p) {
   if (!p.y_int8) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (tid + j * T < n) reinterpret_cast<uint4*>(p.y)[at + tid + j * T] = pack8(v[j], p.bf16);
+      if (c0 + 32 * j < n) reinterpret_cast<uint4*>(p.y)[at + c0 + 32 * j] = pack8(v[j], p.bf16);
     continue;
   }
   uint32_t m = 0;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    if (tid + j * T < n) {
+    if (c0 + 32 * j < n) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[j][i]) & 0x7fffffffu);
     }
   m = warp_most(m);
   if (T > 32) {
-    uint32_t* most = reinterpret_cast<uint32_t*>(part[turn ^ 1]);
-    if ((tid & 31) == 0) most[tid >> 5] = m;
+    turn ^= 1;
+    uint32_t* most = reinterpret_cast<uint32_t*>(part[turn]);
+    if (lane == 0) most[tid >> 5] = m;
     __syncthreads();
-    m = warp_most((tid & 31) < T / 32 ? most[tid & 31] : 0);
+    m = warp_most(lane < T / 32 ? most[lane] : 0);
   }
   const RowScale s = row_scale<false>(m);
   if (tid == 0) p.y_scale[row] = s.scale();
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    if (tid + j * T < n) reinterpret_cast<uint2*>(p.y)[at + tid + j * T] = quantize8<false>(v[j], s);
-  if (T > 32) __syncthreads();  // the maxima have been read
+    if (c0 + 32 * j < n) reinterpret_cast<uint2*>(p.y)[at + c0 + 32 * j] = quantize8<false>(v[j], s);
   }
 }
 
@@ -280,7 +312,7 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStr
   const size_t bytes = ahead ? (size_t)nv * each * T * 16 : 0;
   // CTAs that fit an SM at once, by threads and shared memory
   int fit = 1024 / T < 24 ? 1024 / T : 24;
-  if (bytes && fit > (int)(kNormShared / (bytes + 1280))) fit = (int)(kNormShared / (bytes + 1280));
+  if (bytes && fit > (int)(kNormShared / (bytes + 1536))) fit = (int)(kNormShared / (bytes + 1536));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ahead && op.M > fit * sms ? fit * sms : op.M);
   cfg.blockDim = dim3(T);

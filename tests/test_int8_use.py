@@ -1,0 +1,284 @@
+"""The 8-bit operators and residual_norm as programs use them beside one another: behind calls that write their inputs, on
+several streams and threads at once, from graphs that share a workspace, on parts of larger tensors, at their largest sizes.
+References and tolerances are those of the operators' own tests; where two ways have to agree, they agree in every bit."""
+
+from __future__ import annotations
+
+import threading
+
+import pytest
+import torch
+
+ses = pytest.importorskip("sparse_expert_swiglu_gb300")
+from tests.test_int8 import (_cuda, _expert_case, _expert_ref, _expert_run, _ints, _linear_case, _linear_check, _linear_ref,  # noqa: E402
+                             _linear_run, _product64, _rows64, _within)
+from tests.test_residual_norm import _case as _norm_case, _ref as _norm_ref, _run as _norm_run  # noqa: E402
+
+gpu = pytest.mark.gpu
+
+F16, BF16, F32, I8 = torch.float16, torch.bfloat16, torch.float32, torch.int8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ses.build_library()
+    ses.lib()
+
+
+@gpu
+@pytest.mark.parametrize("M", [1, 6, 40, 200, 520])
+@pytest.mark.parametrize("dense", [False, True])
+def test_weights_and_tokens_written_by_the_calls_before(M, dense):
+    """Weights that the quantiser writes, or a copy behind a long kernel, then the product, which starts its loads early;
+    tokens, residual and workspace that the product before wrote."""
+    N, K = 768, 1040
+    g = torch.Generator().manual_seed(M)
+    weights = [(torch.randn((N, K), generator=g) * 0.05).to(BF16).cuda() for _ in range(3)]
+    x = torch.randn((M, K), generator=g).to(BF16).cuda()
+    ws = ses.Workspace(max(ses.linear_int8_workspace_bytes(M, N, K, True), ses.linear_int8_workspace_bytes(M, 512, N)))
+    last = ses.quantize_int8((torch.randn((512, N), generator=g) * 0.05).cuda())
+    q, scale = ses.quantize_int8(weights[0])
+    big = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+
+    def step(i, ws):
+        ses.quantize_int8(weights[i % 3], out=q, out_scale=scale)
+        if dense:
+            ses.linear(x[:1], weights[1])  # a small product, under which the next call starts
+        h = ses.linear_int8(x, q, scale, act="silu", w_mul=q, w_mul_scale=scale, ws=ws)
+        return ses.linear_int8(h, *last, ws=ws)
+    want = []
+    for i in range(3):
+        torch.cuda.synchronize()
+        want.append(step(i, None))
+        torch.cuda.synchronize()
+    assert not torch.equal(want[0], want[1]) and not torch.equal(want[1], want[2])
+    got = []
+    for i in range(40):
+        if i % 4 == 0:
+            big.fill_(i)
+        got.append(step(i, ws))
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 3]), i
+    assert ws.status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 1024), (12, 512, 2064), (48, 1031, 2064), (300, 1024, 4096)])
+def test_streams_at_once(M, N, K):
+    """Two streams, then two threads with a stream each, every one with a workspace of its own."""
+    cases = [_linear_case(M, N, K, BF16, "16 bits", "silu", True, True, True, seed=s) for s in (1, 2)]
+    args = [{k: _cuda(v) for k, v in c.items()} for c in cases]
+    want = [_linear_check(c) for c in cases]
+    spaces = [ses.Workspace(ses.linear_int8_workspace_bytes(M, N, K, True)) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def run(i, times):
+        with torch.cuda.stream(streams[i]):
+            for _ in range(times):
+                got[i].append(_linear_run(args[i], ws=spaces[i]))
+    for _ in range(20):
+        run(0, 1)
+        run(1, 1)
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=run, args=(i, 50)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 70 and all(torch.equal(y, want[i]) for y in got[i])
+        assert spaces[i].status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_one_workspace_for_all_calls(M):
+    """Calls on 8-bit integers and on uncompressed weights by turns on one workspace, eager, captured apart and replayed in
+    another order."""
+    d, f = 512, 784
+    c = _linear_case(M, f, d, BF16, "16 bits", "gelu", True, True)
+    e = _expert_case(M, d, f, BF16, "16 bits", True)
+    a, b = {k: _cuda(v) for k, v in c.items()}, {**e, "w": [t.cuda() for t in e["w"]], "x": e["x"].cuda(), "residual": e["residual"].cuda()}
+    g = torch.Generator().manual_seed(4)
+    stack = ses.DenseExperts(*((torch.randn((2, f, d), generator=g) * 0.05).to(BF16).cuda() for _ in range(3)))
+    router = torch.randn((d, 2), generator=g).to(BF16).cuda()
+    layer = ses.DenseLayer(router, stack, 1)
+    few = b["x"][:min(M, 64)].contiguous()
+    ws = ses.Workspace(max(ses.linear_int8_workspace_bytes(M, f, d, True), ses.expert_int8_workspace_bytes(M, d, f),
+                           ses.layer_dense_workspace_bytes(layer, len(few)), ses.expert_dense_workspace_bytes(M, d, f)))
+    calls = [lambda ws: _linear_run(a, ws=ws), lambda ws: ses.expert_dense_swiglu(b["x"], stack, 1, ws=ws),
+             lambda ws: _expert_run(b, 1, ws=ws), lambda ws: ses.layer_dense_decode(few, layer, ws=ws)]
+    want = [call(None) for call in calls]
+    for order in ((0, 1, 2, 3), (3, 2, 1, 0), (0, 2, 0, 3, 2, 1)):
+        for i in order:
+            assert torch.equal(calls[i](ws), want[i])
+    graphs, outs = [], []
+    torch.cuda.synchronize()
+    for call in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(call(ws))
+    for order in ((3, 0, 1, 2), (2, 2, 1, 0, 3)):
+        for o in outs:
+            o.zero_()
+        for i in order:
+            graphs[i].replay()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    assert ws.status() == 0
+
+
+def _inside(t, room=16):
+    """t's values in the middle of a larger buffer, 16 bytes from its start, and what lies around."""
+    pad = room // t.element_size()
+    buf = torch.full((t.numel() + 3 * pad,), 77, dtype=t.dtype, device="cuda")
+    view = buf[pad:pad + t.numel()].view(t.shape)
+    view.copy_(t)
+    return view, buf, pad
+
+
+def _around(buf, pad, n):
+    return bool((buf[:pad] == 77).all() and (buf[pad + n:] == 77).all())
+
+
+@gpu
+@pytest.mark.parametrize("M", [1, 7, 33, 130])
+def test_parts_of_larger_tensors(M):
+    """Every tensor 16 bytes into a buffer, no better aligned; nothing around the outputs is written."""
+    c = _linear_case(M, 529, 528, BF16, "int8", "silu", True, True, True)
+    want = _linear_check(c)
+    parts = {k: (_inside(v.cuda())[0] if isinstance(v, torch.Tensor) else v) for k, v in c.items()}
+    out, buf, pad = _inside(torch.zeros_like(want))
+    got = _linear_run(parts, out=out)
+    assert got.data_ptr() % 256 == 16 and torch.equal(got, want) and _around(buf, pad, want.numel())
+
+    x = torch.randn(M, 528)
+    for dtype in (F16, F32):
+        q, qb, qp = _inside(torch.zeros(M, 528, dtype=I8))
+        s, sb, sp = _inside(torch.zeros(M))
+        ses.quantize_int8(_inside(x.to(dtype).cuda())[0], out=q, out_scale=s)
+        wq, wsc = _rows64(x.to(dtype))
+        assert torch.equal(q.cpu().double(), wq) and torch.equal(s.cpu(), wsc)
+        assert _around(qb, qp, q.numel()) and _around(sb, sp, M)
+
+    e = _expert_case(M, 144, 272, F16, "int8", True)
+    want = _expert_run(e, 1)
+    out, buf, pad = _inside(torch.zeros_like(want))
+    parts = {**e, "w": [_inside(t.cuda())[0] for t in e["w"]], "x": _inside(e["x"].cuda())[0], "x_scale": _inside(e["x_scale"].cuda())[0],
+             "residual": _inside(e["residual"].cuda())[0]}
+    assert torch.equal(_expert_run(parts, 1, out=out), want) and _around(buf, pad, want.numel())
+
+
+@gpu
+@pytest.mark.parametrize("M", [2, 700])
+@pytest.mark.parametrize("wide,int8", [(False, False), (True, False), (True, True)])
+def test_norms_of_parts_of_larger_tensors(M, wide, int8):
+    c = _norm_case(M, 1040, BF16, "layer", "rms", wide=wide, gate=M // 2, int8=int8)
+    want = _norm_run(c)
+    parts = {k: (_inside(v.cuda())[0] if isinstance(v, torch.Tensor) else v) for k, v in c.items()}
+    outs = [_inside(torch.zeros_like(t)) for t in want]
+    names = ("residual_out", "out", "out_scale")
+    got = _norm_run(parts, **{n: o[0] for n, o in zip(names, outs)})
+    for t, w, (_, buf, pad) in zip(got, want, outs):
+        assert torch.equal(t, w) and _around(buf, pad, w.numel())
+
+
+@gpu
+@pytest.mark.parametrize("M,d", [(700, 264), (1500, 4096), (400, 16384), (20000, 16), (305, 8200)])
+def test_norms_of_many_tokens_as_of_few(M, d):
+    """A CTA that goes from token to token, the next one's copies under way, gives the bits of one for each token."""
+    for wide, residual, gate in ((False, True, 1), (True, True, 0), (False, False, 5)):
+        c = _norm_case(M, d, F16, "rms", "layer", residual, wide, gate, int8=d % 16 == 0)
+        a = {k: _cuda(v) for k, v in c.items()}
+        full = _norm_run(a)
+        full = full if isinstance(full, tuple) else (full,)
+        for first in (0, M // 2, M - 5):
+            rows = slice(first, first + 5)
+            gates = a["gate"][torch.arange(first, first + 5, device="cuda") // (M // gate)].contiguous() if gate else None
+            some = _norm_run({**a, "x": a["x"][rows].contiguous(), "gate": gates,
+                              "residual": a["residual"][rows].contiguous() if residual else None})
+            some = some if isinstance(some, tuple) else (some,)
+            assert all(torch.equal(f[rows], s) for f, s in zip(full, some))
+        if residual:  # in place
+            r, x = a["residual"].clone(), a["x"].clone()
+            got = _norm_run({**a, "residual": r, "x": x}, residual_out=r, **({} if c["int8"] else {"out": x}))
+            assert got[0] is r and all(torch.equal(p, q) for p, q in zip(got, full))
+
+
+@gpu
+def test_norms_without_eps():
+    """eps 0: a row of zeros has no norm (0 / 0), the rows beside it have; scales of zero leave the residual or its share."""
+    c = _norm_case(4, 256, F16, norm="rms", residual=False, affine=False, eps=0.0)
+    c["x"][2] = 0
+    y = _norm_run(c).cpu()
+    assert torch.isnan(y[2]).all()
+    keep = [0, 1, 3]
+    _, _, ref, bound = _norm_ref({**c, "x": c["x"][keep]})
+    _within(y[keep], ref, bound, F16)
+    q, scale = _norm_run({**c, "int8": True})
+    assert torch.isnan(scale[2]) and (q[2] == 0).all() and not torch.isnan(scale[keep]).any()
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(1 << 20, 16, 16), (1 << 20, 1, 32), (20, 1 << 20, 16), (1, 1 << 20, 48), (300, (1 << 20) - 1, 16)])
+def test_the_largest_sizes(M, N, K):
+    g = torch.Generator().manual_seed(M % 97)
+    x, w = _ints(g, (M, K)), _ints(g, (N, K))
+    xs, ws = torch.rand(M, generator=g) / 32, torch.rand(N, generator=g) / 127
+    bias = torch.randn(N, generator=g).to(F16)
+    y = ses.linear_int8(x.cuda(), w.cuda(), ws.cuda(), xs.cuda(), bias=bias.cuda(), dtype=F16, out_dtype=F32).cpu()
+    for m in (slice(0, 2), slice(M // 2, M // 2 + 200), slice(max(M - 130, 0), M)):
+        for n in (slice(0, 200), slice(N // 2, N // 2 + 300), slice(max(N - 300, 0), N)):
+            ref, bound = _product64(x[m].double(), xs[m], w[n], ws[n], bias[n])
+            _within(y[m, n], ref, bound, F32)
+    assert torch.isfinite(y).all()
+
+
+@gpu
+def test_rows_behind_2_to_the_32():
+    """More than 2^32 elements: the quantiser's, and the norms' in and out."""
+    rows, K = (1 << 28) + 3, 16
+    x = torch.empty(rows, K, dtype=BF16, device="cuda")
+    x.random_(-250, 250, generator=torch.Generator(device="cuda").manual_seed(1))
+    q, s = ses.quantize_int8(x)
+    for r in (slice(0, 5), slice((1 << 27) - 3, (1 << 27) + 3), slice(rows - 7, rows)):
+        want, scale = _rows64(x[r].cpu())
+        assert torch.equal(q[r].cpu().double(), want) and torch.equal(s[r].cpu(), scale)
+    del q, s, x
+    M, d = 1 << 20, 4112
+    x = torch.empty(M, d, dtype=BF16, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(2))
+    out = torch.empty_like(x)
+    w = torch.randn(d).to(BF16)
+    s, y = ses.residual_norm(x, x, weight=w.cuda(), out=out)
+    for r in (slice(0, 3), slice((1 << 19) - 2, (1 << 19) + 2), slice(M - 4, M)):
+        t = x[r].cpu()
+        c = dict(x=t, residual=t, post="none", post_weight=None, post_bias=None, gate=None, residual_scale=1.0, block_scale=1.0,
+                 norm="rms", weight=w, bias=None, eps=1e-6)
+        rs, ds, ry, dy = _norm_ref(c)
+        _within(s[r], rs, ds, BF16)
+        _within(y[r], ry, dy, BF16)
+
+
+@gpu
+def test_one_tensor_for_several_arguments():
+    """The same weights twice, tokens that are the residual, a bias that serves both matrices."""
+    g = torch.Generator().manual_seed(8)
+    for M in (2, 50):
+        x = torch.randn((M, 256), generator=g).to(BF16)
+        w, ws = ses.quantize_int8((torch.randn((256, 256), generator=g) * 0.1).cuda())
+        b = torch.randn(256, generator=g).to(BF16)
+        c = dict(x=x, x_scale=None, w=w.cpu(), w_scale=ws.cpu(), w_mul=w.cpu(), w_mul_scale=ws.cpu(), bias=b, bias_mul=b, residual=x,
+                 act="relu", dtype=BF16, out_dtype=None)
+        xd, bd = x.cuda(), b.cuda()
+        y = ses.linear_int8(xd, w, ws, bias=bd, act="relu", w_mul=w, w_mul_scale=ws, bias_mul=bd, residual=xd)
+        ref, bound = _linear_ref(c)
+        _within(y, ref, bound, BF16)
+        ex = ses.Int8Experts(w[None], ws[None], w[None], ws[None], w[None], ws[None])
+        e = dict(w=[t.cpu()[None] for t in (w, ws, w, ws, w, ws)], x=x, x_scale=None, dtype=BF16, residual=x)
+        y = ses.expert_int8_swiglu(xd, ex, 0, residual=xd)
+        ref, bound = _expert_ref(e, 0)
+        _within(y, ref, bound, BF16)
+        got = ses.expert_int8_swiglu(xd, ex, 0, residual=xd, out=xd)  # tokens, residual and output in one
+        assert got is xd and torch.equal(got, y)
