@@ -93,6 +93,11 @@ __device__ __forceinline__ void peer_store(uint32_t to, const int* v, uint32_t b
 }
 
 __device__ __forceinline__ void tile_of(int t, int T, int MT, int& ft, int& mt) {
+  if (MT == 1) {
+    ft = t;
+    mt = 0;
+    return;
+  }
   const int block = T / MT * kTogether, b = t / block, r = t - b * block;
   const int here = MT - b * kTogether < kTogether ? MT - b * kTogether : kTogether;
   ft = r / here;
@@ -180,6 +185,10 @@ __device__ __forceinline__ void pair_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// The two halves of cluster_sync_all.
+__device__ __forceinline__ void cluster_leave() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_left() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 template <int N>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -188,6 +197,35 @@ template <int N>
 __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+
+// The sums of a tile that a cluster's CTAs share: each finishes its part of them.  A unit is 16 of every 32 tokens of 32
+// features, 8 of a tile or 4 with w_mul, for S CTAs; 8 CTAs take every other group of 4 tokens of a unit of 4.  A cell is one
+// lane's 4 tokens of 32 features, 512 bytes, at [rank][matrix][cell of the owner's][lane], in the owner's stages: from behind
+// the last one that it uses on, whose products are done before all others'.
+template <bool GATED>
+struct Cells {
+  static constexpr int kLogUnits = GATED ? 2 : 3;
+  int g4, log_per, count;  // groups of 4 tokens of a unit; a CTA's units (2 to that power) and cells
+  bool odd;                // owners by groups
+  __device__ Cells(int NT, int log_s) : g4((NT + 31) / 32 * 4), odd(log_s > kLogUnits) {
+    log_per = odd ? 0 : kLogUnits - log_s;
+    count = odd ? g4 / 2 : g4 << log_per;
+  }
+  __device__ int owner(int unit, int g) const { return odd ? 2 * unit + (g & 1) : unit >> log_per; }
+  __device__ int first(int unit) const { return odd ? 0 : (unit & ((1 << log_per) - 1)) * g4; }  // cell of its owner's
+  // a CTA's cells, by a step below or at g4 * 8: the unit and the group of the one after
+  __device__ void start(int rank, int cell, int& unit, int& g) const {
+    unit = odd ? rank >> 1 : rank << log_per;
+    g = odd ? rank & 1 : 0;
+    step(cell, unit, g);
+  }
+  __device__ void step(int by, int& unit, int& g) const {
+    g += odd ? 2 * by : by;
+    for (; g >= g4 && !odd; g -= g4) ++unit;
+  }
+  static __device__ int token(int unit, int g) { return 32 * (g >> 2) + 16 * (unit & 1) + 4 * (g & 3); }  // the first
+  __device__ int bytes(int S) const { return S * (GATED ? 2 : 1) * count * 512; }
+};
 
 // PAIR: CTA pairs, whose tile has 256 features, 128 in each CTA, which keeps half of the tokens.  SHARED: clusters share a
 // tile along k, one tile for each.  GATED: with w_mul; 64 features of w, then the same ones of w_mul.  TB: blocks of 16 columns
@@ -214,8 +252,9 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
   const int S = SHARED ? p.S : 1;
   const int crank = PAIR || SHARED ? (int)cluster_rank() : 0, half_of = PAIR ? crank & 1 : 0, lead = crank - half_of;
   const int rank = SHARED ? crank / P : 0;
-  const int first = blockIdx.x / (P * S), step = gridDim.x / (P * S);
-  const int kc0 = p.KC * rank / S, kc1 = p.KC * (rank + 1) / S;
+  const int log_s = SHARED ? __ffs(S) - 1 : 0;  // (divisions take 100 to 200 clocks each, which a call of few tokens feels)
+  const int first = blockIdx.x >> (P - 1 + log_s), step = gridDim.x >> (P - 1 + log_s);
+  const int kc0 = p.KC * rank >> log_s, kc1 = p.KC * (rank + 1) >> log_s;
   const int tiles = first < p.T ? (p.T - first + step - 1) / step : 0;
   int* status = &p.head->ctrl.status;
   const uint32_t ring_at = smem_addr(ring);
@@ -248,8 +287,19 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
   griddep_launch_dependents();
 
   // (setmaxnreg is one instruction for all warps of a warpgroup: four from a multiple of four on.)
+  const Cells<GATED> cells(NT, log_s);
+  bool left = false;  // this thread has told the cluster that it is done with it
   if (warp < 4) {
     if constexpr (TB >= 4) fewer_registers<48>();
+    if (SHARED && warp == 3) {
+      // what comes into this CTA from all of the cluster (a store that were counted before this would be as well)
+      int ft, mt, there = 0, unit, g;
+      tile_of(first, p.T, p.MT, ft, mt);
+      cells.start(rank, lane, unit, g);
+      for (int i = lane; i < cells.count; i += 32, cells.step(32, unit, g)) there += mt * NT + cells.token(unit, g) < p.M;
+      there = __reduce_add_sync(0xffffffffu, there);
+      if (lane == 0) mbar_arrive_expect_tx(&bars->xfull, there * 512 * S * (GATED ? 2 : 1));
+    }
     if (warp == 0) {
       if (elect_one()) {
         const uint64_t pw = p.stream ? policy_evict_first() : policy_evict_normal();
@@ -298,6 +348,15 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
               ph ^= 1;
             }
           }
+        }
+        if (SHARED && ok) {
+          // The stages behind the last one are free when their products are done (this thread has seen every phase of
+          // theirs but the last end): the cluster may store there, under the products of the others.
+          const int count = kc1 - kc0;
+          for (int at = 0, c = count - ns; ok && at < cells.bytes(S); at += stage_bytes, ++c)
+            ok = c < 0 || dn_wait(&bars->empty[c % ns], c / ns & 1, bars);
+          if (!ok) dn_fail(bars, status);
+          for (int i = 0; ok && i < S; ++i) peer_arrive(peer_addr(smem_addr(&bars->xready), P * i + half_of));
         }
         // No copy of this CTA is in flight when it ends: the last stages have come.
         const int n = issued < ns ? issued : ns;
@@ -473,6 +532,21 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
           scales[i] = p.x_scale[m0 + 32 * (i >> 4) + 16 * half + (i & 15)];
         __syncwarp();
       }
+      // Where a cluster's sums go: those of even and of odd groups of 4 tokens.
+      const int ring_bytes = ns * (int)stage_bytes;
+      auto place = [&](int r) { return ((p.KC * (r + 1) >> log_s) - (p.KC * r >> log_s)) % ns * (int)stage_bytes; };  // CTA r's begin
+      auto wrap = [&](int at) { return at < ring_bytes ? at : at - ring_bytes; };
+      int to[2] = {0, 0}, cta[2] = {0, 0}, from = 0;
+      if constexpr (SHARED) {
+        const int unit = GATED ? (q & 1) * 2 + half : 2 * q + half;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = cells.owner(unit, i);
+          to[i] = place(r) + ((rank * (GATED ? 2 : 1) + mul) * cells.count + cells.first(unit)) * 512 + lane * 16;
+          cta[i] = P * r + half_of;
+        }
+        from = place(rank) + lane * 16;
+      }
       bool ok = true;
       auto release = [&] {  // this set of accumulators has been read
         tc_before_sync();
@@ -573,63 +647,40 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
           turn_blocks(std::integral_constant<int, 16>());
         }
       } else {
-        // The sums go to the CTAs that finish them, in the stages, which are free once every CTA's products are done: 4 tokens
-        // of a feature are 16 bytes at [rank][matrix][unit and group of 4 tokens, of the owner's][lane].  A unit is 16 of every
-        // 32 tokens of 32 features: 8 of them, or 4 with w_mul, for S CTAs; 8 CTAs take every other group of a unit of 4.
-        constexpr int kUnits = GATED ? 4 : 8;
-        const int g4 = (NT + 31) / 32 * 4;
-        const bool odd = S > kUnits;  // owners by groups
-        const int per = odd ? 1 : kUnits / S, cells = odd ? g4 / 2 : per * g4;
-        const int unit = GATED ? (q & 1) * 2 + half : 2 * q + half;
-        auto cell_at = [&](int cell, int& u, int& g) {  // of this CTA's
-          u = odd ? rank >> 1 : rank * per + cell / g4;
-          g = odd ? 2 * cell + (rank & 1) : cell % g4;
-          return 32 * (g >> 2) + 16 * (u & 1) + 4 * (g & 3);  // the first token
-        };
-        if (warp == 12) {
-          // what will come from every CTA of the cluster, then leave for them to store it
-          int there = 0, u, g;
-          for (int cell = lane; cell < cells; cell += 32) there += cell_at(cell, u, g) < nt;
-          there = __reduce_add_sync(0xffffffffu, there);
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&bars->xfull, there * 512 * S * (GATED ? 2 : 1));
-            for (int i = 0; i < S; ++i) peer_arrive(peer_addr(smem_addr(&bars->xready), P * i + half_of));
-          }
-          __syncwarp();
-        }
+        int cell_unit, cell_g;
+        cells.start(rank, warp - 12, cell_unit, cell_g);
         ok = cluster_wait(&bars->xready, 0, bars);
         if (!ok) dn_fail(bars, status);
         if (dn_any(1, 256, !ok)) break;
-        auto cta = [&](int g) { return P * (odd ? 2 * unit + (g & 1) : unit / per) + half_of; };
-        const uint32_t to = ring_at + (uint32_t)((rank * (GATED ? 2 : 1) + mul) * cells * 512) + lane * 16;
 #pragma unroll 1
         for (int n0 = 16 * half; n0 < nt; n0 += 32) {
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int g = (n0 >> 5) * 4 + h, cell = odd ? g >> 1 : (unit % per) * g4 + g;
-            if (n0 + 4 * h < nt) peer_store(peer_addr(to + cell * 512, cta(g)), &acc[0][4 * h], peer_addr(smem_addr(&bars->xfull), cta(g)));
-          }
+          for (int h = 0; h < 4; ++h)
+            if (n0 + 4 * h < nt)
+              peer_store(peer_addr(ring_at + wrap(to[h & 1] + (((n0 >> 5) * 4 + h) >> cells.odd) * 512), cta[h & 1]), &acc[0][4 * h],
+                         peer_addr(smem_addr(&bars->xfull), cta[h & 1]));
           turn_blocks(std::integral_constant<int, 16>());
         }
         ok = cluster_wait(&bars->xfull, 0, bars);
         if (!ok) dn_fail(bars, status);
         if (dn_any(1, 256, !ok)) break;
-        for (int cell = warp - 12; cell < cells; cell += 8) {
-          int u, g;
-          const int tok = cell_at(cell, u, g), at = (u >> 1) * 32 + lane, feat = f0 + at;
+        __syncwarp();
+        cluster_leave();  // (nothing comes into this CTA any more, and nothing leaves it)
+        left = true;
+        for (int cell = warp - 12; cell < cells.count; cell += 8, cells.step(8, cell_unit, cell_g)) {
+          const int tok = cells.token(cell_unit, cell_g), at = (cell_unit >> 1) * 32 + lane, feat = f0 + at;
           if (tok >= nt || at >= feats || feat >= p.N) continue;
           float xs[4];
           unsigned short r[4];
           tile_residual(p, feat, m0 + tok, nt - tok, r);
           token_scales(p.x_scale + m0 + tok, xs);
           float v[2][4];
-          const uint8_t* from = ring + (size_t)cell * 512 + lane * 16;
 #pragma unroll
           for (int m = 0; m < (GATED ? 2 : 1); ++m) {
             const Feature fm(p, m, feat, true);
             int a[4] = {0, 0, 0, 0};
             for (int s = 0; s < S; ++s) {
-              const int4 x = *reinterpret_cast<const int4*>(from + (size_t)((s * (GATED ? 2 : 1) + m) * cells) * 512);
+              const int4 x = *reinterpret_cast<const int4*>(ring + wrap(from + ((s * (GATED ? 2 : 1) + m) * cells.count + cell) * 512));
               a[0] += x.x;
               a[1] += x.y;
               a[2] += x.z;
@@ -647,7 +698,9 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
   tc_before_sync();
   __syncthreads();
   if (PAIR || SHARED) {
-    cluster_sync_all();  // no CTA leaves while another may store into it or read its stages
+    // no CTA ends while another may store into it or read its stages
+    if (!left) cluster_leave();
+    cluster_left();
     if (dn_aborted(bars)) dn_settle();  // stores that this CTA did not wait for
   }
   tc_after_sync();
