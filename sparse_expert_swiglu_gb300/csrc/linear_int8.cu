@@ -20,7 +20,7 @@ constexpr int kFewShared = 200 << 10;  // bytes of tokens
 struct Int8Args {
   int M, N, K, bf16, act, out_f32;
   int x_dtype;          // MOE_I8, MOE_F32, else 16 bits
-  int parts;            // warps that share a row along k
+  int log_parts;        // warps that share a row along k: 2 to that power
   const void* x;
   const float* x_scale;
   const int8_t *w, *w_mul;
@@ -92,10 +92,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const Int8Args
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int V = p.K / 16, segs = (V + 31) / 32, groups = (p.N + RW - 1) / RW;
-  const int part = warp % p.parts, per = kFewWarps / p.parts;
-  const int s0 = segs * part / p.parts, s1 = segs * (part + 1) / p.parts;
+  const int part = warp & ((1 << p.log_parts) - 1), team = warp >> p.log_parts, per = kFewWarps >> p.log_parts;
+  const int s0 = segs * part >> p.log_parts, s1 = segs * (part + 1) >> p.log_parts;
   const int mats = p.w_mul ? 2 : 1;
-  const int first = (warp / p.parts) * gridDim.x + blockIdx.x, step = per * gridDim.x;
+  const int first = team * gridDim.x + blockIdx.x, step = per * gridDim.x;
 
   // a batch: U segments of 32 loads of the group's rows in one matrix
   struct At {
@@ -163,16 +163,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const Int8Args
           if (lane == r * TOK + t) mine = s;
         }
       clear();
-      if (p.parts > 1) shared_sums[round & 1][a.mat][warp][lane] = mine;
+      if (p.log_parts) shared_sums[round & 1][a.mat][warp][lane] = mine;
       if (b.g == a.g) {
         kept = mine;
       } else {
         int sum = mats == 2 ? kept : mine, sum_mul = mine;
-        if (p.parts > 1) {
-          named_barrier(1 + warp / p.parts, p.parts * 32);
+        if (p.log_parts) {
+          named_barrier(1 + team, 32 << p.log_parts);
           sum = sum_mul = 0;
           if (part == 0)
-            for (int i = 0; i < p.parts; ++i) {
+            for (int i = 0; i < 1 << p.log_parts; ++i) {
               sum += shared_sums[round & 1][0][warp + i][lane];
               sum_mul += shared_sums[round & 1][mats - 1][warp + i][lane];
             }
@@ -238,9 +238,10 @@ cudaError_t launch_linear_int8(const LinearInt8Call& c, void* ws, int sms, int s
   p.y = c.y;
   const int rw = tok == 1 ? 1 : tok == 4 || tok == 8 ? 4 : 2, groups = (c.N + rw - 1) / rw;
   const int segs = (c.K / 16 + 31) / 32;
-  p.parts = 1;
-  while (p.parts < kFewWarps && p.parts * 2 <= segs && (long long)groups * p.parts * 2 <= (long long)sms * kFewWarps)
-    p.parts *= 2;
+  int parts = 1;
+  for (p.log_parts = 0; parts < kFewWarps && parts * 2 <= segs && (long long)groups * parts * 2 <= (long long)sms * kFewWarps;
+       ++p.log_parts)
+    parts *= 2;
   using Kernel = void (*)(Int8Args);
   const Kernel kernel = tok == 1 ? int8_few_kernel<1, 1> : tok == 2 ? int8_few_kernel<2, 2>
                         : tok == 4 ? int8_few_kernel<4, 4> : tok == 8 ? int8_few_kernel<8, 4> : int8_few_kernel<16, 2>;
