@@ -27,14 +27,15 @@ inline int int8_stage_bytes(const Int8Plan& l) { return 128 * kI8Chunk + l.NT / 
 // Bytes of a cluster's partial sums in one CTA: 8 warps' tokens, 128 bytes each.
 inline int int8_sum_bytes(const Int8Plan& l) { return (l.NT + 31) / 32 * 16 * 8 * 128; }
 
-// The tile and the cluster with the least time by a model in SM clocks (at 1.9 GHz).  Its terms are fitted to 190 measured
-// times of 17 sizes under every tile and cluster that they allow (1 to 2048 tokens; the fit's error is 6 % in the root mean
-// square, and what it chooses is at most 5 % slower than the fastest measured):
+// The tile and the cluster with the least time by a model in SM clocks (at 1.9 GHz).  Its terms are fitted to measured times
+// under every tile and cluster that a size allows (190 of 17 sizes, the join's again to 258 of 22, 16 to 2048 tokens; the
+// errors' root mean square is 6 and 9 %).  What it chooses of the 258 is in the mean 0.5 % slower than the fastest, 10 % at
+// worst (40 tokens of 2 x 2048 x 2048: 9.95 us, 9.03 in clusters of four):
 //   a call costs 9700 whatever it does, its tokens' kernel included, and 40 for each token of a tile;
 //   an SM takes 57 bytes a clock from L2, all SMs together 3200 out of HBM, to which token tiles that run together add little;
 //   a stage takes 6.8 for each token in one CTA, 5.6 in a pair, and never less than 470 (600), which its barriers take;
 //   filling the ring 1600 a tile; the epilogue 48 for each token and round (with w_mul 13 more a token), under the next
-//   tile's products; joining a cluster's sums 4200 and 68 for each token.
+//   tile's products; joining a cluster's sums 3000 and 28 for each token.
 inline Int8Plan make_int8_plan(int M, int N, int K, bool gated, int sms, int room) {
   const int feats = gated ? 64 : 128, KC = (K + kI8Chunk - 1) / kI8Chunk;
   Int8Plan best;
@@ -76,7 +77,7 @@ inline Int8Plan make_int8_plan(int M, int N, int K, bool gated, int sms, int roo
           if (stage_t < least) stage_t = least;
         const int share = (KC + S - 1) / S;
         const double tile = share * stage_t + 1600, epi = l.NT * (48.0 * ((share + kI8Round - 1) / kI8Round) + (gated ? 13 : 0));
-        const double t = waves * (tile > epi ? tile : epi) + 40.0 * l.NT + (S > 1 ? 4200 + 68.0 * l.NT : 0);
+        const double t = waves * (tile > epi ? tile : epi) + 40.0 * l.NT + (S > 1 ? 3000 + 28.0 * l.NT : 0);
         if (t < best_t) {
           best_t = t;
           best = l;
