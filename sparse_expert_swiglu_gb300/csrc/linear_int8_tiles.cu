@@ -696,12 +696,13 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
   }
   __syncwarp();
   tc_before_sync();
-  __syncthreads();
   if (PAIR || SHARED) {
     // no CTA ends while another may store into it or read its stages
     if (!left) cluster_leave();
     cluster_left();
     if (dn_aborted(bars)) dn_settle();  // stores that this CTA did not wait for
+  } else {
+    __syncthreads();
   }
   tc_after_sync();
   if (warp == 2) {
