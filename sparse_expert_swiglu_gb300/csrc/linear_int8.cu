@@ -3,7 +3,10 @@
 // Few tokens: a stream of w, bound by HBM.  A warp takes RW neighbouring rows of w (with w_mul the same rows of both) at a
 // time, 16 bytes a lane and load, the next loads in flight while it multiplies; the tokens lie in shared memory, where every
 // CTA quantises them itself.  Four products and their sum are one instruction (dp4a: 254 products a clock and SM, of which
-// HBM's rate needs 23 for each token); sums are integers, so that their order is free.
+// HBM's rate needs 23 for each token); sums are integers, so that their order is free.  Rows at a time: with one token one row
+// gives the most loads in flight, with more each token's read from shared memory serves RW rows (4 tokens of 4096 x 14336 with
+// 2 rows 15.8 us, with 4 14.7).  Measured: 1 token of 32000 x 4096 25.5 us (5.1 TB/s; about 6 us of that are a call's own:
+// launch, tokens, first bytes), of 4096 x 4096 6.0 us.
 #include "activate.cuh"
 #include "dense.cuh"
 #include "dense_params.cuh"
@@ -199,13 +202,15 @@ Int8Ws::Int8Ws(int M, int K) {
   bytes = scales + up((size_t)M * 4 + 60);
 }
 
-// Whether the stream of w takes the call, and not the tensor cores.  The stream is a single short kernel (512 x 512: 3.4 us
-// for 5 tokens and 4.5 for 16 against 6.3) whose time grows with the tokens: at 8 tokens they meet at 56 MB of weights (4096 x
-// 14336: 18.4 us both; 32000 x 4096: 36.4 us against 27.2, of 4 tokens 29.6), at 9 to 16 sooner (16 of 2048 x 1408: 6.0 us
-// against 9.3, 16 of 4096 x 4096: 13.0 against 12.2, 9 of them: 10.6 against 12.0).
+// Whether the stream of w takes the call, and not the tensor cores.  The stream is a single short kernel (512 x 512: 2.8 us
+// for 4 tokens and 4.3 for 16 against 5.3) whose time grows with tokens times weights, faster where there are more than 4 and
+// more than 8 tokens.  They meet, in us of stream and tensor cores, for up to 4 tokens at about 450e6 of them (4 of 32000 x
+// 4096 27.5 and 27.3, of 14336 x 4096 15.1 and 15.9), up to 8 at 280e6 (8 of 8192 x 4096 11.9 and 12.9, 6 of 4096 x 14336
+// 16.5 both, 5 of 14336 x 4096 17.3 and 15.7), up to 16 at 70e6 (16 of 4096 x 1024 6.1 and 6.7, 9 of 2048 x 8192 10.7 both,
+// 9 of 4096 x 4096 10.4 and 9.3, 16 12.8 and 9.4).
 static bool int8_few(int M, int N, int K, bool gated, int tok) {
   const double work = (gated ? 2.0 : 1.0) * N * K * M;
-  return M == 1 || (M <= tok && tok * K <= kFewShared && (M <= 2 || work <= (M <= 8 ? 450e6 : 160e6)));
+  return M == 1 || (M <= tok && tok * K <= kFewShared && (M <= 2 || work <= (M <= 4 ? 450e6 : M <= 8 ? 280e6 : 70e6)));
 }
 
 cudaError_t launch_linear_int8(const LinearInt8Call& c, void* ws, int sms, int smem_optin, cudaStream_t st) {
