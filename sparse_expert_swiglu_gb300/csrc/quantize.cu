@@ -1,7 +1,9 @@
 // Rows of 8-bit integers with a scale each (int8.cuh says how they are rounded).
 //
 // Bound by HBM: a row is read once and kept in registers, 16 bytes for each load, between the search for its largest value
-// and the rounding.  One row has 32 to 1024 threads of up to 8 loads; rows of up to 32 threads share a CTA.
+// and the rounding.  One row has 32 to 1024 threads of up to 8 loads; rows of up to 32 threads share a CTA.  Measured: 14336 rows
+// of 4096 bf16 32.7 us (176 MB, 5.4 TB/s; 26 us at a copy's rate, where the rounding of a row and the loads of the next
+// would have to overlap more), 48 rows of 14336 fp16 2.4 us (launch, one latency of memory, one barrier).
 #include "int8.cuh"
 #include "int8_params.cuh"
 

@@ -4,7 +4,11 @@
 // Bound by HBM (with few tokens by the latency of its barriers): x and the residual are read once, a CTA keeps a token's
 // row in registers in fp32 through both norms and writes s and y.  Variances are sums of squared differences from the mean, of
 // values in registers.  With more tokens than CTAs fit at once a CTA goes from token to token, and while it works on one, every
-// thread's own parts of the next come into shared memory by asynchronous copies.
+// thread's own parts of the next come into shared memory by asynchronous copies.  Sums are formed in one order whatever the
+// number of tokens: vectors of 8, then 32 neighbouring vectors as a tree, then those sums as a tree.
+//
+// Measured: 8192 tokens of 4096, two LayerNorms and an fp32 residual, 68 us (403 MB, 5.9 TB/s); RMSNorms and 8-bit tokens 64 us
+// (235 MB; the conversions and the rounding, 2.6 instructions a clock and SM, bound it); one token 1.9 us.
 #include "dense_params.cuh"
 #include "int8.cuh"
 #include "int8_params.cuh"
