@@ -136,6 +136,13 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs p) {
     return block_sum<NV>(t, part[turn]);
   };
   auto normed = [&](int kind, const void* weight, const void* bias) {
+    // One vector a thread: its weight and bias are under way while the sums are formed (8192 x 4096 takes two vectors a thread
+    // and has no registers for them: 97 us against 79).
+    uint4 early[2];
+    if constexpr (NV == 1) {
+      if (weight && c0 < n) early[0] = reinterpret_cast<const uint4*>(weight)[c0];
+      if (bias && c0 < n) early[1] = reinterpret_cast<const uint4*>(bias)[c0];
+    }
     if (kind == MOE_NORM_LAYER) {
       float t[NV] = {};
 #pragma unroll
@@ -166,12 +173,12 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs p) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] *= inv;
       if (weight) {
-        unpack8(reinterpret_cast<const uint4*>(weight)[c], p.bf16, w);
+        unpack8(NV == 1 ? early[0] : reinterpret_cast<const uint4*>(weight)[c], p.bf16, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[j][i] *= w[i];
       }
       if (bias) {
-        unpack8(reinterpret_cast<const uint4*>(bias)[c], p.bf16, w);
+        unpack8(NV == 1 ? early[1] : reinterpret_cast<const uint4*>(bias)[c], p.bf16, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[j][i] += w[i];
       }
