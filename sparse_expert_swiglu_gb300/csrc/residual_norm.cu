@@ -96,7 +96,7 @@ __device__ __forceinline__ void copy16(void* to, const void* from) {
 // One token for each CTA at a time, NV vectors of 8 elements for each thread: a warp has 32 NV neighbouring ones, its lanes
 // every 32nd.  AHEAD: the next token's come ahead.
 template <int NV, bool AHEAD>
-__global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs p) {
+__global__ void __launch_bounds__(AHEAD ? 512 : 1024) residual_norm_kernel(const NormArgs p) {
   __shared__ float part[2][64];
   extern __shared__ uint4 next[];  // AHEAD: [NV][x, residual, the residual's second half][thread]
   griddep_launch_dependents();
@@ -314,10 +314,13 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStr
   p.y = op.y;
   p.y_scale = op.y_scale;
   // Copies ahead pay from a few tokens for each CTA on.  With them 2 vectors for each thread (8192 x 4096, LayerNorms and an fp32
-  // residual: 73 us, with 1 81, with 4 79), without them 1, which leaves one token's barriers with the least work between.
+  // residual: 73 us, with 1 81, with 4 79), without them 1, which leaves one token's barriers with the least work between (64 x
+  // 8192, RMSNorm: 3.1 us, with 2 4.3).  An SM holds one CTA of more than 512 threads: where there are more tokens than SMs
+  // each, two smaller ones are faster (300 x 8192: 5.6 us, else 6.7), but for rows that need 2 vectors of 1024 threads (300 x
+  // 16384: 11.0 us, with 4 of 512 13.9).
   const int n = op.d / 8;
   const bool ahead = op.M > 2 * sms;
-  const int nv = n > 1024 ? 4 : n > 512 || ahead ? 2 : 1;
+  const int nv = ahead ? n > 1024 ? 4 : 2 : n > 1024 || (n > 512 && op.M > sms) ? 2 : 1;
   const int T = ((n + nv - 1) / nv + 31) / 32 * 32;
   const int each = op.residual ? p.s_f32 ? 3 : 2 : 1;
   const size_t bytes = ahead ? (size_t)nv * each * T * 16 : 0;
@@ -335,11 +338,10 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStr
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   using Kernel = void (*)(NormArgs);
-  static constexpr Kernel kernels[2][3] = {
-      {residual_norm_kernel<1, false>, residual_norm_kernel<2, false>, residual_norm_kernel<4, false>},
-      {residual_norm_kernel<1, true>, residual_norm_kernel<2, true>, residual_norm_kernel<4, true>}};
-  const int which = nv == 1 ? 0 : nv == 2 ? 1 : 2;
-  static std::atomic<uint64_t> allowed[3];
+  static constexpr Kernel kernels[2][2] = {{residual_norm_kernel<1, false>, residual_norm_kernel<2, false>},
+                                           {residual_norm_kernel<2, true>, residual_norm_kernel<4, true>}};
+  const int which = nv == (ahead ? 4 : 2);
+  static std::atomic<uint64_t> allowed[2];
   if (ahead) {
     const cudaError_t e = allow_shared(kernels[1][which], allowed[which], kNormShared);
     if (e != cudaSuccess) return e;
