@@ -94,8 +94,9 @@ __device__ __forceinline__ void copy16(void* to, const void* from) {
 }
 
 // One token for each CTA at a time, NV vectors of 8 elements for each thread: a warp has 32 NV neighbouring ones, its lanes
-// every 32nd.  AHEAD: the next token's come ahead.
-template <int NV, bool AHEAD>
+// every 32nd.  AHEAD: the next token's come ahead.  BF16: the type.  (Types known to the
+// compiler are 5 to 10 % of a call: 8192 x 4096, LayerNorms with weights, biases and gates, fp32 residual 79.7 -> 71.8 us.)
+template <int NV, bool AHEAD, int BF16>
 __global__ void __launch_bounds__(AHEAD ? 512 : 1024) residual_norm_kernel(const NormArgs p) {
   __shared__ float part[2][64];
   extern __shared__ uint4 next[];  // AHEAD: [NV][x, residual, the residual's second half][thread]
@@ -173,12 +174,12 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) residual_norm_kernel(const
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] *= inv;
       if (weight) {
-        unpack8(NV == 1 ? early[0] : reinterpret_cast<const uint4*>(weight)[c], p.bf16, w);
+        unpack8(NV == 1 ? early[0] : reinterpret_cast<const uint4*>(weight)[c], BF16, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[j][i] *= w[i];
       }
       if (bias) {
-        unpack8(NV == 1 ? early[1] : reinterpret_cast<const uint4*>(bias)[c], p.bf16, w);
+        unpack8(NV == 1 ? early[1] : reinterpret_cast<const uint4*>(bias)[c], BF16, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[j][i] += w[i];
       }
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) residual_norm_kernel(const
       r[j][0] = c < n ? from[p.s_f32 ? 2 * (at + c) : at + c] : zero;
       r[j][1] = c < n && p.s_f32 ? from[2 * (at + c) + 1] : zero;
     }
-    unpack8(t, p.bf16, v[j]);
+    unpack8(t, BF16, v[j]);
   }
   if (AHEAD) {
     // what a thread reads its own warp has copied: no barrier of the CTA
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) residual_norm_kernel(const
       const uint4 zero = make_uint4(0, 0, 0, 0);
       const bool on = c0 + 32 * j < n;
       const uint4* from = next + j * each * T + tid;
-      unpack8(on ? from[0] : zero, p.bf16, v[j]);
+      unpack8(on ? from[0] : zero, BF16, v[j]);
       if (p.residual) {
         r[j][0] = on ? p.s_f32 ? next[(3 * j + 1) * T + 2 * tid] : from[T] : zero;
         r[j][1] = on && p.s_f32 ? next[(3 * j + 1) * T + 2 * tid + 1] : zero;
@@ -219,13 +220,14 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) residual_norm_kernel(const
     ask(token + gridDim.x);
   }
   if (p.post) normed(p.post, p.post_weight, p.post_bias);
+  const uint4* gates = reinterpret_cast<const uint4*>(p.gate) + (p.gate ? (size_t)((unsigned)token / (unsigned)p.gate_every) * n : 0);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = c0 + 32 * j;
     if (c >= n) break;
     float w[8];
     if (p.gate) {
-      unpack8(reinterpret_cast<const uint4*>(p.gate)[row / p.gate_every * n + c], p.bf16, w);
+      unpack8(gates[c], BF16, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] *= w[i];
     }
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) residual_norm_kernel(const
     }
     if (p.residual) {
       if (p.s_f32) unpack8(r[j][0], r[j][1], w);
-      else unpack8(r[j][0], p.bf16, w);
+      else unpack8(r[j][0], BF16, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] = fmaf(p.residual_scale, w[i], v[j][i]);
     }
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) residual_norm_kernel(const
           reinterpret_cast<float4*>(s)[1] = make_float4(v[j][4], v[j][5], v[j][6], v[j][7]);
         }
       } else {
-        reinterpret_cast<uint4*>(p.s)[at + c] = pack8(v[j], p.bf16);
+        reinterpret_cast<uint4*>(p.s)[at + c] = pack8(v[j], BF16);
       }
     }
   }
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) residual_norm_kernel(const
   if (!p.y_int8) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (c0 + 32 * j < n) reinterpret_cast<uint4*>(p.y)[at + c0 + 32 * j] = pack8(v[j], p.bf16);
+      if (c0 + 32 * j < n) reinterpret_cast<uint4*>(p.y)[at + c0 + 32 * j] = pack8(v[j], BF16);
     continue;
   }
   uint32_t m = 0;
@@ -338,15 +340,16 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStr
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   using Kernel = void (*)(NormArgs);
-  static constexpr Kernel kernels[2][2] = {{residual_norm_kernel<1, false>, residual_norm_kernel<2, false>},
-                                           {residual_norm_kernel<2, true>, residual_norm_kernel<4, true>}};
+  static constexpr Kernel kernels[2][2][2] = {
+      {{residual_norm_kernel<1, false, 0>, residual_norm_kernel<2, false, 0>}, {residual_norm_kernel<2, true, 0>, residual_norm_kernel<4, true, 0>}},
+      {{residual_norm_kernel<1, false, 1>, residual_norm_kernel<2, false, 1>}, {residual_norm_kernel<2, true, 1>, residual_norm_kernel<4, true, 1>}}};
   const int which = nv == (ahead ? 4 : 2);
-  static std::atomic<uint64_t> allowed[2];
+  static std::atomic<uint64_t> allowed[4];
   if (ahead) {
-    const cudaError_t e = allow_shared(kernels[1][which], allowed[which], kNormShared);
+    const cudaError_t e = allow_shared(kernels[p.bf16][1][which], allowed[2 * p.bf16 + which], kNormShared);
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, kernels[ahead][which], p);
+  return cudaLaunchKernelEx(&cfg, kernels[p.bf16][ahead][which], p);
 }
 
 }  // namespace sesg
