@@ -2,8 +2,9 @@
 //
 // Bound by HBM: a row is read once and kept in registers, 16 bytes for each load, between the search for its largest value
 // and the rounding.  One row has 32 to 1024 threads of up to 8 loads; rows of up to 32 threads share a CTA.  Measured: 14336 rows
-// of 4096 bf16 32.7 us (176 MB, 5.4 TB/s; 26 us at a copy's rate, where the rounding of a row and the loads of the next
-// would have to overlap more), 48 rows of 14336 fp16 2.4 us (launch, one latency of memory, one barrier).
+// of 4096 bf16 32.6 us (176 MB, 5.4 TB/s; 26 us at a copy's rate, where the rounding of a row and the loads of the next
+// would have to overlap more), 48 rows of 14336 fp16 2.4 us (launch, one latency of memory, one barrier).  Short rows are bound
+// by the CTAs' coming and going (65536 rows of 128: 15 us).
 #include "int8.cuh"
 #include "int8_params.cuh"
 
@@ -25,9 +26,12 @@ __device__ __forceinline__ uint4 widen8(const uint2& q) {
   return r;
 }
 
-// KEEP loads of 16 bytes are kept by a thread; F32: pairs of them (a thread's eight elements).  WIDE: q as fp16 integers.
-template <bool F32, int KEEP, bool WIDE, int MOST>
-__global__ void __launch_bounds__(MOST) quantize_kernel(const void* x, int bf16, int rows, int K, void* q, float* scale) {
+// X: the type.  KEEP loads of 16 bytes are kept by a thread, of fp32 pairs of them (a thread's eight elements).  WIDE: q as fp16
+// integers.
+template <int X, int KEEP, bool WIDE, int MOST>
+__global__ void __launch_bounds__(MOST) quantize_kernel(const void* x, int rows, int K, void* q, float* scale) {
+  constexpr bool F32 = X == MOE_F32;
+  constexpr int bf16 = X == MOE_BF16;
   constexpr int L = F32 ? 2 : 1;  // loads of eight elements
   __shared__ uint32_t part[32];
   // In this order: the product behind the tokens' kernel takes everything before this kernel for done.
@@ -101,6 +105,17 @@ cudaError_t launch(void (*kernel)(Par...), dim3 grid, dim3 block, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, kernel, arg...);
 }
 
+// T threads for each row, which keep 2 loads or KEEP.
+template <int X, int KEEP, bool WIDE>
+cudaError_t launch_row_kernel(const void* x, int rows, int K, void* q, float* scale, int T, cudaStream_t st) {
+  const int R = T == 32 ? 8 : 1;
+  using Kernel = void (*)(const void*, int, int, void*, float*);
+  const Kernel kernel = K / 8 <= 2 * T ? quantize_kernel<X, 2, WIDE, 1024>
+                        : T <= 256     ? quantize_kernel<X, KEEP, WIDE, 256>
+                                       : quantize_kernel<X, KEEP, WIDE, 1024>;
+  return launch(kernel, dim3((unsigned)(((size_t)rows + R - 1) / R)), dim3(T, R), st, x, rows, K, q, scale);
+}
+
 template <bool WIDE>
 cudaError_t launch_rows(const void* x, int dtype, int rows, int K, void* q, float* scale, cudaStream_t st) {
   const int n = K / 8;
@@ -109,15 +124,9 @@ cudaError_t launch_rows(const void* x, int dtype, int rows, int K, void* q, floa
   const int keep = rows <= 2 * 152 ? 2 : (dtype == MOE_F32 ? 4 : 8);
   int T = 32;
   while (T < 1024 && T * keep < n) T *= 2;
-  const int R = T == 32 ? 8 : 1;
-  using Kernel = void (*)(const void*, int, int, int, void*, float*);
-  const Kernel kernel =
-      dtype == MOE_F32 ? (n <= 2 * T ? quantize_kernel<true, 2, WIDE, 1024>
-                                     : T <= 256 ? quantize_kernel<true, 4, WIDE, 256> : quantize_kernel<true, 4, WIDE, 1024>)
-                       : (n <= 2 * T ? quantize_kernel<false, 2, WIDE, 1024>
-                                     : T <= 256 ? quantize_kernel<false, 8, WIDE, 256> : quantize_kernel<false, 8, WIDE, 1024>);
-  return launch(kernel, dim3((unsigned)(((size_t)rows + R - 1) / R)), dim3(T, R), st, x, (int)(dtype == MOE_BF16), rows, K, q,
-                scale);
+  return dtype == MOE_F32    ? launch_row_kernel<MOE_F32, 4, WIDE>(x, rows, K, q, scale, T, st)
+         : dtype == MOE_BF16 ? launch_row_kernel<MOE_BF16, 8, WIDE>(x, rows, K, q, scale, T, st)
+                             : launch_row_kernel<MOE_F16, 8, WIDE>(x, rows, K, q, scale, T, st);
 }
 
 }  // namespace

@@ -7,8 +7,9 @@
 // thread's own parts of the next come into shared memory by asynchronous copies.  Sums are formed in one order whatever the
 // number of tokens: vectors of 8, then 32 neighbouring vectors as a tree, then those sums as a tree.
 //
-// Measured: 8192 tokens of 4096, two LayerNorms and an fp32 residual, 68 us (403 MB, 5.9 TB/s); RMSNorms and 8-bit tokens 64 us
-// (235 MB; the conversions and the rounding, 2.6 instructions a clock and SM, bound it); one token 1.9 us.
+// Measured: 8192 tokens of 4096, two LayerNorms and an fp32 residual, 69 us (403 MB, 5.8 TB/s), with weights, biases and gates
+// 72; RMSNorms and 8-bit tokens 57 us (235 MB; the conversions and the rounding bound it); one token 1.6 us, 64 of 6144 to 8 bits
+// 3.9 us: launch, one latency of memory, a barrier for each sum.
 #include "dense_params.cuh"
 #include "int8.cuh"
 #include "int8_params.cuh"
@@ -94,17 +95,17 @@ __device__ __forceinline__ void copy16(void* to, const void* from) {
 }
 
 // One token for each CTA at a time, NV vectors of 8 elements for each thread: a warp has 32 NV neighbouring ones, its lanes
-// every 32nd.  AHEAD: the next token's come ahead.  BF16: the type.  (Types known to the
-// compiler are 5 to 10 % of a call: 8192 x 4096, LayerNorms with weights, biases and gates, fp32 residual 79.7 -> 71.8 us.)
-template <int NV, bool AHEAD, int BF16>
-__global__ void __launch_bounds__(AHEAD ? 512 : 1024) residual_norm_kernel(const NormArgs p) {
+// every 32nd.  AHEAD: the next token's come ahead.  BF16, S32: the types, known to the compiler (else 5 to 15 % more: 8192 x
+// 4096, RMSNorms to 8 bits 64 us for 57).  With 64 registers a thread an SM holds 1024 threads.
+template <int NV, bool AHEAD, int BF16, bool S32>
+__global__ void __launch_bounds__(AHEAD ? 512 : 1024, AHEAD && NV == 2 ? 2 : 1) residual_norm_kernel(const NormArgs p) {
   __shared__ float part[2][64];
   extern __shared__ uint4 next[];  // AHEAD: [NV][x, residual, the residual's second half][thread]
   griddep_launch_dependents();
   griddep_wait();
   const int T = blockDim.x, tid = threadIdx.x, n = p.d / 8, lane = tid & 31;
   const int c0 = (tid >> 5) * 32 * NV + lane;  // this thread's first vector
-  const int each = p.residual ? p.s_f32 ? 3 : 2 : 1;  // vectors of 16 bytes
+  const int each = p.residual ? S32 ? 3 : 2 : 1;  // vectors of 16 bytes
   auto ask = [&](int token) {
     const size_t at = (size_t)token * n;
 #pragma unroll
@@ -114,9 +115,9 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) residual_norm_kernel(const
       uint4* to = next + j * each * T + tid;
       copy16(to, reinterpret_cast<const uint4*>(p.x) + at + c);
       const uint4* from = reinterpret_cast<const uint4*>(p.residual);
-      if (p.residual && !p.s_f32) copy16(to + T, from + at + c);
+      if (p.residual && !S32) copy16(to + T, from + at + c);
     }
-    if (p.s_f32 && p.residual) {
+    if (S32 && p.residual) {
       // 32 bytes of a thread: a warp copies its 1024 in their order, whole sectors at a time
 #pragma unroll
       for (int j = 0; j < NV; ++j)
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) residual_norm_kernel(const
   };
   auto normed = [&](int kind, const void* weight, const void* bias) {
     // One vector a thread: its weight and bias are under way while the sums are formed (8192 x 4096 takes two vectors a thread
-    // and has no registers for them: 97 us against 79).
+    // and has no registers for them: 97 us for 79 with all vectors).
     uint4 early[2];
     if constexpr (NV == 1) {
       if (weight && c0 < n) early[0] = reinterpret_cast<const uint4*>(weight)[c0];
@@ -196,8 +197,8 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) residual_norm_kernel(const
     const uint4 t = c < n ? reinterpret_cast<const uint4*>(p.x)[at + c] : zero;
     if (p.residual) {
       const uint4* from = reinterpret_cast<const uint4*>(p.residual);
-      r[j][0] = c < n ? from[p.s_f32 ? 2 * (at + c) : at + c] : zero;
-      r[j][1] = c < n && p.s_f32 ? from[2 * (at + c) + 1] : zero;
+      r[j][0] = c < n ? from[S32 ? 2 * (at + c) : at + c] : zero;
+      r[j][1] = c < n && S32 ? from[2 * (at + c) + 1] : zero;
     }
     unpack8(t, BF16, v[j]);
   }
@@ -212,8 +213,8 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) residual_norm_kernel(const
       const uint4* from = next + j * each * T + tid;
       unpack8(on ? from[0] : zero, BF16, v[j]);
       if (p.residual) {
-        r[j][0] = on ? p.s_f32 ? next[(3 * j + 1) * T + 2 * tid] : from[T] : zero;
-        r[j][1] = on && p.s_f32 ? next[(3 * j + 1) * T + 2 * tid + 1] : zero;
+        r[j][0] = on ? S32 ? next[(3 * j + 1) * T + 2 * tid] : from[T] : zero;
+        r[j][1] = on && S32 ? next[(3 * j + 1) * T + 2 * tid + 1] : zero;
       }
     }
     __syncwarp();
@@ -236,13 +237,13 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) residual_norm_kernel(const
       for (int i = 0; i < 8; ++i) v[j][i] *= p.block_scale;
     }
     if (p.residual) {
-      if (p.s_f32) unpack8(r[j][0], r[j][1], w);
+      if (S32) unpack8(r[j][0], r[j][1], w);
       else unpack8(r[j][0], BF16, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] = fmaf(p.residual_scale, w[i], v[j][i]);
     }
     if (p.s) {
-      if (p.s_f32) {
+      if (S32) {
         float* s = reinterpret_cast<float*>(p.s) + 8 * (at + c);
         if (p.sectors) {
           asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(s), "f"(v[j][0]), "f"(v[j][1]),
@@ -316,7 +317,7 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStr
   p.y = op.y;
   p.y_scale = op.y_scale;
   // Copies ahead pay from a few tokens for each CTA on.  With them 2 vectors for each thread (8192 x 4096, LayerNorms and an fp32
-  // residual: 73 us, with 1 81, with 4 79), without them 1, which leaves one token's barriers with the least work between (64 x
+  // residual, when all were timed: 73 us, with 1 81, with 4 79), without them 1, which leaves one token's barriers with the least work between (64 x
   // 8192, RMSNorm: 3.1 us, with 2 4.3).  An SM holds one CTA of more than 512 threads: where there are more tokens than SMs
   // each, two smaller ones are faster (300 x 8192: 5.6 us, else 6.7), but for rows that need 2 vectors of 1024 threads (300 x
   // 16384: 11.0 us, with 4 of 512 13.9).
@@ -340,16 +341,22 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStr
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   using Kernel = void (*)(NormArgs);
-  static constexpr Kernel kernels[2][2][2] = {
-      {{residual_norm_kernel<1, false, 0>, residual_norm_kernel<2, false, 0>}, {residual_norm_kernel<2, true, 0>, residual_norm_kernel<4, true, 0>}},
-      {{residual_norm_kernel<1, false, 1>, residual_norm_kernel<2, false, 1>}, {residual_norm_kernel<2, true, 1>, residual_norm_kernel<4, true, 1>}}};
-  const int which = nv == (ahead ? 4 : 2);
-  static std::atomic<uint64_t> allowed[4];
+  static constexpr Kernel kernels[4][2][2] = {
+      {{residual_norm_kernel<1, false, 0, false>, residual_norm_kernel<2, false, 0, false>},
+       {residual_norm_kernel<2, true, 0, false>, residual_norm_kernel<4, true, 0, false>}},
+      {{residual_norm_kernel<1, false, 0, true>, residual_norm_kernel<2, false, 0, true>},
+       {residual_norm_kernel<2, true, 0, true>, residual_norm_kernel<4, true, 0, true>}},
+      {{residual_norm_kernel<1, false, 1, false>, residual_norm_kernel<2, false, 1, false>},
+       {residual_norm_kernel<2, true, 1, false>, residual_norm_kernel<4, true, 1, false>}},
+      {{residual_norm_kernel<1, false, 1, true>, residual_norm_kernel<2, false, 1, true>},
+       {residual_norm_kernel<2, true, 1, true>, residual_norm_kernel<4, true, 1, true>}}};
+  const int types = 2 * p.bf16 + p.s_f32, which = nv == (ahead ? 4 : 2);
+  static std::atomic<uint64_t> allowed[8];
   if (ahead) {
-    const cudaError_t e = allow_shared(kernels[p.bf16][1][which], allowed[2 * p.bf16 + which], kNormShared);
+    const cudaError_t e = allow_shared(kernels[types][1][which], allowed[2 * types + which], kNormShared);
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, kernels[p.bf16][ahead][which], p);
+  return cudaLaunchKernelEx(&cfg, kernels[types][ahead][which], p);
 }
 
 }  // namespace sesg
