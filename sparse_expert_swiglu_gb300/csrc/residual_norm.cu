@@ -328,7 +328,8 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStr
   const int each = op.residual ? p.s_f32 ? 3 : 2 : 1;
   const size_t bytes = ahead ? (size_t)nv * each * T * 16 : 0;
   // CTAs that fit an SM at once, by threads and shared memory
-  int fit = 1024 / T < 24 ? 1024 / T : 24;
+  const int room = nv == 4 ? 512 : 1024;  // by registers
+  int fit = room / T < 24 ? room / T : 24;
   if (bytes && fit > (int)(kNormShared / (bytes + 1536))) fit = (int)(kNormShared / (bytes + 1536));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ahead && op.M > fit * sms ? fit * sms : op.M);
