@@ -46,31 +46,16 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8], int bf16) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Sums of 32 neighbouring vectors, one of each lane, for NV of them at once; lane 32 / NV * j has the j-th.  What a lane adds
-// are the same two numbers at every step, whatever NV is.
+// Sums of 32 neighbouring vectors, one of each lane, or of two such groups at once: lanes from 16 on have the second.  What a
+// lane adds are the same two numbers at every step, whatever NV is.
 template <int NV>
 __device__ __forceinline__ float warp_sums(const float (&t)[NV], int lane) {
-  float v = t[0];
-  if constexpr (NV == 1) {
-    v += __shfl_xor_sync(0xffffffffu, v, 16);
-  } else {
-    // lanes keep one of two sums and give the other half's lanes what they add to theirs
-    float h[NV / 2];
-    const bool high = lane & 16;
+  // (with two, a lane keeps one and gives the other half's lanes what they add to theirs)
+  const bool high = NV == 2 && (lane & 16);
+  const float keep = high ? t[NV - 1] : t[0], give = NV == 1 ? keep : high ? t[0] : t[NV - 1];
+  float v = keep + __shfl_xor_sync(0xffffffffu, give, 16);
 #pragma unroll
-    for (int j = 0; j < NV / 2; ++j) {
-      const float keep = high ? t[j + NV / 2] : t[j], give = high ? t[j] : t[j + NV / 2];
-      h[j] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
-    }
-    v = h[0];
-    if constexpr (NV == 4) {
-      const bool odd = lane & 8;
-      const float keep = odd ? h[1] : h[0], give = odd ? h[0] : h[1];
-      v = keep + __shfl_xor_sync(0xffffffffu, give, 8);
-    }
-  }
-#pragma unroll
-  for (int o = NV == 4 ? 4 : 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
@@ -98,7 +83,7 @@ __device__ __forceinline__ void copy16(void* to, const void* from) {
 // every 32nd.  AHEAD: the next token's come ahead.  BF16, S32: the types, known to the compiler (else 5 to 15 % more: 8192 x
 // 4096, RMSNorms to 8 bits 64 us for 57).  With 64 registers a thread an SM holds 1024 threads.
 template <int NV, bool AHEAD, int BF16, bool S32>
-__global__ void __launch_bounds__(AHEAD ? 512 : 1024, AHEAD && NV == 2 ? 2 : 1) residual_norm_kernel(const NormArgs p) {
+__global__ void __launch_bounds__(1024) residual_norm_kernel(const NormArgs p) {
   __shared__ float part[2][64];
   extern __shared__ uint4 next[];  // AHEAD: [NV][x, residual, the residual's second half][thread]
   griddep_launch_dependents();
@@ -317,19 +302,18 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStr
   p.y = op.y;
   p.y_scale = op.y_scale;
   // Copies ahead pay from a few tokens for each CTA on.  With them 2 vectors for each thread (8192 x 4096, LayerNorms and an fp32
-  // residual, when all were timed: 73 us, with 1 81, with 4 79), without them 1, which leaves one token's barriers with the least work between (64 x
+  // residual, when all were timed: 73 us, with 1 81, with 4 79; 1000 x 8208 13.9 us, with 4 15.0), without them 1, which leaves one token's barriers with the least work between (64 x
   // 8192, RMSNorm: 3.1 us, with 2 4.3).  An SM holds one CTA of more than 512 threads: where there are more tokens than SMs
   // each, two smaller ones are faster (300 x 8192: 5.6 us, else 6.7), but for rows that need 2 vectors of 1024 threads (300 x
   // 16384: 11.0 us, with 4 of 512 13.9).
   const int n = op.d / 8;
   const bool ahead = op.M > 2 * sms;
-  const int nv = ahead ? n > 1024 ? 4 : 2 : n > 1024 || (n > 512 && op.M > sms) ? 2 : 1;
+  const int nv = ahead || n > 1024 || (n > 512 && op.M > sms) ? 2 : 1;
   const int T = ((n + nv - 1) / nv + 31) / 32 * 32;
   const int each = op.residual ? p.s_f32 ? 3 : 2 : 1;
   const size_t bytes = ahead ? (size_t)nv * each * T * 16 : 0;
   // CTAs that fit an SM at once, by threads and shared memory
-  const int room = nv == 4 ? 512 : 1024;  // by registers
-  int fit = room / T < 24 ? room / T : 24;
+  int fit = 1024 / T < 24 ? 1024 / T : 24;
   if (bytes && fit > (int)(kNormShared / (bytes + 1536))) fit = (int)(kNormShared / (bytes + 1536));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ahead && op.M > fit * sms ? fit * sms : op.M);
@@ -342,22 +326,19 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStr
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   using Kernel = void (*)(NormArgs);
-  static constexpr Kernel kernels[4][2][2] = {
-      {{residual_norm_kernel<1, false, 0, false>, residual_norm_kernel<2, false, 0, false>},
-       {residual_norm_kernel<2, true, 0, false>, residual_norm_kernel<4, true, 0, false>}},
-      {{residual_norm_kernel<1, false, 0, true>, residual_norm_kernel<2, false, 0, true>},
-       {residual_norm_kernel<2, true, 0, true>, residual_norm_kernel<4, true, 0, true>}},
-      {{residual_norm_kernel<1, false, 1, false>, residual_norm_kernel<2, false, 1, false>},
-       {residual_norm_kernel<2, true, 1, false>, residual_norm_kernel<4, true, 1, false>}},
-      {{residual_norm_kernel<1, false, 1, true>, residual_norm_kernel<2, false, 1, true>},
-       {residual_norm_kernel<2, true, 1, true>, residual_norm_kernel<4, true, 1, true>}}};
-  const int types = 2 * p.bf16 + p.s_f32, which = nv == (ahead ? 4 : 2);
-  static std::atomic<uint64_t> allowed[8];
+  static constexpr Kernel kernels[4][3] = {
+      {residual_norm_kernel<1, false, 0, false>, residual_norm_kernel<2, false, 0, false>, residual_norm_kernel<2, true, 0, false>},
+      {residual_norm_kernel<1, false, 0, true>, residual_norm_kernel<2, false, 0, true>, residual_norm_kernel<2, true, 0, true>},
+      {residual_norm_kernel<1, false, 1, false>, residual_norm_kernel<2, false, 1, false>, residual_norm_kernel<2, true, 1, false>},
+      {residual_norm_kernel<1, false, 1, true>, residual_norm_kernel<2, false, 1, true>, residual_norm_kernel<2, true, 1, true>}};
+  const int types = 2 * p.bf16 + p.s_f32;
+  const Kernel kernel = kernels[types][ahead ? 2 : nv - 1];
+  static std::atomic<uint64_t> allowed[4];
   if (ahead) {
-    const cudaError_t e = allow_shared(kernels[types][1][which], allowed[2 * types + which], kNormShared);
+    const cudaError_t e = allow_shared(kernel, allowed[types], kNormShared);
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, kernels[types][ahead][which], p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace sesg
