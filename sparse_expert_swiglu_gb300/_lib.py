@@ -907,6 +907,8 @@ def quantize_int8(x: torch.Tensor, out: Optional[torch.Tensor] = None, out_scale
     else:
         lead, K, strides = shape[:-1], shape[-1], x.stride()
         rows, lead_strides = x.shape[:-1].numel(), tuple(v // max(K, 1) for v in strides[:-1])
+    if rows > 0x7FFFFFFF or K > 0x7FFFFFFF:  # (ctypes would cut them off)
+        raise ValueError("sizes outside the supported range")
     q, qp = _dense_out(out, shape, strides, torch.int8, device, "out")
     scale, sp = _dense_out(out_scale, lead, lead_strides, torch.float32, device, "out_scale")
     status = (_LIB or lib()).moe_quantize_int8(x.data_ptr(), code, rows, K, qp, sp, _stream_of(device))
@@ -1035,6 +1037,8 @@ def expert_int8_swiglu(x: torch.Tensor, experts: Int8Experts, expert: int, x_sca
     shape = (n, d)
     if x.shape[1] != d:
         raise ValueError(f"x must have shape {shape}, got {tuple(x.shape)}")
+    if n > 0x7FFFFFFF or not 0 <= expert < experts.E:  # (ctypes would cut them off)
+        raise ValueError(f"{n} tokens of expert {expert}: outside the supported range")
     rp = None if residual is None else _dense_in(residual, dt, device, shape, "residual")
     y, yp = _dense_out(out, shape, (d, 1), dt, device, "out")
     if n == 0:

@@ -4,6 +4,7 @@ References and tolerances are those of the operators' own tests; where two ways 
 
 from __future__ import annotations
 
+import struct
 import threading
 
 import pytest
@@ -282,3 +283,59 @@ def test_one_tensor_for_several_arguments():
         _within(y, ref, bound, BF16)
         got = ses.expert_int8_swiglu(xd, ex, 0, residual=xd, out=xd)  # tokens, residual and output in one
         assert got is xd and torch.equal(got, y)
+
+
+@gpu
+def test_shapes_beyond_the_ranges():
+    """Sizes that do not fit 32 bits are refused, not cut off; vectors and empty tensors are rows too."""
+    x = torch.empty(1 << 32, 16, dtype=torch.int8, device="cuda")  # (not read)
+    with pytest.raises(ValueError):
+        ses.quantize_int8(x.view(F16).view(1 << 31, 16))
+    ex = ses.Int8Experts(*(t.cuda() for t in _expert_case(1, 16, 32, F16)["w"]))
+    ws = ses.Workspace(1 << 20)
+    scale = torch.empty(1, device="cuda").expand(1 << 32)  # refused as well: not dense
+    for n, xs in ((1 << 32, None), (1 << 31, scale)):
+        with pytest.raises(ValueError):
+            ses.expert_int8_swiglu(x[:n], ex, 0, x_scale=xs, dtype=F16, ws=ws)
+    del x
+    torch.cuda.empty_cache()
+    x = torch.empty((1 << 31) + 8, 16, dtype=F16, device="cuda")
+    with pytest.raises(ValueError):
+        ses.expert_int8_swiglu(x, ex, 0, ws=ws, out=x)
+    with pytest.raises((ValueError, struct.error)):
+        ses.linear_int8(x, *ses.quantize_int8(x[:16].zero_()), ws=ws, out=x)
+    del x
+    torch.cuda.empty_cache()
+    few = torch.randn(3, 16, device="cuda").to(F16)
+    for expert in (-1, 3, 1 << 32, -(1 << 32)):
+        with pytest.raises(ValueError):
+            ses.expert_int8_swiglu(few, ex, expert, ws=ws)
+    v = torch.randn(48)
+    q, scale = ses.quantize_int8(v.cuda())
+    want, ws64 = _rows64(v)
+    assert q.shape == (48,) and scale.shape == () and torch.equal(q.cpu().double(), want) and float(scale) == float(ws64)
+    for shape in ((0, 16), (2, 0, 16), (0, 5, 16)):
+        q, scale = ses.quantize_int8(torch.empty(shape, device="cuda"))
+        assert q.shape == shape and scale.shape == shape[:-1]
+    v = torch.randn(1, 32).expand(1, 1, 32)
+    q, scale = ses.quantize_int8(v.cuda().expand(1, 1, 32))
+    assert q.shape == (1, 1, 32) and scale.shape == (1, 1) and torch.equal(q.cpu().double()[0], _rows64(v[0])[0])
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K,gated,calls", [(16, 4096, 4096, False, 10000), (64, 1024, 8192, False, 10000),
+                                               (24, 512, 4096, True, 10000), (300, 4096, 14336, False, 5000),
+                                               (130, 384, 2064, True, 10000)])
+def test_clusters_many_calls_in_a_row(M, N, K, gated, calls):
+    """Sizes whose tiles clusters share: thousands of calls end by themselves, and every thousandth result is the first."""
+    c = _linear_case(M, N, K, BF16, "int8", "silu" if gated else "none", gated=gated, residual=True, out=F32)
+    a = {k: _cuda(v) for k, v in c.items()}
+    ws = ses.Workspace(ses.linear_int8_workspace_bytes(M, N, K, gated))
+    first, out = _linear_check(c, ws=ws), torch.empty(M, N, device="cuda")
+    kw = {k: v for k, v in a.items() if k not in ("x", "w", "w_scale")}
+    for i in range(calls):
+        ses.linear_int8(a["x"], a["w"], a["w_scale"], out=out, ws=ws, **kw)
+        if i % 1000 == 999:
+            assert torch.equal(out, first), i
+            out.zero_()
+    assert ws.status() == 0
