@@ -1,14 +1,14 @@
 // The products of linear_int8.cu for more than a few tokens, on the tensor cores.
 //
-// Sums are exact integers: the operands are integers of at most 8 bits, which fp16 holds, their products have at most 14
-// bits and 1024 of them less than 24, which an fp32 accumulator holds.  (This chip's tensor cores have next to no
+// Sums are exact integers: the operands are integers of 8 bits, which fp16 holds, their products are no larger than 2^14 and
+// 1024 of them than 2^24, up to which an fp32 accumulator holds every integer.  (This chip's tensor cores have next to no
 // rate for 8-bit integers: mma.sync takes as long as dp4a.)  So a tile's k goes in rounds of 1024; two sets of accumulators take
 // turns, and the epilogue's warps add the rounds up as 32-bit integers in registers under the next round's products.
 //
-// The features lie on the 128 TMEM lanes (with w_mul 64 of each matrix), the tokens on the columns.  w comes from HBM in 8 bits; eight warps turn 64 k of
-// 128 rows at a time into fp16 on the way from shared memory to TMEM, where the products read them as operand A: the
-// conversion costs shared memory one read of a byte a weight, and no second copy of w exists anywhere.  (In shared memory the
-// fp16 tile would be written and read again, 6 bytes a weight.)  The tokens, few beside w or used by many tiles, have been made
+// The features lie on the 128 TMEM lanes (with w_mul 64 of each matrix), the tokens on the columns.  w comes from HBM in 8 bits;
+// eight warps turn 64 k of 128 rows at a time into fp16 on the way from shared memory to TMEM, where the products read them as
+// operand A: the conversion costs shared memory one read of a byte a weight, and no second copy of w exists anywhere.  (In shared
+// memory the fp16 tile would be written and read again, 6 bytes a weight.)  The tokens, few beside w or used by many tiles, have been made
 // fp16 integers by the kernel before (quantize.cu).  w's copies start before that kernel is done.
 //
 // Where there are fewer tiles than SMs, a cluster's CTAs share a tile along k and join their sums in shared memory; with many
@@ -33,7 +33,7 @@ namespace sesg {
 namespace {
 
 struct TileArgs {
-  int M, N, gated, bf16, act, out_f32;
+  int M, N, bf16, act, out_f32;
   int MT, NT, T, KC, S;
   int rows;                // features of a CTA's tile: up to 128, with w_mul 64
   int stages, slots;
@@ -516,7 +516,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
   } else {
     // Lanes 32 (warp % 4) ... are this warp's.  Of the two warps that have them, each takes every other 16 tokens.
     if constexpr (TB >= 4) more_registers<144>();
-    const int q = warp & 3, half = (warp - 12) >> 2, etid = tid - 384;
+    const int q = warp & 3, half = (warp - 12) >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     int buf = 0;
     uint32_t tph = 0;
@@ -540,7 +540,9 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
       }
       // Where a cluster's sums go: those of even and of odd groups of 4 tokens.
       const int ring_bytes = ns * (int)stage_bytes;
-      auto place = [&](int r) { return ((p.KC * (r + 1) >> log_s) - (p.KC * r >> log_s)) % ns * (int)stage_bytes; };  // CTA r's begin
+      auto place = [&](int r) {  // CTA r's begin
+        return ((p.KC * (r + 1) >> log_s) - (p.KC * r >> log_s)) % ns * (int)stage_bytes;
+      };
       auto wrap = [&](int at) { return at < ring_bytes ? at : at - ring_bytes; };
       int to[2] = {0, 0}, cta[2] = {0, 0}, from = 0;
       if constexpr (SHARED) {
@@ -633,7 +635,8 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
           float v[8], m[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float a = int8_value(acc[0][j], xs[j], f.scale, f.bias), b = int8_value(acc[0][8 + j], xs[8 + j], f.scale, f.bias);
+            const float a = int8_value(acc[0][j], xs[j], f.scale, f.bias);
+            const float b = int8_value(acc[0][8 + j], xs[8 + j], f.scale, f.bias);
             v[j] = mul ? b : a;
             give[32 * j] = mul ? a : b;
           }
@@ -663,8 +666,8 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
 #pragma unroll
           for (int h = 0; h < 4; ++h)
             if (n0 + 4 * h < nt)
-              peer_store(peer_addr(ring_at + wrap(to[h & 1] + (((n0 >> 5) * 4 + h) >> cells.odd) * 512), cta[h & 1]), &acc[0][4 * h],
-                         peer_addr(smem_addr(&bars->xfull), cta[h & 1]));
+              peer_store(peer_addr(ring_at + wrap(to[h & 1] + (((n0 >> 5) * 4 + h) >> cells.odd) * 512), cta[h & 1]),
+                         &acc[0][4 * h], peer_addr(smem_addr(&bars->xfull), cta[h & 1]));
           turn_blocks(std::integral_constant<int, 16>());
         }
         ok = cluster_wait(&bars->xfull, 0, bars);
@@ -686,7 +689,8 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
             const Feature fm(p, m, feat, true);
             int a[4] = {0, 0, 0, 0};
             for (int s = 0; s < S; ++s) {
-              const int4 x = *reinterpret_cast<const int4*>(ring + wrap(from + ((s * (GATED ? 2 : 1) + m) * cells.count + cell) * 512));
+              const int at_s = wrap(from + ((s * (GATED ? 2 : 1) + m) * cells.count + cell) * 512);
+              const int4 x = *reinterpret_cast<const int4*>(ring + at_s);
               a[0] += x.x;
               a[1] += x.y;
               a[2] += x.z;
@@ -736,7 +740,6 @@ cudaError_t launch_int8_tiles(const LinearInt8Call& c, const void* tokens, const
   TileArgs p;
   p.M = c.M;
   p.N = c.N;
-  p.gated = gated;
   p.bf16 = c.bf16;
   p.act = c.act;
   p.out_f32 = c.out_f32;
@@ -761,10 +764,14 @@ cudaError_t launch_int8_tiles(const LinearInt8Call& c, const void* tokens, const
   p.missing = c.tries > 0;
   using Kernel = decltype(&int8_tile_kernel<false, false, false, 1, 2>);
   static constexpr Kernel kernels[32] = {
-      int8_tile_kernel<false, false, false, 1, 2>, int8_tile_kernel<false, false, false, 2, 2>, int8_tile_kernel<false, false, false, 4, 2>, int8_tile_kernel<false, false, false, 6, 1>,
-      int8_tile_kernel<false, false, true, 1, 2>, int8_tile_kernel<false, false, true, 2, 2>, int8_tile_kernel<false, false, true, 4, 2>, int8_tile_kernel<false, false, true, 6, 1>,
-      int8_tile_kernel<false, true, false, 1, 2>, int8_tile_kernel<false, true, false, 2, 2>, int8_tile_kernel<false, true, false, 4, 2>, int8_tile_kernel<false, true, false, 6, 1>,
-      int8_tile_kernel<false, true, true, 1, 2>, int8_tile_kernel<false, true, true, 2, 2>, int8_tile_kernel<false, true, true, 4, 2>, int8_tile_kernel<false, true, true, 6, 1>,
+      int8_tile_kernel<false, false, false, 1, 2>, int8_tile_kernel<false, false, false, 2, 2>,
+      int8_tile_kernel<false, false, false, 4, 2>, int8_tile_kernel<false, false, false, 6, 1>,
+      int8_tile_kernel<false, false, true, 1, 2>, int8_tile_kernel<false, false, true, 2, 2>,
+      int8_tile_kernel<false, false, true, 4, 2>, int8_tile_kernel<false, false, true, 6, 1>,
+      int8_tile_kernel<false, true, false, 1, 2>, int8_tile_kernel<false, true, false, 2, 2>,
+      int8_tile_kernel<false, true, false, 4, 2>, int8_tile_kernel<false, true, false, 6, 1>,
+      int8_tile_kernel<false, true, true, 1, 2>, int8_tile_kernel<false, true, true, 2, 2>,
+      int8_tile_kernel<false, true, true, 4, 2>, int8_tile_kernel<false, true, true, 6, 1>,
       nullptr, nullptr, int8_tile_kernel<true, false, false, 4, 2>, int8_tile_kernel<true, false, false, 6, 1>,
       nullptr, nullptr, int8_tile_kernel<true, false, true, 4, 2>, int8_tile_kernel<true, false, true, 6, 1>,
       nullptr, nullptr, int8_tile_kernel<true, true, false, 4, 2>, int8_tile_kernel<true, true, false, 6, 1>,

@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const NormArgs p) {
     ask(token + gridDim.x);
   }
   if (p.post) normed(p.post, p.post_weight, p.post_bias);
-  const uint4* gates = reinterpret_cast<const uint4*>(p.gate) + (p.gate ? (size_t)((unsigned)token / (unsigned)p.gate_every) * n : 0);
+  const size_t gate_at = p.gate ? (size_t)((unsigned)token / (unsigned)p.gate_every) * n : 0;
+  const uint4* gates = reinterpret_cast<const uint4*>(p.gate) + gate_at;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = c0 + 32 * j;
@@ -302,10 +303,10 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStr
   p.y = op.y;
   p.y_scale = op.y_scale;
   // Copies ahead pay from a few tokens for each CTA on.  With them 2 vectors for each thread (8192 x 4096, LayerNorms and an fp32
-  // residual, when all were timed: 73 us, with 1 81, with 4 79; 1000 x 8208 13.9 us, with 4 15.0), without them 1, which leaves one token's barriers with the least work between (64 x
-  // 8192, RMSNorm: 3.1 us, with 2 4.3).  An SM holds one CTA of more than 512 threads: where there are more tokens than SMs
-  // each, two smaller ones are faster (300 x 8192: 5.6 us, else 6.7), but for rows that need 2 vectors of 1024 threads (300 x
-  // 16384: 11.0 us, with 4 of 512 13.9).
+  // residual, when all were timed: 73 us, with 1 81, with 4 79; 1000 x 8208 13.9 us, with 4 15.0), without them 1, which leaves
+  // one token's barriers with the least work between (64 x 8192, RMSNorm: 3.1 us, with 2 4.3).  An SM holds one CTA of more than
+  // 512 threads: where there are more tokens than SMs, two smaller ones are faster (300 x 8192: 5.6 us, else 6.7), but for rows
+  // that need 2 vectors of 1024 threads (300 x 16384: 11.0 us, with 4 of 512 13.9).
   const int n = op.d / 8;
   const bool ahead = op.M > 2 * sms;
   const int nv = ahead || n > 1024 || (n > 512 && op.M > sms) ? 2 : 1;
