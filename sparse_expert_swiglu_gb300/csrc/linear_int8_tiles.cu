@@ -8,8 +8,8 @@
 // The features lie on the 128 TMEM lanes (with w_mul 64 of each matrix), the tokens on the columns.  w comes from HBM in 8 bits;
 // eight warps turn 64 k of 128 rows at a time into fp16 on the way from shared memory to TMEM, where the products read them as
 // operand A: the conversion costs shared memory one read of a byte a weight, and no second copy of w exists anywhere.  (In shared
-// memory the fp16 tile would be written and read again, 6 bytes a weight.)  The tokens, few beside w or used by many tiles, have been made
-// fp16 integers by the kernel before (quantize.cu).  w's copies start before that kernel is done.
+// memory the fp16 tile would be written and read again, 6 bytes a weight.)  The tokens, few beside w or used by many tiles,
+// have been made fp16 integers by the kernel before (quantize.cu).  w's copies start before that kernel is done.
 //
 // Where there are fewer tiles than SMs, a cluster's CTAs share a tile along k and join their sums in shared memory; with many
 // tokens CTA pairs run one product, so that each fetches half of the tokens.  int8_plan chooses.
