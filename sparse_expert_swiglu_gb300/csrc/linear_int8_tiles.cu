@@ -185,10 +185,11 @@ __device__ __forceinline__ void tile_store(const TileArgs& p, int feat, int tok,
   else tile_write<W, false>(p, at, n, v, r);
 }
 
-// Arrives at a barrier of the pair.  What it orders lies in TMEM, behind tcgen05's own fences; the release over the cluster of
-// peer_arrive would wait 1200 clocks for the thread's other stores.
+// Arrives at a barrier of the pair's first CTA.  What it orders lies in TMEM alone, behind tcgen05's own fences (tokens in shared
+// memory count on a barrier there); the release over the cluster of peer_arrive would wait 1200 clocks for the thread's
+// other stores.
 __device__ __forceinline__ void pair_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // The two halves of cluster_sync_all.
@@ -250,7 +251,6 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
   const int NT = p.NT, toks = NT / P, ns = p.stages;
   const uint32_t tok_bytes = toks * 128, stage_bytes = kW + 2 * tok_bytes;
   const int load_rows = p.N < feats ? p.N : feats, load_toks = p.M < toks ? p.M : toks;  // boxes no higher than the operands
-  const uint32_t load_bytes = (GATED ? 2 : 1) * load_rows * kI8Chunk + 2 * load_toks * 128;
   TileBars* tb = reinterpret_cast<TileBars*>(ring + (size_t)ns * stage_bytes);
   float* halves = reinterpret_cast<float*>(tb + 1) + kI8Cols / 2 * 8;  // GATED: what pairs of epilogue warps exchange
   DenseBars* bars = &tb->d;
@@ -258,6 +258,8 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
   const int S = SHARED ? p.S : 1;
   const int crank = PAIR || SHARED ? (int)cluster_rank() : 0, half_of = PAIR ? crank & 1 : 0, lead = crank - half_of;
   const int rank = SHARED ? crank / P : 0;
+  // what a stage's barrier counts: of a pair, the first CTA's both CTAs' tokens, the second's its weights alone
+  const uint32_t load_bytes = (GATED ? 2 : 1) * load_rows * kI8Chunk + (PAIR ? 2 - 2 * half_of : 1) * 2 * load_toks * 128;
   const int log_s = SHARED ? __ffs(S) - 1 : 0;  // (divisions take 100 to 200 clocks each, which a call of few tokens feels)
   const int first = blockIdx.x >> (P - 1 + log_s), step = gridDim.x >> (P - 1 + log_s);
   const int kc0 = p.KC * rank >> log_s, kc1 = p.KC * (rank + 1) >> log_s;
@@ -321,11 +323,19 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
           tma_2d(a, &mw, kc * kI8Chunk, f0, &bars->full[s], pw);
           if (GATED) tma_2d(a + kW / 2, &mw2, kc * kI8Chunk, f0, &bars->full[s], pw);
         };
+        // A pair's tokens count on the first CTA's barrier: its converting warps wait for that, and the products, which read
+        // both CTAs' tokens, for those warps.
+        const uint32_t full_at = PAIR ? peer_addr(smem_addr(&bars->full[0]), lead) : 0;
         auto tokens = [&](int s, int kc, int mt) {
           const int m0 = mt * NT + half_of * toks;
           const uint32_t b = ring_at + s * stage_bytes + kW;
-          tma_2d(b, &mx, kc * kI8Chunk, m0, &bars->full[s], px);
-          tma_2d(b + tok_bytes, &mx, kc * kI8Chunk + 64, m0, &bars->full[s], px);
+          if constexpr (PAIR) {
+            tma_2d_pair(b, &mx, kc * kI8Chunk, m0, full_at + s * 8, px);
+            tma_2d_pair(b + tok_bytes, &mx, kc * kI8Chunk + 64, m0, full_at + s * 8, px);
+          } else {
+            tma_2d(b, &mx, kc * kI8Chunk, m0, &bars->full[s], px);
+            tma_2d(b + tok_bytes, &mx, kc * kI8Chunk + 64, m0, &bars->full[s], px);
+          }
         };
         int ahead = 0;  // stages of the first tile whose weights are under way before the tokens can be
         if (first < p.T) {
@@ -364,7 +374,8 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
           if (!ok) dn_fail(bars, status);
           for (int i = 0; ok && i < S; ++i) peer_arrive(peer_addr(smem_addr(&bars->xready), P * i + half_of));
         }
-        // No copy of this CTA is in flight when it ends: the last stages have come.
+        // No copy of this CTA is in flight when it ends: the last stages have come (the second CTA's tokens before the first
+        // one leaves the cluster).
         const int n = issued < ns ? issued : ns;
         for (int i = 0; i < n; ++i) {
           if (--st < 0) {
@@ -493,7 +504,8 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
           tc_before_sync();
           __syncwarp();
           if (lane == 0) {
-            if (PAIR) pair_arrive(peer_addr(smem_addr(&tb->afull[slot]), lead));
+            // (the first CTA's arrival also hands on the tokens of both that its stage's barrier has counted)
+            if (PAIR && half_of) pair_arrive(peer_addr(smem_addr(&tb->afull[slot]), lead));
             else mbar_arrive(&tb->afull[slot]);
           }
         }
