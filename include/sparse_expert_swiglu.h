@@ -401,6 +401,9 @@ moe_status_t moe_layer_dense_decode(const uint16_t* x, int32_t B, const moe_dens
  * scale = m / 127 in fp32 and q = 127 x / m rounded to the nearest integer, exact halves to the even one.  A row of
  * zeros has scale 0; a row with an infinity or a NaN has scale NaN and q = 0.
  *
+ * Scales may be any fp32 numbers: where the product of a token's and an output's scale alone would leave fp32's normal range, the
+ * sum is multiplied by the smaller one first, so that a result is lost only where it leaves the range itself.
+ *
  * Workspaces: as in the section above, and the two sections' calls may share one.  A y that overlaps an input, and a
  * workspace that overlaps any tensor of the call, is refused (MOE_ERR_INVALID_ARG) but where stated.
  */

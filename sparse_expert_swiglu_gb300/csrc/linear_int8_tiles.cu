@@ -543,11 +543,17 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
       const bool on = local < feats && feat < p.N;
       float* scales = reinterpret_cast<float*>(tb + 1) + (warp - 12) * (kI8Cols / 2);
       Feature f = {0.f, 0.f};
+      ScaleRange range;
       if (!SHARED) {
         f = Feature(p, mul, feat, on);
         __syncwarp();
-        for (int i = lane; 32 * (i >> 4) + 16 * half < nt; i += 32)
-          scales[i] = p.x_scale[m0 + 32 * (i >> 4) + 16 * half + (i & 15)];
+        for (int i = lane; 32 * (i >> 4) + 16 * half < nt; i += 32) {
+          const int tok = 32 * (i >> 4) + 16 * half + (i & 15);
+          const float s = p.x_scale[m0 + tok];
+          scales[i] = s;
+          if (tok < nt) range.add(s);
+        }
+        range.join();
         __syncwarp();
       }
       // Where a cluster's sums go: those of even and of odd groups of 4 tokens.
@@ -615,58 +621,71 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
 #pragma unroll
         for (int i = 0; i + W < TB * 16; ++i) acc[i / 16][i % 16] = acc[(i + W) / 16][(i + W) % 16];
       };
-      if constexpr (!SHARED && !GATED) {
-        // W tokens at a time: a short call pays for every line of code that it fetches
-        constexpr int W = TB <= 2 ? 8 : 16;
-        for (int n0 = 16 * half; n0 < nt; n0 += 32)
+      // Two copies, so that a decision for each tile is enough (one for each value costs 2048 tokens of 14336 x 4096 168 us for
+      // 158, one for each 16 160; gated, 2 x 14336 x 4096, both 340 to 349 for 320 and this 325).
+      auto finish = [&](auto any) {
+        constexpr bool ODD = decltype(any)::value;
+        auto value = [&](int sum, float x_scale) {
+          return ODD ? int8_value(sum, x_scale, f.scale, f.bias)
+                     : int8_scaled((float)sum, __fmul_rn(x_scale, f.scale), f.bias);
+        };
+        if constexpr (!GATED) {
+          // W tokens at a time: a short call pays for every line of code that it fetches
+          constexpr int W = TB <= 2 || ODD ? 8 : 16;
+          for (int n0 = 16 * half; n0 < nt; n0 += 32)
 #pragma unroll 1
-          for (int i = n0; i < n0 + 16; i += W) {
-            unsigned short r[W];
-            float xs[W], v[W];
-            if (on) tile_residual(p, feat, m0 + i, nt - i, r);
-            token_scales(scales + (n0 >> 5) * 16 + (i & 15), xs);
+            for (int i = n0; i < n0 + 16; i += W) {
+              unsigned short r[W];
+              float xs[W], v[W];
+              if (on) tile_residual(p, feat, m0 + i, nt - i, r);
+              token_scales(scales + (n0 >> 5) * 16 + (i & 15), xs);
 #pragma unroll
-            for (int j = 0; j < W; ++j) v[j] = int8_value(acc[0][j], xs[j], f.scale, f.bias);
-            if (on) tile_store<W, false>(p, feat, m0 + i, nt - i, v, nullptr, r);
-            turn_blocks(std::integral_constant<int, W>());
-          }
-      } else if constexpr (!SHARED) {
-        // Warps q and q + 2 have the two matrices' sums of the same features: of 16 tokens the first finishes eight and
-        // the second eight, and each gives the other what it lacks.
-        const int pair = (q & 1) * 2 + half;
-        int turn = 0;
+              for (int j = 0; j < W; ++j) v[j] = value(acc[0][j], xs[j]);
+              if (on) tile_store<W, false>(p, feat, m0 + i, nt - i, v, nullptr, r);
+              turn_blocks(std::integral_constant<int, W>());
+            }
+        } else {
+          // Warps q and q + 2 have the two matrices' sums of the same features: of 16 tokens the first finishes eight and
+          // the second eight, and each gives the other what it lacks.
+          const int pair = (q & 1) * 2 + half;
+          int turn = 0;
 #pragma unroll 1
-        for (int n0 = 16 * half; n0 < nt; n0 += 32) {
-          float xs[16];
-          unsigned short r[8];
-          const int tok = n0 + 8 * mul;  // the eight of this warp
-          if (on) tile_residual(p, feat, m0 + tok, nt - tok, r);
-          token_scales(scales + (n0 >> 5) * 16, xs);
-          float* give = halves + ((turn * 4 + pair) * 2 + mul) * 256 + lane;
-          const float* take = halves + ((turn * 4 + pair) * 2 + (mul ^ 1)) * 256 + lane;
-          float v[8], m[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float a = int8_value(acc[0][j], xs[j], f.scale, f.bias);
-            const float b = int8_value(acc[0][8 + j], xs[8 + j], f.scale, f.bias);
-            v[j] = mul ? b : a;
-            give[32 * j] = mul ? a : b;
-          }
-          named_barrier(2 + pair, 64);  // (the next turn's writes go to the other buffer)
-          turn ^= 1;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) m[j] = take[32 * j];
-          if (mul) {
+          for (int n0 = 16 * half; n0 < nt; n0 += 32) {
+            float xs[16];
+            unsigned short r[8];
+            const int tok = n0 + 8 * mul;  // the eight of this warp
+            if (on) tile_residual(p, feat, m0 + tok, nt - tok, r);
+            token_scales(scales + (n0 >> 5) * 16, xs);
+            float* give = halves + ((turn * 4 + pair) * 2 + mul) * 256 + lane;
+            const float* take = halves + ((turn * 4 + pair) * 2 + (mul ^ 1)) * 256 + lane;
+            float v[8], m[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float a = m[j];
-              m[j] = v[j];
-              v[j] = a;
+              const float a = value(acc[0][j], xs[j]), b = value(acc[0][8 + j], xs[8 + j]);
+              v[j] = mul ? b : a;
+              give[32 * j] = mul ? a : b;
             }
+            named_barrier(2 + pair, 64);  // (the next turn's writes go to the other buffer)
+            turn ^= 1;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m[j] = take[32 * j];
+            if (mul) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float a = m[j];
+                m[j] = v[j];
+                v[j] = a;
+              }
+            }
+            if (on) tile_store<8, true>(p, feat, m0 + tok, nt - tok, v, m, r);
+            turn_blocks(std::integral_constant<int, 16>());
           }
-          if (on) tile_store<8, true>(p, feat, m0 + tok, nt - tok, v, m, r);
-          turn_blocks(std::integral_constant<int, 16>());
         }
+      };
+      if constexpr (!SHARED) {
+        // whether a product of the warp's scales may leave fp32's normal range
+        if (__any_sync(0xffffffffu, range.odd(f.scale))) finish(std::true_type());
+        else finish(std::false_type());
       } else {
         int cell_unit, cell_g;
         cells.start(rank, warp - 12, cell_unit, cell_g);
