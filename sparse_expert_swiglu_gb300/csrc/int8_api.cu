@@ -179,9 +179,9 @@ moe_status_t moe_expert_int8_swiglu(const void* x, const float* x_scale, int32_t
   if (!aligned(x, 16) || !aligned(x_scale, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(ws, kWsAlign))
     return MOE_ERR_ALIGNMENT;
   const Span out = {y, n * d * 2}, in = {x, n * d * width(x_dtype)}, sc = {x_scale, (size_t)n * 4}, res = {residual, n * d * 2};
-  // x is read before the first value of y is written
+  // x is read before the first value of y is written: y may be x, not a part of it
   if ((y != residual && out.overlaps(res)) || out.overlaps_any(weights)) return MOE_ERR_INVALID_ARG;
-  if (!x16 && (out.overlaps(in) || out.overlaps(sc))) return MOE_ERR_INVALID_ARG;
+  if ((!(x16 && y == x) && out.overlaps(in)) || out.overlaps(sc)) return MOE_ERR_INVALID_ARG;
   const ExpertWs at(n, ex.d, ex.f);
   if (ws_bytes < at.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const Span work = {ws, at.bytes};
