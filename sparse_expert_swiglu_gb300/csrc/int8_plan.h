@@ -12,6 +12,13 @@ constexpr int kI8Cols = 192;         // TMEM columns of one set of accumulators,
 constexpr int kI8MaxSlots = 8;       // of 64 k (32 columns) with more than 128 tokens in a tile, else 128 k: rows of w as fp16
 constexpr int kI8Halves = 16384;     // bytes: what epilogue warps exchange with w_mul
 
+// With more than 64 tokens in a tile the warps share out the registers that a block is launched with: warps 0-3, those that
+// convert, those of the epilogue.  Shares beyond those would wait forever.  Registers are allotted in units of 8 a thread.
+constexpr int kI8RegsIssue = 48, kI8RegsConvert = 72, kI8RegsEpilogue = 144;
+inline bool int8_registers_fit(int a_thread) {
+  return (a_thread + 7) / 8 * 8 * kI8Threads >= 128 * kI8RegsIssue + 256 * kI8RegsConvert + 256 * kI8RegsEpilogue;
+}
+
 struct Int8Plan {
   int P = 1;       // CTAs that run one product (cta_group::2 with 2)
   int S = 0;       // shares of k: a cluster has P S CTAs

@@ -298,7 +298,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
   const Cells<GATED> cells(NT, log_s);
   bool left = false;  // this thread has told the cluster that it is done with it
   if (warp < 4) {
-    if constexpr (TB >= 4) fewer_registers<48>();
+    if constexpr (TB >= 4) fewer_registers<kI8RegsIssue>();
     if (SHARED && warp == 3) {
       // what comes into this CTA from all of the cluster (a store that were counted before this would be as well)
       int ft, mt, there = 0, unit, g;
@@ -454,7 +454,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
     // (With seven, warps that ran ahead took a stage that the others had not seen loaded for their own next one: 3 of 80000
     // calls of 4 tokens by 32000 x 4096 came to a stop.)  A slot's last use but one lies four stages back or more, and these
     // warps have waited for the products of one four stages back when they took their stage before this.
-    if constexpr (TB >= 4) fewer_registers<72>();
+    if constexpr (TB >= 4) fewer_registers<kI8RegsConvert>();
     const int q = warp & 3, set = (warp - 4) >> 2, row = q * 32 + lane;
     const uint32_t lanes = slots_at + ((uint32_t)(q * 32) << 16);
     const int total = tiles * (kc1 - kc0);
@@ -527,7 +527,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
     }
   } else {
     // Lanes 32 (warp % 4) ... are this warp's.  Of the two warps that have them, each takes every other 16 tokens.
-    if constexpr (TB >= 4) more_registers<144>();
+    if constexpr (TB >= 4) more_registers<kI8RegsEpilogue>();
     const int q = warp & 3, half = (warp - 12) >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     int buf = 0;
@@ -812,7 +812,6 @@ cudaError_t launch_int8_tiles(const LinearInt8Call& c, const void* tokens, const
   e = allow_shared(kernels[which], allowed[which], smem_optin);
   if (e != cudaSuccess) return e;
   if (l.blocks >= 4) {
-    // the warps' shares of the registers that a block is launched with: more than those would wait forever
     static std::atomic<int> regs[32];
     int n = regs[which].load(std::memory_order_relaxed);
     if (!n) {
@@ -821,7 +820,7 @@ cudaError_t launch_int8_tiles(const LinearInt8Call& c, const void* tokens, const
       if (e != cudaSuccess) return e;
       regs[which].store(n = attr.numRegs, std::memory_order_relaxed);
     }
-    if (n * kI8Threads < 128 * 48 + 256 * 72 + 256 * 144) return cudaErrorInvalidConfiguration;
+    if (!int8_registers_fit(n)) return cudaErrorInvalidConfiguration;
   }
   const int fit = sms / l.P;
   cudaLaunchConfig_t cfg = {};
