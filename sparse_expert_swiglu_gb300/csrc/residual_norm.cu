@@ -3,7 +3,7 @@
 //
 // Bound by HBM (with few tokens by the latency of its barriers): x and the residual are read once, a CTA keeps a token's
 // row in registers in fp32 through both norms and writes s and y.  Variances are sums of squared differences from the mean, of
-// values in registers.  With more tokens than CTAs fit at once a CTA goes from token to token, and while it works on one, every
+// values in registers.  With many tokens (norm_plan) a CTA goes from token to token, and while it works on one, every
 // thread's own parts of the next come into shared memory by asynchronous copies.  Sums are formed in one order whatever the
 // number of tokens: vectors of 8, then 32 neighbouring vectors as a tree, then those sums as a tree.
 //
@@ -13,14 +13,13 @@
 #include "dense_params.cuh"
 #include "int8.cuh"
 #include "int8_params.cuh"
+#include "norm_plan.h"
 
 #include <cuda_bf16.h>
 
 namespace sesg {
 
 namespace {
-
-constexpr size_t kNormShared = 200 << 10;  // of an SM, for what comes ahead
 
 struct NormArgs {
   int M, d, bf16, s_f32, y_int8, post, norm, gate_every;
@@ -302,24 +301,11 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStr
   p.s = op.s;
   p.y = op.y;
   p.y_scale = op.y_scale;
-  // Copies ahead pay from a few tokens for each CTA on.  With them 2 vectors for each thread (8192 x 4096, LayerNorms and an fp32
-  // residual, when all were timed: 73 us, with 1 81, with 4 79; 1000 x 8208 13.9 us, with 4 15.0), without them 1, which leaves
-  // one token's barriers with the least work between (64 x 8192, RMSNorm: 3.1 us, with 2 4.3).  An SM holds one CTA of more than
-  // 512 threads: where there are more tokens than SMs, two smaller ones are faster (300 x 8192: 5.6 us, else 6.7), but for rows
-  // that need 2 vectors of 1024 threads (300 x 16384: 11.0 us, with 4 of 512 13.9).
-  const int n = op.d / 8;
-  const bool ahead = op.M > 2 * sms;
-  const int nv = ahead || n > 1024 || (n > 512 && op.M > sms) ? 2 : 1;
-  const int T = ((n + nv - 1) / nv + 31) / 32 * 32;
-  const int each = op.residual ? p.s_f32 ? 3 : 2 : 1;
-  const size_t bytes = ahead ? (size_t)nv * each * T * 16 : 0;
-  // CTAs that fit an SM at once, by threads and shared memory
-  int fit = 1024 / T < 24 ? 1024 / T : 24;
-  if (bytes && fit > (int)(kNormShared / (bytes + 1536))) fit = (int)(kNormShared / (bytes + 1536));
+  const NormPlan l = norm_plan(op.M, op.d, op.residual != nullptr, p.s_f32, p.y_int8, sms);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ahead && op.M > fit * sms ? fit * sms : op.M);
-  cfg.blockDim = dim3(T);
-  cfg.dynamicSmemBytes = bytes;
+  cfg.gridDim = dim3(l.ctas);
+  cfg.blockDim = dim3(l.threads);
+  cfg.dynamicSmemBytes = l.bytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -333,9 +319,9 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStr
       {residual_norm_kernel<1, false, 1, false>, residual_norm_kernel<2, false, 1, false>, residual_norm_kernel<2, true, 1, false>},
       {residual_norm_kernel<1, false, 1, true>, residual_norm_kernel<2, false, 1, true>, residual_norm_kernel<2, true, 1, true>}};
   const int types = 2 * p.bf16 + p.s_f32;
-  const Kernel kernel = kernels[types][ahead ? 2 : nv - 1];
+  const Kernel kernel = kernels[types][l.ahead ? 2 : l.nv - 1];
   static std::atomic<uint64_t> allowed[4];
-  if (ahead) {
+  if (l.ahead) {
     const cudaError_t e = allow_shared(kernel, allowed[types], kNormShared);
     if (e != cudaSuccess) return e;
   }
