@@ -81,7 +81,9 @@ moe_status_t moe_quantize_int8(const void* x, int32_t dtype, int32_t rows, int32
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 16)) return MOE_ERR_ALIGNMENT;
   const Span in = {x, (size_t)rows * K * width(dtype)}, out = {q, (size_t)rows * K}, sc = {scale, (size_t)rows * 4};
   if (out.overlaps(in) || sc.overlaps(in) || sc.overlaps(out)) return MOE_ERR_INVALID_ARG;
-  return cuda_status(launch_quantize(x, dtype, rows, K, q, scale, (cudaStream_t)stream));
+  int sms = 0, smem = 0;
+  if (device_sizes(sms, smem) != cudaSuccess) return MOE_ERR_CUDA;
+  return cuda_status(launch_quantize(x, dtype, rows, K, q, scale, sms, (cudaStream_t)stream));
 }
 
 size_t moe_linear_int8_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t gated) {

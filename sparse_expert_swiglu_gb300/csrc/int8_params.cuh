@@ -5,11 +5,11 @@
 
 namespace sesg {
 
-cudaError_t launch_quantize(const void* x, int dtype, int rows, int K, int8_t* q, float* scale, cudaStream_t st);
+cudaError_t launch_quantize(const void* x, int dtype, int rows, int K, int8_t* q, float* scale, int sms, cudaStream_t st);
 
 // The tokens of the kernel that runs behind it (linear_int8_tiles.cu): fp16 integers [M][K], and scales with room for a
 // multiple of 16.  dtype MOE_I8: x with its scales, else x is quantised.
-cudaError_t launch_tokens(const void* x, int dtype, const float* x_scale, int M, int K, void* tokens, float* scales,
+cudaError_t launch_tokens(const void* x, int dtype, const float* x_scale, int M, int K, void* tokens, float* scales, int sms,
                           cudaStream_t st);
 
 struct LinearInt8Call {

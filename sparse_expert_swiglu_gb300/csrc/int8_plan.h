@@ -1,4 +1,5 @@
-// The tile, stages and cluster of a product of 8-bit integers (linear_int8_tiles.cu), by its sizes alone.
+// The tile, stages and cluster of a product of 8-bit integers (linear_int8_tiles.cu) and the threads of the quantiser
+// (quantize.cu), by their sizes alone.
 #pragma once
 
 #include "linear_plan.h"
@@ -93,6 +94,15 @@ inline Int8Plan make_int8_plan(int M, int N, int K, bool gated, int sms, int roo
     }
   }
   return best;
+}
+
+// Threads of the quantiser for each row.  Many rows: 8 loads of 16 bytes for each thread, so that enough bytes are in flight
+// beside the rows that wait or round.  Few (two a SM): 2, so that a row is over soon.
+inline int quantize_threads(int rows, int K, bool f32, int sms) {
+  const int keep = rows <= 2 * sms ? 2 : f32 ? 4 : 8;  // vectors of eight elements, which are two loads in fp32
+  int T = 32;
+  while (T < 1024 && T * keep < K / 8) T *= 2;
+  return T;
 }
 
 // A thread keeps the plans of the sizes that it used last, which a model's calls come back to: 64 of them, by their mixed

@@ -219,7 +219,7 @@ cudaError_t launch_linear_int8(const LinearInt8Call& c, void* ws, int sms, int s
     const Int8Ws at(c.M, c.K);
     uint8_t* base = reinterpret_cast<uint8_t*>(ws);
     float* scales = reinterpret_cast<float*>(base + at.scales);
-    cudaError_t e = launch_tokens(c.x, c.x_dtype, c.x_scale, c.M, c.K, base + at.tokens, scales, st);
+    cudaError_t e = launch_tokens(c.x, c.x_dtype, c.x_scale, c.M, c.K, base + at.tokens, scales, sms, st);
     if (e == cudaSuccess) e = launch_int8_tiles(c, base + at.tokens, scales, ws, sms, smem_optin, st);
     return e;
   }

@@ -7,6 +7,7 @@
 // by the CTAs' coming and going (65536 rows of 128: 15 us).
 #include "int8.cuh"
 #include "int8_params.cuh"
+#include "int8_plan.h"
 
 namespace sesg {
 
@@ -117,13 +118,8 @@ cudaError_t launch_row_kernel(const void* x, int rows, int K, void* q, float* sc
 }
 
 template <bool WIDE>
-cudaError_t launch_rows(const void* x, int dtype, int rows, int K, void* q, float* scale, cudaStream_t st) {
-  const int n = K / 8;
-  // Many rows: 8 loads for each thread, so that enough bytes are in flight beside the rows that wait or round.  Few: 2, so
-  // that a row is over soon.
-  const int keep = rows <= 2 * 152 ? 2 : (dtype == MOE_F32 ? 4 : 8);
-  int T = 32;
-  while (T < 1024 && T * keep < n) T *= 2;
+cudaError_t launch_rows(const void* x, int dtype, int rows, int K, void* q, float* scale, int sms, cudaStream_t st) {
+  const int T = quantize_threads(rows, K, dtype == MOE_F32, sms);
   return dtype == MOE_F32    ? launch_row_kernel<MOE_F32, 4, WIDE>(x, rows, K, q, scale, T, st)
          : dtype == MOE_BF16 ? launch_row_kernel<MOE_BF16, 8, WIDE>(x, rows, K, q, scale, T, st)
                              : launch_row_kernel<MOE_F16, 8, WIDE>(x, rows, K, q, scale, T, st);
@@ -131,13 +127,13 @@ cudaError_t launch_rows(const void* x, int dtype, int rows, int K, void* q, floa
 
 }  // namespace
 
-cudaError_t launch_quantize(const void* x, int dtype, int rows, int K, int8_t* q, float* scale, cudaStream_t st) {
-  return launch_rows<false>(x, dtype, rows, K, q, scale, st);
+cudaError_t launch_quantize(const void* x, int dtype, int rows, int K, int8_t* q, float* scale, int sms, cudaStream_t st) {
+  return launch_rows<false>(x, dtype, rows, K, q, scale, sms, st);
 }
 
-cudaError_t launch_tokens(const void* x, int dtype, const float* x_scale, int M, int K, void* tokens, float* scales,
+cudaError_t launch_tokens(const void* x, int dtype, const float* x_scale, int M, int K, void* tokens, float* scales, int sms,
                           cudaStream_t st) {
-  if (dtype != MOE_I8) return launch_rows<true>(x, dtype, M, K, tokens, scales, st);
+  if (dtype != MOE_I8) return launch_rows<true>(x, dtype, M, K, tokens, scales, sms, st);
   const size_t n = (size_t)M * K / 8;  // at least 2 M
   return launch(widen_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), st, reinterpret_cast<const uint2*>(x), x_scale, M,
                 n, reinterpret_cast<uint4*>(tokens), scales);
