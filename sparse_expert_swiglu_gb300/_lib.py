@@ -945,6 +945,8 @@ def linear_int8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, x_scale
         raise ValueError("bias_mul goes with w_mul")
     M, K = x.shape
     N = w.shape[0]
+    if M > 0x7FFFFFFF or N > 0x7FFFFFFF or K > 0x7FFFFFFF:  # (more than the structure holds)
+        raise ValueError("sizes outside the supported range")
     if out_dtype is None:
         out_dtype = dt
     elif out_dtype is not dt and out_dtype is not torch.float32:
@@ -1068,6 +1070,8 @@ def residual_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, post
     device = _dense_x(x)
     dt, shape = x.dtype, tuple(x.shape)
     M, d = shape
+    if M > 0x7FFFFFFF or d > 0x7FFFFFFF:  # (more than the structure holds)
+        raise ValueError("sizes outside the supported range")
     post_code, norm_code = _NORMS.get(post, -1), _NORMS.get(norm, -1)
     if post_code < 0 or norm_code < 0:
         raise ValueError(f"post and norm must be one of {tuple(_NORMS)}, got {post!r} and {norm!r}")
