@@ -22,6 +22,7 @@ def _built():
 def test_more_tokens_than_32_bits_count():
     x = torch.empty(1 << 31, 16, dtype=F16, device="cuda")  # (not read)
     held = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
     w, ws = torch.zeros(1, 16, dtype=I8, device="cuda"), torch.ones(1, device="cuda")
     with pytest.raises(ValueError):
         ses.linear_int8(x, w, ws)
