@@ -374,9 +374,9 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
           if (!ok) dn_fail(bars, status);
           for (int i = 0; ok && i < S; ++i) peer_arrive(peer_addr(smem_addr(&bars->xready), P * i + half_of));
         }
-        // No copy of this CTA is in flight when it ends: the last stages have come (the second CTA's tokens before the first
-        // one leaves the cluster).
-        const int n = issued < ns ? issued : ns;
+        // No copy of this CTA is in flight when it ends: the last stages have come.  A pair has used every copy when its
+        // epilogues are done, and one that gave up waits at its end (else for copies that the other CTA may not have issued).
+        const int n = PAIR ? 0 : issued < ns ? issued : ns;
         for (int i = 0; i < n; ++i) {
           if (--st < 0) {
             st = ns - 1;

@@ -3,11 +3,15 @@ memory, and one thread of the first CTA starts the products that read both halve
 
 from __future__ import annotations
 
+import ctypes
+import time
+
 import pytest
 import torch
 
 ses = pytest.importorskip("sparse_expert_swiglu_gb300")
 from tests.test_int8 import BF16, F32, _ints, _linear_case, _linear_check  # noqa: E402
+from tests.test_int8_timeouts import _op  # noqa: E402
 
 gpu = pytest.mark.gpu
 
@@ -43,3 +47,25 @@ def test_tokens_that_change_from_call_to_call(M, N, K, gated):
         if i % 5 == 4:  # (the calls between have the next one start under them)
             wrong += (out != want[i % 3]).sum()
     assert int(wrong) == 0 and ws.status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K,gated", [(1024, 4095, 4096, False), (520, 2048, 4096, True), (520, 2048, 14336, False)])
+def test_pairs_that_give_up_end(M, N, K, gated):
+    """A pair that gives up waits for what is in flight, not for copies that its other CTA never issued: it ends within the time of
+    one wait (and no multiple of it by the number of stages), and the next call is right."""
+    c = _linear_case(M, N, K, BF16, "int8", "silu" if gated else "none", gated=gated)
+    t = [c[k].cuda() if c[k] is not None else None for k in ("x", "x_scale", "w", "w_scale", "w_mul", "w_mul_scale")]
+    ws = ses.Workspace(ses.linear_int8_workspace_bytes(M, N, K, gated))
+    y = torch.empty(M, N, dtype=BF16, device="cuda")
+    op = _op(M, N, K, *(v.data_ptr() if v is not None else None for v in t), y.data_ptr(), 1, gated)
+    tries = 1000  # of a millisecond at most: a wait of one thread takes a second
+    torch.cuda.synchronize()
+    start = time.monotonic()
+    stream = torch.cuda.current_stream().cuda_stream
+    assert ses.lib().moe_selftest_linear_int8_timeout(ctypes.byref(op), ws.buf.data_ptr(), ws.nbytes, tries, stream) == 0
+    torch.cuda.synchronize()
+    assert time.monotonic() - start < 2.0
+    assert ws.status() == -6
+    _linear_check(c, ws=ws)
+    assert ws.status() == 0
