@@ -22,7 +22,7 @@ namespace sesg {
 namespace {
 
 struct NormArgs {
-  int M, d, y_int8, post, norm, gate_every;
+  int M, d, bf16, s_f32, y_int8, post, norm, gate_every;
   int sectors;  // s starts on 32 bytes: whole sectors of fp32 at a time
   float residual_scale, block_scale, eps, per;  // per: 1 / d
   const void *x, *residual, *gate, *post_weight, *post_bias, *weight, *bias;
@@ -277,10 +277,11 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const NormArgs p) {
 }  // namespace
 
 cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStream_t st) {
-  const bool s_f32 = op.s_dtype == MOE_F32;
   NormArgs p;
   p.M = op.M;
   p.d = op.d;
+  p.bf16 = op.dtype == MOE_BF16;
+  p.s_f32 = op.s_dtype == MOE_F32;
   p.sectors = (uintptr_t)op.s % 32 == 0;
   p.y_int8 = op.y_dtype == MOE_I8;
   p.post = op.post;
@@ -300,7 +301,7 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStr
   p.s = op.s;
   p.y = op.y;
   p.y_scale = op.y_scale;
-  const NormPlan l = norm_plan(op.M, op.d, op.residual != nullptr, s_f32, p.y_int8, sms);
+  const NormPlan l = norm_plan(op.M, op.d, op.residual != nullptr, p.s_f32, p.y_int8, sms);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(l.ctas);
   cfg.blockDim = dim3(l.threads);
@@ -317,7 +318,7 @@ cudaError_t launch_residual_norm(const moe_residual_norm_t& op, int sms, cudaStr
       {residual_norm_kernel<1, false, 0, true>, residual_norm_kernel<2, false, 0, true>, residual_norm_kernel<2, true, 0, true>},
       {residual_norm_kernel<1, false, 1, false>, residual_norm_kernel<2, false, 1, false>, residual_norm_kernel<2, true, 1, false>},
       {residual_norm_kernel<1, false, 1, true>, residual_norm_kernel<2, false, 1, true>, residual_norm_kernel<2, true, 1, true>}};
-  const int types = 2 * (op.dtype == MOE_BF16) + s_f32;
+  const int types = 2 * p.bf16 + p.s_f32;
   const Kernel kernel = kernels[types][l.ahead ? 2 : l.nv - 1];
   static std::atomic<uint64_t> allowed[4];
   if (l.ahead) {
