@@ -22,6 +22,8 @@ namespace sesg {
 namespace {
 
 struct NormArgs {
+  // (bf16 and s_f32 choose the kernel on the host.  Without them here the compiler gives the kernels other registers: 8192 x 4096,
+  // LayerNorms, 72 us for 68, 64 x 8192 3.04 for 2.91.)
   int M, d, bf16, s_f32, y_int8, post, norm, gate_every;
   int sectors;  // s starts on 32 bytes: whole sectors of fp32 at a time
   float residual_scale, block_scale, eps, per;  // per: 1 / d
