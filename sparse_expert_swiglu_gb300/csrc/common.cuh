@@ -171,8 +171,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Bounded wait: every try_wait suspends for at most ~1 ms, so the bound is a few
-// seconds of wall time; on expiry the caller records MOE_ERR_TIMEOUT and bails out.
+// Bounded wait: a try_wait suspends one thread for at most ~1 ms (a whole warp for about 4 us), so
+// the bound is a few seconds of wall time (15 ms); on expiry the caller records MOE_ERR_TIMEOUT and bails out.
 constexpr uint32_t kWaitTries = 4000;
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   for (uint32_t i = 0; i < kWaitTries; ++i)

@@ -6,7 +6,7 @@
 // HBM's rate needs 23 for each token); sums are integers, so that their order is free.  Rows at a time: with one token one row
 // gives the most loads in flight, with more each token's read from shared memory serves RW rows (4 tokens of 4096 x 14336 with
 // 2 rows 15.8 us, with 4 14.7).  Measured: 1 token of 32000 x 4096 25.5 us (5.1 TB/s; about 6 us of that are a call's own:
-// launch, tokens, first bytes), of 4096 x 4096 6.0 us.
+// launch 0.7, the token's two passes behind w's first loads 2.9, first products 1.1, an end), of 4096 x 4096 6.4 us.
 #include "activate.cuh"
 #include "dense.cuh"
 #include "dense_params.cuh"

@@ -14,9 +14,9 @@
 // Where there are fewer tiles than SMs, a cluster's CTAs share a tile along k and join their sums in shared memory; with many
 // tokens CTA pairs run one product, so that each fetches half of the tokens.  int8_plan chooses.
 //
-// Measured: 2048 tokens of 2 x 14336 x 4096 324 us (1.48 PFLOP/s; tensor cores busy 65 %: a stage of a pair takes 5.6 clocks
+// Measured: 2048 tokens of 2 x 14336 x 4096 326 us (1.48 PFLOP/s; tensor cores busy 63 %: a stage of a pair takes 5.6 clocks
 // for each token, of which the products are 4, as shared memory serves the loads, the conversion and the products); 48 of 2 x
-// 16384 x 6144 42.5 us (4.8 TB/s); 16 of 4096 x 4096 9.5 us and 64 of them 11.5, 1.5 of that the tokens' kernel and 2.2 the
+// 16384 x 6144 42.3 us (4.8 TB/s); 16 of 4096 x 4096 9.4 us and 64 of them 11.4, 1.5 of that the tokens' kernel and 2.2 the
 // join.  What a short call feels beside its bytes is code: integer divisions (100 to 200 clocks each, some 2.5 us a call before
 // they went), barriers, lines of code that no call before has fetched.
 #include "activate.cuh"
@@ -622,7 +622,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
         for (int i = 0; i + W < TB * 16; ++i) acc[i / 16][i % 16] = acc[(i + W) / 16][(i + W) % 16];
       };
       // Two copies, so that a decision for each tile is enough (one for each value costs 2048 tokens of 14336 x 4096 168 us for
-      // 158, one for each 16 160; gated, 2 x 14336 x 4096, both 340 to 349 for 320 and this 325).
+      // 158, one for each 16 160; gated, 2 x 14336 x 4096, both 337 to 349 for 320 and this 325).
       auto finish = [&](auto any) {
         constexpr bool ODD = decltype(any)::value;
         auto value = [&](int sum, float x_scale) {
