@@ -480,8 +480,8 @@ moe_status_t moe_expert_int8_swiglu(const void* x, const float* x_scale, int32_t
  *   y[b] = norm(s[b]), of s before its rounding; fp32 throughout, each result rounded once.
  *   norms: MOE_NORM_NONE; MOE_NORM_RMS: v / sqrt(mean(v^2) + eps) * weight + bias;
  *          MOE_NORM_LAYER: (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * weight + bias
- *          with sums of squares in fp32: a row of values beyond about 1e19 has the norm 0, and with eps = 0 one of values whose
- *          squares are 0 has none (NaN)
+ *          with sums of squares in fp32: a row whose squares add up to more than 3e38 has the norm 0, and with eps = 0 one whose
+ *          squares are all 0 there (values below about 1e-23) has none (NaN)
  *   M 0..1048576 tokens (0 is a no-op), d 8..16384, a multiple of 8 (y_dtype MOE_I8: of 16); eps >= 0
  *   x [M][d], gate [gate_rows][d] (M a multiple of gate_rows; 0: no gate), post_weight, post_bias, weight, bias [d] or
  *   NULL, of dtype MOE_F16 or MOE_BF16; residual [M][d] or NULL (0 in its place) and s [M][d] or NULL (not written) of

@@ -4,8 +4,7 @@
 // and the rounding.  One row has 32 to 1024 threads of up to 8 loads; rows of up to 32 threads share a CTA.  Measured: 14336 rows
 // of 4096 bf16 31.5 us (176 MB, 5.6 TB/s; 26 us at a copy's rate, where the rounding of a row and the loads of the next
 // would have to overlap more), 48 rows of 14336 fp16 2.4 us (launch, one latency of memory, one barrier), 14336 of 4096
-// fp32 45.8 us (6.4 TB/s).  Short rows are bound
-// by the CTAs' coming and going (65536 rows of 128: 15 us).
+// fp32 45.8 us (6.4 TB/s).  Short rows are bound by the CTAs' coming and going (65536 rows of 128: 15 us).
 #include "int8.cuh"
 #include "int8_params.cuh"
 #include "int8_plan.h"
